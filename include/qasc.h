@@ -325,6 +325,112 @@ QASC_API qasc_status ts_ring_flush(const qasc_shape* shape, const qasc_paged_cac
                                    void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Serving calls over packed batches: appending new tokens to the cache, and
+ * causal attention of many new tokens at once.  No counterpart on the source
+ * pages beyond the cache itself ([TokenSelect] section "まとめ", integration
+ * with vLLM's PagedAttention; the sink and local tokens of its
+ * always-included table): what an engine around the decode step needs to fill
+ * the cache and to prefill, with the cache layouts above.
+ *
+ * A batch is T tokens packed without padding.  Sequence b has the new tokens
+ * [cu_q[b], cu_q[b + 1]) and lens[b] cached tokens, of which its new ones are
+ * the last: its new token i stands at cache position
+ *   p = lens[b] - (cu_q[b + 1] - cu_q[b]) + i.
+ * cu_q and lens are read on the device, so a captured call follows them.
+ * Tokens outside [cu_q[0], cu_q[B]) belong to no sequence: nothing is read or
+ * written for them.  A sequence may have no new tokens.  cu_q is ascending
+ * within [0, T] and lens within [0, n_cap]; a value outside is clamped, and
+ * one of lens recorded as QASC_ERR_BAD_TABLE.
+ * The shape's n is not used (pass n_cap); tokens * Hq < 2^31.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  const int32_t* cu_q;   /* device [B + 1]; NULL: one new token per sequence (tokens == B) */
+  const int32_t* lens;   /* device [B]: cached tokens, the new ones among them */
+  int64_t tokens;        /* T */
+} qasc_batch;
+
+/* Position rotation of a head's first rot_dim values (0: none; a multiple of
+ * 16 up to d) in pairs (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved,
+ * i in [0, rot_dim / 2):
+ *   x_a' = x_a cos(p f_i) - x_b sin(p f_i),  x_b' = x_b cos(p f_i) + x_a sin(p f_i)
+ * with f_i = inv_freq[i] and p the token's position: its cache position, or
+ * positions[t] where given (e.g. behind a shared prefix).  Angles are exact
+ * to about 1e-7 radians at any position; results are rounded once to bf16. */
+typedef struct {
+  const float* inv_freq;      /* device [rot_dim / 2] */
+  const int32_t* positions;   /* device [T], or NULL */
+  int32_t rot_dim;
+  int32_t interleaved;
+} qasc_rope;
+
+/* kv_rope_append — the new tokens' keys (rotated) and values into the cache,
+ * and their queries rotated.
+ *
+ *   q        [T, Hq, d]    bf16, read; token t at q + t * q_stride (values);
+ *                          NULL: keys and values only
+ *   k, v     [T, Hkv, d]   bf16, read; token strides k_stride, v_stride
+ *   q_out    [T, Hq, d]    bf16, written (dense; may be q itself when q is dense)
+ *   K, V     the cache: rows of the new tokens written, no others
+ * Strides are multiples of 8 values (e.g. the three parts of one fused
+ * projection).  A token whose position lies outside the cache, or whose page
+ * lies outside the pool, is not written and recorded as QASC_ERR_BAD_TABLE.
+ * Only the block-table entries of the pages written to are read. */
+QASC_API qasc_status kv_rope_append(const qasc_shape* shape, const qasc_batch* batch, const qasc_rope* rope,
+                                    const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                    const uint16_t* v, int64_t v_stride, uint16_t* q_out, uint16_t* K, uint16_t* V,
+                                    void* stream);
+QASC_API qasc_status kv_rope_append_paged(const qasc_shape* shape, const qasc_paged_cache* cache,
+                                          const qasc_batch* batch, const qasc_rope* rope, const uint16_t* q,
+                                          int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                          int64_t v_stride, uint16_t* q_out, uint16_t* K_pool, uint16_t* V_pool,
+                                          void* stream);
+
+/* kv_window_attn — causal attention of the new tokens over the always-attended
+ * tokens of their sequences: the first `sink` and the newest `local` up to
+ * their own position (local >= n_cap: plain causal attention).
+ *
+ *   A(t)       = { j <= p : j < sink or j > p - local }
+ *   out[t,h,:] = sum_{j in A(t)} softmax_j(q[t,h].K[b,g(h),j] / sqrt(d)) V[b,g(h),j,:]
+ *   lse[t,h]   = natural-log sum_{j in A(t)} exp(q.K_j / sqrt(d))   (optional)
+ *
+ *   q      [T, Hq, d]   bf16
+ *   out    [T, Hq, d]   bf16, written (rounded once; the probabilities of the
+ *                       second product are bf16 too, sums and statistics fp32)
+ *   lse    [T, Hq]      fp32, written if non-NULL
+ *   workspace, ws_bytes >= kv_window_attn_workspace_bytes(shape, tokens)
+ * sink >= 0, local >= 1, B <= 2048 (more: QASC_ERR_UNSUPPORTED).  A token with
+ * A(t) empty (its position is negative: more new tokens than cached ones) gives
+ * out 0 and lse -inf.  Cache rows that none of a sequence's queries attends to
+ * may hold anything, NaN and infinities included; a block-table entry is read
+ * only for pages that hold an attended token. */
+QASC_API size_t kv_window_attn_workspace_bytes(const qasc_shape* shape, int64_t tokens);
+QASC_API qasc_status kv_window_attn(const qasc_shape* shape, const qasc_batch* batch, int32_t sink, int32_t local,
+                                    const uint16_t* q, const uint16_t* K, const uint16_t* V, uint16_t* out, float* lse,
+                                    void* workspace, size_t ws_bytes, void* stream);
+QASC_API qasc_status kv_window_attn_paged(const qasc_shape* shape, const qasc_paged_cache* cache,
+                                          const qasc_batch* batch, int32_t sink, int32_t local, const uint16_t* q,
+                                          const uint16_t* K_pool, const uint16_t* V_pool, uint16_t* out, float* lse,
+                                          void* workspace, size_t ws_bytes, void* stream);
+
+/* kv_prefix_attn_paged — causal attention of a batch whose sequences share
+ * their first n_prefix tokens: the prefix is read once for all of them, and
+ * joined with each sequence's own tokens by an exact log-sum-exp merge.
+ *
+ *   A(t) = the whole prefix, and { j <= p } of the sequence's own tokens
+ *
+ *   prefix_table  [ceil(n_prefix / P)] int32, device: pool pages of the prefix
+ *   n_prefix      0 <= n_prefix < 2^24 (0: prefix_table may be NULL)
+ *   cache, batch  the sequences' own tokens, counted from 0 behind the prefix
+ *                 (lens[b] and p leave the prefix out; token 0 begins a page)
+ *   workspace, ws_bytes >= kv_prefix_attn_workspace_bytes(shape, tokens)
+ *   q, out, lse and the rest as for kv_window_attn_paged. */
+QASC_API size_t kv_prefix_attn_workspace_bytes(const qasc_shape* shape, int64_t tokens);
+QASC_API qasc_status kv_prefix_attn_paged(const qasc_shape* shape, const qasc_paged_cache* cache,
+                                          const int32_t* prefix_table, int64_t n_prefix, const qasc_batch* batch,
+                                          const uint16_t* q, const uint16_t* K_pool, const uint16_t* V_pool,
+                                          uint16_t* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * ts_dense_attn — full attention over all n cached tokens: the baseline the
  * TokenSelect page's speed table measures against ([TokenSelect] section
  * "速度性能": attention speed-up relative to full attention at 32K/64K/128K).

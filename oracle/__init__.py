@@ -40,6 +40,10 @@ Pins (what fixes this oracle other than itself) live in
                                    from a contiguous cache by reshapes, page
                                    permutation, flush round trip;
                                    tests/test_oracle_pins_paged.py)
+* ``serving.*``                  pinned (hand-worked rotation, library
+                                   attention with explicit masks, equality
+                                   with the decode step's sink + local
+                                   attention; tests/test_oracle_pins_serving.py)
 """
 
-from . import bf16, tokenselect, snapkv, paged  # noqa: F401
+from . import bf16, tokenselect, snapkv, paged, serving  # noqa: F401

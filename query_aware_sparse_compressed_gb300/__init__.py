@@ -14,6 +14,9 @@ Entry points keep the C names:
   ts_expand_neighbors, ts_sparse_attn_ex, ts_index_append_paged,
   ts_score_vote_select_paged, ts_score_select_per_head_paged,
   ts_sparse_attn_paged, ts_ring_flush,
+  kv_rope_append, kv_rope_append_paged,
+  kv_window_attn_workspace_bytes, kv_window_attn, kv_window_attn_paged,
+  kv_prefix_attn_workspace_bytes, kv_prefix_attn_paged,
   ts_dense_attn_workspace_bytes, ts_dense_attn, snapkv_workspace_bytes,
   snapkv_compress, qasc_status_string, qasc_last_error, qasc_last_cuda_error, qasc_device_error,
   qasc_selftest_bounded_wait, qasc_version.
@@ -417,6 +420,170 @@ def ts_dense_attn(q, K, V, out, workspace, *, n, lse=None, stream=None):
                               _ptr(V, "V", torch.bfloat16), _ptr(out, "out", torch.float32),
                               _ptr(lse, "lse", torch.float32), _ptr(workspace, "workspace", torch.uint8),
                               workspace.numel(), _stream(stream)))
+
+
+# ------------------------------------------------------- packed batches
+# These calls sit in an engine's per-layer loop, where the host's time per call
+# counts: their tensors are checked in one pass (_ptrs) against one reading of
+# the current device.
+def _ptrs(*tensors):
+    """Device pointers of (tensor, name, dtype, dims) tuples, each checked as
+    _ptr and _dims do; dims of None leaves the extents to the caller."""
+    dev = None
+    out = []
+    for t, name, dtype, dims in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if dims is not None and t.shape != dims:
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(dims), tuple(t.shape)))
+        if dev is None and t.is_cuda:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev or t.dtype != dtype or not t.is_contiguous():
+            _ptr(t, name, dtype)     # raises
+        out.append(t.data_ptr())
+    return out
+
+
+def _heads(t, name, T, H):
+    """A [T, H, d] tensor whose tokens may lie apart (a part of a fused
+    projection): its pointer and the values between tokens."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.shape != (T, H, D):
+        raise ValueError("%s must have shape %s, got %s" % (name, (T, H, D), tuple(t.shape)))
+    st = t.stride()
+    if T == 0 or (st[2] == 1 and (st[1] == D or H == 1)):
+        if not t.is_cuda or t.get_device() != torch.cuda.current_device() or t.dtype != torch.bfloat16:
+            _ptr(t[:0], name, torch.bfloat16)     # raises
+        return t.data_ptr(), st[0] if T > 1 else H * D
+    raise ValueError("%s must be contiguous within a token, got strides %s" % (name, st))
+
+
+def _batch(cu_q, lens, T):
+    """The packed batch and B; cu_q [B + 1] (None: one token per sequence)."""
+    _dims(lens, "kv_lens", (None,))
+    B = lens.shape[0]
+    cu, ln = _ptrs((cu_q, "cu_q", torch.int32, (B + 1,)), (lens, "kv_lens", torch.int32, None))
+    return _lib.qasc_batch(cu, ln, T), B
+
+
+def _rope_append(fn, cache, n_cap, Hkv, q, k, v, q_out, K, V, batch, B, inv_freq, positions, interleaved, stream):
+    T = batch.tokens
+    Hq = q.shape[1] if q is not None else Hkv
+    qp, qs = _heads(q, "q", T, Hq) if q is not None else (None, 0)
+    kp, ks = _heads(k, "k", T, Hkv)
+    vp, vs = _heads(v, "v", T, Hkv)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    half = inv_freq.shape[0] if inv_freq is not None else 0
+    op, Kp, Vp, fp, pp = _ptrs((q_out, "q_out", torch.bfloat16, (T, Hq, D)), (K, "K", torch.bfloat16, None),
+                               (V, "V", torch.bfloat16, None), (inv_freq, "inv_freq", torch.float32, (half,)),
+                               (positions, "positions", torch.int32, (T,)))
+    shape = _lib.qasc_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap)
+    rope = _lib.qasc_rope(fp, pp, 2 * half, 1 if interleaved else 0)
+    geometry = (ctypes.byref(shape),) if cache is None else (ctypes.byref(shape), ctypes.byref(cache))
+    _check(fn(*geometry, ctypes.byref(batch), ctypes.byref(rope), qp, qs, kp, ks, vp, vs, op, Kp, Vp,
+              _stream(stream)))
+
+
+def _kv_heads(k):
+    _dims(k, "k", (None, None, D))
+    return k.shape[0], k.shape[1]
+
+
+def kv_rope_append(q, k, v, q_out, K, V, kv_lens, inv_freq, *, cu_q=None, positions=None, interleaved=False,
+                   stream=None):
+    """New tokens' keys (rotated) and values into K, V [B, Hkv, n_cap, d], and
+    their rotated queries into q_out.  q [T, Hq, d] (None: keys and values
+    only), k, v [T, Hkv, d] may be parts of one fused projection; sequence b
+    has tokens cu_q[b] .. cu_q[b + 1] (None: one each), the last of its
+    kv_lens[b] cached ones; inv_freq [rot_dim / 2] (None: no rotation) turns
+    by the cache position, or by positions [T]."""
+    T, Hkv = _kv_heads(k)
+    batch, B = _batch(cu_q, kv_lens, T)
+    _dims(K, "K", (B, Hkv, None, D))
+    _dims(V, "V", tuple(K.shape))
+    _rope_append(_L().kv_rope_append, None, K.shape[2], Hkv, q, k, v, q_out, K, V, batch, B, inv_freq, positions,
+                 interleaved, stream)
+
+
+def kv_rope_append_paged(q, k, v, q_out, K_pool, V_pool, block_table, kv_lens, inv_freq, *, cu_q=None,
+                         positions=None, interleaved=False, stream=None):
+    """kv_rope_append into a paged pool [num_pages, Hkv, P, d]."""
+    T, Hkv = _kv_heads(k)
+    batch, B = _batch(cu_q, kv_lens, T)
+    cache, n_cap = _pool(K_pool, V_pool, block_table, B, Hkv)
+    _rope_append(_L().kv_rope_append_paged, cache, n_cap, Hkv, q, k, v, q_out, K_pool, V_pool, batch, B, inv_freq,
+                 positions, interleaved, stream)
+
+
+def _pool(K_pool, V_pool, block_table, B, Hkv=None):
+    """Descriptor of K and V pools under block_table [B, pages_per_seq], and n_cap."""
+    _dims(K_pool, "K_pool", (None, Hkv, None, D))
+    _dims(V_pool, "V_pool", tuple(K_pool.shape))
+    _dims(block_table, "block_table", (B, None))
+    P, pps = K_pool.shape[2], block_table.shape[1]
+    bt, = _ptrs((block_table, "block_table", torch.int32, None))
+    return _lib.qasc_paged_cache(bt, P, pps, K_pool.shape[0]), pps * P
+
+
+def _kv_attn(fn, geometry, own_args, q, K, V, out, workspace, batch, B, Hkv, n_cap, lse, stream):
+    T, Hq = q.shape[0], q.shape[1]
+    qp, Kp, Vp, op, lp, wp = _ptrs((q, "q", torch.bfloat16, (T, Hq, D)), (K, "K", torch.bfloat16, None),
+                                   (V, "V", torch.bfloat16, None), (out, "out", torch.bfloat16, (T, Hq, D)),
+                                   (lse, "lse", torch.float32, (T, Hq)), (workspace, "workspace", torch.uint8, None))
+    shape = _lib.qasc_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap)
+    _check(fn(ctypes.byref(shape), *geometry, ctypes.byref(batch), *own_args, qp, Kp, Vp, op, lp, wp,
+              workspace.numel(), _stream(stream)))
+
+
+def kv_window_attn_workspace_bytes(T, B, Hq, Hkv, n_cap):
+    return _sized(_L().kv_window_attn_workspace_bytes(ctypes.byref(make_shape(B, Hq, Hkv, n_cap, n_cap)), T))
+
+
+def kv_window_attn(q, K, V, kv_lens, out, workspace, *, local, sink=4, cu_q=None, lse=None, stream=None):
+    """out[t, h] = causal attention of the new token t over the first `sink`
+    and the newest `local` cached tokens of its sequence up to its own
+    position; q, out [T, Hq, d] bf16, K, V [B, Hkv, n_cap, d], the batch as
+    for kv_rope_append."""
+    _dims(q, "q", (None, None, D))
+    batch, B = _batch(cu_q, kv_lens, q.shape[0])
+    _dims(K, "K", (B, None, None, D))
+    _dims(V, "V", tuple(K.shape))
+    _kv_attn(_L().kv_window_attn, (), (sink, local), q, K, V, out, workspace, batch, B, K.shape[1], K.shape[2], lse,
+             stream)
+
+
+def kv_window_attn_paged(q, K_pool, V_pool, block_table, kv_lens, out, workspace, *, local, sink=4, cu_q=None,
+                         lse=None, stream=None):
+    """kv_window_attn over a paged pool [num_pages, Hkv, P, d]."""
+    _dims(q, "q", (None, None, D))
+    batch, B = _batch(cu_q, kv_lens, q.shape[0])
+    cache, n_cap = _pool(K_pool, V_pool, block_table, B)
+    _kv_attn(_L().kv_window_attn_paged, (ctypes.byref(cache),), (sink, local), q, K_pool, V_pool, out, workspace,
+             batch, B, K_pool.shape[1], n_cap, lse, stream)
+
+
+def kv_prefix_attn_workspace_bytes(T, B, Hq, Hkv, n_cap):
+    return _sized(_L().kv_prefix_attn_workspace_bytes(ctypes.byref(make_shape(B, Hq, Hkv, n_cap, n_cap)), T))
+
+
+def kv_prefix_attn_paged(q, K_pool, V_pool, prefix_table, block_table, kv_lens, out, workspace, *, n_prefix,
+                         cu_q=None, lse=None, stream=None):
+    """Causal attention of sequences that share their first n_prefix tokens
+    (the pool pages prefix_table [ceil(n_prefix / P)]), read once for all of
+    them; block_table and kv_lens describe each sequence's own tokens behind
+    the prefix."""
+    _dims(q, "q", (None, None, D))
+    batch, B = _batch(cu_q, kv_lens, q.shape[0])
+    cache, n_cap = _pool(K_pool, V_pool, block_table, B)
+    pages = -(-n_prefix // K_pool.shape[2])
+    pt, = _ptrs((prefix_table if n_prefix > 0 else None, "prefix_table", torch.int32, (pages,)))
+    _kv_attn(_L().kv_prefix_attn_paged, (ctypes.byref(cache), pt, n_prefix), (), q, K_pool, V_pool, out, workspace,
+             batch, B, K_pool.shape[1], n_cap, lse, stream)
 
 
 # ------------------------------------------------------------------ SnapKV

@@ -36,12 +36,25 @@ class qasc_local_ring(ctypes.Structure):
     _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("ring_tokens", ctypes.c_int32)]
 
 
+class qasc_batch(ctypes.Structure):
+    _fields_ = [("cu_q", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("tokens", ctypes.c_int64)]
+
+
+class qasc_rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _SP = ctypes.POINTER(qasc_shape)
 _TP = ctypes.POINTER(qasc_ts_params)
 _NP = ctypes.POINTER(qasc_snap_params)
 _PC = ctypes.POINTER(qasc_paged_cache)
 _RG = ctypes.POINTER(qasc_local_ring)
+_BT = ctypes.POINTER(qasc_batch)
+_RP = ctypes.POINTER(qasc_rope)
+_I64 = ctypes.c_int64
+_I32 = ctypes.c_int32
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -66,6 +79,13 @@ SIGNATURES = {
     "ts_sparse_attn_paged": (ctypes.c_int, [_SP, _TP, _PC, _RG, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P,
                                             ctypes.c_size_t, _P]),
     "ts_ring_flush": (ctypes.c_int, [_SP, _PC, _RG, _P, _P, _P, _P, ctypes.c_int64, ctypes.c_int64, _P]),
+    "kv_rope_append": (ctypes.c_int, [_SP, _BT, _RP, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P]),
+    "kv_rope_append_paged": (ctypes.c_int, [_SP, _PC, _BT, _RP, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P]),
+    "kv_window_attn_workspace_bytes": (ctypes.c_size_t, [_SP, _I64]),
+    "kv_window_attn": (ctypes.c_int, [_SP, _BT, _I32, _I32, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv_window_attn_paged": (ctypes.c_int, [_SP, _PC, _BT, _I32, _I32, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv_prefix_attn_workspace_bytes": (ctypes.c_size_t, [_SP, _I64]),
+    "kv_prefix_attn_paged": (ctypes.c_int, [_SP, _PC, _P, _I64, _BT, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "ts_dense_attn_workspace_bytes": (ctypes.c_size_t, [_SP]),
     "ts_dense_attn": (ctypes.c_int, [_SP, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "snapkv_workspace_bytes": (ctypes.c_size_t, [_SP, _NP]),

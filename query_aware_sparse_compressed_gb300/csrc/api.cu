@@ -191,7 +191,7 @@ const DeviceInfo* device_info() {
     d.err_word = static_cast<unsigned*>(p);
     if (configure_score_kernels(d) != cudaSuccess || configure_select_kernels(d) != cudaSuccess ||
         configure_head_select_kernels(d) != cudaSuccess || configure_group_kernels(d) != cudaSuccess ||
-        configure_expand_kernels(d) != cudaSuccess ||
+        configure_expand_kernels(d) != cudaSuccess || configure_kv_attn_kernels(d) != cudaSuccess ||
         configure_attn_kernels(d) != cudaSuccess || configure_snapkv_kernels(d) != cudaSuccess)
       return nullptr;
     ready[dev] = true;
@@ -539,6 +539,214 @@ QASC_API qasc_status ts_ring_flush(const qasc_shape* shape, const qasc_paged_cac
                                                 dev->err_word, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();
+}
+
+// ------------------------------------------------------- packed-batch calls
+namespace {
+constexpr int kMaxAttnBatch = 2048;   // sequences the attention plan holds in shared memory
+
+qasc_status check_tokens(const qasc_shape* s, int64_t tokens, const char* fn) {
+  if (tokens < 0 || tokens >= (int64_t(1) << 31) / s->Hq)
+    return fail(QASC_ERR_INVALID_ARG, "%s: tokens=%lld must be >= 0 and tokens * Hq < 2^31", fn,
+                static_cast<long long>(tokens));
+  return QASC_OK;
+}
+
+qasc_status check_batch(const qasc_shape* s, const qasc_batch* batch, const char* fn, qasc::Batch* b) {
+  if (!batch) return fail(QASC_ERR_INVALID_ARG, "%s: batch is NULL", fn);
+  QASC_CHECK(check_tokens(s, batch->tokens, fn));
+  if (!batch->cu_q && batch->tokens != s->B)
+    return fail(QASC_ERR_INVALID_ARG, "%s: without cu_q, tokens=%lld must equal B=%d", fn,
+                static_cast<long long>(batch->tokens), s->B);
+  if (!aligned(batch->cu_q, 4)) return fail(QASC_ERR_INVALID_ARG, "%s: cu_q is not 4-byte aligned", fn);
+  QASC_REQUIRE_PTR(batch->lens, 4, fn);
+  b->cu_q = batch->cu_q;
+  b->lens = batch->lens;
+  b->T = batch->tokens;
+  b->B = s->B;
+  return QASC_OK;
+}
+
+qasc_status check_stride(int64_t stride, const char* what, const char* fn) {
+  if (stride < 0 || stride % 8 != 0 || stride >= (int64_t(1) << 32))
+    return fail(QASC_ERR_INVALID_ARG, "%s: %s=%lld must be a multiple of 8 in [0, 2^32)", fn, what,
+                static_cast<long long>(stride));
+  return QASC_OK;
+}
+
+qasc_status rope_append_call(const char* fn, const qasc_shape* shape, const qasc::PageMap& pm, const qasc_batch* batch,
+                             const qasc_rope* rope, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                             int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* q_out, uint16_t* K,
+                             uint16_t* V, void* stream) {
+  QASC_RANGE(fn);
+  qasc::Batch bt;
+  QASC_CHECK(check_batch(shape, batch, fn, &bt));
+  if (!rope) return fail(QASC_ERR_INVALID_ARG, "%s: rope is NULL", fn);
+  if (rope->rot_dim < 0 || rope->rot_dim > shape->d || rope->rot_dim % 16 != 0)
+    return fail(QASC_ERR_INVALID_ARG, "%s: rot_dim=%d must be a multiple of 16 in [0, %d]", fn, rope->rot_dim,
+                shape->d);
+  const float* inv_freq = rope->inv_freq;
+  if (rope->rot_dim > 0) QASC_REQUIRE_PTR(inv_freq, 4, fn);
+  if (!aligned(rope->positions, 4)) return fail(QASC_ERR_INVALID_ARG, "%s: positions is not 4-byte aligned", fn);
+  QASC_CHECK(check_stride(q_stride, "q_stride", fn));
+  QASC_CHECK(check_stride(k_stride, "k_stride", fn));
+  QASC_CHECK(check_stride(v_stride, "v_stride", fn));
+  QASC_REQUIRE_PTR(K, 16, fn);
+  QASC_REQUIRE_PTR(V, 16, fn);
+  if (bt.T == 0) return ok();
+  QASC_REQUIRE_PTR(k, 16, fn);
+  QASC_REQUIRE_PTR(v, 16, fn);
+  if (q) {
+    QASC_REQUIRE_PTR(q, 16, fn);
+    QASC_REQUIRE_PTR(q_out, 16, fn);
+    if (q == q_out && q_stride != static_cast<int64_t>(shape->Hq) * shape->d)
+      return fail(QASC_ERR_INVALID_ARG, "%s: q_out may be q only when q is dense (q_stride=%lld)", fn,
+                  static_cast<long long>(q_stride));
+  }
+  qasc_status st;
+  const qasc::DeviceInfo* dev = need_device(fn, &st);
+  if (!dev) return st;
+  qasc::RopeArgs r;
+  r.inv_freq = inv_freq;
+  r.positions = rope->positions;
+  r.rot_dim = rope->rot_dim;
+  r.interleaved = rope->interleaved != 0;
+  const cudaError_t e = qasc::launch_rope_append(*shape, pm, bt, r, q, q_stride, k, k_stride, v, v_stride, q_out, K, V,
+                                                 *dev, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+qasc_status check_attn_batch(const qasc_shape* s, const char* fn) {
+  if (s->B > kMaxAttnBatch)
+    return fail(QASC_ERR_UNSUPPORTED, "%s: B=%d exceeds the supported %d sequences", fn, s->B, kMaxAttnBatch);
+  return QASC_OK;
+}
+
+size_t kv_attn_size(const char* fn, const qasc_shape* shape, int64_t tokens, bool prefix) {
+  QASC_SIZE_CHECK(check_shape(shape, fn));
+  QASC_SIZE_CHECK(check_attn_batch(shape, fn));
+  QASC_SIZE_CHECK(check_tokens(shape, tokens, fn));
+  ok();
+  return qasc::kv_attn_workspace_bytes(tokens, shape->B, shape->Hq, shape->Hkv, prefix, qasc::kMaxSmsForSizing);
+}
+
+// The shape (and pool) are checked; a carries the operator's own parameters.
+qasc_status kv_attn_call(const char* fn, const qasc_shape* shape, const qasc_batch* batch, qasc::KvAttnArgs& a,
+                         bool prefix, const uint16_t* q, const uint16_t* K, const uint16_t* V, uint16_t* out,
+                         float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  QASC_CHECK(check_attn_batch(shape, fn));
+  QASC_CHECK(check_batch(shape, batch, fn, &a.bt));
+  QASC_REQUIRE_PTR(K, 16, fn);
+  QASC_REQUIRE_PTR(V, 16, fn);
+  if (!aligned(lse, 4)) return fail(QASC_ERR_INVALID_ARG, "%s: lse is not 4-byte aligned", fn);
+  if (a.bt.T == 0) return ok();
+  QASC_REQUIRE_PTR(q, 16, fn);
+  QASC_REQUIRE_PTR(out, 16, fn);
+  const size_t need = qasc::kv_attn_workspace_bytes(a.bt.T, shape->B, shape->Hq, shape->Hkv, prefix,
+                                                    qasc::kMaxSmsForSizing);
+  if (!workspace || ws_bytes < need)
+    return fail(QASC_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                workspace ? ws_bytes : size_t(0));
+  QASC_REQUIRE_PTR(workspace, 256, fn);
+  qasc_status st;
+  const qasc::DeviceInfo* dev = need_device(fn, &st);
+  if (!dev) return st;
+  a.q = q;
+  a.K = K;
+  a.V = V;
+  a.out = out;
+  a.lse = lse;
+  const int rc = qasc::launch_kv_attn(*shape, a, static_cast<uint8_t*>(workspace), *dev,
+                                      static_cast<cudaStream_t>(stream));
+  if (rc != 0) return cuda_fail(rc, fn);
+  return ok();
+}
+
+qasc_status check_window(int32_t sink, int32_t local, const char* fn) {
+  if (sink < 0 || local < 1)
+    return fail(QASC_ERR_INVALID_ARG, "%s: sink=%d must be >= 0 and local=%d >= 1", fn, sink, local);
+  return QASC_OK;
+}
+}  // namespace
+
+QASC_API qasc_status kv_rope_append(const qasc_shape* shape, const qasc_batch* batch, const qasc_rope* rope,
+                                    const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                    const uint16_t* v, int64_t v_stride, uint16_t* q_out, uint16_t* K, uint16_t* V,
+                                    void* stream) {
+  static const char* fn = "kv_rope_append";
+  QASC_CHECK(check_shape(shape, fn));
+  return rope_append_call(fn, shape, qasc::PageMap(), batch, rope, q, q_stride, k, k_stride, v, v_stride, q_out, K, V,
+                          stream);
+}
+
+QASC_API qasc_status kv_rope_append_paged(const qasc_shape* shape, const qasc_paged_cache* cache,
+                                          const qasc_batch* batch, const qasc_rope* rope, const uint16_t* q,
+                                          int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                          int64_t v_stride, uint16_t* q_out, uint16_t* K_pool, uint16_t* V_pool,
+                                          void* stream) {
+  static const char* fn = "kv_rope_append_paged";
+  qasc::PageMap pm;
+  QASC_CHECK(check_paged(shape, cache, fn, &pm));
+  return rope_append_call(fn, shape, pm, batch, rope, q, q_stride, k, k_stride, v, v_stride, q_out, K_pool, V_pool,
+                          stream);
+}
+
+QASC_API size_t kv_window_attn_workspace_bytes(const qasc_shape* shape, int64_t tokens) {
+  return kv_attn_size("kv_window_attn_workspace_bytes", shape, tokens, false);
+}
+
+QASC_API qasc_status kv_window_attn(const qasc_shape* shape, const qasc_batch* batch, int32_t sink, int32_t local,
+                                    const uint16_t* q, const uint16_t* K, const uint16_t* V, uint16_t* out, float* lse,
+                                    void* workspace, size_t ws_bytes, void* stream) {
+  static const char* fn = "kv_window_attn";
+  QASC_RANGE(fn);
+  QASC_CHECK(check_shape(shape, fn));
+  QASC_CHECK(check_window(sink, local, fn));
+  qasc::KvAttnArgs a;
+  a.sink = sink;
+  a.local = local;
+  a.cache_rows = static_cast<int64_t>(shape->B) * shape->Hkv * shape->n_cap;
+  return kv_attn_call(fn, shape, batch, a, false, q, K, V, out, lse, workspace, ws_bytes, stream);
+}
+
+QASC_API qasc_status kv_window_attn_paged(const qasc_shape* shape, const qasc_paged_cache* cache,
+                                          const qasc_batch* batch, int32_t sink, int32_t local, const uint16_t* q,
+                                          const uint16_t* K_pool, const uint16_t* V_pool, uint16_t* out, float* lse,
+                                          void* workspace, size_t ws_bytes, void* stream) {
+  static const char* fn = "kv_window_attn_paged";
+  QASC_RANGE(fn);
+  qasc::KvAttnArgs a;
+  QASC_CHECK(check_paged(shape, cache, fn, &a.pm));
+  QASC_CHECK(check_window(sink, local, fn));
+  a.sink = sink;
+  a.local = local;
+  a.cache_rows = cache->num_pages * shape->Hkv * cache->page_tokens;
+  return kv_attn_call(fn, shape, batch, a, false, q, K_pool, V_pool, out, lse, workspace, ws_bytes, stream);
+}
+
+QASC_API size_t kv_prefix_attn_workspace_bytes(const qasc_shape* shape, int64_t tokens) {
+  return kv_attn_size("kv_prefix_attn_workspace_bytes", shape, tokens, true);
+}
+
+QASC_API qasc_status kv_prefix_attn_paged(const qasc_shape* shape, const qasc_paged_cache* cache,
+                                          const int32_t* prefix_table, int64_t n_prefix, const qasc_batch* batch,
+                                          const uint16_t* q, const uint16_t* K_pool, const uint16_t* V_pool,
+                                          uint16_t* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  static const char* fn = "kv_prefix_attn_paged";
+  QASC_RANGE(fn);
+  qasc::KvAttnArgs a;
+  QASC_CHECK(check_paged(shape, cache, fn, &a.pm));
+  if (n_prefix < 0 || n_prefix >= (int64_t(1) << 24))
+    return fail(QASC_ERR_INVALID_ARG, "%s: n_prefix=%lld outside [0, 2^24)", fn, static_cast<long long>(n_prefix));
+  if (n_prefix > 0) QASC_REQUIRE_PTR(prefix_table, 4, fn);
+  a.sink = 0;
+  a.local = INT32_MAX;
+  a.n_prefix = n_prefix;
+  a.pm_prefix = a.pm;
+  a.pm_prefix.table = prefix_table;
+  a.cache_rows = cache->num_pages * shape->Hkv * cache->page_tokens;
+  return kv_attn_call(fn, shape, batch, a, true, q, K_pool, V_pool, out, lse, workspace, ws_bytes, stream);
 }
 
 namespace {

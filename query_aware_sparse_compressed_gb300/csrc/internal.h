@@ -69,7 +69,50 @@ struct RingMap {
   int64_t R = 0;
 };
 
+// The new tokens of a batch, packed: sequence b has tokens
+// [cu_q[b], cu_q[b + 1]) of T (one token each when cu_q is NULL) and lens[b]
+// cached tokens, its new ones the last of them.
+struct Batch {
+  const int32_t* cu_q = nullptr;
+  const int32_t* lens = nullptr;
+  int64_t T = 0;
+  int B = 0;
+};
+
+// Rotation of keys and queries: frequencies of the rot_dim / 2 pairs, and the
+// positions that rotate (NULL: the cache positions).
+struct RopeArgs {
+  const float* inv_freq = nullptr;
+  const int32_t* positions = nullptr;
+  int rot_dim = 0, interleaved = 0;
+};
+
 #ifdef __CUDACC__
+// Sequence and cache position of packed token t; b < 0: the token belongs to
+// no sequence (it lies outside [cu_q[0], cu_q[B])).
+struct TokenAt {
+  int b;
+  int64_t pos;
+};
+__device__ __forceinline__ TokenAt token_of(const Batch& bt, int64_t t) {
+  TokenAt r;
+  if (bt.cu_q == nullptr) {
+    r.b = static_cast<int>(t);
+    r.pos = static_cast<int64_t>(__ldg(bt.lens + t)) - 1;
+    return r;
+  }
+  int lo = 0, hi = bt.B;   // the last b with cu_q[b] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(bt.cu_q + mid) <= t) lo = mid;
+    else hi = mid;
+  }
+  const int64_t q0 = __ldg(bt.cu_q + lo), q1 = __ldg(bt.cu_q + lo + 1);
+  r.b = t >= q0 && t < q1 ? lo : -1;
+  r.pos = static_cast<int64_t>(__ldg(bt.lens + lo)) - (q1 - t);
+  return r;
+}
+
 // Row of token t of (b, g) under m, or -1 when its block-table entry lies
 // outside the pool.
 __device__ __forceinline__ int64_t cache_row(const PageMap& m, int b, int g, int Hkv, int64_t n_cap, int64_t t) {
@@ -223,6 +266,33 @@ int launch_sparse_attn(const qasc_shape& s, const qasc_ts_params& p, const AttnL
                        uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream, bool sel_per_kv = false,
                        const int32_t* sel_len = nullptr, const PageMap* pm = nullptr,
                        const RingMap* ring = nullptr);
+
+// New tokens' K and V rows into the cache, keys and queries rotated; qs, ks,
+// vs: values between tokens of q, k, v.
+cudaError_t launch_rope_append(const qasc_shape& s, const PageMap& pm, const Batch& bt, const RopeArgs& r,
+                               const uint16_t* q, int64_t qs, const uint16_t* k, int64_t ks, const uint16_t* v,
+                               int64_t vs, uint16_t* q_out, uint16_t* K, uint16_t* V, const DeviceInfo& dev,
+                               cudaStream_t stream);
+
+// Causal attention of packed new tokens over the sink and local tokens of
+// their sequences (n_prefix == 0), or over a prefix shared by all sequences
+// and everything before them in their own (n_prefix > 0: pm_prefix, lens and
+// pm count the tokens behind the prefix).
+struct KvAttnArgs {
+  const uint16_t* q = nullptr;   // [T][Hq][d]
+  const uint16_t* K = nullptr;
+  const uint16_t* V = nullptr;
+  uint16_t* out = nullptr;       // [T][Hq][d] bf16
+  float* lse = nullptr;          // [T][Hq], optional
+  Batch bt;
+  PageMap pm, pm_prefix;
+  int64_t cache_rows = 0;        // rows of K and of V
+  int32_t sink = 0, local = 0;
+  int64_t n_prefix = 0;
+};
+size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms);
+int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t configure_kv_attn_kernels(const DeviceInfo& dev);
 
 // Neighbour expansion: rows of K ascending candidates in, the ascending union
 // of their +-radius neighbourhoods within C out ([rows][cap], the first
