@@ -419,7 +419,8 @@ QASC_API qasc_status kv_window_attn_paged(const qasc_shape* shape, const qasc_pa
  *   A(t) = the whole prefix, and { j <= p } of the sequence's own tokens
  *
  *   prefix_table  [ceil(n_prefix / P)] int32, device: pool pages of the prefix
- *   n_prefix      0 <= n_prefix < 2^24 (0: prefix_table may be NULL)
+ *   n_prefix      0 <= n_prefix < 2^24 (0: prefix_table may be NULL), and
+ *                 tokens * Hq * n_prefix < 2^45
  *   cache, batch  the sequences' own tokens, counted from 0 behind the prefix
  *                 (lens[b] and p leave the prefix out; token 0 begins a page)
  *   workspace, ws_bytes >= kv_prefix_attn_workspace_bytes(shape, tokens)

@@ -65,28 +65,29 @@ def attend(q, K, V):
     return w @ V, m + np.log(total), w @ np.abs(V), float((np.abs(K) @ np.abs(q)).max() / np.sqrt(d))
 
 
-def window_attention(q, K, V, cu_q, lens, sink, local):
+def window_attention(q, K, V, cu_q, lens, sink, local, tokens=None):
     """Causal attention over the first `sink` and the newest `local` tokens up
     to each query's position.  K, V: lists of [Hkv, >= lens[b], d].  Returns
     out [T, Hq, d], lse [T, Hq] and, for error bounds, A = sum_j p_j |V_j| and
-    the largest sum |q_e K_e| / sqrt(d) of every row."""
-    return _attention(q, K, V, cu_q, lens, sink, local, None, None)
+    the largest sum |q_e K_e| / sqrt(d) of every row.  tokens: compute these
+    packed tokens only (the others stay as rows without any key)."""
+    return _attention(q, K, V, cu_q, lens, sink, local, None, None, tokens)
 
 
-def prefix_attention(q, Kp, Vp, K, V, cu_q, lens):
+def prefix_attention(q, Kp, Vp, K, V, cu_q, lens, tokens=None):
     """Attention over a prefix [Hkv, n0, d] and causally over each sequence's
     own tokens (lists as in window_attention)."""
-    return _attention(q, K, V, cu_q, lens, 0, 1 << 40, Kp, Vp)
+    return _attention(q, K, V, cu_q, lens, 0, 1 << 40, Kp, Vp, tokens)
 
 
-def _attention(q, K, V, cu_q, lens, sink, local, Kp, Vp):
+def _attention(q, K, V, cu_q, lens, sink, local, Kp, Vp, tokens):
     q = np.asarray(q, dtype=np.float64)
     T, Hq, d = q.shape
     Hkv = K[0].shape[0]
     out, lse = np.zeros((T, Hq, d)), np.full((T, Hq), -np.inf)
     A, zabs = np.zeros((T, Hq, d)), np.zeros((T, Hq))
     seq, pos = positions(cu_q, lens, T)
-    for t in range(T):
+    for t in range(T) if tokens is None else tokens:
         if seq[t] < 0:
             continue
         j = attended(int(pos[t]), sink, local) if sink > 0 else np.arange(max(0, pos[t] - local + 1), pos[t] + 1)

@@ -1,96 +1,934 @@
-// kv_window_attn and kv_prefix_attn: causal attention of packed new tokens.
+// kv_window_attn and kv_prefix_attn: causal attention of packed new tokens on
+// tcgen05 tensor cores.
 //
 //   out[t,h,:] = sum_{j in A(t)} softmax_j(q[t,h].K_j / sqrt(d)) V_j
 // with A(t) the sink and the newest `local` tokens up to t's own position, or
 // a shared prefix and everything up to t's own position behind it.
 //
-// One warp per (token, head): lane l holds dimensions 4l .. 4l + 3, the dot
-// product of a key is a shuffle sum, and the running maximum, sum and output
-// stay in fp32 registers.
+// Rows.  The queries of a KV head's group share its keys, so the rows of one
+// product are (token, head of the group): 256 rows, two 128-row tiles, are an
+// item's queries.  Keys come in tiles of 128 tokens; an item walks the tiles
+// that some row of it attends to (prefix, sink, window), one pass, with the
+// running maximum and sum of every row in registers:
+//   S = Q K^T        128 x 128, K = d        operands in shared memory
+//   P = exp2(S c - m c) in bf16, written over S in TMEM
+//   O += P V         128 x d, K = tokens     P from TMEM, V read MN-major
+// O stays in TMEM; it is rescaled only when a row's maximum has grown by more
+// than 2^8 since the exponents were last based (the factor cancels in the
+// final division, and fp32 and bf16 hold 2^8 as well as 1).  P is rounded to
+// bf16 (the operand type of V; 2^-9 of each weight on average, the size of the
+// rounding of the bf16 output); the sum that divides takes the unrounded fp32
+// values.
+//
+// Work.  Two schedules, chosen by the number of rows (launch_kv_attn):
+//   whole  many items: CTA c takes items c, c + G, ... whole, heaviest first.
+//   split  few items: the tiles of all items are laid end to end and every CTA
+//          takes an equal range of that line; an item that several CTAs share
+//          leaves partial (max, sum, O) rows in the workspace and merge_kernel
+//          joins them.  With a shared prefix its queries are one sequence of
+//          their own (all tokens of the batch, 256 rows to an item), so that
+//          the prefix is read once per 256 rows and not once per sequence.
+// The line is planned on the device, by every CTA for itself, from the
+// lengths: nothing about them is known to the host.
+//
+// Roles (352 threads):
+//   warps 0-3, 4-7  softmax: group s owns accumulators S_s and O_s, thread r
+//            row r.  An item of more than 128 rows gives each group a query
+//            tile (pair); a smaller one gives the groups alternate key tiles
+//            (parity), each with its own statistics and partial rows.
+//   warp 8   K and Q loads, warp 9  V loads (TMA, 64-row boxes: a page holds
+//            at least 64 tokens, so a box never leaves its page).  Boxes that
+//            no row attends to are not loaded.
+//   warp 10  MMA issue.
+// Rows of V that no row of the item attends to may hold anything (0 x NaN is
+// NaN): the softmax threads zero them in shared memory.
+#include <cuda.h>
+
 #include "common.cuh"
 #include "internal.h"
+#include "tc.cuh"
 
 namespace qasc {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kTile = 128;                    // tokens of a key tile, rows of a query tile
+constexpr int kItemRows = 2 * kTile;
+constexpr int kHalf = kTile * 128;            // 128 rows x 64 bf16 columns
+constexpr int kTileBytes = 2 * kHalf;
+constexpr int kBox = 64;                      // rows of a K / V box
+constexpr int kBoxBytes = kBox * 128;
+constexpr int kSlots = 2;                     // K slots, V slots
+constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10;
+constexpr int kThreads = 352;
+constexpr int kTmemCols = 512;                // S_0, S_1, O_0, O_1
+constexpr int kMaxSeq = 2048 + 1;             // sequences of the plan (the shared prefix is one)
+constexpr int kMaxEnt = 4608;                 // items per KV head of a split plan (see split_plan)
+constexpr int kPart = 128;                    // floats of a partial row
+// log2(e) / sqrt(128): logits in base-2 units.
+constexpr float kScale = 1.4426950408889634f * 0.08838834764831845f;
+constexpr float kRebase = 8.0f;               // growth of a row's maximum (log2) that rescales O
 
 struct Args {
   KvAttnArgs a;
-  int Hq, Hkv;
+  int B, Hq, Hkv, gsh;      // gsh = log2(Hq / Hkv)
   int64_t n_cap;
+  int split, pre;           // pre: the shared prefix is sequence 0 of the plan (split only)
+  int slot_rows;            // partial rows a CTA may add to an item (split)
+  float* part_o;            // [rows][128]
+  float2* part_ml;          // [rows] (max in log2 units, sum)
+  int32_t* plan;            // [kMaxSeq + 1] ent_base, [kMaxEnt + 1] line: for the merge
   unsigned* err;
 };
 
-__global__ void __launch_bounds__(32 * kWarps) kv_attn_rows_kernel(const Args p) {
-  const KvAttnArgs& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  pdl_wait();
-  if (row >= a.bt.T * p.Hq) return;
-  const int64_t t = row / p.Hq;
-  const int h = static_cast<int>(row - t * p.Hq), g = h / (p.Hq / p.Hkv);
-  const TokenAt at = token_of(a.bt, t);
-  if (at.b < 0) return;
-  int64_t pos = at.pos;
-  if (pos >= p.n_cap) {
-    record_error(p.err, kErrBadPage);
-    pos = p.n_cap - 1;
+struct Smem {
+  uint8_t q[2][kTileBytes];
+  uint8_t k[kSlots][kTileBytes];
+  uint8_t v[kSlots][kTileBytes];
+  uint64_t q_full, q_empty;
+  uint64_t k_full[kSlots], k_empty[kSlots];
+  uint64_t v_full[kSlots], v_empty[kSlots];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint32_t tmem_base;
+  int32_t scan[kThreads / 32 + 1];
+  int32_t ent_base[kMaxSeq + 1];   // split: items per KV head before sequence s
+  int32_t line[kMaxEnt + 1];       // split: tiles before entry e (all KV heads); whole: items before sequence s
+};
+
+struct Seq {
+  int q0, ql, len, b;   // first token, tokens, cached tokens; b < 0: the shared prefix
+};
+
+__device__ __forceinline__ int clampi(int64_t v, int64_t lo, int64_t hi) {
+  return static_cast<int>(v < lo ? lo : (v > hi ? hi : v));
+}
+
+__device__ __forceinline__ Seq seq_of(const Args& p, int s) {
+  const Batch& bt = p.a.bt;
+  Seq r;
+  if (p.pre && s == 0) {
+    r.b = -1;
+    r.q0 = bt.cu_q ? clampi(__ldg(bt.cu_q), 0, bt.T) : 0;
+    r.ql = (bt.cu_q ? clampi(__ldg(bt.cu_q + bt.B), r.q0, bt.T) : static_cast<int>(bt.T)) - r.q0;
+    r.len = static_cast<int>(p.a.n_prefix);
+    return r;
   }
-  const uint2 qv = *reinterpret_cast<const uint2*>(a.q + row * kD + 4 * lane);
-  const float2 q0 = bf2_to_f2(qv.x), q1 = bf2_to_f2(qv.y);
-  float M = -INFINITY, L = 0.0f, o0 = 0.0f, o1 = 0.0f, o2 = 0.0f, o3 = 0.0f;
-  auto visit = [&](const PageMap& pm, int b, int64_t j) {
-    int64_t r = cache_row(pm, b, g, p.Hkv, p.n_cap, j);
-    if (r < 0) {
-      record_error(p.err, kErrBadPage);
-      r = 0;
-    }
-    const uint2 kv = __ldg(reinterpret_cast<const uint2*>(a.K + r * kD + 4 * lane));
-    const uint2 vv = __ldg(reinterpret_cast<const uint2*>(a.V + r * kD + 4 * lane));
-    const float2 k0 = bf2_to_f2(kv.x), k1 = bf2_to_f2(kv.y), v0 = bf2_to_f2(vv.x), v1 = bf2_to_f2(vv.y);
-    float z = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
+  r.b = s - p.pre;
+  if (bt.cu_q) {
+    r.q0 = clampi(__ldg(bt.cu_q + r.b), 0, bt.T);
+    r.ql = clampi(__ldg(bt.cu_q + r.b + 1), r.q0, bt.T) - r.q0;
+  } else {
+    r.q0 = r.b;
+    r.ql = 1;
+  }
+  r.len = clampi(__ldg(bt.lens + r.b), 0, p.n_cap);
+  return r;
+}
+
+// Query rows r0 .. r0 + rows - 1 of a sequence for KV head g, and the key
+// tiles that they attend to: np of the prefix, ns of the sink in front of the
+// window, then those of the window from w0 on.
+struct Item {
+  Seq s;
+  int g, r0, rows;
+  int p0, p1;         // positions of the first and last row
+  int lo, hi;         // own tokens attended by some row: [0, min(sink, hi + 1)) and [lo, hi]
+  int np, ns, w0, cnt;
+};
+
+__device__ __forceinline__ int ceil_tiles(int64_t n) { return static_cast<int>((n + kTile - 1) / kTile); }
+
+__device__ __forceinline__ Item make_item(const Args& p, const Seq& s, int qt, int g) {
+  Item it;
+  it.s = s;
+  it.g = g;
+  it.r0 = qt * kItemRows;
+  it.rows = min(kItemRows, (s.ql << p.gsh) - it.r0);
+  it.ns = 0;
+  it.w0 = 0;
+  it.p0 = s.len - s.ql + (it.r0 >> p.gsh);
+  it.p1 = s.len - s.ql + ((it.r0 + it.rows - 1) >> p.gsh);
+  it.lo = 0;
+  it.hi = -1;
+  if (s.b < 0) {
+    it.np = ceil_tiles(p.a.n_prefix);
+    it.cnt = it.np;
+    return it;
+  }
+  it.np = p.pre ? 0 : ceil_tiles(p.a.n_prefix);
+  it.cnt = it.np;
+  if (it.p1 >= 0) {
+    const int64_t lo = static_cast<int64_t>(it.p0) - p.a.local + 1;
+    it.lo = static_cast<int>(lo > 0 ? lo : 0);
+    it.hi = it.p1;
+    it.w0 = it.lo / kTile;
+    it.ns = min(ceil_tiles(min(static_cast<int64_t>(p.a.sink), static_cast<int64_t>(it.hi) + 1)), it.w0);
+    it.cnt += it.ns + it.hi / kTile - it.w0 + 1;
+  }
+  return it;
+}
+
+// Key tile k of an item: first token, and whether it is of the prefix.
+__device__ __forceinline__ int tile_token(const Item& it, int k, bool* prefix) {
+  *prefix = k < it.np;
+  const int t = k < it.np ? k : (k - it.np < it.ns ? k - it.np : it.w0 + (k - it.np - it.ns));
+  return t * kTile;
+}
+
+// Token j (of a prefix tile or an own one) is attended by some row of the item.
+__device__ __forceinline__ bool any_row_sees(const Args& p, const Item& it, bool prefix, int j) {
+  if (prefix) return j < p.a.n_prefix;
+  return j <= it.hi && (j >= it.lo || j < p.a.sink);
+}
+// The same for any token of [j, j + kBox).
+__device__ __forceinline__ bool any_row_sees_box(const Args& p, const Item& it, bool prefix, int j) {
+  if (prefix) return j < p.a.n_prefix;
+  return j <= it.hi && (j + kBox > it.lo || j < p.a.sink);
+}
+
+// CTA of a line of U tiles over G CTAs (ranges [c U / G, (c + 1) U / G)) that
+// holds position x.
+__device__ __forceinline__ int cta_of(int64_t x, int64_t U, int G) {
+  return static_cast<int>(((x + 1) * G - 1) / U);
+}
+
+// Exclusive prefix sums of arr[0 .. n) in place, arr[n] = total (whole block).
+__device__ void block_scan(Smem& S, int32_t* arr, int n) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (n + kThreads - 1) / kThreads;
+  const int b = min(n, tid * per), e = min(n, b + per);
+  __syncthreads();
+  int sum = 0;
+  for (int i = b; i < e; ++i) sum += arr[i];
+  int inc = sum;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    z *= 0.08838834764831845f;
-    const float m = fmaxf(M, z);
-    const float al = M == -INFINITY ? 0.0f : expf(M - m);
-    const float w = m == -INFINITY ? 0.0f : expf(z - m);
-    M = m;
-    L = L * al + w;
-    o0 = o0 * al + w * v0.x;
-    o1 = o1 * al + w * v0.y;
-    o2 = o2 * al + w * v1.x;
-    o3 = o3 * al + w * v1.y;
-  };
-  for (int64_t j = 0; j < a.n_prefix; ++j) visit(a.pm_prefix, 0, j);
-  const int64_t lo = a.n_prefix > 0 ? 0 : max(static_cast<int64_t>(0), pos - a.local + 1);
-  const int64_t head = a.n_prefix > 0 ? 0 : min(static_cast<int64_t>(a.sink), lo);
-  for (int64_t j = 0; j < head; ++j) visit(a.pm, at.b, j);
-  for (int64_t j = lo; j <= pos; ++j) visit(a.pm, at.b, j);
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-  const __nv_bfloat162 y0 = __floats2bfloat162_rn(o0 * inv, o1 * inv), y1 = __floats2bfloat162_rn(o2 * inv, o3 * inv);
-  *reinterpret_cast<uint2*>(a.out + row * kD + 4 * lane) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
-  if (a.lse && lane == 0) a.lse[row] = L > 0.0f ? M + logf(L) : -INFINITY;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) S.scan[warp] = inc;
+  __syncthreads();
+  int base = 0;
+  for (int w = 0; w < warp; ++w) base += S.scan[w];
+  int run = base + inc - sum;
+  for (int i = b; i < e; ++i) {
+    const int v = arr[i];
+    arr[i] = run;
+    run += v;
+  }
+  if (tid == kThreads - 1) arr[n] = base + inc;
+  __syncthreads();
+}
+
+// Last i in [0, n) with arr[i] <= x (arr ascending, arr[0] <= x).
+__device__ __forceinline__ int find_last(const int32_t* arr, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (arr[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int q_tiles(const Args& p, const Seq& s) {
+  return ((s.ql << p.gsh) + kItemRows - 1) / kItemRows;
+}
+
+// First partial row of an item's share of CTA c.  Two rows of the area belong
+// to every query row (a parity item leaves two), ordered as the line is; each
+// CTA crossed adds slot_rows, the most rows of one share, so that no two
+// shares overlap.
+__device__ __forceinline__ int64_t part_row(const Args& p, const Item& it, int cta) {
+  const int64_t fam = p.pre && it.s.b >= 0 ? p.a.bt.T * p.Hq : 0;   // the prefix's shares stand first
+  const int64_t row = fam + static_cast<int64_t>(it.s.q0) * p.Hq + static_cast<int64_t>(it.r0) * p.Hkv +
+                      static_cast<int64_t>(it.g) * it.rows;
+  return 2 * row + static_cast<int64_t>(cta) * p.slot_rows;
+}
+
+// The shares of this CTA in order; every role walks them alike.
+struct Piece {
+  Item it;
+  int k0, k1;      // key tiles
+  bool pair;       // two query tiles (or the first alone); else the groups take alternate key tiles
+  bool whole;      // every tile of the item: the output is written, not a partial
+};
+
+struct Walk {
+  int pos, end, step, n;   // split: position on the line, its end; whole: round
+  int e, s;                // split: current entry and its sequence
+  __device__ __forceinline__ void init(const Args& p, const Smem& S, int entries) {
+    n = entries;
+    if (n == 0) {
+      pos = end = 0;
+      return;
+    }
+    const int U = S.line[n];
+    if (p.split) {
+      const int G = min(static_cast<int>(gridDim.x), U);
+      const int c = blockIdx.x;
+      pos = c < G ? static_cast<int>(static_cast<int64_t>(c) * U / G) : 0;
+      end = c < G ? static_cast<int>(static_cast<int64_t>(c + 1) * U / G) : 0;
+      if (pos < end) {
+        e = find_last(S.line, n, pos);
+        s = find_last(S.ent_base, p.B + p.pre, e);
+      }
+    } else {
+      pos = 0;
+      end = (U + gridDim.x - 1) / gridDim.x;
+    }
+  }
+  __device__ __forceinline__ bool next(const Args& p, const Smem& S, Piece& pc) {
+    if (p.split) {
+      if (pos >= end) return false;
+      while (S.line[e + 1] <= pos) ++e;
+      while (S.ent_base[s + 1] <= e) ++s;
+      const Seq sq = seq_of(p, s);
+      const int span = (S.line[e + 1] - S.line[e]) / p.Hkv;   // tiles of the item (an empty item has one, without work)
+      const int rem = pos - S.line[e], g = rem / span, off = rem - g * span;
+      pc.it = make_item(p, sq, e - S.ent_base[s], g);
+      const int take = min(span - off, end - pos);
+      pc.k0 = min(off, pc.it.cnt);
+      pc.k1 = min(off + take, pc.it.cnt);
+      pc.pair = pc.it.rows > kTile;
+      pc.whole = pc.pair && !p.pre && take == span;
+      pos += take;
+      return true;
+    }
+    const int U = n > 0 ? S.line[n] : 0;
+    while (pos < end) {
+      // rounds alternate direction, so that a CTA with a heavy item gets a light one next
+      const int c = (pos & 1) ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
+      const int u = pos * static_cast<int>(gridDim.x) + c;
+      ++pos;
+      if (u >= U) continue;
+      const int x = U - 1 - u;   // late query tiles attend to the most keys
+      const int s2 = find_last(S.line, n, x);
+      const Seq sq = seq_of(p, s2);
+      const int rem = x - S.line[s2];
+      pc.it = make_item(p, sq, rem / p.Hkv, rem % p.Hkv);
+      pc.k0 = 0;
+      pc.k1 = pc.it.cnt;
+      pc.pair = true;
+      pc.whole = true;
+      return true;
+    }
+    return false;
+  }
+};
+
+// 3-D tiled tensor copy: x innermost (elements), y, z.
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int32_t x, int32_t y, int32_t z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+// 32 columns of this thread's TMEM lane, from registers r[0 .. 32).
+#define KV_TMEM_LD32(addr, r)                                                                                         \
+  asm volatile(                                                                                                       \
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"       \
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"                                              \
+      : "=f"((r)[0]), "=f"((r)[1]), "=f"((r)[2]), "=f"((r)[3]), "=f"((r)[4]), "=f"((r)[5]), "=f"((r)[6]),             \
+        "=f"((r)[7]), "=f"((r)[8]), "=f"((r)[9]), "=f"((r)[10]), "=f"((r)[11]), "=f"((r)[12]), "=f"((r)[13]),         \
+        "=f"((r)[14]), "=f"((r)[15]), "=f"((r)[16]), "=f"((r)[17]), "=f"((r)[18]), "=f"((r)[19]), "=f"((r)[20]),      \
+        "=f"((r)[21]), "=f"((r)[22]), "=f"((r)[23]), "=f"((r)[24]), "=f"((r)[25]), "=f"((r)[26]), "=f"((r)[27]),      \
+        "=f"((r)[28]), "=f"((r)[29]), "=f"((r)[30]), "=f"((r)[31])                                                    \
+      : "r"(addr))
+#define KV_TMEM_ST32(addr, r)                                                                                         \
+  asm volatile(                                                                                                       \
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"    \
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),                                   \
+      "r"((r)[0]), "r"((r)[1]), "r"((r)[2]), "r"((r)[3]), "r"((r)[4]), "r"((r)[5]), "r"((r)[6]), "r"((r)[7]),         \
+      "r"((r)[8]), "r"((r)[9]), "r"((r)[10]), "r"((r)[11]), "r"((r)[12]), "r"((r)[13]), "r"((r)[14]),                 \
+      "r"((r)[15]), "r"((r)[16]), "r"((r)[17]), "r"((r)[18]), "r"((r)[19]), "r"((r)[20]), "r"((r)[21]),               \
+      "r"((r)[22]), "r"((r)[23]), "r"((r)[24]), "r"((r)[25]), "r"((r)[26]), "r"((r)[27]), "r"((r)[28]),               \
+      "r"((r)[29]), "r"((r)[30]), "r"((r)[31])                                                                       \
+      : "memory")
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Bits [0, n) of a word, n any integer.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_attn_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    mbar_init(&S.q_full, 1);
+    mbar_init(&S.q_empty, 1);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&S.k_full[i], 1);
+      mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.v_full[i], 1);
+      mbar_init(&S.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], 4);
+      mbar_init(&S.o_full[i], 1);
+    }
+    fence_barrier_init();
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  if (warp == kMmaWarp) tmem_alloc(&S.tmem_base, kTmemCols);
+  pdl_wait();
+
+  // ---- the plan
+  const int NS = p.B + p.pre;
+  int entries;
+  for (int s = tid; s < NS; s += kThreads) {
+    const Seq sq = seq_of(p, s);
+    if (blockIdx.x == 0 && sq.b >= 0 && __ldg(p.a.bt.lens + sq.b) != sq.len) record_error(p.err, kErrBadPage);
+    if (p.split) S.ent_base[s] = q_tiles(p, sq);
+    else S.line[s] = q_tiles(p, sq) * p.Hkv;
+  }
+  if (p.split) {
+    block_scan(S, S.ent_base, NS);
+    entries = min(S.ent_base[NS], kMaxEnt);
+    for (int e = tid; e < entries; e += kThreads) {
+      const int s = find_last(S.ent_base, NS, e);
+      const Item it = make_item(p, seq_of(p, s), e - S.ent_base[s], 0);
+      S.line[e] = max(1, it.cnt) * p.Hkv;
+    }
+    block_scan(S, S.line, entries);
+    if (blockIdx.x == 0) {
+      for (int i = tid; i <= NS; i += kThreads) p.plan[i] = S.ent_base[i];
+      for (int i = tid; i <= entries; i += kThreads) p.plan[kMaxSeq + 1 + i] = S.line[i];
+    }
+  } else {
+    block_scan(S, S.line, NS);
+    entries = NS;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+
+  Walk walk;
+  walk.init(p, S, entries);
+  Piece pc;
+  int kt = 0;            // key tiles of the CTA so far: slot kt & 1, phase (kt >> 1) & 1
+  bool dead = false;
+  if (warp == kKWarp || warp == kVWarp) {
+    // ---- loads: lanes 0-3 issue the two 64-column halves of the two boxes
+    const bool is_k = warp == kKWarp;
+    const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+    const int h = (lane >> 1) & 1, half = lane & 1;
+    int pieces = 0;
+    while (!dead && walk.next(p, S, pc)) {
+      const int n = pc.k1 - pc.k0;
+      if (n == 0) continue;
+      int64_t row = -1;   // of lane's box in the current batch of 16 tiles
+      for (int i = 0; i < n; ++i) {
+        if ((i & 15) == 0) {
+          const int k = pc.k0 + i + (lane >> 1);
+          row = -1;
+          if (k < pc.k1) {
+            bool prefix;
+            const int tok = tile_token(pc.it, k, &prefix) + (lane & 1) * kBox;
+            if (any_row_sees_box(p, pc.it, prefix, tok)) {
+              row = cache_row(prefix ? p.a.pm_prefix : p.a.pm, prefix ? 0 : pc.it.s.b, pc.it.g, p.Hkv, p.n_cap, tok);
+              if (row < 0) {
+                record_error(p.err, kErrBadPage);
+                row = 0;
+              }
+            }
+          }
+        }
+        const int src = 2 * (i & 15);
+        const int64_t row0 = __shfl_sync(0xffffffffu, row, src), row1 = __shfl_sync(0xffffffffu, row, src + 1);
+        const int slot = kt & 1;
+        uint64_t* full = is_k ? &S.k_full[slot] : &S.v_full[slot];
+        uint64_t* empty = is_k ? &S.k_empty[slot] : &S.v_empty[slot];
+        const bool ok = mbar_wait(empty, ((kt >> 1) & 1u) ^ 1u);
+        if (!__all_sync(0xffffffffu, ok)) {
+          record_error(p.err, kErrTimeout);
+          dead = true;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(full, ((row0 >= 0) + (row1 >= 0)) * 2 * kBoxBytes);
+        __syncwarp();
+        const int64_t y = h ? row1 : row0;
+        if (lane < 4 && y >= 0) {
+          uint8_t* dst = (is_k ? S.k[slot] : S.v[slot]) + half * kHalf + h * kBoxBytes;
+          tma_load_2d(dst, tm, half * 64, static_cast<int32_t>(y), full);
+        }
+        ++kt;
+        if (is_k && i == 0) {
+          // the item's queries, behind its first keys: their buffers are free
+          // only once the last product of the previous item has read them
+          const bool okq = mbar_wait(&S.q_empty, (pieces & 1u) ^ 1u);
+          if (!__all_sync(0xffffffffu, okq)) {
+            record_error(p.err, kErrTimeout);
+            dead = true;
+            break;
+          }
+          const int tiles = pc.it.rows > kTile ? 2 : 1;
+          if (lane == 0) mbar_arrive_expect_tx(&S.q_full, tiles * kTileBytes);
+          __syncwarp();
+          if (lane < 2 * tiles)
+            tma_load_3d(S.q[h] + half * kHalf, &tm_q, half * 64, pc.it.g << p.gsh,
+                        pc.it.s.q0 + ((pc.it.r0 + h * kTile) >> p.gsh), &S.q_full);
+          ++pieces;
+        }
+      }
+    }
+    // nothing of this warp stays in flight past here
+    for (int i = kt > kSlots ? kt - kSlots : 0; i < kt; ++i)
+      mbar_wait(is_k ? &S.k_full[i & 1] : &S.v_full[i & 1], (i >> 1) & 1u);
+    if (is_k && pieces > 0) mbar_wait(&S.q_full, (pieces - 1) & 1u);
+  } else if (warp == kMmaWarp) {
+    // ---- MMA issue (one thread)
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = mma_idesc(128, 128);
+      constexpr uint32_t idesc_o = mma_idesc(128, 128) | (1u << 16);   // B (V) MN-major
+      int pieces = 0;
+      uint32_t np[2] = {0, 0};   // probabilities taken of each group
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead && !mbar_wait(bar, parity)) {
+          record_error(p.err, kErrTimeout);
+          dead = true;
+        }
+      };
+      auto qk = [&](int s, int qtile, int t) {   // S_s = Q_qtile K_t^T
+        tc_fence_after();
+        const uint32_t qb = smem_u32(S.q[qtile]), kb = smem_u32(S.k[t & 1]);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16(tmem + kTile * s, sw128_desc(qb + (kk >> 2) * kHalf + (kk & 3) * 32),
+                   sw128_desc(kb + (kk >> 2) * kHalf + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
+        mma_commit(&S.s_full[s]);
+      };
+      auto pv = [&](int s, int t, bool first) {   // O_s (+)= P_s V_t
+        wait(&S.p_full[s], np[s] & 1u);
+        if (dead) return;
+        ++np[s];
+        tc_fence_after();
+        const uint32_t vb = smem_u32(S.v[t & 1]);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_ta(tmem + 256 + kTile * s, tmem + kTile * s + 8 * kk, sw128_mn_desc(vb + kk * 2048, kHalf, 1024),
+                      idesc_o, (kk > 0 || !first) ? 1u : 0u);
+      };
+      while (!dead && walk.next(p, S, pc)) {
+        const int n = pc.k1 - pc.k0;
+        if (n == 0) continue;
+        wait(&S.q_full, pieces & 1u);
+        ++pieces;
+        if (pc.pair) {
+          const int nt = pc.it.rows > kTile ? 2 : 1;
+          for (int k = -1; k < n && !dead; ++k) {
+            if (k >= 0) wait(&S.v_full[(kt + k) & 1], ((kt + k) >> 1) & 1u);
+            for (int s = 0; s < nt && !dead; ++s) {
+              if (k >= 0) {
+                pv(s, kt + k, k == 0);
+                if (dead) break;
+                if (k == n - 1) mma_commit(&S.o_full[s]);
+                if (s == nt - 1) mma_commit(&S.v_empty[(kt + k) & 1]);
+              }
+              if (k + 1 < n) {
+                if (s == 0) wait(&S.k_full[(kt + k + 1) & 1], ((kt + k + 1) >> 1) & 1u);
+                if (dead) break;
+                qk(s, s, kt + k + 1);
+                if (s == nt - 1) {
+                  mma_commit(&S.k_empty[(kt + k + 1) & 1]);
+                  if (k + 1 == n - 1) mma_commit(&S.q_empty);
+                }
+              }
+            }
+          }
+        } else {
+          for (int k = -2; k < n && !dead; ++k) {
+            if (k >= 0) {
+              wait(&S.v_full[(kt + k) & 1], ((kt + k) >> 1) & 1u);
+              pv(k & 1, kt + k, k < 2);
+              if (dead) break;
+              mma_commit(&S.v_empty[(kt + k) & 1]);
+              if (k >= n - 2) mma_commit(&S.o_full[k & 1]);
+            }
+            if (k + 2 < n) {
+              wait(&S.k_full[(kt + k + 2) & 1], ((kt + k + 2) >> 1) & 1u);
+              if (dead) break;
+              qk(k & 1, 0, kt + k + 2);
+              mma_commit(&S.k_empty[(kt + k + 2) & 1]);
+              if (k + 2 == n - 1) mma_commit(&S.q_empty);
+            }
+          }
+        }
+        kt += n;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax and output: group s = warp / 4, row r of its tile
+    const int s = warp >> 2, r = tid & 127;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + kTile * s + lane_base, to = tmem + 256 + kTile * s + lane_base;
+    uint32_t ns = 0, no = 0;   // accumulators S_s, O_s taken
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (dead) return;
+      const bool ok = mbar_wait(bar, parity);
+      if (!__all_sync(0xffffffffu, ok)) {
+        record_error(p.err, kErrTimeout);
+        dead = true;
+      }
+    };
+    while (!dead && walk.next(p, S, pc)) {
+      const Item& it = pc.it;
+      const int n = pc.k1 - pc.k0;
+      const int row = pc.pair ? kTile * s + r : r;         // of the item
+      const bool active = row < it.rows;                   // the row exists
+      if (pc.pair && kTile * s >= it.rows) {               // no second query tile
+        kt += n;
+        continue;
+      }
+      const int pos = it.p0 - (it.r0 >> p.gsh) + ((it.r0 + row) >> p.gsh);
+      float m = -INFINITY, l = 0.0f;
+      int done = 0;
+      for (int k = 0; k < n && !dead; ++k, ++kt) {
+        if (!pc.pair && (k & 1) != s) continue;
+        bool prefix;
+        const int t0 = tile_token(it, pc.k0 + k, &prefix);
+        const int last = t0 + kTile - 1;
+        wait(&S.s_full[s], ns & 1u);
+        if (dead) break;
+        ++ns;
+        tc_fence_after();
+        // rows of V that nobody attends to are zeroed, by the group whose
+        // product reads the tile first.  (The wait stands behind that for S:
+        // S of this tile was issued after the product with the V slot's last
+        // tile, so that V load is over and the phase is not mistaken for it.)
+        const bool clean = prefix ? last >= p.a.n_prefix : !(last <= it.hi && (t0 >= it.lo || last < p.a.sink));
+        if (clean && (!pc.pair || s == 0)) {
+          wait(&S.v_full[kt & 1], (kt >> 1) & 1u);
+          if (dead) break;
+          if (!any_row_sees(p, it, prefix, t0 + r)) {
+            uint4* v0 = reinterpret_cast<uint4*>(S.v[kt & 1] + r * 128);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v0[i] = v0[i + kHalf / 16] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_async_smem();
+        }
+        if ((warp & 3) * 32 < it.rows - (pc.pair ? kTile * s : 0)) {   // the warp has a row
+          float z[128];
+          KV_TMEM_LD32(ts, z);
+          KV_TMEM_LD32(ts + 32, z + 32);
+          KV_TMEM_LD32(ts + 64, z + 64);
+          KV_TMEM_LD32(ts + 96, z + 96);
+          tmem_wait_ld();
+          const bool all = prefix ? last < p.a.n_prefix
+                                  : last <= it.p0 && (static_cast<int64_t>(t0) > static_cast<int64_t>(it.p1) - p.a.local ||
+                                                      last < p.a.sink);
+          if (!all) {
+            const int64_t lo64 = static_cast<int64_t>(pos) - p.a.local + 1 - t0;
+            const int lo = clampi(lo64, 0, kTile), hi = prefix ? static_cast<int>(p.a.n_prefix) - t0 : pos - t0 + 1;
+            const int sk = prefix ? kTile : p.a.sink - t0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t keep = below(hi - 32 * w) & (~below(lo - 32 * w) | below(sk - 32 * w));
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!((keep >> c) & 1u)) z[32 * w + c] = -INFINITY;
+            }
+          }
+          float mx = fmaxf(z[0], z[1]);
+#pragma unroll
+          for (int c = 2; c < 128; c += 2) mx = fmaxf(mx, fmaxf(z[c], z[c + 1]));
+          if (done == 0) {
+            m = mx;
+          } else {
+            const float mn = fmaxf(m, mx);
+            const bool grow = (mn - m) * kScale > kRebase;   // also from -inf
+            if (__any_sync(0xffffffffu, grow)) {
+              const float al = grow ? ex2_approx((m - mn) * kScale) : 1.0f;
+              l *= al;
+              if (grow) m = mn;
+              // S_s complete means that the product before it (O_s) is, too
+#pragma unroll 1
+              for (int c = 0; c < 128; c += 32) {
+                float o[32];
+                KV_TMEM_LD32(to + c, o);
+                tmem_wait_ld();
+                uint32_t u[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * al);
+                KV_TMEM_ST32(to + c, u);
+              }
+            }
+          }
+          const float mc = m == -INFINITY ? 0.0f : m * kScale;
+          float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t u[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float2 x = __ffma2_rn(make_float2(z[64 * q + 2 * i], z[64 * q + 2 * i + 1]),
+                                          make_float2(kScale, kScale), make_float2(-mc, -mc));
+              const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+              acc[i & 1] = __fadd2_rn(acc[i & 1], e);
+              u[i] = pack_bf16(e.x, e.y);
+            }
+            KV_TMEM_ST32(ts + 32 * q, u);
+          }
+          l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+          tmem_wait_st();
+        }
+        ++done;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[s]);
+      }
+      if (dead) break;
+      if (done > 0) {
+        wait(&S.o_full[s], no & 1u);
+        if (dead) break;
+        ++no;
+        tc_fence_after();
+      }
+      if ((warp & 3) * 32 < it.rows - (pc.pair ? kTile * s : 0)) {
+        const int64_t orow = (static_cast<int64_t>(it.s.q0) + ((it.r0 + row) >> p.gsh)) * p.Hq + (it.g << p.gsh) +
+                             ((it.r0 + row) & ((1 << p.gsh) - 1));
+        const int64_t prow = part_row(p, it, blockIdx.x) + (pc.pair ? row : s * it.rows + row);
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          float o[32];
+          if (done > 0) {
+            KV_TMEM_LD32(to + c, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+          }
+          if (active && pc.whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.a.out + orow * kD + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                  pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                  pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                  pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+          } else if (active && l > 0.0f) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kPart + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+          __syncwarp();
+        }
+        if (active) {
+          if (!pc.whole) p.part_ml[prow] = make_float2(m * kScale, l);
+          else if (p.a.lse) p.a.lse[orow] = l > 0.0f ? (m * kScale + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        }
+        tc_fence_before();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  pdl_trigger();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the partial rows of the items that more than one share (or group)
+// computed: exact log-sum-exp, fp32.  A block per row, warp w taking the
+// partials w, w + 4, ...; lane l holds dimensions 4l .. 4l + 3.
+constexpr int kMergeWarps = 4;
+
+__global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const Args p, int grid) {
+  __shared__ float2 ml[kMergeWarps];
+  __shared__ float4 ov[kMergeWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  const int NS = p.B + p.pre;
+  const int32_t* ent_base = p.plan;
+  const int32_t* line = p.plan + kMaxSeq + 1;
+  const int entries = min(__ldcg(ent_base + NS), kMaxEnt);
+  const int U = entries > 0 ? __ldcg(line + entries) : 0;
+  const int G = min(grid, U);
+  const int64_t rows = p.a.bt.T * p.Hq;
+  for (int64_t orow = blockIdx.x; orow < rows; orow += gridDim.x) {
+    const int64_t t = orow / p.Hq;
+    const int h = static_cast<int>(orow - t * p.Hq);
+    const int g = h >> p.gsh, hh = h & ((1 << p.gsh) - 1);
+    const TokenAt at = token_of(p.a.bt, t);
+    if (at.b < 0) continue;
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    bool direct = false;
+    int seen = 0;   // partials of earlier families
+    for (int f = 0; f <= p.pre; ++f) {
+      const int s = f < p.pre ? 0 : at.b + p.pre;
+      const Seq sq = seq_of(p, s);
+      const int lr = ((static_cast<int>(t) - sq.q0) << p.gsh) + hh;
+      const int qt = lr / kItemRows, e = __ldcg(ent_base + s) + qt;
+      if (lr < 0 || e >= entries) continue;   // lengths that contradict one another
+      const Item it = make_item(p, sq, qt, g);
+      const int64_t span = max(1, it.cnt);
+      const int64_t x0 = __ldcg(line + e) + g * span;
+      const int c0 = cta_of(x0, U, G), c1 = cta_of(x0 + span - 1, U, G);
+      const bool pair = it.rows > kTile;
+      if (pair && c0 == c1 && !p.pre) {   // its share has written the output
+        direct = true;
+        break;
+      }
+      const int row = lr - it.r0;
+      const int subs = pair ? 1 : 2, count = (c1 - c0 + 1) * subs;
+      for (int i = (warp + kMergeWarps - seen % kMergeWarps) % kMergeWarps; i < count; i += kMergeWarps) {
+        const int64_t prow = part_row(p, it, c0 + i / subs) + (pair ? row : (i % subs) * it.rows + row);
+        const float2 v = __ldcg(p.part_ml + prow);
+        if (v.y > 0.0f) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + prow * kPart) + lane);
+          const float mn = fmaxf(m, v.x);
+          const float a = ex2_approx(m - mn), b = ex2_approx(v.x - mn);
+          m = mn;
+          l = l * a + v.y * b;
+          o = make_float4(o.x * a + x.x * b, o.y * a + x.y * b, o.z * a + x.z * b, o.w * a + x.w * b);
+        }
+      }
+      seen += count;
+    }
+    if (direct) continue;
+    if (lane == 0) ml[warp] = make_float2(m, l);
+    ov[warp][lane] = o;
+    __syncthreads();
+    if (warp == 0) {
+      float mt = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) mt = fmaxf(mt, ml[w].x);
+      float lt = 0.0f;
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) {
+        const float b = ml[w].y > 0.0f ? ex2_approx(ml[w].x - mt) : 0.0f;
+        const float4 x = ov[w][lane];
+        lt += ml[w].y * b;
+        y = make_float4(y.x + x.x * b, y.y + x.y * b, y.z + x.z * b, y.w + x.w * b);
+      }
+      const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
+      *reinterpret_cast<uint2*>(p.a.out + orow * kD + 4 * lane) =
+          make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+      if (p.a.lse && lane == 0) p.a.lse[orow] = lt > 0.0f ? (mt + log2f(lt)) * 0.6931471805599453f : -INFINITY;
+    }
+    __syncthreads();
+  }
+  pdl_trigger();
+}
+
+// Few items are split; many are taken whole.  Counted with full tiles only
+// (T * Gq / 256 per KV head), which every batch has at least.  A split plan has
+// at most T Gq / 256 + B entries (T Gq / 256 + 1 more for a shared prefix):
+//   T Gq / 256 Hkv < 4 SMs, or Gq T < 128 B with a shared prefix,
+// so below 2 (1024 + 1) + 2048 of kMaxEnt on any device of up to 256 SMs.
+bool split_plan(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms) {
+  const int64_t gq = Hq / Hkv;
+  const int64_t items = (T * gq + kItemRows - 1) / kItemRows * Hkv;
+  if (prefix && T * gq < static_cast<int64_t>(kTile) * B) return true;
+  return items < 4 * static_cast<int64_t>(num_sms);
+}
+
+struct Layout {
+  size_t off_o = 0, off_ml = 0, off_plan = 0, total = 256;
+  int slot_rows = 0;
+};
+
+Layout layout_of(int64_t T, int Hq, int Hkv, bool prefix, int num_sms) {
+  Layout L;
+  const int64_t most = 2 * T * (Hq / Hkv);
+  L.slot_rows = static_cast<int>(most < kItemRows ? most : kItemRows);
+  const int64_t rows = 2 * T * Hq * (prefix ? 2 : 1) + static_cast<int64_t>(num_sms) * L.slot_rows;
+  L.off_o = 0;
+  L.off_ml = align_up(static_cast<size_t>(rows) * kPart * sizeof(float), 256);
+  L.off_plan = align_up(L.off_ml + static_cast<size_t>(rows) * sizeof(float2), 256);
+  L.total = align_up(L.off_plan + (kMaxSeq + 1 + kMaxEnt + 1) * sizeof(int32_t), 256);
+  return L;
+}
+
+int encode_q(CUtensorMap* m, const uint16_t* q, int64_t T, int Hq, int gq, EncodeTiledFn enc) {
+  const uint64_t gdim[3] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(Hq), static_cast<uint64_t>(T)};
+  const uint64_t gstride[2] = {kD * 2, static_cast<uint64_t>(Hq) * kD * 2};
+  const unsigned box[3] = {64, static_cast<unsigned>(gq), static_cast<unsigned>(kTile / gq)};
+  const unsigned estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(q), gdim, gstride, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+int encode_rows(CUtensorMap* m, const uint16_t* base, int64_t rows, EncodeTiledFn enc) {
+  const uint64_t gdim[2] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(rows)};
+  const uint64_t gstride[1] = {kD * 2};
+  const unsigned box[2] = {64, kBox};
+  const unsigned estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(base), gdim, gstride, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 }  // namespace
 
-size_t kv_attn_workspace_bytes(int64_t, int, int, int, bool, int) { return 256; }
+size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms) {
+  // For the most SMs: a device with fewer splits a subset of these batches.
+  return split_plan(T, B, Hq, Hkv, prefix, num_sms) ? layout_of(T, Hq, Hkv, prefix, num_sms).total : 256;
+}
 
-cudaError_t configure_kv_attn_kernels(const DeviceInfo&) { return cudaSuccess; }
+cudaError_t configure_kv_attn_kernels(const DeviceInfo&) {
+  return cudaFuncSetAttribute(kv_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(sizeof(Smem) + 1024));
+}
 
-int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t*, const DeviceInfo& dev, cudaStream_t stream) {
+int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const int gq = s.Hq / s.Hkv;
+  alignas(64) CUtensorMap tq, tk, tv;
+  if (encode_q(&tq, a.q, a.bt.T, s.Hq, gq, enc) != 0 || encode_rows(&tk, a.K, a.cache_rows, enc) != 0 ||
+      encode_rows(&tv, a.V, a.cache_rows, enc) != 0)
+    return cudaErrorInvalidValue;
   Args p;
   p.a = a;
+  p.B = s.B;
   p.Hq = s.Hq;
   p.Hkv = s.Hkv;
+  p.gsh = gq == 8 ? 3 : (gq == 4 ? 2 : (gq == 2 ? 1 : 0));
   p.n_cap = s.n_cap;
+  const bool prefix = a.n_prefix > 0;
+  p.split = split_plan(a.bt.T, s.B, s.Hq, s.Hkv, prefix, dev.num_sms);
+  p.pre = p.split && prefix;
+  const Layout L = layout_of(a.bt.T, s.Hq, s.Hkv, prefix, dev.num_sms);
+  p.slot_rows = L.slot_rows;
+  p.part_o = reinterpret_cast<float*>(ws + L.off_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);
+  p.plan = reinterpret_cast<int32_t*>(ws + L.off_plan);
   p.err = dev.err_word;
-  const int64_t rows = a.bt.T * s.Hq;
-  return launch_dependent(kv_attn_rows_kernel, dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps)),
-                          dim3(32 * kWarps), 0, stream, 1, p);
+  const cudaError_t e = launch_dependent(kv_attn_kernel, dim3(dev.num_sms), dim3(kThreads), sizeof(Smem) + 1024, stream,
+                                         1, p, tq, tk, tv);
+  if (e != cudaSuccess || !p.split) return e;
+  const int64_t rows = a.bt.T * s.Hq, most = static_cast<int64_t>(dev.num_sms) * 16;
+  return launch_dependent(kv_merge_kernel, dim3(static_cast<unsigned>(rows < most ? rows : most)),
+                          dim3(32 * kMergeWarps), 0, stream, 1, p, dev.num_sms);
 }
 
 }  // namespace qasc

@@ -344,6 +344,50 @@ def test_window_flat_and_peaked_logits(scale):
     check_rows(out, lse, ref, n)
 
 
+LARGE = [2048, 1, 0, 33, 500, 1, 64]       # enough rows that items are taken whole
+
+
+@pytest.mark.parametrize("Hq,Hkv,sink,local", [(64, 8, 4, 300), (64, 8, 0, 1 << 30), (64, 32, 150, 70)])
+def test_window_of_many_rows(Hq, Hkv, sink, local):
+    ql = LARGE
+    lens = [2048, 700, 90, 40, 777, 5, 900]
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    T = cu[-1]
+    pages = Pages(lens, Hkv, 64, cdiv(max(lens), 64) + 1, seed=61)
+    q = rand((T, Hq, 128), 62)
+    rng = np.random.default_rng(63)
+    some = sorted({0, 1, 2, 62, 63, 64, 127, 128, 2047, *cu[1:3], cu[3], *range(cu[3], cu[4], 8), cu[4], T - 65, T - 64, T - 1,
+                   *rng.integers(0, T, 24).tolist()})
+    ref = osv.window_attention(f64(q), *pages.caches(), cu, lens, sink, local, tokens=some)
+    pages.hide(2, 0, 90)
+    out, lse = window(q, pages, cu, lens, sink, local, Hkv)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    check_rows(out, lse, ref, max(lens), rows=some)
+
+
+def test_prefix_of_many_rows():
+    # long own parts: the prefix is walked by each sequence's items
+    Hq, Hkv, P, n0, ql = 64, 8, 64, 333, LARGE
+    lens = [2048, 700, 90, 40, 777, 0, 60]
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    T = cu[-1]
+    both = Pages([n0] + lens, Hkv, P, 34, seed=64)
+    q = rand((T, Hq, 128), 65)
+    some = sorted({0, 63, 64, 1000, 2047, cu[1], cu[3], cu[4] - 1, cu[5], T - 64, T - 60, T - 1})
+    Kc, Vc = both.caches()
+    ref = osv.prefix_attention(f64(q), Kc[0], Vc[0], Kc[1:], Vc[1:], cu, lens, tokens=some)
+    K, V, table = both.cuda()
+    out = torch.full((T, Hq, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, Hq), float("nan"), dtype=torch.float32, device="cuda")
+    ws = qasc.alloc_workspace(qasc.kv_prefix_attn_workspace_bytes(T, len(ql), Hq, Hkv, both.pps * P))
+    c, ln = batch_tensors(cu, lens)
+    qasc.kv_prefix_attn_paged(q.cuda(), K, V, table[0, :cdiv(n0, P)].contiguous(), table[1:].contiguous(), ln, out, ws,
+                              n_prefix=n0, cu_q=c, lse=lse)
+    qasc.qasc_device_error()
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    check_rows(out, lse, ref, n0 + max(lens), rows=some)
+
+
 def test_window_growing_maximum():
     # every later key scores higher: the running maximum moves in every tile
     Hq, Hkv, P, n = 8, 2, 64, 1500
