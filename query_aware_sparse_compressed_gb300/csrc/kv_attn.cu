@@ -31,7 +31,7 @@
 // The line is planned on the device, by every CTA for itself, from the
 // lengths: nothing about them is known to the host.
 //
-// Roles (352 threads):
+// Roles (384 threads):
 //   warps 0-3, 4-7  softmax: group s owns accumulators S_s and O_s, thread r
 //            row r.  An item of more than 128 rows gives each group a query
 //            tile (pair); a smaller one gives the groups alternate key tiles
@@ -59,7 +59,10 @@ constexpr int kBox = 64;                      // rows of a K / V box
 constexpr int kBoxBytes = kBox * 128;
 constexpr int kSlots = 2;                     // K slots, V slots
 constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10;
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;                 // warp 11 only fills its warpgroup
+// Registers: 384 threads start with 168 each (64512); the softmax warpgroups
+// take 200 and the third keeps 104, the same sum.
+constexpr int kSoftRegs = 200, kOtherRegs = 104;
 constexpr int kTmemCols = 512;                // S_0, S_1, O_0, O_1
 constexpr int kMaxSeq = 2048 + 1;             // sequences of the plan (the shared prefix is one)
 constexpr int kMaxEnt = 4608;                 // items per KV head of a split plan (see split_plan)
@@ -87,7 +90,7 @@ struct Smem {
   uint64_t q_full, q_empty;
   uint64_t k_full[kSlots], k_empty[kSlots];
   uint64_t v_full[kSlots], v_empty[kSlots];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2];   // p_full: the first and last 64 tokens
   uint32_t tmem_base;
   int32_t scan[kThreads / 32 + 1];
   int32_t ent_base[kMaxSeq + 1];   // split: items per KV head before sequence s
@@ -355,11 +358,69 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
       "r"((r)[22]), "r"((r)[23]), "r"((r)[24]), "r"((r)[25]), "r"((r)[26]), "r"((r)[27]), "r"((r)[28]),               \
       "r"((r)[29]), "r"((r)[30]), "r"((r)[31])                                                                       \
       : "memory")
+// Wait for this thread's TMEM loads; r[0 .. 32) may be used from here on (an
+// asm statement that names them, so that no use moves in front of the wait).
+#define KV_TIE16(r)                                                                                                   \
+  asm volatile(""                                                                                                     \
+               : "+f"((r)[0]), "+f"((r)[1]), "+f"((r)[2]), "+f"((r)[3]), "+f"((r)[4]), "+f"((r)[5]), "+f"((r)[6]),    \
+                 "+f"((r)[7]), "+f"((r)[8]), "+f"((r)[9]), "+f"((r)[10]), "+f"((r)[11]), "+f"((r)[12]),               \
+                 "+f"((r)[13]), "+f"((r)[14]), "+f"((r)[15]))
+#define KV_TIE32(r)     \
+  do {                  \
+    KV_TIE16(r);        \
+    KV_TIE16((r) + 16); \
+  } while (0)
+#define KV_TMEM_WAIT32(r) \
+  do {                    \
+    tmem_wait_ld();       \
+    KV_TIE32(r);          \
+  } while (0)
+#define KV_TMEM_ST16(addr, r)                                                                                         \
+  asm volatile(                                                                                                       \
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::    \
+          "r"(addr),                                                                                                  \
+      "f"((r)[0]), "f"((r)[1]), "f"((r)[2]), "f"((r)[3]), "f"((r)[4]), "f"((r)[5]), "f"((r)[6]), "f"((r)[7]),         \
+      "f"((r)[8]), "f"((r)[9]), "f"((r)[10]), "f"((r)[11]), "f"((r)[12]), "f"((r)[13]), "f"((r)[14]), "f"((r)[15])   \
+      : "memory")
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Bounded wait whose tries suspend the thread for up to a millisecond each.
+__device__ __forceinline__ bool try_wait_suspended(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
+  if (try_wait_suspended(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (!try_wait_suspended(bar, parity))
+    if (globaltimer_ns() - t0 > kWaitTimeoutNs) return false;
+  return true;
+}
+// The same for a whole warp.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity));
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // Bits [0, n) of a word, n any integer.
@@ -382,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_full[i], 4);
+      mbar_init(&S.p_full[i][0], 4);
+      mbar_init(&S.p_full[i][1], 4);
       mbar_init(&S.o_full[i], 1);
     }
     fence_barrier_init();
@@ -429,6 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Piece pc;
   int kt = 0;            // key tiles of the CTA so far: slot kt & 1, phase (kt >> 1) & 1
   bool dead = false;
+  if (warp >= kKWarp) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == kKWarp || warp == kVWarp) {
     // ---- loads: lanes 0-3 issue the two 64-column halves of the two boxes
     const bool is_k = warp == kKWarp;
@@ -460,8 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = kt & 1;
         uint64_t* full = is_k ? &S.k_full[slot] : &S.v_full[slot];
         uint64_t* empty = is_k ? &S.k_empty[slot] : &S.v_empty[slot];
-        const bool ok = mbar_wait(empty, ((kt >> 1) & 1u) ^ 1u);
-        if (!__all_sync(0xffffffffu, ok)) {
+        if (!wait_warp(empty, ((kt >> 1) & 1u) ^ 1u)) {
           record_error(p.err, kErrTimeout);
           dead = true;
           break;
@@ -477,8 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (is_k && i == 0) {
           // the item's queries, behind its first keys: their buffers are free
           // only once the last product of the previous item has read them
-          const bool okq = mbar_wait(&S.q_empty, (pieces & 1u) ^ 1u);
-          if (!__all_sync(0xffffffffu, okq)) {
+          if (!wait_warp(&S.q_empty, (pieces & 1u) ^ 1u)) {
             record_error(p.err, kErrTimeout);
             dead = true;
             break;
@@ -495,91 +557,119 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // nothing of this warp stays in flight past here
     for (int i = kt > kSlots ? kt - kSlots : 0; i < kt; ++i)
-      mbar_wait(is_k ? &S.k_full[i & 1] : &S.v_full[i & 1], (i >> 1) & 1u);
-    if (is_k && pieces > 0) mbar_wait(&S.q_full, (pieces - 1) & 1u);
+      wait_warp(is_k ? &S.k_full[i & 1] : &S.v_full[i & 1], (i >> 1) & 1u);
+    if (is_k && pieces > 0) wait_warp(&S.q_full, (pieces - 1) & 1u);
   } else if (warp == kMmaWarp) {
-    // ---- MMA issue (one thread)
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = mma_idesc(128, 128);
-      constexpr uint32_t idesc_o = mma_idesc(128, 128) | (1u << 16);   // B (V) MN-major
-      int pieces = 0;
-      uint32_t np[2] = {0, 0};   // probabilities taken of each group
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!dead && !mbar_wait(bar, parity)) {
-          record_error(p.err, kErrTimeout);
-          dead = true;
-        }
-      };
-      auto qk = [&](int s, int qtile, int t) {   // S_s = Q_qtile K_t^T
-        tc_fence_after();
-        const uint32_t qb = smem_u32(S.q[qtile]), kb = smem_u32(S.k[t & 1]);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_bf16(tmem + kTile * s, sw128_desc(qb + (kk >> 2) * kHalf + (kk & 3) * 32),
-                   sw128_desc(kb + (kk >> 2) * kHalf + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
-        mma_commit(&S.s_full[s]);
-      };
-      auto pv = [&](int s, int t, bool first) {   // O_s (+)= P_s V_t
-        wait(&S.p_full[s], np[s] & 1u);
-        if (dead) return;
-        ++np[s];
-        tc_fence_after();
-        const uint32_t vb = smem_u32(S.v[t & 1]);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_bf16_ta(tmem + 256 + kTile * s, tmem + kTile * s + 8 * kk, sw128_mn_desc(vb + kk * 2048, kHalf, 1024),
-                      idesc_o, (kk > 0 || !first) ? 1u : 0u);
-      };
-      while (!dead && walk.next(p, S, pc)) {
-        const int n = pc.k1 - pc.k0;
-        if (n == 0) continue;
-        wait(&S.q_full, pieces & 1u);
-        ++pieces;
-        if (pc.pair) {
-          const int nt = pc.it.rows > kTile ? 2 : 1;
-          for (int k = -1; k < n && !dead; ++k) {
-            if (k >= 0) wait(&S.v_full[(kt + k) & 1], ((kt + k) >> 1) & 1u);
-            for (int s = 0; s < nt && !dead; ++s) {
-              if (k >= 0) {
-                pv(s, kt + k, k == 0);
-                if (dead) break;
-                if (k == n - 1) mma_commit(&S.o_full[s]);
-                if (s == nt - 1) mma_commit(&S.v_empty[(kt + k) & 1]);
-              }
-              if (k + 1 < n) {
-                if (s == 0) wait(&S.k_full[(kt + k + 1) & 1], ((kt + k + 1) >> 1) & 1u);
-                if (dead) break;
-                qk(s, s, kt + k + 1);
-                if (s == nt - 1) {
-                  mma_commit(&S.k_empty[(kt + k + 1) & 1]);
-                  if (k + 1 == n - 1) mma_commit(&S.q_empty);
-                }
-              }
-            }
-          }
-        } else {
-          for (int k = -2; k < n && !dead; ++k) {
-            if (k >= 0) {
-              wait(&S.v_full[(kt + k) & 1], ((kt + k) >> 1) & 1u);
-              pv(k & 1, kt + k, k < 2);
-              if (dead) break;
-              mma_commit(&S.v_empty[(kt + k) & 1]);
-              if (k >= n - 2) mma_commit(&S.o_full[k & 1]);
-            }
-            if (k + 2 < n) {
-              wait(&S.k_full[(kt + k + 2) & 1], ((kt + k + 2) >> 1) & 1u);
-              if (dead) break;
-              qk(k & 1, 0, kt + k + 2);
-              mma_commit(&S.k_empty[(kt + k + 2) & 1]);
-              if (k + 2 == n - 1) mma_commit(&S.q_empty);
-            }
-          }
-        }
-        kt += n;
+    // ---- MMA issue.  The whole warp walks and waits, and one elected lane
+    // issues: in code that only one lane runs every operand of an MMA is moved
+    // to the uniform registers for itself, and the issue falls behind the
+    // tensor cores (85-130 cycles per MMA of 64).  One warp issues for both
+    // groups: with a warp each, their products interleave and each group's
+    // arrive later (909 against 807 us at 8192 causal tokens, 64 heads).
+    constexpr uint32_t idesc_s = mma_idesc(128, 128);
+    constexpr uint32_t idesc_o = mma_idesc(128, 128) | (1u << 16);   // B (V) MN-major
+    constexpr uint32_t kStep = kTileBytes >> 4;                      // of a descriptor, from slot to slot
+    const uint32_t tS = __shfl_sync(0xffffffffu, tmem, 0), tO = tS + 256;
+    const uint64_t qd = sw128_desc(smem_u32(S.q[0])), kd = sw128_desc(smem_u32(S.k[0]));
+    const uint64_t vd = sw128_mn_desc(smem_u32(S.v[0]), kHalf, 1024);
+    int pieces = 0;
+    uint32_t np = 0;   // bit s: phase of the probabilities of group s
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (dead) return;
+      if (!wait_warp(bar, parity)) {
+        record_error(p.err, kErrTimeout);
+        dead = true;
       }
+    };
+    auto wait_k = [&](uint32_t t) { wait(&S.k_full[t & 1u], (t >> 1) & 1u); };
+    auto wait_v = [&](uint32_t t) { wait(&S.v_full[t & 1u], (t >> 1) & 1u); };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) mma_commit(bar);
+    };
+    auto qk = [&](uint32_t s, uint32_t qtile, uint32_t slot) {   // S_s = Q_qtile K^T
+      tc_fence_after();
+      const uint64_t ad = qd + qtile * kStep, bd = kd + slot * kStep;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+          mma_bf16(tS + kTile * s, ad + off, bd + off, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&S.s_full[s]);
+      }
+    };
+    auto pv = [&](uint32_t s, uint32_t slot, bool first) {   // O_s (+)= P_s V
+      const uint64_t bd = vd + slot * kStep;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        wait(&S.p_full[s][h], (np >> s) & 1u);
+        if (dead) return;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+            mma_bf16_ta(tO + kTile * s, tS + kTile * s + 8 * kk, bd + (kk * 2048 >> 4), idesc_o,
+                        (kk > 0 || !first) ? 1u : 0u);
+        }
+      }
+      np ^= 1u << s;
+    };
+    while (!dead && walk.next(p, S, pc)) {
+      const int n = __shfl_sync(0xffffffffu, pc.k1 - pc.k0, 0);
+      if (n == 0) continue;
+      wait(&S.q_full, pieces & 1u);
+      ++pieces;
+      wait_k(kt);
+      if (pc.pair) {
+        // Tile k's S is issued behind tile k - 1's O of the same group.  The
+        // waits for the next tiles' K and V stand between the two products of
+        // group 1, where the tensor cores have work for as long as they take
+        // (some 200 cycles each, even when the data is there).
+        const bool two = pc.it.rows > kTile;
+        for (int k = -1; k < n && !dead; ++k) {
+          const uint32_t t = kt + k, vslot = t & 1u, kslot = vslot ^ 1u;
+          const bool has_k = k + 1 < n;
+          if (k >= 0) pv(0, vslot, k == 0);
+          if (dead) break;
+          if (has_k) qk(0, 0, kslot);
+          else commit(&S.o_full[0]);
+          if (two && k >= 0) pv(1, vslot, k == 0);
+          if (has_k) wait_v(t + 1);
+          if (k + 2 < n) wait_k(t + 2);
+          if (dead) break;
+          if (two) {
+            if (has_k) qk(1, 1, kslot);
+            else commit(&S.o_full[1]);
+          }
+          if (k >= 0) commit(&S.v_empty[vslot]);
+          if (has_k) commit(&S.k_empty[kslot]);
+          if (k + 1 == n - 1) commit(&S.q_empty);
+        }
+      } else {
+        if (n > 1) wait_k(kt + 1);
+        for (int k = -2; k < n && !dead; ++k) {
+          const uint32_t t = kt + k, slot = t & 1u, s = k & 1;   // tile k + 2 has the same slot and group
+          if (k >= 0) {
+            wait_v(t);
+            pv(s, slot, k < 2);
+            if (dead) break;
+            commit(&S.v_empty[slot]);
+            if (k >= n - 2) commit(&S.o_full[s]);
+          }
+          if (k + 2 < n) {
+            if (k >= 0) wait_k(t + 2);
+            if (dead) break;
+            qk(s, 0, slot);
+            commit(&S.k_empty[slot]);
+            if (k + 2 == n - 1) commit(&S.q_empty);
+          }
+        }
+      }
+      kt += n;
     }
-    __syncwarp();
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---- softmax and output: group s = warp / 4, row r of its tile
     const int s = warp >> 2, r = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -587,8 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ns = 0, no = 0;   // accumulators S_s, O_s taken
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (dead) return;
-      const bool ok = mbar_wait(bar, parity);
-      if (!__all_sync(0xffffffffu, ok)) {
+      if (!wait_warp(bar, parity)) {
         record_error(p.err, kErrTimeout);
         dead = true;
       }
@@ -610,16 +699,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool prefix;
         const int t0 = tile_token(it, pc.k0 + k, &prefix);
         const int last = t0 + kTile - 1;
+        const bool clean = prefix ? last >= p.a.n_prefix : !(last <= it.hi && (t0 >= it.lo || last < p.a.sink));
+        const bool all = prefix ? last < p.a.n_prefix
+                                : last <= it.p0 && (static_cast<int64_t>(t0) > static_cast<int64_t>(it.p1) - p.a.local ||
+                                                    last < p.a.sink);
+        const int lo = clampi(static_cast<int64_t>(pos) - p.a.local + 1 - t0, 0, kTile);
+        const int hi = prefix ? static_cast<int>(p.a.n_prefix) - t0 : pos - t0 + 1;
+        const int sk = prefix ? kTile : p.a.sink - t0;
         wait(&S.s_full[s], ns & 1u);
         if (dead) break;
         ++ns;
         tc_fence_after();
-        // rows of V that nobody attends to are zeroed, by the group whose
-        // product reads the tile first.  (The wait stands behind that for S:
+        // rows of V that nobody attends to are zeroed, by each group before
+        // its own product reads them.  (The wait stands behind that for S:
         // S of this tile was issued after the product with the V slot's last
         // tile, so that V load is over and the phase is not mistaken for it.)
-        const bool clean = prefix ? last >= p.a.n_prefix : !(last <= it.hi && (t0 >= it.lo || last < p.a.sink));
-        if (clean && (!pc.pair || s == 0)) {
+        if (clean) {
           wait(&S.v_full[kt & 1], (kt >> 1) & 1u);
           if (dead) break;
           if (!any_row_sees(p, it, prefix, t0 + r)) {
@@ -635,14 +730,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           KV_TMEM_LD32(ts + 32, z + 32);
           KV_TMEM_LD32(ts + 64, z + 64);
           KV_TMEM_LD32(ts + 96, z + 96);
-          tmem_wait_ld();
-          const bool all = prefix ? last < p.a.n_prefix
-                                  : last <= it.p0 && (static_cast<int64_t>(t0) > static_cast<int64_t>(it.p1) - p.a.local ||
-                                                      last < p.a.sink);
+          KV_TMEM_WAIT32(z);
+          KV_TIE32(z + 32);
+          KV_TIE32(z + 64);
+          KV_TIE32(z + 96);
           if (!all) {
-            const int64_t lo64 = static_cast<int64_t>(pos) - p.a.local + 1 - t0;
-            const int lo = clampi(lo64, 0, kTile), hi = prefix ? static_cast<int>(p.a.n_prefix) - t0 : pos - t0 + 1;
-            const int sk = prefix ? kTile : p.a.sink - t0;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               const uint32_t keep = below(hi - 32 * w) & (~below(lo - 32 * w) | below(sk - 32 * w));
@@ -651,9 +743,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!((keep >> c) & 1u)) z[32 * w + c] = -INFINITY;
             }
           }
-          float mx = fmaxf(z[0], z[1]);
+          float a[8];
 #pragma unroll
-          for (int c = 2; c < 128; c += 2) mx = fmaxf(mx, fmaxf(z[c], z[c + 1]));
+          for (int i = 0; i < 8; ++i) a[i] = fmaxf(z[i], z[8 + i]);
+#pragma unroll
+          for (int c = 16; c < 128; c += 16) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = fmaxf(fmaxf(a[i], z[c + i]), z[c + 8 + i]);
+          }
+          const float mx = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), fmaxf(fmaxf(a[4], a[5]), fmaxf(a[6], a[7])));
           if (done == 0) {
             m = mx;
           } else {
@@ -665,14 +763,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (grow) m = mn;
               // S_s complete means that the product before it (O_s) is, too
 #pragma unroll 1
-              for (int c = 0; c < 128; c += 32) {
-                float o[32];
-                KV_TMEM_LD32(to + c, o);
+              for (int c = 0; c < 128; c += 16) {
+                float o[16];
+                tmem_ld_cols<16>(to + c, o);
                 tmem_wait_ld();
-                uint32_t u[32];
+                KV_TIE16(o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * al);
-                KV_TMEM_ST32(to + c, u);
+                for (int i = 0; i < 16; ++i) o[i] *= al;
+                KV_TMEM_ST16(to + c, o);
               }
             }
           }
@@ -690,14 +788,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               u[i] = pack_bf16(e.x, e.y);
             }
             KV_TMEM_ST32(ts + 32 * q, u);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.p_full[s][q]);
           }
           l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-          tmem_wait_st();
+        } else {
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&S.p_full[s][0]);
+            mbar_arrive(&S.p_full[s][1]);
+          }
         }
         ++done;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_full[s]);
       }
       if (dead) break;
       if (done > 0) {
@@ -716,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float o[32];
           if (done > 0) {
             KV_TMEM_LD32(to + c, o);
-            tmem_wait_ld();
+            KV_TMEM_WAIT32(o);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0.0f;
