@@ -36,10 +36,11 @@
 //            row r.  An item of more than 128 rows gives each group a query
 //            tile (pair); a smaller one gives the groups alternate key tiles
 //            (parity), each with its own statistics and partial rows.
-//   warp 8   K and Q loads, warp 9  V loads (TMA, 64-row boxes: a page holds
-//            at least 64 tokens, so a box never leaves its page).  Boxes that
-//            no row attends to are not loaded.
-//   warp 10  MMA issue.
+//   warp 8   K loads, warp 9  V loads (TMA, 64-row boxes: a page holds at least
+//            64 tokens, so a box never leaves its page).  Boxes that no row
+//            attends to are not loaded.  One ring of five tiles, in the order of
+//            use.
+//   warp 10  MMA issue, warp 11  query loads.
 // Rows of V that no row of the item attends to may hold anything (0 x NaN is
 // NaN): the softmax threads zero them in shared memory.
 #include <cuda.h>
@@ -57,16 +58,22 @@ constexpr int kHalf = kTile * 128;            // 128 rows x 64 bf16 columns
 constexpr int kTileBytes = 2 * kHalf;
 constexpr int kBox = 64;                      // rows of a K / V box
 constexpr int kBoxBytes = kBox * 128;
-constexpr int kSlots = 2;                     // K slots, V slots
-constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10;
-constexpr int kThreads = 384;                 // warp 11 only fills its warpgroup
+constexpr int kSlots = 5;                     // ring of K and V tiles
+constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kQWarp = 11;
+constexpr int kThreads = 384;
 // Registers: 384 threads start with 168 each (64512); the softmax warpgroups
 // take 200 and the third keeps 104, the same sum.
 constexpr int kSoftRegs = 200, kOtherRegs = 104;
 constexpr int kTmemCols = 512;                // S_0, S_1, O_0, O_1
 constexpr int kMaxSeq = 2048 + 1;             // sequences of the plan (the shared prefix is one)
 constexpr int kMaxEnt = 4608;                 // items per KV head of a split plan (see split_plan)
-constexpr int kPart = 128;                    // floats of a partial row
+constexpr int kPlanWords = 320;               // of the plan that fit into shared memory beside the ring
+constexpr int kQueue = 4;                     // pieces handed out ahead
+constexpr int kPieceReaders = 11;             // warps that take them: K, V, MMA, softmax
+// An item's share of the line is its tiles and this many more, for what an
+// item costs beside them (queries, the first tile's latency, the output).
+constexpr int kItemCost = 2;
+constexpr int kChunks = kD / 4;               // 16-byte chunks of a partial row
 // log2(e) / sqrt(128): logits in base-2 units.
 constexpr float kScale = 1.4426950408889634f * 0.08838834764831845f;
 constexpr float kRebase = 8.0f;               // growth of a row's maximum (log2) that rescales O
@@ -77,24 +84,50 @@ struct Args {
   int64_t n_cap;
   int split, pre;           // pre: the shared prefix is sequence 0 of the plan (split only)
   int slot_rows;            // partial rows a CTA may add to an item (split)
-  float* part_o;            // [rows][128]
+  float4* part_o;           // [rows][32] of a share: element (row, chunk) at chunk * rows + row
   float2* part_ml;          // [rows] (max in log2 units, sum)
-  int32_t* plan;            // [kMaxSeq + 1] ent_base, [kMaxEnt + 1] line: for the merge
+  int32_t* ent_base;        // [kMaxSeq + 1] the plan in global memory: written by plan_kernel, or
+  int32_t* line;            // [kMaxEnt + 1] (line and info alone, for the merge) by CTA 0
+  int4* info;               // [kMaxEnt] per entry: first token of the sequence, first row, rows, sequence (< 0: prefix)
+  int max_ent;              // entries that T tokens of B sequences can make (malformed cu_q is cut to it)
+  int plan_global;          // the plan is too large for shared memory
   unsigned* err;
 };
 
+// A CTA's share of an item, as its roles take it: key tiles k0 .. k0 + n - 1.
+struct alignas(16) Piece {
+  int tok0, rows;     // first query token, rows
+  int g, b;           // KV head, sequence (< 0: the shared prefix)
+  int p0, p1;         // positions of the first and last row
+  int lo, hi;         // own tokens attended by some row: [0, min(sink, hi + 1)) and [lo, hi]
+  int np, ns, w0;     // tiles of the prefix, of the sink in front of the window, first of the window
+  int k0, n;          // n < 0: no more pieces
+  int flags;
+  int64_t part;       // first partial row
+};
+constexpr int kPair = 1;    // two query tiles (or the first alone); else the groups take alternate key tiles
+constexpr int kWhole = 2;   // every tile of the item: the output is written, not a partial
+
 struct Smem {
   uint8_t q[2][kTileBytes];
-  uint8_t k[kSlots][kTileBytes];
-  uint8_t v[kSlots][kTileBytes];
-  uint64_t q_full, q_empty;
-  uint64_t k_full[kSlots], k_empty[kSlots];
-  uint64_t v_full[kSlots], v_empty[kSlots];
+  uint8_t kv[kSlots][kTileBytes];
+  Piece piece[kQueue];
+  uint64_t pc_full[kQueue], pc_empty[kQueue];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t full[kSlots], empty[kSlots];
   uint64_t s_full[2], p_full[2][2], o_full[2];   // p_full: the first and last 64 tokens
   uint32_t tmem_base;
-  int32_t scan[kThreads / 32 + 1];
-  int32_t ent_base[kMaxSeq + 1];   // split: items per KV head before sequence s
-  int32_t line[kMaxEnt + 1];       // split: tiles before entry e (all KV heads); whole: items before sequence s
+  int32_t plan[kPlanWords];
+};
+
+static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory of a block");
+
+// ent_base[s]: items per KV head before sequence s (split).  line: tiles
+// before entry e, all KV heads (split); items before sequence s (whole).
+struct Plan {
+  const int32_t* ent_base;
+  const int32_t* line;
+  int entries;
 };
 
 struct Seq {
@@ -127,12 +160,12 @@ __device__ __forceinline__ Seq seq_of(const Args& p, int s) {
   return r;
 }
 
-// Query rows r0 .. r0 + rows - 1 of a sequence for KV head g, and the key
+// Query rows r0 .. r0 + rows - 1 of a sequence for a KV head, and the key
 // tiles that they attend to: np of the prefix, ns of the sink in front of the
 // window, then those of the window from w0 on.
 struct Item {
   Seq s;
-  int g, r0, rows;
+  int r0, rows;
   int p0, p1;         // positions of the first and last row
   int lo, hi;         // own tokens attended by some row: [0, min(sink, hi + 1)) and [lo, hi]
   int np, ns, w0, cnt;
@@ -140,10 +173,9 @@ struct Item {
 
 __device__ __forceinline__ int ceil_tiles(int64_t n) { return static_cast<int>((n + kTile - 1) / kTile); }
 
-__device__ __forceinline__ Item make_item(const Args& p, const Seq& s, int qt, int g) {
+__device__ __forceinline__ Item make_item(const Args& p, const Seq& s, int qt) {
   Item it;
   it.s = s;
-  it.g = g;
   it.r0 = qt * kItemRows;
   it.rows = min(kItemRows, (s.ql << p.gsh) - it.r0);
   it.ns = 0;
@@ -171,55 +203,27 @@ __device__ __forceinline__ Item make_item(const Args& p, const Seq& s, int qt, i
 }
 
 // Key tile k of an item: first token, and whether it is of the prefix.
-__device__ __forceinline__ int tile_token(const Item& it, int k, bool* prefix) {
-  *prefix = k < it.np;
-  const int t = k < it.np ? k : (k - it.np < it.ns ? k - it.np : it.w0 + (k - it.np - it.ns));
+__device__ __forceinline__ int tile_token(const Piece& pc, int k, bool* prefix) {
+  *prefix = k < pc.np;
+  const int t = k < pc.np ? k : (k - pc.np < pc.ns ? k - pc.np : pc.w0 + (k - pc.np - pc.ns));
   return t * kTile;
 }
 
 // Token j (of a prefix tile or an own one) is attended by some row of the item.
-__device__ __forceinline__ bool any_row_sees(const Args& p, const Item& it, bool prefix, int j) {
+__device__ __forceinline__ bool any_row_sees(const Args& p, const Piece& pc, bool prefix, int j) {
   if (prefix) return j < p.a.n_prefix;
-  return j <= it.hi && (j >= it.lo || j < p.a.sink);
+  return j <= pc.hi && (j >= pc.lo || j < p.a.sink);
 }
 // The same for any token of [j, j + kBox).
-__device__ __forceinline__ bool any_row_sees_box(const Args& p, const Item& it, bool prefix, int j) {
+__device__ __forceinline__ bool any_row_sees_box(const Args& p, const Piece& pc, bool prefix, int j) {
   if (prefix) return j < p.a.n_prefix;
-  return j <= it.hi && (j + kBox > it.lo || j < p.a.sink);
+  return j <= pc.hi && (j + kBox > pc.lo || j < p.a.sink);
 }
 
 // CTA of a line of U tiles over G CTAs (ranges [c U / G, (c + 1) U / G)) that
 // holds position x.
 __device__ __forceinline__ int cta_of(int64_t x, int64_t U, int G) {
   return static_cast<int>(((x + 1) * G - 1) / U);
-}
-
-// Exclusive prefix sums of arr[0 .. n) in place, arr[n] = total (whole block).
-__device__ void block_scan(Smem& S, int32_t* arr, int n) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (n + kThreads - 1) / kThreads;
-  const int b = min(n, tid * per), e = min(n, b + per);
-  __syncthreads();
-  int sum = 0;
-  for (int i = b; i < e; ++i) sum += arr[i];
-  int inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) S.scan[warp] = inc;
-  __syncthreads();
-  int base = 0;
-  for (int w = 0; w < warp; ++w) base += S.scan[w];
-  int run = base + inc - sum;
-  for (int i = b; i < e; ++i) {
-    const int v = arr[i];
-    arr[i] = run;
-    run += v;
-  }
-  if (tid == kThreads - 1) arr[n] = base + inc;
-  __syncthreads();
 }
 
 // Last i in [0, n) with arr[i] <= x (arr ascending, arr[0] <= x).
@@ -237,87 +241,160 @@ __device__ __forceinline__ int q_tiles(const Args& p, const Seq& s) {
   return ((s.ql << p.gsh) + kItemRows - 1) / kItemRows;
 }
 
+// Exclusive prefix sums of f(0) .. f(n - 1) into arr[0 .. n], by a warp or
+// (kBlock) a block, whose first warp does the adding.
+template <bool kBlock, class F>
+__device__ __forceinline__ void plan_scan(int32_t* arr, int n, F&& f) {
+  const int lane = threadIdx.x & 31;
+  if (kBlock) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) arr[i] = f(i);
+    __syncthreads();
+  }
+  if (!kBlock || threadIdx.x < 32) {
+    int carry = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane, v = i < n ? (kBlock ? arr[i] : f(i)) : 0;
+      int inc = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int w = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += w;
+      }
+      if (i < n) arr[i] = carry + inc - v;
+      carry += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) arr[n] = carry;
+  }
+  if (kBlock) __syncthreads();
+  else __syncwarp();
+}
+
+// The plan in shared memory, by a warp or a block: ent_base [NS + 1] and line
+// [entries + 1].  `publish`: the copies in global memory (for the merge, and
+// for a batch whose plan the attention's CTAs cannot hold), and the check of
+// the lengths.
+template <bool kBlock>
+__device__ __forceinline__ int make_plan(const Args& p, int32_t* ent_base, int32_t* line, bool publish) {
+  const int NS = p.B + p.pre, first = kBlock ? threadIdx.x : threadIdx.x & 31, step = kBlock ? blockDim.x : 32;
+  if (publish)
+    for (int b = first; b < p.B; b += step) {
+      const int v = __ldg(p.a.bt.lens + b);
+      if (v < 0 || v > p.n_cap) record_error(p.err, kErrBadPage);
+    }
+  if (!p.split) {
+    plan_scan<kBlock>(line, NS, [&](int s) { return q_tiles(p, seq_of(p, s)) * p.Hkv; });
+    if (kBlock)
+      for (int s = first; s <= NS; s += step) p.line[s] = line[s];
+    return NS;
+  }
+  plan_scan<kBlock>(ent_base, NS, [&](int s) { return q_tiles(p, seq_of(p, s)); });
+  const int entries = min(ent_base[NS], p.max_ent);
+  plan_scan<kBlock>(line, entries, [&](int e) {
+    const int s = find_last(ent_base, NS, e);
+    const Item it = make_item(p, seq_of(p, s), e - ent_base[s]);
+    if (publish) p.info[e] = make_int4(it.s.q0, it.r0, it.rows, it.s.b);
+    return (it.cnt + kItemCost) * p.Hkv;
+  });
+  if (publish) {
+    for (int e = first; e <= entries; e += step) p.line[e] = line[e];
+    for (int s = first; s < NS; s += step) p.ent_base[s] = min(ent_base[s], entries);
+    if (first == 0) p.ent_base[NS] = entries;
+  }
+  return entries;
+}
+
 // First partial row of an item's share of CTA c.  Two rows of the area belong
 // to every query row (a parity item leaves two), ordered as the line is; each
 // CTA crossed adds slot_rows, the most rows of one share, so that no two
 // shares overlap.
-__device__ __forceinline__ int64_t part_row(const Args& p, const Item& it, int cta) {
+__device__ __forceinline__ int64_t part_row(const Args& p, const Item& it, int g, int cta) {
   const int64_t fam = p.pre && it.s.b >= 0 ? p.a.bt.T * p.Hq : 0;   // the prefix's shares stand first
   const int64_t row = fam + static_cast<int64_t>(it.s.q0) * p.Hq + static_cast<int64_t>(it.r0) * p.Hkv +
-                      static_cast<int64_t>(it.g) * it.rows;
+                      static_cast<int64_t>(g) * it.rows;
   return 2 * row + static_cast<int64_t>(cta) * p.slot_rows;
 }
 
-// The shares of this CTA in order; every role walks them alike.
-struct Piece {
-  Item it;
-  int k0, k1;      // key tiles
-  bool pair;       // two query tiles (or the first alone); else the groups take alternate key tiles
-  bool whole;      // every tile of the item: the output is written, not a partial
-};
-
+// The shares of this CTA in order.
 struct Walk {
-  int pos, end, step, n;   // split: position on the line, its end; whole: round
-  int e, s;                // split: current entry and its sequence
-  __device__ __forceinline__ void init(const Args& p, const Smem& S, int entries) {
-    n = entries;
-    if (n == 0) {
-      pos = end = 0;
-      return;
-    }
+  int pos, end, n;   // split: position on the line, its end; whole: round
+  int e, s;          // split: current entry and its sequence
+  __device__ __forceinline__ void init(const Args& p, const Plan& S) {
+    n = S.entries;
+    pos = end = 0;
+    if (n == 0) return;
     const int U = S.line[n];
     if (p.split) {
-      const int G = min(static_cast<int>(gridDim.x), U);
-      const int c = blockIdx.x;
-      pos = c < G ? static_cast<int>(static_cast<int64_t>(c) * U / G) : 0;
-      end = c < G ? static_cast<int>(static_cast<int64_t>(c + 1) * U / G) : 0;
-      if (pos < end) {
-        e = find_last(S.line, n, pos);
-        s = find_last(S.ent_base, p.B + p.pre, e);
-      }
+      const int G = min(static_cast<int>(gridDim.x), U), c = blockIdx.x;
+      if (c >= G) return;
+      pos = static_cast<int>(static_cast<int64_t>(c) * U / G);
+      end = static_cast<int>(static_cast<int64_t>(c + 1) * U / G);
+      e = find_last(S.line, n, pos);
+      s = find_last(S.ent_base, p.B + p.pre, e);
     } else {
-      pos = 0;
       end = (U + gridDim.x - 1) / gridDim.x;
     }
   }
-  __device__ __forceinline__ bool next(const Args& p, const Smem& S, Piece& pc) {
+  __device__ __forceinline__ bool next(const Args& p, const Plan& S, Piece& pc) {
+    Item it;
+    int g;
     if (p.split) {
-      if (pos >= end) return false;
-      while (S.line[e + 1] <= pos) ++e;
-      while (S.ent_base[s + 1] <= e) ++s;
-      const Seq sq = seq_of(p, s);
-      const int span = (S.line[e + 1] - S.line[e]) / p.Hkv;   // tiles of the item (an empty item has one, without work)
-      const int rem = pos - S.line[e], g = rem / span, off = rem - g * span;
-      pc.it = make_item(p, sq, e - S.ent_base[s], g);
-      const int take = min(span - off, end - pos);
-      pc.k0 = min(off, pc.it.cnt);
-      pc.k1 = min(off + take, pc.it.cnt);
-      pc.pair = pc.it.rows > kTile;
-      pc.whole = pc.pair && !p.pre && take == span;
-      pos += take;
-      return true;
-    }
-    const int U = n > 0 ? S.line[n] : 0;
-    while (pos < end) {
-      // rounds alternate direction, so that a CTA with a heavy item gets a light one next
-      const int c = (pos & 1) ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
-      const int u = pos * static_cast<int>(gridDim.x) + c;
-      ++pos;
-      if (u >= U) continue;
+      int off, take, span, first;
+      do {
+        if (pos >= end) return false;
+        while (S.line[e + 1] <= pos) ++e;
+        while (S.ent_base[s + 1] <= e) ++s;
+        span = (S.line[e + 1] - S.line[e]) / p.Hkv;
+        const int rem = pos - S.line[e];
+        g = rem / span;
+        off = rem - g * span;
+        take = min(span - off, end - pos);
+        pos += take;
+        first = min(kItemCost, span - 1);   // the item's first tile (an empty item: its last place)
+      } while (off + take <= first);        // nothing but the item's cost
+      it = make_item(p, seq_of(p, s), e - S.ent_base[s]);
+      pc.k0 = max(0, off - kItemCost);
+      pc.n = max(0, off + take - kItemCost) - pc.k0;
+      const bool pair = it.rows > kTile;
+      pc.flags = (pair ? kPair : 0) | (pair && !p.pre && off <= first && off + take == span ? kWhole : 0);
+      pc.part = part_row(p, it, g, blockIdx.x);
+    } else {
+      const int U = n > 0 ? S.line[n] : 0;
+      int u;
+      do {
+        if (pos >= end) return false;
+        // rounds alternate direction, so that a CTA with a heavy item gets a light one next
+        u = pos * static_cast<int>(gridDim.x) +
+            ((pos & 1) ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
+        ++pos;
+      } while (u >= U);
       const int x = U - 1 - u;   // late query tiles attend to the most keys
-      const int s2 = find_last(S.line, n, x);
-      const Seq sq = seq_of(p, s2);
-      const int rem = x - S.line[s2];
-      pc.it = make_item(p, sq, rem / p.Hkv, rem % p.Hkv);
+      const int sq = find_last(S.line, n, x), rem = x - S.line[sq];
+      it = make_item(p, seq_of(p, sq), rem / p.Hkv);
+      g = rem % p.Hkv;
       pc.k0 = 0;
-      pc.k1 = pc.it.cnt;
-      pc.pair = true;
-      pc.whole = true;
-      return true;
+      pc.n = it.cnt;
+      pc.flags = kPair | kWhole;
+      pc.part = 0;
     }
-    return false;
+    pc.tok0 = it.s.q0 + (it.r0 >> p.gsh);
+    pc.rows = it.rows;
+    pc.g = g;
+    pc.b = it.s.b;
+    pc.p0 = it.p0;
+    pc.p1 = it.p1;
+    pc.lo = it.lo;
+    pc.hi = it.hi;
+    pc.np = it.np;
+    pc.ns = it.ns;
+    pc.w0 = it.w0;
+    return true;
   }
 };
+
+// Places of K_i and V_i of a piece of n tiles in the ring: `ahead` K tiles
+// stand in front, then V_k and K_{k + ahead} in turn.
+__device__ __forceinline__ uint32_t k_place(int i, int ahead) { return i < ahead ? i : 2 * i - ahead + 1; }
+__device__ __forceinline__ uint32_t v_place(int i, int n, int ahead) { return min(n, i + ahead) + i; }
 
 // 3-D tiled tensor copy: x innermost (elements), y, z.
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int32_t x, int32_t y, int32_t z, uint64_t* bar) {
@@ -433,15 +510,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    mbar_init(&S.q_full, 1);
-    mbar_init(&S.q_empty, 1);
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(&S.pc_full[i], 1);
+      mbar_init(&S.pc_empty[i], kPieceReaders);
+    }
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&S.k_full[i], 1);
-      mbar_init(&S.k_empty[i], 1);
-      mbar_init(&S.v_full[i], 1);
-      mbar_init(&S.v_empty[i], 1);
+      mbar_init(&S.full[i], 1);
+      mbar_init(&S.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.q_full[i], 1);
+      mbar_init(&S.q_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.p_full[i][0], 4);
       mbar_init(&S.p_full[i][1], 4);
@@ -453,65 +532,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tm_v);
   }
   if (warp == kMmaWarp) tmem_alloc(&S.tmem_base, kTmemCols);
-  pdl_wait();
-
-  // ---- the plan
-  const int NS = p.B + p.pre;
-  int entries;
-  for (int s = tid; s < NS; s += kThreads) {
-    const Seq sq = seq_of(p, s);
-    if (blockIdx.x == 0 && sq.b >= 0 && __ldg(p.a.bt.lens + sq.b) != sq.len) record_error(p.err, kErrBadPage);
-    if (p.split) S.ent_base[s] = q_tiles(p, sq);
-    else S.line[s] = q_tiles(p, sq) * p.Hkv;
-  }
-  if (p.split) {
-    block_scan(S, S.ent_base, NS);
-    entries = min(S.ent_base[NS], kMaxEnt);
-    for (int e = tid; e < entries; e += kThreads) {
-      const int s = find_last(S.ent_base, NS, e);
-      const Item it = make_item(p, seq_of(p, s), e - S.ent_base[s], 0);
-      S.line[e] = max(1, it.cnt) * p.Hkv;
-    }
-    block_scan(S, S.line, entries);
-    if (blockIdx.x == 0) {
-      for (int i = tid; i <= NS; i += kThreads) p.plan[i] = S.ent_base[i];
-      for (int i = tid; i <= entries; i += kThreads) p.plan[kMaxSeq + 1 + i] = S.line[i];
-    }
-  } else {
-    block_scan(S, S.line, NS);
-    entries = NS;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
 
-  Walk walk;
-  walk.init(p, S, entries);
-  Piece pc;
-  int kt = 0;            // key tiles of the CTA so far: slot kt & 1, phase (kt >> 1) & 1
+  pdl_wait();
+  uint32_t ring = 0;     // K and V tiles of the CTA so far: slot ring mod kSlots
+  uint32_t pieces = 0;   // pieces taken
+  uint32_t uses[2] = {0, 0};   // of the query buffers
   bool dead = false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (dead) return;
+    if (!wait_warp(bar, parity)) {
+      record_error(p.err, kErrTimeout);
+      dead = true;
+    }
+  };
+  Piece pc;
+  // The next piece, copied; false behind the last.
+  auto take = [&]() {
+    const uint32_t i = pieces % kQueue;
+    wait(&S.pc_full[i], (pieces / kQueue) & 1u);
+    if (dead) return false;
+    pc = S.piece[i];
+    ++pieces;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.pc_empty[i]);
+    return pc.n >= 0;
+  };
+  // Query buffer of a parity piece (they alternate, so that the next piece's
+  // queries load while this one's are in use); a pair's tiles have both.
+  auto q_buffer = [&]() { return (uses[0] + uses[1]) & 1u; };
   if (warp >= kKWarp) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == kKWarp || warp == kVWarp) {
-    // ---- loads: lanes 0-3 issue the two 64-column halves of the two boxes
+    // ---- K loads, V loads: lanes 0-3 issue the two 64-column halves of the two boxes
     const bool is_k = warp == kKWarp;
     const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
     const int h = (lane >> 1) & 1, half = lane & 1;
-    int pieces = 0;
-    while (!dead && walk.next(p, S, pc)) {
-      const int n = pc.k1 - pc.k0;
-      if (n == 0) continue;
-      int64_t row = -1;   // of lane's box in the current batch of 16 tiles
+    uint32_t mine[4] = {0, 0, 0, 0};   // places + 1 of this warp's newest loads
+    while (take()) {
+      const int n = pc.n, ahead = (pc.flags & kPair) ? 1 : 2;
+      int64_t row = -1;   // of lane's box of 16 tiles from tile i on; -1: no row attends to the box
       for (int i = 0; i < n; ++i) {
         if ((i & 15) == 0) {
           const int k = pc.k0 + i + (lane >> 1);
           row = -1;
-          if (k < pc.k1) {
+          if (k < pc.k0 + n) {
             bool prefix;
-            const int tok = tile_token(pc.it, k, &prefix) + (lane & 1) * kBox;
-            if (any_row_sees_box(p, pc.it, prefix, tok)) {
-              row = cache_row(prefix ? p.a.pm_prefix : p.a.pm, prefix ? 0 : pc.it.s.b, pc.it.g, p.Hkv, p.n_cap, tok);
+            const int tok = tile_token(pc, k, &prefix) + (lane & 1) * kBox;
+            if (any_row_sees_box(p, pc, prefix, tok)) {
+              row = cache_row(prefix ? p.a.pm_prefix : p.a.pm, prefix ? 0 : pc.b, pc.g, p.Hkv, p.n_cap, tok);
               if (row < 0) {
                 record_error(p.err, kErrBadPage);
                 row = 0;
@@ -519,46 +591,74 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const int src = 2 * (i & 15);
-        const int64_t row0 = __shfl_sync(0xffffffffu, row, src), row1 = __shfl_sync(0xffffffffu, row, src + 1);
-        const int slot = kt & 1;
-        uint64_t* full = is_k ? &S.k_full[slot] : &S.v_full[slot];
-        uint64_t* empty = is_k ? &S.k_empty[slot] : &S.v_empty[slot];
-        if (!wait_warp(empty, ((kt >> 1) & 1u) ^ 1u)) {
-          record_error(p.err, kErrTimeout);
-          dead = true;
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(full, ((row0 >= 0) + (row1 >= 0)) * 2 * kBoxBytes);
+        const int64_t row0 = __shfl_sync(0xffffffffu, row, 2 * (i & 15)), row1 = __shfl_sync(0xffffffffu, row, 2 * (i & 15) + 1);
+        const uint32_t at = ring + (is_k ? k_place(i, ahead) : v_place(i, n, ahead)), slot = at % kSlots;
+        wait(&S.empty[slot], ((at / kSlots) & 1u) ^ 1u);
+        if (dead) break;
+        if (lane == 0) mbar_arrive_expect_tx(&S.full[slot], ((row0 >= 0) + (row1 >= 0)) * 2 * kBoxBytes);
         __syncwarp();
         const int64_t y = h ? row1 : row0;
-        if (lane < 4 && y >= 0) {
-          uint8_t* dst = (is_k ? S.k[slot] : S.v[slot]) + half * kHalf + h * kBoxBytes;
-          tma_load_2d(dst, tm, half * 64, static_cast<int32_t>(y), full);
-        }
-        ++kt;
-        if (is_k && i == 0) {
-          // the item's queries, behind its first keys: their buffers are free
-          // only once the last product of the previous item has read them
-          if (!wait_warp(&S.q_empty, (pieces & 1u) ^ 1u)) {
-            record_error(p.err, kErrTimeout);
-            dead = true;
-            break;
-          }
-          const int tiles = pc.it.rows > kTile ? 2 : 1;
-          if (lane == 0) mbar_arrive_expect_tx(&S.q_full, tiles * kTileBytes);
-          __syncwarp();
-          if (lane < 2 * tiles)
-            tma_load_3d(S.q[h] + half * kHalf, &tm_q, half * 64, pc.it.g << p.gsh,
-                        pc.it.s.q0 + ((pc.it.r0 + h * kTile) >> p.gsh), &S.q_full);
-          ++pieces;
-        }
+        if (lane < 4 && y >= 0)
+          tma_load_2d(S.kv[slot] + half * kHalf + h * kBoxBytes, tm, half * 64, static_cast<int32_t>(y), &S.full[slot]);
+        mine[3] = mine[2];
+        mine[2] = mine[1];
+        mine[1] = mine[0];
+        mine[0] = at + 1;
+      }
+      ring += 2 * n;
+    }
+    // Every load is over once the MMA warp has waited for it; where a wait ran
+    // out, nothing of this warp stays in flight past here (of the ring's five
+    // tiles at most four are one warp's).
+    if (dead)
+      for (int i = 0; i < 4; ++i)
+        if (mine[i] > 0) wait_warp(&S.full[(mine[i] - 1) % kSlots], ((mine[i] - 1) / kSlots) & 1u);
+  } else if (warp == kQWarp) {
+    // ---- the plan, the pieces, and their queries
+    Plan plan;
+    if (p.plan_global) {
+      plan.ent_base = p.ent_base;
+      plan.line = p.line;
+      plan.entries = p.split ? p.ent_base[p.B + p.pre] : p.B;
+    } else {
+      int32_t* line = S.plan + (p.split ? p.B + p.pre + 1 : 0);
+      plan.ent_base = S.plan;
+      plan.line = line;
+      plan.entries = make_plan<false>(p, S.plan, line, blockIdx.x == 0);
+    }
+    Walk walk;
+    walk.init(p, plan);
+    const int half = lane & 1;
+    bool more = true;
+    while (more && !dead) {
+      more = walk.next(p, plan, pc);
+      const uint32_t i = pieces % kQueue;
+      wait(&S.pc_empty[i], ((pieces / kQueue) & 1u) ^ 1u);
+      if (dead) break;
+      if (lane == 0) {
+        if (!more) pc.n = -1;
+        S.piece[i] = pc;
+        mbar_arrive(&S.pc_full[i]);
+      }
+      ++pieces;
+      if (!more || pc.n == 0) continue;
+      const bool pair = pc.flags & kPair;
+      const uint32_t b0 = pair ? 0 : q_buffer(), nb = pair && pc.rows > kTile ? 2 : 1;
+      for (uint32_t t = 0; t < nb; ++t) {
+        const uint32_t b = b0 + t;
+        wait(&S.q_empty[b], (uses[b] & 1u) ^ 1u);
+        if (dead) break;
+        if (lane == 0) mbar_arrive_expect_tx(&S.q_full[b], kTileBytes);
+        __syncwarp();
+        if (lane < 2)
+          tma_load_3d(S.q[b] + half * kHalf, &tm_q, half * 64, pc.g << p.gsh, pc.tok0 + static_cast<int>((t * kTile) >> p.gsh),
+                      &S.q_full[b]);
+        ++uses[b];
       }
     }
-    // nothing of this warp stays in flight past here
-    for (int i = kt > kSlots ? kt - kSlots : 0; i < kt; ++i)
-      wait_warp(is_k ? &S.k_full[i & 1] : &S.v_full[i & 1], (i >> 1) & 1u);
-    if (is_k && pieces > 0) wait_warp(&S.q_full, (pieces - 1) & 1u);
+    if (dead)
+      for (int b = 0; b < 2; ++b)
+        if (uses[b] > 0) wait_warp(&S.q_full[b], (uses[b] - 1) & 1u);
   } else if (warp == kMmaWarp) {
     // ---- MMA issue.  The whole warp walks and waits, and one elected lane
     // issues: in code that only one lane runs every operand of an MMA is moved
@@ -570,19 +670,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_o = mma_idesc(128, 128) | (1u << 16);   // B (V) MN-major
     constexpr uint32_t kStep = kTileBytes >> 4;                      // of a descriptor, from slot to slot
     const uint32_t tS = __shfl_sync(0xffffffffu, tmem, 0), tO = tS + 256;
-    const uint64_t qd = sw128_desc(smem_u32(S.q[0])), kd = sw128_desc(smem_u32(S.k[0]));
-    const uint64_t vd = sw128_mn_desc(smem_u32(S.v[0]), kHalf, 1024);
-    int pieces = 0;
+    const uint64_t qd = sw128_desc(smem_u32(S.q[0])), kd = sw128_desc(smem_u32(S.kv[0]));
+    const uint64_t vd = sw128_mn_desc(smem_u32(S.kv[0]), kHalf, 1024);
     uint32_t np = 0;   // bit s: phase of the probabilities of group s
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (dead) return;
-      if (!wait_warp(bar, parity)) {
-        record_error(p.err, kErrTimeout);
-        dead = true;
-      }
+    // Waits for the next tile of the ring; its slot.
+    auto next_tile = [&]() {
+      const uint32_t slot = ring % kSlots;
+      wait(&S.full[slot], (ring / kSlots) & 1u);
+      ++ring;
+      return slot;
     };
-    auto wait_k = [&](uint32_t t) { wait(&S.k_full[t & 1u], (t >> 1) & 1u); };
-    auto wait_v = [&](uint32_t t) { wait(&S.v_full[t & 1u], (t >> 1) & 1u); };
     auto commit = [&](uint64_t* bar) {
       if (elect_one()) mma_commit(bar);
     };
@@ -614,58 +711,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       np ^= 1u << s;
     };
-    while (!dead && walk.next(p, S, pc)) {
-      const int n = __shfl_sync(0xffffffffu, pc.k1 - pc.k0, 0);
+    while (take()) {
+      const int n = __shfl_sync(0xffffffffu, pc.n, 0);
       if (n == 0) continue;
-      wait(&S.q_full, pieces & 1u);
-      ++pieces;
-      wait_k(kt);
-      if (pc.pair) {
+      if (pc.flags & kPair) {
         // Tile k's S is issued behind tile k - 1's O of the same group.  The
         // waits for the next tiles' K and V stand between the two products of
         // group 1, where the tensor cores have work for as long as they take
         // (some 200 cycles each, even when the data is there).
-        const bool two = pc.it.rows > kTile;
+        const bool two = pc.rows > kTile;
+        uint32_t kslot = next_tile(), vslot = 0;
+        wait(&S.q_full[0], uses[0] & 1u);
+        ++uses[0];
+        if (two) {
+          wait(&S.q_full[1], uses[1] & 1u);
+          ++uses[1];
+        }
         for (int k = -1; k < n && !dead; ++k) {
-          const uint32_t t = kt + k, vslot = t & 1u, kslot = vslot ^ 1u;
           const bool has_k = k + 1 < n;
           if (k >= 0) pv(0, vslot, k == 0);
           if (dead) break;
           if (has_k) qk(0, 0, kslot);
           else commit(&S.o_full[0]);
           if (two && k >= 0) pv(1, vslot, k == 0);
-          if (has_k) wait_v(t + 1);
-          if (k + 2 < n) wait_k(t + 2);
+          uint32_t vnext = 0, knext = 0;
+          if (has_k) vnext = next_tile();
+          if (k + 2 < n) knext = next_tile();
           if (dead) break;
           if (two) {
             if (has_k) qk(1, 1, kslot);
             else commit(&S.o_full[1]);
           }
-          if (k >= 0) commit(&S.v_empty[vslot]);
-          if (has_k) commit(&S.k_empty[kslot]);
-          if (k + 1 == n - 1) commit(&S.q_empty);
+          if (k >= 0) commit(&S.empty[vslot]);
+          if (has_k) commit(&S.empty[kslot]);
+          if (k + 1 == n - 1) {
+            commit(&S.q_empty[0]);
+            if (two) commit(&S.q_empty[1]);
+          }
+          vslot = vnext;
+          kslot = knext;
         }
       } else {
-        if (n > 1) wait_k(kt + 1);
+        const uint32_t qb = q_buffer();
+        wait(&S.q_full[qb], uses[qb] & 1u);
+        ++uses[qb];
         for (int k = -2; k < n && !dead; ++k) {
-          const uint32_t t = kt + k, slot = t & 1u, s = k & 1;   // tile k + 2 has the same slot and group
+          const uint32_t s = k & 1;   // tile k + 2 is of the same group
           if (k >= 0) {
-            wait_v(t);
+            const uint32_t slot = next_tile();
             pv(s, slot, k < 2);
             if (dead) break;
-            commit(&S.v_empty[slot]);
+            commit(&S.empty[slot]);
             if (k >= n - 2) commit(&S.o_full[s]);
           }
           if (k + 2 < n) {
-            if (k >= 0) wait_k(t + 2);
+            const uint32_t slot = next_tile();
             if (dead) break;
-            qk(s, 0, slot);
-            commit(&S.k_empty[slot]);
-            if (k + 2 == n - 1) commit(&S.q_empty);
+            qk(s, qb, slot);
+            commit(&S.empty[slot]);
+            if (k + 2 == n - 1) commit(&S.q_empty[qb]);
           }
         }
       }
-      kt += n;
     }
   }
   } else {
@@ -675,56 +782,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + kTile * s + lane_base, to = tmem + 256 + kTile * s + lane_base;
     uint32_t ns = 0, no = 0;   // accumulators S_s, O_s taken
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (dead) return;
-      if (!wait_warp(bar, parity)) {
-        record_error(p.err, kErrTimeout);
-        dead = true;
-      }
-    };
-    while (!dead && walk.next(p, S, pc)) {
-      const Item& it = pc.it;
-      const int n = pc.k1 - pc.k0;
-      const int row = pc.pair ? kTile * s + r : r;         // of the item
-      const bool active = row < it.rows;                   // the row exists
-      if (pc.pair && kTile * s >= it.rows) {               // no second query tile
-        kt += n;
-        continue;
-      }
-      const int pos = it.p0 - (it.r0 >> p.gsh) + ((it.r0 + row) >> p.gsh);
+    while (take()) {
+      const bool pair = pc.flags & kPair;
+      const int n = pc.n;
+      const uint32_t ring0 = ring;
+      ring += 2 * n;
+      if (pair && kTile * s >= pc.rows) continue;      // no second query tile
+      const int row = pair ? kTile * s + r : r;        // of the item
+      const bool warp_rows = (warp & 3) * 32 < pc.rows - (pair ? kTile * s : 0);   // the warp has a row
+      const int pos = pc.p0 + (row >> p.gsh);
       float m = -INFINITY, l = 0.0f;
       int done = 0;
-      for (int k = 0; k < n && !dead; ++k, ++kt) {
-        if (!pc.pair && (k & 1) != s) continue;
+      for (int k = 0; k < n && !dead; ++k) {
+        if (!pair && (k & 1) != s) continue;
         bool prefix;
-        const int t0 = tile_token(it, pc.k0 + k, &prefix);
+        const int t0 = tile_token(pc, pc.k0 + k, &prefix);
         const int last = t0 + kTile - 1;
-        const bool clean = prefix ? last >= p.a.n_prefix : !(last <= it.hi && (t0 >= it.lo || last < p.a.sink));
+        const bool clean = prefix ? last >= p.a.n_prefix : !(last <= pc.hi && (t0 >= pc.lo || last < p.a.sink));
         const bool all = prefix ? last < p.a.n_prefix
-                                : last <= it.p0 && (static_cast<int64_t>(t0) > static_cast<int64_t>(it.p1) - p.a.local ||
+                                : last <= pc.p0 && (static_cast<int64_t>(t0) > static_cast<int64_t>(pc.p1) - p.a.local ||
                                                     last < p.a.sink);
         const int lo = clampi(static_cast<int64_t>(pos) - p.a.local + 1 - t0, 0, kTile);
         const int hi = prefix ? static_cast<int>(p.a.n_prefix) - t0 : pos - t0 + 1;
         const int sk = prefix ? kTile : p.a.sink - t0;
-        wait(&S.s_full[s], ns & 1u);
-        if (dead) break;
-        ++ns;
-        tc_fence_after();
-        // rows of V that nobody attends to are zeroed, by each group before
-        // its own product reads them.  (The wait stands behind that for S:
-        // S of this tile was issued after the product with the V slot's last
-        // tile, so that V load is over and the phase is not mistaken for it.)
-        if (clean) {
-          wait(&S.v_full[kt & 1], (kt >> 1) & 1u);
-          if (dead) break;
-          if (!any_row_sees(p, it, prefix, t0 + r)) {
-            uint4* v0 = reinterpret_cast<uint4*>(S.v[kt & 1] + r * 128);
+        // Rows of V that nobody attends to are zeroed, by each group before
+        // its own product reads them.  (Called behind the wait for S: by then
+        // the slot's tile before V is long loaded, and the phase of that load
+        // is not mistaken for this one's.)
+        auto clean_v = [&]() {
+          const uint32_t at = ring0 + v_place(k, n, pair ? 1 : 2), slot = at % kSlots;
+          wait(&S.full[slot], (at / kSlots) & 1u);
+          if (dead) return;
+          if (!any_row_sees(p, pc, prefix, t0 + r)) {
+            uint4* v0 = reinterpret_cast<uint4*>(S.kv[slot] + r * 128);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v0[i] = v0[i + kHalf / 16] = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_async_smem();
-        }
-        if ((warp & 3) * 32 < it.rows - (pc.pair ? kTile * s : 0)) {   // the warp has a row
+        };
+        wait(&S.s_full[s], ns & 1u);
+        if (dead) break;
+        ++ns;
+        tc_fence_after();
+        if (warp_rows) {
           float z[128];
           KV_TMEM_LD32(ts, z);
           KV_TMEM_LD32(ts + 32, z + 32);
@@ -788,6 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               u[i] = pack_bf16(e.x, e.y);
             }
             KV_TMEM_ST32(ts + 32 * q, u);
+            if (q == 0 && clean) clean_v();
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -795,6 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
         } else {
+          if (clean) clean_v();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&S.p_full[s][0]);
@@ -810,10 +912,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++no;
         tc_fence_after();
       }
-      if ((warp & 3) * 32 < it.rows - (pc.pair ? kTile * s : 0)) {
-        const int64_t orow = (static_cast<int64_t>(it.s.q0) + ((it.r0 + row) >> p.gsh)) * p.Hq + (it.g << p.gsh) +
-                             ((it.r0 + row) & ((1 << p.gsh) - 1));
-        const int64_t prow = part_row(p, it, blockIdx.x) + (pc.pair ? row : s * it.rows + row);
+      if (warp_rows) {
+        const bool active = row < pc.rows, whole = pc.flags & kWhole;   // the row exists
+        const int64_t orow = (static_cast<int64_t>(pc.tok0) + (row >> p.gsh)) * p.Hq + (pc.g << p.gsh) + (row & ((1 << p.gsh) - 1));
+        // this group's share: pc.rows rows, chunk-major (32 lanes store 512 contiguous bytes)
+        const int64_t part0 = pc.part + (pair ? 0 : s * pc.rows);
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
@@ -825,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0.0f;
           }
-          if (active && pc.whole) {
+          if (active && whole) {
             uint4* dst = reinterpret_cast<uint4*>(p.a.out + orow * kD + c);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -834,14 +937,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
                                   pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
           } else if (active && l > 0.0f) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kPart + c);
+            float4* dst = p.part_o + part0 * kChunks + static_cast<int64_t>(c / 4) * pc.rows + row;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) dst[i * pc.rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
           __syncwarp();
         }
         if (active) {
-          if (!pc.whole) p.part_ml[prow] = make_float2(m * kScale, l);
+          if (!whole) p.part_ml[part0 + row] = make_float2(m * kScale, l);
           else if (p.a.lse) p.a.lse[orow] = l > 0.0f ? (m * kScale + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
         tc_fence_before();
@@ -857,87 +960,122 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the partial rows of the items that more than one share (or group)
-// computed: exact log-sum-exp, fp32.  A block per row, warp w taking the
-// partials w, w + 4, ...; lane l holds dimensions 4l .. 4l + 3.
-constexpr int kMergeWarps = 4;
-
-__global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const Args p, int grid) {
-  __shared__ float2 ml[kMergeWarps];
-  __shared__ float4 ov[kMergeWarps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// The plan of a batch too large for the attention's shared memory, one block.
+__global__ void __launch_bounds__(1024) kv_plan_kernel(const Args p) {
+  __shared__ int32_t ent_base[kMaxSeq + 1], line[kMaxEnt + 1];
   pdl_wait();
-  const int NS = p.B + p.pre;
-  const int32_t* ent_base = p.plan;
-  const int32_t* line = p.plan + kMaxSeq + 1;
-  const int entries = min(__ldcg(ent_base + NS), kMaxEnt);
-  const int U = entries > 0 ? __ldcg(line + entries) : 0;
-  const int G = min(grid, U);
-  const int64_t rows = p.a.bt.T * p.Hq;
-  for (int64_t orow = blockIdx.x; orow < rows; orow += gridDim.x) {
-    const int64_t t = orow / p.Hq;
-    const int h = static_cast<int>(orow - t * p.Hq);
-    const int g = h >> p.gsh, hh = h & ((1 << p.gsh) - 1);
-    const TokenAt at = token_of(p.a.bt, t);
-    if (at.b < 0) continue;
+  make_plan<true>(p, ent_base, line, true);
+  pdl_trigger();
+}
+
+// Joins the partial rows of the items that more than one share (or group)
+// computed: exact log-sum-exp, fp32.  A thread owns one 16-byte chunk of a
+// query row in every share; PG thread groups of a block take every PG-th share
+// (many shares of few rows).  Rows are counted as (token, head of the group),
+// packed over the batch: an entry covers the rows [key, key + rows).
+constexpr int kMergeThreads = 256;
+constexpr size_t merge_smem(int entries) { return static_cast<size_t>(entries) * 12 + 4; }
+
+// One share's (max, sum, output chunk) into the running ones.
+__device__ __forceinline__ void join(float& m, float& l, float4& o, const float2 v, const float4 y) {
+  if (v.y > 0.0f) {
+    const float mn = fmaxf(m, v.x);
+    const float a = ex2_approx(m - mn), b = ex2_approx(v.x - mn);
+    m = mn;
+    l = l * a + v.y * b;
+    o = make_float4(o.x * a + y.x * b, o.y * a + y.y * b, o.z * a + y.z * b, o.w * a + y.w * b);
+  }
+}
+
+template <int PG>
+__global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const Args p, int grid) {
+  constexpr int kPer = kMergeThreads / PG;          // (row, chunk) elements of a unit
+  constexpr int kRowsU = kPer / kChunks;
+  extern __shared__ int32_t msm[];
+  __shared__ float2 ml[PG][kPer];
+  __shared__ float4 ov[PG][kPer];
+  const int pg = threadIdx.x / kPer, x = threadIdx.x - pg * kPer;
+  pdl_wait();
+  const int entries = __ldcg(p.ent_base + p.B + p.pre);
+  if (entries == 0) return;
+  const int pre_n = p.pre ? __ldcg(p.ent_base + 1) : 0;   // entries of the prefix stand first
+  int32_t* line = msm;                                    // [entries + 1]
+  int32_t* key = line + p.max_ent + 1;                    // [entries]
+  int32_t* rows_of = key + p.max_ent;                     // [entries]
+  for (int e = threadIdx.x; e <= entries; e += kMergeThreads) {
+    line[e] = __ldcg(p.line + e);
+    if (e < entries) {
+      const int4 info = __ldcg(p.info + e);
+      key[e] = (info.x << p.gsh) + info.y;
+      rows_of[e] = info.z;
+    }
+  }
+  __syncthreads();
+  const int U = line[entries], G = min(grid, U);
+  const int64_t R = p.a.bt.T << p.gsh;
+  const int64_t units = (R + kRowsU - 1) / kRowsU * p.Hkv;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int g = static_cast<int>(u % p.Hkv);
+    const int64_t row = u / p.Hkv * kRowsU + x % kRowsU;   // neighbours in a share
+    const int chunk = x / kRowsU;
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    bool direct = false;
-    int seen = 0;   // partials of earlier families
-    for (int f = 0; f <= p.pre; ++f) {
-      const int s = f < p.pre ? 0 : at.b + p.pre;
-      const Seq sq = seq_of(p, s);
-      const int lr = ((static_cast<int>(t) - sq.q0) << p.gsh) + hh;
-      const int qt = lr / kItemRows, e = __ldcg(ent_base + s) + qt;
-      if (lr < 0 || e >= entries) continue;   // lengths that contradict one another
-      const Item it = make_item(p, sq, qt, g);
-      const int64_t span = max(1, it.cnt);
-      const int64_t x0 = __ldcg(line + e) + g * span;
-      const int c0 = cta_of(x0, U, G), c1 = cta_of(x0 + span - 1, U, G);
-      const bool pair = it.rows > kTile;
-      if (pair && c0 == c1 && !p.pre) {   // its share has written the output
-        direct = true;
-        break;
-      }
-      const int row = lr - it.r0;
-      const int subs = pair ? 1 : 2, count = (c1 - c0 + 1) * subs;
-      for (int i = (warp + kMergeWarps - seen % kMergeWarps) % kMergeWarps; i < count; i += kMergeWarps) {
-        const int64_t prow = part_row(p, it, c0 + i / subs) + (pair ? row : (i % subs) * it.rows + row);
-        const float2 v = __ldcg(p.part_ml + prow);
-        if (v.y > 0.0f) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + prow * kPart) + lane);
-          const float mn = fmaxf(m, v.x);
-          const float a = ex2_approx(m - mn), b = ex2_approx(v.x - mn);
-          m = mn;
-          l = l * a + v.y * b;
-          o = make_float4(o.x * a + x.x * b, o.y * a + x.y * b, o.z * a + x.z * b, o.w * a + x.w * b);
+    bool write = false;
+    for (int f = p.pre ? 0 : 1; f < 2; ++f) {
+      // f = 0: the prefix's item that holds this row, f = 1: its own sequence's
+      const int e0 = f == 0 ? 0 : pre_n, e1 = f == 0 ? pre_n : entries;
+      if (e0 >= e1 || row >= R) continue;
+      const int e = e0 + find_last(key + e0, e1 - e0, static_cast<int>(row));
+      const int rr = static_cast<int>(row) - key[e], rows = rows_of[e];
+      if (rr < 0 || rr >= rows) continue;    // a token of no sequence
+      const int span = (line[e + 1] - line[e]) / p.Hkv;
+      const int64_t x0 = line[e] + static_cast<int64_t>(g) * span;
+      const int c0 = cta_of(x0 + min(kItemCost, span - 1), U, G), c1 = cta_of(x0 + span - 1, U, G);
+      const bool pair = rows > kTile;
+      if (pair && c0 == c1 && !p.pre) continue;   // its share has written the output
+      write |= f == 1;
+      const int count = pair ? c1 - c0 + 1 : 2 * (c1 - c0 + 1);
+      const int64_t base = 2 * ((f == 1 && p.pre ? R * p.Hkv : 0) + static_cast<int64_t>(key[e]) * p.Hkv +
+                                static_cast<int64_t>(g) * rows);
+      auto share = [&](int i) {
+        return base + static_cast<int64_t>(c0 + (pair ? i : i >> 1)) * p.slot_rows + (pair ? 0 : (i & 1) * rows);
+      };
+      int i = pg;
+      for (; i + 3 * PG < count; i += 4 * PG) {
+        float2 v[4];
+        float4 y[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int64_t part0 = share(i + w * PG);
+          v[w] = __ldcg(p.part_ml + part0 + rr);
+          y[w] = __ldcg(p.part_o + part0 * kChunks + static_cast<int64_t>(chunk) * rows + rr);
         }
-      }
-      seen += count;
-    }
-    if (direct) continue;
-    if (lane == 0) ml[warp] = make_float2(m, l);
-    ov[warp][lane] = o;
-    __syncthreads();
-    if (warp == 0) {
-      float mt = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) mt = fmaxf(mt, ml[w].x);
-      float lt = 0.0f;
-      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) {
-        const float b = ml[w].y > 0.0f ? ex2_approx(ml[w].x - mt) : 0.0f;
-        const float4 x = ov[w][lane];
-        lt += ml[w].y * b;
-        y = make_float4(y.x + x.x * b, y.y + x.y * b, y.z + x.z * b, y.w + x.w * b);
+        for (int w = 0; w < 4; ++w) join(m, l, o, v[w], y[w]);
       }
-      const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
-      *reinterpret_cast<uint2*>(p.a.out + orow * kD + 4 * lane) =
-          make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
-      if (p.a.lse && lane == 0) p.a.lse[orow] = lt > 0.0f ? (mt + log2f(lt)) * 0.6931471805599453f : -INFINITY;
+      for (; i < count; i += PG) {
+        const int64_t part0 = share(i);
+        const float2 v = __ldcg(p.part_ml + part0 + rr);
+        join(m, l, o, v, __ldcg(p.part_o + part0 * kChunks + static_cast<int64_t>(chunk) * rows + rr));
+      }
     }
-    __syncthreads();
+    if (PG > 1) {
+      ml[pg][x] = make_float2(m, l);
+      ov[pg][x] = o;
+      __syncthreads();
+      if (pg == 0) {
+#pragma unroll
+        for (int w = 1; w < PG; ++w) join(m, l, o, ml[w][x], ov[w][x]);
+      }
+      __syncthreads();
+    }
+    if (write && pg == 0) {
+      const int64_t orow = (row >> p.gsh) * p.Hq + (g << p.gsh) + (row & ((1 << p.gsh) - 1));
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      *reinterpret_cast<uint2*>(p.a.out + orow * kD + 4 * chunk) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      if (p.a.lse && chunk == 0) p.a.lse[orow] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
   }
   pdl_trigger();
 }
@@ -955,19 +1093,21 @@ bool split_plan(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms) {
 }
 
 struct Layout {
-  size_t off_o = 0, off_ml = 0, off_plan = 0, total = 256;
+  size_t off_o = 0, off_ml = 0, off_base = 0, off_line = 0, off_info = 0, total = 0;
   int slot_rows = 0;
 };
 
-Layout layout_of(int64_t T, int Hq, int Hkv, bool prefix, int num_sms) {
+Layout layout_of(int64_t T, int Hq, int Hkv, bool prefix, bool split, int num_sms) {
   Layout L;
   const int64_t most = 2 * T * (Hq / Hkv);
   L.slot_rows = static_cast<int>(most < kItemRows ? most : kItemRows);
-  const int64_t rows = 2 * T * Hq * (prefix ? 2 : 1) + static_cast<int64_t>(num_sms) * L.slot_rows;
-  L.off_o = 0;
-  L.off_ml = align_up(static_cast<size_t>(rows) * kPart * sizeof(float), 256);
-  L.off_plan = align_up(L.off_ml + static_cast<size_t>(rows) * sizeof(float2), 256);
-  L.total = align_up(L.off_plan + (kMaxSeq + 1 + kMaxEnt + 1) * sizeof(int32_t), 256);
+  const int64_t rows = split ? 2 * T * Hq * (prefix ? 2 : 1) + static_cast<int64_t>(num_sms) * L.slot_rows : 0;
+  L.off_base = 0;
+  L.off_line = align_up(L.off_base + (kMaxSeq + 1) * sizeof(int32_t), 256);
+  L.off_info = align_up(L.off_line + (kMaxEnt + 1) * sizeof(int32_t), 256);
+  L.off_ml = align_up(L.off_info + kMaxEnt * sizeof(int4), 256);
+  L.off_o = align_up(L.off_ml + static_cast<size_t>(rows) * sizeof(float2), 256);
+  L.total = align_up(L.off_o + static_cast<size_t>(rows) * kChunks * sizeof(float4), 256);
   return L;
 }
 
@@ -995,12 +1135,18 @@ int encode_rows(CUtensorMap* m, const uint16_t* base, int64_t rows, EncodeTiledF
 
 size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms) {
   // For the most SMs: a device with fewer splits a subset of these batches.
-  return split_plan(T, B, Hq, Hkv, prefix, num_sms) ? layout_of(T, Hq, Hkv, prefix, num_sms).total : 256;
+  return layout_of(T, Hq, Hkv, prefix, split_plan(T, B, Hq, Hkv, prefix, num_sms), num_sms).total;
 }
 
 cudaError_t configure_kv_attn_kernels(const DeviceInfo&) {
-  return cudaFuncSetAttribute(kv_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(sizeof(Smem) + 1024));
+  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(sizeof(Smem) + 1024));
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kv_merge_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(merge_smem(kMaxEnt)));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(kv_merge_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(merge_smem(kMaxEnt)));
 }
 
 int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream) {
@@ -1021,18 +1167,33 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const 
   const bool prefix = a.n_prefix > 0;
   p.split = split_plan(a.bt.T, s.B, s.Hq, s.Hkv, prefix, dev.num_sms);
   p.pre = p.split && prefix;
-  const Layout L = layout_of(a.bt.T, s.Hq, s.Hkv, prefix, dev.num_sms);
+  const Layout L = layout_of(a.bt.T, s.Hq, s.Hkv, prefix, p.split, dev.num_sms);
   p.slot_rows = L.slot_rows;
-  p.part_o = reinterpret_cast<float*>(ws + L.off_o);
+  p.part_o = reinterpret_cast<float4*>(ws + L.off_o);
   p.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);
-  p.plan = reinterpret_cast<int32_t*>(ws + L.off_plan);
+  p.ent_base = reinterpret_cast<int32_t*>(ws + L.off_base);
+  p.line = reinterpret_cast<int32_t*>(ws + L.off_line);
+  p.info = reinterpret_cast<int4*>(ws + L.off_info);
   p.err = dev.err_word;
-  const cudaError_t e = launch_dependent(kv_attn_kernel, dim3(dev.num_sms), dim3(kThreads), sizeof(Smem) + 1024, stream,
-                                         1, p, tq, tk, tv);
+  // Words of the plan: the most items per KV head that T tokens of B sequences can make.
+  const int64_t items = (a.bt.T * gq + kItemRows - 1) / kItemRows;
+  const int64_t entries = items + s.B + (p.pre ? items : 0);
+  p.max_ent = static_cast<int>(entries < kMaxEnt ? entries : kMaxEnt);
+  const int64_t words = p.split ? (s.B + p.pre + 1) + (p.max_ent + 1) : s.B + 1;
+  p.plan_global = words > kPlanWords;
+  cudaError_t e;
+  if (p.plan_global) {
+    e = launch_dependent(kv_plan_kernel, dim3(1), dim3(1024), 0, stream, 1, p);
+    if (e != cudaSuccess) return e;
+  }
+  e = launch_dependent(kv_attn_kernel, dim3(dev.num_sms), dim3(kThreads), sizeof(Smem) + 1024, stream, 1, p, tq, tk, tv);
   if (e != cudaSuccess || !p.split) return e;
-  const int64_t rows = a.bt.T * s.Hq, most = static_cast<int64_t>(dev.num_sms) * 16;
-  return launch_dependent(kv_merge_kernel, dim3(static_cast<unsigned>(rows < most ? rows : most)),
-                          dim3(32 * kMergeWarps), 0, stream, 1, p, dev.num_sms);
+  // Few rows: four thread groups to an element.
+  const bool few = a.bt.T * s.Hq <= 1024;
+  const int per_unit = kMergeThreads / (few ? 4 : 1) / kChunks;
+  const int64_t units = (a.bt.T * gq + per_unit - 1) / per_unit * s.Hkv, most = static_cast<int64_t>(dev.num_sms) * 8;
+  return launch_dependent(few ? kv_merge_kernel<4> : kv_merge_kernel<1>, dim3(static_cast<unsigned>(units < most ? units : most)),
+                          dim3(kMergeThreads), merge_smem(p.max_ent), stream, 1, p, dev.num_sms);
 }
 
 }  // namespace qasc
