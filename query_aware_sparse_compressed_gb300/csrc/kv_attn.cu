@@ -466,28 +466,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Bounded wait whose tries suspend the thread for up to a millisecond each.
-__device__ __forceinline__ bool try_wait_suspended(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
-  if (try_wait_suspended(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer_ns();
-  while (!try_wait_suspended(bar, parity))
-    if (globaltimer_ns() - t0 > kWaitTimeoutNs) return false;
-  return true;
-}
-// The same for a whole warp.
+// Bounded wait of a whole warp.  All lanes try and vote, so that the warp
+// never diverges: a wait by one lane, or a loop that lanes leave one by one,
+// costs the product pipeline more than the tries do (8192 causal tokens of 64
+// heads: 888 us with one lane waiting, 742 with a loop per lane, 710 so).  The
+// tries without a suspend-time hint wake sooner (745 us with one).
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_one(bar, parity));
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitTimeoutNs)) return false;
+  return true;
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -666,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tensor cores (85-130 cycles per MMA of 64).  One warp issues for both
     // groups: with a warp each, their products interleave and each group's
     // arrive later (909 against 807 us at 8192 causal tokens, 64 heads).
+    const bool leader = elect_one();
     constexpr uint32_t idesc_s = mma_idesc(128, 128);
     constexpr uint32_t idesc_o = mma_idesc(128, 128) | (1u << 16);   // B (V) MN-major
     constexpr uint32_t kStep = kTileBytes >> 4;                      // of a descriptor, from slot to slot
@@ -673,6 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t qd = sw128_desc(smem_u32(S.q[0])), kd = sw128_desc(smem_u32(S.kv[0]));
     const uint64_t vd = sw128_mn_desc(smem_u32(S.kv[0]), kHalf, 1024);
     uint32_t np = 0;   // bit s: phase of the probabilities of group s
+    // A wait that ran out ends the loop over the tiles, not the tile: its
+    // products are computed on what is there.
     // Waits for the next tile of the ring; its slot.
     auto next_tile = [&]() {
       const uint32_t slot = ring % kSlots;
@@ -681,12 +673,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       return slot;
     };
     auto commit = [&](uint64_t* bar) {
-      if (elect_one()) mma_commit(bar);
+      if (leader) mma_commit(bar);
     };
     auto qk = [&](uint32_t s, uint32_t qtile, uint32_t slot) {   // S_s = Q_qtile K^T
       tc_fence_after();
       const uint64_t ad = qd + qtile * kStep, bd = kd + slot * kStep;
-      if (elect_one()) {
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const uint64_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
@@ -700,9 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         wait(&S.p_full[s][h], (np >> s) & 1u);
-        if (dead) return;
         tc_fence_after();
-        if (elect_one()) {
+        if (leader) {
 #pragma unroll
           for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
             mma_bf16_ta(tO + kTile * s, tS + kTile * s + 8 * kk, bd + (kk * 2048 >> 4), idesc_o,
@@ -730,14 +721,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = -1; k < n && !dead; ++k) {
           const bool has_k = k + 1 < n;
           if (k >= 0) pv(0, vslot, k == 0);
-          if (dead) break;
           if (has_k) qk(0, 0, kslot);
           else commit(&S.o_full[0]);
           if (two && k >= 0) pv(1, vslot, k == 0);
           uint32_t vnext = 0, knext = 0;
           if (has_k) vnext = next_tile();
           if (k + 2 < n) knext = next_tile();
-          if (dead) break;
           if (two) {
             if (has_k) qk(1, 1, kslot);
             else commit(&S.o_full[1]);
@@ -760,13 +749,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k >= 0) {
             const uint32_t slot = next_tile();
             pv(s, slot, k < 2);
-            if (dead) break;
             commit(&S.empty[slot]);
             if (k >= n - 2) commit(&S.o_full[s]);
           }
           if (k + 2 < n) {
             const uint32_t slot = next_tile();
-            if (dead) break;
             qk(s, qb, slot);
             commit(&S.empty[slot]);
             if (k + 2 == n - 1) commit(&S.q_empty[qb]);
