@@ -70,8 +70,10 @@ constexpr int kMaxEnt = 4608;                 // items per KV head of a split pl
 constexpr int kPlanWords = 320;               // of the plan that fit into shared memory beside the ring
 constexpr int kQueue = 4;                     // pieces handed out ahead
 constexpr int kPieceReaders = 11;             // warps that take them: K, V, MMA, softmax
-// An item's share of the line is its tiles and this many more, for what an
-// item costs beside them (queries, the first tile's latency, the output).
+// Places of an item on the line: kItemCost for what it costs beside its tiles
+// (queries, the first tile's latency, the output), then one per tile, or two
+// of a pair item.  Measured with 128 sequences over a 128K prefix: 1.8 us a
+// tile of two query tiles, 1.0 a tile of one, 1.8 an item.
 constexpr int kItemCost = 2;
 constexpr int kChunks = kD / 4;               // 16-byte chunks of a partial row
 // log2(e) / sqrt(128): logits in base-2 units.
@@ -122,7 +124,7 @@ struct Smem {
 
 static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory of a block");
 
-// ent_base[s]: items per KV head before sequence s (split).  line: tiles
+// ent_base[s]: items per KV head before sequence s (split).  line: places
 // before entry e, all KV heads (split); items before sequence s (whole).
 struct Plan {
   const int32_t* ent_base;
@@ -220,7 +222,12 @@ __device__ __forceinline__ bool any_row_sees_box(const Args& p, const Piece& pc,
   return j <= pc.hi && (j + kBox > pc.lo || j < p.a.sink);
 }
 
-// CTA of a line of U tiles over G CTAs (ranges [c U / G, (c + 1) U / G)) that
+__device__ __forceinline__ int tile_weight(int rows) { return rows > kTile ? 2 : 1; }
+// Place of an item's first and last tile on its span (an empty item: its last place).
+__device__ __forceinline__ int first_place(int span) { return min(kItemCost, span - 1); }
+__device__ __forceinline__ int last_place(int span, int w) { return span > kItemCost ? span - w : span - 1; }
+
+// CTA of a line of U places over G CTAs (ranges [c U / G, (c + 1) U / G)) that
 // holds position x.
 __device__ __forceinline__ int cta_of(int64_t x, int64_t U, int G) {
   return static_cast<int>(((x + 1) * G - 1) / U);
@@ -293,7 +300,7 @@ __device__ __forceinline__ int make_plan(const Args& p, int32_t* ent_base, int32
     const int s = find_last(ent_base, NS, e);
     const Item it = make_item(p, seq_of(p, s), e - ent_base[s]);
     if (publish) p.info[e] = make_int4(it.s.q0, it.r0, it.rows, it.s.b);
-    return (it.cnt + kItemCost) * p.Hkv;
+    return (it.cnt * tile_weight(it.rows) + kItemCost) * p.Hkv;
   });
   if (publish) {
     for (int e = first; e <= entries; e += step) p.line[e] = line[e];
@@ -316,7 +323,7 @@ __device__ __forceinline__ int64_t part_row(const Args& p, const Item& it, int g
 
 // The shares of this CTA in order.
 struct Walk {
-  int pos, end, n;   // split: position on the line, its end; whole: round
+  int pos, end, n;   // split: place on the line, its end; whole: round
   int e, s;          // split: current entry and its sequence
   __device__ __forceinline__ void init(const Args& p, const Plan& S) {
     n = S.entries;
@@ -338,8 +345,8 @@ struct Walk {
     Item it;
     int g;
     if (p.split) {
-      int off, take, span, first;
-      do {
+      int off, take, span, w;
+      while (true) {
         if (pos >= end) return false;
         while (S.line[e + 1] <= pos) ++e;
         while (S.ent_base[s + 1] <= e) ++s;
@@ -349,13 +356,16 @@ struct Walk {
         off = rem - g * span;
         take = min(span - off, end - pos);
         pos += take;
-        first = min(kItemCost, span - 1);   // the item's first tile (an empty item: its last place)
-      } while (off + take <= first);        // nothing but the item's cost
-      it = make_item(p, seq_of(p, s), e - S.ent_base[s]);
-      pc.k0 = max(0, off - kItemCost);
-      pc.n = max(0, off + take - kItemCost) - pc.k0;
+        it = make_item(p, seq_of(p, s), e - S.ent_base[s]);
+        w = tile_weight(it.rows);
+        if (off + take > first_place(span) && off <= last_place(span, w)) break;   // not the item's cost alone
+      }
+      // a tile belongs to the share that holds its first place
+      pc.k0 = (max(0, off - kItemCost) + w - 1) / w;
+      pc.n = (max(0, off + take - kItemCost) + w - 1) / w - pc.k0;
       const bool pair = it.rows > kTile;
-      pc.flags = (pair ? kPair : 0) | (pair && !p.pre && off <= first && off + take == span ? kWhole : 0);
+      const bool all = off <= first_place(span) && off + take > last_place(span, w);
+      pc.flags = (pair ? kPair : 0) | (pair && !p.pre && all ? kWhole : 0);
       pc.part = part_row(p, it, g, blockIdx.x);
     } else {
       const int U = n > 0 ? S.line[n] : 0;
@@ -707,9 +717,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n == 0) continue;
       if (pc.flags & kPair) {
         // Tile k's S is issued behind tile k - 1's O of the same group.  The
-        // waits for the next tiles' K and V stand between the two products of
-        // group 1, where the tensor cores have work for as long as they take
-        // (some 200 cycles each, even when the data is there).
+        // waits for the next tiles' V and K (some 200 cycles each, even when
+        // the data is there) stand around group 1's O, where the tensor cores
+        // have work meanwhile; six other orders measured 680 to 706 us against
+        // 677 (8192 causal tokens, 64 heads).
         const bool two = pc.rows > kTile;
         uint32_t kslot = next_tile(), vslot = 0;
         wait(&S.q_full[0], uses[0] & 1u);
@@ -723,9 +734,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k >= 0) pv(0, vslot, k == 0);
           if (has_k) qk(0, 0, kslot);
           else commit(&S.o_full[0]);
-          if (two && k >= 0) pv(1, vslot, k == 0);
           uint32_t vnext = 0, knext = 0;
           if (has_k) vnext = next_tile();
+          if (two && k >= 0) pv(1, vslot, k == 0);
           if (k + 2 < n) knext = next_tile();
           if (two) {
             if (has_k) qk(1, 1, kslot);
@@ -940,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  pdl_trigger();
+  pdl_trigger();   // (at the CTA's start: 93 against 88 us for one 128K sequence, decoding)
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -1017,7 +1028,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const Args p, i
       if (rr < 0 || rr >= rows) continue;    // a token of no sequence
       const int span = (line[e + 1] - line[e]) / p.Hkv;
       const int64_t x0 = line[e] + static_cast<int64_t>(g) * span;
-      const int c0 = cta_of(x0 + min(kItemCost, span - 1), U, G), c1 = cta_of(x0 + span - 1, U, G);
+      const int c0 = cta_of(x0 + first_place(span), U, G), c1 = cta_of(x0 + last_place(span, tile_weight(rows)), U, G);
       const bool pair = rows > kTile;
       if (pair && c0 == c1 && !p.pre) continue;   // its share has written the output
       write |= f == 1;
