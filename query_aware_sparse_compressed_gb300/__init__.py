@@ -424,74 +424,126 @@ def ts_dense_attn(q, K, V, out, workspace, *, n, lse=None, stream=None):
 
 # ------------------------------------------------------- packed batches
 # These calls sit in an engine's per-layer loop, where the host's time per call
-# counts: their tensors are checked in one pass (_ptrs) against one reading of
-# the current device.
-def _ptrs(*tensors):
-    """Device pointers of (tensor, name, dtype, dims) tuples, each checked as
-    _ptr and _dims do; dims of None leaves the extents to the caller."""
-    dev = None
-    out = []
-    for t, name, dtype, dims in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a torch.Tensor" % name)
-        if dims is not None and t.shape != dims:
-            raise ValueError("%s must have shape %s, got %s" % (name, tuple(dims), tuple(t.shape)))
-        if dev is None and t.is_cuda:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev or t.dtype != dtype or not t.is_contiguous():
-            _ptr(t, name, dtype)     # raises
-        out.append(t.data_ptr())
-    return out
+# counts: one test per tensor against the call's device, and the device against
+# the current one at the end.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_Tensor = torch.Tensor
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
-def _heads(t, name, T, H):
+def _at(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of this dtype and shape on device index
+    dev (the checks of _dims and _ptr)."""
+    if (isinstance(t, _Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if not isinstance(t, _Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    _dims(t, name, tuple(shape))
+    _on_device(t.get_device(), name)
+    return _ptr(t, name, dtype).value
+
+
+def _on_device(dev, name):
+    """Raise unless dev is the current CUDA device, where the library launches."""
+    if dev < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    current = torch.cuda.current_device()
+    if dev != current:
+        raise ValueError("%s is on cuda:%d but the current device is cuda:%d" % (name, dev, current))
+
+
+def _heads(t, name, T, H, dev):
     """A [T, H, d] tensor whose tokens may lie apart (a part of a fused
-    projection): its pointer and the values between tokens."""
-    if not isinstance(t, torch.Tensor):
+    projection): its address and the values between tokens."""
+    if not isinstance(t, _Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.shape != (T, H, D):
-        raise ValueError("%s must have shape %s, got %s" % (name, (T, H, D), tuple(t.shape)))
+        _dims(t, name, (T, H, D))
     st = t.stride()
-    if T == 0 or (st[2] == 1 and (st[1] == D or H == 1)):
-        if not t.is_cuda or t.get_device() != torch.cuda.current_device() or t.dtype != torch.bfloat16:
-            _ptr(t[:0], name, torch.bfloat16)     # raises
-        return t.data_ptr(), st[0] if T > 1 else H * D
-    raise ValueError("%s must be contiguous within a token, got strides %s" % (name, st))
+    if T > 0 and (st[2] != 1 or (st[1] != D and H > 1)):
+        raise ValueError("%s must be contiguous within a token, got strides %s" % (name, st))
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        _on_device(t.get_device(), name)
+        _ptr(t[:0], name, _BF16)     # raises
+    return t.data_ptr(), st[0] if T > 1 else H * D
 
 
-def _batch(cu_q, lens, T):
+def _batch(cu_q, lens, T, dev):
     """The packed batch and B; cu_q [B + 1] (None: one token per sequence)."""
-    _dims(lens, "kv_lens", (None,))
-    B = lens.shape[0]
-    cu, ln = _ptrs((cu_q, "cu_q", torch.int32, (B + 1,)), (lens, "kv_lens", torch.int32, None))
-    return _lib.qasc_batch(cu, ln, T), B
+    if not isinstance(lens, _Tensor) or lens.dim() != 1:
+        raise ValueError("kv_lens must be a [B] tensor")
+    B = len(lens)
+    return _lib.qasc_batch(None if cu_q is None else _at(cu_q, "cu_q", _I32, (B + 1,), dev),
+                           _at(lens, "kv_lens", _I32, (B,), dev), T), B
 
 
-def _rope_append(fn, cache, n_cap, Hkv, q, k, v, q_out, K, V, batch, B, inv_freq, positions, interleaved, stream):
-    T = batch.tokens
-    Hq = q.shape[1] if q is not None else Hkv
-    qp, qs = _heads(q, "q", T, Hq) if q is not None else (None, 0)
-    kp, ks = _heads(k, "k", T, Hkv)
-    vp, vs = _heads(v, "v", T, Hkv)
+def _cache(K, V, block_table, B, Hkv, dev):
+    """K and V [B, Hkv, n_cap, d], or pools [num_pages, Hkv, P, d] under
+    block_table [B, pages_per_seq]: (descriptor or None, n_cap, Hkv, addresses
+    of K and V)."""
+    shape = K.shape
+    if len(shape) != 4 or shape[3] != D or (Hkv is not None and shape[1] != Hkv):
+        _dims(K, "K", (None if block_table is not None else B, Hkv, None, D))
+    if block_table is None:
+        if shape[0] != B:
+            _dims(K, "K", (B, Hkv, None, D))
+        cache, n_cap = None, shape[2]
+    else:
+        table = block_table.shape
+        if len(table) != 2 or table[0] != B:
+            _dims(block_table, "block_table", (B, None))
+        n_cap = table[1] * shape[2]
+        cache = _lib.qasc_paged_cache(_at(block_table, "block_table", _I32, table, dev), shape[2], table[1], shape[0])
+    return cache, n_cap, shape[1], _at(K, "K", _BF16, shape, dev), _at(V, "V", _BF16, shape, dev)
+
+
+def _table(block_table):
+    if not isinstance(block_table, _Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must have shape (B, pages_per_seq)")
+
+
+def _run(fn, dev, stream, shape, cache, *args):
+    """One call of the library: shape and cache descriptors, then args and the stream."""
+    _on_device(dev, "the call's first tensor")
+    if stream is None:
+        s = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    else:
+        s = _stream(stream)
+    if cache is None:
+        status = fn(ctypes.byref(shape), *args, s)
+    else:
+        status = fn(ctypes.byref(shape), ctypes.byref(cache), *args, s)
+    if status != _lib.QASC_OK:
+        _check(status)
+
+
+def _rope_append(name, q, k, v, q_out, K, V, block_table, kv_lens, inv_freq, cu_q, positions, interleaved, stream):
+    if not isinstance(k, _Tensor) or k.dim() != 3:
+        raise ValueError("k must be a [T, Hkv, %d] tensor" % D)
+    dev = k.get_device()
+    T, Hkv, _ = k.shape
+    batch, B = _batch(cu_q, kv_lens, T, dev)
+    cache, n_cap, Hkv, Kp, Vp = _cache(K, V, block_table, B, Hkv, dev)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
-    half = inv_freq.shape[0] if inv_freq is not None else 0
-    op, Kp, Vp, fp, pp = _ptrs((q_out, "q_out", torch.bfloat16, (T, Hq, D)), (K, "K", torch.bfloat16, None),
-                               (V, "V", torch.bfloat16, None), (inv_freq, "inv_freq", torch.float32, (half,)),
-                               (positions, "positions", torch.int32, (T,)))
-    shape = _lib.qasc_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap)
-    rope = _lib.qasc_rope(fp, pp, 2 * half, 1 if interleaved else 0)
-    geometry = (ctypes.byref(shape),) if cache is None else (ctypes.byref(shape), ctypes.byref(cache))
-    _check(fn(*geometry, ctypes.byref(batch), ctypes.byref(rope), qp, qs, kp, ks, vp, vs, op, Kp, Vp,
-              _stream(stream)))
-
-
-def _kv_heads(k):
-    _dims(k, "k", (None, None, D))
-    return k.shape[0], k.shape[1]
+    Hq, qp, qs, op = Hkv, None, 0, None
+    if q is not None:
+        if not isinstance(q, _Tensor) or q.dim() != 3:
+            raise ValueError("q must be a [T, Hq, %d] tensor" % D)
+        Hq = q.shape[1]
+        qp, qs = _heads(q, "q", T, Hq, dev)
+        op = _at(q_out, "q_out", _BF16, (T, Hq, D), dev)
+    kp, ks = _heads(k, "k", T, Hkv, dev)
+    vp, vs = _heads(v, "v", T, Hkv, dev)
+    rot, fp = 0, None
+    if inv_freq is not None:
+        _dims(inv_freq, "inv_freq", (None,))
+        rot, fp = 2 * inv_freq.shape[0], _at(inv_freq, "inv_freq", _F32, inv_freq.shape, dev)
+    pp = None if positions is None else _at(positions, "positions", _I32, (T,), dev)
+    rope = _lib.qasc_rope(fp, pp, rot, 1 if interleaved else 0)
+    _run(getattr(_L(), name), dev, stream, _lib.qasc_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap), cache,
+         ctypes.byref(batch), ctypes.byref(rope), qp, qs, kp, ks, vp, vs, op, Kp, Vp)
 
 
 def kv_rope_append(q, k, v, q_out, K, V, kv_lens, inv_freq, *, cu_q=None, positions=None, interleaved=False,
@@ -502,42 +554,36 @@ def kv_rope_append(q, k, v, q_out, K, V, kv_lens, inv_freq, *, cu_q=None, positi
     has tokens cu_q[b] .. cu_q[b + 1] (None: one each), the last of its
     kv_lens[b] cached ones; inv_freq [rot_dim / 2] (None: no rotation) turns
     by the cache position, or by positions [T]."""
-    T, Hkv = _kv_heads(k)
-    batch, B = _batch(cu_q, kv_lens, T)
-    _dims(K, "K", (B, Hkv, None, D))
-    _dims(V, "V", tuple(K.shape))
-    _rope_append(_L().kv_rope_append, None, K.shape[2], Hkv, q, k, v, q_out, K, V, batch, B, inv_freq, positions,
-                 interleaved, stream)
+    _rope_append("kv_rope_append", q, k, v, q_out, K, V, None, kv_lens, inv_freq, cu_q, positions, interleaved,
+                 stream)
 
 
 def kv_rope_append_paged(q, k, v, q_out, K_pool, V_pool, block_table, kv_lens, inv_freq, *, cu_q=None,
                          positions=None, interleaved=False, stream=None):
     """kv_rope_append into a paged pool [num_pages, Hkv, P, d]."""
-    T, Hkv = _kv_heads(k)
-    batch, B = _batch(cu_q, kv_lens, T)
-    cache, n_cap = _pool(K_pool, V_pool, block_table, B, Hkv)
-    _rope_append(_L().kv_rope_append_paged, cache, n_cap, Hkv, q, k, v, q_out, K_pool, V_pool, batch, B, inv_freq,
+    _table(block_table)
+    _rope_append("kv_rope_append_paged", q, k, v, q_out, K_pool, V_pool, block_table, kv_lens, inv_freq, cu_q,
                  positions, interleaved, stream)
 
 
-def _pool(K_pool, V_pool, block_table, B, Hkv=None):
-    """Descriptor of K and V pools under block_table [B, pages_per_seq], and n_cap."""
-    _dims(K_pool, "K_pool", (None, Hkv, None, D))
-    _dims(V_pool, "V_pool", tuple(K_pool.shape))
-    _dims(block_table, "block_table", (B, None))
-    P, pps = K_pool.shape[2], block_table.shape[1]
-    bt, = _ptrs((block_table, "block_table", torch.int32, None))
-    return _lib.qasc_paged_cache(bt, P, pps, K_pool.shape[0]), pps * P
-
-
-def _kv_attn(fn, geometry, own_args, q, K, V, out, workspace, batch, B, Hkv, n_cap, lse, stream):
-    T, Hq = q.shape[0], q.shape[1]
-    qp, Kp, Vp, op, lp, wp = _ptrs((q, "q", torch.bfloat16, (T, Hq, D)), (K, "K", torch.bfloat16, None),
-                                   (V, "V", torch.bfloat16, None), (out, "out", torch.bfloat16, (T, Hq, D)),
-                                   (lse, "lse", torch.float32, (T, Hq)), (workspace, "workspace", torch.uint8, None))
-    shape = _lib.qasc_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap)
-    _check(fn(ctypes.byref(shape), *geometry, ctypes.byref(batch), *own_args, qp, Kp, Vp, op, lp, wp,
-              workspace.numel(), _stream(stream)))
+def _attn(name, q, K, V, block_table, kv_lens, out, workspace, cu_q, lse, stream, front, behind):
+    """front: the library's arguments before the batch, behind: those after it."""
+    if not isinstance(q, _Tensor) or q.dim() != 3:
+        raise ValueError("q must have shape (T, Hq, %d)" % D)
+    dev = q.get_device()
+    shape = q.shape
+    T, Hq, d = shape
+    if d != D:
+        _dims(q, "q", (T, Hq, D))
+    batch, B = _batch(cu_q, kv_lens, T, dev)
+    cache, n_cap, Hkv, Kp, Vp = _cache(K, V, block_table, B, None, dev)
+    qp = _at(q, "q", _BF16, shape, dev)
+    op = _at(out, "out", _BF16, shape, dev)
+    lp = None if lse is None else _at(lse, "lse", _F32, (T, Hq), dev)
+    ws_bytes = workspace.numel()
+    wp = _at(workspace, "workspace", _U8, (ws_bytes,), dev)
+    _run(getattr(_L(), name), dev, stream, _lib.qasc_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap), cache, *front,
+         ctypes.byref(batch), *behind, qp, Kp, Vp, op, lp, wp, ws_bytes)
 
 
 def kv_window_attn_workspace_bytes(T, B, Hq, Hkv, n_cap):
@@ -549,22 +595,15 @@ def kv_window_attn(q, K, V, kv_lens, out, workspace, *, local, sink=4, cu_q=None
     and the newest `local` cached tokens of its sequence up to its own
     position; q, out [T, Hq, d] bf16, K, V [B, Hkv, n_cap, d], the batch as
     for kv_rope_append."""
-    _dims(q, "q", (None, None, D))
-    batch, B = _batch(cu_q, kv_lens, q.shape[0])
-    _dims(K, "K", (B, None, None, D))
-    _dims(V, "V", tuple(K.shape))
-    _kv_attn(_L().kv_window_attn, (), (sink, local), q, K, V, out, workspace, batch, B, K.shape[1], K.shape[2], lse,
-             stream)
+    _attn("kv_window_attn", q, K, V, None, kv_lens, out, workspace, cu_q, lse, stream, (), (sink, local))
 
 
 def kv_window_attn_paged(q, K_pool, V_pool, block_table, kv_lens, out, workspace, *, local, sink=4, cu_q=None,
                          lse=None, stream=None):
     """kv_window_attn over a paged pool [num_pages, Hkv, P, d]."""
-    _dims(q, "q", (None, None, D))
-    batch, B = _batch(cu_q, kv_lens, q.shape[0])
-    cache, n_cap = _pool(K_pool, V_pool, block_table, B)
-    _kv_attn(_L().kv_window_attn_paged, (ctypes.byref(cache),), (sink, local), q, K_pool, V_pool, out, workspace,
-             batch, B, K_pool.shape[1], n_cap, lse, stream)
+    _table(block_table)
+    _attn("kv_window_attn_paged", q, K_pool, V_pool, block_table, kv_lens, out, workspace, cu_q, lse, stream, (),
+          (sink, local))
 
 
 def kv_prefix_attn_workspace_bytes(T, B, Hq, Hkv, n_cap):
@@ -577,13 +616,12 @@ def kv_prefix_attn_paged(q, K_pool, V_pool, prefix_table, block_table, kv_lens, 
     (the pool pages prefix_table [ceil(n_prefix / P)]), read once for all of
     them; block_table and kv_lens describe each sequence's own tokens behind
     the prefix."""
-    _dims(q, "q", (None, None, D))
-    batch, B = _batch(cu_q, kv_lens, q.shape[0])
-    cache, n_cap = _pool(K_pool, V_pool, block_table, B)
-    pages = -(-n_prefix // K_pool.shape[2])
-    pt, = _ptrs((prefix_table if n_prefix > 0 else None, "prefix_table", torch.int32, (pages,)))
-    _kv_attn(_L().kv_prefix_attn_paged, (ctypes.byref(cache), pt, n_prefix), (), q, K_pool, V_pool, out, workspace,
-             batch, B, K_pool.shape[1], n_cap, lse, stream)
+    _table(block_table)
+    pt = None
+    if n_prefix > 0:
+        pt = _at(prefix_table, "prefix_table", _I32, (-(-n_prefix // K_pool.shape[2]),), q.get_device())
+    _attn("kv_prefix_attn_paged", q, K_pool, V_pool, block_table, kv_lens, out, workspace, cu_q, lse, stream,
+          (pt, n_prefix), ())
 
 
 # ------------------------------------------------------------------ SnapKV

@@ -227,11 +227,26 @@ __device__ __forceinline__ int tile_weight(int rows) { return rows > kTile ? 2 :
 __device__ __forceinline__ int first_place(int span) { return min(kItemCost, span - 1); }
 __device__ __forceinline__ int last_place(int span, int w) { return span > kItemCost ? span - w : span - 1; }
 
-// CTA of a line of U places over G CTAs (ranges [c U / G, (c + 1) U / G)) that
-// holds position x.
-__device__ __forceinline__ int cta_of(int64_t x, int64_t U, int G) {
-  return static_cast<int>(((x + 1) * G - 1) / U);
-}
+// A line of U places over G <= 2^15 CTAs: CTA c has the places
+// [c U / G, (c + 1) U / G).  In 32 bits, with U = q G + r.
+struct Ranges {
+  unsigned U, G, q, r;
+  __device__ __forceinline__ Ranges(int places, int grid) {
+    U = places;
+    G = min(grid, places);
+    q = U / G;
+    r = U - q * G;
+  }
+  __device__ __forceinline__ int start(unsigned c) const { return static_cast<int>(c * q + c * r / G); }
+  // The CTA that holds place x.
+  __device__ __forceinline__ int cta(int x) const {
+    int c = min(static_cast<int>(__fdividef(static_cast<float>(x) * static_cast<float>(G), static_cast<float>(U))),
+                static_cast<int>(G) - 1);
+    while (start(c) > x) --c;
+    while (start(c + 1) <= x) ++c;
+    return c;
+  }
+};
 
 // Last i in [0, n) with arr[i] <= x (arr ascending, arr[0] <= x).
 __device__ __forceinline__ int find_last(const int32_t* arr, int n, int x) {
@@ -331,10 +346,10 @@ struct Walk {
     if (n == 0) return;
     const int U = S.line[n];
     if (p.split) {
-      const int G = min(static_cast<int>(gridDim.x), U), c = blockIdx.x;
-      if (c >= G) return;
-      pos = static_cast<int>(static_cast<int64_t>(c) * U / G);
-      end = static_cast<int>(static_cast<int64_t>(c + 1) * U / G);
+      const Ranges line(U, gridDim.x);
+      if (blockIdx.x >= line.G) return;
+      pos = line.start(blockIdx.x);
+      end = line.start(blockIdx.x + 1);
       e = find_last(S.line, n, pos);
       s = find_last(S.ent_base, p.B + p.pre, e);
     } else {
@@ -916,31 +931,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this group's share: pc.rows rows, chunk-major (32 lanes store 512 contiguous bytes)
         const int64_t part0 = pc.part + (pair ? 0 : s * pc.rows);
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          float o[32];
-          if (done > 0) {
-            KV_TMEM_LD32(to + c, o);
-            KV_TMEM_WAIT32(o);
-          } else {
+        float o[128];
+        if (done > 0) {
+          KV_TMEM_LD32(to, o);
+          KV_TMEM_LD32(to + 32, o + 32);
+          KV_TMEM_LD32(to + 64, o + 64);
+          KV_TMEM_LD32(to + 96, o + 96);
+          KV_TMEM_WAIT32(o);
+          KV_TIE32(o + 32);
+          KV_TIE32(o + 64);
+          KV_TIE32(o + 96);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-          }
-          if (active && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.a.out + orow * kD + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                  pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                  pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                  pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-          } else if (active && l > 0.0f) {
-            float4* dst = p.part_o + part0 * kChunks + static_cast<int64_t>(c / 4) * pc.rows + row;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i * pc.rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
-          __syncwarp();
+          for (int i = 0; i < 128; ++i) o[i] = 0.0f;
         }
+        if (active && whole) {
+          uint4* dst = reinterpret_cast<uint4*>(p.a.out + orow * kD);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        } else if (active && l > 0.0f) {
+          float4* dst = p.part_o + part0 * kChunks + row;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) dst[i * pc.rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+        __syncwarp();
         if (active) {
           if (!whole) p.part_ml[part0 + row] = make_float2(m * kScale, l);
           else if (p.a.lse) p.a.lse[orow] = l > 0.0f ? (m * kScale + log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -995,21 +1013,21 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const Args p, i
   const int pg = threadIdx.x / kPer, x = threadIdx.x - pg * kPer;
   pdl_wait();
   const int entries = __ldcg(p.ent_base + p.B + p.pre);
-  if (entries == 0) return;
   const int pre_n = p.pre ? __ldcg(p.ent_base + 1) : 0;   // entries of the prefix stand first
   int32_t* line = msm;                                    // [entries + 1]
   int32_t* key = line + p.max_ent + 1;                    // [entries]
   int32_t* rows_of = key + p.max_ent;                     // [entries]
-  for (int e = threadIdx.x; e <= entries; e += kMergeThreads) {
+  for (int e = threadIdx.x; e <= p.max_ent; e += kMergeThreads) {   // those behind `entries` hold anything
     line[e] = __ldcg(p.line + e);
-    if (e < entries) {
+    if (e < p.max_ent) {
       const int4 info = __ldcg(p.info + e);
       key[e] = (info.x << p.gsh) + info.y;
       rows_of[e] = info.z;
     }
   }
   __syncthreads();
-  const int U = line[entries], G = min(grid, U);
+  if (entries == 0) return;
+  const Ranges ranges(line[entries], grid);
   const int64_t R = p.a.bt.T << p.gsh;
   const int64_t units = (R + kRowsU - 1) / kRowsU * p.Hkv;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
@@ -1027,8 +1045,8 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const Args p, i
       const int rr = static_cast<int>(row) - key[e], rows = rows_of[e];
       if (rr < 0 || rr >= rows) continue;    // a token of no sequence
       const int span = (line[e + 1] - line[e]) / p.Hkv;
-      const int64_t x0 = line[e] + static_cast<int64_t>(g) * span;
-      const int c0 = cta_of(x0 + first_place(span), U, G), c1 = cta_of(x0 + last_place(span, tile_weight(rows)), U, G);
+      const int x0 = line[e] + g * span;
+      const int c0 = ranges.cta(x0 + first_place(span)), c1 = ranges.cta(x0 + last_place(span, tile_weight(rows)));
       const bool pair = rows > kTile;
       if (pair && c0 == c1 && !p.pre) continue;   // its share has written the output
       write |= f == 1;

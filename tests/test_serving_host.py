@@ -205,6 +205,19 @@ def t(*shape, dtype=bf):
     # k not [T, Hkv, d]
     lambda: qasc.kv_rope_append(None, t(4, 2, 64), t(4, 2, 128), None, t(4, 2, 64, 128), t(4, 2, 64, 128),
                                 t(4, dtype=i32), None),
+    # a block table of one dimension, or none
+    lambda: qasc.kv_window_attn_paged(t(4, 8, 128), t(9, 2, 64, 128), t(9, 2, 64, 128), t(4, dtype=i32),
+                                      t(4, dtype=i32), t(4, 8, 128), t(256, dtype=u8), local=10),
+    # cu_q of another batch
+    lambda: qasc.kv_window_attn(t(4, 8, 128), t(2, 2, 64, 128), t(2, 2, 64, 128), t(2, dtype=i32), t(4, 8, 128),
+                                t(256, dtype=u8), local=10, cu_q=t(4, dtype=i32)),
+    # prefix pages
+    lambda: qasc.kv_prefix_attn_paged(t(4, 8, 128), t(9, 2, 64, 128), t(9, 2, 64, 128), t(1, dtype=i32),
+                                      t(4, 3, dtype=i32), t(4, dtype=i32), t(4, 8, 128), t(256, dtype=u8),
+                                      n_prefix=65),
+    # positions of another batch
+    lambda: qasc.kv_rope_append(None, t(4, 2, 128), t(4, 2, 128), None, t(4, 2, 64, 128), t(4, 2, 64, 128),
+                                t(4, dtype=i32), None, positions=t(3, dtype=i32)),
 ])
 def test_wrong_extents_are_rejected_before_the_library(call):
     with pytest.raises(ValueError, match="must have shape|must be a CUDA tensor"):
@@ -217,8 +230,12 @@ def test_tensors_on_the_host_are_rejected(monkeypatch):
         qasc.kv_window_attn(t(4, 8, 128), t(4, 2, 64, 128), t(4, 2, 64, 128), t(4, dtype=i32), t(4, 8, 128),
                             t(256, dtype=u8), local=10)
     with pytest.raises(ValueError, match="must have shape"):
-        qasc._heads(t(3, 2, 128), "k", 4, 2)
+        qasc._heads(t(3, 2, 128), "k", 4, 2, -1)
     with pytest.raises(ValueError, match="contiguous within a token"):
-        qasc._heads(t(4, 128, 2).transpose(1, 2), "k", 4, 2)
+        qasc._heads(t(4, 128, 2).transpose(1, 2), "k", 4, 2, -1)
     with pytest.raises(ValueError, match="must have shape"):
-        qasc._ptrs((t(4, 8, 128), "out", bf, (4, 8, 64)))
+        qasc._at(t(4, 8, 128), "out", bf, (4, 8, 64), -1)
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        qasc._at(t(4, 8, 128), "out", bf, (4, 8, 128), 0)
+    with pytest.raises(TypeError, match="must be a torch.Tensor"):
+        qasc._at([1, 2], "out", bf, (2,), 0)
