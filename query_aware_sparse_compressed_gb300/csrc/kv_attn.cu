@@ -20,7 +20,7 @@
 // rounding of the bf16 output); the sum that divides takes the unrounded fp32
 // values.
 //
-// Work.  Two schedules, chosen by the number of rows (launch_kv_attn):
+// Work.  Two schedules, chosen by the numbers of rows and tiles (split_is_faster):
 //   whole  many items: CTA c takes items c, c + G, ... whole, heaviest first.
 //   split  few items: the tiles of all items are laid end to end and every CTA
 //          takes an equal range of that line; an item that several CTAs share
@@ -45,6 +45,8 @@
 // NaN): the softmax threads zero them in shared memory.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
@@ -66,15 +68,16 @@ constexpr int kThreads = 384;
 constexpr int kSoftRegs = 200, kOtherRegs = 104;
 constexpr int kTmemCols = 512;                // S_0, S_1, O_0, O_1
 constexpr int kMaxSeq = 2048 + 1;             // sequences of the plan (the shared prefix is one)
-constexpr int kMaxEnt = 4608;                 // items per KV head of a split plan (see split_plan)
+constexpr int kMaxEnt = 4608;                 // items per KV head of a split plan (see may_split)
 constexpr int kPlanWords = 320;               // of the plan that fit into shared memory beside the ring
 constexpr int kQueue = 4;                     // pieces handed out ahead
 constexpr int kPieceReaders = 11;             // warps that take them: K, V, MMA, softmax
 // Places of an item on the line: kItemCost for what it costs beside its tiles
 // (queries, the first tile's latency, the output), then one per tile, or two
 // of a pair item.  Measured with 128 sequences over a 128K prefix: 1.8 us a
-// tile of two query tiles, 1.0 a tile of one, 1.8 an item.
-constexpr int kItemCost = 2;
+// tile of two query tiles, 1.0 a tile of one, 2.4 an item (262 us in all; 283
+// with an item at two places, 315 at one).
+constexpr int kItemCost = 3;
 constexpr int kChunks = kD / 4;               // 16-byte chunks of a partial row
 // log2(e) / sqrt(128): logits in base-2 units.
 constexpr float kScale = 1.4426950408889634f * 0.08838834764831845f;
@@ -84,6 +87,7 @@ struct Args {
   KvAttnArgs a;
   int B, Hq, Hkv, gsh;      // gsh = log2(Hq / Hkv)
   int64_t n_cap;
+  int once;                 // keys are read by one item, or two
   int split, pre;           // pre: the shared prefix is sequence 0 of the plan (split only)
   int slot_rows;            // partial rows a CTA may add to an item (split)
   float4* part_o;           // [rows][32] of a share: element (row, chunk) at chunk * rows + row
@@ -585,6 +589,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool is_k = warp == kKWarp;
     const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
     const int h = (lane >> 1) & 1, half = lane & 1;
+    // Where a sequence has few rows its keys are read once: they are the first
+    // to leave L2 (32 sequences over a 32K prefix: 45 us, 50 without
+    // the hint; 54 with tiles prefetched into L2 ahead of the ring).  Whole
+    // items share their keys (677 against 667 us with the hint).
+    const uint64_t once = policy_evict_first();
     uint32_t mine[4] = {0, 0, 0, 0};   // places + 1 of this warp's newest loads
     while (take()) {
       const int n = pc.n, ahead = (pc.flags & kPair) ? 1 : 2;
@@ -612,8 +621,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(&S.full[slot], ((row0 >= 0) + (row1 >= 0)) * 2 * kBoxBytes);
         __syncwarp();
         const int64_t y = h ? row1 : row0;
-        if (lane < 4 && y >= 0)
-          tma_load_2d(S.kv[slot] + half * kHalf + h * kBoxBytes, tm, half * 64, static_cast<int32_t>(y), &S.full[slot]);
+        if (lane < 4 && y >= 0) {
+          uint8_t* dst = S.kv[slot] + half * kHalf + h * kBoxBytes;
+          if (p.once) tma_load_2d_hint(dst, tm, half * 64, static_cast<int32_t>(y), &S.full[slot], once);
+          else tma_load_2d(dst, tm, half * 64, static_cast<int32_t>(y), &S.full[slot]);
+        }
         mine[3] = mine[2];
         mine[2] = mine[1];
         mine[1] = mine[0];
@@ -1096,16 +1108,38 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const Args p, i
   pdl_trigger();
 }
 
-// Few items are split; many are taken whole.  Counted with full tiles only
-// (T * Gq / 256 per KV head), which every batch has at least.  A split plan has
-// at most T Gq / 256 + B entries (T Gq / 256 + 1 more for a shared prefix):
+// Whether a batch of T tokens may be split, which bounds its workspace and its
+// plan: fewer items than 4 per SM, or with a shared prefix short sequences.
+// Counted with full tiles only (T Gq / 256 per KV head), which every batch has
+// at least.  A split plan has at most T Gq / 256 + B entries (T Gq / 256 + 1
+// more for a shared prefix), and with
 //   T Gq / 256 Hkv < 4 SMs, or Gq T < 128 B with a shared prefix,
-// so below 2 (1024 + 1) + 2048 of kMaxEnt on any device of up to 256 SMs.
-bool split_plan(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms) {
+// these are below 2 (1024 + 1) + 2048, of kMaxEnt, on a device of up to 256 SMs.
+bool may_split(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms) {
   const int64_t gq = Hq / Hkv;
   const int64_t items = (T * gq + kItemRows - 1) / kItemRows * Hkv;
   if (prefix && T * gq < static_cast<int64_t>(kTile) * B) return true;
   return items < 4 * static_cast<int64_t>(num_sms);
+}
+
+// Key tiles that any item of a window call can have.
+int64_t most_tiles(const KvAttnArgs& a, int64_t n_cap, int gq) {
+  const int64_t tokens = std::min<int64_t>(a.bt.T, kItemRows / gq);
+  const int64_t span = std::min<int64_t>(n_cap, static_cast<int64_t>(a.local) + tokens - 1);   // of the window
+  return (span + 2 * kTile - 2) / kTile + (std::min<int64_t>(a.sink, n_cap) + kTile - 1) / kTile;
+}
+
+// Split or whole, where either is possible, by the time each takes for items of
+// `tiles` key tiles (microseconds, fitted to both schedules at 1 to 64
+// sequences of 1 to 2048 new tokens, windows of 256 to 4096 tokens).  Whole items take rounds over the
+// SMs, a split costs the merge, and more for the partial rows of pair items.
+bool split_is_faster(int64_t T, int B, int gq, int Hkv, int64_t tiles, int num_sms) {
+  const bool pair = T * gq > static_cast<int64_t>(kTile) * B;
+  const int64_t items = Hkv * static_cast<int64_t>(B) * ((T * gq + static_cast<int64_t>(kItemRows) * B - 1) / (static_cast<int64_t>(kItemRows) * B));
+  const double per_sm = static_cast<double>(items) / num_sms, rounds = static_cast<double>((items + num_sms - 1) / num_sms);
+  const double whole = pair ? 8.0 + rounds * (1.35 * tiles + 5.0) : 3.7 + rounds * (1.4 * tiles + 4.5);
+  const double split = pair ? 20.0 + per_sm * (1.7 * tiles + 20.0) : 12.0 + per_sm * (1.3 * tiles + 4.0);
+  return split < whole;
 }
 
 struct Layout {
@@ -1151,7 +1185,7 @@ int encode_rows(CUtensorMap* m, const uint16_t* base, int64_t rows, EncodeTiledF
 
 size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms) {
   // For the most SMs: a device with fewer splits a subset of these batches.
-  return layout_of(T, Hq, Hkv, prefix, split_plan(T, B, Hq, Hkv, prefix, num_sms), num_sms).total;
+  return layout_of(T, Hq, Hkv, prefix, may_split(T, B, Hq, Hkv, prefix, num_sms), num_sms).total;
 }
 
 cudaError_t configure_kv_attn_kernels(const DeviceInfo&) {
@@ -1181,7 +1215,9 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const 
   p.gsh = gq == 8 ? 3 : (gq == 4 ? 2 : (gq == 2 ? 1 : 0));
   p.n_cap = s.n_cap;
   const bool prefix = a.n_prefix > 0;
-  p.split = split_plan(a.bt.T, s.B, s.Hq, s.Hkv, prefix, dev.num_sms);
+  p.split = may_split(a.bt.T, s.B, s.Hq, s.Hkv, prefix, dev.num_sms) &&
+            (prefix || split_is_faster(a.bt.T, s.B, gq, s.Hkv, most_tiles(a, s.n_cap, gq), dev.num_sms));
+  p.once = a.bt.T * gq <= static_cast<int64_t>(kItemRows) * s.B;
   p.pre = p.split && prefix;
   const Layout L = layout_of(a.bt.T, s.Hq, s.Hkv, prefix, p.split, dev.num_sms);
   p.slot_rows = L.slot_rows;
