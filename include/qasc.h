@@ -355,7 +355,8 @@ typedef struct {
  *   x_a' = x_a cos(p f_i) - x_b sin(p f_i),  x_b' = x_b cos(p f_i) + x_a sin(p f_i)
  * with f_i = inv_freq[i] and p the token's position: its cache position, or
  * positions[t] where given (e.g. behind a shared prefix).  Angles are exact
- * to about 1e-7 radians at any position; results are rounded once to bf16. */
+ * to 3e-7 radians for frequencies up to 1 at any position; results are rounded
+ * once to bf16. */
 typedef struct {
   const float* inv_freq;      /* device [rot_dim / 2] */
   const int32_t* positions;   /* device [T], or NULL */
@@ -401,8 +402,11 @@ QASC_API qasc_status kv_rope_append_paged(const qasc_shape* shape, const qasc_pa
  * sink >= 0, local >= 1, B <= 2048 (more: QASC_ERR_UNSUPPORTED).  A token with
  * A(t) empty (its position is negative: more new tokens than cached ones) gives
  * out 0 and lse -inf.  Cache rows that none of a sequence's queries attends to
- * may hold anything, NaN and infinities included; a block-table entry is read
- * only for pages that hold an attended token. */
+ * may hold anything, NaN and infinities included; V rows that some attend to
+ * are taken as finite (a NaN in one may reach its sequence's other queries).  A
+ * block-table entry is read only for pages that hold an attended token.  The
+ * workspace need not be cleared and is free again once the call has finished
+ * on the stream; calls that can overlap need one each. */
 QASC_API size_t kv_window_attn_workspace_bytes(const qasc_shape* shape, int64_t tokens);
 QASC_API qasc_status kv_window_attn(const qasc_shape* shape, const qasc_batch* batch, int32_t sink, int32_t local,
                                     const uint16_t* q, const uint16_t* K, const uint16_t* V, uint16_t* out, float* lse,
@@ -420,7 +424,7 @@ QASC_API qasc_status kv_window_attn_paged(const qasc_shape* shape, const qasc_pa
  *
  *   prefix_table  [ceil(n_prefix / P)] int32, device: pool pages of the prefix
  *   n_prefix      0 <= n_prefix < 2^24 (0: prefix_table may be NULL), and
- *                 tokens * Hq * n_prefix < 2^45
+ *                 tokens * Hq * n_prefix < 2^43
  *   cache, batch  the sequences' own tokens, counted from 0 behind the prefix
  *                 (lens[b] and p leave the prefix out; token 0 begins a page)
  *   workspace, ws_bytes >= kv_prefix_attn_workspace_bytes(shape, tokens)

@@ -740,10 +740,10 @@ QASC_API qasc_status kv_prefix_attn_paged(const qasc_shape* shape, const qasc_pa
   if (n_prefix < 0 || n_prefix >= (int64_t(1) << 24))
     return fail(QASC_ERR_INVALID_ARG, "%s: n_prefix=%lld outside [0, 2^24)", fn, static_cast<long long>(n_prefix));
   if (n_prefix > 0) QASC_REQUIRE_PTR(prefix_table, 4, fn);
-  // the plan counts key tiles of 128 tokens by 256 query rows in 32 bits
+  // the plan counts places (two per 128 tokens by 256 query rows) in 32 bits
   if (batch && batch->tokens > 0 && n_prefix > 0 &&
-      batch->tokens >= (int64_t(1) << 45) / (static_cast<int64_t>(shape->Hq) * n_prefix))
-    return fail(QASC_ERR_INVALID_ARG, "%s: tokens=%lld times Hq times n_prefix=%lld reaches 2^45", fn,
+      batch->tokens >= (int64_t(1) << 43) / (static_cast<int64_t>(shape->Hq) * n_prefix))
+    return fail(QASC_ERR_INVALID_ARG, "%s: tokens=%lld times Hq times n_prefix=%lld reaches 2^43", fn,
                 static_cast<long long>(batch->tokens), static_cast<long long>(n_prefix));
   a.sink = 0;
   a.local = INT32_MAX;

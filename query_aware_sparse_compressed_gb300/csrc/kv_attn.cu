@@ -942,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t orow = (static_cast<int64_t>(pc.tok0) + (row >> p.gsh)) * p.Hq + (pc.g << p.gsh) + (row & ((1 << p.gsh) - 1));
         // this group's share: pc.rows rows, chunk-major (32 lanes store 512 contiguous bytes)
         const int64_t part0 = pc.part + (pair ? 0 : s * pc.rows);
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
         float o[128];
         if (done > 0) {
           KV_TMEM_LD32(to, o);
@@ -965,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                                 pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
                                 pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-        } else if (active && l > 0.0f) {
+        } else if (active && l != 0.0f) {
           float4* dst = p.part_o + part0 * kChunks + row;
 #pragma unroll
           for (int i = 0; i < 32; ++i) dst[i * pc.rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -973,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (active) {
           if (!whole) p.part_ml[part0 + row] = make_float2(m * kScale, l);
-          else if (p.a.lse) p.a.lse[orow] = l > 0.0f ? (m * kScale + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          else if (p.a.lse) p.a.lse[orow] = l != 0.0f ? (m * kScale + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
         tc_fence_before();
       }
@@ -1004,9 +1004,10 @@ __global__ void __launch_bounds__(1024) kv_plan_kernel(const Args p) {
 constexpr int kMergeThreads = 256;
 constexpr size_t merge_smem(int entries) { return static_cast<size_t>(entries) * 12 + 4; }
 
-// One share's (max, sum, output chunk) into the running ones.
+// One share's (max, sum, output chunk) into the running ones.  A sum of 0 is a
+// share without any token (its output chunk is not written); NaN passes.
 __device__ __forceinline__ void join(float& m, float& l, float4& o, const float2 v, const float4 y) {
-  if (v.y > 0.0f) {
+  if (v.y != 0.0f) {
     const float mn = fmaxf(m, v.x);
     const float a = ex2_approx(m - mn), b = ex2_approx(v.x - mn);
     m = mn;
@@ -1099,10 +1100,10 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const Args p, i
     }
     if (write && pg == 0) {
       const int64_t orow = (row >> p.gsh) * p.Hq + (g << p.gsh) + (row & ((1 << p.gsh) - 1));
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
       *reinterpret_cast<uint2*>(p.a.out + orow * kD + 4 * chunk) =
           make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-      if (p.a.lse && chunk == 0) p.a.lse[orow] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if (p.a.lse && chunk == 0) p.a.lse[orow] = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
   }
   pdl_trigger();
@@ -1124,7 +1125,7 @@ bool may_split(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms) {
 
 // Key tiles that any item of a window call can have.
 int64_t most_tiles(const KvAttnArgs& a, int64_t n_cap, int gq) {
-  const int64_t tokens = std::min<int64_t>(a.bt.T, kItemRows / gq);
+  const int64_t tokens = a.bt.cu_q ? std::min<int64_t>(a.bt.T, kItemRows / gq) : 1;
   const int64_t span = std::min<int64_t>(n_cap, static_cast<int64_t>(a.local) + tokens - 1);   // of the window
   return (span + 2 * kTile - 2) / kTile + (std::min<int64_t>(a.sink, n_cap) + kTile - 1) / kTile;
 }

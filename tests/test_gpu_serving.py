@@ -388,6 +388,102 @@ def test_prefix_of_many_rows():
     check_rows(out, lse, ref, n0 + max(lens), rows=some)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,sink,local", [(400, 8, 2, 4, 2000), (2048, 4, 2, 4, 100), (700, 8, 8, 0, 64)])
+def test_window_of_many_sequences(B, Hq, Hkv, sink, local):
+    # plans too large for a block's shared memory
+    lens = [1 + (37 * b) % 300 for b in range(B)]
+    lens[3] = 1500
+    pages = Pages(lens, Hkv, 64, cdiv(1500, 64), seed=71)
+    q = rand((B, Hq, 128), 72)
+    some = sorted({0, 1, 2, 3, 4, B - 1, *range(5, B, 41)})
+    ref = osv.window_attention(f64(q), *pages.caches(), list(range(B + 1)), lens, sink, local, tokens=some)
+    out, lse = window(q, pages, None, lens, sink, local, Hkv)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    check_rows(out, lse, ref, 1500, rows=some)
+
+
+def test_window_of_many_ragged_sequences():
+    B, Hq, Hkv = 500, 8, 2
+    ql = [(7 * b) % 5 for b in range(B)]
+    lens = [max(1, m) + (53 * b) % 400 for b, m in enumerate(ql)]
+    cu = (3 + np.concatenate([[0], np.cumsum(ql)])).tolist()      # three tokens in front of the first sequence
+    T = cu[-1] + 2
+    pages = Pages(lens, Hkv, 64, 8, seed=73)
+    q = rand((T, Hq, 128), 74)
+    some = sorted({3, 4, 5, T - 3, *range(6, T - 3, 37)})
+    ref = osv.window_attention(f64(q), *pages.caches(), cu, lens, 4, 5000, tokens=some)
+    out, lse = window(q, pages, cu, lens, 4, 5000, Hkv)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    check_rows(out, lse, ref, 404, rows=some)
+    outside = [0, 1, 2, T - 2, T - 1]
+    assert bool((out[outside] == CANARY).all()) and bool((lse[outside] == CANARY).all())
+
+
+def test_prefix_of_many_sequences():
+    B, Hq, Hkv, P, n0 = 300, 8, 2, 64, 700
+    lens = [(11 * b) % 90 for b in range(B)]
+    both = Pages([n0] + lens, Hkv, P, 11, seed=75)
+    q = rand((B, Hq, 128), 76)
+    some = sorted({0, 1, 2, B - 1, *range(3, B, 23)})
+    Kc, Vc = both.caches()
+    ref = osv.prefix_attention(f64(q), Kc[0], Vc[0], Kc[1:], Vc[1:], list(range(B + 1)), lens, tokens=some)
+    K, V, table = both.cuda()
+    out = torch.full((B, Hq, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, Hq), float("nan"), dtype=torch.float32, device="cuda")
+    ws = qasc.alloc_workspace(qasc.kv_prefix_attn_workspace_bytes(B, B, Hq, Hkv, both.pps * P))
+    ws.fill_(255)
+    qasc.kv_prefix_attn_paged(q.cuda(), K, V, table[0, :cdiv(n0, P)].contiguous(), table[1:].contiguous(),
+                              batch_tensors(None, lens)[1], out, ws, n_prefix=n0, lse=lse)
+    qasc.qasc_device_error()
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    check_rows(out, lse, ref, n0 + 90, rows=some)
+
+
+@pytest.mark.parametrize("T", [5, 3000])
+def test_window_without_any_sequence(T):
+    pages = Pages([10, 20], 8, 64, 1, seed=77)
+    out, lse = window(rand((T, 64, 128), 78), pages, [0, 0, 0], [10, 20], 4, 100, 8)
+    assert bool((out == CANARY).all()) and bool((lse == CANARY).all())
+
+
+@pytest.mark.parametrize("n,m", [(1900, 1), (900, 200)])
+def test_window_not_a_number_stays_visible(n, m):
+    # a NaN key makes the queries that attend to it NaN, and no others
+    Hq, Hkv, P, local = 8, 2, 64, 300
+    pages = Pages([n], Hkv, P, cdiv(n, P), seed=79)
+    j = n - 50
+    pages.K[int(pages.table[0, j // P]), 1, j % P, 5] = float("nan")
+    q = rand((m, Hq, 128), 80)
+    out, lse = window(q, pages, [0, m], [n], 4, local, Hkv)
+    pos = torch.arange(n - m, n)
+    hit = ((pos >= j) & (pos - local < j)).cuda()
+    bad = torch.isnan(out).any(-1)
+    assert bool((torch.isnan(out).all(-1) == bad).all()) and bool((torch.isnan(lse) == bad).all())
+    assert bool((bad[:, 4:] == hit[:, None]).all()) and not bool(bad[:, :4].any())
+
+
+def test_window_long_positions():
+    # 2^23 tokens through a table that repeats a few pages: positions, sink and
+    # window far apart
+    Hq, Hkv, P = 8, 2, 65536
+    n = (1 << 23) - 77
+    pool_k, pool_v = rand((2, Hkv, P, 128), 81), rand((2, Hkv, P, 128), 82)
+    table = (torch.arange(128, dtype=torch.int32) % 2)[None].cuda()
+    q = rand((3, Hq, 128), 83)
+    j = [*range(0, 150), *range(n - 3 - 399, n)]
+    Kj, Vj = (np.stack([f64(x[(t // P) % 2, :, t % P]) for t in j], axis=1) for x in (pool_k, pool_v))
+    out = torch.empty((3, Hq, 128), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((3, Hq), dtype=torch.float32, device="cuda")
+    ws = qasc.alloc_workspace(qasc.kv_window_attn_workspace_bytes(3, 1, Hq, Hkv, 128 * P))
+    c, ln = batch_tensors([0, 3], [n])
+    qasc.kv_window_attn_paged(q.cuda(), pool_k.cuda(), pool_v.cuda(), table, ln, out, ws, sink=150, local=400, cu_q=c,
+                              lse=lse)
+    qasc.qasc_device_error()
+    # the same rows as a short cache: the sink, then the window
+    ref = osv.window_attention(f64(q), [Kj], [Vj], [0, 3], [len(j)], 150, 400)
+    check_rows(out, lse, ref, 552)
+
+
 def test_window_growing_maximum():
     # every later key scores higher: the running maximum moves in every tile
     Hq, Hkv, P, n = 8, 2, 64, 1500
