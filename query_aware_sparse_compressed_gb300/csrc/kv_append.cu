@@ -17,7 +17,13 @@
 // are slow; F_i is computed once per thread and the products are integer.)
 //
 // Bound: bytes.  Every value is read and written once, (Hq + 2 Hkv) 256 bytes
-// each way per token.
+// each way per token.  32768 tokens of 64 + 8 + 8 heads (1.34 GB): 203 us, 6.63
+// TB/s, 99 % of a plain copy's rate.  What that took: a thread keeps the angles
+// of its 16 values in registers over all heads of its slice (no division, no
+// shared-memory reads per head), has two heads in flight, and four blocks of
+// 256 threads share an SM (five or six spill: 234, 296 us; one head in flight:
+// 253; four and two blocks an SM: 223; streaming hints on loads or stores: 203
+// to 206).
 #include "common.cuh"
 #include "internal.h"
 
@@ -27,6 +33,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 4;       // tokens of a block's tile
 constexpr int kFreqs = kD / 2;
+constexpr int kUnits = 8;        // threads of a head: 16 values each
+constexpr int kBatch = 2;        // heads whose loads a thread has in flight
 
 struct AppendArgs {
   const uint16_t* q;       // NULL: no queries
@@ -55,17 +63,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // A unit of 16 values of a head, two 16-byte chunks: both members of eight
 // pairs (or values that are only copied).  Unit u of a head uses the
 // frequencies 8u .. 8u + 7 in either pairing.
-__device__ __forceinline__ void unit_chunks(int u, int rot, int interleaved, int* c0, int* c1) {
-  if (interleaved || u >= rot / 16) {
-    *c0 = 2 * u;
-    *c1 = 2 * u + 1;
-  } else {
-    *c0 = u;
-    *c1 = u + rot / 16;
-  }
-}
-
-__device__ __forceinline__ void rotate_split(uint4& x, uint4& y, const float* cs, const float* sn) {
+__device__ __forceinline__ void rotate_split(uint4& x, uint4& y, const float (&cs)[8], const float (&sn)[8]) {
   uint32_t* xa = &x.x;
   uint32_t* ya = &y.x;
 #pragma unroll
@@ -77,16 +75,17 @@ __device__ __forceinline__ void rotate_split(uint4& x, uint4& y, const float* cs
   }
 }
 
-__device__ __forceinline__ void rotate_pairs(uint4& x, const float* cs, const float* sn) {
+template <int F0>
+__device__ __forceinline__ void rotate_pairs(uint4& x, const float (&cs)[8], const float (&sn)[8]) {
   uint32_t* xa = &x.x;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 a = bf2_to_f2(xa[i]);
-    xa[i] = pack_bf16(a.x * cs[i] - a.y * sn[i], a.y * cs[i] + a.x * sn[i]);
+    xa[i] = pack_bf16(a.x * cs[F0 + i] - a.y * sn[F0 + i], a.y * cs[F0 + i] + a.x * sn[F0 + i]);
   }
 }
 
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const AppendArgs a) {
   __shared__ float cosv[kMaxTok][kFreqs], sinv[kMaxTok][kFreqs];
   __shared__ int64_t row0[kMaxTok];     // cache row of KV head 0, -1: not written
   __shared__ int32_t rpos[kMaxTok];     // position that rotates
@@ -126,46 +125,61 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const AppendArgs 
       sinv[tk][freq] = s;
     }
     __syncthreads();
-    const int units = n * heads * 8;
-    for (int i = tid; i < units; i += kThreads) {
-      const int u = i & 7, rest = i >> 3;
-      const int tk = rest / heads, h = rest - tk * heads;
-      if (!live[tk]) continue;
-      const int64_t t = t0 + tk;
-      const uint16_t* src;
-      uint16_t* dst;
-      bool rotated = u < a.rot / 16;
-      if (h < nq) {
-        src = a.q + t * a.qs + h * kD;
-        dst = a.q_out + (t * a.Hq + h) * kD;
-      } else {
-        if (row0[tk] < 0) continue;
-        const int g = h - nq;
-        if (g < a.Hkv) {
-          src = a.k + t * a.ks + g * kD;
-          dst = a.K + (row0[tk] + g * head_rows) * kD;
-        } else {
-          src = a.v + t * a.vs + (g - a.Hkv) * kD;
-          dst = a.V + (row0[tk] + (g - a.Hkv) * head_rows) * kD;
-          rotated = false;
+    // thread = (head slice, token, unit): its angles stay in registers over
+    // the heads of its slice
+    const int u = tid & (kUnits - 1), tk = (tid / kUnits) & (a.tok - 1), slice = tid / (kUnits * a.tok);
+    const int step = kThreads / (kUnits * a.tok);
+    if (tk < n && live[tk]) {
+      const int64_t t = t0 + tk, row = row0[tk];
+      const bool turns = u < a.rot / 16;
+      float cs[8], sn[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cs[i] = turns ? cosv[tk][8 * u + i] : 1.0f;
+        sn[i] = turns ? sinv[tk][8 * u + i] : 0.0f;
+      }
+      // chunks of the unit in a rotated head and in a copied one
+      const int c0 = turns && !a.interleaved ? u : 2 * u, c1 = turns && !a.interleaved ? u + a.rot / 16 : 2 * u + 1;
+      for (int h0 = slice; h0 < heads; h0 += kBatch * step) {
+        uint4 x[kBatch], y[kBatch];
+        uint16_t* dst[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int h = h0 + i * step;
+          dst[i] = nullptr;
+          if (h < heads && (h < nq || row >= 0)) {
+            const uint16_t* src;
+            const bool value = h >= nq + a.Hkv;
+            if (h < nq) {
+              src = a.q + t * a.qs + h * kD;
+              dst[i] = a.q_out + (t * a.Hq + h) * kD;
+            } else if (!value) {
+              src = a.k + t * a.ks + (h - nq) * kD;
+              dst[i] = a.K + (row + (h - nq) * head_rows) * kD;
+            } else {
+              src = a.v + t * a.vs + (h - nq - a.Hkv) * kD;
+              dst[i] = a.V + (row + (h - nq - a.Hkv) * head_rows) * kD;
+            }
+            x[i] = *reinterpret_cast<const uint4*>(src + 8 * (value ? 2 * u : c0));
+            y[i] = *reinterpret_cast<const uint4*>(src + 8 * (value ? 2 * u + 1 : c1));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (dst[i] == nullptr) continue;
+          const bool value = h0 + i * step >= nq + a.Hkv;
+          if (turns && !value) {
+            if (a.interleaved) {
+              rotate_pairs<0>(x[i], cs, sn);
+              rotate_pairs<4>(y[i], cs, sn);
+            } else {
+              rotate_split(x[i], y[i], cs, sn);
+            }
+          }
+          *reinterpret_cast<uint4*>(dst[i] + 8 * (value ? 2 * u : c0)) = x[i];
+          *reinterpret_cast<uint4*>(dst[i] + 8 * (value ? 2 * u + 1 : c1)) = y[i];
         }
       }
-      int c0, c1;
-      unit_chunks(u, rotated ? a.rot : 0, a.interleaved, &c0, &c1);
-      uint4 x = *reinterpret_cast<const uint4*>(src + 8 * c0);
-      uint4 y = *reinterpret_cast<const uint4*>(src + 8 * c1);
-      if (rotated) {
-        const float* cs = &cosv[tk][8 * u];
-        const float* sn = &sinv[tk][8 * u];
-        if (a.interleaved) {
-          rotate_pairs(x, cs, sn);
-          rotate_pairs(y, cs + 4, sn + 4);
-        } else {
-          rotate_split(x, y, cs, sn);
-        }
-      }
-      *reinterpret_cast<uint4*>(dst + 8 * c0) = x;
-      *reinterpret_cast<uint4*>(dst + 8 * c1) = y;
     }
     __syncthreads();   // the next tile rewrites the angles
   }
