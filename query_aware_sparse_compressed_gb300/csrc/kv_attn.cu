@@ -16,20 +16,22 @@
 // O stays in TMEM; it is rescaled only when a row's maximum has grown by more
 // than 2^8 since the exponents were last based (the factor cancels in the
 // final division, and fp32 and bf16 hold 2^8 as well as 1).  P is rounded to
-// bf16 (the operand type of V; 2^-9 of each weight on average, the size of the
-// rounding of the bf16 output); the sum that divides takes the unrounded fp32
-// values.
+// bf16, the type that its product with V takes (at most 2^-8 of each weight, the
+// size of the bf16 output's own rounding; on random values the two together are
+// 1.35 times the rounding alone); the sum that divides takes the unrounded fp32
+// values, so lse is as exact as fp32.
 //
 // Work.  Two schedules, chosen by the numbers of rows and tiles (split_is_faster):
 //   whole  many items: CTA c takes items c, c + G, ... whole, heaviest first.
 //   split  few items: the tiles of all items are laid end to end and every CTA
 //          takes an equal range of that line; an item that several CTAs share
-//          leaves partial (max, sum, O) rows in the workspace and merge_kernel
+//          leaves partial (max, sum, O) rows in the workspace and kv_merge_kernel
 //          joins them.  With a shared prefix its queries are one sequence of
 //          their own (all tokens of the batch, 256 rows to an item), so that
 //          the prefix is read once per 256 rows and not once per sequence.
-// The line is planned on the device, by every CTA for itself, from the
-// lengths: nothing about them is known to the host.
+// The line is planned on the device from the lengths, of which the host knows
+// nothing: by a warp of every CTA for itself, or by kv_plan_kernel for a batch
+// whose plan does not fit beside the tiles.
 //
 // Roles (384 threads):
 //   warps 0-3, 4-7  softmax: group s owns accumulators S_s and O_s, thread r
@@ -40,9 +42,28 @@
 //            64 tokens, so a box never leaves its page).  Boxes that no row
 //            attends to are not loaded.  One ring of five tiles, in the order of
 //            use.
-//   warp 10  MMA issue, warp 11  query loads.
+//   warp 10  MMA issue.
+//   warp 11  the plan, the CTA's shares (handed to the others through a queue of
+//            four) and their query loads.
 // Rows of V that no row of the item attends to may hold anything (0 x NaN is
 // NaN): the softmax threads zero them in shared memory.
+//
+// Bounds.  Prefill: the tensor cores.  4 d FLOP per query row and key; S has both
+// operands in shared memory, 128 bytes a cycle, all that there is.  One tile of
+// two query tiles takes 2048 cycles at their full rate and 3100 to 3300 here:
+// what is left are the waits between softmax and products (a row's softmax takes
+// 1100 cycles to its first half, 1500 to its second, and each group's products
+// 1024).  Measured: 8192 causal tokens, 64 heads: 670 us, 1640 TFLOP/s (86 % of
+// cuBLAS's burst rate); 32768 tokens, 32 heads, a window of 4096: 1370 us, 1500
+// TFLOP/s of useful products (6 % more are computed at the window's edges).  ncu
+// (4096 tokens): tensor pipe 62 % of its active peak, special functions 31 %,
+// issue 39 %, DRAM 7 %.
+// Decode: HBM.  64 sequences, a window of 4096, 8 KV heads (0.99 GB): 157 us, 6.3
+// TB/s (94 % of a copy's rate); one sequence of 131072 tokens (0.54 GB): 87 us.
+// ncu: 382 MB read where 373 are needed.
+// Few tokens: latency.  4 sequences' 260 tokens: 10.4 us on the GPU, of which the
+// plan takes 1.5, the first share 1.1, its first key 1.7, the tile 1.4, the end
+// 0.9.
 #include <cuda.h>
 
 #include <algorithm>
@@ -583,223 +604,224 @@ __global__ void __launch_bounds__(kThreads, 1)
   // queries load while this one's are in use); a pair's tiles have both.
   auto q_buffer = [&]() { return (uses[0] + uses[1]) & 1u; };
   if (warp >= kKWarp) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == kKWarp || warp == kVWarp) {
-    // ---- K loads, V loads: lanes 0-3 issue the two 64-column halves of the two boxes
-    const bool is_k = warp == kKWarp;
-    const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
-    const int h = (lane >> 1) & 1, half = lane & 1;
-    // Where a sequence has few rows its keys are read once: they are the first
-    // to leave L2 (32 sequences over a 32K prefix: 45 us, 50 without
-    // the hint; 54 with tiles prefetched into L2 ahead of the ring).  Whole
-    // items share their keys (677 against 667 us with the hint).
-    const uint64_t once = policy_evict_first();
-    uint32_t mine[4] = {0, 0, 0, 0};   // places + 1 of this warp's newest loads
-    while (take()) {
-      const int n = pc.n, ahead = (pc.flags & kPair) ? 1 : 2;
-      int64_t row = -1;   // of lane's box of 16 tiles from tile i on; -1: no row attends to the box
-      for (int i = 0; i < n; ++i) {
-        if ((i & 15) == 0) {
-          const int k = pc.k0 + i + (lane >> 1);
-          row = -1;
-          if (k < pc.k0 + n) {
-            bool prefix;
-            const int tok = tile_token(pc, k, &prefix) + (lane & 1) * kBox;
-            if (any_row_sees_box(p, pc, prefix, tok)) {
-              row = cache_row(prefix ? p.a.pm_prefix : p.a.pm, prefix ? 0 : pc.b, pc.g, p.Hkv, p.n_cap, tok);
-              if (row < 0) {
-                record_error(p.err, kErrBadPage);
-                row = 0;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kKWarp || warp == kVWarp) {
+      // ---- K loads, V loads: lanes 0-3 issue the two 64-column halves of the two boxes
+      const bool is_k = warp == kKWarp;
+      const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+      const int h = (lane >> 1) & 1, half = lane & 1;
+      // Where a sequence has few rows its keys are read once: they are the first
+      // to leave L2 (32 sequences over a 32K prefix: 45 us, 50 without
+      // the hint; 54 with tiles prefetched into L2 ahead of the ring).  Whole
+      // items share their keys (677 against 667 us with the hint).
+      const uint64_t once = policy_evict_first();
+      uint32_t mine[4] = {0, 0, 0, 0};   // places + 1 of this warp's newest loads
+      while (take()) {
+        const int n = pc.n, ahead = (pc.flags & kPair) ? 1 : 2;
+        int64_t row = -1;   // of lane's box of 16 tiles from tile i on; -1: no row attends to the box
+        for (int i = 0; i < n; ++i) {
+          if ((i & 15) == 0) {
+            const int k = pc.k0 + i + (lane >> 1);
+            row = -1;
+            if (k < pc.k0 + n) {
+              bool prefix;
+              const int tok = tile_token(pc, k, &prefix) + (lane & 1) * kBox;
+              if (any_row_sees_box(p, pc, prefix, tok)) {
+                row = cache_row(prefix ? p.a.pm_prefix : p.a.pm, prefix ? 0 : pc.b, pc.g, p.Hkv, p.n_cap, tok);
+                if (row < 0) {
+                  record_error(p.err, kErrBadPage);
+                  row = 0;
+                }
               }
             }
           }
-        }
-        const int64_t row0 = __shfl_sync(0xffffffffu, row, 2 * (i & 15)), row1 = __shfl_sync(0xffffffffu, row, 2 * (i & 15) + 1);
-        const uint32_t at = ring + (is_k ? k_place(i, ahead) : v_place(i, n, ahead)), slot = at % kSlots;
-        wait(&S.empty[slot], ((at / kSlots) & 1u) ^ 1u);
-        if (dead) break;
-        if (lane == 0) mbar_arrive_expect_tx(&S.full[slot], ((row0 >= 0) + (row1 >= 0)) * 2 * kBoxBytes);
-        __syncwarp();
-        const int64_t y = h ? row1 : row0;
-        if (lane < 4 && y >= 0) {
-          uint8_t* dst = S.kv[slot] + half * kHalf + h * kBoxBytes;
-          if (p.once) tma_load_2d_hint(dst, tm, half * 64, static_cast<int32_t>(y), &S.full[slot], once);
-          else tma_load_2d(dst, tm, half * 64, static_cast<int32_t>(y), &S.full[slot]);
-        }
-        mine[3] = mine[2];
-        mine[2] = mine[1];
-        mine[1] = mine[0];
-        mine[0] = at + 1;
-      }
-      ring += 2 * n;
-    }
-    // Every load is over once the MMA warp has waited for it; where a wait ran
-    // out, nothing of this warp stays in flight past here (of the ring's five
-    // tiles at most four are one warp's).
-    if (dead)
-      for (int i = 0; i < 4; ++i)
-        if (mine[i] > 0) wait_warp(&S.full[(mine[i] - 1) % kSlots], ((mine[i] - 1) / kSlots) & 1u);
-  } else if (warp == kQWarp) {
-    // ---- the plan, the pieces, and their queries
-    Plan plan;
-    if (p.plan_global) {
-      plan.ent_base = p.ent_base;
-      plan.line = p.line;
-      plan.entries = p.split ? p.ent_base[p.B + p.pre] : p.B;
-    } else {
-      int32_t* line = S.plan + (p.split ? p.B + p.pre + 1 : 0);
-      plan.ent_base = S.plan;
-      plan.line = line;
-      plan.entries = make_plan<false>(p, S.plan, line, blockIdx.x == 0);
-    }
-    Walk walk;
-    walk.init(p, plan);
-    const int half = lane & 1;
-    bool more = true;
-    while (more && !dead) {
-      more = walk.next(p, plan, pc);
-      const uint32_t i = pieces % kQueue;
-      wait(&S.pc_empty[i], ((pieces / kQueue) & 1u) ^ 1u);
-      if (dead) break;
-      if (lane == 0) {
-        if (!more) pc.n = -1;
-        S.piece[i] = pc;
-        mbar_arrive(&S.pc_full[i]);
-      }
-      ++pieces;
-      if (!more || pc.n == 0) continue;
-      const bool pair = pc.flags & kPair;
-      const uint32_t b0 = pair ? 0 : q_buffer(), nb = pair && pc.rows > kTile ? 2 : 1;
-      for (uint32_t t = 0; t < nb; ++t) {
-        const uint32_t b = b0 + t;
-        wait(&S.q_empty[b], (uses[b] & 1u) ^ 1u);
-        if (dead) break;
-        if (lane == 0) mbar_arrive_expect_tx(&S.q_full[b], kTileBytes);
-        __syncwarp();
-        if (lane < 2)
-          tma_load_3d(S.q[b] + half * kHalf, &tm_q, half * 64, pc.g << p.gsh, pc.tok0 + static_cast<int>((t * kTile) >> p.gsh),
-                      &S.q_full[b]);
-        ++uses[b];
-      }
-    }
-    if (dead)
-      for (int b = 0; b < 2; ++b)
-        if (uses[b] > 0) wait_warp(&S.q_full[b], (uses[b] - 1) & 1u);
-  } else if (warp == kMmaWarp) {
-    // ---- MMA issue.  The whole warp walks and waits, and one elected lane
-    // issues: in code that only one lane runs every operand of an MMA is moved
-    // to the uniform registers for itself, and the issue falls behind the
-    // tensor cores (85-130 cycles per MMA of 64).  One warp issues for both
-    // groups: with a warp each, their products interleave and each group's
-    // arrive later (909 against 807 us at 8192 causal tokens, 64 heads).
-    const bool leader = elect_one();
-    constexpr uint32_t idesc_s = mma_idesc(128, 128);
-    constexpr uint32_t idesc_o = mma_idesc(128, 128) | (1u << 16);   // B (V) MN-major
-    constexpr uint32_t kStep = kTileBytes >> 4;                      // of a descriptor, from slot to slot
-    const uint32_t tS = __shfl_sync(0xffffffffu, tmem, 0), tO = tS + 256;
-    const uint64_t qd = sw128_desc(smem_u32(S.q[0])), kd = sw128_desc(smem_u32(S.kv[0]));
-    const uint64_t vd = sw128_mn_desc(smem_u32(S.kv[0]), kHalf, 1024);
-    uint32_t np = 0;   // bit s: phase of the probabilities of group s
-    // A wait that ran out ends the loop over the tiles, not the tile: its
-    // products are computed on what is there.
-    // Waits for the next tile of the ring; its slot.
-    auto next_tile = [&]() {
-      const uint32_t slot = ring % kSlots;
-      wait(&S.full[slot], (ring / kSlots) & 1u);
-      ++ring;
-      return slot;
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (leader) mma_commit(bar);
-    };
-    auto qk = [&](uint32_t s, uint32_t qtile, uint32_t slot) {   // S_s = Q_qtile K^T
-      tc_fence_after();
-      const uint64_t ad = qd + qtile * kStep, bd = kd + slot * kStep;
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint64_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-          mma_bf16(tS + kTile * s, ad + off, bd + off, idesc_s, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(&S.s_full[s]);
-      }
-    };
-    auto pv = [&](uint32_t s, uint32_t slot, bool first) {   // O_s (+)= P_s V
-      const uint64_t bd = vd + slot * kStep;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        wait(&S.p_full[s][h], (np >> s) & 1u);
-        tc_fence_after();
-        if (leader) {
-#pragma unroll
-          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-            mma_bf16_ta(tO + kTile * s, tS + kTile * s + 8 * kk, bd + (kk * 2048 >> 4), idesc_o,
-                        (kk > 0 || !first) ? 1u : 0u);
-        }
-      }
-      np ^= 1u << s;
-    };
-    while (take()) {
-      const int n = __shfl_sync(0xffffffffu, pc.n, 0);
-      if (n == 0) continue;
-      if (pc.flags & kPair) {
-        // Tile k's S is issued behind tile k - 1's O of the same group.  The
-        // waits for the next tiles' V and K (some 200 cycles each, even when
-        // the data is there) stand around group 1's O, where the tensor cores
-        // have work meanwhile; six other orders measured 680 to 706 us against
-        // 677 (8192 causal tokens, 64 heads).
-        const bool two = pc.rows > kTile;
-        uint32_t kslot = next_tile(), vslot = 0;
-        wait(&S.q_full[0], uses[0] & 1u);
-        ++uses[0];
-        if (two) {
-          wait(&S.q_full[1], uses[1] & 1u);
-          ++uses[1];
-        }
-        for (int k = -1; k < n && !dead; ++k) {
-          const bool has_k = k + 1 < n;
-          if (k >= 0) pv(0, vslot, k == 0);
-          if (has_k) qk(0, 0, kslot);
-          else commit(&S.o_full[0]);
-          uint32_t vnext = 0, knext = 0;
-          if (has_k) vnext = next_tile();
-          if (two && k >= 0) pv(1, vslot, k == 0);
-          if (k + 2 < n) knext = next_tile();
-          if (two) {
-            if (has_k) qk(1, 1, kslot);
-            else commit(&S.o_full[1]);
+          const int64_t row0 = __shfl_sync(0xffffffffu, row, 2 * (i & 15));
+          const int64_t row1 = __shfl_sync(0xffffffffu, row, 2 * (i & 15) + 1);
+          const uint32_t at = ring + (is_k ? k_place(i, ahead) : v_place(i, n, ahead)), slot = at % kSlots;
+          wait(&S.empty[slot], ((at / kSlots) & 1u) ^ 1u);
+          if (dead) break;
+          if (lane == 0) mbar_arrive_expect_tx(&S.full[slot], ((row0 >= 0) + (row1 >= 0)) * 2 * kBoxBytes);
+          __syncwarp();
+          const int64_t y = h ? row1 : row0;
+          if (lane < 4 && y >= 0) {
+            uint8_t* dst = S.kv[slot] + half * kHalf + h * kBoxBytes;
+            if (p.once) tma_load_2d_hint(dst, tm, half * 64, static_cast<int32_t>(y), &S.full[slot], once);
+            else tma_load_2d(dst, tm, half * 64, static_cast<int32_t>(y), &S.full[slot]);
           }
-          if (k >= 0) commit(&S.empty[vslot]);
-          if (has_k) commit(&S.empty[kslot]);
-          if (k + 1 == n - 1) {
-            commit(&S.q_empty[0]);
-            if (two) commit(&S.q_empty[1]);
-          }
-          vslot = vnext;
-          kslot = knext;
+          mine[3] = mine[2];
+          mine[2] = mine[1];
+          mine[1] = mine[0];
+          mine[0] = at + 1;
         }
+        ring += 2 * n;
+      }
+      // Every load is over once the MMA warp has waited for it; where a wait ran
+      // out, nothing of this warp stays in flight past here (of the ring's five
+      // tiles at most four are one warp's).
+      if (dead)
+        for (int i = 0; i < 4; ++i)
+          if (mine[i] > 0) wait_warp(&S.full[(mine[i] - 1) % kSlots], ((mine[i] - 1) / kSlots) & 1u);
+    } else if (warp == kQWarp) {
+      // ---- the plan, the pieces, and their queries
+      Plan plan;
+      if (p.plan_global) {
+        plan.ent_base = p.ent_base;
+        plan.line = p.line;
+        plan.entries = p.split ? p.ent_base[p.B + p.pre] : p.B;
       } else {
-        const uint32_t qb = q_buffer();
-        wait(&S.q_full[qb], uses[qb] & 1u);
-        ++uses[qb];
-        for (int k = -2; k < n && !dead; ++k) {
-          const uint32_t s = k & 1;   // tile k + 2 is of the same group
-          if (k >= 0) {
-            const uint32_t slot = next_tile();
-            pv(s, slot, k < 2);
-            commit(&S.empty[slot]);
-            if (k >= n - 2) commit(&S.o_full[s]);
+        int32_t* line = S.plan + (p.split ? p.B + p.pre + 1 : 0);
+        plan.ent_base = S.plan;
+        plan.line = line;
+        plan.entries = make_plan<false>(p, S.plan, line, blockIdx.x == 0);
+      }
+      Walk walk;
+      walk.init(p, plan);
+      const int half = lane & 1;
+      bool more = true;
+      while (more && !dead) {
+        more = walk.next(p, plan, pc);
+        const uint32_t i = pieces % kQueue;
+        wait(&S.pc_empty[i], ((pieces / kQueue) & 1u) ^ 1u);
+        if (dead) break;
+        if (lane == 0) {
+          if (!more) pc.n = -1;
+          S.piece[i] = pc;
+          mbar_arrive(&S.pc_full[i]);
+        }
+        ++pieces;
+        if (!more || pc.n == 0) continue;
+        const bool pair = pc.flags & kPair;
+        const uint32_t b0 = pair ? 0 : q_buffer(), nb = pair && pc.rows > kTile ? 2 : 1;
+        for (uint32_t t = 0; t < nb; ++t) {
+          const uint32_t b = b0 + t;
+          wait(&S.q_empty[b], (uses[b] & 1u) ^ 1u);
+          if (dead) break;
+          if (lane == 0) mbar_arrive_expect_tx(&S.q_full[b], kTileBytes);
+          __syncwarp();
+          if (lane < 2)
+            tma_load_3d(S.q[b] + half * kHalf, &tm_q, half * 64, pc.g << p.gsh,
+                        pc.tok0 + static_cast<int>((t * kTile) >> p.gsh), &S.q_full[b]);
+          ++uses[b];
+        }
+      }
+      if (dead)
+        for (int b = 0; b < 2; ++b)
+          if (uses[b] > 0) wait_warp(&S.q_full[b], (uses[b] - 1) & 1u);
+    } else if (warp == kMmaWarp) {
+      // ---- MMA issue.  The whole warp walks and waits, and one elected lane
+      // issues: in code that only one lane runs every operand of an MMA is moved
+      // to the uniform registers for itself, and the issue falls behind the
+      // tensor cores (85-130 cycles per MMA of 64).  One warp issues for both
+      // groups: with a warp each, their products interleave and each group's
+      // arrive later (909 against 807 us at 8192 causal tokens, 64 heads).
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_s = mma_idesc(128, 128);
+      constexpr uint32_t idesc_o = mma_idesc(128, 128) | (1u << 16);   // B (V) MN-major
+      constexpr uint32_t kStep = kTileBytes >> 4;                      // of a descriptor, from slot to slot
+      const uint32_t tS = __shfl_sync(0xffffffffu, tmem, 0), tO = tS + 256;
+      const uint64_t qd = sw128_desc(smem_u32(S.q[0])), kd = sw128_desc(smem_u32(S.kv[0]));
+      const uint64_t vd = sw128_mn_desc(smem_u32(S.kv[0]), kHalf, 1024);
+      uint32_t np = 0;   // bit s: phase of the probabilities of group s
+      // A wait that ran out ends the loop over the tiles, not the tile: its
+      // products are computed on what is there.
+      // Waits for the next tile of the ring; its slot.
+      auto next_tile = [&]() {
+        const uint32_t slot = ring % kSlots;
+        wait(&S.full[slot], (ring / kSlots) & 1u);
+        ++ring;
+        return slot;
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) mma_commit(bar);
+      };
+      auto qk = [&](uint32_t s, uint32_t qtile, uint32_t slot) {   // S_s = Q_qtile K^T
+        tc_fence_after();
+        const uint64_t ad = qd + qtile * kStep, bd = kd + slot * kStep;
+        if (leader) {
+  #pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+            mma_bf16(tS + kTile * s, ad + off, bd + off, idesc_s, kk > 0 ? 1u : 0u);
           }
-          if (k + 2 < n) {
-            const uint32_t slot = next_tile();
-            qk(s, qb, slot);
-            commit(&S.empty[slot]);
-            if (k + 2 == n - 1) commit(&S.q_empty[qb]);
+          mma_commit(&S.s_full[s]);
+        }
+      };
+      auto pv = [&](uint32_t s, uint32_t slot, bool first) {   // O_s (+)= P_s V
+        const uint64_t bd = vd + slot * kStep;
+  #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          wait(&S.p_full[s][h], (np >> s) & 1u);
+          tc_fence_after();
+          if (leader) {
+  #pragma unroll
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+              mma_bf16_ta(tO + kTile * s, tS + kTile * s + 8 * kk, bd + (kk * 2048 >> 4), idesc_o,
+                          (kk > 0 || !first) ? 1u : 0u);
+          }
+        }
+        np ^= 1u << s;
+      };
+      while (take()) {
+        const int n = __shfl_sync(0xffffffffu, pc.n, 0);
+        if (n == 0) continue;
+        if (pc.flags & kPair) {
+          // Tile k's S is issued behind tile k - 1's O of the same group.  The
+          // waits for the next tiles' V and K (some 200 cycles each, even when
+          // the data is there) stand around group 1's O, where the tensor cores
+          // have work meanwhile; six other orders measured 680 to 706 us against
+          // 677 (8192 causal tokens, 64 heads).
+          const bool two = pc.rows > kTile;
+          uint32_t kslot = next_tile(), vslot = 0;
+          wait(&S.q_full[0], uses[0] & 1u);
+          ++uses[0];
+          if (two) {
+            wait(&S.q_full[1], uses[1] & 1u);
+            ++uses[1];
+          }
+          for (int k = -1; k < n && !dead; ++k) {
+            const bool has_k = k + 1 < n;
+            if (k >= 0) pv(0, vslot, k == 0);
+            if (has_k) qk(0, 0, kslot);
+            else commit(&S.o_full[0]);
+            uint32_t vnext = 0, knext = 0;
+            if (has_k) vnext = next_tile();
+            if (two && k >= 0) pv(1, vslot, k == 0);
+            if (k + 2 < n) knext = next_tile();
+            if (two) {
+              if (has_k) qk(1, 1, kslot);
+              else commit(&S.o_full[1]);
+            }
+            if (k >= 0) commit(&S.empty[vslot]);
+            if (has_k) commit(&S.empty[kslot]);
+            if (k + 1 == n - 1) {
+              commit(&S.q_empty[0]);
+              if (two) commit(&S.q_empty[1]);
+            }
+            vslot = vnext;
+            kslot = knext;
+          }
+        } else {
+          const uint32_t qb = q_buffer();
+          wait(&S.q_full[qb], uses[qb] & 1u);
+          ++uses[qb];
+          for (int k = -2; k < n && !dead; ++k) {
+            const uint32_t s = k & 1;   // tile k + 2 is of the same group
+            if (k >= 0) {
+              const uint32_t slot = next_tile();
+              pv(s, slot, k < 2);
+              commit(&S.empty[slot]);
+              if (k >= n - 2) commit(&S.o_full[s]);
+            }
+            if (k + 2 < n) {
+              const uint32_t slot = next_tile();
+              qk(s, qb, slot);
+              commit(&S.empty[slot]);
+              if (k + 2 == n - 1) commit(&S.q_empty[qb]);
+            }
           }
         }
       }
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---- softmax and output: group s = warp / 4, row r of its tile
@@ -939,7 +961,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (warp_rows) {
         const bool active = row < pc.rows, whole = pc.flags & kWhole;   // the row exists
-        const int64_t orow = (static_cast<int64_t>(pc.tok0) + (row >> p.gsh)) * p.Hq + (pc.g << p.gsh) + (row & ((1 << p.gsh) - 1));
+        const int64_t orow =
+            (static_cast<int64_t>(pc.tok0) + (row >> p.gsh)) * p.Hq + (pc.g << p.gsh) + (row & ((1 << p.gsh) - 1));
         // this group's share: pc.rows rows, chunk-major (32 lanes store 512 contiguous bytes)
         const int64_t part0 = pc.part + (pair ? 0 : s * pc.rows);
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
@@ -1136,7 +1159,8 @@ int64_t most_tiles(const KvAttnArgs& a, int64_t n_cap, int gq) {
 // SMs, a split costs the merge, and more for the partial rows of pair items.
 bool split_is_faster(int64_t T, int B, int gq, int Hkv, int64_t tiles, int num_sms) {
   const bool pair = T * gq > static_cast<int64_t>(kTile) * B;
-  const int64_t items = Hkv * static_cast<int64_t>(B) * ((T * gq + static_cast<int64_t>(kItemRows) * B - 1) / (static_cast<int64_t>(kItemRows) * B));
+  const int64_t seq_rows = static_cast<int64_t>(kItemRows) * B;   // an item's of every sequence
+  const int64_t items = static_cast<int64_t>(Hkv) * B * ((T * gq + seq_rows - 1) / seq_rows);
   const double per_sm = static_cast<double>(items) / num_sms, rounds = static_cast<double>((items + num_sms - 1) / num_sms);
   const double whole = pair ? 8.0 + rounds * (1.35 * tiles + 5.0) : 3.7 + rounds * (1.4 * tiles + 4.5);
   const double split = pair ? 20.0 + per_sm * (1.7 * tiles + 20.0) : 12.0 + per_sm * (1.3 * tiles + 4.0);
@@ -1193,11 +1217,12 @@ cudaError_t configure_kv_attn_kernels(const DeviceInfo&) {
   cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(sizeof(Smem) + 1024));
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kv_merge_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(merge_smem(kMaxEnt)));
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(kv_merge_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(merge_smem(kMaxEnt)));
+  const int merge = static_cast<int>(merge_smem(kMaxEnt));
+  if ((e = cudaFuncSetAttribute(kv_merge_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, merge)) != cudaSuccess)
+    return e;
+  if ((e = cudaFuncSetAttribute(kv_merge_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, merge)) != cudaSuccess)
+    return e;
+  return cudaFuncSetAttribute(kv_merge_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, merge);
 }
 
 int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream) {
@@ -1241,11 +1266,14 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const 
   }
   e = launch_dependent(kv_attn_kernel, dim3(dev.num_sms), dim3(kThreads), sizeof(Smem) + 1024, stream, 1, p, tq, tk, tv);
   if (e != cudaSuccess || !p.split) return e;
-  // Few rows: four thread groups to an element.
-  const bool few = a.bt.T * s.Hq <= 1024;
-  const int per_unit = kMergeThreads / (few ? 4 : 1) / kChunks;
+  // Few rows: several thread groups to an element (one 128K sequence 86.3 us,
+  // 32 over a 32K prefix 42.7; with one group from 1024 rows on 43.8, with four
+  // up to 4096 rows 64 sequences with a 4K window 159 against 157).
+  const int64_t out_rows = a.bt.T * s.Hq;
+  const int pg = out_rows <= 512 ? 4 : (out_rows <= 2048 ? 2 : 1), per_unit = kMergeThreads / pg / kChunks;
   const int64_t units = (a.bt.T * gq + per_unit - 1) / per_unit * s.Hkv, most = static_cast<int64_t>(dev.num_sms) * 8;
-  return launch_dependent(few ? kv_merge_kernel<4> : kv_merge_kernel<1>, dim3(static_cast<unsigned>(units < most ? units : most)),
+  const auto merge = pg == 4 ? kv_merge_kernel<4> : (pg == 2 ? kv_merge_kernel<2> : kv_merge_kernel<1>);
+  return launch_dependent(merge, dim3(static_cast<unsigned>(units < most ? units : most)),
                           dim3(kMergeThreads), merge_smem(p.max_ent), stream, 1, p, dev.num_sms);
 }
 
