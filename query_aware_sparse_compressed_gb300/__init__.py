@@ -619,7 +619,7 @@ def kv_prefix_attn_paged(q, K_pool, V_pool, prefix_table, block_table, kv_lens, 
     _table(block_table)
     pt = None
     if n_prefix > 0:
-        pt = _at(prefix_table, "prefix_table", _I32, (-(-n_prefix // K_pool.shape[2]),), q.get_device())
+        pt = _at(prefix_table, "prefix_table", _I32, (-(-n_prefix // K_pool.shape[2]),), block_table.get_device())
     _attn("kv_prefix_attn_paged", q, K_pool, V_pool, block_table, kv_lens, out, workspace, cu_q, lse, stream,
           (pt, n_prefix), ())
 

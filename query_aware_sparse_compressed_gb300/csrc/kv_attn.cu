@@ -113,8 +113,8 @@ struct Args {
   int slot_rows;            // partial rows a CTA may add to an item (split)
   float4* part_o;           // [rows][32] of a share: element (row, chunk) at chunk * rows + row
   float2* part_ml;          // [rows] (max in log2 units, sum)
-  int32_t* ent_base;        // [kMaxSeq + 1] the plan in global memory: written by plan_kernel, or
-  int32_t* line;            // [kMaxEnt + 1] (line and info alone, for the merge) by CTA 0
+  int32_t* ent_base;        // [kMaxSeq + 1] the plan in global memory: written by kv_plan_kernel, or by
+  int32_t* line;            // [kMaxEnt + 1] CTA 0 for the merge
   int4* info;               // [kMaxEnt] per entry: first token of the sequence, first row, rows, sequence (< 0: prefix)
   int max_ent;              // entries that T tokens of B sequences can make (malformed cu_q is cut to it)
   int plan_global;          // the plan is too large for shared memory
