@@ -21,8 +21,9 @@
 // 1.35 times the rounding alone); the sum that divides takes the unrounded fp32
 // values, so lse is as exact as fp32.
 //
-// Work.  Two schedules, chosen by the numbers of rows and tiles (split_is_faster):
-//   whole  many items: CTA c takes items c, c + G, ... whole, heaviest first.
+// Work.  Two schedules, chosen by the numbers of rows and tiles (window_schedule):
+//   whole  many items, or short ones: CTA c takes items c, c + G, ... whole,
+//          heaviest first (items of 128 rows where those of 256 are few).
 //   split  few items: the tiles of all items are laid end to end and every CTA
 //          takes an equal range of that line; an item that several CTAs share
 //          leaves partial (max, sum, O) rows in the workspace and kv_merge_kernel
@@ -37,7 +38,8 @@
 //   warps 0-3, 4-7  softmax: group s owns accumulators S_s and O_s, thread r
 //            row r.  An item of more than 128 rows gives each group a query
 //            tile (pair); a smaller one gives the groups alternate key tiles
-//            (parity), each with its own statistics and partial rows.
+//            (parity), each with its own statistics and O, joined by group 0 or
+//            (of a share) by the merge.
 //   warp 8   K loads, warp 9  V loads (TMA, 64-row boxes: a page holds at least
 //            64 tokens, so a box never leaves its page).  Boxes that no row
 //            attends to are not loaded.  One ring of five tiles, in the order of
@@ -53,17 +55,19 @@
 // two query tiles takes 2048 cycles at their full rate and 3100 to 3300 here:
 // what is left are the waits between softmax and products (a row's softmax takes
 // 1100 cycles to its first half, 1500 to its second, and each group's products
-// 1024).  Measured: 8192 causal tokens, 64 heads: 670 us, 1640 TFLOP/s (86 % of
-// cuBLAS's burst rate); 32768 tokens, 32 heads, a window of 4096: 1370 us, 1500
+// 1024).  Measured: 8192 causal tokens, 64 heads: 665 us, 1650 TFLOP/s (86 % of
+// cuBLAS's burst rate); 32768 tokens, 32 heads, a window of 4096: 1360 us, 1515
 // TFLOP/s of useful products (6 % more are computed at the window's edges).  ncu
 // (4096 tokens): tensor pipe 62 % of its active peak, special functions 31 %,
 // issue 39 %, DRAM 7 %.
 // Decode: HBM.  64 sequences, a window of 4096, 8 KV heads (0.99 GB): 157 us, 6.3
 // TB/s (94 % of a copy's rate); one sequence of 131072 tokens (0.54 GB): 87 us.
 // ncu: 382 MB read where 373 are needed.
-// Few tokens: latency.  4 sequences' 260 tokens: 10.4 us on the GPU, of which the
-// plan takes 1.5, the first share 1.1, its first key 1.7, the tile 1.4, the end
-// 0.9.
+// Few tokens: latency.  4 sequences' 260 tokens: 9.6 us on the GPU, of which the
+// plan takes 1.5, the first share 1.1, its first key 1.7, a tile 0.7 to 1.4.  16
+// ragged sequences of 1 to 64 tokens, up to 1400 cached: 18 us with items of 128
+// rows, joined in the block; with 256-row items and a join by the merge 30.
+// A shared prefix: 128 sequences over 131072 tokens, 64 heads: 257 us.
 #include <cuda.h>
 
 #include <algorithm>
@@ -108,6 +112,7 @@ struct Args {
   KvAttnArgs a;
   int B, Hq, Hkv, gsh;      // gsh = log2(Hq / Hkv)
   int64_t n_cap;
+  int item_rows;            // query rows of an item: 256, or 128 (whole only)
   int once;                 // keys are read by one item, or two
   int split, pre;           // pre: the shared prefix is sequence 0 of the plan (split only)
   int slot_rows;            // partial rows a CTA may add to an item (split)
@@ -132,7 +137,7 @@ struct alignas(16) Piece {
   int flags;
   int64_t part;       // first partial row
 };
-constexpr int kPair = 1;    // two query tiles (or the first alone); else the groups take alternate key tiles
+constexpr int kPair = 1;    // two query tiles, one per group; else the groups take alternate key tiles of one
 constexpr int kWhole = 2;   // every tile of the item: the output is written, not a partial
 
 struct Smem {
@@ -143,11 +148,13 @@ struct Smem {
   uint64_t q_full[2], q_empty[2];
   uint64_t full[kSlots], empty[kSlots];
   uint64_t s_full[2], p_full[2][2], o_full[2];   // p_full: the first and last 64 tokens
+  uint64_t x_full, x_empty;                      // group 1's part of a whole parity item is there, is taken
+  float2 x_ml[kTile];                            // its rows' (max in log2 units, sum)
   uint32_t tmem_base;
   int32_t plan[kPlanWords];
 };
 
-static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory of a block");
+static_assert(sizeof(Smem) <= 232448, "shared memory of a block");
 
 // ent_base[s]: items per KV head before sequence s (split).  line: places
 // before entry e, all KV heads (split); items before sequence s (whole).
@@ -203,8 +210,8 @@ __device__ __forceinline__ int ceil_tiles(int64_t n) { return static_cast<int>((
 __device__ __forceinline__ Item make_item(const Args& p, const Seq& s, int qt) {
   Item it;
   it.s = s;
-  it.r0 = qt * kItemRows;
-  it.rows = min(kItemRows, (s.ql << p.gsh) - it.r0);
+  it.r0 = qt * p.item_rows;
+  it.rows = min(p.item_rows, (s.ql << p.gsh) - it.r0);
   it.ns = 0;
   it.w0 = 0;
   it.p0 = s.len - s.ql + (it.r0 >> p.gsh);
@@ -285,7 +292,7 @@ __device__ __forceinline__ int find_last(const int32_t* arr, int n, int x) {
 }
 
 __device__ __forceinline__ int q_tiles(const Args& p, const Seq& s) {
-  return ((s.ql << p.gsh) + kItemRows - 1) / kItemRows;
+  return ((s.ql << p.gsh) + p.item_rows - 1) / p.item_rows;
 }
 
 // Exclusive prefix sums of f(0) .. f(n - 1) into arr[0 .. n], by a warp or
@@ -351,9 +358,9 @@ __device__ __forceinline__ int make_plan(const Args& p, int32_t* ent_base, int32
 }
 
 // First partial row of an item's share of CTA c.  Two rows of the area belong
-// to every query row (a parity item leaves two), ordered as the line is; each
-// CTA crossed adds slot_rows, the most rows of one share, so that no two
-// shares overlap.
+// to every query row (each group leaves one of a parity item), ordered as the
+// line is; each CTA crossed adds slot_rows, the most rows of one share, so that
+// no two shares overlap.
 __device__ __forceinline__ int64_t part_row(const Args& p, const Item& it, int g, int cta) {
   const int64_t fam = p.pre && it.s.b >= 0 ? p.a.bt.T * p.Hq : 0;   // the prefix's shares stand first
   const int64_t row = fam + static_cast<int64_t>(it.s.q0) * p.Hq + static_cast<int64_t>(it.r0) * p.Hkv +
@@ -362,6 +369,7 @@ __device__ __forceinline__ int64_t part_row(const Args& p, const Item& it, int g
 }
 
 // The shares of this CTA in order.
+template <bool kSplit>
 struct Walk {
   int pos, end, n;   // split: place on the line, its end; whole: round
   int e, s;          // split: current entry and its sequence
@@ -370,7 +378,7 @@ struct Walk {
     pos = end = 0;
     if (n == 0) return;
     const int U = S.line[n];
-    if (p.split) {
+    if (kSplit) {
       const Ranges line(U, gridDim.x);
       if (blockIdx.x >= line.G) return;
       pos = line.start(blockIdx.x);
@@ -384,7 +392,7 @@ struct Walk {
   __device__ __forceinline__ bool next(const Args& p, const Plan& S, Piece& pc) {
     Item it;
     int g;
-    if (p.split) {
+    if (kSplit) {
       int off, take, span, w;
       while (true) {
         if (pos >= end) return false;
@@ -423,7 +431,7 @@ struct Walk {
       g = rem % p.Hkv;
       pc.k0 = 0;
       pc.n = it.cnt;
-      pc.flags = kPair | kWhole;
+      pc.flags = (it.rows > kTile ? kPair : 0) | kWhole;
       pc.part = 0;
     }
     pc.tok0 = it.s.q0 + (it.r0 >> p.gsh);
@@ -542,12 +550,20 @@ __device__ __forceinline__ bool elect_one() {
 // Bits [0, n) of a word, n any integer.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
+// kSplit: the schedule.  Two kernels, since the code of one schedule costs the
+// other: with the join of whole parity items in the split's kernel 128 sequences
+// over a 128K prefix take 297 us, without it 262.
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_attn_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Smem& S = *reinterpret_cast<Smem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(smem_raw) & 1023u) {   // the tiles' swizzle counts from here; the whole block leaves
+    record_error(p.err, kErrInternal);
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(&S.pc_full[i], 1);
@@ -565,6 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.p_full[i][1], 4);
       mbar_init(&S.o_full[i], 1);
     }
+    mbar_init(&S.x_full, 4);
+    mbar_init(&S.x_empty, 4);
     fence_barrier_init();
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
@@ -667,14 +685,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.plan_global) {
         plan.ent_base = p.ent_base;
         plan.line = p.line;
-        plan.entries = p.split ? p.ent_base[p.B + p.pre] : p.B;
+        plan.entries = kSplit ? p.ent_base[p.B + p.pre] : p.B;
       } else {
-        int32_t* line = S.plan + (p.split ? p.B + p.pre + 1 : 0);
+        int32_t* line = S.plan + (kSplit ? p.B + p.pre + 1 : 0);
         plan.ent_base = S.plan;
         plan.line = line;
         plan.entries = make_plan<false>(p, S.plan, line, blockIdx.x == 0);
       }
-      Walk walk;
+      Walk<kSplit> walk;
       walk.init(p, plan);
       const int half = lane & 1;
       bool more = true;
@@ -691,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++pieces;
         if (!more || pc.n == 0) continue;
         const bool pair = pc.flags & kPair;
-        const uint32_t b0 = pair ? 0 : q_buffer(), nb = pair && pc.rows > kTile ? 2 : 1;
+        const uint32_t b0 = pair ? 0 : q_buffer(), nb = pair ? 2 : 1;
         for (uint32_t t = 0; t < nb; ++t) {
           const uint32_t b = b0 + t;
           wait(&S.q_empty[b], (uses[b] & 1u) ^ 1u);
@@ -770,14 +788,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the data is there) stand around group 1's O, where the tensor cores
           // have work meanwhile; six other orders measured 680 to 706 us against
           // 677 (8192 causal tokens, 64 heads).
-          const bool two = pc.rows > kTile;
           uint32_t kslot = next_tile(), vslot = 0;
           wait(&S.q_full[0], uses[0] & 1u);
+          wait(&S.q_full[1], uses[1] & 1u);
           ++uses[0];
-          if (two) {
-            wait(&S.q_full[1], uses[1] & 1u);
-            ++uses[1];
-          }
+          ++uses[1];
           for (int k = -1; k < n && !dead; ++k) {
             const bool has_k = k + 1 < n;
             if (k >= 0) pv(0, vslot, k == 0);
@@ -785,17 +800,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             else commit(&S.o_full[0]);
             uint32_t vnext = 0, knext = 0;
             if (has_k) vnext = next_tile();
-            if (two && k >= 0) pv(1, vslot, k == 0);
+            if (k >= 0) pv(1, vslot, k == 0);
             if (k + 2 < n) knext = next_tile();
-            if (two) {
-              if (has_k) qk(1, 1, kslot);
-              else commit(&S.o_full[1]);
-            }
+            if (has_k) qk(1, 1, kslot);
+            else commit(&S.o_full[1]);
             if (k >= 0) commit(&S.empty[vslot]);
             if (has_k) commit(&S.empty[kslot]);
             if (k + 1 == n - 1) {
               commit(&S.q_empty[0]);
-              if (two) commit(&S.q_empty[1]);
+              commit(&S.q_empty[1]);
             }
             vslot = vnext;
             kslot = knext;
@@ -829,17 +842,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + kTile * s + lane_base, to = tmem + 256 + kTile * s + lane_base;
     uint32_t ns = 0, no = 0;   // accumulators S_s, O_s taken
+    uint32_t nx = 0;           // items joined
+    bool lent = false;         // group 1: group 0 may still be reading O_1 and x_ml
     while (take()) {
       const bool pair = pc.flags & kPair;
       const int n = pc.n;
       const uint32_t ring0 = ring;
       ring += 2 * n;
-      if (pair && kTile * s >= pc.rows) continue;      // no second query tile
       const int row = pair ? kTile * s + r : r;        // of the item
       const bool warp_rows = (warp & 3) * 32 < pc.rows - (pair ? kTile * s : 0);   // the warp has a row
       const int pos = pc.p0 + (row >> p.gsh);
       float m = -INFINITY, l = 0.0f;
       int done = 0;
+      if (lent) {   // the next product overwrites O_1, the next hand-over x_ml
+        wait(&S.x_empty, (nx - 1) & 1u);
+        lent = false;
+      }
       for (int k = 0; k < n && !dead; ++k) {
         if (!pair && (k & 1) != s) continue;
         bool prefix;
@@ -959,46 +977,98 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++no;
         tc_fence_after();
       }
+      // The statistics in log2 units.  Of a whole parity item group 0 joins both
+      // groups' (every thread has the same row in both) and writes the output;
+      // of a share each group leaves its own, since the groups would wait for
+      // each other (128 sequences over a 4K prefix: 56 us joined, 49 so).
+      const bool whole = !kSplit || (pc.flags & kWhole), join_groups = !kSplit && !pair;
+      float a0 = 1.0f, a1 = 0.0f;
+      m *= kScale;
+      if (join_groups) {
+        if (s == 1) {
+          S.x_ml[r] = make_float2(m, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.x_full);
+          ++nx;
+          lent = true;
+          continue;
+        }
+        wait(&S.x_full, nx & 1u);
+        if (dead) break;
+        ++nx;
+        tc_fence_after();
+        const float2 v = S.x_ml[r];
+        const float mt = fmaxf(m, v.x);
+        a0 = l != 0.0f ? ex2_approx(m - mt) : 0.0f;
+        a1 = v.y != 0.0f ? ex2_approx(v.x - mt) : 0.0f;
+        m = mt;
+        l = l * a0 + v.y * a1;
+      }
       if (warp_rows) {
-        const bool active = row < pc.rows, whole = pc.flags & kWhole;   // the row exists
+        const bool active = row < pc.rows;                // the row exists
+        const int64_t part = pc.part + (pair ? 0 : s * pc.rows);
         const int64_t orow =
             (static_cast<int64_t>(pc.tok0) + (row >> p.gsh)) * p.Hq + (pc.g << p.gsh) + (row & ((1 << p.gsh) - 1));
-        // this group's share: pc.rows rows, chunk-major (32 lanes store 512 contiguous bytes)
-        const int64_t part0 = pc.part + (pair ? 0 : s * pc.rows);
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-        float o[128];
-        if (done > 0) {
-          KV_TMEM_LD32(to, o);
-          KV_TMEM_LD32(to + 32, o + 32);
-          KV_TMEM_LD32(to + 64, o + 64);
-          KV_TMEM_LD32(to + 96, o + 96);
-          KV_TMEM_WAIT32(o);
-          KV_TIE32(o + 32);
-          KV_TIE32(o + 64);
-          KV_TIE32(o + 96);
+        auto store_out = [&](const float* o, int c) {   // 32 columns from c on
+          uint4* dst = reinterpret_cast<uint4*>(p.a.out + orow * kD + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                                pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+        };
+        if (join_groups) {
+          const float b0 = done > 0 ? a0 * inv : 0.0f, b1 = a1 * inv;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            float o[32], y[32];
+            KV_TMEM_LD32(to + c, o);   // holds anything where the group had no tile
+            KV_TMEM_LD32(to + kTile + c, y);
+            KV_TMEM_WAIT32(o);
+            KV_TIE32(y);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = (done > 0 ? o[i] * b0 : 0.0f) + (n > 1 ? y[i] * b1 : 0.0f);
+            if (active) store_out(o, c);
+            __syncwarp();
+          }
         } else {
+          float o[128];
+          if (done > 0) {
+            KV_TMEM_LD32(to, o);
+            KV_TMEM_LD32(to + 32, o + 32);
+            KV_TMEM_LD32(to + 64, o + 64);
+            KV_TMEM_LD32(to + 96, o + 96);
+            KV_TMEM_WAIT32(o);
+            KV_TIE32(o + 32);
+            KV_TIE32(o + 64);
+            KV_TIE32(o + 96);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 128; ++i) o[i] = 0.0f;
+            for (int i = 0; i < 128; ++i) o[i] = 0.0f;
+          }
+          if (active && whole) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) o[i] *= inv;
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) store_out(o + c, c);
+          } else if (active && l != 0.0f) {
+            // pc.rows rows, chunk-major: 32 lanes store 512 contiguous bytes
+            float4* dst = p.part_o + part * kChunks + row;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) dst[i * pc.rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+          __syncwarp();
         }
-        if (active && whole) {
-          uint4* dst = reinterpret_cast<uint4*>(p.a.out + orow * kD);
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-        } else if (active && l != 0.0f) {
-          float4* dst = p.part_o + part0 * kChunks + row;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) dst[i * pc.rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        }
-        __syncwarp();
         if (active) {
-          if (!whole) p.part_ml[part0 + row] = make_float2(m * kScale, l);
-          else if (p.a.lse) p.a.lse[orow] = l != 0.0f ? (m * kScale + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          if (!whole) p.part_ml[part + row] = make_float2(m, l);
+          else if (p.a.lse) p.a.lse[orow] = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
         tc_fence_before();
+      }
+      if (join_groups) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.x_empty);
       }
     }
   }
@@ -1146,25 +1216,40 @@ bool may_split(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms) {
   return items < 4 * static_cast<int64_t>(num_sms);
 }
 
-// Key tiles that any item of a window call can have.
-int64_t most_tiles(const KvAttnArgs& a, int64_t n_cap, int gq) {
-  const int64_t tokens = a.bt.cu_q ? std::min<int64_t>(a.bt.T, kItemRows / gq) : 1;
+// Key tiles that any item of `rows` query rows of a window call can have.
+int64_t most_tiles(const KvAttnArgs& a, int64_t n_cap, int gq, int rows) {
+  const int64_t tokens = a.bt.cu_q ? std::min<int64_t>(a.bt.T, rows / gq) : 1;
   const int64_t span = std::min<int64_t>(n_cap, static_cast<int64_t>(a.local) + tokens - 1);   // of the window
   return (span + 2 * kTile - 2) / kTile + (std::min<int64_t>(a.sink, n_cap) + kTile - 1) / kTile;
 }
 
-// Split or whole, where either is possible, by the time each takes for items of
-// `tiles` key tiles (microseconds, fitted to both schedules at 1 to 64
-// sequences of 1 to 2048 new tokens, windows of 256 to 4096 tokens).  Whole items take rounds over the
-// SMs, a split costs the merge, and more for the partial rows of pair items.
-bool split_is_faster(int64_t T, int B, int gq, int Hkv, int64_t tiles, int num_sms) {
-  const bool pair = T * gq > static_cast<int64_t>(kTile) * B;
-  const int64_t seq_rows = static_cast<int64_t>(kItemRows) * B;   // an item's of every sequence
-  const int64_t items = static_cast<int64_t>(Hkv) * B * ((T * gq + seq_rows - 1) / seq_rows);
-  const double per_sm = static_cast<double>(items) / num_sms, rounds = static_cast<double>((items + num_sms - 1) / num_sms);
-  const double whole = pair ? 8.0 + rounds * (1.35 * tiles + 5.0) : 3.7 + rounds * (1.4 * tiles + 4.5);
-  const double split = pair ? 20.0 + per_sm * (1.7 * tiles + 20.0) : 12.0 + per_sm * (1.3 * tiles + 4.0);
-  return split < whole;
+// The schedule of a window call that may be split, by the time each would take
+// (microseconds, fitted to all three at 1 to 64 sequences of 1 to 2048 new
+// tokens and windows of 256 to 16384 tokens).  Whole items take rounds over the
+// SMs: of 256 rows (a tile 1.35 us), or of 128 (0.7 us, 0.8 on all SMs, 1.1 when
+// each of them reads keys of its own); a split takes equal shares and the merge,
+// and more for the partial rows of 256-row items.  32 heads, 8 KV heads, split
+// and whole items of 128 rows: one token, a window of 256 11.5 and 10.5 us, of
+// 4096 14.4 and 32; 8 sequences of 64 tokens 30.2 and 13.4, 53 and 36.7.
+struct Schedule {
+  bool split;
+  int item_rows;
+};
+Schedule window_schedule(const KvAttnArgs& a, int B, int gq, int Hkv, int64_t n_cap, int num_sms) {
+  const int64_t rows = a.bt.T * gq;   // of all sequences, for one KV head
+  auto items_of = [&](int64_t per) { return static_cast<int64_t>(Hkv) * B * ((rows + per * B - 1) / (per * B)); };
+  auto rounds = [&](int64_t items) { return static_cast<double>((items + num_sms - 1) / num_sms); };
+  const double tiles = static_cast<double>(most_tiles(a, n_cap, gq, kItemRows));
+  const int64_t items = items_of(kItemRows), halves = items_of(kTile);
+  const double per_sm = static_cast<double>(items) / num_sms;
+  const double busy = std::min(1.0, static_cast<double>(halves) / num_sms);
+  const double reading = std::min(1.0, static_cast<double>(Hkv) * B / num_sms);
+  const bool pair = rows > static_cast<int64_t>(kTile) * B;
+  const double whole256 = pair ? 8.0 + rounds(items) * (1.35 * tiles + 5.0) : 1e30;
+  const double whole128 = 5.0 + rounds(halves) * ((0.7 + 0.1 * busy + 0.32 * reading * reading) * tiles + 3.3);
+  const double split = pair ? 20.0 + per_sm * (1.7 * tiles + 20.0) : 13.0 + per_sm * (1.2 * tiles + 4.5);
+  if (split < whole256 && split < whole128) return {true, kItemRows};
+  return {false, whole128 < whole256 ? kTile : kItemRows};
 }
 
 struct Layout {
@@ -1214,8 +1299,11 @@ size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, bool prefix, i
 }
 
 cudaError_t configure_kv_attn_kernels(const DeviceInfo&) {
-  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(sizeof(Smem) + 1024));
+  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(sizeof(Smem)));
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kv_attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(sizeof(Smem)));
   if (e != cudaSuccess) return e;
   const int merge = static_cast<int>(merge_smem(kMaxEnt));
   if ((e = cudaFuncSetAttribute(kv_merge_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, merge)) != cudaSuccess)
@@ -1241,8 +1329,10 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const 
   p.gsh = gq == 8 ? 3 : (gq == 4 ? 2 : (gq == 2 ? 1 : 0));
   p.n_cap = s.n_cap;
   const bool prefix = a.n_prefix > 0;
-  p.split = may_split(a.bt.T, s.B, s.Hq, s.Hkv, prefix, dev.num_sms) &&
-            (prefix || split_is_faster(a.bt.T, s.B, gq, s.Hkv, most_tiles(a, s.n_cap, gq), dev.num_sms));
+  Schedule plan = {may_split(a.bt.T, s.B, s.Hq, s.Hkv, prefix, dev.num_sms), kItemRows};
+  if (plan.split && !prefix) plan = window_schedule(a, s.B, gq, s.Hkv, s.n_cap, dev.num_sms);
+  p.split = plan.split;
+  p.item_rows = plan.item_rows;
   p.once = a.bt.T * gq <= static_cast<int64_t>(kItemRows) * s.B;
   p.pre = p.split && prefix;
   const Layout L = layout_of(a.bt.T, s.Hq, s.Hkv, prefix, p.split, dev.num_sms);
@@ -1264,7 +1354,8 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const 
     e = launch_dependent(kv_plan_kernel, dim3(1), dim3(1024), 0, stream, 1, p);
     if (e != cudaSuccess) return e;
   }
-  e = launch_dependent(kv_attn_kernel, dim3(dev.num_sms), dim3(kThreads), sizeof(Smem) + 1024, stream, 1, p, tq, tk, tv);
+  e = launch_dependent(p.split ? kv_attn_kernel<true> : kv_attn_kernel<false>, dim3(dev.num_sms), dim3(kThreads),
+                       sizeof(Smem), stream, 1, p, tq, tk, tv);
   if (e != cudaSuccess || !p.split) return e;
   // Few rows: several thread groups to an element (one 128K sequence 86.3 us,
   // 32 over a 32K prefix 42.7; with one group from 1024 rows on 43.8, with four

@@ -462,6 +462,44 @@ def test_window_not_a_number_stays_visible(n, m):
     assert bool((bad[:, 4:] == hit[:, None]).all()) and not bool(bad[:, :4].any())
 
 
+# Caches long enough that an item's keys are shared between blocks (the shares'
+# borders fall inside items, key tiles of either parity and of the sink).
+LONG = [
+    # Hq, Hkv, q_lens, lens, sink, local
+    (8, 2, [1], [9000], 4, 1 << 30),
+    (8, 2, [1, 1, 1], [9000, 10, 3001], 300, 6000),
+    (4, 1, [70, 1, 3], [9000, 6000, 10], 4, 1 << 30),
+    (16, 2, [100, 40, 0, 1], [8001, 3000, 7, 1], 0, 5000),
+    (8, 4, [130, 64, 65], [4000, 6100, 65], 130, 1 << 30),
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,ql,lens,sink,local", LONG)
+def test_window_shared_between_blocks(Hq, Hkv, ql, lens, sink, local):
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    pages = Pages(lens, Hkv, 128, cdiv(max(lens), 128), seed=81)
+    q = rand((cu[-1], Hq, 128), 82)
+    some = sorted({0, cu[-1] - 1, *(c for c in cu if c < cu[-1]), *(c - 1 for c in cu if c), *range(0, cu[-1], 17)})
+    ref = osv.window_attention(f64(q), *pages.caches(), cu, lens, sink, local, tokens=some)
+    out, lse = window(q, pages, None if ql == [1] * len(ql) else cu, lens, sink, local, Hkv)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    check_rows(out, lse, ref, max(lens), rows=some)
+
+
+@pytest.mark.parametrize("Hq,Hkv,ql,local", [(16, 2, [300] * 6, 90), (8, 8, [1] * 60, 700), (32, 8, [64] * 8, 500)])
+def test_window_items_of_half_the_rows(Hq, Hkv, ql, local):
+    # several items of 128 rows or less to a block, whose two groups join their sums
+    lens = [m + (211 * b) % 1500 for b, m in enumerate(ql)]
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    pages = Pages(lens, Hkv, 64, cdiv(max(lens), 64), seed=83)
+    q = rand((cu[-1], Hq, 128), 84)
+    some = sorted({0, cu[-1] - 1, *cu[:-1], *range(0, cu[-1], 29)})
+    ref = osv.window_attention(f64(q), *pages.caches(), cu, lens, 4, local, tokens=some)
+    out, lse = window(q, pages, None if ql == [1] * len(ql) else cu, lens, 4, local, Hkv)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    check_rows(out, lse, ref, max(lens), rows=some)
+
+
 def test_window_long_positions():
     # 2^23 tokens through a table that repeats a few pages: positions, sink and
     # window far apart
