@@ -404,8 +404,10 @@ QASC_API qasc_status kv_rope_append_paged(const qasc_shape* shape, const qasc_pa
  * out 0 and lse -inf.  Cache rows that none of a sequence's queries attends to
  * may hold anything, NaN and infinities included; V rows that some attend to
  * are taken as finite (a NaN in one may reach its sequence's other queries).  A
- * block-table entry is read only for pages that hold an attended token.  The
- * workspace need not be cleared and is free again once the call has finished
+ * block-table entry is read only for pages that hold an attended token.  How the
+ * work is shared between blocks is chosen from T, B, the heads, local, n_prefix
+ * and n_cap, the bound on the lengths that the host knows (a table with fewer
+ * columns states a lower one).  The workspace need not be cleared and is free again once the call has finished
  * on the stream; calls that can overlap need one each. */
 QASC_API size_t kv_window_attn_workspace_bytes(const qasc_shape* shape, int64_t tokens);
 QASC_API qasc_status kv_window_attn(const qasc_shape* shape, const qasc_batch* batch, int32_t sink, int32_t local,
@@ -417,8 +419,9 @@ QASC_API qasc_status kv_window_attn_paged(const qasc_shape* shape, const qasc_pa
                                           void* workspace, size_t ws_bytes, void* stream);
 
 /* kv_prefix_attn_paged — causal attention of a batch whose sequences share
- * their first n_prefix tokens: the prefix is read once for all of them, and
- * joined with each sequence's own tokens by an exact log-sum-exp merge.
+ * their first n_prefix tokens: the prefix is read once for all of them (a
+ * short one where that is slower by each sequence, from L2), and joined with
+ * each sequence's own tokens by an exact log-sum-exp merge.
  *
  *   A(t) = the whole prefix, and { j <= p } of the sequence's own tokens
  *

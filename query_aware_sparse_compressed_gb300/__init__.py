@@ -613,8 +613,8 @@ def kv_prefix_attn_workspace_bytes(T, B, Hq, Hkv, n_cap):
 def kv_prefix_attn_paged(q, K_pool, V_pool, prefix_table, block_table, kv_lens, out, workspace, *, n_prefix,
                          cu_q=None, lse=None, stream=None):
     """Causal attention of sequences that share their first n_prefix tokens
-    (the pool pages prefix_table [ceil(n_prefix / P)]), read once for all of
-    them; block_table and kv_lens describe each sequence's own tokens behind
+    (the pool pages prefix_table [ceil(n_prefix / P)]), a long one read once for
+    all of them; block_table and kv_lens describe each sequence's own tokens behind
     the prefix."""
     _table(block_table)
     pt = None

@@ -21,7 +21,7 @@
 // 1.35 times the rounding alone); the sum that divides takes the unrounded fp32
 // values, so lse is as exact as fp32.
 //
-// Work.  Two schedules, chosen by the numbers of rows and tiles (window_schedule):
+// Work.  Two schedules, chosen by the numbers of rows and tiles (attn_schedule):
 //   whole  many items, or short ones: CTA c takes items c, c + G, ... whole,
 //          heaviest first (items of 128 rows where those of 256 are few).
 //   split  few items: the tiles of all items are laid end to end and every CTA
@@ -1223,31 +1223,41 @@ int64_t most_tiles(const KvAttnArgs& a, int64_t n_cap, int gq, int rows) {
   return (span + 2 * kTile - 2) / kTile + (std::min<int64_t>(a.sink, n_cap) + kTile - 1) / kTile;
 }
 
-// The schedule of a window call that may be split, by the time each would take
-// (microseconds, fitted to all three at 1 to 64 sequences of 1 to 2048 new
-// tokens and windows of 256 to 16384 tokens).  Whole items take rounds over the
-// SMs: of 256 rows (a tile 1.35 us), or of 128 (0.7 us, 0.8 on all SMs, 1.1 when
-// each of them reads keys of its own); a split takes equal shares and the merge,
-// and more for the partial rows of 256-row items.  32 heads, 8 KV heads, split
-// and whole items of 128 rows: one token, a window of 256 11.5 and 10.5 us, of
-// 4096 14.4 and 32; 8 sequences of 64 tokens 30.2 and 13.4, 53 and 36.7.
+// The schedule of a call that may be split, by the time each would take
+// (microseconds, fitted to all three at 1 to 128 sequences of 1 to 2048 new
+// tokens, windows of 256 to 16384 tokens and prefixes of 128 to 8000).  Whole
+// items take rounds over the SMs: of 256 rows (a tile 1.35 us), or of 128 (0.7
+// us, 0.8 on all SMs, 1.1 when each of them reads keys of its own); they walk
+// the prefix too.  A split takes equal shares and the merge, and more for the
+// partial rows of 256-row items, the prefix's among them.  The host knows only
+// n_cap of the lengths; single tokens' are taken to be 0.7 of it on average,
+// since equal shares gain where they differ.  32 heads, 8 KV heads, split and
+// whole items of 128 rows: one token, a window of 256 11.5 and 10.5 us, of 4096
+// 14.4 and 32; 8 sequences of 64 tokens 30.2 and 13.4, 53 and 36.7; 2048 new
+// tokens behind a prefix of 1000 149 and 69, with 256 rows 56; 32 tokens of 32
+// sequences behind one of 4000 24 and 59.
 struct Schedule {
   bool split;
   int item_rows;
 };
-Schedule window_schedule(const KvAttnArgs& a, int B, int gq, int Hkv, int64_t n_cap, int num_sms) {
+Schedule attn_schedule(const KvAttnArgs& a, int B, int gq, int Hkv, int64_t n_cap, int num_sms) {
   const int64_t rows = a.bt.T * gq;   // of all sequences, for one KV head
   auto items_of = [&](int64_t per) { return static_cast<int64_t>(Hkv) * B * ((rows + per * B - 1) / (per * B)); };
   auto rounds = [&](int64_t items) { return static_cast<double>((items + num_sms - 1) / num_sms); };
+  const double prefix = static_cast<double>((a.n_prefix + kTile - 1) / kTile);
   const double tiles = static_cast<double>(most_tiles(a, n_cap, gq, kItemRows));
+  const double mean = std::min(tiles, 1.0 + 0.7 * static_cast<double>(n_cap) / kTile);
   const int64_t items = items_of(kItemRows), halves = items_of(kTile);
   const double per_sm = static_cast<double>(items) / num_sms;
-  const double busy = std::min(1.0, static_cast<double>(halves) / num_sms);
+  const double pre_per_sm = static_cast<double>((rows + kItemRows - 1) / kItemRows * Hkv) / num_sms;
+  const double busy = 0.7 + 0.1 * std::min(1.0, static_cast<double>(halves) / num_sms);
   const double reading = std::min(1.0, static_cast<double>(Hkv) * B / num_sms);
   const bool pair = rows > static_cast<int64_t>(kTile) * B;
-  const double whole256 = pair ? 8.0 + rounds(items) * (1.35 * tiles + 5.0) : 1e30;
-  const double whole128 = 5.0 + rounds(halves) * ((0.7 + 0.1 * busy + 0.32 * reading * reading) * tiles + 3.3);
-  const double split = pair ? 20.0 + per_sm * (1.7 * tiles + 20.0) : 13.0 + per_sm * (1.2 * tiles + 4.5);
+  const double whole256 = pair ? 8.0 + rounds(items) * (1.35 * (tiles + prefix) + 5.0) : 1e30;
+  const double whole128 =
+      5.0 + rounds(halves) * ((busy + 0.32 * reading * reading) * tiles + busy * prefix + 3.3);
+  const double split = (pair ? 20.0 + per_sm * (1.7 * tiles + 20.0) : 13.0 + per_sm * (1.2 * mean + 4.5)) +
+                       (a.n_prefix ? pre_per_sm * (2.0 * prefix + 20.0) : 0.0);
   if (split < whole256 && split < whole128) return {true, kItemRows};
   return {false, whole128 < whole256 ? kTile : kItemRows};
 }
@@ -1330,11 +1340,11 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const 
   p.n_cap = s.n_cap;
   const bool prefix = a.n_prefix > 0;
   Schedule plan = {may_split(a.bt.T, s.B, s.Hq, s.Hkv, prefix, dev.num_sms), kItemRows};
-  if (plan.split && !prefix) plan = window_schedule(a, s.B, gq, s.Hkv, s.n_cap, dev.num_sms);
+  if (plan.split) plan = attn_schedule(a, s.B, gq, s.Hkv, s.n_cap, dev.num_sms);
   p.split = plan.split;
   p.item_rows = plan.item_rows;
-  p.once = a.bt.T * gq <= static_cast<int64_t>(kItemRows) * s.B;
   p.pre = p.split && prefix;
+  p.once = a.bt.T * gq <= static_cast<int64_t>(kItemRows) * s.B && p.pre == prefix;
   const Layout L = layout_of(a.bt.T, s.Hq, s.Hkv, prefix, p.split, dev.num_sms);
   p.slot_rows = L.slot_rows;
   p.part_o = reinterpret_cast<float4*>(ws + L.off_o);

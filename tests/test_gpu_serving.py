@@ -680,6 +680,20 @@ def test_prefix(Hq, Hkv, P, n0, ql, lens):
     check_rows(out, lse, ref, n0 + max(lens))
 
 
+# long prefixes, whose items blocks share, and short ones, which every item walks
+@pytest.mark.parametrize("Hq,Hkv,P,n0,ql,lens", [
+    (8, 2, 64, 6000, [1] * 5, [1, 300, 0, 130, 64]),
+    (16, 2, 64, 5000, [100, 40, 0, 1], [100, 333, 0, 1]),
+    (64, 8, 64, 4100, [9, 1, 3], [9, 700, 3]),
+    (8, 1, 128, 4000, [40, 60, 0, 5], [40, 1200, 3, 5]),
+    (16, 2, 64, 130, [100, 40, 0, 1], [100, 333, 0, 1]),
+    (8, 2, 64, 200, [300] * 4, [300, 411, 350, 299]),      # a token stands in front of its own cache
+    (32, 8, 64, 65, [1] * 40, [(17 * i) % 200 for i in range(40)]),
+])
+def test_prefix_long_and_short(Hq, Hkv, P, n0, ql, lens):
+    test_prefix(Hq, Hkv, P, n0, ql, lens)
+
+
 def test_prefix_leaves_other_rows_alone():
     Hq, Hkv, P = 8, 2, 64
     both = Pages([100, 20, 30], Hkv, P, 2, seed=33)
