@@ -139,6 +139,7 @@ struct alignas(16) Piece {
 };
 constexpr int kPair = 1;    // two query tiles, one per group; else the groups take alternate key tiles of one
 constexpr int kWhole = 2;   // every tile of the item: the output is written, not a partial
+constexpr int kTurn = 4;    // the first tile of a parity piece is group 1's
 
 struct Smem {
   uint8_t q[2][kTileBytes];
@@ -366,6 +367,14 @@ __device__ __forceinline__ int64_t part_row(const Args& p, const Item& it, int g
   const int64_t row = fam + static_cast<int64_t>(it.s.q0) * p.Hq + static_cast<int64_t>(it.r0) * p.Hkv +
                       static_cast<int64_t>(g) * it.rows;
   return 2 * row + static_cast<int64_t>(cta) * p.slot_rows;
+}
+
+// The group of a parity piece's first tile.  Of a split they go on alternating
+// from piece to piece: while one group writes a short piece's rows the other has
+// the next piece's tile.
+template <bool kSplit>
+__device__ __forceinline__ int first_group(const Piece& pc) {
+  return kSplit && (pc.flags & kTurn) ? 1 : 0;
 }
 
 // The shares of this CTA in order.
@@ -696,8 +705,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       walk.init(p, plan);
       const int half = lane & 1;
       bool more = true;
+      int turn = 0;
       while (more && !dead) {
         more = walk.next(p, plan, pc);
+        pc.flags |= turn;
+        if (kSplit && !(pc.flags & kPair)) turn ^= (pc.n & 1) * kTurn;
         const uint32_t i = pieces % kQueue;
         wait(&S.pc_empty[i], ((pieces / kQueue) & 1u) ^ 1u);
         if (dead) break;
@@ -814,11 +826,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             kslot = knext;
           }
         } else {
-          const uint32_t qb = q_buffer();
+          const uint32_t qb = q_buffer(), turn = __shfl_sync(0xffffffffu, first_group<kSplit>(pc), 0);
           wait(&S.q_full[qb], uses[qb] & 1u);
           ++uses[qb];
           for (int k = -2; k < n && !dead; ++k) {
-            const uint32_t s = k & 1;   // tile k + 2 is of the same group
+            const uint32_t s = (k + turn) & 1;   // tile k + 2 is of the same group
             if (k >= 0) {
               const uint32_t slot = next_tile();
               pv(s, slot, k < 2);
@@ -846,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool lent = false;         // group 1: group 0 may still be reading O_1 and x_ml
     while (take()) {
       const bool pair = pc.flags & kPair;
-      const int n = pc.n;
+      const int n = pc.n, turn = first_group<kSplit>(pc);
       const uint32_t ring0 = ring;
       ring += 2 * n;
       const int row = pair ? kTile * s + r : r;        // of the item
@@ -859,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         lent = false;
       }
       for (int k = 0; k < n && !dead; ++k) {
-        if (!pair && (k & 1) != s) continue;
+        if (!pair && ((k + turn) & 1) != s) continue;
         bool prefix;
         const int t0 = tile_token(pc, pc.k0 + k, &prefix);
         const int last = t0 + kTile - 1;
@@ -878,10 +890,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t at = ring0 + v_place(k, n, pair ? 1 : 2), slot = at % kSlots;
           wait(&S.full[slot], (at / kSlots) & 1u);
           if (dead) return;
-          if (!any_row_sees(p, pc, prefix, t0 + r)) {
-            uint4* v0 = reinterpret_cast<uint4*>(S.kv[slot] + r * 128);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v0[i] = v0[i + kHalf / 16] = make_uint4(0u, 0u, 0u, 0u);
+          // Eight lanes to a row of a half: a store of 512 contiguous bytes (a row
+          // to a lane would meet in the same banks 32 times over).
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const int v_row = (warp & 3) * 32 + 4 * i + (lane >> 3);
+            if (!any_row_sees(p, pc, prefix, t0 + v_row)) {
+              uint4* v0 = reinterpret_cast<uint4*>(S.kv[slot] + v_row * 128) + (lane & 7);
+              v0[0] = v0[kHalf / 16] = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
           fence_async_smem();
         };
