@@ -23,13 +23,15 @@
 //
 // Work.  Two schedules, chosen by the numbers of rows and tiles (attn_schedule):
 //   whole  many items, or short ones: CTA c takes items c, c + G, ... whole,
-//          heaviest first (items of 128 rows where those of 256 are few).
+//          heaviest first (items of 128 rows where those of 256 are few, and
+//          those in twos where there are several to an SM).
 //   split  few items: the tiles of all items are laid end to end and every CTA
 //          takes an equal range of that line; an item that several CTAs share
 //          leaves partial (max, sum, O) rows in the workspace and kv_merge_kernel
 //          joins them.  With a shared prefix its queries are one sequence of
 //          their own (all tokens of the batch, 256 rows to an item), so that
-//          the prefix is read once per 256 rows and not once per sequence.
+//          the prefix is read once per 256 rows and not once per sequence (from
+//          HBM once for all: see tile_of).
 // The line is planned on the device from the lengths, of which the host knows
 // nothing: by a warp of every CTA for itself, or by kv_plan_kernel for a batch
 // whose plan does not fit beside the tiles.
@@ -39,7 +41,9 @@
 //            row r.  An item of more than 128 rows gives each group a query
 //            tile (pair); a smaller one gives the groups alternate key tiles
 //            (parity), each with its own statistics and O, joined by group 0 or
-//            (of a share) by the merge.
+//            (of a share) by the merge; or two such items, of neighbouring KV
+//            heads, get a group each (dual), which hides the start and end of
+//            short items behind each other.
 //   warp 8   K loads, warp 9  V loads (TMA, 64-row boxes: a page holds at least
 //            64 tokens, so a box never leaves its page).  Boxes that no row
 //            attends to are not loaded.  One ring of five tiles, in the order of
@@ -99,10 +103,9 @@ constexpr int kQueue = 4;                     // pieces handed out ahead
 constexpr int kPieceReaders = 11;             // warps that take them: K, V, MMA, softmax
 // Places of an item on the line: kItemCost for what it costs beside its tiles
 // (queries, the first tile's latency, the output), then one per tile, or two
-// of a pair item.  Measured with 128 sequences over a 128K prefix: 1.8 us a
-// tile of two query tiles, 1.0 a tile of one, 2.4 an item (262 us in all; 283
-// with an item at two places, 315 at one).
-constexpr int kItemCost = 3;
+// of a pair item.  Measured at one, two, three places: 128 sequences over a 128K
+// prefix 250, 237, 254 us, over a 4K prefix 42, 43, 47; 8 over 8K 20.1, 19.5, 18.5.
+constexpr int kItemCost = 2;
 constexpr int kChunks = kD / 4;               // 16-byte chunks of a partial row
 // log2(e) / sqrt(128): logits in base-2 units.
 constexpr float kScale = 1.4426950408889634f * 0.08838834764831845f;
@@ -113,6 +116,7 @@ struct Args {
   int B, Hq, Hkv, gsh;      // gsh = log2(Hq / Hkv)
   int64_t n_cap;
   int item_rows;            // query rows of an item: 256, or 128 (whole only)
+  int dual;                 // whole items (of 128 rows) in twos: a unit is two neighbouring KV heads
   int once;                 // keys are read by one item, or two
   int split, pre;           // pre: the shared prefix is sequence 0 of the plan (split only)
   int slot_rows;            // partial rows a CTA may add to an item (split)
@@ -140,6 +144,7 @@ struct alignas(16) Piece {
 constexpr int kPair = 1;    // two query tiles, one per group; else the groups take alternate key tiles of one
 constexpr int kWhole = 2;   // every tile of the item: the output is written, not a partial
 constexpr int kTurn = 4;    // the first tile of a parity piece is group 1's
+constexpr int kDual = 8;    // the items of KV heads g and g + 1, one per group: their tiles alternate in the ring
 
 struct Smem {
   uint8_t q[2][kTileBytes];
@@ -235,6 +240,20 @@ __device__ __forceinline__ Item make_item(const Args& p, const Seq& s, int qt) {
     it.cnt += it.ns + it.hi / kTile - it.w0 + 1;
   }
   return it;
+}
+
+// The i-th key tile of a piece of n.  A share of the prefix begins at its tile
+// w0 and goes around: a tile comes up at the same time in every share that holds
+// it, those of the prefix's other items, so that it is read from HBM once (128
+// sequences of 4 rows a KV head over a 128K prefix: 237 us, 255 without; 256 of
+// them 383 and 422).
+template <bool kSplit>
+__device__ __forceinline__ int tile_of(const Piece& pc, int i, int n) {
+  if (kSplit && pc.b < 0) {
+    i += pc.w0;
+    if (i >= n) i -= n;
+  }
+  return pc.k0 + i;
 }
 
 // Key tile k of an item: first token, and whether it is of the prefix.
@@ -337,7 +356,7 @@ __device__ __forceinline__ int make_plan(const Args& p, int32_t* ent_base, int32
       if (v < 0 || v > p.n_cap) record_error(p.err, kErrBadPage);
     }
   if (!p.split) {
-    plan_scan<kBlock>(line, NS, [&](int s) { return q_tiles(p, seq_of(p, s)) * p.Hkv; });
+    plan_scan<kBlock>(line, NS, [&](int s) { return q_tiles(p, seq_of(p, s)) * (p.Hkv >> p.dual); });
     if (kBlock)
       for (int s = first; s <= NS; s += step) p.line[s] = line[s];
     return NS;
@@ -374,7 +393,7 @@ __device__ __forceinline__ int64_t part_row(const Args& p, const Item& it, int g
 // the next piece's tile.
 template <bool kSplit>
 __device__ __forceinline__ int first_group(const Piece& pc) {
-  return kSplit && (pc.flags & kTurn) ? 1 : 0;
+  return kSplit && (pc.flags & (kTurn | kDual)) == kTurn ? 1 : 0;
 }
 
 // The shares of this CTA in order.
@@ -424,6 +443,10 @@ struct Walk {
       const bool all = off <= first_place(span) && off + take > last_place(span, w);
       pc.flags = (pair ? kPair : 0) | (pair && !p.pre && all ? kWhole : 0);
       pc.part = part_row(p, it, g, blockIdx.x);
+      if (!pair && all && it.cnt > 0 && g + 1 < p.Hkv && end - pos >= span) {   // the next head's item as well
+        pc.flags |= kDual;
+        pos += span;
+      }
     } else {
       const int U = n > 0 ? S.line[n] : 0;
       int u;
@@ -436,11 +459,12 @@ struct Walk {
       } while (u >= U);
       const int x = U - 1 - u;   // late query tiles attend to the most keys
       const int sq = find_last(S.line, n, x), rem = x - S.line[sq];
-      it = make_item(p, seq_of(p, sq), rem / p.Hkv);
-      g = rem % p.Hkv;
+      const int heads = p.Hkv >> p.dual;
+      it = make_item(p, seq_of(p, sq), rem / heads);
+      g = (rem % heads) << p.dual;
       pc.k0 = 0;
       pc.n = it.cnt;
-      pc.flags = (it.rows > kTile ? kPair : 0) | kWhole;
+      pc.flags = (it.rows > kTile ? kPair : 0) | kWhole | p.dual * kDual;
       pc.part = 0;
     }
     pc.tok0 = it.s.q0 + (it.r0 >> p.gsh);
@@ -454,6 +478,14 @@ struct Walk {
     pc.np = it.np;
     pc.ns = it.ns;
     pc.w0 = it.w0;
+    if (kSplit && it.s.b < 0) {
+      // the first tile in the share of which a CTA's places on an item's span begin a multiple of a share's length
+      const Ranges line(S.line[n], gridDim.x);
+      const int w = tile_weight(it.rows);
+      const unsigned m = static_cast<unsigned>((static_cast<uint64_t>(pc.k0) * w * line.G + line.U - 1) / line.U);
+      const int first = (line.start(m) + w - 1) / w - pc.k0;
+      pc.w0 = first > 0 && first < pc.n ? first : 0;
+    }
     return true;
   }
 };
@@ -559,13 +591,21 @@ __device__ __forceinline__ bool elect_one() {
 // Bits [0, n) of a word, n any integer.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
-// kSplit: the schedule.  Two kernels, since the code of one schedule costs the
-// other: with the join of whole parity items in the split's kernel 128 sequences
-// over a 128K prefix take 297 us, without it 262.
-template <bool kSplit>
+// Three kernels, since the code of one schedule costs the others: with the join
+// of whole parity items in the split's kernel 128 sequences over a 128K prefix
+// took 297 us, without it 262; 608 sequences of one 36-token item a KV head take
+// 97 us in a kernel of twos alone, 108 in one that also holds whole pair items.
+enum Mode { kModeSplit, kModeWhole, kModeTwos };
+
+template <Mode kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_attn_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v) {
+  constexpr bool kSplit = kMode == kModeSplit;
+  auto is_pair = [](const Piece& pc) { return kMode != kModeTwos && (pc.flags & kPair) != 0; };
+  auto is_dual = [](const Piece& pc) {   // 0, 1
+    return kMode == kModeTwos || (kMode == kModeSplit && (pc.flags & kDual)) ? 1 : 0;
+  };
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& S = *reinterpret_cast<Smem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -644,17 +684,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t once = policy_evict_first();
       uint32_t mine[4] = {0, 0, 0, 0};   // places + 1 of this warp's newest loads
       while (take()) {
-        const int n = pc.n, ahead = (pc.flags & kPair) ? 1 : 2;
+        const int dual = is_dual(pc), n = pc.n << dual, ahead = is_pair(pc) ? 1 : 2;
         int64_t row = -1;   // of lane's box of 16 tiles from tile i on; -1: no row attends to the box
         for (int i = 0; i < n; ++i) {
           if ((i & 15) == 0) {
-            const int k = pc.k0 + i + (lane >> 1);
+            const int j = i + (lane >> 1), k = tile_of<kSplit>(pc, j >> dual, pc.n);
             row = -1;
-            if (k < pc.k0 + n) {
+            if (j < n) {
               bool prefix;
               const int tok = tile_token(pc, k, &prefix) + (lane & 1) * kBox;
               if (any_row_sees_box(p, pc, prefix, tok)) {
-                row = cache_row(prefix ? p.a.pm_prefix : p.a.pm, prefix ? 0 : pc.b, pc.g, p.Hkv, p.n_cap, tok);
+                row = cache_row(prefix ? p.a.pm_prefix : p.a.pm, prefix ? 0 : pc.b, pc.g + (j & dual), p.Hkv, p.n_cap, tok);
                 if (row < 0) {
                   record_error(p.err, kErrBadPage);
                   row = 0;
@@ -709,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (more && !dead) {
         more = walk.next(p, plan, pc);
         pc.flags |= turn;
-        if (kSplit && !(pc.flags & kPair)) turn ^= (pc.n & 1) * kTurn;
+        if (kSplit && !is_pair(pc) && !is_dual(pc)) turn ^= (pc.n & 1) * kTurn;
         const uint32_t i = pieces % kQueue;
         wait(&S.pc_empty[i], ((pieces / kQueue) & 1u) ^ 1u);
         if (dead) break;
@@ -720,8 +760,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++pieces;
         if (!more || pc.n == 0) continue;
-        const bool pair = pc.flags & kPair;
-        const uint32_t b0 = pair ? 0 : q_buffer(), nb = pair ? 2 : 1;
+        const int next_head = is_dual(pc), next_row = is_pair(pc) ? kTile : 0;
+        const bool both = next_head || next_row;
+        const uint32_t b0 = both ? 0 : q_buffer(), nb = both ? 2 : 1;
         for (uint32_t t = 0; t < nb; ++t) {
           const uint32_t b = b0 + t;
           wait(&S.q_empty[b], (uses[b] & 1u) ^ 1u);
@@ -729,8 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_expect_tx(&S.q_full[b], kTileBytes);
           __syncwarp();
           if (lane < 2)
-            tma_load_3d(S.q[b] + half * kHalf, &tm_q, half * 64, pc.g << p.gsh,
-                        pc.tok0 + static_cast<int>((t * kTile) >> p.gsh), &S.q_full[b]);
+            tma_load_3d(S.q[b] + half * kHalf, &tm_q, half * 64, (pc.g + static_cast<int>(t) * next_head) << p.gsh,
+                        pc.tok0 + ((static_cast<int>(t) * next_row) >> p.gsh), &S.q_full[b]);
           ++uses[b];
         }
       }
@@ -792,9 +833,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         np ^= 1u << s;
       };
       while (take()) {
-        const int n = __shfl_sync(0xffffffffu, pc.n, 0);
+        const int dual = __shfl_sync(0xffffffffu, is_dual(pc), 0);
+        const int n = __shfl_sync(0xffffffffu, pc.n, 0) << dual;
         if (n == 0) continue;
-        if (pc.flags & kPair) {
+        if (is_pair(pc)) {
           // Tile k's S is issued behind tile k - 1's O of the same group.  The
           // waits for the next tiles' V and K (some 200 cycles each, even when
           // the data is there) stand around group 1's O, where the tensor cores
@@ -826,9 +868,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             kslot = knext;
           }
         } else {
-          const uint32_t qb = q_buffer(), turn = __shfl_sync(0xffffffffu, first_group<kSplit>(pc), 0);
+          const uint32_t qb = dual ? 0 : q_buffer(), turn = __shfl_sync(0xffffffffu, first_group<kSplit>(pc), 0);
           wait(&S.q_full[qb], uses[qb] & 1u);
           ++uses[qb];
+          if (dual) {
+            wait(&S.q_full[1], uses[1] & 1u);
+            ++uses[1];
+          }
           for (int k = -2; k < n && !dead; ++k) {
             const uint32_t s = (k + turn) & 1;   // tile k + 2 is of the same group
             if (k >= 0) {
@@ -839,9 +885,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (k + 2 < n) {
               const uint32_t slot = next_tile();
-              qk(s, qb, slot);
+              const uint32_t qs = dual ? s : qb;
+              qk(s, qs, slot);
               commit(&S.empty[slot]);
-              if (k + 2 == n - 1) commit(&S.q_empty[qb]);
+              if (k + 2 >= n - 1 - dual) commit(&S.q_empty[qs]);   // its last use
             }
           }
         }
@@ -857,8 +904,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t nx = 0;           // items joined
     bool lent = false;         // group 1: group 0 may still be reading O_1 and x_ml
     while (take()) {
-      const bool pair = pc.flags & kPair;
-      const int n = pc.n, turn = first_group<kSplit>(pc);
+      const bool pair = is_pair(pc);
+      const int dual = is_dual(pc), n = pc.n << dual, turn = first_group<kSplit>(pc);
       const uint32_t ring0 = ring;
       ring += 2 * n;
       const int row = pair ? kTile * s + r : r;        // of the item
@@ -873,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < n && !dead; ++k) {
         if (!pair && ((k + turn) & 1) != s) continue;
         bool prefix;
-        const int t0 = tile_token(pc, pc.k0 + k, &prefix);
+        const int t0 = tile_token(pc, tile_of<kSplit>(pc, k >> dual, pc.n), &prefix);
         const int last = t0 + kTile - 1;
         const bool clean = prefix ? last >= p.a.n_prefix : !(last <= pc.hi && (t0 >= pc.lo || last < p.a.sink));
         const bool all = prefix ? last < p.a.n_prefix
@@ -998,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // groups' (every thread has the same row in both) and writes the output;
       // of a share each group leaves its own, since the groups would wait for
       // each other (128 sequences over a 4K prefix: 56 us joined, 49 so).
-      const bool whole = !kSplit || (pc.flags & kWhole), join_groups = !kSplit && !pair;
+      const bool whole = !kSplit || (pc.flags & kWhole), join_groups = kMode == kModeWhole && !pair;
       float a0 = 1.0f, a1 = 0.0f;
       m *= kScale;
       if (join_groups) {
@@ -1024,9 +1071,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (warp_rows) {
         const bool active = row < pc.rows;                // the row exists
-        const int64_t part = pc.part + (pair ? 0 : s * pc.rows);
+        const int64_t part = pc.part + (pair ? 0 : (s << dual) * pc.rows);
+        const int g = pc.g + (s & dual);
         const int64_t orow =
-            (static_cast<int64_t>(pc.tok0) + (row >> p.gsh)) * p.Hq + (pc.g << p.gsh) + (row & ((1 << p.gsh) - 1));
+            (static_cast<int64_t>(pc.tok0) + (row >> p.gsh)) * p.Hq + (g << p.gsh) + (row & ((1 << p.gsh) - 1));
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
         auto store_out = [&](const float* o, int c) {   // 32 columns from c on
           uint4* dst = reinterpret_cast<uint4*>(p.a.out + orow * kD + c);
@@ -1078,8 +1126,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         if (active) {
-          if (!whole) p.part_ml[part + row] = make_float2(m, l);
-          else if (p.a.lse) p.a.lse[orow] = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          if (!whole) {
+            p.part_ml[part + row] = make_float2(m, l);
+            if (dual) p.part_ml[part + pc.rows + row] = make_float2(-INFINITY, 0.0f);   // the other group's, of this head
+          }
+          if (whole && p.a.lse) p.a.lse[orow] = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
         tc_fence_before();
       }
@@ -1240,12 +1291,13 @@ int64_t most_tiles(const KvAttnArgs& a, int64_t n_cap, int gq, int rows) {
   return (span + 2 * kTile - 2) / kTile + (std::min<int64_t>(a.sink, n_cap) + kTile - 1) / kTile;
 }
 
-// The schedule of a call that may be split, by the time each would take
+// The schedule of a call, `may` it be split, by the time each would take
 // (microseconds, fitted to all three at 1 to 128 sequences of 1 to 2048 new
 // tokens, windows of 256 to 16384 tokens and prefixes of 128 to 8000).  Whole
-// items take rounds over the SMs: of 256 rows (a tile 1.35 us), or of 128 (0.7
-// us, 0.8 on all SMs, 1.1 when each of them reads keys of its own); they walk
-// the prefix too.  A split takes equal shares and the merge, and more for the
+// items take rounds over the SMs: of 256 rows (a tile 1.32 us), or of 128 (0.7
+// us, 0.8 on all SMs, 1.1 when each of them reads keys of its own) one by one or
+// in twos, which saves a start (152 sequences, 8 KV heads: a window of 32 tokens
+// 29.3 us in twos, 41.9 joined, of 500 62 and 67); they walk the prefix too.  A split takes equal shares and the merge, and more for the
 // partial rows of 256-row items, the prefix's among them.  The host knows only
 // n_cap of the lengths; single tokens' are taken to be 0.7 of it on average,
 // since equal shares gain where they differ.  32 heads, 8 KV heads, split and
@@ -1256,8 +1308,9 @@ int64_t most_tiles(const KvAttnArgs& a, int64_t n_cap, int gq, int rows) {
 struct Schedule {
   bool split;
   int item_rows;
+  int dual;
 };
-Schedule attn_schedule(const KvAttnArgs& a, int B, int gq, int Hkv, int64_t n_cap, int num_sms) {
+Schedule attn_schedule(const KvAttnArgs& a, int B, int gq, int Hkv, int64_t n_cap, int num_sms, bool may) {
   const int64_t rows = a.bt.T * gq;   // of all sequences, for one KV head
   auto items_of = [&](int64_t per) { return static_cast<int64_t>(Hkv) * B * ((rows + per * B - 1) / (per * B)); };
   auto rounds = [&](int64_t items) { return static_cast<double>((items + num_sms - 1) / num_sms); };
@@ -1270,13 +1323,17 @@ Schedule attn_schedule(const KvAttnArgs& a, int B, int gq, int Hkv, int64_t n_ca
   const double busy = 0.7 + 0.1 * std::min(1.0, static_cast<double>(halves) / num_sms);
   const double reading = std::min(1.0, static_cast<double>(Hkv) * B / num_sms);
   const bool pair = rows > static_cast<int64_t>(kTile) * B;
-  const double whole256 = pair ? 8.0 + rounds(items) * (1.35 * (tiles + prefix) + 5.0) : 1e30;
-  const double whole128 =
-      5.0 + rounds(halves) * ((busy + 0.32 * reading * reading) * tiles + busy * prefix + 3.3);
-  const double split = (pair ? 20.0 + per_sm * (1.7 * tiles + 20.0) : 13.0 + per_sm * (1.2 * mean + 4.5)) +
-                       (a.n_prefix ? pre_per_sm * (2.0 * prefix + 20.0) : 0.0);
-  if (split < whole256 && split < whole128) return {true, kItemRows};
-  return {false, whole128 < whole256 ? kTile : kItemRows};
+  const double full = std::min(1.0, static_cast<double>(rows) / (static_cast<double>(kTile) * B));   // of an item's rows
+  const double whole256 = pair ? 7.0 + rounds(items) * (1.32 * (tiles + prefix) + 4.8) : 1e30;
+  const double walk = (busy + 0.32 * reading * reading) * tiles + busy * prefix;   // of an item's tiles
+  const double joined = rounds(halves) * (walk + 3.3);
+  const double dual = Hkv % 2 ? 1e30 : rounds((halves + 1) / 2) * (2.0 * walk + 3.3 + 2.0 * full);
+  const double whole128 = 5.0 + std::min(joined, dual);
+  const double split = (may ? 0.0 : 1e30) + (a.n_prefix ? pre_per_sm * (2.0 * prefix + 20.0) : 0.0) +
+                       (pair ? 20.0 + per_sm * (1.7 * tiles + 20.0) : 13.0 + per_sm * (1.2 * mean + 4.5));
+  if (split < whole256 && split < whole128) return {true, kItemRows, 0};
+  if (whole256 <= whole128) return {false, kItemRows, 0};
+  return {false, kTile, dual < joined ? 1 : 0};
 }
 
 struct Layout {
@@ -1326,10 +1383,13 @@ size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, bool prefix, i
 }
 
 cudaError_t configure_kv_attn_kernels(const DeviceInfo&) {
-  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<kModeSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(sizeof(Smem)));
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kv_attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(kv_attn_kernel<kModeWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(sizeof(Smem)));
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kv_attn_kernel<kModeTwos>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(sizeof(Smem)));
   if (e != cudaSuccess) return e;
   const int merge = static_cast<int>(merge_smem(kMaxEnt));
@@ -1356,10 +1416,11 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const 
   p.gsh = gq == 8 ? 3 : (gq == 4 ? 2 : (gq == 2 ? 1 : 0));
   p.n_cap = s.n_cap;
   const bool prefix = a.n_prefix > 0;
-  Schedule plan = {may_split(a.bt.T, s.B, s.Hq, s.Hkv, prefix, dev.num_sms), kItemRows};
-  if (plan.split) plan = attn_schedule(a, s.B, gq, s.Hkv, s.n_cap, dev.num_sms);
+  const Schedule plan = attn_schedule(a, s.B, gq, s.Hkv, s.n_cap, dev.num_sms,
+                                      may_split(a.bt.T, s.B, s.Hq, s.Hkv, prefix, dev.num_sms));
   p.split = plan.split;
   p.item_rows = plan.item_rows;
+  p.dual = plan.dual;
   p.pre = p.split && prefix;
   p.once = a.bt.T * gq <= static_cast<int64_t>(kItemRows) * s.B && p.pre == prefix;
   const Layout L = layout_of(a.bt.T, s.Hq, s.Hkv, prefix, p.split, dev.num_sms);
@@ -1381,8 +1442,8 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const 
     e = launch_dependent(kv_plan_kernel, dim3(1), dim3(1024), 0, stream, 1, p);
     if (e != cudaSuccess) return e;
   }
-  e = launch_dependent(p.split ? kv_attn_kernel<true> : kv_attn_kernel<false>, dim3(dev.num_sms), dim3(kThreads),
-                       sizeof(Smem), stream, 1, p, tq, tk, tv);
+  const auto attn = p.split ? kv_attn_kernel<kModeSplit> : (p.dual ? kv_attn_kernel<kModeTwos> : kv_attn_kernel<kModeWhole>);
+  e = launch_dependent(attn, dim3(dev.num_sms), dim3(kThreads), sizeof(Smem), stream, 1, p, tq, tk, tv);
   if (e != cudaSuccess || !p.split) return e;
   // Few rows: several thread groups to an element (one 128K sequence 86.3 us,
   // 32 over a 32K prefix 42.7; with one group from 1024 rows on 43.8, with four

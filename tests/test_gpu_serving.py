@@ -694,6 +694,41 @@ def test_prefix_long_and_short(Hq, Hkv, P, n0, ql, lens):
     test_prefix(Hq, Hkv, P, n0, ql, lens)
 
 
+# several items of the prefix to a KV head (their shares go around), KV heads in twos and an odd one
+@pytest.mark.parametrize("B,Hq,Hkv,n0", [(70, 32, 4, 9000), (90, 24, 3, 5000), (64, 24, 3, 100)])
+def test_prefix_of_several_items(B, Hq, Hkv, n0):
+    P = 64
+    lens = [(29 * b) % 260 for b in range(B)]
+    both = Pages([n0] + lens, Hkv, P, max(5, cdiv(n0, P)), seed=85)
+    q = rand((B, Hq, 128), 86)
+    some = sorted({0, 1, 9, 10, B - 1, *range(2, B, 7)})
+    Kc, Vc = both.caches()
+    ref = osv.prefix_attention(f64(q), Kc[0], Vc[0], Kc[1:], Vc[1:], list(range(B + 1)), lens, tokens=some)
+    K, V, table = both.cuda()
+    own = table[1:, :5].contiguous()                     # 5 pages hold 260 tokens
+    out = torch.full((B, Hq, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, Hq), float("nan"), dtype=torch.float32, device="cuda")
+    ws = qasc.alloc_workspace(qasc.kv_prefix_attn_workspace_bytes(B, B, Hq, Hkv, 5 * P))
+    ws.fill_(255)
+    qasc.kv_prefix_attn_paged(q.cuda(), K, V, table[0, :cdiv(n0, P)].contiguous(), own, batch_tensors(None, lens)[1], out,
+                              ws, n_prefix=n0, lse=lse)
+    qasc.qasc_device_error()
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    check_rows(out, lse, ref, n0 + 260, rows=some)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (24, 3), (16, 16)])
+def test_window_of_short_and_empty_sequences(Hq, Hkv):
+    # many short items, some without any token (the query stands in front of an empty cache)
+    B = 240 // Hkv + 60
+    lens = [(13 * b) % 170 for b in range(B)]
+    pages = Pages(lens, Hkv, 64, 3, seed=87)
+    q = rand((B, Hq, 128), 88)
+    ref = osv.window_attention(f64(q), *pages.caches(), list(range(B + 1)), lens, 4, 100)
+    out, lse = window(q, pages, None, lens, 4, 100, Hkv)
+    check_rows(out, lse, ref, 170)
+
+
 def test_prefix_leaves_other_rows_alone():
     Hq, Hkv, P = 8, 2, 64
     both = Pages([100, 20, 30], Hkv, P, 2, seed=33)
