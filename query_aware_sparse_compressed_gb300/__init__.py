@@ -429,6 +429,8 @@ def ts_dense_attn(q, K, V, out, workspace, *, n, lse=None, stream=None):
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _Tensor = torch.Tensor
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+# of a process that holds a CUDA tensor, so that CUDA is up (0.06 us; torch.cuda.current_device 0.3)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def _at(t, name, dtype, shape, dev):
@@ -448,7 +450,7 @@ def _on_device(dev, name):
     """Raise unless dev is the current CUDA device, where the library launches."""
     if dev < 0:
         raise ValueError("%s must be a CUDA tensor" % name)
-    current = torch.cuda.current_device()
+    current = _current_device()
     if dev != current:
         raise ValueError("%s is on cuda:%d but the current device is cuda:%d" % (name, dev, current))
 
@@ -473,8 +475,8 @@ def _batch(cu_q, lens, T, dev):
     """The packed batch and B; cu_q [B + 1] (None: one token per sequence)."""
     if not isinstance(lens, _Tensor) or lens.dim() != 1:
         raise ValueError("kv_lens must be a [B] tensor")
-    B = len(lens)
-    return _lib.qasc_batch(None if cu_q is None else _at(cu_q, "cu_q", _I32, (B + 1,), dev),
+    B = lens.shape[0]
+    return _lib.pack_batch(0 if cu_q is None else _at(cu_q, "cu_q", _I32, (B + 1,), dev),
                            _at(lens, "kv_lens", _I32, (B,), dev), T), B
 
 
@@ -494,7 +496,7 @@ def _cache(K, V, block_table, B, Hkv, dev):
         if len(table) != 2 or table[0] != B:
             _dims(block_table, "block_table", (B, None))
         n_cap = table[1] * shape[2]
-        cache = _lib.qasc_paged_cache(_at(block_table, "block_table", _I32, table, dev), shape[2], table[1], shape[0])
+        cache = _lib.pack_cache(_at(block_table, "block_table", _I32, table, dev), shape[2], table[1], shape[0])
     return cache, n_cap, shape[1], _at(K, "K", _BF16, shape, dev), _at(V, "V", _BF16, shape, dev)
 
 
@@ -504,16 +506,16 @@ def _table(block_table):
 
 
 def _run(fn, dev, stream, shape, cache, *args):
-    """One call of the library: shape and cache descriptors, then args and the stream."""
+    """One call of the library: shape and cache descriptors (packed), then args and the stream."""
     _on_device(dev, "the call's first tensor")
     if stream is None:
         s = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
     else:
         s = _stream(stream)
     if cache is None:
-        status = fn(ctypes.byref(shape), *args, s)
+        status = fn(shape, *args, s)
     else:
-        status = fn(ctypes.byref(shape), ctypes.byref(cache), *args, s)
+        status = fn(shape, cache, *args, s)
     if status != _lib.QASC_OK:
         _check(status)
 
@@ -536,14 +538,14 @@ def _rope_append(name, q, k, v, q_out, K, V, block_table, kv_lens, inv_freq, cu_
         op = _at(q_out, "q_out", _BF16, (T, Hq, D), dev)
     kp, ks = _heads(k, "k", T, Hkv, dev)
     vp, vs = _heads(v, "v", T, Hkv, dev)
-    rot, fp = 0, None
+    rot, fp = 0, 0
     if inv_freq is not None:
         _dims(inv_freq, "inv_freq", (None,))
         rot, fp = 2 * inv_freq.shape[0], _at(inv_freq, "inv_freq", _F32, inv_freq.shape, dev)
-    pp = None if positions is None else _at(positions, "positions", _I32, (T,), dev)
-    rope = _lib.qasc_rope(fp, pp, rot, 1 if interleaved else 0)
-    _run(getattr(_L(), name), dev, stream, _lib.qasc_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap), cache,
-         ctypes.byref(batch), ctypes.byref(rope), qp, qs, kp, ks, vp, vs, op, Kp, Vp)
+    pp = 0 if positions is None else _at(positions, "positions", _I32, (T,), dev)
+    rope = _lib.pack_rope(fp, pp, rot, 1 if interleaved else 0)
+    _run(getattr(_L(), name), dev, stream, _lib.pack_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap), cache, batch, rope,
+         qp, qs, kp, ks, vp, vs, op, Kp, Vp)
 
 
 def kv_rope_append(q, k, v, q_out, K, V, kv_lens, inv_freq, *, cu_q=None, positions=None, interleaved=False,
@@ -582,8 +584,8 @@ def _attn(name, q, K, V, block_table, kv_lens, out, workspace, cu_q, lse, stream
     lp = None if lse is None else _at(lse, "lse", _F32, (T, Hq), dev)
     ws_bytes = workspace.numel()
     wp = _at(workspace, "workspace", _U8, (ws_bytes,), dev)
-    _run(getattr(_L(), name), dev, stream, _lib.qasc_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap), cache, *front,
-         ctypes.byref(batch), *behind, qp, Kp, Vp, op, lp, wp, ws_bytes)
+    _run(getattr(_L(), name), dev, stream, _lib.pack_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap), cache, *front,
+         batch, *behind, qp, Kp, Vp, op, lp, wp, ws_bytes)
 
 
 def kv_window_attn_workspace_bytes(T, B, Hq, Hkv, n_cap):

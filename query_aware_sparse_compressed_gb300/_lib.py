@@ -2,6 +2,7 @@
 
 import ctypes
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqasc.so")
 
@@ -45,14 +46,19 @@ class qasc_rope(ctypes.Structure):
                 ("interleaved", ctypes.c_int32)]
 
 
+# The descriptors of the packed-batch calls as bytes, which a void pointer
+# argument takes (0.1 us each; a ctypes structure and its byref 0.5).
+pack_shape = struct.Struct("@6i2q").pack
+pack_cache = struct.Struct("@P2iq").pack
+pack_batch = struct.Struct("@2Pq").pack
+pack_rope = struct.Struct("@2P2i").pack
+
 _P = ctypes.c_void_p
 _SP = ctypes.POINTER(qasc_shape)
 _TP = ctypes.POINTER(qasc_ts_params)
 _NP = ctypes.POINTER(qasc_snap_params)
 _PC = ctypes.POINTER(qasc_paged_cache)
 _RG = ctypes.POINTER(qasc_local_ring)
-_BT = ctypes.POINTER(qasc_batch)
-_RP = ctypes.POINTER(qasc_rope)
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 
@@ -79,13 +85,13 @@ SIGNATURES = {
     "ts_sparse_attn_paged": (ctypes.c_int, [_SP, _TP, _PC, _RG, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P,
                                             ctypes.c_size_t, _P]),
     "ts_ring_flush": (ctypes.c_int, [_SP, _PC, _RG, _P, _P, _P, _P, ctypes.c_int64, ctypes.c_int64, _P]),
-    "kv_rope_append": (ctypes.c_int, [_SP, _BT, _RP, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P]),
-    "kv_rope_append_paged": (ctypes.c_int, [_SP, _PC, _BT, _RP, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P]),
+    "kv_rope_append": (ctypes.c_int, [_P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P]),
+    "kv_rope_append_paged": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P]),
     "kv_window_attn_workspace_bytes": (ctypes.c_size_t, [_SP, _I64]),
-    "kv_window_attn": (ctypes.c_int, [_SP, _BT, _I32, _I32, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
-    "kv_window_attn_paged": (ctypes.c_int, [_SP, _PC, _BT, _I32, _I32, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv_window_attn": (ctypes.c_int, [_P, _P, _I32, _I32, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv_window_attn_paged": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "kv_prefix_attn_workspace_bytes": (ctypes.c_size_t, [_SP, _I64]),
-    "kv_prefix_attn_paged": (ctypes.c_int, [_SP, _PC, _P, _I64, _BT, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv_prefix_attn_paged": (ctypes.c_int, [_P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "ts_dense_attn_workspace_bytes": (ctypes.c_size_t, [_SP]),
     "ts_dense_attn": (ctypes.c_int, [_SP, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "snapkv_workspace_bytes": (ctypes.c_size_t, [_SP, _NP]),

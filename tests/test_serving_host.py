@@ -239,3 +239,11 @@ def test_tensors_on_the_host_are_rejected(monkeypatch):
         qasc._at(t(4, 8, 128), "out", bf, (4, 8, 128), 0)
     with pytest.raises(TypeError, match="must be a torch.Tensor"):
         qasc._at([1, 2], "out", bf, (2,), 0)
+
+
+def test_packed_descriptors_equal_the_structures():
+    big = 1 << 40
+    assert _lib.pack_shape(3, 8, 2, 128, 32, 0, big, big + 1) == bytes(_lib.qasc_shape(3, 8, 2, 128, 32, 0, big, big + 1))
+    assert _lib.pack_cache(big, 64, 8, big) == bytes(_lib.qasc_paged_cache(big, 64, 8, big))
+    assert _lib.pack_batch(0, big, 10) == bytes(_lib.qasc_batch(None, big, 10))
+    assert _lib.pack_rope(big, 0, 128, 1) == bytes(_lib.qasc_rope(big, None, 128, 1))
