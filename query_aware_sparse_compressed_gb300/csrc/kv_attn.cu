@@ -75,6 +75,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -136,7 +137,7 @@ struct alignas(16) Piece {
   int g, b;           // KV head, sequence (< 0: the shared prefix)
   int p0, p1;         // positions of the first and last row
   int lo, hi;         // own tokens attended by some row: [0, min(sink, hi + 1)) and [lo, hi]
-  int np, ns, w0;     // tiles of the prefix, of the sink in front of the window, first of the window
+  int np, ns, w0;     // tiles of the prefix; boxes of the sink in front of the window, first box of the window
   int k0, n;          // n < 0: no more pieces
   int flags;
   int64_t part;       // first partial row
@@ -235,9 +236,12 @@ __device__ __forceinline__ Item make_item(const Args& p, const Seq& s, int qt) {
     const int64_t lo = static_cast<int64_t>(it.p0) - p.a.local + 1;
     it.lo = static_cast<int>(lo > 0 ? lo : 0);
     it.hi = it.p1;
-    it.w0 = it.lo / kTile;
-    it.ns = min(ceil_tiles(min(static_cast<int64_t>(p.a.sink), static_cast<int64_t>(it.hi) + 1)), it.w0);
-    it.cnt += it.ns + it.hi / kTile - it.w0 + 1;
+    it.w0 = it.lo / kBox;
+    it.ns = min(min(p.a.sink, it.hi + 1) / kBox + (min(p.a.sink, it.hi + 1) % kBox > 0), it.w0);
+    // With an odd number of boxes an empty one stands behind the sink's, not at
+    // the end: the window's tiles are then likely to be attended to in full.
+    if (it.ns < it.w0 && it.ns > 0 && ((it.ns + it.hi / kBox - it.w0 + 1) & 1)) --it.w0;
+    it.cnt += (it.ns + it.hi / kBox - it.w0 + 2) / 2;
   }
   return it;
 }
@@ -256,11 +260,14 @@ __device__ __forceinline__ int tile_of(const Piece& pc, int i, int n) {
   return pc.k0 + i;
 }
 
-// Key tile k of an item: first token, and whether it is of the prefix.
-__device__ __forceinline__ int tile_token(const Piece& pc, int k, bool* prefix) {
+// Key tile k of an item is two boxes of 64 tokens: the first token of one, and
+// whether it is of the prefix.  An item's own boxes are those of the sink, then
+// those of the window, so that a sink of a few tokens takes half a tile (a box
+// behind the last one begins behind hi).
+__device__ __forceinline__ int box_token(const Piece& pc, int k, int half, bool* prefix) {
   *prefix = k < pc.np;
-  const int t = k < pc.np ? k : (k - pc.np < pc.ns ? k - pc.np : pc.w0 + (k - pc.np - pc.ns));
-  return t * kTile;
+  const int b = 2 * (k < pc.np ? k : k - pc.np) + half;
+  return (k < pc.np || b < pc.ns ? b : pc.w0 + b - pc.ns) * kBox;
 }
 
 // Token j (of a prefix tile or an own one) is attended by some row of the item.
@@ -692,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             row = -1;
             if (j < n) {
               bool prefix;
-              const int tok = tile_token(pc, k, &prefix) + (lane & 1) * kBox;
+              const int tok = box_token(pc, k, lane & 1, &prefix);
               if (any_row_sees_box(p, pc, prefix, tok)) {
                 row = cache_row(prefix ? p.a.pm_prefix : p.a.pm, prefix ? 0 : pc.b, pc.g + (j & dual), p.Hkv, p.n_cap, tok);
                 if (row < 0) {
@@ -911,6 +918,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = pair ? kTile * s + r : r;        // of the item
       const bool warp_rows = (warp & 3) * 32 < pc.rows - (pair ? kTile * s : 0);   // the warp has a row
       const int pos = pc.p0 + (row >> p.gsh);
+      // first token of the row's window, and of the last row's
+      const int row_first = clampi(static_cast<int64_t>(pos) - p.a.local + 1, 0, INT_MAX);
+      const int last_first = clampi(static_cast<int64_t>(pc.p1) - p.a.local + 1, 0, INT_MAX);
       float m = -INFINITY, l = 0.0f;
       int done = 0;
       if (lent) {   // the next product overwrites O_1, the next hand-over x_ml
@@ -920,15 +930,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < n && !dead; ++k) {
         if (!pair && ((k + turn) & 1) != s) continue;
         bool prefix;
-        const int t0 = tile_token(pc, tile_of<kSplit>(pc, k >> dual, pc.n), &prefix);
-        const int last = t0 + kTile - 1;
-        const bool clean = prefix ? last >= p.a.n_prefix : !(last <= pc.hi && (t0 >= pc.lo || last < p.a.sink));
-        const bool all = prefix ? last < p.a.n_prefix
-                                : last <= pc.p0 && (static_cast<int64_t>(t0) > static_cast<int64_t>(pc.p1) - p.a.local ||
-                                                    last < p.a.sink);
-        const int lo = clampi(static_cast<int64_t>(pos) - p.a.local + 1 - t0, 0, kTile);
-        const int hi = prefix ? static_cast<int>(p.a.n_prefix) - t0 : pos - t0 + 1;
-        const int sk = prefix ? kTile : p.a.sink - t0;
+        const int tile = tile_of<kSplit>(pc, k >> dual, pc.n);
+        const int t0 = box_token(pc, tile, 0, &prefix), t1 = box_token(pc, tile, 1, &prefix);
+        // Tokens [0, sink) and [first, end) are attended to: by some row, by every
+        // row, by this row.
+        const int n_prefix = static_cast<int>(p.a.n_prefix), sink = prefix ? 0 : p.a.sink;
+        const int any_first = prefix ? 0 : pc.lo, any_end = prefix ? n_prefix : pc.hi + 1;
+        const int all_first = prefix ? 0 : last_first, all_end = prefix ? n_prefix : pc.p0 + 1;
+        auto inside = [&](int t, int first, int end) { return t + kBox <= end && (t >= first || t + kBox <= sink); };
+        const bool clean = !inside(t0, any_first, any_end) || !inside(t1, any_first, any_end);
+        const bool all = inside(t0, all_first, all_end) && inside(t1, all_first, all_end);
+        uint32_t keep[4] = {0, 0, 0, 0};   // bits: this row attends to the token
+        if (!all) {
+          const int first = prefix ? 0 : row_first, end = prefix ? n_prefix : pos + 1;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int t = (w < 2 ? t0 : t1) + 32 * (w & 1);   // the word's first token
+            keep[w] = below(end - t) & (~below(first - t) | below(sink - t));
+          }
+        }
         // Rows of V that nobody attends to are zeroed, by each group before
         // its own product reads them.  (Called behind the wait for S: by then
         // the slot's tile before V is long loaded, and the phase of that load
@@ -942,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < 8; ++i) {
             const int v_row = (warp & 3) * 32 + 4 * i + (lane >> 3);
-            if (!any_row_sees(p, pc, prefix, t0 + v_row)) {
+            if (!any_row_sees(p, pc, prefix, (v_row < kBox ? t0 : t1 - kBox) + v_row)) {
               uint4* v0 = reinterpret_cast<uint4*>(S.kv[slot] + v_row * 128) + (lane & 7);
               v0[0] = v0[kHalf / 16] = make_uint4(0u, 0u, 0u, 0u);
             }
@@ -966,10 +986,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!all) {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const uint32_t keep = below(hi - 32 * w) & (~below(lo - 32 * w) | below(sk - 32 * w));
 #pragma unroll
               for (int c = 0; c < 32; ++c)
-                if (!((keep >> c) & 1u)) z[32 * w + c] = -INFINITY;
+                if (!((keep[w] >> c) & 1u)) z[32 * w + c] = -INFINITY;
             }
           }
           float a[8];
@@ -1288,7 +1307,8 @@ bool may_split(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms) {
 int64_t most_tiles(const KvAttnArgs& a, int64_t n_cap, int gq, int rows) {
   const int64_t tokens = a.bt.cu_q ? std::min<int64_t>(a.bt.T, rows / gq) : 1;
   const int64_t span = std::min<int64_t>(n_cap, static_cast<int64_t>(a.local) + tokens - 1);   // of the window
-  return (span + 2 * kTile - 2) / kTile + (std::min<int64_t>(a.sink, n_cap) + kTile - 1) / kTile;
+  const int64_t boxes = (span + 2 * kBox - 2) / kBox + (std::min<int64_t>(a.sink, n_cap) + kBox - 1) / kBox;
+  return (boxes + 1) / 2;
 }
 
 // The schedule of a call, `may` it be split, by the time each would take
