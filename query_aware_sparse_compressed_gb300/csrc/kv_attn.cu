@@ -59,19 +59,19 @@
 // two query tiles takes 2048 cycles at their full rate and 3100 to 3300 here:
 // what is left are the waits between softmax and products (a row's softmax takes
 // 1100 cycles to its first half, 1500 to its second, and each group's products
-// 1024).  Measured: 8192 causal tokens, 64 heads: 665 us, 1650 TFLOP/s (86 % of
-// cuBLAS's burst rate); 32768 tokens, 32 heads, a window of 4096: 1360 us, 1515
-// TFLOP/s of useful products (6 % more are computed at the window's edges).  ncu
-// (4096 tokens): tensor pipe 62 % of its active peak, special functions 31 %,
-// issue 39 %, DRAM 7 %.
-// Decode: HBM.  64 sequences, a window of 4096, 8 KV heads (0.99 GB): 157 us, 6.3
-// TB/s (94 % of a copy's rate); one sequence of 131072 tokens (0.54 GB): 87 us.
+// 1024).  Measured: 8192 causal tokens, 64 heads: 660 us, 1670 TFLOP/s (87 % of
+// cuBLAS's burst rate); 32768 tokens, 32 heads, a window of 4096: 1262 us, 1635
+// TFLOP/s of useful products (3 % more are computed at the window's edges).  ncu
+// (4096 tokens): tensor pipe 63 % of its active peak, special functions 32 %,
+// issue 42 %, DRAM 7 %.
+// Decode: HBM.  64 sequences, a window of 4096, 8 KV heads (0.99 GB): 152 us, 6.5
+// TB/s (97 % of a copy's rate); one sequence of 131072 tokens (0.54 GB): 86 us.
 // ncu: 382 MB read where 373 are needed.
-// Few tokens: latency.  4 sequences' 260 tokens: 9.6 us on the GPU, of which the
+// Few tokens: latency.  4 sequences' 260 tokens: 9.5 us on the GPU, of which the
 // plan takes 1.5, the first share 1.1, its first key 1.7, a tile 0.7 to 1.4.  16
-// ragged sequences of 1 to 64 tokens, up to 1400 cached: 18 us with items of 128
+// ragged sequences of 1 to 64 tokens, up to 1400 cached: 16 us with items of 128
 // rows, joined in the block; with 256-row items and a join by the merge 30.
-// A shared prefix: 128 sequences over 131072 tokens, 64 heads: 257 us.
+// A shared prefix: 128 sequences over 131072 tokens, 32 heads: 230 us.
 #include <cuda.h>
 
 #include <algorithm>
