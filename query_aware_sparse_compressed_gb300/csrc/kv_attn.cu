@@ -34,7 +34,8 @@
 //          HBM once for all: see tile_of).
 // The line is planned on the device from the lengths, of which the host knows
 // nothing: by a warp of every CTA for itself, or by kv_plan_kernel for a batch
-// whose plan does not fit beside the tiles.
+// whose plan does not fit beside the tiles.  Whole items of single tokens need no
+// plan.
 //
 // Roles (384 threads):
 //   warps 0-3, 4-7  softmax: group s owns accumulators S_s and O_s, thread r
@@ -67,9 +68,9 @@
 // Decode: HBM.  64 sequences, a window of 4096, 8 KV heads (0.99 GB): 152 us, 6.5
 // TB/s (97 % of a copy's rate); one sequence of 131072 tokens (0.54 GB): 86 us.
 // ncu: 382 MB read where 373 are needed.
-// Few tokens: latency.  4 sequences' 260 tokens: 9.5 us on the GPU, of which the
-// plan takes 1.5, the first share 1.1, its first key 1.7, a tile 0.7 to 1.4.  16
-// ragged sequences of 1 to 64 tokens, up to 1400 cached: 16 us with items of 128
+// Few tokens: latency.  4 sequences' 260 tokens: 8.9 us on the GPU: the
+// first item takes 1.1, its first key 1.7, a tile 0.7 to 1.4 (and a plan, where
+// one is needed, 0.6).  16 ragged sequences of 1 to 64 tokens, up to 1400 cached: 16 us with items of 128
 // rows, joined in the block; with 256-row items and a join by the merge 30.
 // A shared prefix: 128 sequences over 131072 tokens, 32 heads: 230 us.
 #include <cuda.h>
@@ -118,6 +119,7 @@ struct Args {
   int64_t n_cap;
   int item_rows;            // query rows of an item: 256, or 128 (whole only)
   int dual;                 // whole items (of 128 rows) in twos: a unit is two neighbouring KV heads
+  int uniform;              // whole items of single tokens: one per sequence and KV head, no plan
   int once;                 // keys are read by one item, or two
   int split, pre;           // pre: the shared prefix is sequence 0 of the plan (split only)
   int slot_rows;            // partial rows a CTA may add to an item (split)
@@ -350,6 +352,13 @@ __device__ __forceinline__ void plan_scan(int32_t* arr, int n, F&& f) {
   else __syncwarp();
 }
 
+__device__ __forceinline__ void check_lens(const Args& p, int first, int step) {
+  for (int b = first; b < p.B; b += step) {
+    const int v = __ldg(p.a.bt.lens + b);
+    if (v < 0 || v > p.n_cap) record_error(p.err, kErrBadPage);
+  }
+}
+
 // The plan in shared memory, by a warp or a block: ent_base [NS + 1] and line
 // [entries + 1].  `publish`: the copies in global memory (for the merge, and
 // for a batch whose plan the attention's CTAs cannot hold), and the check of
@@ -357,11 +366,7 @@ __device__ __forceinline__ void plan_scan(int32_t* arr, int n, F&& f) {
 template <bool kBlock>
 __device__ __forceinline__ int make_plan(const Args& p, int32_t* ent_base, int32_t* line, bool publish) {
   const int NS = p.B + p.pre, first = kBlock ? threadIdx.x : threadIdx.x & 31, step = kBlock ? blockDim.x : 32;
-  if (publish)
-    for (int b = first; b < p.B; b += step) {
-      const int v = __ldg(p.a.bt.lens + b);
-      if (v < 0 || v > p.n_cap) record_error(p.err, kErrBadPage);
-    }
+  if (publish) check_lens(p, first, step);
   if (!p.split) {
     plan_scan<kBlock>(line, NS, [&](int s) { return q_tiles(p, seq_of(p, s)) * (p.Hkv >> p.dual); });
     if (kBlock)
@@ -408,11 +413,14 @@ template <bool kSplit>
 struct Walk {
   int pos, end, n;   // split: place on the line, its end; whole: round
   int e, s;          // split: current entry and its sequence
+  __device__ __forceinline__ int units(const Args& p, const Plan& S) const {
+    return !kSplit && p.uniform ? n * (p.Hkv >> p.dual) : S.line[n];
+  }
   __device__ __forceinline__ void init(const Args& p, const Plan& S) {
     n = S.entries;
     pos = end = 0;
     if (n == 0) return;
-    const int U = S.line[n];
+    const int U = units(p, S);
     if (kSplit) {
       const Ranges line(U, gridDim.x);
       if (blockIdx.x >= line.G) return;
@@ -455,7 +463,7 @@ struct Walk {
         pos += span;
       }
     } else {
-      const int U = n > 0 ? S.line[n] : 0;
+      const int U = n > 0 ? units(p, S) : 0;
       int u;
       do {
         if (pos >= end) return false;
@@ -465,8 +473,8 @@ struct Walk {
         ++pos;
       } while (u >= U);
       const int x = U - 1 - u;   // late query tiles attend to the most keys
-      const int sq = find_last(S.line, n, x), rem = x - S.line[sq];
       const int heads = p.Hkv >> p.dual;
+      const int sq = p.uniform ? x / heads : find_last(S.line, n, x), rem = x - (p.uniform ? sq * heads : S.line[sq]);
       it = make_item(p, seq_of(p, sq), rem / heads);
       g = (rem % heads) << p.dual;
       pc.k0 = 0;
@@ -738,7 +746,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kQWarp) {
       // ---- the plan, the pieces, and their queries
       Plan plan;
-      if (p.plan_global) {
+      const bool uniform = !kSplit && p.uniform;
+      if (uniform) {
+        plan.entries = p.B;
+      } else if (p.plan_global) {
         plan.ent_base = p.ent_base;
         plan.line = p.line;
         plan.entries = kSplit ? p.ent_base[p.B + p.pre] : p.B;
@@ -782,6 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++uses[b];
         }
       }
+      if (uniform && blockIdx.x == 0) check_lens(p, lane, 32);
       if (dead)
         for (int b = 0; b < 2; ++b)
           if (uses[b] > 0) wait_warp(&S.q_full[b], (uses[b] - 1) & 1u);
@@ -1456,7 +1468,8 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const 
   const int64_t entries = items + s.B + (p.pre ? items : 0);
   p.max_ent = static_cast<int>(entries < kMaxEnt ? entries : kMaxEnt);
   const int64_t words = p.split ? (s.B + p.pre + 1) + (p.max_ent + 1) : s.B + 1;
-  p.plan_global = words > kPlanWords;
+  p.uniform = !p.split && !a.bt.cu_q;
+  p.plan_global = !p.uniform && words > kPlanWords;
   cudaError_t e;
   if (p.plan_global) {
     e = launch_dependent(kv_plan_kernel, dim3(1), dim3(1024), 0, stream, 1, p);

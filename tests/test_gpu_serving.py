@@ -558,6 +558,39 @@ def test_window_step_equals_sink_and_local_of_the_sparse_step():
     assert float((lse - ref_lse).abs().max()) <= 1e-4
 
 
+# Lengths outside [0, n_cap] are clamped and recorded, on every path: single
+# tokens whole and shared between blocks, several tokens, behind a prefix.
+@pytest.mark.parametrize("ql,n_cap,n0", [([1, 1, 1], 256, 0), ([1, 1, 1], 8192, 0), ([9, 2, 40], 256, 0),
+                                         ([1, 1, 1], 256, 70), ([1, 1, 1], 256, 6000)])
+def test_lengths_outside_are_clamped_and_reported(ql, n_cap, n0):
+    Hq, Hkv, P, B = 8, 2, 64, 3
+    pages = Pages([n_cap] * B + [n0], Hkv, P, cdiv(max(n_cap, n0), P), seed=91)
+    K, V, table = pages.cuda()
+    own, pt = table[:B, :n_cap // P].contiguous(), table[B, :cdiv(n0, P)].contiguous()
+    q = rand((sum(ql), Hq, 128), 92).cuda()
+    cu = None if ql == [1] * B else np.concatenate([[0], np.cumsum(ql)]).tolist()
+    size = qasc.kv_prefix_attn_workspace_bytes if n0 else qasc.kv_window_attn_workspace_bytes
+    ws = qasc.alloc_workspace(size(sum(ql), B, Hq, Hkv, n_cap))
+
+    def call(lens):
+        out = torch.zeros((sum(ql), Hq, 128), dtype=torch.bfloat16, device="cuda")
+        c, ln = batch_tensors(cu, lens)
+        if n0:
+            qasc.kv_prefix_attn_paged(q, K, V, pt, own, ln, out, ws, n_prefix=n0, cu_q=c)
+        else:
+            qasc.kv_window_attn_paged(q, K, V, own, ln, out, ws, local=1 << 30, cu_q=c)
+        return out
+    want = call([n_cap, 100, 0])
+    qasc.qasc_device_error()
+    got = call([n_cap + 70, 100, -3])
+    with pytest.raises(qasc.QascError) as e:
+        qasc.qasc_device_error()
+    assert e.value.status == 6
+    assert torch.equal(want, got)
+    call([n_cap, 100, 0])
+    qasc.qasc_device_error()
+
+
 def test_window_bad_page_is_reported():
     Hq, Hkv, P = 8, 2, 64
     pages = Pages([200], Hkv, P, 4, seed=19)
