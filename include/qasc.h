@@ -327,10 +327,10 @@ QASC_API qasc_status ts_ring_flush(const qasc_shape* shape, const qasc_paged_cac
 /* ---------------------------------------------------------------------------
  * Serving calls over packed batches: appending new tokens to the cache, and
  * causal attention of many new tokens at once.  No counterpart on the source
- * pages beyond the cache itself ([TokenSelect] section "まとめ", integration
- * with vLLM's PagedAttention; the sink and local tokens of its
- * always-included table): what an engine around the decode step needs to fill
- * the cache and to prefill, with the cache layouts above.
+ * pages beyond the cache itself ([TokenSelect] section "まとめ", a serving
+ * engine's paged cache; the sink and local tokens of its always-included
+ * table): what an engine around the decode step needs to fill the cache and to
+ * prefill, with the cache layouts above.
  *
  * A batch is T tokens packed without padding.  Sequence b has the new tokens
  * [cu_q[b], cu_q[b + 1]) and lens[b] cached tokens, of which its new ones are

@@ -61,9 +61,9 @@
 // what is left are the waits between softmax and products (a row's softmax takes
 // 1100 cycles to its first half, 1500 to its second, and each group's products
 // 1024).  Measured: 8192 causal tokens, 64 heads: 660 us, 1670 TFLOP/s (87 % of
-// cuBLAS's burst rate); 32768 tokens, 32 heads, a window of 4096: 1262 us, 1635
-// TFLOP/s of useful products (3 % more are computed at the window's edges).  ncu
-// (4096 tokens): tensor pipe 63 % of its active peak, special functions 32 %,
+// cuBLAS's burst rate); 32768 tokens, 32 heads, a window of 4096: 1260 to 1330
+// us, 1550 to 1635 TFLOP/s of useful products (3 % more are computed at the
+// window's edges).  ncu (4096 tokens): tensor pipe 63 % of its active peak, special functions 32 %,
 // issue 42 %, DRAM 7 %.
 // Decode: HBM.  64 sequences, a window of 4096, 8 KV heads (0.99 GB): 152 us, 6.5
 // TB/s (97 % of a copy's rate); one sequence of 131072 tokens (0.54 GB): 86 us.
