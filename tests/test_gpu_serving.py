@@ -762,6 +762,40 @@ def test_window_of_short_and_empty_sequences(Hq, Hkv):
     check_rows(out, lse, ref, 170)
 
 
+@pytest.mark.parametrize("n0,ql", [(100, [1] * 30), (6000, [1] * 30), (6000, [40, 3, 90])])
+def test_prefix_replays_in_a_graph(n0, ql):
+    Hq, Hkv, P, B, T = 16, 4, 64, len(ql), sum(ql)
+    lens = [m + (37 * b) % 200 for b, m in enumerate(ql)]
+    both = Pages([n0] + lens, Hkv, P, max(5, cdiv(n0, P)), seed=93)
+    K, V, table = both.cuda()
+    own, pt = table[1:, :5].contiguous(), table[0, :cdiv(n0, P)].contiguous()
+    q = rand((T, Hq, 128), 94).cuda()
+    c, ln = batch_tensors(None if T == B else np.concatenate([[0], np.cumsum(ql)]).tolist(), lens)
+    ws = qasc.alloc_workspace(qasc.kv_prefix_attn_workspace_bytes(T, B, Hq, Hkv, 5 * P))
+
+    def call(out, lse):
+        qasc.kv_prefix_attn_paged(q, K, V, pt, own, ln, out, ws, n_prefix=n0, cu_q=c, lse=lse)
+
+    def fresh():
+        return (torch.zeros((T, Hq, 128), dtype=torch.bfloat16, device="cuda"),
+                torch.zeros((T, Hq), dtype=torch.float32, device="cuda"))
+    a, b, g_out = fresh(), fresh(), fresh()
+    call(*a)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        call(*g_out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], g_out[0]) and torch.equal(a[1], g_out[1])
+    ln.copy_(torch.tensor([max(0, x - 60) for x in lens], dtype=torch.int32))   # the replay follows the lengths
+    graph.replay()
+    call(*b)
+    torch.cuda.synchronize()
+    assert torch.equal(b[0], g_out[0]) and torch.equal(b[1], g_out[1]) and not torch.equal(a[0], b[0])
+    qasc.qasc_device_error()
+
+
 def test_prefix_leaves_other_rows_alone():
     Hq, Hkv, P = 8, 2, 64
     both = Pages([100, 20, 30], Hkv, P, 2, seed=33)
