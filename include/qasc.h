@@ -533,6 +533,19 @@ QASC_API qasc_status qasc_device_error(void* stream);
  * QASC_ERR_INVALID_ARG for limit_us outside [1, 2000000]. */
 QASC_API qasc_status qasc_selftest_bounded_wait(int32_t limit_us, void* stream);
 
+/* The same for the roles of the attention kernel: kv_window_attn in which no
+ * block gets the K and V tiles from its `stall`-th on (each counted, from 0),
+ * with waits that give up after limit_us microseconds.  Where one does, the
+ * block loads nothing more, waits (with the library's own limit) for its
+ * copies and products in flight, frees its tensor memory and returns, and the
+ * next qasc_device_error() reports QASC_ERR_TIMEOUT; `out` and `lse` are then
+ * undefined.  Blocks that need fewer tiles finish.  QASC_ERR_INVALID_ARG for
+ * limit_us outside [1, 2000000] or stall < 0. */
+QASC_API qasc_status qasc_selftest_attn_wait(int32_t limit_us, int32_t stall, const qasc_shape* shape,
+                                             const qasc_batch* batch, int32_t sink, int32_t local, const uint16_t* q,
+                                             const uint16_t* K, const uint16_t* V, uint16_t* out, float* lse,
+                                             void* workspace, size_t ws_bytes, void* stream);
+
 /* Library version as 10000 * major + 100 * minor + patch. */
 QASC_API int32_t qasc_version(void);
 

@@ -19,7 +19,7 @@ Entry points keep the C names:
   kv_prefix_attn_workspace_bytes, kv_prefix_attn_paged,
   ts_dense_attn_workspace_bytes, ts_dense_attn, snapkv_workspace_bytes,
   snapkv_compress, qasc_status_string, qasc_last_error, qasc_last_cuda_error, qasc_device_error,
-  qasc_selftest_bounded_wait, qasc_version.
+  qasc_selftest_bounded_wait, qasc_selftest_attn_wait, qasc_version.
 """
 
 import ctypes
@@ -568,8 +568,9 @@ def kv_rope_append_paged(q, k, v, q_out, K_pool, V_pool, block_table, kv_lens, i
                  positions, interleaved, stream)
 
 
-def _attn(name, q, K, V, block_table, kv_lens, out, workspace, cu_q, lse, stream, front, behind):
-    """front: the library's arguments before the batch, behind: those after it."""
+def _attn(name, q, K, V, block_table, kv_lens, out, workspace, cu_q, lse, stream, front, behind, fn=None):
+    """front: the library's arguments before the batch, behind: those after it;
+    fn: called in place of the library's `name`."""
     if not isinstance(q, _Tensor) or q.dim() != 3:
         raise ValueError("q must have shape (T, Hq, %d)" % D)
     dev = q.get_device()
@@ -584,7 +585,7 @@ def _attn(name, q, K, V, block_table, kv_lens, out, workspace, cu_q, lse, stream
     lp = None if lse is None else _at(lse, "lse", _F32, (T, Hq), dev)
     ws_bytes = workspace.numel()
     wp = _at(workspace, "workspace", _U8, (ws_bytes,), dev)
-    _run(getattr(_L(), name), dev, stream, _lib.pack_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap), cache, *front,
+    _run(fn or getattr(_L(), name), dev, stream, _lib.pack_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap), cache, *front,
          batch, *behind, qp, Kp, Vp, op, lp, wp, ws_bytes)
 
 
@@ -674,6 +675,16 @@ def qasc_selftest_bounded_wait(limit_us, stream=None):
     """Run one kernel whose bounded wait cannot complete; it gives up after
     limit_us and records a timeout for the next qasc_device_error()."""
     _check(_L().qasc_selftest_bounded_wait(int(limit_us), _stream(stream)))
+
+
+def qasc_selftest_attn_wait(limit_us, stall, q, K, V, kv_lens, out, workspace, *, local, sink=4, cu_q=None, lse=None,
+                            stream=None):
+    """kv_window_attn in which no block gets its K and V tiles from the stall-th
+    on, with waits that give up after limit_us: the next qasc_device_error()
+    reports the timeout and out and lse are undefined."""
+    call = _L().qasc_selftest_attn_wait
+    _attn("qasc_selftest_attn_wait", q, K, V, None, kv_lens, out, workspace, cu_q, lse, stream, (), (sink, local),
+          fn=lambda *args: call(int(limit_us), int(stall), *args))
 
 
 def qasc_version():

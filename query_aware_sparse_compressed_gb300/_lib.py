@@ -101,6 +101,8 @@ SIGNATURES = {
     "qasc_last_cuda_error": (ctypes.c_char_p, []),
     "qasc_device_error": (ctypes.c_int, [_P]),
     "qasc_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_int32, _P]),
+    "qasc_selftest_attn_wait": (ctypes.c_int, [_I32, _I32, _P, _P, _I32, _I32, _P, _P, _P, _P, _P, _P, ctypes.c_size_t,
+                                               _P]),
     "qasc_version": (ctypes.c_int32, []),
 }
 

@@ -696,18 +696,40 @@ QASC_API size_t kv_window_attn_workspace_bytes(const qasc_shape* shape, int64_t 
   return kv_attn_size("kv_window_attn_workspace_bytes", shape, tokens, false);
 }
 
-QASC_API qasc_status kv_window_attn(const qasc_shape* shape, const qasc_batch* batch, int32_t sink, int32_t local,
-                                    const uint16_t* q, const uint16_t* K, const uint16_t* V, uint16_t* out, float* lse,
-                                    void* workspace, size_t ws_bytes, void* stream) {
-  static const char* fn = "kv_window_attn";
+namespace {
+qasc_status window_attn_call(const char* fn, const qasc_shape* shape, const qasc_batch* batch, qasc::KvAttnArgs& a,
+                             int32_t sink, int32_t local, const uint16_t* q, const uint16_t* K, const uint16_t* V,
+                             uint16_t* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
   QASC_RANGE(fn);
   QASC_CHECK(check_shape(shape, fn));
   QASC_CHECK(check_window(sink, local, fn));
-  qasc::KvAttnArgs a;
   a.sink = sink;
   a.local = local;
   a.cache_rows = static_cast<int64_t>(shape->B) * shape->Hkv * shape->n_cap;
   return kv_attn_call(fn, shape, batch, a, false, q, K, V, out, lse, workspace, ws_bytes, stream);
+}
+}  // namespace
+
+QASC_API qasc_status kv_window_attn(const qasc_shape* shape, const qasc_batch* batch, int32_t sink, int32_t local,
+                                    const uint16_t* q, const uint16_t* K, const uint16_t* V, uint16_t* out, float* lse,
+                                    void* workspace, size_t ws_bytes, void* stream) {
+  qasc::KvAttnArgs a;
+  return window_attn_call("kv_window_attn", shape, batch, a, sink, local, q, K, V, out, lse, workspace, ws_bytes,
+                          stream);
+}
+
+QASC_API qasc_status qasc_selftest_attn_wait(int32_t limit_us, int32_t stall, const qasc_shape* shape,
+                                             const qasc_batch* batch, int32_t sink, int32_t local, const uint16_t* q,
+                                             const uint16_t* K, const uint16_t* V, uint16_t* out, float* lse,
+                                             void* workspace, size_t ws_bytes, void* stream) {
+  static const char* fn = "qasc_selftest_attn_wait";
+  if (limit_us < 1 || limit_us > 2000000)
+    return fail(QASC_ERR_INVALID_ARG, "%s: limit_us=%d must lie in [1, 2000000]", fn, limit_us);
+  if (stall < 0) return fail(QASC_ERR_INVALID_ARG, "%s: stall=%d must be >= 0", fn, stall);
+  qasc::KvAttnArgs a;
+  a.wait_ns = static_cast<unsigned long long>(limit_us) * 1000ull;
+  a.stall = stall;
+  return window_attn_call(fn, shape, batch, a, sink, local, q, K, V, out, lse, workspace, ws_bytes, stream);
 }
 
 QASC_API qasc_status kv_window_attn_paged(const qasc_shape* shape, const qasc_paged_cache* cache,

@@ -289,6 +289,8 @@ struct KvAttnArgs {
   int64_t cache_rows = 0;        // rows of K and of V
   int32_t sink = 0, local = 0;
   int64_t n_prefix = 0;
+  int64_t stall = -1;            // self-test (>= 0): the tile at this place of each block's ring never comes,
+  unsigned long long wait_ns = 0;   // and waits give up after this time
 };
 size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms);
 int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream);

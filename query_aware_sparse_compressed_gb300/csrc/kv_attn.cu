@@ -161,6 +161,9 @@ struct Smem {
   float2 x_ml[kTile];                            // its rows' (max in log2 units, sum)
   uint32_t tmem_base;
   int32_t plan[kPlanWords];
+  uint64_t mma_done;                             // every product of the CTA is complete (where a wait ran out)
+  uint4 last[3];                                 // what the loaders (K, V, queries) issued last
+  int32_t failed;                                // a wait ran out
 };
 
 static_assert(sizeof(Smem) <= 232448, "shared memory of a block");
@@ -585,11 +588,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // costs the product pipeline more than the tries do (8192 causal tokens of 64
 // heads: 888 us with one lane waiting, 742 with a loop per lane, 710 so).  The
 // tries without a suspend-time hint wake sooner (745 us with one).
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity,
+                                          unsigned long long limit_ns = kWaitTimeoutNs) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const unsigned long long t0 = globaltimer_ns();
   while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitTimeoutNs)) return false;
+    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) return false;
   return true;
 }
 
@@ -603,6 +607,33 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Behind the roles, where a wait ran out, of any warp: the issuers wait for the
+// loads and products that they have in flight (otherwise the warp that uses
+// them has), so that nothing writes into shared or tensor memory that is the
+// next block's by then.  Of the ring's five tiles at most four are one loader's.
+// (A call of its own, since the code of the roles is sensitive to what stands
+// behind them: inlined, 128 sequences over a 128K prefix took 264 us, 258 so; as
+// unconditional waits in the roles it cost decoding 1.3 %.)
+__device__ __noinline__ void finish_issued(Smem& S, int warp) {
+  if (warp == kKWarp || warp == kVWarp) {
+    const uint4 at = S.last[warp - kKWarp];   // places + 1
+    auto done = [&](uint32_t x) {
+      if (x > 0) wait_warp(&S.full[(x - 1) % kSlots], ((x - 1) / kSlots) & 1u);
+    };
+    done(at.x);
+    done(at.y);
+    done(at.z);
+    done(at.w);
+  } else if (warp == kQWarp) {
+    const uint4 n = S.last[2];
+    if (n.x > 0) wait_warp(&S.q_full[0], (n.x - 1) & 1u);
+    if (n.y > 0) wait_warp(&S.q_full[1], (n.y - 1) & 1u);
+  } else if (warp == kMmaWarp) {
+    if (elect_one()) mma_commit(&S.mma_done);   // the lane that issued
+    wait_warp(&S.mma_done, 0);
+  }
+}
+
 // Bits [0, n) of a word, n any integer.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
@@ -612,7 +643,9 @@ __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32
 // 97 us in a kernel of twos alone, 108 in one that also holds whole pair items.
 enum Mode { kModeSplit, kModeWhole, kModeTwos };
 
-template <Mode kMode>
+// kTest: the waits give up after p.a.wait_ns, and the tile at place p.a.stall of
+// the ring never comes (the failure path of every role, without a fault).
+template <Mode kMode, bool kTest = false>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_attn_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v) {
@@ -647,6 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&S.x_full, 4);
     mbar_init(&S.x_empty, 4);
+    mbar_init(&S.mma_done, 1);
+    S.failed = 0;
     fence_barrier_init();
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
@@ -665,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool dead = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (dead) return;
-    if (!wait_warp(bar, parity)) {
+    if (!wait_warp(bar, parity, kTest ? p.a.wait_ns : kWaitTimeoutNs)) {
       record_error(p.err, kErrTimeout);
       dead = true;
     }
@@ -721,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t row1 = __shfl_sync(0xffffffffu, row, 2 * (i & 15) + 1);
           const uint32_t at = ring + (is_k ? k_place(i, ahead) : v_place(i, n, ahead)), slot = at % kSlots;
           wait(&S.empty[slot], ((at / kSlots) & 1u) ^ 1u);
+          if (kTest && at >= p.a.stall) dead = true;
           if (dead) break;
           if (lane == 0) mbar_arrive_expect_tx(&S.full[slot], ((row0 >= 0) + (row1 >= 0)) * 2 * kBoxBytes);
           __syncwarp();
@@ -737,12 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ring += 2 * n;
       }
-      // Every load is over once the MMA warp has waited for it; where a wait ran
-      // out, nothing of this warp stays in flight past here (of the ring's five
-      // tiles at most four are one warp's).
-      if (dead)
-        for (int i = 0; i < 4; ++i)
-          if (mine[i] > 0) wait_warp(&S.full[(mine[i] - 1) % kSlots], ((mine[i] - 1) / kSlots) & 1u);
+      if (lane == 0) S.last[warp - kKWarp] = make_uint4(mine[0], mine[1], mine[2], mine[3]);
     } else if (warp == kQWarp) {
       // ---- the plan, the pieces, and their queries
       Plan plan;
@@ -794,9 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (uniform && blockIdx.x == 0) check_lens(p, lane, 32);
-      if (dead)
-        for (int b = 0; b < 2; ++b)
-          if (uses[b] > 0) wait_warp(&S.q_full[b], (uses[b] - 1) & 1u);
+      if (lane == 0) S.last[2] = make_uint4(uses[0], uses[1], 0, 0);
     } else if (warp == kMmaWarp) {
       // ---- MMA issue.  The whole warp walks and waits, and one elected lane
       // issues: in code that only one lane runs every operand of an MMA is moved
@@ -812,8 +841,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t qd = sw128_desc(smem_u32(S.q[0])), kd = sw128_desc(smem_u32(S.kv[0]));
       const uint64_t vd = sw128_mn_desc(smem_u32(S.kv[0]), kHalf, 1024);
       uint32_t np = 0;   // bit s: phase of the probabilities of group s
-      // A wait that ran out ends the loop over the tiles, not the tile: its
-      // products are computed on what is there.
+      // A wait that ran out ends the loop over the tiles.  The tile's own products
+      // may still be computed, on what is there (a test at each of them costs 1.7 %
+      // of a prompt's time), but no tile is handed back to its loader any more: one
+      // that never came still belongs to the copy in flight.
       // Waits for the next tile of the ring; its slot.
       auto next_tile = [&]() {
         const uint32_t slot = ring % kSlots;
@@ -877,6 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k + 2 < n) knext = next_tile();
             if (has_k) qk(1, 1, kslot);
             else commit(&S.o_full[1]);
+            if (dead) break;
             if (k >= 0) commit(&S.empty[vslot]);
             if (has_k) commit(&S.empty[kslot]);
             if (k + 1 == n - 1) {
@@ -899,12 +931,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k >= 0) {
               const uint32_t slot = next_tile();
               pv(s, slot, k < 2);
+              if (dead) break;
               commit(&S.empty[slot]);
               if (k >= n - 2) commit(&S.o_full[s]);
             }
             if (k + 2 < n) {
               const uint32_t slot = next_tile();
               const uint32_t qs = dual ? s : qb;
+              if (dead) break;
               qk(s, qs, slot);
               commit(&S.empty[slot]);
               if (k + 2 >= n - 1 - dual) commit(&S.q_empty[qs]);   // its last use
@@ -1171,9 +1205,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  if (dead) S.failed = 1;
   tc_fence_before();
   __syncthreads();
   pdl_trigger();   // (at the CTA's start: 93 against 88 us for one 128K sequence, decoding)
+  if (S.failed) finish_issued(S, warp);
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -1407,6 +1443,15 @@ int encode_rows(CUtensorMap* m, const uint16_t* base, int64_t rows, EncodeTiledF
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+using AttnKernel = void (*)(Args, CUtensorMap, CUtensorMap, CUtensorMap);
+AttnKernel kernel_of(Mode mode, bool test) {
+  switch (mode) {
+    case kModeSplit: return test ? kv_attn_kernel<kModeSplit, true> : kv_attn_kernel<kModeSplit>;
+    case kModeWhole: return test ? kv_attn_kernel<kModeWhole, true> : kv_attn_kernel<kModeWhole>;
+    default: return test ? kv_attn_kernel<kModeTwos, true> : kv_attn_kernel<kModeTwos>;
+  }
+}
+
 }  // namespace
 
 size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms) {
@@ -1415,15 +1460,12 @@ size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, bool prefix, i
 }
 
 cudaError_t configure_kv_attn_kernels(const DeviceInfo&) {
-  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<kModeSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(sizeof(Smem)));
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kv_attn_kernel<kModeWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(sizeof(Smem)));
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kv_attn_kernel<kModeTwos>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(sizeof(Smem)));
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  for (const bool test : {false, true})
+    for (const Mode mode : {kModeSplit, kModeWhole, kModeTwos})
+      if ((e = cudaFuncSetAttribute(kernel_of(mode, test), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(sizeof(Smem)))) != cudaSuccess)
+        return e;
   const int merge = static_cast<int>(merge_smem(kMaxEnt));
   if ((e = cudaFuncSetAttribute(kv_merge_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, merge)) != cudaSuccess)
     return e;
@@ -1475,7 +1517,7 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const 
     e = launch_dependent(kv_plan_kernel, dim3(1), dim3(1024), 0, stream, 1, p);
     if (e != cudaSuccess) return e;
   }
-  const auto attn = p.split ? kv_attn_kernel<kModeSplit> : (p.dual ? kv_attn_kernel<kModeTwos> : kv_attn_kernel<kModeWhole>);
+  const auto attn = kernel_of(p.split ? kModeSplit : (p.dual ? kModeTwos : kModeWhole), a.stall >= 0);
   e = launch_dependent(attn, dim3(dev.num_sms), dim3(kThreads), sizeof(Smem), stream, 1, p, tq, tk, tv);
   if (e != cudaSuccess || !p.split) return e;
   // Few rows: several thread groups to an element (one 128K sequence 86.3 us,

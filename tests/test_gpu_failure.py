@@ -52,3 +52,44 @@ def test_context_usable_after_a_timeout():
     qasc.qasc_device_error()
     s = sel.cpu()
     assert s.shape == (cfg.B, K) and bool((s[:, 1:] > s[:, :-1]).all())
+
+
+# The attention kernel's roles, with a tile that never comes: whichever it is,
+# the call returns with the error status and leaves nothing behind for the next
+# one.  The schedules: shares and a merge (2 x 471 places over 152 blocks: three
+# tiles of K and of V to each); whole items of two query tiles; of one, joined; in
+# twos.
+@pytest.mark.parametrize("Hq,Hkv,ql,lens,local", [
+    (8, 2, [1], [60000], 1 << 30),
+    (64, 8, [2048], [2100], 300),
+    (16, 2, [300] * 6, [500] * 6, 90),
+    (8, 8, [1] * 60, [700] * 60, 700),
+])
+def test_attention_returns_where_a_tile_never_comes(Hq, Hkv, ql, lens, local):
+    B, T, n_cap = len(ql), sum(ql), max(lens)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+    q, K, V = rand(T, Hq, 128), rand(B, Hkv, n_cap, 128), rand(B, Hkv, n_cap, 128)
+    cu = torch.tensor([sum(ql[:b]) for b in range(B + 1)], dtype=torch.int32, device="cuda")
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = qasc.alloc_workspace(qasc.kv_window_attn_workspace_bytes(T, B, Hq, Hkv, n_cap))
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    kw = dict(local=local, cu_q=None if T == B else cu)
+    qasc.kv_window_attn(q, K, V, ln, want, ws, **kw)
+    qasc.qasc_device_error()
+    for stall in (0, 1, 2, 3, 1 << 30):
+        out.zero_()
+        t0 = time.perf_counter()
+        qasc.qasc_selftest_attn_wait(5000, stall, q, K, V, ln, out, ws, **kw)
+        if stall < 1 << 30:
+            with pytest.raises(qasc.QascError) as e:
+                qasc.qasc_device_error()
+            assert e.value.status == 5
+            assert time.perf_counter() - t0 < 20.0
+        else:
+            qasc.qasc_device_error()
+            assert torch.equal(out, want)
+        out.zero_()
+        qasc.kv_window_attn(q, K, V, ln, out, ws, **kw)
+        qasc.qasc_device_error()
+        assert torch.equal(out, want), "the call behind one without tile %d" % stall

@@ -188,6 +188,15 @@ def test_workspace_queries(lib):
         qasc.kv_window_attn_workspace_bytes(-1, 1, 8, 2, 512)
 
 
+def test_selftest_of_the_attention_rejects_bad_limits(lib):
+    c = Call()
+    call = lambda limit, stall: lib.qasc_selftest_attn_wait(limit, stall, ctypes.byref(c.s), ctypes.byref(c.b), 4, 256,
+                                                            FAKE, FAKE, FAKE, FAKE, None, FAKE, 1 << 40, None)
+    assert call(0, 0) == 1 and call(-5, 0) == 1 and call(2000001, 0) == 1 and call(1000, -1) == 1
+    c.s.n_cap = 0
+    assert call(1000, 0) == 1
+
+
 def t(*shape, dtype=bf):
     return torch.zeros(shape, dtype=dtype)
 
