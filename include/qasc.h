@@ -408,7 +408,13 @@ QASC_API qasc_status kv_rope_append_paged(const qasc_shape* shape, const qasc_pa
  * work is shared between blocks is chosen from T, B, the heads, local, n_prefix
  * and n_cap, the bound on the lengths that the host knows (a table with fewer
  * columns states a lower one).  The workspace need not be cleared and is free again once the call has finished
- * on the stream; calls that can overlap need one each. */
+ * on the stream; calls that can overlap need one each.  Its size does not fall
+ * with more tokens or sequences, so that one of the largest batch's size serves
+ * every smaller one.  It holds the partial rows of calls that are shared between
+ * blocks, some 1040 bytes for a token and query head (2080 with a prefix), of the
+ * most tokens that such a call can have: below 320 MB, or 600 MB with a prefix
+ * and, there, 2080 * 128 * B * Hkv bytes.  A call that is not shared accepts the
+ * size for 0 tokens. */
 QASC_API size_t kv_window_attn_workspace_bytes(const qasc_shape* shape, int64_t tokens);
 QASC_API qasc_status kv_window_attn(const qasc_shape* shape, const qasc_batch* batch, int32_t sink, int32_t local,
                                     const uint16_t* q, const uint16_t* K, const uint16_t* V, uint16_t* out, float* lse,

@@ -643,10 +643,9 @@ qasc_status kv_attn_call(const char* fn, const qasc_shape* shape, const qasc_bat
   if (a.bt.T == 0) return ok();
   QASC_REQUIRE_PTR(q, 16, fn);
   QASC_REQUIRE_PTR(out, 16, fn);
-  const size_t need = qasc::kv_attn_workspace_bytes(a.bt.T, shape->B, shape->Hq, shape->Hkv, prefix,
-                                                    qasc::kMaxSmsForSizing);
-  if (!workspace || ws_bytes < need)
-    return fail(QASC_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+  if (!workspace || ws_bytes < qasc::kv_attn_whole_bytes())
+    return fail(QASC_ERR_WORKSPACE, "%s: workspace of up to %zu bytes needed, %zu given", fn,
+                qasc::kv_attn_workspace_bytes(a.bt.T, shape->B, shape->Hq, shape->Hkv, prefix, qasc::kMaxSmsForSizing),
                 workspace ? ws_bytes : size_t(0));
   QASC_REQUIRE_PTR(workspace, 256, fn);
   qasc_status st;
@@ -657,8 +656,11 @@ qasc_status kv_attn_call(const char* fn, const qasc_shape* shape, const qasc_bat
   a.V = V;
   a.out = out;
   a.lse = lse;
-  const int rc = qasc::launch_kv_attn(*shape, a, static_cast<uint8_t*>(workspace), *dev,
+  size_t need = ws_bytes;
+  const int rc = qasc::launch_kv_attn(*shape, a, static_cast<uint8_t*>(workspace), &need, *dev,
                                       static_cast<cudaStream_t>(stream));
+  if (rc == qasc::kSmallWorkspace)
+    return fail(QASC_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need, ws_bytes);
   if (rc != 0) return cuda_fail(rc, fn);
   return ok();
 }

@@ -293,7 +293,11 @@ struct KvAttnArgs {
   unsigned long long wait_ns = 0;   // and waits give up after this time
 };
 size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms);
-int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream);
+size_t kv_attn_whole_bytes();   // of a call that is not split: the least of any
+// kSmallWorkspace, with *ws_bytes set to what the call's schedule needs, where it is less.
+constexpr int kSmallWorkspace = -2;
+int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, size_t* ws_bytes, const DeviceInfo& dev,
+                   cudaStream_t stream);
 cudaError_t configure_kv_attn_kernels(const DeviceInfo& dev);
 
 // Neighbour expansion: rows of K ascending candidates in, the ascending union

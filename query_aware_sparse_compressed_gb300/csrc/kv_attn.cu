@@ -1454,10 +1454,17 @@ AttnKernel kernel_of(Mode mode, bool test) {
 
 }  // namespace
 
+// Enough for every batch of at most T tokens (and B sequences): the most tokens
+// that may be split take the most, more tokens no partial rows.  For the most
+// SMs: a device with fewer splits a subset of these batches.
 size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, bool prefix, int num_sms) {
-  // For the most SMs: a device with fewer splits a subset of these batches.
-  return layout_of(T, Hq, Hkv, prefix, may_split(T, B, Hq, Hkv, prefix, num_sms), num_sms).total;
+  const int64_t gq = Hq / Hkv;
+  int64_t most = (4 * static_cast<int64_t>(num_sms) - 1) / Hkv * kItemRows / gq;   // the bounds of may_split
+  if (prefix) most = std::max(most, (static_cast<int64_t>(kTile) * B - 1) / gq);
+  return layout_of(std::min(T, most), Hq, Hkv, prefix, true, num_sms).total;
 }
+
+size_t kv_attn_whole_bytes() { return layout_of(0, 1, 1, false, false, 0).total; }
 
 cudaError_t configure_kv_attn_kernels(const DeviceInfo&) {
   cudaError_t e;
@@ -1474,7 +1481,8 @@ cudaError_t configure_kv_attn_kernels(const DeviceInfo&) {
   return cudaFuncSetAttribute(kv_merge_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, merge);
 }
 
-int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream) {
+int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, size_t* ws_bytes, const DeviceInfo& dev,
+                   cudaStream_t stream) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return cudaErrorNotSupported;
   const int gq = s.Hq / s.Hkv;
@@ -1498,6 +1506,10 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, const 
   p.pre = p.split && prefix;
   p.once = a.bt.T * gq <= static_cast<int64_t>(kItemRows) * s.B && p.pre == prefix;
   const Layout L = layout_of(a.bt.T, s.Hq, s.Hkv, prefix, p.split, dev.num_sms);
+  if (*ws_bytes < L.total) {
+    *ws_bytes = L.total;
+    return kSmallWorkspace;
+  }
   p.slot_rows = L.slot_rows;
   p.part_o = reinterpret_cast<float4*>(ws + L.off_o);
   p.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);

@@ -677,6 +677,31 @@ def test_two_windows_on_two_streams():
     assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
 
 
+def test_a_workspace_of_the_prompt_serves_every_smaller_call():
+    Hq, Hkv, P, n = 64, 8, 64, 5000             # more rows than a shared call can have
+    pages = Pages([n], Hkv, P, cdiv(n, P), seed=25)
+    K, V, table = pages.cuda()
+    q = rand((n, Hq, 128), 26).cuda()
+    size = lambda m: qasc.kv_window_attn_workspace_bytes(m, 1, Hq, Hkv, pages.pps * P)
+    shared = qasc.alloc_workspace(size(n))
+
+    def call(m, ws):
+        out = torch.zeros((m, Hq, 128), dtype=torch.bfloat16, device="cuda")
+        c, ln = batch_tensors([0, m], [n])
+        qasc.kv_window_attn_paged(q[:m], K, V, table, ln, out, ws, local=n, cu_q=c)
+        return out
+    for m in (n, 1, 300, 4064, 7):
+        own = call(m, qasc.alloc_workspace(size(m)))
+        assert torch.equal(call(m, shared), own)
+    # no rows are shared: the least workspace is enough; one token's are, and it is not
+    least = qasc.alloc_workspace(size(0))
+    assert torch.equal(call(n, least), call(n, shared))
+    with pytest.raises(qasc.QascError) as e:
+        call(1, least)
+    assert e.value.status == 3
+    qasc.qasc_device_error()
+
+
 # --------------------------------------------------------------------- prefix
 PREFIX = [
     # Hq, Hkv, P, n_prefix, q_lens, lens

@@ -188,6 +188,23 @@ def test_workspace_queries(lib):
         qasc.kv_window_attn_workspace_bytes(-1, 1, 8, 2, 512)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(64, 8), (32, 8), (8, 2), (24, 3), (64, 64), (1, 1), (8, 1)])
+def test_workspace_does_not_fall_with_tokens_or_sequences(lib, Hq, Hkv):
+    # an engine allocates for its largest batch and calls with smaller ones
+    names = "kv_window_attn_workspace_bytes", "kv_prefix_attn_workspace_bytes"
+    tokens = sorted({max(0, t + d) for t in [int(1.2 ** i) for i in range(80)] + [2 ** i for i in range(22)]
+                     for d in (-1, 0, 1)})
+    sized = {}
+    for B in (1, 2, 7, 300, 2048 if Hkv < 64 else 1000):
+        s = _lib.qasc_shape(B, Hq, Hkv, 128, 32, 0, 64, 64)
+        for name in names:
+            sizes = [getattr(lib, name)(ctypes.byref(s), t) for t in tokens]
+            assert all(x > 0 for x in sizes) and sizes == sorted(sizes)
+            assert all(x >= y for x, y in zip(sizes, sized.get(name, sizes)))
+            sized[name] = sizes
+        assert all(x >= y for x, y in zip(sized[names[1]], sized[names[0]]))
+
+
 def test_selftest_of_the_attention_rejects_bad_limits(lib):
     c = Call()
     call = lambda limit, stall: lib.qasc_selftest_attn_wait(limit, stall, ctypes.byref(c.s), ctypes.byref(c.b), 4, 256,
