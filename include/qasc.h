@@ -339,8 +339,10 @@ QASC_API qasc_status ts_ring_flush(const qasc_shape* shape, const qasc_paged_cac
  * cu_q and lens are read on the device, so a captured call follows them.
  * Tokens outside [cu_q[0], cu_q[B]) belong to no sequence: nothing is read or
  * written for them.  A sequence may have no new tokens.  cu_q is ascending
- * within [0, T] and lens within [0, n_cap]; a value outside is clamped, and
- * one of lens recorded as QASC_ERR_BAD_TABLE.
+ * within [0, T], a value outside is clamped; lens lies within [0, n_cap], a value
+ * outside is recorded as QASC_ERR_BAD_TABLE.  With such a length the attention
+ * calls clamp it, and the append leaves out the tokens that it places outside the
+ * cache.
  * The shape's n is not used (pass n_cap); tokens * Hq < 2^31.
  * ------------------------------------------------------------------------- */
 typedef struct {

@@ -107,7 +107,8 @@ __device__ __forceinline__ TokenAt token_of(const Batch& bt, int64_t t) {
     if (__ldg(bt.cu_q + mid) <= t) lo = mid;
     else hi = mid;
   }
-  const int64_t q0 = __ldg(bt.cu_q + lo), q1 = __ldg(bt.cu_q + lo + 1);
+  int64_t q0 = __ldg(bt.cu_q + lo), q1 = __ldg(bt.cu_q + lo + 1);
+  if (q1 > bt.T) q1 = bt.T;   // clamped, as the attention calls do
   r.b = t >= q0 && t < q1 ? lo : -1;
   r.pos = static_cast<int64_t>(__ldg(bt.lens + lo)) - (q1 - t);
   return r;

@@ -93,6 +93,14 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const AppendAr
   const int tid = threadIdx.x;
   const int freq = tid & (kFreqs - 1), half = a.rot >> 1;
   pdl_wait();
+  // Lengths outside the cache are recorded, of sequences without new tokens as
+  // well (the first warp, whose loads the block waits for, has no part in it).
+  if (tid >= 32)
+    for (int64_t b = static_cast<int64_t>(blockIdx.x) * (kThreads - 32) + tid - 32; b < a.bt.B;
+         b += static_cast<int64_t>(gridDim.x) * (kThreads - 32)) {
+      const int len = __ldg(a.bt.lens + b);
+      if (len < 0 || len > a.n_cap) record_error(a.err, kErrBadPage);
+    }
   uint64_t F = 0;
   if (freq < half) {
     const double turns = static_cast<double>(__ldg(a.inv_freq + freq)) * 0.15915494309189533577;

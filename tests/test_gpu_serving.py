@@ -276,6 +276,48 @@ def test_append_skips_what_lies_outside():
     assert bool((q_out[7:] == CANARY).all()) and not bool((q_out[:7] == CANARY).all())
 
 
+def test_append_and_attention_read_one_batch_alike():
+    # cu_q reaches behind the T = 7 tokens: sequence 1 has the four that are there
+    Hq, Hkv, P, T = 8, 2, 64, 7
+    lens = [10, 20]
+    pages = Pages(lens, Hkv, P, 2, seed=6)
+    q, k, v = (rand((T, H, 128), s).cuda() for H, s in ((Hq, 5), (Hkv, 6), (Hkv, 8)))
+    inv = freqs(128).cuda()
+    got = []
+    for cu in ([0, 3, 7], [0, 3, 12]):
+        K, V, table = pages.cuda()
+        q_rot, out = torch.zeros_like(q), torch.zeros_like(q)
+        c, ln = batch_tensors(cu, lens)
+        qasc.kv_rope_append_paged(q, k, v, q_rot, K, V, table, ln, inv, cu_q=c)
+        ws = qasc.alloc_workspace(qasc.kv_window_attn_workspace_bytes(T, 2, Hq, Hkv, 2 * P))
+        qasc.kv_window_attn_paged(q_rot, K, V, table, ln, out, ws, local=100, cu_q=c)
+        qasc.qasc_device_error()
+        got.append([x.view(torch.int16) for x in (K, V, q_rot, out)])
+    assert torch.equal(V[int(pages.table[1, 0]), :, 16:20], v[3:].transpose(0, 1))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("B,bad", [(3, 2), (600, 599), (600, 0)])
+@pytest.mark.parametrize("length", [-1, 129])
+def test_append_reports_lengths_of_sequences_without_tokens(B, bad, length):
+    # as the attention calls do; the others are written all the same
+    Hkv, P = 2, 64
+    K = torch.zeros((2, Hkv, P, 128), dtype=torch.bfloat16, device="cuda")
+    V = torch.zeros_like(K)
+    k, v = rand((1, Hkv, 128), 2).cuda(), rand((1, Hkv, 128), 3).cuda()
+    table = torch.tensor([[0, 1]] * B, dtype=torch.int32, device="cuda")
+    c, ln = batch_tensors([0, 0, 1] + [1] * (B - 2), [5] * B)
+    qasc.kv_rope_append_paged(None, k, v, None, K, V, table, ln, None, cu_q=c)
+    qasc.qasc_device_error()
+    ln[bad] = length
+    V.zero_()
+    qasc.kv_rope_append_paged(None, k, v, None, K, V, table, ln, None, cu_q=c)
+    with pytest.raises(qasc.QascError) as e:
+        qasc.qasc_device_error()
+    assert e.value.status == 6
+    assert torch.equal(V[0, :, 4], v[0]) and not bool(V[0, :, 5:].any())
+
+
 # --------------------------------------------------------------------- window
 WINDOW = [
     # Hq, Hkv, P, q_lens, lens, sink, local
