@@ -589,6 +589,12 @@ def _attn(name, q, K, V, block_table, kv_lens, out, workspace, cu_q, lse, stream
          batch, *behind, qp, Kp, Vp, op, lp, wp, ws_bytes)
 
 
+def _tokens32(n):
+    """A number of tokens in the library's 32 bits, to which ctypes cuts without
+    an error: a cache holds fewer than 2^24, so that any more mean the same."""
+    return n if -0x80000000 <= n < 0x80000000 else (0x7fffffff if n > 0 else -1)
+
+
 def kv_window_attn_workspace_bytes(T, B, Hq, Hkv, n_cap):
     return _sized(_L().kv_window_attn_workspace_bytes(ctypes.byref(make_shape(B, Hq, Hkv, n_cap, n_cap)), T))
 
@@ -598,7 +604,8 @@ def kv_window_attn(q, K, V, kv_lens, out, workspace, *, local, sink=4, cu_q=None
     and the newest `local` cached tokens of its sequence up to its own
     position; q, out [T, Hq, d] bf16, K, V [B, Hkv, n_cap, d], the batch as
     for kv_rope_append."""
-    _attn("kv_window_attn", q, K, V, None, kv_lens, out, workspace, cu_q, lse, stream, (), (sink, local))
+    _attn("kv_window_attn", q, K, V, None, kv_lens, out, workspace, cu_q, lse, stream, (),
+          (_tokens32(sink), _tokens32(local)))
 
 
 def kv_window_attn_paged(q, K_pool, V_pool, block_table, kv_lens, out, workspace, *, local, sink=4, cu_q=None,
@@ -606,7 +613,7 @@ def kv_window_attn_paged(q, K_pool, V_pool, block_table, kv_lens, out, workspace
     """kv_window_attn over a paged pool [num_pages, Hkv, P, d]."""
     _table(block_table)
     _attn("kv_window_attn_paged", q, K_pool, V_pool, block_table, kv_lens, out, workspace, cu_q, lse, stream, (),
-          (sink, local))
+          (_tokens32(sink), _tokens32(local)))
 
 
 def kv_prefix_attn_workspace_bytes(T, B, Hq, Hkv, n_cap):
@@ -683,8 +690,8 @@ def qasc_selftest_attn_wait(limit_us, stall, q, K, V, kv_lens, out, workspace, *
     on, with waits that give up after limit_us: the next qasc_device_error()
     reports the timeout and out and lse are undefined."""
     call = _L().qasc_selftest_attn_wait
-    _attn("qasc_selftest_attn_wait", q, K, V, None, kv_lens, out, workspace, cu_q, lse, stream, (), (sink, local),
-          fn=lambda *args: call(int(limit_us), int(stall), *args))
+    _attn("qasc_selftest_attn_wait", q, K, V, None, kv_lens, out, workspace, cu_q, lse, stream, (),
+          (_tokens32(sink), _tokens32(local)), fn=lambda *args: call(int(limit_us), int(stall), *args))
 
 
 def qasc_version():

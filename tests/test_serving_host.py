@@ -267,6 +267,22 @@ def test_tensors_on_the_host_are_rejected(monkeypatch):
         qasc._at([1, 2], "out", bf, (2,), 0)
 
 
+@pytest.mark.parametrize("given,sent", [(0, 0), (4, 4), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                                        (2 ** 32 + 5, 2 ** 31 - 1), (2 ** 63, 2 ** 31 - 1), (-3, -3), (-2 ** 40, -1)])
+def test_sink_and_local_beyond_32_bits_keep_their_meaning(lib, monkeypatch, given, sent):
+    # the library takes 32 bits, to which ctypes cuts without a word: 2^32 + 5 would be 5
+    calls = []
+    monkeypatch.setattr(qasc, "_run", lambda fn, dev, stream, shape, cache, *args: calls.append(args))
+    args = (t(2, 8, 128), t(2, 2, 64, 128), t(2, 2, 64, 128), t(2, dtype=i32), t(2, 8, 128), t(256, dtype=u8))
+    qasc.kv_window_attn(*args, local=given, sink=given)
+    args = (t(2, 8, 128), t(9, 2, 64, 128), t(9, 2, 64, 128), t(2, 3, dtype=i32), t(2, dtype=i32), t(2, 8, 128),
+            t(256, dtype=u8))
+    qasc.kv_window_attn_paged(*args, local=given, sink=given)
+    for sink, local in (c[1:3] for c in calls):
+        assert sink == local == sent and ctypes.c_int32(sink).value == sink
+    assert len(calls) == 2
+
+
 def test_packed_descriptors_equal_the_structures():
     big = 1 << 40
     assert _lib.pack_shape(3, 8, 2, 128, 32, 0, big, big + 1) == bytes(_lib.qasc_shape(3, 8, 2, 128, 32, 0, big, big + 1))
