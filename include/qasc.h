@@ -403,9 +403,11 @@ QASC_API qasc_status kv_rope_append_paged(const qasc_shape* shape, const qasc_pa
  *   workspace, ws_bytes >= kv_window_attn_workspace_bytes(shape, tokens)
  * sink >= 0, local >= 1, B <= 2048 (more: QASC_ERR_UNSUPPORTED).  A token with
  * A(t) empty (its position is negative: more new tokens than cached ones) gives
- * out 0 and lse -inf.  Cache rows that none of a sequence's queries attends to
- * may hold anything, NaN and infinities included; V rows that some attend to
- * are taken as finite (a NaN in one may reach its sequence's other queries).  A
+ * out 0 and lse -inf, and so does one all of whose logits are -inf.  Cache rows
+ * that none of a sequence's queries attends to may hold anything, NaN and
+ * infinities included; V rows that some attend to are taken as finite (a NaN in
+ * one reaches its value of the queries that attend to it, and may reach the same
+ * value of its sequence's other queries, in that KV head).  A
  * block-table entry is read only for pages that hold an attended token.  How the
  * work is shared between blocks is chosen from T, B, the heads, local, n_prefix
  * and n_cap, the bound on the lengths that the host knows (a table with fewer

@@ -276,6 +276,72 @@ def test_append_skips_what_lies_outside():
     assert bool((q_out[7:] == CANARY).all()) and not bool((q_out[:7] == CANARY).all())
 
 
+@pytest.mark.parametrize("ql", [[1, 1, 1], [300, 2, 400]])
+def test_append_replays_in_a_graph(ql):
+    # the replay follows cu_q, the lengths and the positions on the device
+    Hq, Hkv, P, B, T = 8, 2, 64, len(ql), sum(ql)
+    lens = [m + 70 * (b + 1) for b, m in enumerate(ql)]
+    table = torch.randperm(3 * B * 4, generator=torch.Generator().manual_seed(8)).view(B, -1).to(torch.int32).cuda()
+    q, k, v = rand((T, Hq + 2 * Hkv, 128), 9).cuda().split([Hq, Hkv, Hkv], dim=1)
+    inv, pos = freqs(128).cuda(), torch.arange(T, dtype=torch.int32, device="cuda")
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    c, ln = batch_tensors(None if T == B else cu, lens)
+
+    def fresh():
+        K = torch.zeros((table.numel(), Hkv, P, 128), dtype=torch.bfloat16, device="cuda")
+        return K, K.clone(), torch.zeros((T, Hq, 128), dtype=torch.bfloat16, device="cuda")
+
+    def call(K, V, q_out):
+        qasc.kv_rope_append_paged(q, k, v, q_out, K, V, table, ln, inv, cu_q=c, positions=pos)
+
+    def same(a, b):
+        return all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(a, b))
+    a, b, g_out = fresh(), fresh(), fresh()
+    call(*a)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        call(*g_out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert same(a, g_out)
+    ln.copy_(torch.tensor([x - 33 for x in lens], dtype=torch.int32))
+    pos.add_(1000)
+    if c is not None:
+        c.copy_(torch.tensor([0, 5, 290, T - 3], dtype=torch.int32))
+        ln[1] = 300
+    for x in g_out:
+        x.zero_()
+    graph.replay()
+    call(*b)
+    torch.cuda.synchronize()
+    qasc.qasc_device_error()
+    assert same(b, g_out) and not same(a, b)
+
+
+def test_two_appends_on_two_streams():
+    Hq, Hkv, P, T = 8, 2, 64, 600
+    q, k, v = rand((T, Hq + 2 * Hkv, 128), 9).cuda().split([Hq, Hkv, Hkv], dim=1)
+    table = torch.arange(10, dtype=torch.int32, device="cuda")[None].contiguous()
+    inv = freqs(128).cuda()
+    c, ln = batch_tensors([0, T], [T + 9])
+    pools = [[torch.zeros((10, Hkv, P, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)] +
+             [torch.zeros((T, Hq, 128), dtype=torch.bfloat16, device="cuda")] for _ in range(3)]
+
+    def call(K, V, q_out, stream=None):
+        qasc.kv_rope_append_paged(q, k, v, q_out, K, V, table, ln, inv, cu_q=c, stream=stream)
+    call(*pools[2])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for pool, s in zip(pools, streams):
+            call(*pool, stream=s)
+    torch.cuda.synchronize()
+    qasc.qasc_device_error()
+    for pool in pools[:2]:
+        assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(pool, pools[2]))
+
+
 def test_append_and_attention_read_one_batch_alike():
     # cu_q reaches behind the T = 7 tokens: sequence 1 has the four that are there
     Hq, Hkv, P, T = 8, 2, 64, 7
@@ -504,6 +570,50 @@ def test_window_not_a_number_stays_visible(n, m):
     assert bool((bad[:, 4:] == hit[:, None]).all()) and not bool(bad[:, :4].any())
 
 
+@pytest.mark.parametrize("n,m", [(1900, 1), (900, 200), (9000, 1)])
+def test_window_not_a_number_in_a_value(n, m):
+    # it reaches its column of the queries that attend to it; no other column, KV head or lse
+    Hq, Hkv, P, local = 8, 2, 64, 300 if n < 9000 else 9000
+    pages = Pages([n], Hkv, P, cdiv(n, P), seed=95)
+    j = n - 50
+    pages.V[int(pages.table[0, j // P]), 1, j % P, 5] = float("nan")
+    q = rand((m, Hq, 128), 96)
+    out, lse = window(q, pages, [0, m], [n], 4, local, Hkv)
+    pos = torch.arange(n - m, n)
+    hit = ((pos >= j) & (pos - local < j)).cuda()
+    bad = torch.isnan(out)
+    assert bool(bad[hit][:, 4:, 5].all())
+    bad[:, 4:, 5] = False
+    assert not bool(bad.any()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("n,m", [(1, 1), (1900, 1), (900, 200), (9000, 1)])
+def test_window_logits_of_minus_infinity(n, m):
+    # a row that has no others counts as one that attends to nothing; one that has any is untouched
+    Hq, Hkv, P, local = 8, 2, 64, 300 if n < 9000 else 9000
+    pages = Pages([n], Hkv, P, cdiv(n, P), seed=97)
+    for i in range(cdiv(n, P)):
+        page = int(pages.table[0, i])
+        pages.K[page, 1, :, 5] = float("-inf")                                 # every key of KV head 1
+        pages.K[page, 0, ::3, 5] = float("-inf")                               # every third of KV head 0, by page
+        for t in range(i * P, min(n, i * P + P)):
+            pages.logical[0][0][:, t] = pages.K[page, :, t % P]
+    q = rand((m, Hq, 128), 98)
+    q[..., 5] = 1.0
+    out, lse = window(q, pages, [0, m], [n], 4, local, Hkv)
+    assert bool((out[:, 4:] == 0).all()) and bool(torch.isneginf(lse[:, 4:]).all())
+    if n == 1:
+        return
+    # KV head 0: the keys at -inf leave the sums
+    k, v = pages.caches()
+    finite = np.isfinite(k[0][0, :, 5])
+    for t in sorted({0, m // 2, m - 1}):
+        p = n - m + t
+        seen = [j for j in range(p + 1) if finite[j] and (j < 4 or j > p - local)]
+        one = osv.window_attention(f64(q[t:t + 1, :4]), [k[0][:1, seen]], [v[0][:1, seen]], [0, 1], [len(seen)], 0, n)
+        check_rows(out[t:t + 1, :4], lse[t:t + 1, :4], one, n)
+
+
 # Caches long enough that an item's keys are shared between blocks (the shares'
 # borders fall inside items, key tiles of either parity and of the sink).
 LONG = [
@@ -524,6 +634,40 @@ def test_window_shared_between_blocks(Hq, Hkv, ql, lens, sink, local):
     some = sorted({0, cu[-1] - 1, *(c for c in cu if c < cu[-1]), *(c - 1 for c in cu if c), *range(0, cu[-1], 17)})
     ref = osv.window_attention(f64(q), *pages.caches(), cu, lens, sink, local, tokens=some)
     out, lse = window(q, pages, None if ql == [1] * len(ql) else cu, lens, sink, local, Hkv)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    check_rows(out, lse, ref, max(lens), rows=some)
+
+
+def contiguous(pages, n_cap):
+    """The same caches as [B, Hkv, n_cap, 128], NaN behind each sequence."""
+    K = torch.full((len(pages.lens), pages.Hkv, n_cap, 128), float("nan"), dtype=torch.bfloat16)
+    V = K.clone()
+    for b, (k, v) in enumerate(pages.logical):
+        K[b, :, :k.shape[1]], V[b, :, :k.shape[1]] = k, v
+    return K.cuda(), V.cuda()
+
+
+# A contiguous cache whose sequences and heads begin anywhere: shared between
+# blocks, and with plans too large for a block's shared memory.
+@pytest.mark.parametrize("Hq,Hkv,ql,lens,sink,local", LONG + [
+    (8, 2, [1] * 400, [1 + (37 * b) % 300 for b in range(400)], 4, 2000),
+    (8, 2, [(7 * b) % 5 for b in range(500)], [5 + (53 * b) % 400 for b in range(500)], 4, 5000),
+])
+def test_window_contiguous_long_and_many(Hq, Hkv, ql, lens, sink, local):
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    T, B, n_cap = cu[-1], len(ql), max(lens) + 5
+    pages = Pages(lens, Hkv, 64, cdiv(max(lens), 64), seed=89)
+    K, V = contiguous(pages, n_cap)
+    q = rand((T, Hq, 128), 90)
+    some = sorted({0, T - 1, *range(0, T, 17 if T < 400 else 41)})
+    ref = osv.window_attention(f64(q), *pages.caches(), cu, lens, sink, local, tokens=some)
+    out = torch.full((T, Hq, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, Hq), float("nan"), dtype=torch.float32, device="cuda")
+    ws = qasc.alloc_workspace(qasc.kv_window_attn_workspace_bytes(T, B, Hq, Hkv, n_cap))
+    ws.fill_(255)
+    c, ln = batch_tensors(None if ql == [1] * B else cu, lens)
+    qasc.kv_window_attn(q.cuda(), K, V, ln, out, ws, sink=sink, local=local, cu_q=c, lse=lse)
+    qasc.qasc_device_error()
     assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
     check_rows(out, lse, ref, max(lens), rows=some)
 
