@@ -343,7 +343,8 @@ QASC_API qasc_status ts_ring_flush(const qasc_shape* shape, const qasc_paged_cac
  * outside is recorded as QASC_ERR_BAD_TABLE.  With such a length the attention
  * calls clamp it, and the append leaves out the tokens that it places outside the
  * cache.
- * The shape's n is not used (pass n_cap); tokens * Hq < 2^31.
+ * The shape's n is not used (pass n_cap).  tokens * Hq < 2^31, n_cap < 2^24 and
+ * B * Hkv * n_cap < 2^31, of a paged cache too, whose n_cap is the table's width.
  * ------------------------------------------------------------------------- */
 typedef struct {
   const int32_t* cu_q;   /* device [B + 1]; NULL: one new token per sequence (tokens == B) */
@@ -398,7 +399,9 @@ QASC_API qasc_status kv_rope_append_paged(const qasc_shape* shape, const qasc_pa
  *
  *   q      [T, Hq, d]   bf16
  *   out    [T, Hq, d]   bf16, written (rounded once; the probabilities of the
- *                       second product are bf16 too, sums and statistics fp32)
+ *                       second product are bf16 too, sums and statistics fp32;
+ *                       ts_sparse_attn keeps 2^-17 of them and writes fp32); not
+ *                       to overlap q
  *   lse    [T, Hq]      fp32, written if non-NULL
  *   workspace, ws_bytes >= kv_window_attn_workspace_bytes(shape, tokens)
  * sink >= 0, local >= 1, B <= 2048 (more: QASC_ERR_UNSUPPORTED).  A token with

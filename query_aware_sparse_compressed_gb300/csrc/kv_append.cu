@@ -17,8 +17,8 @@
 // are slow; F_i is computed once per thread and the products are integer.)
 //
 // Bound: bytes.  Every value is read and written once, (Hq + 2 Hkv) 256 bytes
-// each way per token.  32768 tokens of 64 + 8 + 8 heads (1.34 GB): 203 us, 6.63
-// TB/s, 99 % of a plain copy's rate.  What that took: a thread keeps the angles
+// each way per token.  32768 tokens of 64 + 8 + 8 heads (1.34 GB): 201 us, 6.68
+// TB/s, a plain copy's rate.  What that took: a thread keeps the angles
 // of its 16 values in registers over all heads of its slice (no division, no
 // shared-memory reads per head), has two heads in flight, and four blocks of
 // 256 threads share an SM (five or six spill: 234, 296 us; one head in flight:

@@ -22,9 +22,12 @@
 // values, so lse is as exact as fp32.
 //
 // Work.  Two schedules, chosen by the numbers of rows and tiles (attn_schedule):
-//   whole  many items, or short ones: CTA c takes items c, c + G, ... whole,
-//          heaviest first (items of 128 rows where those of 256 are few, and
-//          those in twos where there are several to an SM).
+//   whole  many items, or short ones: each CTA takes one of every round of G
+//          items whole, from the batch's end to its beginning (a sequence's last
+//          query tiles attend to the most keys; different sequences are not
+//          weighed against each other), every other round in reverse (items of
+//          128 rows where those of 256 are few, and those in twos where there are
+//          several to an SM).
 //   split  few items: the tiles of all items are laid end to end and every CTA
 //          takes an equal range of that line; an item that several CTAs share
 //          leaves partial (max, sum, O) rows in the workspace and kv_merge_kernel
@@ -60,19 +63,22 @@
 // two query tiles takes 2048 cycles at their full rate and 3100 to 3300 here:
 // what is left are the waits between softmax and products (a row's softmax takes
 // 1100 cycles to its first half, 1500 to its second, and each group's products
-// 1024).  Measured: 8192 causal tokens, 64 heads: 660 us, 1670 TFLOP/s (87 % of
-// cuBLAS's burst rate); 32768 tokens, 32 heads, a window of 4096: 1260 to 1330
-// us, 1550 to 1635 TFLOP/s of useful products (3 % more are computed at the
-// window's edges).  ncu (4096 tokens): tensor pipe 63 % of its active peak, special functions 32 %,
-// issue 42 %, DRAM 7 %.
-// Decode: HBM.  64 sequences, a window of 4096, 8 KV heads (0.99 GB): 152 us, 6.5
-// TB/s (97 % of a copy's rate); one sequence of 131072 tokens (0.54 GB): 86 us.
+// 1024).  Measured among others of its kind, the power cap active: 8192 causal
+// tokens, 64 heads: 715 to 765 us, 1440 to 1540 TFLOP/s (75 to 80 % of cuBLAS's burst
+// rate, 84 to 89 % of its sustained one); 32768 tokens, 32 heads, a window of
+// 4096: 1370 to 1400 us, 1480 to 1510 TFLOP/s of useful products (3 % more are
+// computed at the window's edges).  The comparisons beside the code were timed
+// in short runs, in which the first of these takes 660 to 680 us.  ncu (4096
+// tokens): tensor pipe 63 % of its active peak, special functions 32 %, issue 42
+// %, DRAM 7 %.
+// Decode: HBM.  64 sequences, a window of 4096, 8 KV heads (0.99 GB): 149 to 154 us,
+// 6.5 TB/s (97 % of a copy's rate); one sequence of 131072 tokens (0.54 GB): 87 us.
 // ncu: 382 MB read where 373 are needed.
 // Few tokens: latency.  4 sequences' 260 tokens: 8.9 us on the GPU: the
 // first item takes 1.1, its first key 1.7, a tile 0.7 to 1.4 (and a plan, where
 // one is needed, 0.6).  16 ragged sequences of 1 to 64 tokens, up to 1400 cached: 16 us with items of 128
 // rows, joined in the block; with 256-row items and a join by the merge 30.
-// A shared prefix: 128 sequences over 131072 tokens, 32 heads: 230 us.
+// A shared prefix: 128 sequences over 131072 tokens, 32 heads: 252 to 268 us.
 #include <cuda.h>
 
 #include <algorithm>
@@ -363,7 +369,11 @@ __device__ __forceinline__ void check_lens(const Args& p, int first, int step) {
 }
 
 // The plan in shared memory, by a warp or a block: ent_base [NS + 1] and line
-// [entries + 1].  `publish`: the copies in global memory (for the merge, and
+// [entries + 1].  Places are counted in 32 bits: an item has at most 2 n_cap / 128
+// + 6 of its own tiles, and with B Hkv n_cap < 2^31 and n_cap < 2^24, which every
+// call checks, the last items of the sequences have below 2^26 together, all
+// others of a split (may_split) below 2^29; those of a prefix have below 2^29 +
+// 2^25 with T Hq n_prefix < 2^43, which its call checks.  `publish`: the copies in global memory (for the merge, and
 // for a batch whose plan the attention's CTAs cannot hold), and the check of
 // the lengths.
 template <bool kBlock>
