@@ -452,6 +452,109 @@ QASC_API qasc_status kv_prefix_attn_paged(const qasc_shape* shape, const qasc_pa
                                           uint16_t* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The 4-bit KV cache: the serving calls and sparse attention over a cache of
+ * 4.5 bits a value.  No counterpart on the source pages, which keep bf16; the
+ * batches, shapes and pools are those above.
+ *
+ * A head's row of d values is d / 2 bytes of codes and d / 16 scales:
+ *   value i = t * scale[i / 16] * code[i]
+ * code: a 4-bit float (bit 3 the sign, bits 0-2: 0 0.5 1 1.5 2 3 4 6), that of an
+ * even i in the low half of byte i / 2; scale: one e4m3 byte for 16 values; t: the
+ * cache's factor k_scale or v_scale, a power of two in [2^-32, 2^32], one for all
+ * calls on that cache.  It moves the range of the scales: with 1 a group of 16 is
+ * held best where its largest magnitude lies in [0.1, 2688].
+ *
+ * Quantising 16 values x, of bf16: a = max |x| / t, scale = e4m3(a / 6) (at most
+ * 448), code = e2m1(x / t / scale), both rounded to nearest, ties to even.  Larger
+ * magnitudes than 2688 t, infinities among them, become 2688 t; a group with a NaN
+ * reads back as NaN; one whose scale rounds to 0 (a <= 2^-10 * 6) as 0.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint8_t* K;      /* device [B, Hkv, n_cap, d / 2], or a pool's [num_pages, Hkv, P, d / 2] */
+  uint8_t* K_sf;   /* device [.., d / 16] e4m3 */
+  uint8_t* V;
+  uint8_t* V_sf;
+  float k_scale, v_scale;
+} qasc_kv4;
+
+/* kv4_rope_append — kv_rope_append into a 4-bit cache: the new tokens' keys
+ * (rotated) and values quantised, their queries rotated.
+ *
+ * Arguments, strides and refusals as for kv_rope_append.  What is quantised of a
+ * key is its rotation rounded to bf16, which is computed to 2^-40 here (the
+ * angles to their fp64 product's error), so that the cache does not depend on how
+ * a batch was cut; the queries as in kv_rope_append. */
+QASC_API qasc_status kv4_rope_append(const qasc_shape* shape, const qasc_batch* batch, const qasc_rope* rope,
+                                     const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                     const uint16_t* v, int64_t v_stride, uint16_t* q_out, const qasc_kv4* kv,
+                                     void* stream);
+QASC_API qasc_status kv4_rope_append_paged(const qasc_shape* shape, const qasc_paged_cache* cache,
+                                           const qasc_batch* batch, const qasc_rope* rope, const uint16_t* q,
+                                           int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                           int64_t v_stride, uint16_t* q_out, const qasc_kv4* kv_pool, void* stream);
+
+/* kv4_read — cached tokens back in bf16, exactly (a magnitude below bf16's
+ * smallest normal number aside): the newest cu_q[b + 1] - cu_q[b] tokens of
+ * sequence b, packed as the batch's new tokens are (cu_q of the lengths' sums: whole
+ * sequences).
+ *
+ *   K_out, V_out   [T, Hkv, d] bf16, written; value e of token t and head g at
+ *                  t * token_stride + g * head_stride + e (values, multiples of 8
+ *                  in [0, 2^32)), e.g. a bf16 cache [Hkv, n, d] of one sequence
+ * Tokens of no sequence are not written; one whose position lies outside the
+ * cache, or whose page lies outside the pool, neither, and is recorded as
+ * QASC_ERR_BAD_TABLE. */
+QASC_API qasc_status kv4_read(const qasc_shape* shape, const qasc_batch* batch, const qasc_kv4* kv, uint16_t* K_out,
+                              int64_t k_token_stride, int64_t k_head_stride, uint16_t* V_out, int64_t v_token_stride,
+                              int64_t v_head_stride, void* stream);
+QASC_API qasc_status kv4_read_paged(const qasc_shape* shape, const qasc_paged_cache* cache, const qasc_batch* batch,
+                                    const qasc_kv4* kv_pool, uint16_t* K_out, int64_t k_token_stride,
+                                    int64_t k_head_stride, uint16_t* V_out, int64_t v_token_stride,
+                                    int64_t v_head_stride, void* stream);
+
+/* kv4_window_attn — kv_window_attn over a 4-bit cache.
+ *
+ *   max_q  the most new tokens of any sequence, or any larger number up to
+ *          tokens (without cu_q: not used).  It chooses how the work is done;
+ *          a sequence of more tokens is computed all the same.
+ *   workspace, ws_bytes >= kv4_window_attn_workspace_bytes(shape, tokens, max_q,
+ *          sink, local)
+ *   other arguments, refusals and rows without a token as for kv_window_attn; out
+ *   is rounded once from fp32, the probabilities of the second product hold 11
+ *   bits or more.  A block-table entry outside the pool stands for rows of zeros
+ *   and is recorded as QASC_ERR_BAD_TABLE. */
+QASC_API size_t kv4_window_attn_workspace_bytes(const qasc_shape* shape, int64_t tokens, int64_t max_q, int32_t sink,
+                                                int32_t local);
+QASC_API qasc_status kv4_window_attn(const qasc_shape* shape, const qasc_batch* batch, int64_t max_q, int32_t sink,
+                                     int32_t local, const uint16_t* q, const qasc_kv4* kv, uint16_t* out, float* lse,
+                                     void* workspace, size_t ws_bytes, void* stream);
+QASC_API qasc_status kv4_window_attn_paged(const qasc_shape* shape, const qasc_paged_cache* cache,
+                                           const qasc_batch* batch, int64_t max_q, int32_t sink, int32_t local,
+                                           const uint16_t* q, const qasc_kv4* kv_pool, uint16_t* out, float* lse,
+                                           void* workspace, size_t ws_bytes, void* stream);
+
+/* kv4_sparse_attn — the decode step's attention (ts_sparse_attn_ex) over a 4-bit
+ * cache of n tokens in every sequence: sink, listed and local tokens.
+ *
+ *   q        [B, Hq, d] bf16;  out [B, Hq, d] bf16, written (rounded once; not to
+ *            overlap q);  lse [B, Hq] fp32, written if non-NULL
+ *   sel, sel_len, sel_per_kv_head   as for ts_sparse_attn_ex, in any order; an
+ *            entry in use outside [0, n) stands for a row of zeros and is recorded as
+ *            QASC_ERR_BAD_TABLE
+ *   workspace, ws_bytes >= kv4_sparse_attn_workspace_bytes(shape, params)
+ * A row without any token gives out 0 and lse -inf.  B <= 2048 (more:
+ * QASC_ERR_UNSUPPORTED). */
+QASC_API size_t kv4_sparse_attn_workspace_bytes(const qasc_shape* shape, const qasc_ts_params* params);
+QASC_API qasc_status kv4_sparse_attn(const qasc_shape* shape, const qasc_ts_params* params, const uint16_t* q,
+                                     const qasc_kv4* kv, const int32_t* sel, const int32_t* sel_len,
+                                     int32_t sel_per_kv_head, uint16_t* out, float* lse, void* workspace,
+                                     size_t ws_bytes, void* stream);
+QASC_API qasc_status kv4_sparse_attn_paged(const qasc_shape* shape, const qasc_ts_params* params,
+                                           const qasc_paged_cache* cache, const uint16_t* q, const qasc_kv4* kv_pool,
+                                           const int32_t* sel, const int32_t* sel_len, int32_t sel_per_kv_head,
+                                           uint16_t* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * ts_dense_attn — full attention over all n cached tokens: the baseline the
  * TokenSelect page's speed table measures against ([TokenSelect] section
  * "速度性能": attention speed-up relative to full attention at 32K/64K/128K).

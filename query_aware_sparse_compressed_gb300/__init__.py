@@ -17,12 +17,17 @@ Entry points keep the C names:
   kv_rope_append, kv_rope_append_paged,
   kv_window_attn_workspace_bytes, kv_window_attn, kv_window_attn_paged,
   kv_prefix_attn_workspace_bytes, kv_prefix_attn_paged,
+  KV4, alloc_kv4, kv4_rope_append, kv4_rope_append_paged, kv4_read,
+  kv4_read_paged, kv4_window_attn_workspace_bytes, kv4_window_attn,
+  kv4_window_attn_paged, kv4_sparse_attn_workspace_bytes, kv4_sparse_attn,
+  kv4_sparse_attn_paged,
   ts_dense_attn_workspace_bytes, ts_dense_attn, snapkv_workspace_bytes,
   snapkv_compress, qasc_status_string, qasc_last_error, qasc_last_cuda_error, qasc_device_error,
   qasc_selftest_bounded_wait, qasc_selftest_attn_wait, qasc_version.
 """
 
 import ctypes
+import typing
 
 import torch
 
@@ -520,13 +525,9 @@ def _run(fn, dev, stream, shape, cache, *args):
         _check(status)
 
 
-def _rope_append(name, q, k, v, q_out, K, V, block_table, kv_lens, inv_freq, cu_q, positions, interleaved, stream):
-    if not isinstance(k, _Tensor) or k.dim() != 3:
-        raise ValueError("k must be a [T, Hkv, %d] tensor" % D)
-    dev = k.get_device()
-    T, Hkv, _ = k.shape
-    batch, B = _batch(cu_q, kv_lens, T, dev)
-    cache, n_cap, Hkv, Kp, Vp = _cache(K, V, block_table, B, Hkv, dev)
+def _new_rows(q, k, v, q_out, T, Hkv, inv_freq, positions, interleaved, dev):
+    """An append's queries, keys and values: Hq, the library's arguments for them,
+    and the rotation's descriptor."""
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
     Hq, qp, qs, op = Hkv, None, 0, None
@@ -543,9 +544,19 @@ def _rope_append(name, q, k, v, q_out, K, V, block_table, kv_lens, inv_freq, cu_
         _dims(inv_freq, "inv_freq", (None,))
         rot, fp = 2 * inv_freq.shape[0], _at(inv_freq, "inv_freq", _F32, inv_freq.shape, dev)
     pp = 0 if positions is None else _at(positions, "positions", _I32, (T,), dev)
-    rope = _lib.pack_rope(fp, pp, rot, 1 if interleaved else 0)
+    return Hq, (qp, qs, kp, ks, vp, vs, op), _lib.pack_rope(fp, pp, rot, 1 if interleaved else 0)
+
+
+def _rope_append(name, q, k, v, q_out, K, V, block_table, kv_lens, inv_freq, cu_q, positions, interleaved, stream):
+    if not isinstance(k, _Tensor) or k.dim() != 3:
+        raise ValueError("k must be a [T, Hkv, %d] tensor" % D)
+    dev = k.get_device()
+    T, Hkv, _ = k.shape
+    batch, B = _batch(cu_q, kv_lens, T, dev)
+    cache, n_cap, Hkv, Kp, Vp = _cache(K, V, block_table, B, Hkv, dev)
+    Hq, rows, rope = _new_rows(q, k, v, q_out, T, Hkv, inv_freq, positions, interleaved, dev)
     _run(getattr(_L(), name), dev, stream, _lib.pack_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap), cache, batch, rope,
-         qp, qs, kp, ks, vp, vs, op, Kp, Vp)
+         *rows, Kp, Vp)
 
 
 def kv_rope_append(q, k, v, q_out, K, V, kv_lens, inv_freq, *, cu_q=None, positions=None, interleaved=False,
@@ -632,6 +643,201 @@ def kv_prefix_attn_paged(q, K_pool, V_pool, prefix_table, block_table, kv_lens, 
         pt = _at(prefix_table, "prefix_table", _I32, (-(-n_prefix // K_pool.shape[2]),), block_table.get_device())
     _attn("kv_prefix_attn_paged", q, K_pool, V_pool, block_table, kv_lens, out, workspace, cu_q, lse, stream,
           (pt, n_prefix), ())
+
+
+# ---------------------------------------------------------- the 4-bit cache
+class KV4(typing.NamedTuple):
+    """A 4-bit cache: codes K, V [B, Hkv, n_cap, 64] uint8 and scales K_sf, V_sf
+    [B, Hkv, n_cap, 8] float8_e4m3fn, or pools [num_pages, Hkv, P, ..] of them;
+    value i of a row = factor * scale[i // 16] * code[i], the codes 4-bit floats,
+    k_scale and v_scale the factors of keys and values (powers of two)."""
+    K: torch.Tensor
+    K_sf: torch.Tensor
+    V: torch.Tensor
+    V_sf: torch.Tensor
+    k_scale: float = 1.0
+    v_scale: float = 1.0
+
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def alloc_kv4(rows, Hkv, tokens, device=None, k_scale=1.0, v_scale=1.0):
+    """A cache of zeros: rows = B and tokens = n_cap, or the pages of a pool and
+    their tokens."""
+    codes, scales = (torch.zeros((2, rows, Hkv, tokens, w), dtype=torch.uint8, device=device or "cuda")
+                     for w in (D // 2, D // 16))
+    return KV4(codes[0], scales[0].view(_E4M3), codes[1], scales[1].view(_E4M3), k_scale, v_scale)
+
+
+def _cache4(kv, block_table, B, Hkv, dev):
+    """A KV4 [B, Hkv, n_cap, ..], or of pools under block_table [B, pages_per_seq]:
+    (descriptor of the pool or None, n_cap, Hkv, descriptor of the cache)."""
+    if not isinstance(kv, KV4):
+        raise TypeError("kv must be a KV4")
+    if not isinstance(kv.K, _Tensor) or kv.K.dim() != 4:
+        raise ValueError("kv.K must be a [%s, Hkv, tokens, %d] tensor" % ("B" if block_table is None else "num_pages", D // 2))
+    rows, heads, tokens, _ = shape = kv.K.shape
+    if shape[3] != D // 2 or (Hkv is not None and heads != Hkv) or (block_table is None and rows != B):
+        _dims(kv.K, "kv.K", (B if block_table is None else None, Hkv, None, D // 2))
+    if block_table is None:
+        cache, n_cap = None, tokens
+    else:
+        table = block_table.shape
+        if len(table) != 2 or table[0] != B:
+            _dims(block_table, "block_table", (B, None))
+        n_cap = table[1] * tokens
+        cache = _lib.pack_cache(_at(block_table, "block_table", _I32, table, dev), tokens, table[1], rows)
+    scales = (rows, heads, tokens, D // 16)
+    return cache, n_cap, heads, _lib.pack_kv4(
+        _at(kv.K, "kv.K", _U8, shape, dev), _at(kv.K_sf, "kv.K_sf", _E4M3, scales, dev),
+        _at(kv.V, "kv.V", _U8, shape, dev), _at(kv.V_sf, "kv.V_sf", _E4M3, scales, dev), kv.k_scale, kv.v_scale)
+
+
+def _rope_append4(name, q, k, v, q_out, kv, block_table, kv_lens, inv_freq, cu_q, positions, interleaved, stream):
+    if not isinstance(k, _Tensor) or k.dim() != 3:
+        raise ValueError("k must be a [T, Hkv, %d] tensor" % D)
+    dev = k.get_device()
+    T, Hkv, _ = k.shape
+    batch, B = _batch(cu_q, kv_lens, T, dev)
+    cache, n_cap, Hkv, kvp = _cache4(kv, block_table, B, Hkv, dev)
+    Hq, rows, rope = _new_rows(q, k, v, q_out, T, Hkv, inv_freq, positions, interleaved, dev)
+    _run(getattr(_L(), name), dev, stream, _lib.pack_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap), cache, batch, rope,
+         *rows, kvp)
+
+
+def kv4_rope_append(q, k, v, q_out, kv, kv_lens, inv_freq, *, cu_q=None, positions=None, interleaved=False, stream=None):
+    """kv_rope_append into a 4-bit cache kv (KV4): new tokens' keys (rotated) and
+    values quantised, their rotated queries into q_out."""
+    _rope_append4("kv4_rope_append", q, k, v, q_out, kv, None, kv_lens, inv_freq, cu_q, positions, interleaved, stream)
+
+
+def kv4_rope_append_paged(q, k, v, q_out, kv_pool, block_table, kv_lens, inv_freq, *, cu_q=None, positions=None,
+                          interleaved=False, stream=None):
+    """kv4_rope_append into pools (a KV4 of [num_pages, Hkv, P, ..])."""
+    _table(block_table)
+    _rope_append4("kv4_rope_append_paged", q, k, v, q_out, kv_pool, block_table, kv_lens, inv_freq, cu_q, positions,
+                  interleaved, stream)
+
+
+def _strided_rows(t, name, T, Hkv, dev):
+    """A [T, Hkv, d] output whose tokens and heads may lie apart: its address and the
+    values between tokens and between heads."""
+    if not isinstance(t, _Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.shape != (T, Hkv, D):
+        _dims(t, name, (T, Hkv, D))
+    st = t.stride()
+    if T > 0 and st[2] != 1:
+        raise ValueError("%s must be contiguous within a head, got strides %s" % (name, st))
+    # rows that share memory would be written by several threads
+    a, b = sorted(((st[0], T), (st[1], Hkv)))
+    if (a[1] > 1 and a[0] < D) or (b[1] > 1 and b[0] < D + (a[1] - 1) * a[0]):
+        raise ValueError("%s: rows overlap, got strides %s" % (name, st))
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        _on_device(t.get_device(), name)
+        _ptr(t[:0], name, _BF16)     # raises
+    return t.data_ptr(), st[0] if T > 1 else Hkv * D, st[1] if Hkv > 1 else D
+
+
+def _read4(name, kv, block_table, kv_lens, K_out, V_out, cu_q, stream):
+    if not isinstance(K_out, _Tensor) or K_out.dim() != 3:
+        raise ValueError("K_out must be a [T, Hkv, %d] tensor" % D)
+    dev = K_out.get_device()
+    T = K_out.shape[0]
+    batch, B = _batch(cu_q, kv_lens, T, dev)
+    cache, n_cap, Hkv, kvp = _cache4(kv, block_table, B, None, dev)
+    _run(getattr(_L(), name), dev, stream, _lib.pack_shape(B, Hkv, Hkv, D, D_IDX, 0, n_cap, n_cap), cache, batch, kvp,
+         *_strided_rows(K_out, "K_out", T, Hkv, dev), *_strided_rows(V_out, "V_out", T, Hkv, dev))
+
+
+def kv4_read(kv, kv_lens, K_out, V_out, *, cu_q=None, stream=None):
+    """The newest tokens of a 4-bit cache back in bf16: K_out, V_out [T, Hkv, d],
+    packed as new tokens are (cu_q; whole sequences with the sums of kv_lens).
+    Their tokens and heads may lie apart (e.g. cache[0].transpose(0, 1))."""
+    _read4("kv4_read", kv, None, kv_lens, K_out, V_out, cu_q, stream)
+
+
+def kv4_read_paged(kv_pool, block_table, kv_lens, K_out, V_out, *, cu_q=None, stream=None):
+    """kv4_read from pools (a KV4 of [num_pages, Hkv, P, ..])."""
+    _table(block_table)
+    _read4("kv4_read_paged", kv_pool, block_table, kv_lens, K_out, V_out, cu_q, stream)
+
+
+def kv4_window_attn_workspace_bytes(T, B, Hq, Hkv, n_cap, *, local, sink=4, max_q=None):
+    return _sized(_L().kv4_window_attn_workspace_bytes(ctypes.byref(make_shape(B, Hq, Hkv, n_cap, n_cap)), T,
+                                                       T if max_q is None else max_q, _tokens32(sink), _tokens32(local)))
+
+
+def _queries(q):
+    if not isinstance(q, _Tensor) or q.dim() != 3 or q.shape[2] != D:
+        raise ValueError("q must have shape (T, Hq, %d)" % D)
+    return q.shape[0], q.shape[1], q.get_device()
+
+
+def _outputs(q, out, lse, workspace, dev):
+    """Addresses of the queries, and the arguments that end every attention call."""
+    ws_bytes = workspace.numel()
+    return _at(q, "q", _BF16, q.shape, dev), (
+        _at(out, "out", _BF16, q.shape, dev), None if lse is None else _at(lse, "lse", _F32, q.shape[:2], dev),
+        _at(workspace, "workspace", _U8, (ws_bytes,), dev), ws_bytes)
+
+
+def _window4(name, q, kv, block_table, kv_lens, out, workspace, local, sink, cu_q, max_q, lse, stream):
+    T, Hq, dev = _queries(q)
+    batch, B = _batch(cu_q, kv_lens, T, dev)
+    cache, n_cap, Hkv, kvp = _cache4(kv, block_table, B, None, dev)
+    qp, outputs = _outputs(q, out, lse, workspace, dev)
+    _run(getattr(_L(), name), dev, stream, _lib.pack_shape(B, Hq, Hkv, D, D_IDX, 0, n_cap, n_cap), cache, batch,
+         T if max_q is None else max_q, _tokens32(sink), _tokens32(local), qp, kvp, *outputs)
+
+
+def kv4_window_attn(q, kv, kv_lens, out, workspace, *, local, sink=4, cu_q=None, max_q=None, lse=None, stream=None):
+    """kv_window_attn over a 4-bit cache kv (KV4); max_q: the most new tokens of any
+    sequence where the caller knows it (None: T)."""
+    _window4("kv4_window_attn", q, kv, None, kv_lens, out, workspace, local, sink, cu_q, max_q, lse, stream)
+
+
+def kv4_window_attn_paged(q, kv_pool, block_table, kv_lens, out, workspace, *, local, sink=4, cu_q=None, max_q=None,
+                          lse=None, stream=None):
+    """kv4_window_attn over pools (a KV4 of [num_pages, Hkv, P, ..])."""
+    _table(block_table)
+    _window4("kv4_window_attn_paged", q, kv_pool, block_table, kv_lens, out, workspace, local, sink, cu_q, max_q, lse,
+             stream)
+
+
+def kv4_sparse_attn_workspace_bytes(B, Hq, Hkv, n, n_cap, K, sink=4, local=256):
+    shape, params = make_shape(B, Hq, Hkv, n, n_cap), ts_params(K, sink, local, 1)
+    return _sized(_L().kv4_sparse_attn_workspace_bytes(ctypes.byref(shape), ctypes.byref(params)))
+
+
+def _sparse4(name, q, kv, block_table, sel, out, workspace, n, sink, local, lengths, per_kv_head, lse, stream):
+    B, Hq, dev = _queries(q)
+    cache, n_cap, Hkv, kvp = _cache4(kv, block_table, B, None, dev)
+    qp, outputs = _outputs(q, out, lse, workspace, dev)
+    lists = (B, Hkv) if per_kv_head else (B,)
+    K = sel.shape[-1] if sel is not None else 0
+    sp = _at(sel, "sel", _I32, lists + (K,), dev) if K else None
+    up = None if lengths is None else _at(lengths, "lengths", _I32, lists, dev)
+    params = _lib.pack_params(K, sink, local, 1)
+    _run(getattr(_L(), name), dev, stream, _lib.pack_shape(B, Hq, Hkv, D, D_IDX, 0, n, n_cap), None,
+         *((params,) if cache is None else (params, cache)), qp, kvp, sp, up, 1 if per_kv_head else 0, *outputs)
+
+
+def kv4_sparse_attn(q, kv, sel, out, workspace, *, n, sink=4, local=256, lengths=None, per_kv_head=False, lse=None,
+                    stream=None):
+    """out[b, h] = attention over the sink, listed and local tokens of a 4-bit cache kv
+    (KV4) of n tokens: sel [B, K] or (per_kv_head) [B, Hkv, K] with lengths [B] or
+    [B, Hkv], as for ts_sparse_attn_ex; q, out [B, Hq, d] bf16."""
+    _sparse4("kv4_sparse_attn", q, kv, None, sel, out, workspace, n, sink, local, lengths, per_kv_head, lse, stream)
+
+
+def kv4_sparse_attn_paged(q, kv_pool, block_table, sel, out, workspace, *, n, sink=4, local=256, lengths=None,
+                          per_kv_head=False, lse=None, stream=None):
+    """kv4_sparse_attn over pools (a KV4 of [num_pages, Hkv, P, ..])."""
+    _table(block_table)
+    _sparse4("kv4_sparse_attn_paged", q, kv_pool, block_table, sel, out, workspace, n, sink, local, lengths,
+             per_kv_head, lse, stream)
 
 
 # ------------------------------------------------------------------ SnapKV

@@ -46,12 +46,19 @@ class qasc_rope(ctypes.Structure):
                 ("interleaved", ctypes.c_int32)]
 
 
+class qasc_kv4(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("K_sf", ctypes.c_void_p), ("V", ctypes.c_void_p), ("V_sf", ctypes.c_void_p),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
 # The descriptors of the packed-batch calls as bytes, which a void pointer
 # argument takes (0.1 us each; a ctypes structure and its byref 0.5).
 pack_shape = struct.Struct("@6i2q").pack
 pack_cache = struct.Struct("@P2iq").pack
 pack_batch = struct.Struct("@2Pq").pack
 pack_rope = struct.Struct("@2P2i").pack
+pack_kv4 = struct.Struct("@4P2f").pack
+pack_params = struct.Struct("@4i").pack
 
 _P = ctypes.c_void_p
 _SP = ctypes.POINTER(qasc_shape)
@@ -92,6 +99,16 @@ SIGNATURES = {
     "kv_window_attn_paged": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "kv_prefix_attn_workspace_bytes": (ctypes.c_size_t, [_SP, _I64]),
     "kv_prefix_attn_paged": (ctypes.c_int, [_P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv4_rope_append": (ctypes.c_int, [_P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P]),
+    "kv4_rope_append_paged": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P]),
+    "kv4_read": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _P]),
+    "kv4_read_paged": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _P]),
+    "kv4_window_attn_workspace_bytes": (ctypes.c_size_t, [_SP, _I64, _I64, _I32, _I32]),
+    "kv4_window_attn": (ctypes.c_int, [_P, _P, _I64, _I32, _I32, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv4_window_attn_paged": (ctypes.c_int, [_P, _P, _P, _I64, _I32, _I32, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv4_sparse_attn_workspace_bytes": (ctypes.c_size_t, [_SP, _TP]),
+    "kv4_sparse_attn": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv4_sparse_attn_paged": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _P, ctypes.c_size_t, _P]),
     "ts_dense_attn_workspace_bytes": (ctypes.c_size_t, [_SP]),
     "ts_dense_attn": (ctypes.c_int, [_SP, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "snapkv_workspace_bytes": (ctypes.c_size_t, [_SP, _NP]),

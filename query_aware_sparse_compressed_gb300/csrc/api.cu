@@ -2,6 +2,7 @@
 // kernel launches.  See include/qasc.h for the contract of each call.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -192,6 +193,7 @@ const DeviceInfo* device_info() {
     if (configure_score_kernels(d) != cudaSuccess || configure_select_kernels(d) != cudaSuccess ||
         configure_head_select_kernels(d) != cudaSuccess || configure_group_kernels(d) != cudaSuccess ||
         configure_expand_kernels(d) != cudaSuccess || configure_kv_attn_kernels(d) != cudaSuccess ||
+        configure_kv4_kernels(d) != cudaSuccess ||
         configure_attn_kernels(d) != cudaSuccess || configure_snapkv_kernels(d) != cudaSuccess)
       return nullptr;
     ready[dev] = true;
@@ -574,13 +576,7 @@ qasc_status check_stride(int64_t stride, const char* what, const char* fn) {
   return QASC_OK;
 }
 
-qasc_status rope_append_call(const char* fn, const qasc_shape* shape, const qasc::PageMap& pm, const qasc_batch* batch,
-                             const qasc_rope* rope, const uint16_t* q, int64_t q_stride, const uint16_t* k,
-                             int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* q_out, uint16_t* K,
-                             uint16_t* V, void* stream) {
-  QASC_RANGE(fn);
-  qasc::Batch bt;
-  QASC_CHECK(check_batch(shape, batch, fn, &bt));
+qasc_status check_rope(const qasc_shape* shape, const qasc_rope* rope, const char* fn, qasc::RopeArgs* r) {
   if (!rope) return fail(QASC_ERR_INVALID_ARG, "%s: rope is NULL", fn);
   if (rope->rot_dim < 0 || rope->rot_dim > shape->d || rope->rot_dim % 16 != 0)
     return fail(QASC_ERR_INVALID_ARG, "%s: rot_dim=%d must be a multiple of 16 in [0, %d]", fn, rope->rot_dim,
@@ -588,12 +584,16 @@ qasc_status rope_append_call(const char* fn, const qasc_shape* shape, const qasc
   const float* inv_freq = rope->inv_freq;
   if (rope->rot_dim > 0) QASC_REQUIRE_PTR(inv_freq, 4, fn);
   if (!aligned(rope->positions, 4)) return fail(QASC_ERR_INVALID_ARG, "%s: positions is not 4-byte aligned", fn);
-  QASC_CHECK(check_stride(q_stride, "q_stride", fn));
-  QASC_CHECK(check_stride(k_stride, "k_stride", fn));
-  QASC_CHECK(check_stride(v_stride, "v_stride", fn));
-  QASC_REQUIRE_PTR(K, 16, fn);
-  QASC_REQUIRE_PTR(V, 16, fn);
-  if (bt.T == 0) return ok();
+  r->inv_freq = inv_freq;
+  r->positions = rope->positions;
+  r->rot_dim = rope->rot_dim;
+  r->interleaved = rope->interleaved != 0;
+  return QASC_OK;
+}
+
+// The new tokens of an append that has any.
+qasc_status check_new_rows(const qasc_shape* shape, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                           const uint16_t* v, const uint16_t* q_out, const char* fn) {
   QASC_REQUIRE_PTR(k, 16, fn);
   QASC_REQUIRE_PTR(v, 16, fn);
   if (q) {
@@ -603,14 +603,28 @@ qasc_status rope_append_call(const char* fn, const qasc_shape* shape, const qasc
       return fail(QASC_ERR_INVALID_ARG, "%s: q_out may be q only when q is dense (q_stride=%lld)", fn,
                   static_cast<long long>(q_stride));
   }
+  return QASC_OK;
+}
+
+qasc_status rope_append_call(const char* fn, const qasc_shape* shape, const qasc::PageMap& pm, const qasc_batch* batch,
+                             const qasc_rope* rope, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                             int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* q_out, uint16_t* K,
+                             uint16_t* V, void* stream) {
+  QASC_RANGE(fn);
+  qasc::Batch bt;
+  QASC_CHECK(check_batch(shape, batch, fn, &bt));
+  qasc::RopeArgs r;
+  QASC_CHECK(check_rope(shape, rope, fn, &r));
+  QASC_CHECK(check_stride(q_stride, "q_stride", fn));
+  QASC_CHECK(check_stride(k_stride, "k_stride", fn));
+  QASC_CHECK(check_stride(v_stride, "v_stride", fn));
+  QASC_REQUIRE_PTR(K, 16, fn);
+  QASC_REQUIRE_PTR(V, 16, fn);
+  if (bt.T == 0) return ok();
+  QASC_CHECK(check_new_rows(shape, q, q_stride, k, v, q_out, fn));
   qasc_status st;
   const qasc::DeviceInfo* dev = need_device(fn, &st);
   if (!dev) return st;
-  qasc::RopeArgs r;
-  r.inv_freq = inv_freq;
-  r.positions = rope->positions;
-  r.rot_dim = rope->rot_dim;
-  r.interleaved = rope->interleaved != 0;
   const cudaError_t e = qasc::launch_rope_append(*shape, pm, bt, r, q, q_stride, k, k_stride, v, v_stride, q_out, K, V,
                                                  *dev, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
@@ -776,6 +790,252 @@ QASC_API qasc_status kv_prefix_attn_paged(const qasc_shape* shape, const qasc_pa
   a.pm_prefix.table = prefix_table;
   a.cache_rows = cache->num_pages * shape->Hkv * cache->page_tokens;
   return kv_attn_call(fn, shape, batch, a, true, q, K_pool, V_pool, out, lse, workspace, ws_bytes, stream);
+}
+
+// ------------------------------------------------------- the 4-bit cache
+namespace {
+// A power of two in [2^-32, 2^32].
+bool is_cache_factor(float f) {
+  int e = 0;
+  return f > 0.0f && std::frexp(f, &e) == 0.5f && e >= -31 && e <= 33;
+}
+
+qasc_status check_kv4(const qasc_kv4* kv, const char* fn, qasc::Kv4Cache* c) {
+  if (!kv) return fail(QASC_ERR_INVALID_ARG, "%s: kv is NULL", fn);
+  QASC_REQUIRE_PTR(kv->K, 16, fn);
+  QASC_REQUIRE_PTR(kv->K_sf, 16, fn);
+  QASC_REQUIRE_PTR(kv->V, 16, fn);
+  QASC_REQUIRE_PTR(kv->V_sf, 16, fn);
+  if (!is_cache_factor(kv->k_scale) || !is_cache_factor(kv->v_scale))
+    return fail(QASC_ERR_INVALID_ARG, "%s: k_scale=%g and v_scale=%g must be powers of two in [2^-32, 2^32]", fn,
+                static_cast<double>(kv->k_scale), static_cast<double>(kv->v_scale));
+  c->K = kv->K;
+  c->K_sf = kv->K_sf;
+  c->V = kv->V;
+  c->V_sf = kv->V_sf;
+  c->k_scale = kv->k_scale;
+  c->v_scale = kv->v_scale;
+  return QASC_OK;
+}
+
+qasc_status kv4_append_call(const char* fn, const qasc_shape* shape, const qasc::PageMap& pm, const qasc_batch* batch,
+                            const qasc_rope* rope, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                            int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* q_out, const qasc_kv4* kv,
+                            void* stream) {
+  QASC_RANGE(fn);
+  qasc::Batch bt;
+  qasc::RopeArgs r;
+  qasc::Kv4Cache c;
+  QASC_CHECK(check_batch(shape, batch, fn, &bt));
+  QASC_CHECK(check_rope(shape, rope, fn, &r));
+  QASC_CHECK(check_stride(q_stride, "q_stride", fn));
+  QASC_CHECK(check_stride(k_stride, "k_stride", fn));
+  QASC_CHECK(check_stride(v_stride, "v_stride", fn));
+  QASC_CHECK(check_kv4(kv, fn, &c));
+  if (bt.T == 0) return ok();
+  QASC_CHECK(check_new_rows(shape, q, q_stride, k, v, q_out, fn));
+  qasc_status st;
+  const qasc::DeviceInfo* dev = need_device(fn, &st);
+  if (!dev) return st;
+  const cudaError_t e = qasc::launch_kv4_append(*shape, pm, bt, r, q, q_stride, k, k_stride, v, v_stride, q_out, c, *dev,
+                                                static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+qasc_status kv4_read_call(const char* fn, const qasc_shape* shape, const qasc::PageMap& pm, const qasc_batch* batch,
+                          const qasc_kv4* kv, uint16_t* K_out, int64_t k_token_stride, int64_t k_head_stride,
+                          uint16_t* V_out, int64_t v_token_stride, int64_t v_head_stride, void* stream) {
+  QASC_RANGE(fn);
+  qasc::Batch bt;
+  qasc::Kv4Cache c;
+  QASC_CHECK(check_batch(shape, batch, fn, &bt));
+  QASC_CHECK(check_stride(k_token_stride, "k_token_stride", fn));
+  QASC_CHECK(check_stride(k_head_stride, "k_head_stride", fn));
+  QASC_CHECK(check_stride(v_token_stride, "v_token_stride", fn));
+  QASC_CHECK(check_stride(v_head_stride, "v_head_stride", fn));
+  QASC_CHECK(check_kv4(kv, fn, &c));
+  if (bt.T == 0) return ok();
+  QASC_REQUIRE_PTR(K_out, 16, fn);
+  QASC_REQUIRE_PTR(V_out, 16, fn);
+  qasc_status st;
+  const qasc::DeviceInfo* dev = need_device(fn, &st);
+  if (!dev) return st;
+  const cudaError_t e = qasc::launch_kv4_read(*shape, pm, bt, c, K_out, k_token_stride, k_head_stride, V_out,
+                                              v_token_stride, v_head_stride, *dev, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+qasc_status check_max_q(const qasc_shape* s, int64_t tokens, int64_t max_q, const char* fn) {
+  QASC_CHECK(check_tokens(s, tokens, fn));
+  if (max_q < 0 || max_q > tokens)
+    return fail(QASC_ERR_INVALID_ARG, "%s: max_q=%lld outside [0, tokens=%lld]", fn, static_cast<long long>(max_q),
+                static_cast<long long>(tokens));
+  return QASC_OK;
+}
+
+// The shape (and pool) are checked; a carries the operator's own parameters.
+qasc_status kv4_attn_call(const char* fn, const qasc_shape* shape, qasc::Kv4AttnArgs& a, const uint16_t* q,
+                          const qasc_kv4* kv, uint16_t* out, float* lse, void* workspace, size_t ws_bytes,
+                          void* stream) {
+  QASC_CHECK(check_kv4(kv, fn, &a.kv));
+  if (!aligned(lse, 4)) return fail(QASC_ERR_INVALID_ARG, "%s: lse is not 4-byte aligned", fn);
+  if (a.bt.T == 0) return ok();
+  QASC_REQUIRE_PTR(q, 16, fn);
+  QASC_REQUIRE_PTR(out, 16, fn);
+  const size_t need = qasc::kv4_attn_least_bytes();
+  if (!workspace || ws_bytes < need)
+    return fail(QASC_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need, workspace ? ws_bytes : size_t(0));
+  QASC_REQUIRE_PTR(workspace, 256, fn);
+  qasc_status st;
+  const qasc::DeviceInfo* dev = need_device(fn, &st);
+  if (!dev) return st;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  const int rc = qasc::launch_kv4_attn(*shape, a, static_cast<uint8_t*>(workspace), ws_bytes, *dev,
+                                       static_cast<cudaStream_t>(stream));
+  if (rc != 0) return cuda_fail(rc, fn);
+  return ok();
+}
+
+qasc_status kv4_window_call(const char* fn, const qasc_shape* shape, qasc::Kv4AttnArgs& a, const qasc_batch* batch,
+                            int64_t max_q, int32_t sink, int32_t local, const uint16_t* q, const qasc_kv4* kv,
+                            uint16_t* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  QASC_CHECK(check_window(sink, local, fn));
+  QASC_CHECK(check_attn_batch(shape, fn));
+  QASC_CHECK(check_batch(shape, batch, fn, &a.bt));
+  QASC_CHECK(check_max_q(shape, a.bt.T, max_q, fn));
+  a.sink = sink;
+  a.local = local;
+  a.max_q = a.bt.cu_q ? max_q : 1;
+  return kv4_attn_call(fn, shape, a, q, kv, out, lse, workspace, ws_bytes, stream);
+}
+
+qasc_status kv4_sparse_call(const char* fn, const qasc_shape* shape, const qasc_ts_params* params,
+                            qasc::Kv4AttnArgs& a, const uint16_t* q, const qasc_kv4* kv, const int32_t* sel,
+                            const int32_t* sel_len, int32_t sel_per_kv_head, uint16_t* out, float* lse, void* workspace,
+                            size_t ws_bytes, void* stream) {
+  QASC_CHECK(check_ts_params(shape, params, fn));
+  QASC_CHECK(check_attn_batch(shape, fn));
+  if (params->K > 0) QASC_REQUIRE_PTR(sel, 4, fn);
+  if (!aligned(sel_len, 4)) return fail(QASC_ERR_INVALID_ARG, "%s: sel_len is not 4-byte aligned", fn);
+  a.listed = true;
+  a.bt.T = a.bt.B = shape->B;
+  a.sink = params->sink;
+  a.local = params->local;
+  a.K = params->K;
+  a.sel = sel;
+  a.sel_len = params->K > 0 ? sel_len : nullptr;
+  a.sel_per_kv = sel_per_kv_head != 0;
+  return kv4_attn_call(fn, shape, a, q, kv, out, lse, workspace, ws_bytes, stream);
+}
+}  // namespace
+
+QASC_API qasc_status kv4_rope_append(const qasc_shape* shape, const qasc_batch* batch, const qasc_rope* rope,
+                                     const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                     const uint16_t* v, int64_t v_stride, uint16_t* q_out, const qasc_kv4* kv,
+                                     void* stream) {
+  static const char* fn = "kv4_rope_append";
+  QASC_CHECK(check_shape(shape, fn));
+  return kv4_append_call(fn, shape, qasc::PageMap(), batch, rope, q, q_stride, k, k_stride, v, v_stride, q_out, kv,
+                         stream);
+}
+
+QASC_API qasc_status kv4_rope_append_paged(const qasc_shape* shape, const qasc_paged_cache* cache,
+                                           const qasc_batch* batch, const qasc_rope* rope, const uint16_t* q,
+                                           int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                           int64_t v_stride, uint16_t* q_out, const qasc_kv4* kv_pool, void* stream) {
+  static const char* fn = "kv4_rope_append_paged";
+  qasc::PageMap pm;
+  QASC_CHECK(check_paged(shape, cache, fn, &pm));
+  return kv4_append_call(fn, shape, pm, batch, rope, q, q_stride, k, k_stride, v, v_stride, q_out, kv_pool, stream);
+}
+
+QASC_API qasc_status kv4_read(const qasc_shape* shape, const qasc_batch* batch, const qasc_kv4* kv, uint16_t* K_out,
+                              int64_t k_token_stride, int64_t k_head_stride, uint16_t* V_out, int64_t v_token_stride,
+                              int64_t v_head_stride, void* stream) {
+  static const char* fn = "kv4_read";
+  QASC_CHECK(check_shape(shape, fn));
+  return kv4_read_call(fn, shape, qasc::PageMap(), batch, kv, K_out, k_token_stride, k_head_stride, V_out,
+                       v_token_stride, v_head_stride, stream);
+}
+
+QASC_API qasc_status kv4_read_paged(const qasc_shape* shape, const qasc_paged_cache* cache, const qasc_batch* batch,
+                                    const qasc_kv4* kv_pool, uint16_t* K_out, int64_t k_token_stride,
+                                    int64_t k_head_stride, uint16_t* V_out, int64_t v_token_stride,
+                                    int64_t v_head_stride, void* stream) {
+  static const char* fn = "kv4_read_paged";
+  qasc::PageMap pm;
+  QASC_CHECK(check_paged(shape, cache, fn, &pm));
+  return kv4_read_call(fn, shape, pm, batch, kv_pool, K_out, k_token_stride, k_head_stride, V_out, v_token_stride,
+                       v_head_stride, stream);
+}
+
+QASC_API size_t kv4_window_attn_workspace_bytes(const qasc_shape* shape, int64_t tokens, int64_t max_q, int32_t sink,
+                                                int32_t local) {
+  static const char* fn = "kv4_window_attn_workspace_bytes";
+  QASC_SIZE_CHECK(check_shape(shape, fn));
+  QASC_SIZE_CHECK(check_attn_batch(shape, fn));
+  QASC_SIZE_CHECK(check_max_q(shape, tokens, max_q, fn));
+  QASC_SIZE_CHECK(check_window(sink, local, fn));
+  ok();
+  return qasc::kv4_window_workspace_bytes(*shape, tokens, max_q, sink, local);
+}
+
+QASC_API qasc_status kv4_window_attn(const qasc_shape* shape, const qasc_batch* batch, int64_t max_q, int32_t sink,
+                                     int32_t local, const uint16_t* q, const qasc_kv4* kv, uint16_t* out, float* lse,
+                                     void* workspace, size_t ws_bytes, void* stream) {
+  static const char* fn = "kv4_window_attn";
+  QASC_RANGE(fn);
+  qasc::Kv4AttnArgs a;
+  QASC_CHECK(check_shape(shape, fn));
+  return kv4_window_call(fn, shape, a, batch, max_q, sink, local, q, kv, out, lse, workspace, ws_bytes, stream);
+}
+
+QASC_API qasc_status kv4_window_attn_paged(const qasc_shape* shape, const qasc_paged_cache* cache,
+                                           const qasc_batch* batch, int64_t max_q, int32_t sink, int32_t local,
+                                           const uint16_t* q, const qasc_kv4* kv_pool, uint16_t* out, float* lse,
+                                           void* workspace, size_t ws_bytes, void* stream) {
+  static const char* fn = "kv4_window_attn_paged";
+  QASC_RANGE(fn);
+  qasc::Kv4AttnArgs a;
+  QASC_CHECK(check_paged(shape, cache, fn, &a.pm));
+  return kv4_window_call(fn, shape, a, batch, max_q, sink, local, q, kv_pool, out, lse, workspace, ws_bytes, stream);
+}
+
+QASC_API size_t kv4_sparse_attn_workspace_bytes(const qasc_shape* shape, const qasc_ts_params* params) {
+  static const char* fn = "kv4_sparse_attn_workspace_bytes";
+  QASC_SIZE_CHECK(check_shape(shape, fn));
+  QASC_SIZE_CHECK(check_ts_params(shape, params, fn));
+  QASC_SIZE_CHECK(check_attn_batch(shape, fn));
+  ok();
+  return qasc::kv4_attn_least_bytes();
+}
+
+QASC_API qasc_status kv4_sparse_attn(const qasc_shape* shape, const qasc_ts_params* params, const uint16_t* q,
+                                     const qasc_kv4* kv, const int32_t* sel, const int32_t* sel_len,
+                                     int32_t sel_per_kv_head, uint16_t* out, float* lse, void* workspace,
+                                     size_t ws_bytes, void* stream) {
+  static const char* fn = "kv4_sparse_attn";
+  QASC_RANGE(fn);
+  qasc::Kv4AttnArgs a;
+  QASC_CHECK(check_shape(shape, fn));
+  return kv4_sparse_call(fn, shape, params, a, q, kv, sel, sel_len, sel_per_kv_head, out, lse, workspace, ws_bytes,
+                         stream);
+}
+
+QASC_API qasc_status kv4_sparse_attn_paged(const qasc_shape* shape, const qasc_ts_params* params,
+                                           const qasc_paged_cache* cache, const uint16_t* q, const qasc_kv4* kv_pool,
+                                           const int32_t* sel, const int32_t* sel_len, int32_t sel_per_kv_head,
+                                           uint16_t* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  static const char* fn = "kv4_sparse_attn_paged";
+  QASC_RANGE(fn);
+  qasc::Kv4AttnArgs a;
+  QASC_CHECK(check_paged(shape, cache, fn, &a.pm));
+  return kv4_sparse_call(fn, shape, params, a, q, kv_pool, sel, sel_len, sel_per_kv_head, out, lse, workspace, ws_bytes,
+                         stream);
 }
 
 namespace {

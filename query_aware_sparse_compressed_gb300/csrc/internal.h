@@ -301,6 +301,51 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, size_t
                    cudaStream_t stream);
 cudaError_t configure_kv_attn_kernels(const DeviceInfo& dev);
 
+// A 4-bit cache (kv4.cuh): codes [B][Hkv][n_cap][64] or of a pool, scales
+// [..][8], and the factors of keys and values, powers of two.
+struct Kv4Cache {
+  uint8_t* K = nullptr;
+  uint8_t* K_sf = nullptr;
+  uint8_t* V = nullptr;
+  uint8_t* V_sf = nullptr;
+  float k_scale = 1.0f, v_scale = 1.0f;
+};
+
+// kv_rope_append's arguments, into a 4-bit cache.
+cudaError_t launch_kv4_append(const qasc_shape& s, const PageMap& pm, const Batch& bt, const RopeArgs& r,
+                              const uint16_t* q, int64_t qs, const uint16_t* k, int64_t ks, const uint16_t* v,
+                              int64_t vs, uint16_t* q_out, const Kv4Cache& kv, const DeviceInfo& dev,
+                              cudaStream_t stream);
+// The newest tokens of a batch (its new ones) from the cache in bf16; strides
+// of the outputs in values.
+cudaError_t launch_kv4_read(const qasc_shape& s, const PageMap& pm, const Batch& bt, const Kv4Cache& kv, uint16_t* K_out,
+                            int64_t k_token, int64_t k_head, uint16_t* V_out, int64_t v_token, int64_t v_head,
+                            const DeviceInfo& dev, cudaStream_t stream);
+
+// Attention over a 4-bit cache: a window call's batch, or one token of every
+// sequence over sink, listed and local tokens (listed: lists as in
+// launch_sparse_attn, shape.n tokens in every sequence).
+struct Kv4AttnArgs {
+  const uint16_t* q = nullptr;   // [T][Hq][d]
+  uint16_t* out = nullptr;       // [T][Hq][d] bf16
+  float* lse = nullptr;          // [T][Hq], optional
+  Kv4Cache kv;
+  Batch bt;
+  PageMap pm;
+  int32_t sink = 0, local = 0;
+  int64_t max_q = 1;             // most new tokens of a sequence, as the caller has them
+  bool listed = false;
+  const int32_t* sel = nullptr;
+  const int32_t* sel_len = nullptr;
+  int32_t K = 0;                 // entries of a list
+  bool sel_per_kv = false;
+};
+size_t kv4_attn_least_bytes();   // for the most SMs
+size_t kv4_window_workspace_bytes(const qasc_shape& s, int64_t T, int64_t max_q, int32_t sink, int32_t local);
+int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, size_t ws_bytes, const DeviceInfo& dev,
+                    cudaStream_t stream);
+cudaError_t configure_kv4_kernels(const DeviceInfo& dev);
+
 // Neighbour expansion: rows of K ascending candidates in, the ascending union
 // of their +-radius neighbourhoods within C out ([rows][cap], the first
 // len[row] entries in use, the rest repeating the last).

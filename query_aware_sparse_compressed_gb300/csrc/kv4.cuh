@@ -1,0 +1,85 @@
+// The 4-bit KV cache: what a row holds, and the conversions.
+//
+// A head's row of 128 values is 64 bytes of codes and 8 bytes of scales, in two
+// arrays: value i = t * scale[i / 16] * code[i], code a 4-bit float (sign, two
+// exponent bits, one mantissa bit: 0 0.5 1 1.5 2 3 4 6, the even i of a pair
+// in a byte's low half), scale an e4m3, t the cache's own factor, a power of
+// two.  4.5 bits a value.  A code has 2 significant bits and a scale 4, so that
+// scale * code is exact in bf16 and, with the factor below, in fp16.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace qasc {
+
+constexpr int kKv4Group = 16;                    // values of a scale
+constexpr int kKv4Groups = kD / kKv4Group;       // scales of a row, bytes
+constexpr int kKv4Codes = kD / 2;                // bytes of a row's codes
+
+// Scales are taken to fp16 times 2^-7: scale * code reaches 448 * 6 = 2688, and
+// its smallest step 2^-9 * 0.5 is 2^-17 then, a whole number of fp16's 2^-24.
+constexpr float kKv4HalfScale = 0.0078125f;
+
+// Two e4m3 of a word's low 16 bits -> fp16 pair times 2^-7 (exact).
+__device__ __forceinline__ __half2 kv4_scales(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  return __hmul2(*reinterpret_cast<__half2*>(&h), __half2half2(__ushort_as_half(0x2000)));   // 2^-7
+}
+
+// The four bytes of w, two codes each -> fp16 pairs (low code, high code).
+__device__ __forceinline__ void kv4_codes(uint32_t w, __half2 (&h)[4]) {
+  uint32_t r[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<__half2*>(&r[i]);
+}
+
+// Scale byte of a group whose largest magnitude is `a` (NaN where it holds one):
+// a / 6 rounded to e4m3, at most 448.
+__device__ __forceinline__ uint32_t kv4_scale_of(float a) {
+  uint16_t e;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.0f), "f"(__fdiv_rn(a, 6.0f)));
+  return e & 0xffu;
+}
+
+// What divides the values of a group with this scale byte; 0 for a scale of 0.
+__device__ __forceinline__ float kv4_divisor(uint32_t byte) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(byte)));
+  const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
+  return s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+}
+
+// x / scale rounded to 16 significant bits, from x times the rounded 1 / scale.
+// A border between two codes that a quotient of 8 bits (x) by 4 (scale) meets it
+// meets exactly, and otherwise it stays 2^-8 off, so that the product's error (2^-22) taken off
+// here leaves every comparison with a border, ties among them, as exact division has it.
+__device__ __forceinline__ float kv4_quotient(float x, float divisor) {
+  return __uint_as_float((__float_as_uint(__fmul_rn(x, divisor)) + 0x80u) & 0xffffff00u);
+}
+
+// Eight quotients -> eight codes, the first in the lowest bits.
+__device__ __forceinline__ uint32_t kv4_pack(const float (&q)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  return w;
+}
+
+}  // namespace qasc

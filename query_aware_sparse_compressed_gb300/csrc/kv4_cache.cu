@@ -1,0 +1,451 @@
+// kv4_rope_append and kv4_read: new tokens' keys and values into the 4-bit
+// cache (kv4.cuh), keys and queries rotated on the way, and cached rows back in
+// bf16.
+//
+// Append.  The rotation is kv_rope_append's (rounded once to bf16; values
+// behind rot_dim are copied), and what is quantised is its bf16 result:
+//   a = max |x| of 16 values,  scale = e4m3(a / 6),  code = e2m1(x / scale)
+// both rounded to nearest, ties to even.  Near the border between two codes
+// the smallest error of a rotated key moves its code by a step, so that its
+// rotation is computed to 2^-40 and then rounded: the cache does not depend on
+// how a batch was cut or where its angles were computed.  cos and sin of an angle come as
+// pairs (high, low part) from a table of 1024 points of the turn and the
+// series of the remainder r < 2^-8:
+//   cos(t + r) = C - (S sin r + C (1 - cos r)),  sin(t + r) = S + (C sin r - S (1 - cos r))
+// and the products' errors from fused multiply-adds (Dekker's and Knuth's exact
+// sums).  The queries take the high parts alone, with fp32's error.
+//
+// Read.  A thread takes 8 values of a row: 4 bytes of codes, one scale, 16
+// bytes out; scale * code is exact.
+//
+// Bound: bytes.
+#include "kv4.cuh"
+#include "internal.h"
+
+namespace qasc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTok = 4;       // tokens of an append block's tile
+constexpr int kFreqs = kD / 2;
+constexpr int kUnits = 8;        // threads of a head: 16 values each
+constexpr int kBatch = 2;        // heads whose loads a thread has in flight
+constexpr int kPoints = 256;     // of a quarter turn
+
+struct Points {
+  float4 at[kPoints];   // cos and sin of i / 1024 turn: high and low parts
+};
+constexpr double series_sin(double x) {
+  double t = x, s = x;
+  for (int k = 1; k < 14; ++k) {
+    t *= -x * x / ((2 * k) * (2 * k + 1));
+    s += t;
+  }
+  return s;
+}
+constexpr double series_cos(double x) {
+  double t = 1.0, s = 1.0;
+  for (int k = 1; k < 14; ++k) {
+    t *= -x * x / ((2 * k - 1) * (2 * k));
+    s += t;
+  }
+  return s;
+}
+constexpr Points make_points() {
+  Points p{};
+  for (int i = 0; i < kPoints; ++i) {
+    const double x = 6.283185307179586476925 * i / (4 * kPoints);
+    const double c = series_cos(x), s = series_sin(x);
+    p.at[i].x = static_cast<float>(c);
+    p.at[i].y = static_cast<float>(c - static_cast<double>(p.at[i].x));
+    p.at[i].z = static_cast<float>(s);
+    p.at[i].w = static_cast<float>(s - static_cast<double>(p.at[i].z));
+  }
+  return p;
+}
+__device__ constexpr Points g_points = make_points();
+
+struct Pair {
+  float h, l;
+};
+
+// h + l of a + b exactly (Knuth), and with a low part added, renormalised.
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float t = __fadd_rn(a, b), bb = __fadd_rn(t, -a);
+  return {t, __fadd_rn(__fadd_rn(a, -__fadd_rn(t, -bb)), __fadd_rn(b, -bb))};
+}
+__device__ __forceinline__ Pair add_low(Pair t, float low) {
+  const float l = __fadd_rn(t.l, low), h = __fadd_rn(t.h, l);
+  return {h, __fadd_rn(l, -__fadd_rn(h, -t.h))};
+}
+
+// cos and sin of `ang` / 2^64 turns, to 2^-41.
+__device__ __forceinline__ void turn_cos_sin(uint64_t ang, Pair& c, Pair& s) {
+  const uint64_t j = (ang + (1ull << 53)) >> 54;
+  const int64_t rem = static_cast<int64_t>(ang - (j << 54));       // [-2^53, 2^53)
+  const float4 p = __ldg(&g_points.at[j & (kPoints - 1)]);
+  Pair C{p.x, p.y}, S{p.z, p.w};
+  if (j & kPoints) {   // a quarter turn on: (cos, sin) = (-sin, cos)
+    const Pair t = C;
+    C = {-S.h, -S.l};
+    S = t;
+  }
+  if (j & (2 * kPoints)) {
+    C = {-C.h, -C.l};
+    S = {-S.h, -S.l};
+  }
+  // r = rem 2 pi / 2^64 as rh + rl, from 24 and 24 bits of rem
+  const float a = static_cast<float>(static_cast<int32_t>(rem >> 30));
+  const float b = static_cast<float>(static_cast<int32_t>((rem & 0x3fffffff) >> 6));
+  constexpr double unit = 6.283185307179586476925 / 17179869184.0;
+  constexpr float k1 = static_cast<float>(unit), k1l = static_cast<float>(unit - static_cast<double>(k1));
+  constexpr float k2 = static_cast<float>(unit / 16777216.0);
+  const float rh = __fmul_rn(a, k1);
+  const float rl = fmaf(a, k1, -rh) + (a * k1l + b * k2);
+  const float r2 = rh * rh;
+  const float sl = rl - rh * r2 * 0.16666667f;                     // sin r = rh + sl
+  const float v = 0.5f * r2 - r2 * r2 * 0.041666668f + rh * rl;    // 1 - cos r
+  const float pc = __fmul_rn(S.h, rh), ec = fmaf(S.h, rh, -pc);
+  c = add_low(two_sum(C.h, -pc), C.l - (ec + (S.h * sl + (S.l * rh + C.h * v))));
+  const float ps = __fmul_rn(C.h, rh), es = fmaf(C.h, rh, -ps);
+  s = add_low(two_sum(S.h, ps), S.l + (es + (C.h * sl + (C.l * rh - S.h * v))));
+}
+
+// a c + b s (or minus) rounded once to bf16, bits.  Where the high part stands
+// on the middle between two bf16 values, the low part decides.
+__device__ __forceinline__ uint32_t rotated_bf16(float a, Pair c, float b, Pair s) {
+  const float p1 = __fmul_rn(a, c.h), e1 = fmaf(a, c.h, -p1);
+  const float p2 = __fmul_rn(b, s.h), e2 = fmaf(b, s.h, -p2);
+  const Pair t = two_sum(p1, p2);
+  const Pair y = add_low(t, (e1 + e2) + (a * c.l + b * s.l));
+  uint32_t u = __float_as_uint(y.h);
+  if ((u & 0xffffu) == 0x8000u && y.l != 0.0f) u += (y.l > 0.0f) == !(u >> 31) ? 1u : 0xffffffffu;
+  if (!(fabsf(y.h) <= 3.402823466e38f)) u = __float_as_uint(t.h);   // infinities and NaN
+  return static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(u))));
+}
+
+struct AppendArgs {
+  const uint16_t* q;       // NULL: no queries
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t qs, ks, vs;      // values between tokens
+  uint16_t* q_out;
+  Kv4Cache kv;
+  float k_inv, v_inv;      // 1 / the cache's factors
+  const float* inv_freq;
+  const int32_t* positions;
+  int rot, interleaved;
+  PageMap pm;
+  Batch bt;
+  int Hq, Hkv;
+  int64_t n_cap;
+  int tok;                 // tokens per tile
+  unsigned* err;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+
+// Largest magnitude of eight bf16 values, as bits (those of a NaN are above all others).
+__device__ __forceinline__ uint32_t abs_max(const uint4& x) {
+  const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
+}
+
+__device__ __forceinline__ uint32_t codes_of(const uint4& x, float inv, float divisor) {
+  const uint32_t* w = &x.x;
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = bf2_to_f2(w[i]);
+    q[2 * i] = kv4_quotient(f.x * inv, divisor);
+    q[2 * i + 1] = kv4_quotient(f.y * inv, divisor);
+  }
+  return kv4_pack(q);
+}
+
+// A unit of a head is 16 values in two 16-byte chunks: both members of eight
+// pairs, or values that are only copied; unit u of a head uses the frequencies
+// 8u .. 8u + 7 in either pairing.
+__global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const AppendArgs a) {
+  __shared__ float4 turn[kMaxTok][kFreqs];   // cos and sin, high and low parts
+  __shared__ int64_t row0[kMaxTok];     // cache row of KV head 0, -1: not written
+  __shared__ int32_t rpos[kMaxTok];     // position that rotates
+  __shared__ int8_t live[kMaxTok];      // the token belongs to a sequence
+  const int tid = threadIdx.x;
+  const int freq = tid & (kFreqs - 1), half = a.rot >> 1;
+  pdl_wait();
+  // Lengths outside the cache are recorded, of sequences without new tokens as
+  // well (the first warp, whose loads the block waits for, has no part in it).
+  if (tid >= 32)
+    for (int64_t b = static_cast<int64_t>(blockIdx.x) * (kThreads - 32) + tid - 32; b < a.bt.B;
+         b += static_cast<int64_t>(gridDim.x) * (kThreads - 32)) {
+      const int len = __ldg(a.bt.lens + b);
+      if (len < 0 || len > a.n_cap) record_error(a.err, kErrBadPage);
+    }
+  uint64_t F = 0;   // of a turn per position, times 2^64
+  if (freq < half) {
+    const double turns = static_cast<double>(__ldg(a.inv_freq + freq)) * 0.15915494309189533577;
+    const double frac = turns - floor(turns);
+    F = frac < 1.0 ? __double2ull_rn(frac * 18446744073709551616.0) : 0;
+  }
+  const int64_t head_rows = a.pm.table ? (int64_t(1) << a.pm.page_shift) : a.n_cap;   // rows from head to head
+  const int nq = a.q ? a.Hq : 0, heads = nq + 2 * a.Hkv;
+  const int lane8 = tid & (kUnits - 1);
+  const unsigned unit_mask = 0xffu << (tid & 24);
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tok; t0 < a.bt.T; t0 += static_cast<int64_t>(gridDim.x) * a.tok) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(a.tok), a.bt.T - t0));
+    if (tid < n) {
+      const int64_t t = t0 + tid;
+      TokenAt at = token_of(a.bt, t);
+      live[tid] = at.b >= 0;
+      int64_t row = -1;
+      if (at.b >= 0) {
+        if (at.pos >= 0 && at.pos < a.n_cap) row = cache_row(a.pm, at.b, 0, a.Hkv, a.n_cap, at.pos);
+        if (row < 0) record_error(a.err, kErrBadPage);
+      }
+      row0[tid] = row;
+      rpos[tid] = a.positions ? __ldg(a.positions + t) : static_cast<int32_t>(at.pos);
+    }
+    __syncthreads();
+    for (int i = tid; i < n * kFreqs; i += kThreads) {   // i mod 64 = freq: the block is a multiple of 64
+      const int tk = i / kFreqs;
+      Pair c, s;
+      turn_cos_sin(F * static_cast<uint64_t>(static_cast<int64_t>(rpos[tk])), c, s);
+      turn[tk][freq] = make_float4(c.h, s.h, c.l, s.l);
+    }
+    __syncthreads();
+    const int u = lane8, tk = (tid / kUnits) & (a.tok - 1), slice = tid / (kUnits * a.tok);
+    const int step = kThreads / (kUnits * a.tok);
+    if (tk < n && live[tk]) {
+      const int64_t t = t0 + tk, row = row0[tk];
+      const int r16 = a.rot / 16;
+      const bool turns = u < r16;
+      // chunks of the unit in a rotated head and in a copied one
+      const int c0 = turns && !a.interleaved ? u : 2 * u, c1 = turns && !a.interleaved ? u + r16 : 2 * u + 1;
+      // the unit, and which of its chunks, that holds chunk c of a rotated head
+      auto unit_of = [&](int c) { return a.interleaved || c >= 2 * r16 ? c >> 1 : (c < r16 ? c : c - r16); };
+      auto second_of = [&](int c) { return a.interleaved || c >= 2 * r16 ? (c & 1) != 0 : c >= r16; };
+      for (int h0 = slice; h0 < heads; h0 += kBatch * step) {
+        uint4 x[kBatch], y[kBatch];
+        bool there[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int h = h0 + i * step;
+          there[i] = h < heads && (h < nq || row >= 0);
+          if (there[i]) {
+            const bool value = h >= nq + a.Hkv;
+            const uint16_t* src = h < nq ? a.q + t * a.qs + h * kD
+                                         : (value ? a.v + t * a.vs + (h - nq - a.Hkv) * kD : a.k + t * a.ks + (h - nq) * kD);
+            x[i] = *reinterpret_cast<const uint4*>(src + 8 * (value ? 2 * u : c0));
+            y[i] = *reinterpret_cast<const uint4*>(src + 8 * (value ? 2 * u + 1 : c1));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (!there[i]) continue;
+          const int h = h0 + i * step;
+          uint32_t* xa = &x[i].x;
+          uint32_t* ya = &y[i].x;
+          if (h < nq) {
+            if (turns) {
+              if (a.interleaved) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float4 p = turn[tk][8 * u + e], r = turn[tk][8 * u + 4 + e];
+                  const float2 f = bf2_to_f2(xa[e]), g = bf2_to_f2(ya[e]);
+                  xa[e] = pack_bf16(f.x * p.x - f.y * p.y, f.y * p.x + f.x * p.y);
+                  ya[e] = pack_bf16(g.x * r.x - g.y * r.y, g.y * r.x + g.x * r.y);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float4 p = turn[tk][8 * u + 2 * e], r = turn[tk][8 * u + 2 * e + 1];
+                  const float2 f = bf2_to_f2(xa[e]), g = bf2_to_f2(ya[e]);
+                  xa[e] = pack_bf16(f.x * p.x - g.x * p.y, f.y * r.x - g.y * r.y);
+                  ya[e] = pack_bf16(g.x * p.x + f.x * p.y, g.y * r.x + f.y * r.y);
+                }
+              }
+            }
+            uint16_t* dst = a.q_out + (t * a.Hq + h) * kD;
+            *reinterpret_cast<uint4*>(dst + 8 * c0) = x[i];
+            *reinterpret_cast<uint4*>(dst + 8 * c1) = y[i];
+            continue;
+          }
+          const bool value = h >= nq + a.Hkv;
+          if (turns && !value) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = bf2_to_f2(xa[e]), g = bf2_to_f2(ya[e]);
+              const float4 p = turn[tk][8 * u + (a.interleaved ? e : 2 * e)];
+              const float4 r = turn[tk][8 * u + (a.interleaved ? 4 + e : 2 * e + 1)];
+              const Pair pc{p.x, p.z}, ps{p.y, p.w}, pn{-p.y, -p.w}, rc{r.x, r.z}, rs{r.y, r.w}, rn{-r.y, -r.w};
+              if (a.interleaved) {
+                xa[e] = rotated_bf16(f.x, pc, f.y, pn) | rotated_bf16(f.y, pc, f.x, ps) << 16;
+                ya[e] = rotated_bf16(g.x, rc, g.y, rn) | rotated_bf16(g.y, rc, g.x, rs) << 16;
+              } else {
+                xa[e] = rotated_bf16(f.x, pc, g.x, pn) | rotated_bf16(f.y, rc, g.y, rn) << 16;
+                ya[e] = rotated_bf16(g.x, pc, f.x, ps) | rotated_bf16(g.y, rc, f.y, rs) << 16;
+              }
+            }
+          }
+          // Largest magnitudes of the groups that x and y lie in: each of them is half
+          // of a group, the other half being another thread's chunk, or its own.
+          const int cx = value ? 2 * u : c0, cy = value ? 2 * u + 1 : c1;
+          uint32_t mx = abs_max(x[i]), my = abs_max(y[i]);
+          if (value || a.interleaved) {
+            mx = my = max(mx, my);
+          } else {
+            const int px = cx ^ 1, py = cy ^ 1, base = tid & 24;
+            const uint32_t xx = __shfl_sync(unit_mask, mx, base + unit_of(px)), xy = __shfl_sync(unit_mask, my, base + unit_of(px));
+            const uint32_t yx = __shfl_sync(unit_mask, mx, base + unit_of(py)), yy = __shfl_sync(unit_mask, my, base + unit_of(py));
+            mx = max(mx, second_of(px) ? xy : xx);
+            my = max(my, second_of(py) ? yy : yx);
+          }
+          const float inv = value ? a.v_inv : a.k_inv;
+          const uint32_t sx = kv4_scale_of(__uint_as_float(mx << 16) * inv), sy = kv4_scale_of(__uint_as_float(my << 16) * inv);
+          const int64_t r = row + (value ? h - nq - a.Hkv : h - nq) * head_rows;
+          uint8_t* codes = (value ? a.kv.V : a.kv.K) + r * kKv4Codes;
+          *reinterpret_cast<uint32_t*>(codes + 4 * cx) = codes_of(x[i], inv, kv4_divisor(sx));
+          *reinterpret_cast<uint32_t*>(codes + 4 * cy) = codes_of(y[i], inv, kv4_divisor(sy));
+          // the row's eight scales, gathered from its eight threads
+          const uint64_t mine = static_cast<uint64_t>(sx) << (8 * (cx >> 1)) | static_cast<uint64_t>(sy) << (8 * (cy >> 1));
+          const uint32_t lo = __reduce_or_sync(unit_mask, static_cast<uint32_t>(mine));
+          const uint32_t hi = __reduce_or_sync(unit_mask, static_cast<uint32_t>(mine >> 32));
+          if (u == 0) *reinterpret_cast<uint2*>((value ? a.kv.V_sf : a.kv.K_sf) + r * kKv4Groups) = make_uint2(lo, hi);
+        }
+      }
+    }
+    __syncthreads();   // the next tile rewrites the angles
+  }
+  pdl_trigger();
+}
+
+constexpr int kReadTok = 16;     // tokens of a read block's tile
+constexpr int kRowLanes = 16;    // threads of a row: 8 values each
+
+struct ReadArgs {
+  Kv4Cache kv;
+  uint16_t* K_out;
+  uint16_t* V_out;
+  int64_t k_token, k_head, v_token, v_head;   // values between tokens and heads of the outputs
+  PageMap pm;
+  Batch bt;
+  int Hkv;
+  int64_t n_cap;
+  unsigned* err;
+};
+
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
+  __shared__ int64_t row0[kReadTok];
+  const int tid = threadIdx.x, c = tid & (kRowLanes - 1);
+  pdl_wait();
+  for (int64_t b = static_cast<int64_t>(blockIdx.x) * kThreads + tid; b < a.bt.B; b += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int len = __ldg(a.bt.lens + b);
+    if (len < 0 || len > a.n_cap) record_error(a.err, kErrBadPage);
+  }
+  const int64_t head_rows = a.pm.table ? (int64_t(1) << a.pm.page_shift) : a.n_cap;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kReadTok; t0 < a.bt.T; t0 += static_cast<int64_t>(gridDim.x) * kReadTok) {
+    __syncthreads();
+    if (tid < kReadTok) {
+      int64_t row = -1;
+      if (t0 + tid < a.bt.T) {
+        const TokenAt at = token_of(a.bt, t0 + tid);
+        if (at.b >= 0) {
+          if (at.pos >= 0 && at.pos < a.n_cap) row = cache_row(a.pm, at.b, 0, a.Hkv, a.n_cap, at.pos);
+          if (row < 0) record_error(a.err, kErrBadPage);
+        }
+      }
+      row0[tid] = row;
+    }
+    __syncthreads();
+    const int tk = tid / kRowLanes;   // rows of one pass: the tile's tokens, of one head
+    const int64_t row = row0[tk];
+    if (row < 0) continue;
+    const int64_t t = t0 + tk;
+#pragma unroll 4
+    for (int g = 0; g < a.Hkv; ++g) {
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const int64_t r = row + g * head_rows;
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>((side ? a.kv.V : a.kv.K) + r * kKv4Codes) + c);
+        const uint32_t sf = __ldg((side ? a.kv.V_sf : a.kv.K_sf) + r * kKv4Groups + (c >> 1));
+        const float f = (side ? a.kv.v_scale : a.kv.k_scale) / kKv4HalfScale;
+        const __half2 s = kv4_scales(sf * 0x101u);
+        __half2 h[4];
+        kv4_codes(w, h);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = __half22float2(__hmul2(h[i], s));
+          o[i] = pack_bf16(v.x * f, v.y * f);
+        }
+        uint16_t* dst = side ? a.V_out + t * a.v_token + g * a.v_head : a.K_out + t * a.k_token + g * a.k_head;
+        *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+  pdl_trigger();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_append(const qasc_shape& s, const PageMap& pm, const Batch& bt, const RopeArgs& r,
+                              const uint16_t* q, int64_t qs, const uint16_t* k, int64_t ks, const uint16_t* v,
+                              int64_t vs, uint16_t* q_out, const Kv4Cache& kv, const DeviceInfo& dev,
+                              cudaStream_t stream) {
+  AppendArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.qs = qs;
+  a.ks = ks;
+  a.vs = vs;
+  a.q_out = q_out;
+  a.kv = kv;
+  a.k_inv = 1.0f / kv.k_scale;
+  a.v_inv = 1.0f / kv.v_scale;
+  a.inv_freq = r.inv_freq;
+  a.positions = r.positions;
+  a.rot = r.rot_dim;
+  a.interleaved = r.interleaved;
+  a.pm = pm;
+  a.bt = bt;
+  a.Hq = s.Hq;
+  a.Hkv = s.Hkv;
+  a.n_cap = s.n_cap;
+  a.err = dev.err_word;
+  // Tiles of four tokens fill the block's 256 threads with angles; few tokens
+  // go one to a block, over more SMs.
+  a.tok = bt.T >= 4 * dev.num_sms ? kMaxTok : 1;
+  const int64_t tiles = (bt.T + a.tok - 1) / a.tok;
+  const int64_t most = static_cast<int64_t>(dev.num_sms) * 6;
+  return launch_dependent(kv4_append_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads), 0,
+                          stream, 1, a);
+}
+
+cudaError_t launch_kv4_read(const qasc_shape& s, const PageMap& pm, const Batch& bt, const Kv4Cache& kv, uint16_t* K_out,
+                            int64_t k_token, int64_t k_head, uint16_t* V_out, int64_t v_token, int64_t v_head,
+                            const DeviceInfo& dev, cudaStream_t stream) {
+  ReadArgs a;
+  a.kv = kv;
+  a.K_out = K_out;
+  a.V_out = V_out;
+  a.k_token = k_token;
+  a.k_head = k_head;
+  a.v_token = v_token;
+  a.v_head = v_head;
+  a.pm = pm;
+  a.bt = bt;
+  a.Hkv = s.Hkv;
+  a.n_cap = s.n_cap;
+  a.err = dev.err_word;
+  const int64_t tiles = (bt.T + kReadTok - 1) / kReadTok;
+  const int64_t most = static_cast<int64_t>(dev.num_sms) * 8;
+  return launch_dependent(kv4_read_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads), 0, stream,
+                          1, a);
+}
+
+}  // namespace qasc

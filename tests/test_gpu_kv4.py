@@ -1,0 +1,795 @@
+"""GPU parity of the 4-bit cache's calls (kv4_rope_append*, kv4_read*, kv4_window_attn*,
+kv4_sparse_attn*) against the fp64 oracle.
+
+Tolerances, fixed before the first run (A = sum_j p_j |V_j|, from the oracle):
+  codes, scales   equal: the oracle quantises the fp64 rotation rounded to bf16, which
+                  the kernel has to 2^-40
+  values read     equal
+  rotated query   2^-8 |y| (one rounding to bf16: half a step) + 2^-20 (|x_a| + |x_b|)
+  logit           e = 2^-17 max_j sum_e |q_e K_e| / sqrt(d) (128 fp32 additions of
+                  exact products, 128 2^-24 each relative to the sum of magnitudes)
+  output          2^-8 |out| (one rounding) + 2^-11 A (each fp16 probability: half a
+                  step is 2^-11 relative) + n 2^-35 max |V| (those below fp16's normal range:
+                  2^-25 absolute where the largest is 2^10)
+                  + 2 (e + 2^-18) A (a logit's error moves a weight and the sum)
+                  + (n 2^-24 + 2^-20) A (fp32 sums over n keys)
+  lse             e + n 2^-24 + 2^-20 + 2^-22 |lse|
+Rows of the cache that nothing attends to hold NaN scales, block-table entries that
+must not be read lie outside the pool, and outputs are canaries beforehand.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import kv4 as okv4
+from oracle import serving as osv
+from oracle import tokenselect as ots
+from oracle.bf16 import round_bf16
+
+pytestmark = pytest.mark.gpu
+
+qasc = pytest.importorskip("query_aware_sparse_compressed_gb300")
+POISON = -7
+CANARY = 77.0
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    qasc._lib.load()
+
+
+def rand(shape, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(torch.bfloat16)
+
+
+def f64(x):
+    return synth.to_f64(x)
+
+
+def cdiv(a, b):
+    return -(-a // b)
+
+
+def packed(x, t=1.0):
+    """Codes and scale bytes (CPU uint8 tensors) of fp64 rows, and their values."""
+    codes, sf = okv4.quantise(x, t)
+    return torch.from_numpy(codes), torch.from_numpy(sf), okv4.values(codes, sf, t)
+
+
+class Pages4:
+    """4-bit pools with the caches of several sequences: NaN scales everywhere else, and
+    a table whose unused entries lie outside the pool.  random: codes and scales drawn
+    at once (large caches)."""
+
+    def __init__(self, lens, Hkv, P, pps, seed, extra=3, t=(1.0, 1.0), kscale=1.0, random=False):
+        self.lens, self.Hkv, self.P, self.pps, self.t = list(lens), Hkv, P, pps, t
+        self.num_pages = sum(cdiv(n, P) for n in lens) + extra
+        order = torch.randperm(self.num_pages, generator=torch.Generator().manual_seed(seed)).tolist()
+        self.table = torch.full((len(lens), pps), POISON, dtype=torch.int32)
+        self.codes = torch.full((2, self.num_pages, Hkv, P, 64), 255, dtype=torch.uint8)
+        self.sf = torch.full((2, self.num_pages, Hkv, P, 8), 127, dtype=torch.uint8)
+        self.logical = []
+        for b, n in enumerate(lens):
+            held = []
+            for side in range(2):
+                if random:
+                    g = torch.Generator().manual_seed(seed + 10 * b + side)
+                    c = torch.randint(0, 256, (Hkv, n, 64), generator=g, dtype=torch.uint8)
+                    s = torch.randint(40, 56, (Hkv, n, 8), generator=g, dtype=torch.uint8)   # 0.25 .. 0.94
+                    v = None
+                else:
+                    x = f64(rand((Hkv, n, 128), seed + 10 * b + side + 1, kscale if side == 0 else 1.0))
+                    c, s, v = packed(x * t[side], t[side])
+                held.append((c, s, v))
+            for i in range(cdiv(n, P)):
+                page = order.pop()
+                self.table[b, i] = page
+                m = min(P, n - i * P)
+                for side, (c, s, _) in enumerate(held):
+                    self.codes[side, page, :, :m] = c[:, i * P:i * P + m]
+                    self.sf[side, page, :, :m] = s[:, i * P:i * P + m]
+            self.logical.append(held)
+
+    def hide(self, b, lo, hi):
+        """Rows [lo, hi) of sequence b get NaN scales; pages wholly inside them
+        leave the table."""
+        for t in range(lo, hi):
+            page = int(self.table[b, t // self.P])
+            if page >= 0:
+                self.sf[:, page, :, t % self.P] = 127
+        for i in range(cdiv(lo, self.P), hi // self.P):
+            self.table[b, i] = POISON
+
+    def cache(self):
+        c, s = self.codes.cuda(), self.sf.cuda().view(torch.float8_e4m3fn)
+        return qasc.KV4(c[0], s[0], c[1], s[1], *self.t)
+
+    def contiguous(self, n_cap):
+        B = len(self.lens)
+        codes = torch.full((2, B, self.Hkv, n_cap, 64), 255, dtype=torch.uint8)
+        sf = torch.full((2, B, self.Hkv, n_cap, 8), 127, dtype=torch.uint8)
+        for b, n in enumerate(self.lens):
+            for t in range(n):
+                page = int(self.table[b, t // self.P])
+                if page >= 0:
+                    codes[:, b, :, t] = self.codes[:, page, :, t % self.P]
+                    sf[:, b, :, t] = self.sf[:, page, :, t % self.P]
+        c, s = codes.cuda(), sf.cuda().view(torch.float8_e4m3fn)
+        return qasc.KV4(c[0], s[0], c[1], s[1], *self.t)
+
+    def values(self, side):
+        return [held[side][2] if held[side][2] is not None else
+                okv4.values(held[side][0].numpy(), held[side][1].numpy(), self.t[side]) for held in self.logical]
+
+
+def batch_tensors(cu, lens):
+    c = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    return c, torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def check_rows(out, lse, ref, n_keys, vmax, rows=None):
+    want, want_lse, A, zabs = ref
+    got, got_lse = f64(out), lse.cpu().numpy().astype(np.float64)
+    if rows is not None:
+        got, got_lse, want, want_lse, A, zabs = (x[rows] for x in (got, got_lse, want, want_lse, A, zabs))
+    e = 2.0 ** -17 * zabs
+    sums = n_keys * 2.0 ** -24 + 2.0 ** -20
+    tol = (2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * (e[..., None] + 2.0 ** -18) + sums) * A
+           + n_keys * 2.0 ** -35 * vmax + 1e-30)
+    bad = np.abs(got - want) / tol
+    assert np.all(np.isfinite(got)), "output not finite"
+    assert bad.max() <= 1.0, "output off by %.2f tolerances at %s" % (bad.max(), np.unravel_index(bad.argmax(), bad.shape))
+    empty = np.isneginf(want_lse)
+    assert np.array_equal(np.isneginf(got_lse), empty)
+    ltol = e + sums + 2.0 ** -22 * np.abs(np.where(empty, 0, want_lse))
+    ldiff = np.abs(np.where(empty, 0, got_lse) - np.where(empty, 0, want_lse))
+    assert np.all(ldiff <= ltol), "lse off by %.2f tolerances" % (ldiff / ltol).max()
+
+
+def outputs(T, Hq):
+    return (torch.full((T, Hq, 128), CANARY, dtype=torch.bfloat16, device="cuda"),
+            torch.full((T, Hq), CANARY, dtype=torch.float32, device="cuda"))
+
+
+def window_ws(T, B, Hq, Hkv, n_cap, local, sink=4, max_q=None):
+    ws = qasc.alloc_workspace(qasc.kv4_window_attn_workspace_bytes(T, B, Hq, Hkv, n_cap, local=local, sink=sink,
+                                                                   max_q=max_q))
+    ws.fill_(255)
+    return ws
+
+
+def window(q, pages, cu, lens, sink, local, max_q=None):
+    """kv4_window_attn_paged into canary outputs."""
+    T, Hq, _ = q.shape
+    out, lse = outputs(T, Hq)
+    ws = window_ws(T, len(lens), Hq, pages.Hkv, pages.pps * pages.P, local, sink, max_q)
+    c, ln = batch_tensors(cu, lens)
+    qasc.kv4_window_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), ln, out, ws, sink=sink, local=local, cu_q=c,
+                               max_q=max_q, lse=lse)
+    qasc.qasc_device_error()
+    return out, lse
+
+
+def vmax_of(pages):
+    return max(np.abs(v).max() if v.size else 0.0 for v in pages.values(1))
+
+
+# --------------------------------------------------------------------- append
+APPEND = [
+    # Hq, Hkv, P, new tokens, lens, rot, interleaved, override of positions, factors
+    (8, 2, 64, [1, 1, 1], [1, 64, 130], 128, False, False, (1.0, 1.0)),
+    (8, 2, 64, [70, 0, 3, 129], [70, 9, 67, 400], 64, True, False, (1.0, 0.25)),
+    (8, 8, 128, [33], [300], 128, True, False, (4.0, 2.0 ** -20)),
+    (16, 8, 64, [5, 6], [4000, 90], 48, False, True, (1.0, 1.0)),
+    (8, 1, 64, [40], [64], 16, False, False, (2.0 ** -9, 1.0)),
+    (64, 8, 256, [700], [700], 128, False, True, (1.0, 1.0)),
+    (4, 4, 64, [9, 2], [9, 2], 0, False, False, (1.0, 1.0)),
+    (8, 2, 64, [20], [25], 112, False, False, (1.0, 1.0)),
+    (8, 2, 64, [20], [25], 80, True, False, (1.0, 1.0)),
+]
+
+
+def special_rows(k, v):
+    """Groups whose quotients stand on the codes' borders, zeros of both signs, the ends
+    of the scales' range, infinities and NaN (in v; k where it is not rotated)."""
+    x = torch.tensor([12, -12, 0.5, 1.5, 2.5, 3.5, 5, 7, 10, -0.5, 1, -0.0, 3, 0, 6, 8])
+    v[0, 0, :16] = x.bfloat16()
+    v[0, 0, 16:32] = x.bfloat16() * 2.0 ** -9
+    v[0, 0, 32:48] = 0
+    v[0, 0, 48:64] = 6 * 2.0 ** -10
+    v[0, 0, 64:80] = 6.375                                 # its scale stands between two
+    v[0, -1, 80:96] = torch.tensor([float("inf"), -float("inf"), 3e38, -1.0] * 4).bfloat16()
+    v[0, -1, 96] = float("nan")
+    v[0, -1, 112:128] = torch.tensor([2800.0, -2800.0, 2688.0, 100.0] * 4).bfloat16()
+    k[-1, 0] *= 300
+
+
+@pytest.mark.parametrize("Hq,Hkv,P,ql,lens,rot,inter,override,t", APPEND)
+@pytest.mark.parametrize("paged", [True, False])
+def test_append(Hq, Hkv, P, ql, lens, rot, inter, override, t, paged):
+    T, B = sum(ql), len(ql)
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    single = ql == [1] * B
+    extra = 0 if single else 2                             # tokens of no sequence
+    qkv = rand((T + extra, Hq + 2 * Hkv, 128), 5)
+    q, k, v = qkv.split([Hq, Hkv, Hkv], dim=1)
+    special_rows(k, v)
+    k, v = k * t[0], v * t[1]
+    qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:] = k, v
+    f = (10000.0 ** (-torch.arange(rot // 2, dtype=torch.float64) / max(1, rot // 2))).float()
+    pos = torch.randint(0, 1 << 24, (T + extra,), generator=torch.Generator().manual_seed(6)).int() if override else None
+    seq, cpos = osv.positions(cu, lens, T)
+    rpos = cpos if pos is None else pos[:T].numpy()
+    krot = round_bf16(osv.rotate(f64(k[:T]), rpos, f.numpy(), inter))
+    qrot = osv.rotate(f64(q[:T]), rpos, f.numpy(), inter)
+    want = [okv4.quantise(krot, t[0]), okv4.quantise(f64(v[:T]), t[1])]
+
+    n_cap = cdiv(max(lens), P) * P + P
+    num_pages = B * n_cap // P + 2
+    rows = num_pages if paged else B
+    codes = torch.full((2, rows, Hkv, P if paged else n_cap, 64), 0x5a, dtype=torch.uint8)
+    sf = torch.full((2, rows, Hkv, P if paged else n_cap, 8), 0x11, dtype=torch.uint8)
+    table = torch.randperm(num_pages, generator=torch.Generator().manual_seed(8))[:B * n_cap // P].reshape(B, -1).int()
+    for b in range(B):                                     # pages that nothing is written to must not be read
+        first = max(0, lens[b] - ql[b]) // P
+        table[b, :first] = POISON
+        table[b, cdiv(lens[b], P) if ql[b] else 0:] = POISON
+    exp_codes, exp_sf = codes.numpy().copy(), sf.numpy().copy()
+    for i in range(T):
+        p = int(cpos[i])
+        at = (int(table[seq[i], p // P]), slice(None), p % P) if paged else (seq[i], slice(None), p)
+        for side in range(2):
+            exp_codes[side][at], exp_sf[side][at] = want[side][0][i], want[side][1][i]
+    dc, ds = codes.cuda(), sf.cuda()
+    kv = qasc.KV4(dc[0], ds[0].view(torch.float8_e4m3fn), dc[1], ds[1].view(torch.float8_e4m3fn), *t)
+    c, ln = batch_tensors(None if single else cu, lens)
+    d = qkv.cuda()
+    q_out = torch.full((T + extra, Hq, 128), CANARY, dtype=torch.bfloat16, device="cuda")
+    args = (d[:, :Hq], d[:, Hq:Hq + Hkv], d[:, Hq + Hkv:], q_out, kv)
+    kw = dict(cu_q=c, positions=None if pos is None else pos.cuda(), interleaved=inter)
+    freq = f.cuda() if rot else None
+    if paged:
+        qasc.kv4_rope_append_paged(*args, table.cuda(), ln, freq, **kw)
+    else:
+        qasc.kv4_rope_append(*args, ln, freq, **kw)
+    qasc.qasc_device_error()
+    got_codes, got_sf = dc.cpu().numpy(), ds.cpu().numpy()
+    assert np.array_equal(got_sf, exp_sf)
+    broken = np.repeat(exp_sf == 127, 8, axis=-1)          # a NaN group's codes may be any
+    assert np.array_equal(np.where(broken, 0, got_codes), np.where(broken, 0, exp_codes))
+    mag = np.zeros_like(qrot)
+    for i in range(rot // 2):
+        a, b = (2 * i, 2 * i + 1) if inter else (i, i + rot // 2)
+        mag[..., a] = mag[..., b] = np.abs(f64(q[:T]))[..., a] + np.abs(f64(q[:T]))[..., b]
+    assert np.all(np.abs(f64(q_out[:T]) - qrot) <= 2.0 ** -8 * np.abs(qrot) + 2.0 ** -20 * mag)
+    assert bool((q_out[T:] == CANARY).all())
+
+
+def test_append_of_a_long_prompt_is_exact():
+    """2048 tokens at far positions: 4 million rotated keys, each rounded as the fp64 rotation is."""
+    T, Hkv, P = 2048, 16, 64
+    k, v = rand((T, Hkv, 128), 9), rand((T, Hkv, 128), 10)
+    f = (500000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float()
+    pos = (torch.arange(T) * 61 + 3).int()
+    want = okv4.quantise(round_bf16(osv.rotate(f64(k), pos.numpy(), f.numpy(), False)))
+    kv = qasc.alloc_kv4(1, Hkv, T)
+    c, ln = batch_tensors([0, T], [T])
+    qasc.kv4_rope_append(None, k.cuda(), v.cuda(), None, kv, ln, f.cuda(), cu_q=c, positions=pos.cuda())
+    qasc.qasc_device_error()
+    assert np.array_equal(kv.K_sf.view(torch.uint8)[0].cpu().numpy().transpose(1, 0, 2), want[1])
+    assert np.array_equal(kv.K[0].cpu().numpy().transpose(1, 0, 2), want[0])
+
+
+def test_append_does_not_depend_on_the_cut():
+    """Token by token, in chunks and at once: the same cache, bit for bit."""
+    T, Hkv = 900, 4
+    k, v = rand((T, Hkv, 128), 11).cuda(), rand((T, Hkv, 128), 12).cuda()
+    f = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float().cuda()
+    caches = []
+    for cuts in ([0, T], [0, 1, 2, 3, 500, 501, 899, T]):
+        kv = qasc.alloc_kv4(1, Hkv, T + 3)
+        for lo, hi in zip(cuts, cuts[1:]):
+            c, ln = batch_tensors([0, hi - lo], [hi])
+            qasc.kv4_rope_append(None, k[lo:hi], v[lo:hi], None, kv, ln, f, cu_q=c)
+        caches.append(kv)
+    qasc.qasc_device_error()
+    for a, b in zip(caches[0][:4], caches[1][:4]):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("bad", ["page", "position", "length"])
+def test_append_and_read_skip_what_lies_outside(bad):
+    P, Hkv = 64, 2
+    lens, ql = [70, 130], [70, 5]
+    cu = [0, 70, 75]
+    table = torch.tensor([[1, 2, 5], [3, 4, 0]], dtype=torch.int32)
+    if bad == "page":
+        table[0, 1] = 9                                    # tokens 64 .. 69 of sequence 0
+        lost = range(64, 70)
+    elif bad == "position":
+        lens[1] = 3                                        # its first two stand in front of the cache
+        lost = range(70, 72)
+    else:
+        lens[1] = 3 * P + 2                                # its last two behind it
+        lost = range(73, 75)
+    k, v = rand((75, Hkv, 128), 13).cuda(), rand((75, Hkv, 128), 14).cuda()
+    kv = qasc.alloc_kv4(6, Hkv, P)
+    c, ln = batch_tensors(cu, lens)
+    qasc.kv4_rope_append_paged(None, k, v, None, kv, table.cuda(), ln, None, cu_q=c)
+    with pytest.raises(qasc.QascError, match="BAD_TABLE"):
+        qasc.qasc_device_error()
+    K, V = (torch.full((75, Hkv, 128), CANARY, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qasc.kv4_read_paged(kv, table.cuda(), ln, K, V, cu_q=c)
+    with pytest.raises(qasc.QascError, match="BAD_TABLE"):
+        qasc.qasc_device_error()
+    keep = torch.ones(75, dtype=torch.bool)
+    keep[list(lost)] = False
+    assert bool((K[~keep] == CANARY).all()) and bool((V[~keep] == CANARY).all())
+    assert np.array_equal(f64(K[keep]), okv4.values(*okv4.quantise(f64(k[keep]))))
+    assert np.array_equal(f64(V[keep]), okv4.values(*okv4.quantise(f64(v[keep]))))
+
+
+# ----------------------------------------------------------------------- read
+@pytest.mark.parametrize("Hkv,P,ql,lens,t", [
+    (2, 64, [5, 0, 64, 130], [5, 9, 64, 300], (1.0, 1.0)),
+    (8, 128, [1], [1000], (2.0 ** -6, 8.0)),
+    (1, 64, [257], [257], (1.0, 2.0 ** 30)),
+])
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("split_heads", [True, False])
+def test_read(Hkv, P, ql, lens, t, paged, split_heads):
+    T = sum(ql)
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    pages = Pages4(lens, Hkv, P, cdiv(max(lens), P) + 1, 15, t=t)
+    for b, n in enumerate(lens):
+        pages.hide(b, 0, n - ql[b])
+    c, ln = batch_tensors(cu, lens)
+    if split_heads:                                        # heads first, tokens behind each other, with room between
+        K, V = (torch.full((Hkv, T + 9, 128), CANARY, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        outs = K.transpose(0, 1)[:T + 2], V.transpose(0, 1)[:T + 2]
+    else:
+        K, V = (torch.full((T + 2, Hkv, 128), CANARY, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        outs = K, V
+    if paged:
+        qasc.kv4_read_paged(pages.cache(), pages.table.cuda(), ln, *outs, cu_q=c)
+    else:
+        qasc.kv4_read(pages.contiguous(max(lens) + 3), ln, *outs, cu_q=c)
+    qasc.qasc_device_error()
+    for side, out in enumerate(outs):
+        want = np.concatenate([x[:, n - m:n] for x, n, m in zip(pages.values(side), lens, ql)], axis=1)
+        assert np.array_equal(f64(out[:T]).transpose(1, 0, 2), want)
+        assert bool((out[T:] == CANARY).all())
+    if split_heads:
+        assert bool((K[:, T + 2:] == CANARY).all())
+
+
+def test_read_of_every_code_and_scale():
+    kv = qasc.alloc_kv4(1, 1, 256)
+    kv.K.copy_(torch.arange(256, dtype=torch.uint8).reshape(1, 1, 256, 1).expand(1, 1, 256, 64))
+    kv.K_sf.view(torch.uint8).copy_(torch.arange(256, dtype=torch.uint8).reshape(1, 1, 256, 1).expand(1, 1, 256, 8))
+    kv.V.copy_(kv.K.flip(2))
+    kv.V_sf.view(torch.uint8).copy_(kv.K_sf.view(torch.uint8).flip(2).roll(1, 2))
+    K, V = (torch.zeros((256, 1, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    c, ln = batch_tensors([0, 256], [256])
+    qasc.kv4_read(kv, ln, K, V, cu_q=c)
+    for out, codes, sf in ((K, kv.K, kv.K_sf), (V, kv.V, kv.V_sf)):
+        want = okv4.values(codes[0, 0].cpu().numpy(), sf.view(torch.uint8)[0, 0].cpu().numpy())
+        assert np.array_equal(f64(out[:, 0]), want, equal_nan=True)
+
+
+# --------------------------------------------------------------------- window
+WINDOW = [
+    # Hq, Hkv, P, new tokens, lens, sink, local
+    (8, 2, 64, [1, 1, 1, 1], [1, 31, 64, 300], 4, 1000),
+    (32, 8, 64, [1, 1], [200, 517], 4, 64),
+    (8, 8, 64, [1, 1], [33, 700], 3, 5000),
+    (16, 8, 128, [1], [1500], 0, 400),
+    (64, 8, 256, [1], [600], 4, 600),
+    (8, 2, 64, [131, 1, 0, 40], [131, 90, 77, 400], 4, 100),
+    (8, 1, 128, [33, 2], [33, 257], 130, 17),
+    (8, 4, 64, [64, 65], [64, 321], 0, 128),
+    (64, 8, 64, [9], [140], 1, 139),
+    (8, 2, 64, [5, 3], [2, 3], 4, 9),          # three tokens stand in front of their cache
+    (8, 2, 64, [300], [300], 0, 300),
+    (8, 2, 64, [3, 0, 2], [0, 0, 130], 2, 1),
+    (32, 8, 64, [5, 5, 5], [700, 5, 64], 4, 90),
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,P,ql,lens,sink,local", WINDOW)
+@pytest.mark.parametrize("paged", [True, False])
+def test_window(Hq, Hkv, P, ql, lens, sink, local, paged):
+    T, B = sum(ql), len(ql)
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    pages = Pages4(lens, Hkv, P, cdiv(max(lens), P) + 1, seed=21, t=(0.5, 4.0) if paged else (1.0, 1.0))
+    single = ql == [1] * B
+    q = rand((T + (0 if single else 2), Hq, 128), 22)      # two tokens of no sequence
+    ref = osv.window_attention(f64(q[:T]), pages.values(0), pages.values(1), cu, lens, sink, local)
+    for b, n in enumerate(lens):                           # what no query attends to
+        first = max(0, n - ql[b])
+        if ql[b] == 0:
+            pages.hide(b, 0, n)
+        elif first - local + 1 > sink:
+            pages.hide(b, sink, first - local + 1)
+    cu_arg = None if single else cu
+    if paged:
+        out, lse = window(q, pages, cu_arg, lens, sink, local, max_q=max(ql))
+    else:
+        n_cap = max(lens) + 5
+        out, lse = outputs(q.shape[0], Hq)
+        c, ln = batch_tensors(cu_arg, lens)
+        ws = window_ws(q.shape[0], B, Hq, Hkv, n_cap, local, sink)
+        qasc.kv4_window_attn(q.cuda(), pages.contiguous(n_cap), ln, out, ws, sink=sink, local=local, cu_q=c, lse=lse)
+        qasc.qasc_device_error()
+    check_rows(out[:T], lse[:T], ref, max(lens), vmax_of(pages))
+    assert bool((out[T:] == CANARY).all()) and bool((lse[T:] == CANARY).all())
+
+
+@pytest.mark.parametrize("max_q", [1, 2, 7, 60])
+def test_window_max_q_changes_no_answer(max_q):
+    """A number that is too small or too large: other kernels, the same rows."""
+    ql, lens = [7, 1, 50, 2], [300, 77, 400, 2]
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    pages = Pages4(lens, 2, 64, 8, seed=23)
+    q = rand((60, 8, 128), 24)
+    ref = osv.window_attention(f64(q), pages.values(0), pages.values(1), cu, lens, 4, 120)
+    out, lse = window(q, pages, cu, lens, 4, 120, max_q=max_q)
+    check_rows(out, lse, ref, 400, vmax_of(pages))
+
+
+@pytest.mark.parametrize("qscale", [0.0, 1e-30, 20.0, 1e4])
+def test_window_flat_and_peaked_logits(qscale):
+    lens, P = [900, 33], 64
+    pages = Pages4(lens, 2, P, 16, seed=25)
+    q = rand((2, 8, 128), 26, qscale)
+    ref = osv.window_attention(f64(q), pages.values(0), pages.values(1), [0, 1, 2], lens, 4, 5000)
+    out, lse = window(q, pages, None, lens, 4, 5000)
+    check_rows(out, lse, ref, 900, vmax_of(pages))
+
+
+def test_window_queries_of_very_different_values():
+    """One value of a query row 2^20 times the others: those keep their bits as well."""
+    pages = Pages4([500], 2, 64, 9, seed=27)
+    q = rand((1, 8, 128), 28)
+    q[0, :, 5] = 2.0 ** -20
+    q[0, ::2, 7] = 2.0 ** 12
+    ref = osv.window_attention(f64(q), pages.values(0), pages.values(1), [0, 1], [500], 4, 5000)
+    out, lse = window(q, pages, None, [500], 4, 5000)
+    check_rows(out, lse, ref, 500, vmax_of(pages))
+
+
+def test_window_growing_maximum():
+    """Keys whose logits grow along the sequence: the base moves again and again."""
+    n, Hkv = 3000, 2
+    pages = Pages4([n], Hkv, 64, cdiv(n, 64), seed=29)
+    q = rand((1, 8, 128), 30)
+    ramp = np.linspace(0, 30, n)[None, :, None] * np.sign(f64(q)[0, ::4])[:, None, :] / 16
+    held = pages.logical[0]
+    c, s, v = packed(ramp + held[0][2] * 0.1)
+    held[0] = (c, s, v)
+    for i in range(cdiv(n, 64)):
+        page, m = int(pages.table[0, i]), min(64, n - 64 * i)
+        pages.codes[0, page, :, :m], pages.sf[0, page, :, :m] = c[:, 64 * i:64 * i + m], s[:, 64 * i:64 * i + m]
+    ref = osv.window_attention(f64(q), pages.values(0), pages.values(1), [0, 1], [n], 4, n)
+    out, lse = window(q, pages, None, [n], 4, n)
+    check_rows(out, lse, ref, n, vmax_of(pages))
+
+
+LONG = [
+    # Hq, Hkv, new tokens, lens, sink, local: shared between blocks
+    (8, 2, [1], [40000], 4, 40000),
+    (64, 8, [1, 1], [9000, 20001], 4, 19000),
+    (8, 8, [1] * 5, [7000, 1, 300, 12345, 64], 0, 100000),
+    (32, 8, [3, 2], [9000, 8999], 4, 100000),
+    (8, 1, [40], [6000], 4, 5500),
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,ql,lens,sink,local", LONG)
+def test_window_shared_between_blocks(Hq, Hkv, ql, lens, sink, local):
+    T, P = sum(ql), 128
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    pages = Pages4(lens, Hkv, P, cdiv(max(lens), P), seed=31, random=True)
+    q = rand((T, Hq, 128), 32)
+    out, lse = window(q, pages, cu, lens, sink, local, max_q=max(ql))
+    K, V = pages.values(0), pages.values(1)
+    tokens = sorted({0, T // 2, T - 1})
+    ref = osv.window_attention(f64(q), K, V, cu, lens, sink, local, tokens=tokens)
+    check_rows(out, lse, ref, max(lens), 6.0, rows=tokens)
+
+
+def test_window_of_many_sequences():
+    B, Hq, Hkv, P = 2048, 4, 2, 64
+    lens = [1 + (37 * b) % 150 for b in range(B)]
+    pages = Pages4(lens, Hkv, P, 3, seed=33, random=True)
+    q = rand((B, Hq, 128), 34)
+    out, lse = window(q, pages, None, lens, 4, 100)
+    tokens = list(range(0, B, 61)) + [B - 1]
+    ref = osv.window_attention(f64(q), pages.values(0), pages.values(1), list(range(B + 1)), lens, 4, 100, tokens=tokens)
+    check_rows(out, lse, ref, 150, 6.0, rows=tokens)
+
+
+def test_window_equals_the_bf16_call_on_the_cache_read_back():
+    """What kv4_read gives, attended to by kv_window_attn: the same up to both calls' roundings."""
+    lens, ql, Hq, Hkv, n_cap = [700, 64], [90, 1], 16, 4, 704
+    pages = Pages4(lens, Hkv, 64, 11, seed=35)
+    kv = pages.contiguous(n_cap)
+    q = rand((91, Hq, 128), 36).cuda()
+    c, ln = batch_tensors([0, 90, 91], lens)
+    K, V = (torch.zeros((2, Hkv, n_cap, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for b, n in enumerate(lens):
+        one = qasc.KV4(*(x[b:b + 1] for x in kv[:4]))
+        cb, lb = batch_tensors([0, n], [n])
+        qasc.kv4_read(one, lb, K[b, :, :n].transpose(0, 1), V[b, :, :n].transpose(0, 1), cu_q=cb)
+    want, want_lse = outputs(91, Hq)
+    ws = qasc.alloc_workspace(qasc.kv_window_attn_workspace_bytes(91, 2, Hq, Hkv, n_cap))
+    qasc.kv_window_attn(q, K, V, ln, want, ws, local=300, cu_q=c, lse=want_lse)
+    out, lse = outputs(91, Hq)
+    qasc.kv4_window_attn(q, kv, ln, out, window_ws(91, 2, Hq, Hkv, n_cap, 300), local=300, cu_q=c, lse=lse)
+    qasc.qasc_device_error()
+    A = float(np.abs(pages.values(1)[0]).max())
+    # bf16 outputs (2^-8 each) and probabilities (2^-8 and 2^-11) of values up to A
+    assert float((out.float() - want.float()).abs().max()) <= A * (2 * 2.0 ** -8 + 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16)
+    assert float((lse - want_lse).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("n,m", [(1900, 1), (900, 40)])
+@pytest.mark.parametrize("side", [0, 1])
+def test_window_not_a_number_stays_visible(n, m, side):
+    Hq, Hkv = 8, 2
+    pages = Pages4([n], Hkv, 64, cdiv(n, 64), seed=37, random=True)
+    at = n - m                                             # the first new token: all new ones see it
+    pages.sf[side, int(pages.table[0, at // 64]), 1, at % 64, 3] = 127
+    q = rand((m, Hq, 128), 38)
+    out, lse = window(q, pages, [0, m], [n], 4, n, max_q=m)
+    assert bool(torch.isfinite(out[:, :4].float()).all()) and bool(torch.isfinite(lse[:, :4]).all())
+    if side == 0:
+        assert bool(torch.isnan(out[:, 4:].float()).all()) and bool(torch.isnan(lse[:, 4:]).all())
+    else:
+        assert bool(torch.isnan(out[:, 4:, 48:64].float()).all()) and bool(torch.isfinite(lse).all())
+        assert bool(torch.isfinite(out[:, 4:, :48].float()).all()) and bool(torch.isfinite(out[:, 4:, 64:].float()).all())
+
+
+@pytest.mark.parametrize("ql,n_cap", [([1, 1, 1], 256), ([9, 2, 40], 512)])
+def test_window_lengths_outside_are_clamped_and_reported(ql, n_cap):
+    P, Hkv = 64, 2
+    T, cu = sum(ql), np.concatenate([[0], np.cumsum(ql)]).tolist()
+    pages = Pages4([n_cap] * 3, Hkv, P, n_cap // P, seed=39, random=True)
+    q = rand((T, 8, 128), 40)
+    ref = window(q, pages, cu, [n_cap, 0, 100], 4, 90)
+    out, lse = outputs(T, 8)
+    c, ln = batch_tensors(cu, [n_cap + 5, -3, 100])
+    qasc.kv4_window_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), ln, out,
+                               window_ws(T, 3, 8, Hkv, n_cap, 90), local=90, cu_q=c, lse=lse)
+    with pytest.raises(qasc.QascError, match="BAD_TABLE"):
+        qasc.qasc_device_error()
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
+def test_window_bad_page_is_reported():
+    pages = Pages4([300], 2, 64, 5, seed=41, random=True)
+    pages.table[0, 2] = pages.num_pages
+    out, lse = outputs(1, 8)
+    q = rand((1, 8, 128), 42)
+    ln = batch_tensors(None, [300])[1]
+    ws = window_ws(1, 1, 8, 2, 320, 300)
+    qasc.kv4_window_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), ln, out, ws, local=300, lse=lse)
+    with pytest.raises(qasc.QascError, match="BAD_TABLE"):
+        qasc.qasc_device_error()
+    K, V = pages.values(0), pages.values(1)
+    K[0][:, 128:192], V[0][:, 128:192] = 0, 0              # rows of zeros
+    check_rows(out, lse, osv.window_attention(f64(q), K, V, [0, 1], [300], 4, 300), 300, 6.0)
+    # behind the window it is not read
+    qasc.kv4_window_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), ln, out, ws, local=100, lse=lse)
+    qasc.qasc_device_error()
+
+
+@pytest.mark.parametrize("T,B,n", [(1, 1, 5000), (300, 1, 1400), (40, 40, 900)])
+def test_window_is_deterministic_and_replays_in_a_graph(T, B, n):
+    Hq, Hkv, P = 16, 4, 128
+    lens = [n - 17 * b for b in range(B)]
+    pages = Pages4(lens, Hkv, P, cdiv(n, P), seed=43, random=True)
+    kv, table = pages.cache(), pages.table.cuda()
+    q = rand((T, Hq, 128), 44).cuda()
+    c, ln = batch_tensors(None if T == B else [0, T], lens)
+    ws = window_ws(T, B, Hq, Hkv, pages.pps * P, 700)
+
+    def call(out, lse):
+        qasc.kv4_window_attn_paged(q, kv, table, ln, out, ws, local=700, cu_q=c, lse=lse)
+
+    a, b, g_out = outputs(T, Hq), outputs(T, Hq), outputs(T, Hq)
+    call(*a)
+    ws.fill_(255)
+    call(*b)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call(*g_out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], g_out[0]) and torch.equal(a[1], g_out[1])
+    ln.copy_(torch.tensor([max(1, x - 200) for x in lens], dtype=torch.int32))   # the replay follows the lengths
+    graph.replay()
+    call(*a)
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], g_out[0]) and not torch.equal(a[0], b[0])
+    qasc.qasc_device_error()
+
+
+def test_two_windows_on_two_streams():
+    Hq, Hkv, P, n = 16, 4, 64, 6000
+    pages = Pages4([n, n - 3], Hkv, P, cdiv(n, P), seed=45, random=True)
+    kv, table = pages.cache(), pages.table.cuda()
+    q = rand((2, Hq, 128), 46).cuda()
+    ln = batch_tensors(None, [n, n - 3])[1]
+    outs = [outputs(2, Hq)[0] for _ in range(3)]
+    wss = [window_ws(2, 2, Hq, Hkv, pages.pps * P, n) for _ in range(3)]
+    qasc.kv4_window_attn_paged(q, kv, table, ln, outs[2], wss[2], local=n)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            qasc.kv4_window_attn_paged(q, kv, table, ln, outs[i], wss[i], local=n, stream=s)
+    torch.cuda.synchronize()
+    qasc.qasc_device_error()
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
+
+
+# --------------------------------------------------------------------- sparse
+def sparse_ref(q, pages, lists, n, sink, local):
+    """lists[b][g]: listed tokens."""
+    B, Hq, _ = q.shape
+    out, lse = np.zeros((B, Hq, 128)), np.full((B, Hq), -np.inf)
+    A, zabs = np.zeros_like(out), np.zeros_like(lse)
+    K, V = pages.values(0), pages.values(1)
+    end = min(n, sink)
+    always = list(range(end)), list(range(max(end, n - local), n))
+    for b in range(B):
+        for h in range(Hq):
+            g = h // (Hq // pages.Hkv)
+            j = np.array(always[0] + list(lists[b][g]) + always[1], dtype=np.int64)
+            out[b, h], lse[b, h], A[b, h], zabs[b, h] = osv.attend(q[b, h], K[b][g][j], V[b][g][j])
+    return out, lse, A, zabs
+
+
+SPARSE = [
+    # B, Hq, Hkv, n, K, sink, local, per head, lengths
+    (1, 8, 2, 600, 100, 4, 256, False, False),
+    (2, 32, 8, 700, 77, 4, 64, True, True),
+    (3, 8, 8, 300, 0, 4, 256, False, False),
+    (2, 8, 1, 400, 200, 0, 0, False, True),
+    (2, 16, 8, 900, 300, 0, 0, True, True),
+    (1, 64, 8, 5, 0, 4, 256, False, False),
+    (1, 8, 4, 20000, 9000, 4, 256, True, False),
+]
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,n,K,sink,local,per_head,with_len", SPARSE)
+@pytest.mark.parametrize("paged", [True, False])
+def test_sparse(B, Hq, Hkv, n, K, sink, local, per_head, with_len, paged):
+    P = 64
+    pages = Pages4([n] * B, Hkv, P, cdiv(n, P) + 2, seed=51, random=n > 2000, t=(2.0, 0.25))
+    g = torch.Generator().manual_seed(52)
+    c1 = max(sink, n - local)
+    rows = B * (Hkv if per_head else 1)
+    sel = torch.stack([(sink + torch.randperm(c1 - sink, generator=g)[:K]) for _ in range(rows)]).int()
+    lens = None
+    if with_len:
+        lens = torch.randint(0, K + 1, (rows,), generator=g).int()
+        lens[0] = 0                                        # no entry; without sink and local no token at all
+        lens[-1] = K + 9                                   # clamped
+        for i in range(rows):
+            sel[i, min(K, int(lens[i])):] = 1 << 30        # entries that are not in use
+    lists = [[sel[b * Hkv + gg if per_head else b][:K if lens is None else min(K, int(lens[b * Hkv + gg if per_head else b]))].tolist()
+              for gg in range(Hkv)] for b in range(B)]
+    q = rand((B, Hq, 128), 53)
+    ref = sparse_ref(f64(q), pages, lists, n, sink, local)
+    # what no head attends to
+    for b in range(B):
+        used = set(range(min(n, sink))) | set(range(max(min(n, sink), n - local), n))
+        used |= {t for gg in range(Hkv) for t in lists[b][gg]}
+        if n <= 2000:
+            for t in range(n):
+                if t not in used:
+                    pages.hide(b, t, t + 1)
+    shape = (B, Hkv) if per_head else (B,)
+    out, lse = outputs(B, Hq)
+    args = dict(n=n, sink=sink, local=local, lengths=None if lens is None else lens.reshape(shape).cuda(),
+                per_kv_head=per_head, lse=lse)
+    sel_arg = sel.reshape(*shape, K).cuda() if K else None
+    if K == 0 and per_head:
+        pytest.skip("no list")
+    n_cap = pages.pps * P if paged else n + 7
+    ws = qasc.alloc_workspace(qasc.kv4_sparse_attn_workspace_bytes(B, Hq, Hkv, n, n_cap, K, sink, local))
+    ws.fill_(255)
+    if paged:
+        qasc.kv4_sparse_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), sel_arg, out, ws, **args)
+    else:
+        qasc.kv4_sparse_attn(q.cuda(), pages.contiguous(n_cap), sel_arg, out, ws, **args)
+    qasc.qasc_device_error()
+    check_rows(out, lse, ref, n, max(6.0, vmax_of(pages)))
+
+
+def test_sparse_entry_outside_is_reported():
+    n, P = 400, 64
+    pages = Pages4([n], 2, P, 7, seed=54, random=True)
+    q = rand((1, 8, 128), 55)
+    sel = torch.tensor([[10, n, -1, 40]], dtype=torch.int32)
+    out, lse = outputs(1, 8)
+    ws = qasc.alloc_workspace(qasc.kv4_sparse_attn_workspace_bytes(1, 8, 2, n, 448, 4, 4, 64))
+    qasc.kv4_sparse_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), sel.cuda(), out, ws, n=n, local=64, lse=lse)
+    with pytest.raises(qasc.QascError, match="BAD_TABLE"):
+        qasc.qasc_device_error()
+    K, V = pages.values(0), pages.values(1)
+    K[0][:, 11], V[0][:, 11], K[0][:, 12], V[0][:, 12] = 0, 0, 0, 0   # rows of zeros in their places
+    pages.values = lambda side: (K, V)[side]
+    check_rows(out, lse, sparse_ref(f64(q), pages, [[[10, 11, 12, 40]] * 2], n, 4, 64), n, 6.0)
+
+
+def test_decode_steps_over_a_4_bit_cache():
+    """The run of a serving loop: a prompt in two chunks, then steps that append, select on the
+    index and attend to the selected tokens, against the oracle on what the cache holds."""
+    B, Hq, Hkv, P, n0, K = 2, 8, 2, 64, 500, 60
+    n_cap = 640
+    table = torch.randperm(22, generator=torch.Generator().manual_seed(60))[:20].reshape(2, 10).int().cuda()
+    kv = qasc.alloc_kv4(22, Hkv, P)
+    W = rand((Hkv, 128, 32), 61, 128 ** -0.5).cuda()
+    index = torch.zeros((B, Hkv, n_cap, 32), dtype=torch.bfloat16, device="cuda")
+    Kb = torch.zeros((B, Hkv, n_cap, 128), dtype=torch.bfloat16, device="cuda")     # bf16 keys of the index
+    Vb = torch.zeros_like(Kb)
+    f = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float()
+    log = []
+    at = 0
+    for step, m in enumerate([300, 200, 1, 1, 1]):
+        n = at + m
+        qkv = rand((B * m, Hq + 2 * Hkv, 128), 70 + step).cuda()
+        q, k, v = qkv.split([Hq, Hkv, Hkv], dim=1)
+        log.append((m, f64(k), f64(v)))
+        c, ln = batch_tensors(None if m == 1 else [0, m, 2 * m], [n] * B)
+        q_rot, q_same = (torch.zeros((B * m, Hq, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        qasc.kv4_rope_append_paged(q, k, v, q_rot, kv, table, ln, f.cuda(), cu_q=c)
+        qasc.kv_rope_append(q, k, v, q_same, Kb, Vb, ln, f.cuda(), cu_q=c)
+        qasc.ts_index_append(Kb, W, index, at, m, Hq=Hq)
+        at = n
+        out, lse = outputs(B * m, Hq)
+        if m > 1:
+            ws = window_ws(B * m, B, Hq, Hkv, n_cap, n_cap, max_q=m)
+            qasc.kv4_window_attn_paged(q_rot, kv, table, ln, out, ws, local=n_cap, cu_q=c, max_q=m, lse=lse)
+        else:
+            sel = torch.empty((B, K), dtype=torch.int32, device="cuda")
+            ws = qasc.alloc_workspace(qasc.ts_select_workspace_bytes(B, Hq, Hkv, n, n_cap, K))
+            qasc.ts_score_vote_select(q_rot, W, index, sel, ws, n=n, K=K)
+            ws = qasc.alloc_workspace(qasc.kv4_sparse_attn_workspace_bytes(B, Hq, Hkv, n, n_cap, K))
+            qasc.kv4_sparse_attn_paged(q_rot, kv, table, sel, out, ws, n=n, lse=lse)
+        qasc.qasc_device_error()
+        # the cache that the oracle keeps
+        pos = 0
+        sides = [[], []]
+        for mm, kk, vv in log:
+            p = np.tile(np.arange(pos, pos + mm), B)
+            sides[0].append(okv4.values(*okv4.quantise(round_bf16(osv.rotate(kk, p, f.numpy(), False)))).reshape(B, mm, Hkv, 128))
+            sides[1].append(okv4.values(*okv4.quantise(vv)).reshape(B, mm, Hkv, 128))
+            pos += mm
+        caches = [[np.concatenate(s, axis=1)[b].transpose(1, 0, 2) for b in range(B)] for s in sides]
+        vmax = max(np.abs(x).max() for x in caches[1])
+        if m > 1:
+            tokens = [0, m - 1, m, 2 * m - 1]
+            ref = osv.window_attention(f64(q_rot), *caches, [0, m, 2 * m], [n] * B, 4, n_cap, tokens=tokens)
+            check_rows(out, lse, ref, n, vmax, rows=tokens)
+        else:
+            S = sel.cpu().numpy()
+            want, _ = ots.sparse_attention(f64(q_rot), np.stack(caches[0]), np.stack(caches[1]), S, n, 4, 256)
+
+            class Held:
+                values = staticmethod(lambda side: caches[side])
+            Held.Hkv = Hkv
+            ref = sparse_ref(f64(q_rot), Held, [[S[b].tolist()] * Hkv for b in range(B)], n, 4, 256)
+            assert np.abs(ref[0] - want).max() < 1e-9
+            check_rows(out, lse, ref, n, vmax)
