@@ -16,11 +16,18 @@
 // Work.  The queries of a KV head's group share its keys: an item is up to
 // 8 kNT rows (token, head of the group) of a sequence and KV head.  Its tokens
 // (sink, window or list) are numbered without gaps, in tiles of 32.  The tiles of
-// all items are laid end to end, every block takes an equal range of that line,
-// and its warps take every kWarps-th tile of an item, each with a running maximum
-// and sum of its own, so that nothing but an item's end makes them wait for each
-// other.  Keys stand as rows of the first product and channels as rows of the
-// second, queries as columns of both:
+// all items are laid end to end, every block takes an equal range of that line and
+// every warp of it an equal part of the range: a warp walks its tiles alone, loads
+// three ahead of their use, and writes the rows of items that are all its own.
+// Of an item that it shares it keeps (max, sum, O); the block joins its warps' at
+// its end, once, and those that go beyond it are left in the workspace, two places a block
+// (the item that it begins with, the one that it ends with), where
+// kv4_merge_kernel joins them.  (With the tiles of every item dealt to all warps and
+// joined in the block, a third of the instructions were the joins': 64 sequences
+// with a 4K window 91 us.)  Short items are not shared between blocks, and have no
+// merge to wait for.
+// Keys stand as rows of the first product and channels as rows of the second,
+// queries as columns of both:
 //   S^T = K Q^T      (16 tokens x 8 queries, over d)
 //   P = exp2(S c - m) in fp16
 //   O^T += V^T P^T   (16 channels x 8 queries, over tokens)
@@ -38,10 +45,6 @@
 // when the maximum grows by more than 2^5: P stays below 2^15, and weights down
 // to 2^-24 of the largest keep all their bits.  The sum that divides takes P
 // unrounded.
-//
-// An item that several blocks share leaves (max, sum, O) of each in the
-// workspace, two places a block (the item that it begins with, the one that it ends
-// with), and kv4_merge_kernel joins them.
 #include <algorithm>
 #include <climits>
 
@@ -52,19 +55,23 @@ namespace qasc {
 namespace {
 
 constexpr int kTile = 32;                      // tokens of a warp's tile
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 4;                     // tiles of a warp's ring
+#ifndef KV4_W
+#define KV4_W 12
+#define KV4_S 3
+#define KV4_C 2
+#endif
+constexpr int warps_of(int nt) { return nt == 1 ? KV4_W : 8; }
+constexpr int stages_of(int nt) { return nt == 1 ? KV4_S : 4; }   // tiles of a warp's ring
 constexpr int kTileCodes = kTile * kKv4Codes;  // bytes
 constexpr int kTileScales = kTile * kKv4Groups;
 constexpr int kStage = 2 * (kTileCodes + kTileScales);
-constexpr int kMaxSeq = 2048;
-constexpr int kPieces = 64;                    // items of a block's range planned at once
-constexpr int kItemCost = 8;                   // places of an item beside its tiles: queries, join, output
-constexpr int kLeast = 16;                     // places that a block takes at least
+constexpr int kSums = 512;                     // places are summed for as many groups of sequences at most
+constexpr int kQueue = 8;                      // items that a warp's loads are ahead of its products, at most
+constexpr int kItemCost = KV4_C;                   // places of an item beside its tiles: queries, output
+constexpr int kLeast = 8;                      // places that a block takes at least
+constexpr int kWholeTokens = 1024;             // an item of more tokens may be shared between blocks
 constexpr float kBase = 10.0f;                 // log2 of P at the maximum that the base was taken from
 constexpr float kGrow = 5.0f;                  // growth of the maximum that moves the base
-constexpr int kOutPad = 4;
 // log2(e) / sqrt(128): logits in base-2 units.
 constexpr float kScale = 1.4426950408889634f * 0.08838834764831845f;
 
@@ -74,6 +81,8 @@ struct Args {
   int64_t n_cap;
   int n, sink_end, local_start;   // listed: tokens of every sequence, its regions
   int64_t most_rows;        // sequences with more rows are left out (0: none)
+  int whole;                // items are not shared between blocks
+  int ssh;                  // sequences of a sum: 2^ssh
   float* part_o;            // [grid][2][rows][128]
   float2* part_ml;          // [grid][2][rows] (max in log2 units, sum)
   struct Share* share;      // [grid] the item that a block shares with those behind it
@@ -88,20 +97,35 @@ struct Share {
   int last, pad;
 };
 
-// A block's part of an item: tiles t0 .. t0 + n - 1.
-struct Piece {
+// A warp's part of an item: tiles t0 .. t0 + n - 1 of `tiles`.
+struct alignas(16) Piece {
   int tok0, rows;      // first query token, rows
   int b, g;
   int p0, p1;          // positions of the first and last row
   int lo;              // window: token behind the sink's; listed: list's entries
   int head, cnt;       // tokens of the sink, of all
-  int t0, n;
-  int whole;           // every tile: the output is written, not a part
-  int slot, last;      // part's place; last block that has one
+  int t0, n, tiles;
+  int64_t x0;          // its first place on the line
 };
 
 struct Seq {
   int q0, ql, len;
+};
+
+// Where a warp's loads stand on the line: item `rem` of sequence b's `items`.
+struct Walk {
+  int64_t x0;          // the item's first place
+  int b, rem, items, span;
+  Seq s;
+};
+
+// Part of an item in shared memory: rows [kRows][128] fp32, their chunks of four
+// turned by (row / 2) mod 4 (which the products' layout writes without
+// bank conflicts), and their (max, sum).
+template <int kRows>
+struct Part {
+  float4 o[kRows][kD / 4];
+  float2 ml[kRows];
 };
 
 __device__ __forceinline__ int clampi(int64_t v, int64_t lo, int64_t hi) {
@@ -136,7 +160,7 @@ __device__ __forceinline__ int list_len(const Args& p, int b, int g) {
 
 // Items of a sequence (row blocks times KV heads) and the places of each: the
 // most tiles that any of them has.
-template <bool kList, int kRows>
+template <int kRows>
 __device__ __forceinline__ int items_of(const Args& p, const Seq& s) {
   const int64_t rows = static_cast<int64_t>(s.ql) << p.gsh;
   if (p.most_rows && rows > p.most_rows) return 0;
@@ -156,18 +180,6 @@ __device__ __forceinline__ int span_of(const Args& p, const Seq& s, int b) {
   return static_cast<int>((cnt + kTile - 1) / kTile) + kItemCost;
 }
 
-// The last i in [0, n) with arr[i] <= x (arr ascending, arr[0] <= x).
-template <class T>
-__device__ __forceinline__ int find_last(const T* arr, int n, T x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (arr[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 // A line of U places over G blocks: block c has the places [c U / G, (c + 1) U / G).
 struct Line {
   int64_t U;
@@ -178,14 +190,14 @@ struct Line {
 
 template <int kNT>
 struct Smem {
-  static constexpr int kRows = 8 * kNT;
-  uint8_t ring[kWarps][kStages][kStage];
-  float o[kWarps / 2][kRows][kD + kOutPad];
-  float m[kWarps][kRows], l[kWarps][kRows];
-  Piece piece[kPieces];
-  int64_t place[kMaxSeq + 1];    // places before sequence s
-  int32_t item[kMaxSeq + 1];     // items before sequence s
-  int shared_out;                // a share behind this block's range was noted
+  static constexpr int kRows = 8 * kNT, kWarps = warps_of(kNT), kStages = stages_of(kNT);
+  static_assert(kStages * kStage >= sizeof(Part<kRows>), "a warp's last part stands in its ring");
+  alignas(16) uint8_t ring[kWarps][kStages * kStage];
+  Part<kRows> first[kWarps];
+  Piece queue[kWarps][kQueue];
+  Piece part[2 * kWarps];        // of every warp: the item that it shares with earlier ones, with later ones
+  int there[2 * kWarps];         // 0: none, 1: the item goes on, 2: it ends here
+  int64_t place[kSums + 1];      // places before a group of sequences
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -222,6 +234,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Row of the queries and outputs of row `col` of an item.
+__device__ __forceinline__ int64_t row_of(const Args& p, int tok0, int g, int col) {
+  return static_cast<int64_t>(tok0 + (col >> p.gsh)) * p.Hq + (g << p.gsh) + (col & ((1 << p.gsh) - 1));
+}
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l != 0.0f ? (m == -INFINITY ? l : (m - kBase + log2f(l)) * 0.6931471805599453f) : -INFINITY;
+}
+__device__ __forceinline__ float inverse_of(const Args& p, float l) {
+  return l != 0.0f ? p.a.kv.v_scale / kKv4HalfScale / l : 0.0f;
+}
+
 // Token of slot s of an item; -1 behind the last.
 template <bool kList>
 __device__ __forceinline__ int token_of_slot(const Args& p, const Piece& pc, int s) {
@@ -237,27 +260,62 @@ __device__ __forceinline__ int token_of_slot(const Args& p, const Piece& pc, int
   return -1;
 }
 
-template <bool kList, int kNT>
-__device__ __forceinline__ Piece make_piece(const Args& p, const Smem<kNT>& S, const Line& line, int e, int64_t start,
-                                            int64_t end) {
-  constexpr int kRows = 8 * kNT;
+// The item that holds place x.
+template <bool kList, int kRows>
+__device__ __forceinline__ Walk walk_at(const Args& p, const int64_t* place, int64_t x) {
+  int lo = 0, hi = (p.B + (1 << p.ssh) - 1) >> p.ssh;   // the last group with place <= x
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (place[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  Walk w;
+  int64_t at = place[lo];
+  for (w.b = lo << p.ssh;; ++w.b) {
+    w.s = seq_of<kList>(p, w.b);
+    w.items = items_of<kRows>(p, w.s);
+    if (w.items == 0) continue;
+    w.span = span_of<kList, kRows>(p, w.s, w.b);
+    const int64_t all = static_cast<int64_t>(w.items) * w.span;
+    if (x < at + all) break;
+    at += all;
+  }
+  w.rem = static_cast<int>((x - at) / w.span);
+  w.x0 = at + static_cast<int64_t>(w.rem) * w.span;
+  return w;
+}
+
+// The next item (w.b == p.B behind the last).
+template <bool kList, int kRows>
+__device__ __forceinline__ void walk_on(const Args& p, Walk& w) {
+  w.x0 += w.span;
+  if (++w.rem < w.items) return;
+  w.rem = 0;
+  while (++w.b < p.B) {
+    w.s = seq_of<kList>(p, w.b);
+    w.items = items_of<kRows>(p, w.s);
+    if (w.items == 0) continue;
+    w.span = span_of<kList, kRows>(p, w.s, w.b);
+    return;
+  }
+}
+
+// The part of item w on the places [start, end).
+template <bool kList, int kRows>
+__device__ __forceinline__ Piece piece_of(const Args& p, const Walk& w, int64_t start, int64_t end) {
   Piece pc;
-  const int b = find_last(S.item, p.B, e);
-  const int items = S.item[b + 1] - S.item[b], rem = e - S.item[b];
-  const int span = static_cast<int>((S.place[b + 1] - S.place[b]) / items);
-  const int64_t x0 = S.place[b] + static_cast<int64_t>(rem) * span;
-  const int blocks = items / p.Hkv;
-  const Seq s = seq_of<kList>(p, b);
-  pc.b = b;
-  pc.g = rem / blocks;
-  const int r0 = (rem - pc.g * blocks) * kRows;
-  pc.rows = static_cast<int>(min(static_cast<int64_t>(kRows), (static_cast<int64_t>(s.ql) << p.gsh) - r0));
-  pc.tok0 = s.q0 + (r0 >> p.gsh);
-  pc.p0 = s.len - s.ql + (r0 >> p.gsh);
-  pc.p1 = s.len - s.ql + ((r0 + pc.rows - 1) >> p.gsh);
+  const int blocks = w.items / p.Hkv;
+  pc.b = w.b;
+  pc.g = w.rem / blocks;
+  pc.x0 = w.x0;
+  const int r0 = (w.rem - pc.g * blocks) * kRows;
+  pc.rows = static_cast<int>(min(static_cast<int64_t>(kRows), (static_cast<int64_t>(w.s.ql) << p.gsh) - r0));
+  pc.tok0 = w.s.q0 + (r0 >> p.gsh);
+  pc.p0 = w.s.len - w.s.ql + (r0 >> p.gsh);
+  pc.p1 = w.s.len - w.s.ql + ((r0 + pc.rows - 1) >> p.gsh);
   if (kList) {
     pc.head = p.sink_end;
-    pc.lo = list_len(p, b, pc.g);
+    pc.lo = list_len(p, pc.b, pc.g);
     pc.cnt = p.sink_end + pc.lo + (p.n - p.local_start);
   } else {
     const int64_t lo = static_cast<int64_t>(pc.p0) - p.a.local + 1;
@@ -265,28 +323,17 @@ __device__ __forceinline__ Piece make_piece(const Args& p, const Smem<kNT>& S, c
     pc.head = min(p.a.sink, pc.lo);
     pc.cnt = pc.p1 >= 0 ? pc.head + pc.p1 - pc.lo + 1 : 0;
   }
-  const int tiles = (pc.cnt + kTile - 1) / kTile;
-  const int64_t off = max(start, x0) - x0 - kItemCost, till = min(end, x0 + span) - x0 - kItemCost;
-  pc.t0 = static_cast<int>(max(static_cast<int64_t>(0), off));
-  pc.n = max(0, static_cast<int>(min(static_cast<int64_t>(tiles), till)) - pc.t0);
-  pc.whole = 0;
-  pc.slot = 0;
-  pc.last = blockIdx.x;
-  if (tiles == 0) {
-    pc.whole = x0 >= start;   // rows without a token: written by the block that has the item's first place
-  } else if (pc.n > 0) {
-    const int first = line.block(x0 + kItemCost);
-    pc.last = line.block(x0 + kItemCost + tiles - 1);
-    pc.whole = first == pc.last;
-    pc.slot = first == static_cast<int>(blockIdx.x);
-  }
+  pc.tiles = (pc.cnt + kTile - 1) / kTile;
+  const int64_t first = w.x0 + kItemCost;
+  pc.t0 = static_cast<int>(max(static_cast<int64_t>(0), start - first));
+  pc.n = max(0, static_cast<int>(min(static_cast<int64_t>(pc.tiles), end - first)) - pc.t0);
   return pc;
 }
 
 template <int kNT, bool kList>
-__global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Args p) {
+__global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const Args p) {
   using Sm = Smem<kNT>;
-  constexpr int kRows = Sm::kRows;
+  constexpr int kRows = Sm::kRows, kWarps = Sm::kWarps, kThreads = 32 * kWarps, kStages = Sm::kStages;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Sm& S = *reinterpret_cast<Sm*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -294,439 +341,445 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Args p) {
   pdl_wait();
 
   // ---- the line
-  for (int b = tid; b < p.B; b += kThreads) {
-    const Seq s = seq_of<kList>(p, b);
-    const int items = items_of<kList, kRows>(p, s);
-    S.item[b] = items;
-    S.place[b] = items > 0 ? static_cast<int64_t>(items) * span_of<kList, kRows>(p, s, b) : 0;
-    if (!kList && blockIdx.x == 0) {
-      const int len = __ldg(p.a.bt.lens + b);
-      if (len < 0 || len > p.n_cap) record_error(p.err, kErrBadPage);
+  const int groups = (p.B + (1 << p.ssh) - 1) >> p.ssh;
+  for (int i = tid; i < groups; i += kThreads) {
+    int64_t places = 0;
+    for (int b = i << p.ssh; b < min(p.B, (i + 1) << p.ssh); ++b) {
+      const Seq s = seq_of<kList>(p, b);
+      const int items = items_of<kRows>(p, s);
+      if (items > 0) places += static_cast<int64_t>(items) * span_of<kList, kRows>(p, s, b);
+      if (!kList && blockIdx.x == 0) {
+        const int len = __ldg(p.a.bt.lens + b);
+        if (len < 0 || len > p.n_cap) record_error(p.err, kErrBadPage);
+      }
     }
+    S.place[i] = places;
   }
-  if (tid == 0) S.shared_out = 0;
+  if (tid < 2 * kWarps) S.there[tid] = 0;
   __syncthreads();
   if (warp == 0) {
     int64_t places = 0;
-    int items = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
+    for (int b0 = 0; b0 < groups; b0 += 32) {
       const int b = b0 + lane;
-      const int64_t v = b < p.B ? S.place[b] : 0;
-      const int w = b < p.B ? S.item[b] : 0;
+      const int64_t v = b < groups ? S.place[b] : 0;
       int64_t vi = v;
-      int wi = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t x = __shfl_up_sync(0xffffffffu, vi, o);
-        const int y = __shfl_up_sync(0xffffffffu, wi, o);
-        if (lane >= o) {
-          vi += x;
-          wi += y;
-        }
+        if (lane >= o) vi += x;
       }
-      if (b < p.B) {
-        S.place[b] = places + vi - v;
-        S.item[b] = items + wi - w;
-      }
+      if (b < groups) S.place[b] = places + vi - v;
       places += __shfl_sync(0xffffffffu, vi, 31);
-      items += __shfl_sync(0xffffffffu, wi, 31);
     }
-    if (lane == 0) {
-      S.place[p.B] = places;
-      S.item[p.B] = items;
-    }
+    if (lane == 0) S.place[groups] = places;
   }
   __syncthreads();
   Line line;
-  line.U = S.place[p.B];
-  line.G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (line.U + kLeast - 1) / kLeast));
-  int64_t start = 0, end = 0;
-  int e0 = 0, count = 0;   // first item of the range, items
+  line.U = S.place[groups];
+  line.G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), p.whole ? line.U : (line.U + kLeast - 1) / kLeast));
+  Walk walk;
+  walk.b = p.B;
+  int64_t start = 0, end = 0;   // this warp's places
   if (static_cast<int>(blockIdx.x) < line.G) {
-    start = line.start(blockIdx.x);
-    end = line.start(blockIdx.x + 1);
-    auto item_at = [&](int64_t x) {
-      const int b = find_last(S.place, p.B, x);
-      const int items = S.item[b + 1] - S.item[b];
-      const int64_t span = (S.place[b + 1] - S.place[b]) / items;
-      return S.item[b] + static_cast<int>((x - S.place[b]) / span);
+    // an item belongs to the block that has its first place, where they are not shared
+    auto bound = [&](int c) {
+      int64_t x = line.start(c);
+      if (p.whole && x < line.U) {
+        const Walk w = walk_at<kList, kRows>(p, S.place, x);
+        if (w.x0 < x) x = w.x0 + w.span;
+      }
+      return x;
     };
-    e0 = item_at(start);
-    count = item_at(end - 1) - e0 + 1;
+    const int64_t first = bound(blockIdx.x), all = bound(blockIdx.x + 1) - first;
+    start = first + all * warp / kWarps;
+    end = first + all * (warp + 1) / kWarps;
+    if (start < end) walk = walk_at<kList, kRows>(p, S.place, start);
   }
 
-  uint8_t* const ring = S.ring[warp][0];
+  uint8_t* const ring = S.ring[warp];
   const uint32_t ring_s = smem_u32(ring);
-  for (int i0 = 0; i0 < count; i0 += kPieces) {
-    const int np = min(kPieces, count - i0);
-    if (tid < np) S.piece[tid] = make_piece<kList, kNT>(p, S, line, e0 + i0 + tid, start, end);
-    __syncthreads();
 
-    // ---- loads: the next tile's tokens and their rows are known a tile ahead of
-    // their copies each (the block table and the list are read on the way)
-    int lp = 0, lt = S.piece[0].t0 + warp;
-    int tok = -1, tok_b = 0, tok_g = 0;       // lane's token of the tile after the next
-    int row = -1;                             // lane's row of the next tile; -1: none
-    bool row_any = false, tok_any = false;
-    auto next_tokens = [&]() {
-      while (lp < np && lt >= S.piece[lp].t0 + S.piece[lp].n) {
-        ++lp;
-        if (lp < np) lt = S.piece[lp].t0 + warp;
-      }
-      tok_any = lp < np;
-      tok = -1;
-      if (tok_any) {
-        const Piece& pc = S.piece[lp];
-        tok = token_of_slot<kList>(p, pc, lt * kTile + lane);
-        tok_b = pc.b;
-        tok_g = pc.g;
-        lt += kWarps;
-      }
-    };
-    auto next_rows = [&]() {
-      row_any = tok_any;
-      row = -1;
-      if (tok >= 0) {
-        row = static_cast<int>(cache_row(p.a.pm, tok_b, tok_g, p.Hkv, p.n_cap, tok));
-        if (row < 0) record_error(p.err, kErrBadPage);
-      }
-      next_tokens();
-    };
-    uint32_t put = 0;   // stage that the next copies go to
-    auto issue = [&]() {
-      if (row_any) {
-        const uint32_t at = ring_s + put * kStage;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rk = __shfl_sync(0xffffffffu, row, r + 8 * i);
-          // V rows stand with the low bits of their number swapped and their chunks
-          // turned by a half where bit 2 is set: a lane's four tokens, 2j and 2j + 1 of
-          // eight, are then in banks of their own.
-          const int rv = __shfl_sync(0xffffffffu, row, ((r & 4) | (r & 1) << 1 | (r >> 1 & 1)) + 8 * i);
-          cp_async16(at + (r + 8 * i) * kKv4Codes + 16 * j, p.a.kv.K + static_cast<int64_t>(max(rk, 0)) * kKv4Codes + 16 * j,
-                     rk >= 0 ? 16 : 0);
-          cp_async16(at + kTileCodes + kTileScales + (r + 8 * i) * kKv4Codes + 16 * (j ^ (r >> 1 & 2)),
-                     p.a.kv.V + static_cast<int64_t>(max(rv, 0)) * kKv4Codes + 16 * j, rv >= 0 ? 16 : 0);
+  // ---- loads: the next tile's tokens and their rows are known a tile ahead of
+  // their copies each (the block table and the list are read on the way)
+  int pushed = 0;                           // items found
+  int lt = 0, left = 0;                     // next tile of the newest item, tiles left of it
+  int tok = -1, tok_b = 0, tok_g = 0;       // lane's token of the tile after the next
+  int row = -1;                             // lane's row of the next tile; -1: none
+  bool row_any = false, tok_any = false;
+  auto next_tokens = [&]() {
+    while (left == 0 && walk.b < p.B && walk.x0 < end) {
+      const Piece pc = piece_of<kList, kRows>(p, walk, start, end);
+      if (pc.tiles == 0 && walk.x0 >= start) {   // rows without a token
+        for (int i = 0; i < pc.rows; ++i) {
+          const int64_t at = row_of(p, pc.tok0, pc.g, i);
+          *reinterpret_cast<uint2*>(p.a.out + at * kD + 4 * lane) = make_uint2(0, 0);
+          if (p.a.lse && lane == 0) p.a.lse[at] = -INFINITY;
         }
-        const int64_t own = static_cast<int64_t>(max(row, 0)) * kKv4Groups;
-        cp_async8(at + kTileCodes + lane * kKv4Groups, p.a.kv.K_sf + own, row >= 0 ? 8 : 0);
-        cp_async8(at + 2 * kTileCodes + kTileScales + lane * kKv4Groups, p.a.kv.V_sf + own, row >= 0 ? 8 : 0);
       }
-      cp_async_commit();
-      put = put + 1 == kStages ? 0 : put + 1;
-      next_rows();
-    };
+      if (pc.n > 0) {
+        if (lane == 0) S.queue[warp][pushed % kQueue] = pc;
+        ++pushed;
+        lt = pc.t0;
+        left = pc.n;
+      }
+      walk_on<kList, kRows>(p, walk);
+    }
+    __syncwarp();
+    tok_any = left > 0;
+    tok = -1;
+    if (tok_any) {
+      const Piece& pc = S.queue[warp][(pushed - 1) % kQueue];
+      tok = token_of_slot<kList>(p, pc, lt * kTile + lane);
+      tok_b = pc.b;
+      tok_g = pc.g;
+      ++lt;
+      --left;
+    }
+  };
+  auto next_rows = [&]() {
+    row_any = tok_any;
+    row = -1;
+    if (tok >= 0) {
+      row = static_cast<int>(cache_row(p.a.pm, tok_b, tok_g, p.Hkv, p.n_cap, tok));
+      if (row < 0) record_error(p.err, kErrBadPage);
+    }
     next_tokens();
+  };
+  uint32_t put = 0;   // stage that the next copies go to
+  auto issue = [&]() {
+    if (row_any) {
+      const uint32_t at = ring_s + put * kStage;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rk = __shfl_sync(0xffffffffu, row, r + 8 * i);
+        // V rows stand with the low bits of their number swapped and their chunks
+        // turned by a half where bit 2 is set: a lane's four tokens, 2j and 2j + 1 of
+        // eight, are then in banks of their own.
+        const int rv = __shfl_sync(0xffffffffu, row, ((r & 4) | (r & 1) << 1 | (r >> 1 & 1)) + 8 * i);
+        cp_async16(at + (r + 8 * i) * kKv4Codes + 16 * j, p.a.kv.K + static_cast<int64_t>(max(rk, 0)) * kKv4Codes + 16 * j,
+                   rk >= 0 ? 16 : 0);
+        cp_async16(at + kTileCodes + kTileScales + (r + 8 * i) * kKv4Codes + 16 * (j ^ (r >> 1 & 2)),
+                   p.a.kv.V + static_cast<int64_t>(max(rv, 0)) * kKv4Codes + 16 * j, rv >= 0 ? 16 : 0);
+      }
+      const int64_t own = static_cast<int64_t>(max(row, 0)) * kKv4Groups;
+      cp_async8(at + kTileCodes + lane * kKv4Groups, p.a.kv.K_sf + own, row >= 0 ? 8 : 0);
+      cp_async8(at + 2 * kTileCodes + kTileScales + lane * kKv4Groups, p.a.kv.V_sf + own, row >= 0 ? 8 : 0);
+    }
+    cp_async_commit();
+    put = put + 1 == kStages ? 0 : put + 1;
     next_rows();
+  };
+  next_tokens();
+  next_rows();
 #pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) issue();
-    uint32_t take = 0;   // stage of the next tile
+  for (int i = 0; i < kStages - 1; ++i) issue();
+  uint32_t take = 0;   // stage of the next tile
 
-    for (int ip = 0; ip < np; ++ip) {
-      const Piece pc = S.piece[ip];
-      if (pc.n == 0 && !pc.whole) continue;
+  for (int done = 0; done < pushed; ++done) {
+    __syncwarp();
+    const Piece pc = S.queue[warp][done % kQueue];
 
-      // ---- queries: column 8 nt + r of the group's rows; a lane holds 32 values
-      uint32_t qf[kNT][16];
-      float cs[kNT][2];   // of columns 2j, 2j + 1: logits in log2 units per unit of the product
+    // ---- queries: column 8 nt + r of the group's rows; a lane holds 32 values
+    uint32_t qf[kNT][16];
+    float cs[kNT][2];   // of columns 2j, 2j + 1: logits in log2 units per unit of the product
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        const int col = 8 * nt + r;
-        uint4 x[4];
-        uint32_t top = 0;
+    for (int nt = 0; nt < kNT; ++nt) {
+      const int col = 8 * nt + r;
+      uint4 x[4];
+      uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (col < pc.rows) {
-            const int64_t at = static_cast<int64_t>(pc.tok0 + (col >> p.gsh)) * p.Hq + (pc.g << p.gsh) + (col & ((1 << p.gsh) - 1));
-            x[i] = __ldg(reinterpret_cast<const uint4*>(p.a.q + at * kD + 32 * j) + i);
+      for (int i = 0; i < 4; ++i) {
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (col < pc.rows) x[i] = __ldg(reinterpret_cast<const uint4*>(p.a.q + row_of(p, pc.tok0, pc.g, col) * kD + 32 * j) + i);
+        const uint32_t m = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                    __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+        top = max(top, max(m & 0xffffu, m >> 16));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int ex = min(max(static_cast<int>(top >> 7), 32), 254);   // 2^(ex - 127) <= largest value
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);     // to 2^14 ..
+      const float down = __uint_as_float(static_cast<uint32_t>(127 + ex - 141) << 23) * (kScale / kKv4HalfScale) * p.a.kv.k_scale;
+      cs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * j);
+      cs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * j + 4);
+      const uint32_t* w = &x[0].x;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 f = bf2_to_f2(w[i]);
+        qf[nt][i] = pack_half(f.x * up, f.y * up);
+      }
+    }
+
+    float o[8][kNT][4];
+    float mx[kNT][2], l[kNT][2];
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      mx[nt][0] = mx[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.0f;
+    }
+
+    for (int t = pc.t0; t < pc.t0 + pc.n; ++t) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      issue();   // into the stage that the tile before this one has left
+      const uint8_t* st = ring + take * kStage;
+      take = take + 1 == kStages ? 0 : take + 1;
+
+      // ---- S^T = K Q^T
+      float s[2][kNT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.0f;
+        const int row0 = 16 * mt + r;
+        const uint4 k0 = *reinterpret_cast<const uint4*>(st + row0 * kKv4Codes + 16 * j);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(st + (row0 + 8) * kKv4Codes + 16 * j);
+        const __half2 f0 = kv4_scales(*reinterpret_cast<const uint16_t*>(st + kTileCodes + row0 * kKv4Groups + 2 * j));
+        const __half2 f1 = kv4_scales(*reinterpret_cast<const uint16_t*>(st + kTileCodes + (row0 + 8) * kKv4Groups + 2 * j));
+        const uint32_t* w0 = &k0.x;
+        const uint32_t* w1 = &k1.x;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const __half2 g0 = w < 2 ? __low2half2(f0) : __high2half2(f0), g1 = w < 2 ? __low2half2(f1) : __high2half2(f1);
+          __half2 c0[4], c1[4];
+          kv4_codes(w0[w], c0);
+          kv4_codes(w1[w], c1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a0 = bits(__hmul2(c0[2 * h], g0)), a1 = bits(__hmul2(c1[2 * h], g1));
+            const uint32_t a2 = bits(__hmul2(c0[2 * h + 1], g0)), a3 = bits(__hmul2(c1[2 * h + 1], g1));
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) mma16816(s[mt][nt], a0, a1, a2, a3, qf[nt][4 * w + 2 * h], qf[nt][4 * w + 2 * h + 1]);
           }
-          const uint32_t m = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                      __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
-          top = max(top, max(m & 0xffffu, m >> 16));
-        }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int ex = min(max(static_cast<int>(top >> 7), 32), 254);   // 2^(ex - 127) <= largest value
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);     // to 2^14 ..
-        const float down = __uint_as_float(static_cast<uint32_t>(127 + ex - 141) << 23) * (kScale / kKv4HalfScale) * p.a.kv.k_scale;
-        cs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * j);
-        cs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * j + 4);
-        const uint32_t* w = &x[0].x;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 f = bf2_to_f2(w[i]);
-          qf[nt][i] = pack_half(f.x * up, f.y * up);
         }
       }
 
-      float o[8][kNT][4];
-      float mx[kNT][2], l[kNT][2];
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        mx[nt][0] = mx[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.0f;
+      // ---- logits, masked where the tile is not attended to as a whole
+      bool full = kTile * (t + 1) <= pc.cnt;
+      if (!kList && full && pc.p0 != pc.p1) {
+        const int a0 = kTile * t, a1 = a0 + kTile - 1;
+        const int first = pc.lo + max(a0, pc.head) - pc.head, last = a1 < pc.head ? a1 : pc.lo + a1 - pc.head;
+        full = last <= pc.p0 && (a1 < pc.head || first > pc.p1 - p.a.local);
       }
-
-      for (int t = pc.t0 + warp; t < pc.t0 + pc.n; t += kWarps) {
-        cp_async_wait<kStages - 2>();
-        __syncwarp();
-        issue();   // into the stage that the tile before this one has left
-        const uint8_t* st = ring + take * kStage;
-        take = take + 1 == kStages ? 0 : take + 1;
-
-        // ---- S^T = K Q^T
-        float s[2][kNT][4];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.0f;
-          const int row0 = 16 * mt + r;
-          const uint4 k0 = *reinterpret_cast<const uint4*>(st + row0 * kKv4Codes + 16 * j);
-          const uint4 k1 = *reinterpret_cast<const uint4*>(st + (row0 + 8) * kKv4Codes + 16 * j);
-          const __half2 f0 = kv4_scales(*reinterpret_cast<const uint16_t*>(st + kTileCodes + row0 * kKv4Groups + 2 * j));
-          const __half2 f1 = kv4_scales(*reinterpret_cast<const uint16_t*>(st + kTileCodes + (row0 + 8) * kKv4Groups + 2 * j));
-          const uint32_t* w0 = &k0.x;
-          const uint32_t* w1 = &k1.x;
+        for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const __half2 g0 = w < 2 ? __low2half2(f0) : __high2half2(f0), g1 = w < 2 ? __low2half2(f1) : __high2half2(f1);
-            __half2 c0[4], c1[4];
-            kv4_codes(w0[w], c0);
-            kv4_codes(w1[w], c1);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t a0 = bits(__hmul2(c0[2 * h], g0)), a1 = bits(__hmul2(c1[2 * h], g1));
-              const uint32_t a2 = bits(__hmul2(c0[2 * h + 1], g0)), a3 = bits(__hmul2(c1[2 * h + 1], g1));
-#pragma unroll
-              for (int nt = 0; nt < kNT; ++nt) mma16816(s[mt][nt], a0, a1, a2, a3, qf[nt][4 * w + 2 * h], qf[nt][4 * w + 2 * h + 1]);
-            }
-          }
-        }
-
-        // ---- logits, masked where the tile is not attended to as a whole
-        bool full = kTile * (t + 1) <= pc.cnt;
-        if (!kList && full && pc.p0 != pc.p1) {
-          const int a0 = kTile * t, a1 = a0 + kTile - 1;
-          const int first = pc.lo + max(a0, pc.head) - pc.head, last = a1 < pc.head ? a1 : pc.lo + a1 - pc.head;
-          full = last <= pc.p0 && (a1 < pc.head || first > pc.p1 - p.a.local);
-        }
+          for (int e = 0; e < 4; ++e) s[mt][nt][e] *= cs[nt][e & 1];
+      if (!full) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
+          for (int h = 0; h < 2; ++h) {
+            const int slot = kTile * t + 16 * mt + 8 * h + r;
+            const int token = kList ? 0 : (slot < pc.head ? slot : pc.lo + slot - pc.head);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][nt][e] *= cs[nt][e & 1];
-        if (!full) {
+            for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int slot = kTile * t + 16 * mt + 8 * h + r;
-              const int token = kList ? 0 : (slot < pc.head ? slot : pc.lo + slot - pc.head);
-#pragma unroll
-              for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  const int pos = pc.p0 + ((8 * nt + 2 * j + c) >> p.gsh);
-                  const bool seen = slot < pc.cnt && (kList || (token <= pos && (token > pos - p.a.local || token < p.a.sink)));
-                  if (!seen) s[mt][nt][2 * h + c] = -INFINITY;
-                }
-            }
-        }
+              for (int c = 0; c < 2; ++c) {
+                const int pos = pc.p0 + ((8 * nt + 2 * j + c) >> p.gsh);
+                const bool seen = slot < pc.cnt && (kList || (token <= pos && (token > pos - p.a.local || token < p.a.sink)));
+                if (!seen) s[mt][nt][2 * h + c] = -INFINITY;
+              }
+          }
+      }
 
-        // ---- the rows' maxima: the base moves where one grew by more than kGrow
-        bool grown = false;
-        float top[kNT][2];
+      // ---- the rows' maxima: the base moves where one grew by more than kGrow
+      bool grown = false;
+      float top[kNT][2];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          top[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]), fmaxf(s[1][nt][c], s[1][nt][2 + c]));
+          grown |= top[nt][c] > mx[nt][c] + kGrow;
+        }
+      if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            top[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]), fmaxf(s[1][nt][c], s[1][nt][2 + c]));
-            grown |= top[nt][c] > mx[nt][c] + kGrow;
-          }
-        if (__any_sync(0xffffffffu, grown)) {
+            float m = top[nt][c];
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
+            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            if (m > mx[nt][c]) {
+              const float f = ex2_approx(mx[nt][c] - m);   // 0 for the first
+              mx[nt][c] = m;
+              l[nt][c] *= f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float m = top[nt][c];
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-              if (m > mx[nt][c]) {
-                const float f = ex2_approx(mx[nt][c] - m);   // 0 for the first
-                mx[nt][c] = m;
-                l[nt][c] *= f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  o[i][nt][c] *= f;
-                  o[i][nt][2 + c] *= f;
-                }
+              for (int i = 0; i < 8; ++i) {
+                o[i][nt][c] *= f;
+                o[i][nt][2 + c] *= f;
               }
             }
-        }
+          }
+      }
 
-        // ---- P, and turned to the second product's operand
-        uint32_t pf[2][kNT][2];
+      // ---- P, and turned to the second product's operand
+      uint32_t pf[2][kNT][2];
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          const float b0 = mx[nt][0] == -INFINITY ? 0.0f : mx[nt][0] - kBase;
-          const float b1 = mx[nt][1] == -INFINITY ? 0.0f : mx[nt][1] - kBase;
+      for (int nt = 0; nt < kNT; ++nt) {
+        const float b0 = mx[nt][0] == -INFINITY ? 0.0f : mx[nt][0] - kBase;
+        const float b1 = mx[nt][1] == -INFINITY ? 0.0f : mx[nt][1] - kBase;
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float p0 = ex2_approx(s[mt][nt][2 * h] - b0), p1 = ex2_approx(s[mt][nt][2 * h + 1] - b1);
-              l[nt][0] += p0;
-              l[nt][1] += p1;
-              pf[mt][nt][h] = transpose8x8(pack_half(p0, p1));
-            }
-        }
-
-        // ---- O^T += V^T P^T: channels 16 r + 2 i and + 1 are rows r and r + 8 of tile i
-        const uint8_t* vt = st + kTileCodes + kTileScales;
-        const uint8_t* vf = vt + kTileCodes + r;
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          uint2 w[2][2];
-          __half2 f[2];
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int at = 16 * mt + 8 * h + ((j & 1) | e << 1 | (j & 2) << 1);
-              w[h][e] = *reinterpret_cast<const uint2*>(vt + at * kKv4Codes + 16 * ((r >> 1) ^ (j & 2)) + 8 * (r & 1));
-            }
-            const uint8_t* sf = vf + (16 * mt + 8 * h + 2 * j) * kKv4Groups;
-            f[h] = kv4_scales(sf[0] | static_cast<uint32_t>(sf[kKv4Groups]) << 8);
+            const float p0 = ex2_approx(s[mt][nt][2 * h] - b0), p1 = ex2_approx(s[mt][nt][2 * h + 1] - b1);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            pf[mt][nt][h] = transpose8x8(pack_half(p0, p1));
           }
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            __half2 ev[2][4], od[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t x = half ? w[h][0].y : w[h][0].x, y = half ? w[h][1].y : w[h][1].x;
-              kv4_codes((x & 0x0f0f0f0fu) | (y << 4 & 0xf0f0f0f0u), ev[h]);
-              kv4_codes((x >> 4 & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), od[h]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t a0 = bits(__hmul2(ev[0][i], f[0])), a1 = bits(__hmul2(od[0][i], f[0]));
-              const uint32_t a2 = bits(__hmul2(ev[1][i], f[1])), a3 = bits(__hmul2(od[1][i], f[1]));
-#pragma unroll
-              for (int nt = 0; nt < kNT; ++nt) mma16816(o[4 * half + i][nt], a0, a1, a2, a3, pf[mt][nt][0], pf[mt][nt][1]);
-            }
-          }
-        }
       }
 
-      // ---- the warps' rows joined
+      // ---- O^T += V^T P^T: channels 16 r + 2 i and + 1 are rows r and r + 8 of tile i
+      const uint8_t* vt = st + kTileCodes + kTileScales;
+      const uint8_t* vf = vt + kTileCodes + r;
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int mt = 0; mt < 2; ++mt) {
+        uint2 w[2][2];
+        __half2 f[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
-          if (r == 0) S.m[warp][8 * nt + 2 * j + c] = mx[nt][c];
+          for (int e = 0; e < 2; ++e) {
+            const int at = 16 * mt + 8 * h + ((j & 1) | e << 1 | (j & 2) << 1);
+            w[h][e] = *reinterpret_cast<const uint2*>(vt + at * kKv4Codes + 16 * ((r >> 1) ^ (j & 2)) + 8 * (r & 1));
+          }
+          const uint8_t* sf = vf + (16 * mt + 8 * h + 2 * j) * kKv4Groups;
+          f[h] = kv4_scales(sf[0] | static_cast<uint32_t>(sf[kKv4Groups]) << 8);
         }
-      __syncthreads();
-      float all[kNT][2], f[kNT][2];
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+        for (int half = 0; half < 2; ++half) {
+          __half2 ev[2][4], od[2][4];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float m = -INFINITY;
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = half ? w[h][0].y : w[h][0].x, y = half ? w[h][1].y : w[h][1].x;
+            kv4_codes((x & 0x0f0f0f0fu) | (y << 4 & 0xf0f0f0f0u), ev[h]);
+            kv4_codes((x >> 4 & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), od[h]);
+          }
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) m = fmaxf(m, S.m[w][8 * nt + 2 * j + c]);
-          all[nt][c] = m;
-          f[nt][c] = m == -INFINITY ? 1.0f : ex2_approx(mx[nt][c] - m);
-          if (r == 0) S.l[warp][8 * nt + 2 * j + c] = l[nt][c] * f[nt][c];
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = bits(__hmul2(ev[0][i], f[0])), a1 = bits(__hmul2(od[0][i], f[0]));
+            const uint32_t a2 = bits(__hmul2(ev[1][i], f[1])), a3 = bits(__hmul2(od[1][i], f[1]));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            o[i][nt][c] *= f[nt][c];
-            o[i][nt][2 + c] *= f[nt][c];
+            for (int nt = 0; nt < kNT; ++nt) mma16816(o[4 * half + i][nt], a0, a1, a2, a3, pf[mt][nt][0], pf[mt][nt][1]);
           }
         }
-#pragma unroll
-      for (int n = kWarps; n > 1; n = (n + 1) / 2) {
-        const int keep = (n + 1) / 2;
-        if (warp >= keep && warp < n) {
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(&S.o[warp - keep][8 * nt + 2 * j + c][16 * r + 4 * i]) =
-                    make_float4(o[2 * i][nt][c], o[2 * i][nt][2 + c], o[2 * i + 1][nt][c], o[2 * i + 1][nt][2 + c]);
-        }
-        __syncthreads();
-        if (warp < n - keep) {
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float4 y = *reinterpret_cast<const float4*>(&S.o[warp][8 * nt + 2 * j + c][16 * r + 4 * i]);
-                o[2 * i][nt][c] += y.x;
-                o[2 * i][nt][2 + c] += y.y;
-                o[2 * i + 1][nt][c] += y.z;
-                o[2 * i + 1][nt][2 + c] += y.w;
-              }
-        }
-        if (n > 2) __syncthreads();
       }
-      if (warp == 0) {
-        const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + pc.slot) * kRows;
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int col = 8 * nt + 2 * j + c;
-            if (col >= pc.rows) continue;
-            float sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) sum += S.l[w][col];
-            if (pc.whole) {
-              const int64_t at = static_cast<int64_t>(pc.tok0 + (col >> p.gsh)) * p.Hq + (pc.g << p.gsh) + (col & ((1 << p.gsh) - 1));
-              const float inv = sum != 0.0f ? p.a.kv.v_scale / kKv4HalfScale / sum : 0.0f;
-              uint4* dst = reinterpret_cast<uint4*>(p.a.out + at * kD + 16 * r);
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                dst[i] = make_uint4(pack_bf16(o[4 * i][nt][c] * inv, o[4 * i][nt][2 + c] * inv),
-                                    pack_bf16(o[4 * i + 1][nt][c] * inv, o[4 * i + 1][nt][2 + c] * inv),
-                                    pack_bf16(o[4 * i + 2][nt][c] * inv, o[4 * i + 2][nt][2 + c] * inv),
-                                    pack_bf16(o[4 * i + 3][nt][c] * inv, o[4 * i + 3][nt][2 + c] * inv));
-              if (p.a.lse && r == 0)
-                p.a.lse[at] = sum != 0.0f ? (all[nt][c] == -INFINITY ? sum : (all[nt][c] - kBase + log2f(sum)) * 0.6931471805599453f)
-                                          : -INFINITY;
-            } else {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + (part + col) * kD + 16 * r);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                dst[i] = make_float4(o[2 * i][nt][c], o[2 * i][nt][2 + c], o[2 * i + 1][nt][c], o[2 * i + 1][nt][2 + c]);
-              if (r == 0) p.part_ml[part + col] = make_float2(all[nt][c], sum);
-            }
-          }
-        if (lane == 0 && !pc.whole && pc.slot == 1) {
-          Share sh;
-          sh.first = (static_cast<int64_t>(pc.tok0) << p.gsh);
-          sh.rows = pc.rows;
-          sh.g = pc.g;
-          sh.last = pc.last;
-          sh.pad = 0;
-          p.share[blockIdx.x] = sh;
-          S.shared_out = 1;
-        }
-      }
-      __syncthreads();   // S.m, S.l and S.o are the next piece's
     }
-    __syncthreads();     // the pieces are the next batch's
+
+    // ---- the piece's rows
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+    const bool begins = pc.t0 == 0, ends = pc.t0 + pc.n == pc.tiles;
+    if (begins && ends) {
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = 8 * nt + 2 * j + c;
+          if (col >= pc.rows) continue;
+          const int64_t at = row_of(p, pc.tok0, pc.g, col);
+          const float inv = inverse_of(p, l[nt][c]);
+          uint4* dst = reinterpret_cast<uint4*>(p.a.out + at * kD + 16 * r);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            dst[i] = make_uint4(pack_bf16(o[4 * i][nt][c] * inv, o[4 * i][nt][2 + c] * inv),
+                                pack_bf16(o[4 * i + 1][nt][c] * inv, o[4 * i + 1][nt][2 + c] * inv),
+                                pack_bf16(o[4 * i + 2][nt][c] * inv, o[4 * i + 2][nt][2 + c] * inv),
+                                pack_bf16(o[4 * i + 3][nt][c] * inv, o[4 * i + 3][nt][2 + c] * inv));
+          if (p.a.lse && r == 0) p.a.lse[at] = lse_of(mx[nt][c], l[nt][c]);
+        }
+    } else {
+      // The item that goes on behind this warp's range is its last: its ring is free by then.
+      if (begins) cp_async_wait<0>();
+      __syncwarp();
+      Part<kRows>& to = begins ? *reinterpret_cast<Part<kRows>*>(ring) : S.first[warp];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = 8 * nt + 2 * j + c;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            to.o[col][(4 * r + i) ^ j] = make_float4(o[2 * i][nt][c], o[2 * i][nt][2 + c], o[2 * i + 1][nt][c], o[2 * i + 1][nt][2 + c]);
+          if (r == 0) to.ml[col] = make_float2(mx[nt][c], l[nt][c]);
+        }
+      if (lane == 0) {
+        S.part[2 * warp + begins] = pc;
+        S.there[2 * warp + begins] = ends ? 2 : 1;
+      }
+    }
   }
-  if (tid == 0 && S.shared_out == 0 && p.share) p.share[blockIdx.x].rows = 0;
+
+  // ---- the warps' parts joined: a chain begins with an item's first part, or with
+  // the block's first one where the item began before; parts of earlier items of a
+  // warp (even places) continue it until one ends.  A warp joins a row.
+  __syncthreads();
+  bool left_over = false;   // an item goes on behind the block
+  int before = 0;           // parts before place i
+  for (int i = 0; i < 2 * kWarps; ++i) {
+    if (S.there[i] == 0) continue;
+    const bool begins = (i & 1) != 0, head = begins || before == 0;
+    ++before;
+    if (!head) continue;
+    const Piece& pc = S.part[i];
+    int last = i;
+    bool ends = S.there[i] == 2;
+    for (int k = (i | 1) + 1; k < 2 * kWarps && !ends; k += 2)
+      if (S.there[k] != 0) {
+        last = k;
+        ends = S.there[k] == 2;
+      }
+    const bool whole = begins && ends;
+    left_over |= begins && !ends;
+    for (int col = warp; col < pc.rows; col += kWarps) {
+      float m = -INFINITY, l = 0.0f;
+      auto part = [&](int k) -> const Part<kRows>& {
+        return (k & 1) ? *reinterpret_cast<const Part<kRows>*>(S.ring[k >> 1]) : S.first[k >> 1];
+      };
+      for (int k = i; k <= last; k = (k | 1) + 1)
+        if (S.there[k] != 0) m = fmaxf(m, part(k).ml[col].x);
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int k = i; k <= last; k = (k | 1) + 1) {
+        if (S.there[k] == 0) continue;
+        const float2 ml = part(k).ml[col];
+        const float f = m == -INFINITY ? 1.0f : ex2_approx(ml.x - m);
+        const float4 y = part(k).o[col][lane ^ (col >> 1 & 3)];
+        l += ml.y * f;
+        o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
+      }
+      if (whole) {
+        const int64_t at = row_of(p, pc.tok0, pc.g, col);
+        const float inv = inverse_of(p, l);
+        *reinterpret_cast<uint2*>(p.a.out + at * kD + 4 * lane) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        if (p.a.lse && lane == 0) p.a.lse[at] = lse_of(m, l);
+      } else {
+        const int64_t to = (static_cast<int64_t>(blockIdx.x) * 2 + begins) * kRows + col;
+        *(reinterpret_cast<float4*>(p.part_o + to * kD) + lane) = o;
+        if (lane == 0) p.part_ml[to] = make_float2(m, l);
+      }
+    }
+    if (tid == 0 && begins && !ends) {
+      Share sh;
+      sh.first = static_cast<int64_t>(pc.tok0) << p.gsh;
+      sh.rows = pc.rows;
+      sh.g = pc.g;
+      sh.last = line.block(pc.x0 + kItemCost + pc.tiles - 1);
+      sh.pad = 0;
+      p.share[blockIdx.x] = sh;
+    }
+  }
+  if (tid == 0 && !left_over && !p.whole) p.share[blockIdx.x].rows = 0;
   pdl_trigger();
 }
 
@@ -756,11 +809,10 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Args p) 
     }
     const int64_t row = sh.first + col;
     const int64_t at = (row >> p.gsh) * p.Hq + (sh.g << p.gsh) + (row & ((1 << p.gsh) - 1));
-    const float inv = l != 0.0f ? p.a.kv.v_scale / kKv4HalfScale / l : 0.0f;
+    const float inv = inverse_of(p, l);
     *reinterpret_cast<uint2*>(p.a.out + at * kD + 4 * chunk) =
         make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (p.a.lse && chunk == 0)
-      p.a.lse[at] = l != 0.0f ? (m == -INFINITY ? l : (m - kBase + log2f(l)) * 0.6931471805599453f) : -INFINITY;
+    if (p.a.lse && chunk == 0) p.a.lse[at] = lse_of(m, l);
   }
   pdl_trigger();
 }
@@ -783,7 +835,7 @@ Kernel kernel_of(int nt, bool list) {
 }
 Kernel merge_of(int nt) { return nt == 1 ? kv4_merge_kernel<1> : kv4_merge_kernel<2>; }
 size_t smem_of(int nt) { return nt == 1 ? sizeof(Smem<1>) : sizeof(Smem<2>); }
-static_assert(sizeof(Smem<2>) <= 232448, "shared memory of a block");
+static_assert(sizeof(Smem<1>) <= 232448 && sizeof(Smem<2>) <= 232448, "shared memory of a block");
 
 // Columns of an item: single tokens have at most eight.
 int tiles_of(const qasc_shape& s, int64_t max_q) { return max_q * (s.Hq / s.Hkv) <= 8 ? 1 : 2; }
@@ -816,7 +868,12 @@ int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, size
     p.sink_end = static_cast<int>(R.sink_end);
     p.local_start = static_cast<int>(R.local_start);
   }
+  while ((s.B - 1) >> p.ssh >= kSums) ++p.ssh;
   p.err = dev.err_word;
+  // Items of few tiles are not shared between blocks, which saves the merge.
+  const int64_t most = a.listed ? p.sink_end + static_cast<int64_t>(a.K) + (p.n - p.local_start)
+                                : std::min<int64_t>(s.n_cap, static_cast<int64_t>(a.local) + a.sink + a.max_q - 1);
+  p.whole = most <= kWholeTokens;
   const int nt = a.listed ? 1 : tiles_of(s, a.max_q);
   const int grid = dev.num_sms;
   const Layout L = layout_of(8 * nt, grid);
@@ -824,8 +881,8 @@ int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, size
   p.share = reinterpret_cast<Share*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);
   p.part_o = reinterpret_cast<float*>(ws + L.off_o);
-  cudaError_t e = launch_dependent(kernel_of(nt, a.listed), dim3(grid), dim3(kThreads), smem_of(nt), stream, 1, p);
-  if (e != cudaSuccess) return static_cast<int>(e);
+  cudaError_t e = launch_dependent(kernel_of(nt, a.listed), dim3(grid), dim3(32 * warps_of(nt)), smem_of(nt), stream, 1, p);
+  if (e != cudaSuccess || p.whole) return static_cast<int>(e);
   e = launch_dependent(merge_of(nt), dim3(grid), dim3(kMergeThreads), 0, stream, 1, p);
   return static_cast<int>(e);
 }
