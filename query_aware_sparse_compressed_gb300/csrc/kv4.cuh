@@ -5,7 +5,7 @@
 // exponent bits, one mantissa bit: 0 0.5 1 1.5 2 3 4 6, the even i of a pair
 // in a byte's low half), scale an e4m3, t the cache's own factor, a power of
 // two.  4.5 bits a value.  A code has 2 significant bits and a scale 4, so that
-// scale * code is exact in bf16 and, with the factor below, in fp16.
+// scale * code, 2^-10 to 2688 or 0, is exact in bf16 and in fp16.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -18,15 +18,11 @@ constexpr int kKv4Group = 16;                    // values of a scale
 constexpr int kKv4Groups = kD / kKv4Group;       // scales of a row, bytes
 constexpr int kKv4Codes = kD / 2;                // bytes of a row's codes
 
-// Scales are taken to fp16 times 2^-7: scale * code reaches 448 * 6 = 2688, and
-// its smallest step 2^-9 * 0.5 is 2^-17 then, a whole number of fp16's 2^-24.
-constexpr float kKv4HalfScale = 0.0078125f;
-
-// Two e4m3 of a word's low 16 bits -> fp16 pair times 2^-7 (exact).
+// Two e4m3 of a word's low 16 bits -> fp16 pair (exact).
 __device__ __forceinline__ __half2 kv4_scales(uint32_t two) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-  return __hmul2(*reinterpret_cast<__half2*>(&h), __half2half2(__ushort_as_half(0x2000)));   // 2^-7
+  return *reinterpret_cast<__half2*>(&h);
 }
 
 // The four bytes of w, two codes each -> fp16 pairs (low code, high code).

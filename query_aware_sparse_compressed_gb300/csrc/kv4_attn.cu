@@ -68,6 +68,7 @@ constexpr int kStage = 2 * (kTileCodes + kTileScales);
 constexpr int kSums = 512;                     // places are summed for as many groups of sequences at most
 constexpr int kQueue = 8;                      // items that a warp's loads are ahead of its products, at most
 constexpr int kItemCost = KV4_C;                   // places of an item beside its tiles: queries, output
+constexpr int kTilesMost = (1 << 24) / kTile;  // n_cap < 2^24
 constexpr int kLeast = 8;                      // places that a block takes at least
 constexpr int kWholeTokens = 1024;             // an item of more tokens may be shared between blocks
 constexpr float kBase = 10.0f;                 // log2 of P at the maximum that the base was taken from
@@ -83,6 +84,7 @@ struct Args {
   int64_t most_rows;        // sequences with more rows are left out (0: none)
   int whole;                // items are not shared between blocks
   int ssh;                  // sequences of a sum: 2^ssh
+  int ush;                  // tiles of a place: 2^ush, so that the line has fewer than 2^31 places
   float* part_o;            // [grid][2][rows][128]
   float2* part_ml;          // [grid][2][rows] (max in log2 units, sum)
   struct Share* share;      // [grid] the item that a block shares with those behind it
@@ -102,10 +104,12 @@ struct alignas(16) Piece {
   int tok0, rows;      // first query token, rows
   int b, g;
   int p0, p1;          // positions of the first and last row
-  int lo;              // window: token behind the sink's; listed: list's entries
-  int head, cnt;       // tokens of the sink, of all
+  int lo;              // window: token of the slot behind the sink's, a multiple of 32; listed: list's entries
+  int head, cnt;       // slots of the sink, of all
   int t0, n, tiles;
-  int64_t x0;          // its first place on the line
+  int m0, m1;          // tiles [m0, m1) are attended to as a whole by every row
+  int x0;              // its first place on the line
+  int64_t base;        // the sequence's first entry of the block table, or the KV head's first row
 };
 
 struct Seq {
@@ -114,7 +118,7 @@ struct Seq {
 
 // Where a warp's loads stand on the line: item `rem` of sequence b's `items`.
 struct Walk {
-  int64_t x0;          // the item's first place
+  int x0;              // the item's first place
   int b, rem, items, span;
   Seq s;
 };
@@ -174,18 +178,31 @@ __device__ __forceinline__ int span_of(const Args& p, const Seq& s, int b) {
     for (int g = 0; g < (p.a.sel_per_kv ? p.Hkv : 1); ++g) most = max(most, list_len(p, b, g));
     cnt = p.sink_end + most + (p.n - p.local_start);
   } else {
-    cnt = min(static_cast<int64_t>(s.len),
-              static_cast<int64_t>(p.a.local) + min(s.ql, kRows >> p.gsh) - 1 + p.a.sink);
+    // the sink's tiles, the window's, and one more where it begins inside a tile
+    const int64_t window = (static_cast<int64_t>(p.a.local) + min(s.ql, kRows >> p.gsh) - 1 + 2 * (kTile - 1)) / kTile;
+    cnt = min((static_cast<int64_t>(s.len) + kTile - 1) / kTile, window + (static_cast<int64_t>(p.a.sink) + kTile - 1) / kTile) * kTile;
   }
-  return static_cast<int>((cnt + kTile - 1) / kTile) + kItemCost;
+  return static_cast<int>(((cnt + kTile - 1) / kTile + (1 << p.ush) - 1) >> p.ush) + kItemCost;
 }
 
-// A line of U places over G blocks: block c has the places [c U / G, (c + 1) U / G).
+// A line of U places over G blocks: block c has the places [c U / G, (c + 1) U / G),
+// in 32 bits (64-bit divisions at a block's start cost it 2 us).
 struct Line {
-  int64_t U;
-  int G;
-  __device__ __forceinline__ int64_t start(int c) const { return c * U / G; }
-  __device__ __forceinline__ int block(int64_t x) const { return static_cast<int>(((x + 1) * G - 1) / U); }
+  unsigned U, G, q, r;
+  __device__ __forceinline__ Line(int places, int grid) {
+    U = places;
+    G = grid;
+    q = U / G;
+    r = U - q * G;
+  }
+  __device__ __forceinline__ int start(unsigned c) const { return static_cast<int>(c * q + c * r / G); }
+  // The block that holds place x.
+  __device__ __forceinline__ int block(int x) const {
+    int c = min(static_cast<int>(__fdividef(static_cast<float>(x) * static_cast<float>(G), static_cast<float>(U))), static_cast<int>(G) - 1);
+    while (start(c) > x) --c;
+    while (start(c + 1) <= x) ++c;
+    return c;
+  }
 };
 
 template <int kNT>
@@ -197,11 +214,17 @@ struct Smem {
   Piece queue[kWarps][kQueue];
   Piece part[2 * kWarps];        // of every warp: the item that it shares with earlier ones, with later ones
   int there[2 * kWarps];         // 0: none, 1: the item goes on, 2: it ends here
-  int64_t place[kSums + 1];      // places before a group of sequences
+  int place[kSums + 1];          // places before a group of sequences
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {   // the rest zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -215,7 +238,7 @@ __device__ __forceinline__ void cp_async_wait() {
 // c (+)= A (16 x 16, rows) B (16 x 8, columns), fp16 operands.
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -242,15 +265,26 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l != 0.0f ? (m == -INFINITY ? l : (m - kBase + log2f(l)) * 0.6931471805599453f) : -INFINITY;
 }
 __device__ __forceinline__ float inverse_of(const Args& p, float l) {
-  return l != 0.0f ? p.a.kv.v_scale / kKv4HalfScale / l : 0.0f;
+  return l != 0.0f ? p.a.kv.v_scale / l : 0.0f;
 }
 
-// Token of slot s of an item; -1 behind the last.
+// Row `pos` of a window call attends to token t.
+__device__ __forceinline__ bool attends(const Args& p, int pos, int t) {
+  return t <= pos && (t < p.a.sink || static_cast<int64_t>(t) > static_cast<int64_t>(pos) - p.a.local);
+}
+
+// Token of slot s of an item; -1: none that any of its rows attends to.  Of a window
+// call the slots of the sink end with a tile and the window's begin with a multiple of
+// 32 tokens, so that a tile never leaves its page and its rows stand in a line.
 template <bool kList>
 __device__ __forceinline__ int token_of_slot(const Args& p, const Piece& pc, int s) {
   if (s >= pc.cnt) return -1;
+  if (!kList) {
+    if (s < pc.head) return s < p.a.sink ? s : -1;
+    const int t = pc.lo + s - pc.head;
+    return t <= pc.p1 && (t < p.a.sink || static_cast<int64_t>(t) > static_cast<int64_t>(pc.p0) - p.a.local) ? t : -1;
+  }
   if (s < pc.head) return s;
-  if (!kList) return pc.lo + s - pc.head;
   const int i = s - pc.head;
   if (i >= pc.lo) return p.local_start + i - pc.lo;
   const int64_t list = p.a.sel_per_kv ? static_cast<int64_t>(pc.b) * p.Hkv + pc.g : pc.b;
@@ -262,26 +296,27 @@ __device__ __forceinline__ int token_of_slot(const Args& p, const Piece& pc, int
 
 // The item that holds place x.
 template <bool kList, int kRows>
-__device__ __forceinline__ Walk walk_at(const Args& p, const int64_t* place, int64_t x) {
+__device__ __forceinline__ Walk walk_at(const Args& p, const int* place, int x) {
   int lo = 0, hi = (p.B + (1 << p.ssh) - 1) >> p.ssh;   // the last group with place <= x
+  if (hi == 1) hi = 0;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (place[mid] <= x) lo = mid;
     else hi = mid;
   }
   Walk w;
-  int64_t at = place[lo];
+  int at = hi == 0 ? 0 : place[lo];
   for (w.b = lo << p.ssh;; ++w.b) {
     w.s = seq_of<kList>(p, w.b);
     w.items = items_of<kRows>(p, w.s);
     if (w.items == 0) continue;
     w.span = span_of<kList, kRows>(p, w.s, w.b);
-    const int64_t all = static_cast<int64_t>(w.items) * w.span;
+    const int all = w.items * w.span;
     if (x < at + all) break;
     at += all;
   }
-  w.rem = static_cast<int>((x - at) / w.span);
-  w.x0 = at + static_cast<int64_t>(w.rem) * w.span;
+  w.rem = static_cast<unsigned>(x - at) / static_cast<unsigned>(w.span);
+  w.x0 = at + w.rem * w.span;
   return w;
 }
 
@@ -302,13 +337,13 @@ __device__ __forceinline__ void walk_on(const Args& p, Walk& w) {
 
 // The part of item w on the places [start, end).
 template <bool kList, int kRows>
-__device__ __forceinline__ Piece piece_of(const Args& p, const Walk& w, int64_t start, int64_t end) {
+__device__ __forceinline__ Piece piece_of(const Args& p, const Walk& w, int start, int end) {
   Piece pc;
-  const int blocks = w.items / p.Hkv;
+  const unsigned blocks = static_cast<unsigned>(w.items) / static_cast<unsigned>(p.Hkv);
   pc.b = w.b;
-  pc.g = w.rem / blocks;
+  pc.g = blocks == 1 ? w.rem : static_cast<int>(static_cast<unsigned>(w.rem) / blocks);
   pc.x0 = w.x0;
-  const int r0 = (w.rem - pc.g * blocks) * kRows;
+  const int r0 = (w.rem - pc.g * static_cast<int>(blocks)) * kRows;
   pc.rows = static_cast<int>(min(static_cast<int64_t>(kRows), (static_cast<int64_t>(w.s.ql) << p.gsh) - r0));
   pc.tok0 = w.s.q0 + (r0 >> p.gsh);
   pc.p0 = w.s.len - w.s.ql + (r0 >> p.gsh);
@@ -319,14 +354,23 @@ __device__ __forceinline__ Piece piece_of(const Args& p, const Walk& w, int64_t 
     pc.cnt = p.sink_end + pc.lo + (p.n - p.local_start);
   } else {
     const int64_t lo = static_cast<int64_t>(pc.p0) - p.a.local + 1;
-    pc.lo = static_cast<int>(lo > 0 ? lo : 0);
-    pc.head = min(p.a.sink, pc.lo);
+    pc.lo = static_cast<int>(lo > 0 ? lo : 0) & ~(kTile - 1);
+    pc.head = p.a.sink < pc.lo ? (p.a.sink + kTile - 1) & ~(kTile - 1) : pc.lo;
+    if (pc.head >= pc.lo) pc.head = pc.lo = 0;   // the sink's tiles reach the window's
     pc.cnt = pc.p1 >= 0 ? pc.head + pc.p1 - pc.lo + 1 : 0;
   }
   pc.tiles = (pc.cnt + kTile - 1) / kTile;
-  const int64_t first = w.x0 + kItemCost;
-  pc.t0 = static_cast<int>(max(static_cast<int64_t>(0), start - first));
-  pc.n = max(0, static_cast<int>(min(static_cast<int64_t>(pc.tiles), end - first)) - pc.t0);
+  pc.m0 = 0;
+  pc.m1 = pc.cnt / kTile;
+  if (!kList) {
+    const int64_t open = static_cast<int64_t>(pc.p1) - p.a.local + 1 - pc.lo;   // tokens that the last row no longer sees
+    pc.m0 = pc.head / kTile + (open > 0 ? static_cast<int>((open + kTile - 1) / kTile) : 0);
+    pc.m1 = pc.head / kTile + (pc.p0 >= pc.lo ? (pc.p0 - pc.lo + 1) / kTile : 0);
+  }
+  pc.base = p.a.pm.table ? pc.b * p.a.pm.pages_per_seq : (static_cast<int64_t>(pc.b) * p.Hkv + pc.g) * p.n_cap;
+  const int first = w.x0 + kItemCost;
+  pc.t0 = max(0, start - first) << p.ush;
+  pc.n = max(0, min(pc.tiles, min(max(end - first, 0), (kTilesMost >> p.ush) + 1) << p.ush) - pc.t0);
   return pc;
 }
 
@@ -343,11 +387,11 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
   // ---- the line
   const int groups = (p.B + (1 << p.ssh) - 1) >> p.ssh;
   for (int i = tid; i < groups; i += kThreads) {
-    int64_t places = 0;
+    int places = 0;
     for (int b = i << p.ssh; b < min(p.B, (i + 1) << p.ssh); ++b) {
       const Seq s = seq_of<kList>(p, b);
       const int items = items_of<kRows>(p, s);
-      if (items > 0) places += static_cast<int64_t>(items) * span_of<kList, kRows>(p, s, b);
+      if (items > 0) places += items * span_of<kList, kRows>(p, s, b);
       if (!kList && blockIdx.x == 0) {
         const int len = __ldg(p.a.bt.lens + b);
         if (len < 0 || len > p.n_cap) record_error(p.err, kErrBadPage);
@@ -357,42 +401,45 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
   }
   if (tid < 2 * kWarps) S.there[tid] = 0;
   __syncthreads();
-  if (warp == 0) {
-    int64_t places = 0;
-    for (int b0 = 0; b0 < groups; b0 += 32) {
-      const int b = b0 + lane;
-      const int64_t v = b < groups ? S.place[b] : 0;
-      int64_t vi = v;
+  if (groups > 1) {
+    if (warp == 0) {
+      int places = 0;
+      for (int b0 = 0; b0 < groups; b0 += 32) {
+        const int b = b0 + lane;
+        const int v = b < groups ? S.place[b] : 0;
+        int vi = v;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, vi, o);
-        if (lane >= o) vi += x;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, vi, o);
+          if (lane >= o) vi += x;
+        }
+        if (b < groups) S.place[b] = places + vi - v;
+        places += __shfl_sync(0xffffffffu, vi, 31);
       }
-      if (b < groups) S.place[b] = places + vi - v;
-      places += __shfl_sync(0xffffffffu, vi, 31);
+      if (lane == 0) S.place[groups] = places;
     }
-    if (lane == 0) S.place[groups] = places;
+    __syncthreads();
   }
-  __syncthreads();
-  Line line;
-  line.U = S.place[groups];
-  line.G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), p.whole ? line.U : (line.U + kLeast - 1) / kLeast));
+  const int places = groups > 1 ? S.place[groups] : S.place[0];
+  // (of one group the sum stands in place 0, whose first place is 0 all the same)
+  const Line line(places, max(1, min(static_cast<int>(gridDim.x), p.whole ? places : (places + kLeast - 1) / kLeast)));
   Walk walk;
   walk.b = p.B;
-  int64_t start = 0, end = 0;   // this warp's places
-  if (static_cast<int>(blockIdx.x) < line.G) {
+  int start = 0, end = 0;   // this warp's places
+  if (blockIdx.x < line.G && places > 0) {
     // an item belongs to the block that has its first place, where they are not shared
-    auto bound = [&](int c) {
-      int64_t x = line.start(c);
-      if (p.whole && x < line.U) {
+    auto bound = [&](unsigned c) {
+      int x = line.start(c);
+      if (p.whole && x < places) {
         const Walk w = walk_at<kList, kRows>(p, S.place, x);
         if (w.x0 < x) x = w.x0 + w.span;
       }
       return x;
     };
-    const int64_t first = bound(blockIdx.x), all = bound(blockIdx.x + 1) - first;
-    start = first + all * warp / kWarps;
-    end = first + all * (warp + 1) / kWarps;
+    const unsigned first = bound(blockIdx.x), all = bound(blockIdx.x + 1) - first;
+    const unsigned each = all / kWarps, more = all - each * kWarps;
+    start = first + each * warp + more * warp / kWarps;
+    end = first + each * (warp + 1) + more * (warp + 1) / kWarps;
     if (start < end) walk = walk_at<kList, kRows>(p, S.place, start);
   }
 
@@ -401,69 +448,105 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
 
   // ---- loads: the next tile's tokens and their rows are known a tile ahead of
   // their copies each (the block table and the list are read on the way)
+  enum { kNone, kLine, kRowwise };          // no tile; 32 rows in a line; rows of their own
   int pushed = 0;                           // items found
   int lt = 0, left = 0;                     // next tile of the newest item, tiles left of it
-  int tok = -1, tok_b = 0, tok_g = 0;       // lane's token of the tile after the next
-  int row = -1;                             // lane's row of the next tile; -1: none
-  bool row_any = false, tok_any = false;
+  int at0 = 0, m0 = 0, m1 = 0, tg = 0;      // of that item: token of tile 0's first slot in a line, whole tiles, KV head
+  int64_t base = 0;
+  int tok = -1, tok_g = 0, tok_kind = kNone;   // lane's token of the tile after the next (of a line: its first)
+  int64_t tok_base = 0;
+  int row = -1, row_kind = kNone;           // lane's row of the next tile (of a line: its first); -1: none
   auto next_tokens = [&]() {
-    while (left == 0 && walk.b < p.B && walk.x0 < end) {
-      const Piece pc = piece_of<kList, kRows>(p, walk, start, end);
-      if (pc.tiles == 0 && walk.x0 >= start) {   // rows without a token
-        for (int i = 0; i < pc.rows; ++i) {
-          const int64_t at = row_of(p, pc.tok0, pc.g, i);
-          *reinterpret_cast<uint2*>(p.a.out + at * kD + 4 * lane) = make_uint2(0, 0);
-          if (p.a.lse && lane == 0) p.a.lse[at] = -INFINITY;
+    if (left == 0) {
+      while (left == 0 && walk.b < p.B && walk.x0 < end) {
+        const Piece pc = piece_of<kList, kRows>(p, walk, start, end);
+        if (pc.tiles == 0 && walk.x0 >= start) {   // rows without a token
+          for (int i = 0; i < pc.rows; ++i) {
+            const int64_t at = row_of(p, pc.tok0, pc.g, i);
+            *reinterpret_cast<uint2*>(p.a.out + at * kD + 4 * lane) = make_uint2(0, 0);
+            if (p.a.lse && lane == 0) p.a.lse[at] = -INFINITY;
+          }
         }
+        if (pc.n > 0) {
+          if (lane == 0) S.queue[warp][pushed % kQueue] = pc;
+          ++pushed;
+          lt = pc.t0;
+          left = pc.n;
+          at0 = pc.lo - pc.head;
+          m0 = pc.m0;
+          m1 = pc.m1;
+          tg = pc.g;
+          base = pc.base;
+        }
+        walk_on<kList, kRows>(p, walk);
       }
-      if (pc.n > 0) {
-        if (lane == 0) S.queue[warp][pushed % kQueue] = pc;
-        ++pushed;
-        lt = pc.t0;
-        left = pc.n;
+      __syncwarp();
+      if (left == 0) {
+        tok_kind = kNone;
+        return;
       }
-      walk_on<kList, kRows>(p, walk);
     }
-    __syncwarp();
-    tok_any = left > 0;
-    tok = -1;
-    if (tok_any) {
-      const Piece& pc = S.queue[warp][(pushed - 1) % kQueue];
-      tok = token_of_slot<kList>(p, pc, lt * kTile + lane);
-      tok_b = pc.b;
-      tok_g = pc.g;
-      ++lt;
-      --left;
+    if (!kList && lt >= m0 && lt < m1) {
+      tok_kind = kLine;
+      tok = at0 + lt * kTile;
+    } else {
+      tok_kind = kRowwise;
+      tok = token_of_slot<kList>(p, S.queue[warp][(pushed - 1) % kQueue], lt * kTile + lane);
     }
+    tok_g = tg;
+    tok_base = base;
+    ++lt;
+    --left;
   };
   auto next_rows = [&]() {
-    row_any = tok_any;
+    row_kind = tok_kind;
     row = -1;
-    if (tok >= 0) {
-      row = static_cast<int>(cache_row(p.a.pm, tok_b, tok_g, p.Hkv, p.n_cap, tok));
-      if (row < 0) record_error(p.err, kErrBadPage);
+    if (tok_kind != kNone && tok >= 0) {
+      if (p.a.pm.table == nullptr) {
+        row = static_cast<int>(tok_base) + tok;
+      } else {
+        const int page = __ldg(p.a.pm.table + tok_base + (tok >> p.a.pm.page_shift));
+        if (page >= 0 && page < p.a.pm.num_pages) {
+          row = ((page * p.Hkv + tok_g) << p.a.pm.page_shift) + (tok & ((1 << p.a.pm.page_shift) - 1));
+        } else {
+          record_error(p.err, kErrBadPage);
+          row_kind = kRowwise;
+        }
+      }
     }
     next_tokens();
   };
   uint32_t put = 0;   // stage that the next copies go to
+  // K rows stand as they are; V rows with the low bits of their number swapped
+  // and their chunks turned by a half where bit 2 is set: a lane's four tokens, 2j
+  // and 2j + 1 of eight, are then in banks of their own.
+  const uint32_t k_at = 16 * lane, kf_at = kTileCodes + lane * kKv4Groups;
+  const uint32_t v_at = kTileCodes + kTileScales + ((r & 4) | (r & 1) << 1 | (r >> 1 & 1)) * kKv4Codes + 16 * (j ^ (r >> 1 & 2));
   auto issue = [&]() {
-    if (row_any) {
-      const uint32_t at = ring_s + put * kStage;
+    const uint32_t at = ring_s + put * kStage;
+    if (row_kind == kLine) {
+      const int64_t codes = static_cast<int64_t>(row) * kKv4Codes + 16 * lane;
+      const int64_t scales = static_cast<int64_t>(row) * kKv4Groups + kKv4Groups * lane;
+      const uint8_t* k = p.a.kv.K + codes;
+      const uint8_t* v = p.a.kv.V + codes;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int rk = __shfl_sync(0xffffffffu, row, r + 8 * i);
-        // V rows stand with the low bits of their number swapped and their chunks
-        // turned by a half where bit 2 is set: a lane's four tokens, 2j and 2j + 1 of
-        // eight, are then in banks of their own.
-        const int rv = __shfl_sync(0xffffffffu, row, ((r & 4) | (r & 1) << 1 | (r >> 1 & 1)) + 8 * i);
-        cp_async16(at + (r + 8 * i) * kKv4Codes + 16 * j, p.a.kv.K + static_cast<int64_t>(max(rk, 0)) * kKv4Codes + 16 * j,
-                   rk >= 0 ? 16 : 0);
-        cp_async16(at + kTileCodes + kTileScales + (r + 8 * i) * kKv4Codes + 16 * (j ^ (r >> 1 & 2)),
-                   p.a.kv.V + static_cast<int64_t>(max(rv, 0)) * kKv4Codes + 16 * j, rv >= 0 ? 16 : 0);
+        cp_async16(at + k_at + 8 * i * kKv4Codes, k + 8 * i * kKv4Codes);
+        cp_async16(at + v_at + 8 * i * kKv4Codes, v + 8 * i * kKv4Codes);
+      }
+      cp_async8(at + kf_at, p.a.kv.K_sf + scales);
+      cp_async8(at + kf_at + kTileCodes + kTileScales, p.a.kv.V_sf + scales);
+    } else if (row_kind == kRowwise) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int from = __shfl_sync(0xffffffffu, row, r + 8 * i);   // rows that are none: zeros
+        const int64_t src = static_cast<int64_t>(max(from, 0)) * kKv4Codes + 16 * j;
+        cp_async16(at + k_at + 8 * i * kKv4Codes, p.a.kv.K + src, from >= 0 ? 16 : 0);
+        cp_async16(at + v_at + 8 * i * kKv4Codes, p.a.kv.V + src, from >= 0 ? 16 : 0);
       }
       const int64_t own = static_cast<int64_t>(max(row, 0)) * kKv4Groups;
-      cp_async8(at + kTileCodes + lane * kKv4Groups, p.a.kv.K_sf + own, row >= 0 ? 8 : 0);
-      cp_async8(at + 2 * kTileCodes + kTileScales + lane * kKv4Groups, p.a.kv.V_sf + own, row >= 0 ? 8 : 0);
+      cp_async8(at + kf_at, p.a.kv.K_sf + own, row >= 0 ? 8 : 0);
+      cp_async8(at + kf_at + kTileCodes + kTileScales, p.a.kv.V_sf + own, row >= 0 ? 8 : 0);
     }
     cp_async_commit();
     put = put + 1 == kStages ? 0 : put + 1;
@@ -499,7 +582,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int ex = min(max(static_cast<int>(top >> 7), 32), 254);   // 2^(ex - 127) <= largest value
       const float up = __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);     // to 2^14 ..
-      const float down = __uint_as_float(static_cast<uint32_t>(127 + ex - 141) << 23) * (kScale / kKv4HalfScale) * p.a.kv.k_scale;
+      const float down = __uint_as_float(static_cast<uint32_t>(127 + ex - 141) << 23) * kScale * p.a.kv.k_scale;
       cs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * j);
       cs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * j + 4);
       const uint32_t* w = &x[0].x;
@@ -512,9 +595,11 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
 
     float o[8][kNT][4];
     float mx[kNT][2], l[kNT][2];
+    float base2[kNT][2];   // added to a logit: kBase - mx, 0 before there is a maximum
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
       mx[nt][0] = mx[nt][1] = -INFINITY;
+      base2[nt][0] = base2[nt][1] = 0.0f;
       l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.0f;
@@ -529,23 +614,27 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
 
       // ---- S^T = K Q^T
       float s[2][kNT][4];
+      uint4 kw[2][2];
+      __half2 kf[2][2];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.0f;
-        const int row0 = 16 * mt + r;
-        const uint4 k0 = *reinterpret_cast<const uint4*>(st + row0 * kKv4Codes + 16 * j);
-        const uint4 k1 = *reinterpret_cast<const uint4*>(st + (row0 + 8) * kKv4Codes + 16 * j);
-        const __half2 f0 = kv4_scales(*reinterpret_cast<const uint16_t*>(st + kTileCodes + row0 * kKv4Groups + 2 * j));
-        const __half2 f1 = kv4_scales(*reinterpret_cast<const uint16_t*>(st + kTileCodes + (row0 + 8) * kKv4Groups + 2 * j));
-        const uint32_t* w0 = &k0.x;
-        const uint32_t* w1 = &k1.x;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const __half2 g0 = w < 2 ? __low2half2(f0) : __high2half2(f0), g1 = w < 2 ? __low2half2(f1) : __high2half2(f1);
+        for (int h = 0; h < 2; ++h) {
+          kw[mt][h] = *reinterpret_cast<const uint4*>(st + k_at + (16 * mt + 8 * h) * kKv4Codes);
+          kf[mt][h] = kv4_scales(*reinterpret_cast<const uint16_t*>(st + kTileCodes + (16 * mt + 8 * h + r) * kKv4Groups + 2 * j));
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const __half2 g0 = w < 2 ? __low2half2(kf[mt][0]) : __high2half2(kf[mt][0]);
+          const __half2 g1 = w < 2 ? __low2half2(kf[mt][1]) : __high2half2(kf[mt][1]);
           __half2 c0[4], c1[4];
-          kv4_codes(w0[w], c0);
-          kv4_codes(w1[w], c1);
+          kv4_codes((&kw[mt][0].x)[w], c0);
+          kv4_codes((&kw[mt][1].x)[w], c1);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t a0 = bits(__hmul2(c0[2 * h], g0)), a1 = bits(__hmul2(c1[2 * h], g1));
@@ -554,35 +643,21 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
             for (int nt = 0; nt < kNT; ++nt) mma16816(s[mt][nt], a0, a1, a2, a3, qf[nt][4 * w + 2 * h], qf[nt][4 * w + 2 * h + 1]);
           }
         }
-      }
 
-      // ---- logits, masked where the tile is not attended to as a whole
-      bool full = kTile * (t + 1) <= pc.cnt;
-      if (!kList && full && pc.p0 != pc.p1) {
-        const int a0 = kTile * t, a1 = a0 + kTile - 1;
-        const int first = pc.lo + max(a0, pc.head) - pc.head, last = a1 < pc.head ? a1 : pc.lo + a1 - pc.head;
-        full = last <= pc.p0 && (a1 < pc.head || first > pc.p1 - p.a.local);
-      }
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][nt][e] *= cs[nt][e & 1];
-      if (!full) {
+      // ---- masked where the tile is not attended to as a whole
+      if (t < pc.m0 || t >= pc.m1) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int slot = kTile * t + 16 * mt + 8 * h + r;
-            const int token = kList ? 0 : (slot < pc.head ? slot : pc.lo + slot - pc.head);
+            const int token = kList ? 0 : token_of_slot<false>(p, pc, slot);
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 const int pos = pc.p0 + ((8 * nt + 2 * j + c) >> p.gsh);
-                const bool seen = slot < pc.cnt && (kList || (token <= pos && (token > pos - p.a.local || token < p.a.sink)));
-                if (!seen) s[mt][nt][2 * h + c] = -INFINITY;
+                if (kList ? slot >= pc.cnt : token < 0 || !attends(p, pos, token)) s[mt][nt][2 * h + c] = -INFINITY;
               }
           }
       }
@@ -594,7 +669,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
       for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          top[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]), fmaxf(s[1][nt][c], s[1][nt][2 + c]));
+          top[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]), fmaxf(s[1][nt][c], s[1][nt][2 + c])) * cs[nt][c];
           grown |= top[nt][c] > mx[nt][c] + kGrow;
         }
       if (__any_sync(0xffffffffu, grown)) {
@@ -608,6 +683,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
             if (m > mx[nt][c]) {
               const float f = ex2_approx(mx[nt][c] - m);   // 0 for the first
               mx[nt][c] = m;
+              base2[nt][c] = kBase - m;
               l[nt][c] *= f;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -622,13 +698,12 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
       uint32_t pf[2][kNT][2];
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
-        const float b0 = mx[nt][0] == -INFINITY ? 0.0f : mx[nt][0] - kBase;
-        const float b1 = mx[nt][1] == -INFINITY ? 0.0f : mx[nt][1] - kBase;
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float p0 = ex2_approx(s[mt][nt][2 * h] - b0), p1 = ex2_approx(s[mt][nt][2 * h + 1] - b1);
+            const float p0 = ex2_approx(fmaf(s[mt][nt][2 * h], cs[nt][0], base2[nt][0]));
+            const float p1 = ex2_approx(fmaf(s[mt][nt][2 * h + 1], cs[nt][1], base2[nt][1]));
             l[nt][0] += p0;
             l[nt][1] += p1;
             pf[mt][nt][h] = transpose8x8(pack_half(p0, p1));
@@ -774,7 +849,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
       sh.first = static_cast<int64_t>(pc.tok0) << p.gsh;
       sh.rows = pc.rows;
       sh.g = pc.g;
-      sh.last = line.block(pc.x0 + kItemCost + pc.tiles - 1);
+      sh.last = line.block(pc.x0 + kItemCost + ((pc.tiles - 1) >> p.ush));
       sh.pad = 0;
       p.share[blockIdx.x] = sh;
     }
@@ -784,35 +859,44 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
 }
 
 // Joins the parts of an item that several blocks share: exact log-sum-exp,
-// fp32.  Block c has the item whose first tiles attention block c had; its
-// threads a row's 4 channels each, 8 rows at a time.
-constexpr int kMergeThreads = 256;
+// fp32.  Block (c, row) has a row of the item whose first tiles attention block c
+// had: its warps take every eighth part, a lane four channels.
+constexpr int kMergeWarps = 8;
 
 template <int kNT>
-__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Args p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Args p) {
   constexpr int kRows = 8 * kNT;
+  __shared__ float4 so[kMergeWarps][32];
+  __shared__ float2 sml[kMergeWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.y;
   pdl_wait();
   const Share sh = p.share[blockIdx.x];
-  const int chunk = threadIdx.x & 31;
-  for (int col = threadIdx.x >> 5; col < sh.rows; col += kMergeThreads / 32) {
+  if (col < sh.rows) {
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int c = blockIdx.x; c <= sh.last; ++c) {
-      const int64_t part = (static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x))) * kRows + col;
-      const float2 v = __ldcg(p.part_ml + part);
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + part * kD) + chunk);
+    auto join = [&](const float2 v, const float4 y) {
       const float mn = fmaxf(m, v.x);
       const float a = mn == -INFINITY ? 1.0f : ex2_approx(m - mn), b = mn == -INFINITY ? 1.0f : ex2_approx(v.x - mn);
       m = mn;
       l = l * a + v.y * b;
       o = make_float4(o.x * a + y.x * b, o.y * a + y.y * b, o.z * a + y.z * b, o.w * a + y.w * b);
+    };
+    for (int c = blockIdx.x + warp; c <= sh.last; c += kMergeWarps) {
+      const int64_t part = (static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x))) * kRows + col;
+      join(__ldcg(p.part_ml + part), __ldcg(reinterpret_cast<const float4*>(p.part_o + part * kD) + lane));
     }
-    const int64_t row = sh.first + col;
-    const int64_t at = (row >> p.gsh) * p.Hq + (sh.g << p.gsh) + (row & ((1 << p.gsh) - 1));
-    const float inv = inverse_of(p, l);
-    *reinterpret_cast<uint2*>(p.a.out + at * kD + 4 * chunk) =
-        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (p.a.lse && chunk == 0) p.a.lse[at] = lse_of(m, l);
+    so[warp][lane] = o;
+    if (lane == 0) sml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp == 0) {
+      for (int w = 1; w < kMergeWarps; ++w) join(sml[w], so[w][lane]);
+      const int64_t row = sh.first + col;
+      const int64_t at = (row >> p.gsh) * p.Hq + (sh.g << p.gsh) + (row & ((1 << p.gsh) - 1));
+      const float inv = inverse_of(p, l);
+      *reinterpret_cast<uint2*>(p.a.out + at * kD + 4 * lane) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      if (p.a.lse && lane == 0) p.a.lse[at] = lse_of(m, l);
+    }
   }
   pdl_trigger();
 }
@@ -870,11 +954,13 @@ int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, size
   }
   while ((s.B - 1) >> p.ssh >= kSums) ++p.ssh;
   p.err = dev.err_word;
+  const int nt = a.listed ? 1 : tiles_of(s, a.max_q);
+  const int64_t blocks = (a.bt.T * (s.Hq / s.Hkv) + 8 * nt - 1) / (8 * nt) + s.B;   // row blocks of a KV head, at most
+  while (blocks * s.Hkv * (((s.n_cap / kTile + 2) >> p.ush) + 1 + kItemCost) >= (int64_t(1) << 31)) ++p.ush;
   // Items of few tiles are not shared between blocks, which saves the merge.
   const int64_t most = a.listed ? p.sink_end + static_cast<int64_t>(a.K) + (p.n - p.local_start)
                                 : std::min<int64_t>(s.n_cap, static_cast<int64_t>(a.local) + a.sink + a.max_q - 1);
   p.whole = most <= kWholeTokens;
-  const int nt = a.listed ? 1 : tiles_of(s, a.max_q);
   const int grid = dev.num_sms;
   const Layout L = layout_of(8 * nt, grid);
   if (ws_bytes < L.total) return static_cast<int>(cudaErrorInvalidValue);
@@ -883,7 +969,7 @@ int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, size
   p.part_o = reinterpret_cast<float*>(ws + L.off_o);
   cudaError_t e = launch_dependent(kernel_of(nt, a.listed), dim3(grid), dim3(32 * warps_of(nt)), smem_of(nt), stream, 1, p);
   if (e != cudaSuccess || p.whole) return static_cast<int>(e);
-  e = launch_dependent(merge_of(nt), dim3(grid), dim3(kMergeThreads), 0, stream, 1, p);
+  e = launch_dependent(merge_of(nt), dim3(grid, 8 * nt), dim3(32 * kMergeWarps), 0, stream, 1, p);
   return static_cast<int>(e);
 }
 

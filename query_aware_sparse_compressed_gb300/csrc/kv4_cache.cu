@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
         const int64_t r = row + g * head_rows;
         const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>((side ? a.kv.V : a.kv.K) + r * kKv4Codes) + c);
         const uint32_t sf = __ldg((side ? a.kv.V_sf : a.kv.K_sf) + r * kKv4Groups + (c >> 1));
-        const float f = (side ? a.kv.v_scale : a.kv.k_scale) / kKv4HalfScale;
+        const float f = side ? a.kv.v_scale : a.kv.k_scale;
         const __half2 s = kv4_scales(sf * 0x101u);
         __half2 h[4];
         kv4_codes(w, h);
