@@ -68,7 +68,8 @@ constexpr int kStage = 2 * (kTileCodes + kTileScales);
 constexpr int kSums = 512;                     // places are summed for as many groups of sequences at most
 constexpr int kQueue = 8;                      // items that a warp's loads are ahead of its products, at most
 constexpr int kItemCost = KV4_C;                   // places of an item beside its tiles: queries, output
-constexpr int kTilesMost = (1 << 24) / kTile;  // n_cap < 2^24
+constexpr int kTokensMost = 1 << 24;           // above n_cap, and sink and local as the kernel has them
+constexpr int kTilesMost = kTokensMost / kTile;
 constexpr int kLeast = 8;                      // places that a block takes at least
 constexpr int kWholeTokens = 1024;             // an item of more tokens may be shared between blocks
 constexpr float kBase = 10.0f;                 // log2 of P at the maximum that the base was taken from
@@ -116,10 +117,12 @@ struct Seq {
   int q0, ql, len;
 };
 
-// Where a warp's loads stand on the line: item `rem` of sequence b's `items`.
+// Where a warp's loads stand: item `rem` of sequence b's `items`.
 struct Walk {
   int x0;              // the item's first place
   int b, rem, items, span;
+  int start, end;      // the warp's places; whole items: its part of each of them and their parts
+  int left;            // whole items: items left
   Seq s;
 };
 
@@ -163,7 +166,7 @@ __device__ __forceinline__ int list_len(const Args& p, int b, int g) {
 }
 
 // Items of a sequence (row blocks times KV heads) and the places of each: the
-// most tiles that any of them has.
+// most tiles that any of them has (whole items: one).
 template <int kRows>
 __device__ __forceinline__ int items_of(const Args& p, const Seq& s) {
   const int64_t rows = static_cast<int64_t>(s.ql) << p.gsh;
@@ -172,17 +175,18 @@ __device__ __forceinline__ int items_of(const Args& p, const Seq& s) {
 }
 template <bool kList, int kRows>
 __device__ __forceinline__ int span_of(const Args& p, const Seq& s, int b) {
-  int64_t cnt;
+  if (p.whole) return 1;
+  int tiles;
   if (kList) {
     int most = 0;
     for (int g = 0; g < (p.a.sel_per_kv ? p.Hkv : 1); ++g) most = max(most, list_len(p, b, g));
-    cnt = p.sink_end + most + (p.n - p.local_start);
+    tiles = (p.sink_end + most + (p.n - p.local_start) + kTile - 1) / kTile;
   } else {
     // the sink's tiles, the window's, and one more where it begins inside a tile
-    const int64_t window = (static_cast<int64_t>(p.a.local) + min(s.ql, kRows >> p.gsh) - 1 + 2 * (kTile - 1)) / kTile;
-    cnt = min((static_cast<int64_t>(s.len) + kTile - 1) / kTile, window + (static_cast<int64_t>(p.a.sink) + kTile - 1) / kTile) * kTile;
+    const int window = (p.a.local + min(s.ql, kRows >> p.gsh) - 1 + 2 * (kTile - 1)) / kTile;
+    tiles = min((s.len + kTile - 1) / kTile, window + (p.a.sink + kTile - 1) / kTile);
   }
-  return static_cast<int>(((cnt + kTile - 1) / kTile + (1 << p.ush) - 1) >> p.ush) + kItemCost;
+  return ((tiles + (1 << p.ush) - 1) >> p.ush) + kItemCost;
 }
 
 // A line of U places over G blocks: block c has the places [c U / G, (c + 1) U / G),
@@ -208,10 +212,12 @@ struct Line {
 template <int kNT>
 struct Smem {
   static constexpr int kRows = 8 * kNT, kWarps = warps_of(kNT), kStages = stages_of(kNT);
+  static_assert(2 * kWarps <= 32, "a lane for each part");
   static_assert(kStages * kStage >= sizeof(Part<kRows>), "a warp's last part stands in its ring");
   alignas(16) uint8_t ring[kWarps][kStages * kStage];
   Part<kRows> first[kWarps];
   Piece queue[kWarps][kQueue];
+  Walk walk[kWarps];
   Piece part[2 * kWarps];        // of every warp: the item that it shares with earlier ones, with later ones
   int there[2 * kWarps];         // 0: none, 1: the item goes on, 2: it ends here
   int place[kSums + 1];          // places before a group of sequences
@@ -270,7 +276,7 @@ __device__ __forceinline__ float inverse_of(const Args& p, float l) {
 
 // Row `pos` of a window call attends to token t.
 __device__ __forceinline__ bool attends(const Args& p, int pos, int t) {
-  return t <= pos && (t < p.a.sink || static_cast<int64_t>(t) > static_cast<int64_t>(pos) - p.a.local);
+  return t <= pos && (t < p.a.sink || t > pos - p.a.local);
 }
 
 // Token of slot s of an item; -1: none that any of its rows attends to.  Of a window
@@ -282,7 +288,7 @@ __device__ __forceinline__ int token_of_slot(const Args& p, const Piece& pc, int
   if (!kList) {
     if (s < pc.head) return s < p.a.sink ? s : -1;
     const int t = pc.lo + s - pc.head;
-    return t <= pc.p1 && (t < p.a.sink || static_cast<int64_t>(t) > static_cast<int64_t>(pc.p0) - p.a.local) ? t : -1;
+    return t <= pc.p1 && (t < p.a.sink || t > pc.p0 - p.a.local) ? t : -1;
   }
   if (s < pc.head) return s;
   const int i = s - pc.head;
@@ -335,9 +341,9 @@ __device__ __forceinline__ void walk_on(const Args& p, Walk& w) {
   }
 }
 
-// The part of item w on the places [start, end).
+// The warp's part of item w.
 template <bool kList, int kRows>
-__device__ __forceinline__ Piece piece_of(const Args& p, const Walk& w, int start, int end) {
+__device__ __forceinline__ Piece piece_of(const Args& p, const Walk& w) {
   Piece pc;
   const unsigned blocks = static_cast<unsigned>(w.items) / static_cast<unsigned>(p.Hkv);
   pc.b = w.b;
@@ -348,13 +354,13 @@ __device__ __forceinline__ Piece piece_of(const Args& p, const Walk& w, int star
   pc.tok0 = w.s.q0 + (r0 >> p.gsh);
   pc.p0 = w.s.len - w.s.ql + (r0 >> p.gsh);
   pc.p1 = w.s.len - w.s.ql + ((r0 + pc.rows - 1) >> p.gsh);
+  pc.p0 = max(pc.p0, -kTokensMost);   // in front of the cache all the same
   if (kList) {
     pc.head = p.sink_end;
     pc.lo = list_len(p, pc.b, pc.g);
     pc.cnt = p.sink_end + pc.lo + (p.n - p.local_start);
   } else {
-    const int64_t lo = static_cast<int64_t>(pc.p0) - p.a.local + 1;
-    pc.lo = static_cast<int>(lo > 0 ? lo : 0) & ~(kTile - 1);
+    pc.lo = max(pc.p0 - p.a.local + 1, 0) & ~(kTile - 1);
     pc.head = p.a.sink < pc.lo ? (p.a.sink + kTile - 1) & ~(kTile - 1) : pc.lo;
     if (pc.head >= pc.lo) pc.head = pc.lo = 0;   // the sink's tiles reach the window's
     pc.cnt = pc.p1 >= 0 ? pc.head + pc.p1 - pc.lo + 1 : 0;
@@ -363,19 +369,54 @@ __device__ __forceinline__ Piece piece_of(const Args& p, const Walk& w, int star
   pc.m0 = 0;
   pc.m1 = pc.cnt / kTile;
   if (!kList) {
-    const int64_t open = static_cast<int64_t>(pc.p1) - p.a.local + 1 - pc.lo;   // tokens that the last row no longer sees
-    pc.m0 = pc.head / kTile + (open > 0 ? static_cast<int>((open + kTile - 1) / kTile) : 0);
-    pc.m1 = pc.head / kTile + (pc.p0 >= pc.lo ? (pc.p0 - pc.lo + 1) / kTile : 0);
+    const int open = max(pc.p1, 0) - p.a.local + 1 - pc.lo;   // tokens that the last row no longer sees
+    pc.m0 = pc.head / kTile + (max(open, 0) + kTile - 1) / kTile;
+    pc.m1 = pc.head / kTile + max(pc.p0 - pc.lo + 1, 0) / kTile;
   }
   pc.base = p.a.pm.table ? pc.b * p.a.pm.pages_per_seq : (static_cast<int64_t>(pc.b) * p.Hkv + pc.g) * p.n_cap;
-  const int first = w.x0 + kItemCost;
-  pc.t0 = max(0, start - first) << p.ush;
-  pc.n = max(0, min(pc.tiles, min(max(end - first, 0), (kTilesMost >> p.ush) + 1) << p.ush) - pc.t0);
+  if (p.whole) {
+    pc.t0 = pc.tiles * w.start / w.end;   // few tiles, few parts
+    pc.n = pc.tiles * (w.start + 1) / w.end - pc.t0;
+  } else {
+    const int first = w.x0 + kItemCost;
+    pc.t0 = max(0, w.start - first) << p.ush;
+    pc.n = max(0, min(pc.tiles, min(max(w.end - first, 0), (kTilesMost >> p.ush) + 1) << p.ush) - pc.t0);
+  }
   return pc;
 }
 
+// Puts the next item of a warp's range into `to`: 0 where there is none, 1 for the
+// last, else 2.  Items without a token are written on the way.  (A call of its own: what runs once an
+// item would stand in the loop over its tiles otherwise, whose code is long as it is.)
 template <int kNT, bool kList>
-__global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const Args p) {
+__device__ __noinline__ int next_piece(const Args& p, Smem<kNT>& S, int warp, Piece& to) {
+  constexpr int kRows = 8 * kNT;
+  const int lane = threadIdx.x & 31;
+  Walk walk = S.walk[warp];
+  bool found = false;
+  auto more = [&]() { return p.whole ? walk.left > 0 : walk.b < p.B && walk.x0 < walk.end; };
+  __syncwarp();
+  while (!found && more()) {
+    const Piece pc = piece_of<kList, kRows>(p, walk);
+    if (pc.tiles == 0 && (p.whole ? walk.start == 0 : walk.x0 >= walk.start)) {
+      for (int i = 0; i < pc.rows; ++i) {
+        const int64_t at = row_of(p, pc.tok0, pc.g, i);
+        *reinterpret_cast<uint2*>(p.a.out + at * kD + 4 * lane) = make_uint2(0, 0);
+        if (p.a.lse && lane == 0) p.a.lse[at] = -INFINITY;
+      }
+    }
+    found = pc.n > 0;
+    if (found && lane == 0) to = pc;
+    --walk.left;
+    if (!p.whole || walk.left > 0) walk_on<kList, kRows>(p, walk);
+  }
+  if (lane == 0) S.walk[warp] = walk;
+  __syncwarp();
+  return found ? 1 + more() : 0;
+}
+
+template <int kNT, bool kList>
+__global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const __grid_constant__ Args p) {
   using Sm = Smem<kNT>;
   constexpr int kRows = Sm::kRows, kWarps = Sm::kWarps, kThreads = 32 * kWarps, kStages = Sm::kStages;
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -384,64 +425,90 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
   const int r = lane >> 2, j = lane & 3;
   pdl_wait();
 
-  // ---- the line
+  // ---- this warp's part of the work.  Whole items of single tokens need no sums.
   const int groups = (p.B + (1 << p.ssh) - 1) >> p.ssh;
-  for (int i = tid; i < groups; i += kThreads) {
-    int places = 0;
-    for (int b = i << p.ssh; b < min(p.B, (i + 1) << p.ssh); ++b) {
-      const Seq s = seq_of<kList>(p, b);
-      const int items = items_of<kRows>(p, s);
-      if (items > 0) places += items * span_of<kList, kRows>(p, s, b);
-      if (!kList && blockIdx.x == 0) {
-        const int len = __ldg(p.a.bt.lens + b);
-        if (len < 0 || len > p.n_cap) record_error(p.err, kErrBadPage);
-      }
-    }
-    S.place[i] = places;
-  }
+  const bool plain = p.whole && (kList || p.a.bt.cu_q == nullptr);
   if (tid < 2 * kWarps) S.there[tid] = 0;
-  __syncthreads();
-  if (groups > 1) {
-    if (warp == 0) {
-      int places = 0;
-      for (int b0 = 0; b0 < groups; b0 += 32) {
-        const int b = b0 + lane;
-        const int v = b < groups ? S.place[b] : 0;
-        int vi = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, vi, o);
-          if (lane >= o) vi += x;
-        }
-        if (b < groups) S.place[b] = places + vi - v;
-        places += __shfl_sync(0xffffffffu, vi, 31);
+  if (!kList && blockIdx.x == gridDim.x - 1)
+    for (int b = tid; b < p.B; b += kThreads) {
+      const int len = __ldg(p.a.bt.lens + b);
+      if (len < 0 || len > p.n_cap) record_error(p.err, kErrBadPage);
+    }
+  int places = p.B * p.Hkv;
+  if (!plain) {
+    for (int i = tid; i < groups; i += kThreads) {
+      int sum = 0;
+      for (int b = i << p.ssh; b < min(p.B, (i + 1) << p.ssh); ++b) {
+        const Seq s = seq_of<kList>(p, b);
+        const int items = items_of<kRows>(p, s);
+        if (items > 0) sum += items * span_of<kList, kRows>(p, s, b);
       }
-      if (lane == 0) S.place[groups] = places;
+      S.place[i] = sum;
     }
     __syncthreads();
+    if (groups > 1) {
+      if (warp == 0) {
+        int sum = 0;
+        for (int b0 = 0; b0 < groups; b0 += 32) {
+          const int b = b0 + lane;
+          const int v = b < groups ? S.place[b] : 0;
+          int vi = v;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, vi, o);
+            if (lane >= o) vi += x;
+          }
+          if (b < groups) S.place[b] = sum + vi - v;
+          sum += __shfl_sync(0xffffffffu, vi, 31);
+        }
+        if (lane == 0) S.place[groups] = sum;
+      }
+      __syncthreads();
+    }
+    places = S.place[groups > 1 ? groups : 0];   // (of one group the sum itself stands there)
   }
-  const int places = groups > 1 ? S.place[groups] : S.place[0];
-  // (of one group the sum stands in place 0, whose first place is 0 all the same)
   const Line line(places, max(1, min(static_cast<int>(gridDim.x), p.whole ? places : (places + kLeast - 1) / kLeast)));
   Walk walk;
   walk.b = p.B;
-  int start = 0, end = 0;   // this warp's places
+  walk.x0 = walk.end = walk.start = walk.left = 0;
   if (blockIdx.x < line.G && places > 0) {
-    // an item belongs to the block that has its first place, where they are not shared
-    auto bound = [&](unsigned c) {
-      int x = line.start(c);
-      if (p.whole && x < places) {
-        const Walk w = walk_at<kList, kRows>(p, S.place, x);
-        if (w.x0 < x) x = w.x0 + w.span;
+    const unsigned first = line.start(blockIdx.x), all = line.start(blockIdx.x + 1) - first;
+    if (p.whole) {   // items of its own for every warp, or warps for every item
+      int item, left = 0, part = 0, parts = 1;
+      if (all >= kWarps) {
+        item = all * warp / kWarps;
+        left = all * (warp + 1) / kWarps - item;
+      } else {
+        parts = kWarps / all;
+        item = warp / parts;
+        part = warp - item * parts;
+        left = item < static_cast<int>(all);
       }
-      return x;
-    };
-    const unsigned first = bound(blockIdx.x), all = bound(blockIdx.x + 1) - first;
-    const unsigned each = all / kWarps, more = all - each * kWarps;
-    start = first + each * warp + more * warp / kWarps;
-    end = first + each * (warp + 1) + more * (warp + 1) / kWarps;
-    if (start < end) walk = walk_at<kList, kRows>(p, S.place, start);
+      if (left > 0) {
+        if (plain) {
+          walk.b = (first + item) / p.Hkv;
+          walk.rem = first + item - walk.b * p.Hkv;
+          walk.s = seq_of<kList>(p, walk.b);
+          walk.items = p.Hkv;
+          walk.span = 1;
+        } else {
+          walk = walk_at<kList, kRows>(p, S.place, first + item);
+        }
+      }
+      walk.left = left;
+      walk.start = part;
+      walk.end = parts;
+    } else {
+      const unsigned each = all / kWarps, more = all - each * kWarps;
+      const int start = first + each * warp + more * warp / kWarps;
+      const int end = first + each * (warp + 1) + more * (warp + 1) / kWarps;
+      if (start < end) walk = walk_at<kList, kRows>(p, S.place, start);
+      walk.start = start;
+      walk.end = end;
+    }
   }
+  if (lane == 0) S.walk[warp] = walk;
+  __syncwarp();
 
   uint8_t* const ring = S.ring[warp];
   const uint32_t ring_s = smem_u32(ring);
@@ -450,6 +517,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
   // their copies each (the block table and the list are read on the way)
   enum { kNone, kLine, kRowwise };          // no tile; 32 rows in a line; rows of their own
   int pushed = 0;                           // items found
+  bool more = true;                         // there may be others
   int lt = 0, left = 0;                     // next tile of the newest item, tiles left of it
   int at0 = 0, m0 = 0, m1 = 0, tg = 0;      // of that item: token of tile 0's first slot in a line, whole tiles, KV head
   int64_t base = 0;
@@ -457,36 +525,24 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
   int64_t tok_base = 0;
   int row = -1, row_kind = kNone;           // lane's row of the next tile (of a line: its first); -1: none
   auto next_tokens = [&]() {
-    if (left == 0) {
-      while (left == 0 && walk.b < p.B && walk.x0 < end) {
-        const Piece pc = piece_of<kList, kRows>(p, walk, start, end);
-        if (pc.tiles == 0 && walk.x0 >= start) {   // rows without a token
-          for (int i = 0; i < pc.rows; ++i) {
-            const int64_t at = row_of(p, pc.tok0, pc.g, i);
-            *reinterpret_cast<uint2*>(p.a.out + at * kD + 4 * lane) = make_uint2(0, 0);
-            if (p.a.lse && lane == 0) p.a.lse[at] = -INFINITY;
-          }
-        }
-        if (pc.n > 0) {
-          if (lane == 0) S.queue[warp][pushed % kQueue] = pc;
-          ++pushed;
-          lt = pc.t0;
-          left = pc.n;
-          at0 = pc.lo - pc.head;
-          m0 = pc.m0;
-          m1 = pc.m1;
-          tg = pc.g;
-          base = pc.base;
-        }
-        walk_on<kList, kRows>(p, walk);
-      }
-      __syncwarp();
-      if (left == 0) {
+    if (__builtin_expect(left == 0, 0)) {
+      Piece& pc = S.queue[warp][pushed % kQueue];
+      const int found = more ? next_piece<kNT, kList>(p, S, warp, pc) : 0;
+      more = found == 2;
+      if (found == 0) {
         tok_kind = kNone;
         return;
       }
+      ++pushed;
+      lt = pc.t0;
+      left = pc.n;
+      at0 = pc.lo - pc.head;
+      m0 = pc.m0;
+      m1 = pc.m1;
+      tg = pc.g;
+      base = pc.base;
     }
-    if (!kList && lt >= m0 && lt < m1) {
+    if (!kList && __builtin_expect(lt >= m0 && lt < m1, 1)) {
       tok_kind = kLine;
       tok = at0 + lt * kTile;
     } else {
@@ -524,7 +580,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
   const uint32_t v_at = kTileCodes + kTileScales + ((r & 4) | (r & 1) << 1 | (r >> 1 & 1)) * kKv4Codes + 16 * (j ^ (r >> 1 & 2));
   auto issue = [&]() {
     const uint32_t at = ring_s + put * kStage;
-    if (row_kind == kLine) {
+    if (__builtin_expect(!kList && row_kind == kLine, !kList)) {
       const int64_t codes = static_cast<int64_t>(row) * kKv4Codes + 16 * lane;
       const int64_t scales = static_cast<int64_t>(row) * kKv4Groups + kKv4Groups * lane;
       const uint8_t* k = p.a.kv.K + codes;
@@ -553,6 +609,20 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
     next_rows();
   };
   next_tokens();
+
+  // Queries of an item, column 8 nt + r of its rows: a lane holds 32 values.  Those of
+  // the next item are on their way while an item's rows are written.
+  uint4 qx[kNT][4];
+  auto load_queries = [&](const Piece& pc) {
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      const int col = 8 * nt + r;
+      const uint4* q = reinterpret_cast<const uint4*>(p.a.q + row_of(p, pc.tok0, pc.g, col) * kD + 32 * j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qx[nt][i] = col < pc.rows ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (pushed > 0) load_queries(S.queue[warp][0]);
   next_rows();
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) issue();
@@ -560,22 +630,18 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
 
   for (int done = 0; done < pushed; ++done) {
     __syncwarp();
-    const Piece pc = S.queue[warp][done % kQueue];
+    const Piece& pc = S.queue[warp][done % kQueue];   // written again only when its products are long done
 
-    // ---- queries: column 8 nt + r of the group's rows; a lane holds 32 values
+    // ---- queries in fp16
     uint32_t qf[kNT][16];
     float cs[kNT][2];   // of columns 2j, 2j + 1: logits in log2 units per unit of the product
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
-      const int col = 8 * nt + r;
-      uint4 x[4];
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (col < pc.rows) x[i] = __ldg(reinterpret_cast<const uint4*>(p.a.q + row_of(p, pc.tok0, pc.g, col) * kD + 32 * j) + i);
-        const uint32_t m = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                    __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+        const uint4 x = qx[nt][i];
+        const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
         top = max(top, max(m & 0xffffu, m >> 16));
       }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -585,7 +651,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
       const float down = __uint_as_float(static_cast<uint32_t>(127 + ex - 141) << 23) * kScale * p.a.kv.k_scale;
       cs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * j);
       cs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * j + 4);
-      const uint32_t* w = &x[0].x;
+      const uint32_t* w = &qx[nt][0].x;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float2 f = bf2_to_f2(w[i]);
@@ -605,7 +671,8 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
       for (int i = 0; i < 8; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.0f;
     }
 
-    for (int t = pc.t0; t < pc.t0 + pc.n; ++t) {
+    const int t_end = pc.t0 + pc.n, w0 = pc.m0, w1 = pc.m1;
+    for (int t = pc.t0; t < t_end; ++t) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
       issue();   // into the stage that the tile before this one has left
@@ -645,7 +712,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
         }
 
       // ---- masked where the tile is not attended to as a whole
-      if (t < pc.m0 || t >= pc.m1) {
+      if (__builtin_expect(t < w0 || t >= w1, 0)) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -672,7 +739,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
           top[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]), fmaxf(s[1][nt][c], s[1][nt][2 + c])) * cs[nt][c];
           grown |= top[nt][c] > mx[nt][c] + kGrow;
         }
-      if (__any_sync(0xffffffffu, grown)) {
+      if (__builtin_expect(__any_sync(0xffffffffu, grown), 0)) {
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -748,6 +815,8 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
     }
 
     // ---- the piece's rows
+    __syncwarp();
+    if (done + 1 < pushed) load_queries(S.queue[warp][(done + 1) % kQueue]);
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -797,42 +866,44 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const A
 
   // ---- the warps' parts joined: a chain begins with an item's first part, or with
   // the block's first one where the item began before; parts of earlier items of a
-  // warp (even places) continue it until one ends.  A warp joins a row.
+  // warp (even places) continue it until one ends.  A warp joins a row; lane k has
+  // part k's maximum and sum.
   __syncthreads();
+  const int state = lane < 2 * kWarps ? S.there[lane] : 0;
+  const unsigned present = __ballot_sync(0xffffffffu, state != 0), ended = __ballot_sync(0xffffffffu, state == 2);
+  constexpr unsigned kFirsts = 0x55555555u;   // even places
+  const unsigned heads = present & (~kFirsts | (present & -present));
   bool left_over = false;   // an item goes on behind the block
-  int before = 0;           // parts before place i
-  for (int i = 0; i < 2 * kWarps; ++i) {
-    if (S.there[i] == 0) continue;
-    const bool begins = (i & 1) != 0, head = begins || before == 0;
-    ++before;
-    if (!head) continue;
-    const Piece& pc = S.part[i];
-    int last = i;
-    bool ends = S.there[i] == 2;
-    for (int k = (i | 1) + 1; k < 2 * kWarps && !ends; k += 2)
-      if (S.there[k] != 0) {
-        last = k;
-        ends = S.there[k] == 2;
-      }
-    const bool whole = begins && ends;
+  for (unsigned todo = heads; todo != 0; todo &= todo - 1) {
+    const int i = __ffs(todo) - 1;
+    const bool begins = (i & 1) != 0;
+    // the even places behind i up to the first that ends (the one at i itself may)
+    const unsigned behind = present & kFirsts & ~((2u << i) - 1);
+    const unsigned stop = ((ended >> i) & 1) ? 0 : behind & ended;   // first of them
+    const unsigned reach = ((ended >> i) & 1) ? 0 : (stop ? behind & ((2u << (__ffs(stop) - 1)) - 1) : behind);
+    const unsigned chain = (1u << i) | reach;
+    const bool ends = ((ended >> i) & 1) || stop != 0;
     left_over |= begins && !ends;
+    const Piece& pc = S.part[i];
+    const bool mine = (chain >> lane) & 1;
+    const Part<kRows>* own = (lane & 1) ? reinterpret_cast<const Part<kRows>*>(S.ring[lane >> 1]) : &S.first[lane >> 1];
     for (int col = warp; col < pc.rows; col += kWarps) {
-      float m = -INFINITY, l = 0.0f;
-      auto part = [&](int k) -> const Part<kRows>& {
-        return (k & 1) ? *reinterpret_cast<const Part<kRows>*>(S.ring[k >> 1]) : S.first[k >> 1];
-      };
-      for (int k = i; k <= last; k = (k | 1) + 1)
-        if (S.there[k] != 0) m = fmaxf(m, part(k).ml[col].x);
+      const float2 ml = mine ? own->ml[col] : make_float2(-INFINITY, 0.0f);
+      const float m = warp_max(ml.x);
+      const float f = mine ? (m == -INFINITY ? 1.0f : ex2_approx(ml.x - m)) : 0.0f;
+      float l = mine ? ml.y * f : 0.0f;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int k = i; k <= last; k = (k | 1) + 1) {
-        if (S.there[k] == 0) continue;
-        const float2 ml = part(k).ml[col];
-        const float f = m == -INFINITY ? 1.0f : ex2_approx(ml.x - m);
-        const float4 y = part(k).o[col][lane ^ (col >> 1 & 3)];
-        l += ml.y * f;
-        o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
+#pragma unroll 4
+      for (unsigned rest = chain; rest != 0; rest &= rest - 1) {
+        const int k = __ffs(rest) - 1;
+        const Part<kRows>* from = (k & 1) ? reinterpret_cast<const Part<kRows>*>(S.ring[k >> 1]) : &S.first[k >> 1];
+        const float g = __shfl_sync(0xffffffffu, f, k);
+        const float4 y = from->o[col][lane ^ (col >> 1 & 3)];
+        o = make_float4(o.x + y.x * g, o.y + y.y * g, o.z + y.z * g, o.w + y.w * g);
       }
-      if (whole) {
+      if (begins && ends) {
         const int64_t at = row_of(p, pc.tok0, pc.g, col);
         const float inv = inverse_of(p, l);
         *reinterpret_cast<uint2*>(p.a.out + at * kD + 4 * lane) =
@@ -941,6 +1012,8 @@ int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, size
                     cudaStream_t stream) {
   Args p{};
   p.a = a;
+  p.a.sink = std::min(a.sink, kTokensMost);   // more mean the same
+  p.a.local = std::min(a.local, kTokensMost);
   p.B = s.B;
   p.Hq = s.Hq;
   p.Hkv = s.Hkv;
