@@ -40,28 +40,29 @@ __device__ __forceinline__ void kv4_codes(uint32_t w, __half2 (&h)[4]) {
   for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<__half2*>(&r[i]);
 }
 
+// x rounded to 16 significant bits.  A quotient of 8 bits (bf16) by 4 (e4m3) or by 6
+// meets a border between two values of the format exactly or stays 2^-8 of
+// itself away from it, so that a quotient made with a rounded reciprocal (2^-22 off
+// at most) has every comparison with a border, ties among them, as exact
+// division has it once its last bits are rounded away.
+__device__ __forceinline__ float kv4_quotient(float x) { return __uint_as_float((__float_as_uint(x) + 0x80u) & 0xffffff00u); }
+
 // Scale byte of a group whose largest magnitude is `a` (NaN where it holds one):
 // a / 6 rounded to e4m3, at most 448.
 __device__ __forceinline__ uint32_t kv4_scale_of(float a) {
   uint16_t e;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.0f), "f"(__fdiv_rn(a, 6.0f)));
-  return e & 0xffu;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.0f), "f"(a == a ? kv4_quotient(a * (1.0f / 6.0f)) : a));
+  return e;
 }
 
-// What divides the values of a group with this scale byte; 0 for a scale of 0.
+// 1 / scale, to an ulp; 0 for a scale of 0 or NaN.
 __device__ __forceinline__ float kv4_divisor(uint32_t byte) {
   uint32_t h;
+  float r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(byte)));
   const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
-  return s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
-}
-
-// x / scale rounded to 16 significant bits, from x times the rounded 1 / scale.
-// A border between two codes that a quotient of 8 bits (x) by 4 (scale) meets it
-// meets exactly, and otherwise it stays 2^-8 off, so that the product's error (2^-22) taken off
-// here leaves every comparison with a border, ties among them, as exact division has it.
-__device__ __forceinline__ float kv4_quotient(float x, float divisor) {
-  return __uint_as_float((__float_as_uint(__fmul_rn(x, divisor)) + 0x80u) & 0xffffff00u);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return s > 0.0f ? r : 0.0f;
 }
 
 // Eight quotients -> eight codes, the first in the lowest bits.

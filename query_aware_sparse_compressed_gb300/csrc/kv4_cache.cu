@@ -154,23 +154,55 @@ __device__ __forceinline__ uint32_t abs_max(const uint4& x) {
   return max(m & 0xffffu, m >> 16);
 }
 
-__device__ __forceinline__ uint32_t codes_of(const uint4& x, float inv, float divisor) {
+// Codes of eight values, `f` what turns them into quotients.
+__device__ __forceinline__ uint32_t codes_of(const uint4& x, float f) {
   const uint32_t* w = &x.x;
   float q[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = bf2_to_f2(w[i]);
-    q[2 * i] = kv4_quotient(f.x * inv, divisor);
-    q[2 * i + 1] = kv4_quotient(f.y * inv, divisor);
+    const float2 v = bf2_to_f2(w[i]);
+    q[2 * i] = kv4_quotient(v.x * f);
+    q[2 * i + 1] = kv4_quotient(v.y * f);
   }
   return kv4_pack(q);
+}
+
+// A unit's two chunks of a head, cx and cy, quantised into row r.  Each of them is
+// half of a group of 16; px and py are their other halves: whose lane they are on
+// and whether they are its second chunk.
+struct Halves {
+  int lane;
+  bool second;
+};
+__device__ __forceinline__ void store_quantised(const uint4& x, const uint4& y, int cx, int cy, bool together, Halves px, Halves py,
+                                                float inv, uint8_t* codes, uint8_t* sf, unsigned unit_mask, bool first) {
+  uint32_t mx = abs_max(x), my = abs_max(y);
+  if (together) {
+    mx = my = max(mx, my);
+  } else {
+    const uint32_t xx = __shfl_sync(unit_mask, mx, px.lane), xy = __shfl_sync(unit_mask, my, px.lane);
+    const uint32_t yx = __shfl_sync(unit_mask, mx, py.lane), yy = __shfl_sync(unit_mask, my, py.lane);
+    mx = max(mx, px.second ? xy : xx);
+    my = max(my, py.second ? yy : yx);
+  }
+  const uint32_t sx = kv4_scale_of(__uint_as_float(mx << 16) * inv), sy = kv4_scale_of(__uint_as_float(my << 16) * inv);
+  *reinterpret_cast<uint32_t*>(codes + 4 * cx) = codes_of(x, kv4_divisor(sx) * inv);
+  *reinterpret_cast<uint32_t*>(codes + 4 * cy) = codes_of(y, kv4_divisor(sy) * inv);
+  // the row's eight scales, gathered from its eight threads
+  const int gx = 8 * (cx >> 1), gy = 8 * (cy >> 1);
+  const uint32_t lo = __reduce_or_sync(unit_mask, (gx < 32 ? sx << gx : 0u) | (gy < 32 ? sy << gy : 0u));
+  const uint32_t hi = __reduce_or_sync(unit_mask, (gx < 32 ? 0u : sx << (gx - 32)) | (gy < 32 ? 0u : sy << (gy - 32)));
+  if (first) *reinterpret_cast<uint2*>(sf) = make_uint2(lo, hi);
 }
 
 // A unit of a head is 16 values in two 16-byte chunks: both members of eight
 // pairs, or values that are only copied; unit u of a head uses the frequencies
 // 8u .. 8u + 7 in either pairing.
-__global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const AppendArgs a) {
-  __shared__ float4 turn[kMaxTok][kFreqs];   // cos and sin, high and low parts
+#ifndef KV4_AB
+#define KV4_AB 3
+#endif
+__global__ void __launch_bounds__(kThreads, KV4_AB) kv4_append_kernel(const AppendArgs a) {
+  __shared__ __align__(16) float turn[4][kMaxTok][kFreqs];   // cos, sin, and their low parts
   __shared__ int64_t row0[kMaxTok];     // cache row of KV head 0, -1: not written
   __shared__ int32_t rpos[kMaxTok];     // position that rotates
   __shared__ int8_t live[kMaxTok];      // the token belongs to a sequence
@@ -192,8 +224,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const AppendArg
     F = frac < 1.0 ? __double2ull_rn(frac * 18446744073709551616.0) : 0;
   }
   const int64_t head_rows = a.pm.table ? (int64_t(1) << a.pm.page_shift) : a.n_cap;   // rows from head to head
-  const int nq = a.q ? a.Hq : 0, heads = nq + 2 * a.Hkv;
-  const int lane8 = tid & (kUnits - 1);
+  const int nq = a.q ? a.Hq : 0;
   const unsigned unit_mask = 0xffu << (tid & 24);
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tok; t0 < a.bt.T; t0 += static_cast<int64_t>(gridDim.x) * a.tok) {
     const int n = static_cast<int>(min(static_cast<int64_t>(a.tok), a.bt.T - t0));
@@ -214,10 +245,13 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const AppendArg
       const int tk = i / kFreqs;
       Pair c, s;
       turn_cos_sin(F * static_cast<uint64_t>(static_cast<int64_t>(rpos[tk])), c, s);
-      turn[tk][freq] = make_float4(c.h, s.h, c.l, s.l);
+      turn[0][tk][freq] = c.h;
+      turn[1][tk][freq] = s.h;
+      turn[2][tk][freq] = c.l;
+      turn[3][tk][freq] = s.l;
     }
     __syncthreads();
-    const int u = lane8, tk = (tid / kUnits) & (a.tok - 1), slice = tid / (kUnits * a.tok);
+    const int u = tid & (kUnits - 1), tk = (tid / kUnits) & (a.tok - 1), slice = tid / (kUnits * a.tok);
     const int step = kThreads / (kUnits * a.tok);
     if (tk < n && live[tk]) {
       const int64_t t = t0 + tk, row = row0[tk];
@@ -225,106 +259,98 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const AppendArg
       const bool turns = u < r16;
       // chunks of the unit in a rotated head and in a copied one
       const int c0 = turns && !a.interleaved ? u : 2 * u, c1 = turns && !a.interleaved ? u + r16 : 2 * u + 1;
-      // the unit, and which of its chunks, that holds chunk c of a rotated head
-      auto unit_of = [&](int c) { return a.interleaved || c >= 2 * r16 ? c >> 1 : (c < r16 ? c : c - r16); };
-      auto second_of = [&](int c) { return a.interleaved || c >= 2 * r16 ? (c & 1) != 0 : c >= r16; };
-      for (int h0 = slice; h0 < heads; h0 += kBatch * step) {
+      float cs[8], sn[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cs[i] = turns ? turn[0][tk][8 * u + i] : 1.0f;
+        sn[i] = turns ? turn[1][tk][8 * u + i] : 0.0f;
+      }
+      for (int h0 = slice; h0 < nq; h0 += kBatch * step) {
         uint4 x[kBatch], y[kBatch];
-        bool there[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           const int h = h0 + i * step;
-          there[i] = h < heads && (h < nq || row >= 0);
-          if (there[i]) {
-            const bool value = h >= nq + a.Hkv;
-            const uint16_t* src = h < nq ? a.q + t * a.qs + h * kD
-                                         : (value ? a.v + t * a.vs + (h - nq - a.Hkv) * kD : a.k + t * a.ks + (h - nq) * kD);
-            x[i] = *reinterpret_cast<const uint4*>(src + 8 * (value ? 2 * u : c0));
-            y[i] = *reinterpret_cast<const uint4*>(src + 8 * (value ? 2 * u + 1 : c1));
+          if (h < nq) {
+            const uint16_t* src = a.q + t * a.qs + h * kD;
+            x[i] = *reinterpret_cast<const uint4*>(src + 8 * c0);
+            y[i] = *reinterpret_cast<const uint4*>(src + 8 * c1);
           }
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          if (!there[i]) continue;
           const int h = h0 + i * step;
+          if (h >= nq) continue;
           uint32_t* xa = &x[i].x;
           uint32_t* ya = &y[i].x;
-          if (h < nq) {
-            if (turns) {
-              if (a.interleaved) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float4 p = turn[tk][8 * u + e], r = turn[tk][8 * u + 4 + e];
-                  const float2 f = bf2_to_f2(xa[e]), g = bf2_to_f2(ya[e]);
-                  xa[e] = pack_bf16(f.x * p.x - f.y * p.y, f.y * p.x + f.x * p.y);
-                  ya[e] = pack_bf16(g.x * r.x - g.y * r.y, g.y * r.x + g.x * r.y);
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float4 p = turn[tk][8 * u + 2 * e], r = turn[tk][8 * u + 2 * e + 1];
-                  const float2 f = bf2_to_f2(xa[e]), g = bf2_to_f2(ya[e]);
-                  xa[e] = pack_bf16(f.x * p.x - g.x * p.y, f.y * r.x - g.y * r.y);
-                  ya[e] = pack_bf16(g.x * p.x + f.x * p.y, g.y * r.x + f.y * r.y);
-                }
-              }
-            }
-            uint16_t* dst = a.q_out + (t * a.Hq + h) * kD;
-            *reinterpret_cast<uint4*>(dst + 8 * c0) = x[i];
-            *reinterpret_cast<uint4*>(dst + 8 * c1) = y[i];
-            continue;
-          }
-          const bool value = h >= nq + a.Hkv;
-          if (turns && !value) {
+          if (turns) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 f = bf2_to_f2(xa[e]), g = bf2_to_f2(ya[e]);
-              const float4 p = turn[tk][8 * u + (a.interleaved ? e : 2 * e)];
-              const float4 r = turn[tk][8 * u + (a.interleaved ? 4 + e : 2 * e + 1)];
-              const Pair pc{p.x, p.z}, ps{p.y, p.w}, pn{-p.y, -p.w}, rc{r.x, r.z}, rs{r.y, r.w}, rn{-r.y, -r.w};
               if (a.interleaved) {
-                xa[e] = rotated_bf16(f.x, pc, f.y, pn) | rotated_bf16(f.y, pc, f.x, ps) << 16;
-                ya[e] = rotated_bf16(g.x, rc, g.y, rn) | rotated_bf16(g.y, rc, g.x, rs) << 16;
+                xa[e] = pack_bf16(f.x * cs[e] - f.y * sn[e], f.y * cs[e] + f.x * sn[e]);
+                ya[e] = pack_bf16(g.x * cs[4 + e] - g.y * sn[4 + e], g.y * cs[4 + e] + g.x * sn[4 + e]);
               } else {
-                xa[e] = rotated_bf16(f.x, pc, g.x, pn) | rotated_bf16(f.y, rc, g.y, rn) << 16;
-                ya[e] = rotated_bf16(g.x, pc, f.x, ps) | rotated_bf16(g.y, rc, f.y, rs) << 16;
+                xa[e] = pack_bf16(f.x * cs[2 * e] - g.x * sn[2 * e], f.y * cs[2 * e + 1] - g.y * sn[2 * e + 1]);
+                ya[e] = pack_bf16(g.x * cs[2 * e] + f.x * sn[2 * e], g.y * cs[2 * e + 1] + f.y * sn[2 * e + 1]);
               }
             }
           }
-          // Largest magnitudes of the groups that x and y lie in: each of them is half
-          // of a group, the other half being another thread's chunk, or its own.
-          const int cx = value ? 2 * u : c0, cy = value ? 2 * u + 1 : c1;
-          uint32_t mx = abs_max(x[i]), my = abs_max(y[i]);
-          if (value || a.interleaved) {
-            mx = my = max(mx, my);
-          } else {
-            const int px = cx ^ 1, py = cy ^ 1, base = tid & 24;
-            const uint32_t xx = __shfl_sync(unit_mask, mx, base + unit_of(px)), xy = __shfl_sync(unit_mask, my, base + unit_of(px));
-            const uint32_t yx = __shfl_sync(unit_mask, mx, base + unit_of(py)), yy = __shfl_sync(unit_mask, my, base + unit_of(py));
-            mx = max(mx, second_of(px) ? xy : xx);
-            my = max(my, second_of(py) ? yy : yx);
-          }
-          const float inv = value ? a.v_inv : a.k_inv;
-          const uint32_t sx = kv4_scale_of(__uint_as_float(mx << 16) * inv), sy = kv4_scale_of(__uint_as_float(my << 16) * inv);
-          const int64_t r = row + (value ? h - nq - a.Hkv : h - nq) * head_rows;
-          uint8_t* codes = (value ? a.kv.V : a.kv.K) + r * kKv4Codes;
-          *reinterpret_cast<uint32_t*>(codes + 4 * cx) = codes_of(x[i], inv, kv4_divisor(sx));
-          *reinterpret_cast<uint32_t*>(codes + 4 * cy) = codes_of(y[i], inv, kv4_divisor(sy));
-          // the row's eight scales, gathered from its eight threads
-          const uint64_t mine = static_cast<uint64_t>(sx) << (8 * (cx >> 1)) | static_cast<uint64_t>(sy) << (8 * (cy >> 1));
-          const uint32_t lo = __reduce_or_sync(unit_mask, static_cast<uint32_t>(mine));
-          const uint32_t hi = __reduce_or_sync(unit_mask, static_cast<uint32_t>(mine >> 32));
-          if (u == 0) *reinterpret_cast<uint2*>((value ? a.kv.V_sf : a.kv.K_sf) + r * kKv4Groups) = make_uint2(lo, hi);
+          uint16_t* dst = a.q_out + (t * a.Hq + h) * kD;
+          *reinterpret_cast<uint4*>(dst + 8 * c0) = x[i];
+          *reinterpret_cast<uint4*>(dst + 8 * c1) = y[i];
         }
       }
+      // the lane, and which of its chunks, that holds chunk c of a rotated head
+      auto holder = [&](int c) {
+        const bool pairs = a.interleaved || c >= 2 * r16;
+        return Halves{(tid & 24) + (pairs ? c >> 1 : (c < r16 ? c : c - r16)), pairs ? (c & 1) != 0 : c >= r16};
+      };
+      const Halves px = holder(c0 ^ 1), py = holder(c1 ^ 1);
+      if (row >= 0)
+        for (int h = slice; h < a.Hkv; h += step) {
+          const uint16_t* ksrc = a.k + t * a.ks + h * kD;
+          const uint16_t* vsrc = a.v + t * a.vs + h * kD;
+          uint4 x = *reinterpret_cast<const uint4*>(ksrc + 8 * c0), y = *reinterpret_cast<const uint4*>(ksrc + 8 * c1);
+          const uint4 v0 = *reinterpret_cast<const uint4*>(vsrc + 16 * u), v1 = *reinterpret_cast<const uint4*>(vsrc + 16 * u + 8);
+          const int64_t r = row + h * head_rows;
+          store_quantised(v0, v1, 2 * u, 2 * u + 1, true, px, py, a.v_inv, a.kv.V + r * kKv4Codes, a.kv.V_sf + r * kKv4Groups,
+                          unit_mask, u == 0);
+          if (turns) {
+            uint32_t* xa = &x.x;
+            uint32_t* ya = &y.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = bf2_to_f2(xa[e]), g = bf2_to_f2(ya[e]);
+              const int e0 = a.interleaved ? e : 2 * e, e1 = a.interleaved ? 4 + e : 2 * e + 1;
+              const Pair c{turn[0][tk][8 * u + e0], turn[2][tk][8 * u + e0]}, s{turn[1][tk][8 * u + e0], turn[3][tk][8 * u + e0]};
+              const Pair d{turn[0][tk][8 * u + e1], turn[2][tk][8 * u + e1]}, w{turn[1][tk][8 * u + e1], turn[3][tk][8 * u + e1]};
+              const Pair sm{-s.h, -s.l}, wm{-w.h, -w.l};
+              if (a.interleaved) {
+                xa[e] = rotated_bf16(f.x, c, f.y, sm) | rotated_bf16(f.y, c, f.x, s) << 16;
+                ya[e] = rotated_bf16(g.x, d, g.y, wm) | rotated_bf16(g.y, d, g.x, w) << 16;
+              } else {
+                xa[e] = rotated_bf16(f.x, c, g.x, sm) | rotated_bf16(f.y, d, g.y, wm) << 16;
+                ya[e] = rotated_bf16(g.x, c, f.x, s) | rotated_bf16(g.y, d, f.y, w) << 16;
+              }
+            }
+          }
+          store_quantised(x, y, c0, c1, a.interleaved != 0, px, py, a.k_inv, a.kv.K + r * kKv4Codes, a.kv.K_sf + r * kKv4Groups,
+                          unit_mask, u == 0);
+        }
     }
     __syncthreads();   // the next tile rewrites the angles
   }
   pdl_trigger();
 }
 
-constexpr int kReadTok = 16;     // tokens of a read block's tile
+constexpr int kReadTok = 32;     // tokens of a read block's tile
 constexpr int kRowLanes = 16;    // threads of a row: 8 values each
+constexpr int kReadRows = kThreads / kRowLanes;   // rows of a pass
+#ifndef KV4_RB
+#define KV4_RB 4
+#define KV4_RF 4
+#endif
+constexpr int kReadBatch = KV4_RF;    // rows whose loads a thread has in flight
 
 struct ReadArgs {
   Kv4Cache kv;
@@ -338,7 +364,7 @@ struct ReadArgs {
   unsigned* err;
 };
 
-__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kThreads, KV4_RB) kv4_read_kernel(const ReadArgs a) {
   __shared__ int64_t row0[kReadTok];
   const int tid = threadIdx.x, c = tid & (kRowLanes - 1);
   pdl_wait();
@@ -361,28 +387,35 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
       row0[tid] = row;
     }
     __syncthreads();
-    const int tk = tid / kRowLanes;   // rows of one pass: the tile's tokens, of one head
-    const int64_t row = row0[tk];
-    if (row < 0) continue;
-    const int64_t t = t0 + tk;
-#pragma unroll 4
-    for (int g = 0; g < a.Hkv; ++g) {
+    // rows in passes of 16 tokens of one head and side: keys and values of a head, the tile's halves
+    const int passes = 2 * (kReadTok / kReadRows) * a.Hkv;
+    for (int i0 = 0; i0 < passes; i0 += kReadBatch) {
+      uint32_t w[kReadBatch], sf[kReadBatch];
 #pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        const int64_t r = row + g * head_rows;
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>((side ? a.kv.V : a.kv.K) + r * kKv4Codes) + c);
-        const uint32_t sf = __ldg((side ? a.kv.V_sf : a.kv.K_sf) + r * kKv4Groups + (c >> 1));
+      for (int k = 0; k < kReadBatch; ++k) {
+        const int i = i0 + k, side = i & 1, g = i >> 2;
+        const int64_t row = row0[tid / kRowLanes + (i >> 1 & 1) * kReadRows];
+        if (i < passes && row >= 0) {
+          const int64_t r = row + g * head_rows;
+          w[k] = __ldg(reinterpret_cast<const uint32_t*>((side ? a.kv.V : a.kv.K) + r * kKv4Codes) + c);
+          sf[k] = __ldg((side ? a.kv.V_sf : a.kv.K_sf) + r * kKv4Groups + (c >> 1));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kReadBatch; ++k) {
+        const int i = i0 + k, side = i & 1, g = i >> 2, tk = tid / kRowLanes + (i >> 1 & 1) * kReadRows;
+        if (i >= passes || row0[tk] < 0) continue;
         const float f = side ? a.kv.v_scale : a.kv.k_scale;
-        const __half2 s = kv4_scales(sf * 0x101u);
+        const __half2 s = kv4_scales(sf[k] * 0x101u);
         __half2 h[4];
-        kv4_codes(w, h);
+        kv4_codes(w[k], h);
         uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = __half22float2(__hmul2(h[i], s));
-          o[i] = pack_bf16(v.x * f, v.y * f);
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = __half22float2(__hmul2(h[e], s));
+          o[e] = pack_bf16(v.x * f, v.y * f);
         }
-        uint16_t* dst = side ? a.V_out + t * a.v_token + g * a.v_head : a.K_out + t * a.k_token + g * a.k_head;
+        uint16_t* dst = side ? a.V_out + (t0 + tk) * a.v_token + g * a.v_head : a.K_out + (t0 + tk) * a.k_token + g * a.k_head;
         *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
