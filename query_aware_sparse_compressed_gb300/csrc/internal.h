@@ -322,6 +322,24 @@ cudaError_t launch_kv4_read(const qasc_shape& s, const PageMap& pm, const Batch&
                             int64_t k_token, int64_t k_head, uint16_t* V_out, int64_t v_token, int64_t v_head,
                             const DeviceInfo& dev, cudaStream_t stream);
 
+// A bf16 copy of the tokens that the long sequences of a window call attend to, as a
+// paged cache of its own: pages of kCopyPage tokens, those between sink and window left out.
+constexpr int kCopyPage = 256;
+struct Kv4Copy {
+  int64_t most_rows = 0;           // sequences with more query rows of a KV head are copied
+  int64_t capacity = 0;            // pages of K and of V
+  int64_t pages_per_seq = 0;       // of the copy's block table
+  int32_t* copied = nullptr;       // [B] 1: copied
+  int32_t* lens = nullptr;         // [B] tokens in the copy (0: not copied)
+  int32_t* first = nullptr;        // [B + 1] first page of each sequence, and all pages
+  int32_t* drop = nullptr;         // [B] tokens left out behind the sink
+  int32_t* table = nullptr;        // [B][pages_per_seq]
+  uint16_t* K = nullptr;           // [capacity][Hkv][kCopyPage][d]
+  uint16_t* V = nullptr;
+};
+cudaError_t launch_kv4_copy(const qasc_shape& s, const PageMap& pm, const Batch& bt, const Kv4Cache& kv, int32_t sink,
+                            int32_t local, const Kv4Copy& c, const DeviceInfo& dev, cudaStream_t stream);
+
 // Attention over a 4-bit cache: a window call's batch, or one token of every
 // sequence over sink, listed and local tokens (listed: lists as in
 // launch_sparse_attn, shape.n tokens in every sequence).
@@ -342,8 +360,8 @@ struct Kv4AttnArgs {
 };
 size_t kv4_attn_least_bytes();   // for the most SMs
 size_t kv4_window_workspace_bytes(const qasc_shape& s, int64_t T, int64_t max_q, int32_t sink, int32_t local);
-int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, size_t ws_bytes, const DeviceInfo& dev,
-                    cudaStream_t stream);
+// The workspace has the size above (kv4_attn_least_bytes() of a listed call).
+int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t configure_kv4_kernels(const DeviceInfo& dev);
 
 // Neighbour expansion: rows of K ascending candidates in, the ascending union

@@ -82,7 +82,7 @@ struct Args {
   int B, Hq, Hkv, gsh;      // gsh = log2(Hq / Hkv)
   int64_t n_cap;
   int n, sink_end, local_start;   // listed: tokens of every sequence, its regions
-  int64_t most_rows;        // sequences with more rows are left out (0: none)
+  const int32_t* copied;    // [B] not 0: a sequence that is left out here (NULL: none)
   int whole;                // items are not shared between blocks
   int ssh;                  // sequences of a sum: 2^ssh
   int ush;                  // tiles of a place: 2^ush, so that the line has fewer than 2^31 places
@@ -168,9 +168,9 @@ __device__ __forceinline__ int list_len(const Args& p, int b, int g) {
 // Items of a sequence (row blocks times KV heads) and the places of each: the
 // most tiles that any of them has (whole items: one).
 template <int kRows>
-__device__ __forceinline__ int items_of(const Args& p, const Seq& s) {
+__device__ __forceinline__ int items_of(const Args& p, const Seq& s, int b) {
   const int64_t rows = static_cast<int64_t>(s.ql) << p.gsh;
-  if (p.most_rows && rows > p.most_rows) return 0;
+  if (p.copied && __ldcg(p.copied + b)) return 0;
   return static_cast<int>((rows + kRows - 1) / kRows) * p.Hkv;
 }
 template <bool kList, int kRows>
@@ -314,7 +314,7 @@ __device__ __forceinline__ Walk walk_at(const Args& p, const int* place, int x) 
   int at = hi == 0 ? 0 : place[lo];
   for (w.b = lo << p.ssh;; ++w.b) {
     w.s = seq_of<kList>(p, w.b);
-    w.items = items_of<kRows>(p, w.s);
+    w.items = items_of<kRows>(p, w.s, w.b);
     if (w.items == 0) continue;
     w.span = span_of<kList, kRows>(p, w.s, w.b);
     const int all = w.items * w.span;
@@ -334,7 +334,7 @@ __device__ __forceinline__ void walk_on(const Args& p, Walk& w) {
   w.rem = 0;
   while (++w.b < p.B) {
     w.s = seq_of<kList>(p, w.b);
-    w.items = items_of<kRows>(p, w.s);
+    w.items = items_of<kRows>(p, w.s, w.b);
     if (w.items == 0) continue;
     w.span = span_of<kList, kRows>(p, w.s, w.b);
     return;
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
       int sum = 0;
       for (int b = i << p.ssh; b < min(p.B, (i + 1) << p.ssh); ++b) {
         const Seq s = seq_of<kList>(p, b);
-        const int items = items_of<kRows>(p, s);
+        const int items = items_of<kRows>(p, s, b);
         if (items > 0) sum += items * span_of<kList, kRows>(p, s, b);
       }
       S.place[i] = sum;
@@ -995,21 +995,50 @@ static_assert(sizeof(Smem<1>) <= 232448 && sizeof(Smem<2>) <= 232448, "shared me
 // Columns of an item: single tokens have at most eight.
 int tiles_of(const qasc_shape& s, int64_t max_q) { return max_q * (s.Hq / s.Hkv) <= 8 ? 1 : 2; }
 
+// Sequences of more rows than this take their keys and values from a bf16 copy and
+// go to kv_window_attn's kernel, whose products are tcgen05's.
+#ifndef KV4_CR
+#define KV4_CR 128
+#endif
+constexpr int64_t kCopyRows = KV4_CR;
+constexpr int64_t kCopyBytes = int64_t(1) << 32;   // of a copy, at most
+
+struct CopyLayout {
+  int64_t capacity = 0, pages_per_seq = 0;   // capacity 0: no copy
+  size_t off_lists = 0, off_attn = 0, attn_bytes = 0, off_k = 0, off_v = 0, total = 0;
+};
+// Of a call whose sequences have at most max_q new tokens.
+CopyLayout copy_layout(const qasc_shape& s, int64_t T, int64_t max_q, int32_t sink, int32_t local) {
+  CopyLayout L;
+  const int64_t gq = s.Hq / s.Hkv;
+  L.total = kv4_attn_least_bytes();
+  if (max_q * gq <= kCopyRows) return L;
+  const int64_t tokens = std::min<int64_t>(s.n_cap, static_cast<int64_t>(sink) + local + max_q - 1);
+  L.pages_per_seq = (tokens + kCopyPage - 1) / kCopyPage;
+  const int64_t cap = L.pages_per_seq * kCopyPage;
+  if (cap >= kTokensMost || static_cast<int64_t>(s.B) * s.Hkv * cap >= (int64_t(1) << 31)) return L;
+  const int64_t seqs = std::min<int64_t>(s.B, T * gq / (kCopyRows + 1));   // that can be as long
+  const int64_t page_bytes = static_cast<int64_t>(s.Hkv) * kCopyPage * kD * 2;
+  const int64_t most = std::min(kCopyBytes / (2 * page_bytes), ((int64_t(1) << 31) - 1) / (s.Hkv * kCopyPage));
+  L.capacity = std::min(seqs * L.pages_per_seq, most);
+  L.off_lists = align_up(L.total, 256);
+  L.off_attn = align_up(L.off_lists + (4 * static_cast<size_t>(s.B) + 1 + static_cast<size_t>(s.B) * L.pages_per_seq) * sizeof(int32_t), 256);
+  L.attn_bytes = kv_attn_workspace_bytes(T, s.B, s.Hq, s.Hkv, false, kMaxSmsForSizing);
+  L.off_k = align_up(L.off_attn + L.attn_bytes, 256);
+  L.off_v = L.off_k + static_cast<size_t>(L.capacity * page_bytes);
+  L.total = L.off_v + static_cast<size_t>(L.capacity * page_bytes);
+  return L;
+}
+
 }  // namespace
 
 size_t kv4_attn_least_bytes() { return layout_of(16, kMaxSmsForSizing).total; }
 
 size_t kv4_window_workspace_bytes(const qasc_shape& s, int64_t T, int64_t max_q, int32_t sink, int32_t local) {
-  (void)s;
-  (void)T;
-  (void)max_q;
-  (void)sink;
-  (void)local;
-  return kv4_attn_least_bytes();
+  return copy_layout(s, T, max_q, sink, local).total;
 }
 
-int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, size_t ws_bytes, const DeviceInfo& dev,
-                    cudaStream_t stream) {
+int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream) {
   Args p{};
   p.a = a;
   p.a.sink = std::min(a.sink, kTokensMost);   // more mean the same
@@ -1027,16 +1056,58 @@ int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, size
   }
   while ((s.B - 1) >> p.ssh >= kSums) ++p.ssh;
   p.err = dev.err_word;
-  const int nt = a.listed ? 1 : tiles_of(s, a.max_q);
-  const int64_t blocks = (a.bt.T * (s.Hq / s.Hkv) + 8 * nt - 1) / (8 * nt) + s.B;   // row blocks of a KV head, at most
+
+  const CopyLayout C = a.listed ? CopyLayout() : copy_layout(s, a.bt.T, a.max_q, a.sink, a.local);
+  if (C.capacity > 0) {
+    Kv4Copy c;
+    c.most_rows = kCopyRows;
+    c.capacity = C.capacity;
+    c.pages_per_seq = C.pages_per_seq;
+    c.copied = reinterpret_cast<int32_t*>(ws + C.off_lists);
+    c.lens = c.copied + s.B;
+    c.drop = c.lens + s.B;
+    c.first = c.drop + s.B;
+    c.table = c.first + s.B + 1;
+    c.K = reinterpret_cast<uint16_t*>(ws + C.off_k);
+    c.V = reinterpret_cast<uint16_t*>(ws + C.off_v);
+    const cudaError_t e = launch_kv4_copy(s, a.pm, a.bt, a.kv, p.a.sink, p.a.local, c, dev, stream);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    // The copied sequences; rows of the others come out as those of sequences without a
+    // token, and are written again below.
+    qasc_shape s2 = s;
+    s2.n = s2.n_cap = C.pages_per_seq * kCopyPage;
+    KvAttnArgs k;
+    k.q = a.q;
+    k.K = c.K;
+    k.V = c.V;
+    k.out = a.out;
+    k.lse = a.lse;
+    k.bt = a.bt;
+    k.bt.lens = c.lens;
+    k.pm.table = c.table;
+    k.pm.pages_per_seq = C.pages_per_seq;
+    k.pm.num_pages = C.capacity;
+    while ((1 << k.pm.page_shift) < kCopyPage) ++k.pm.page_shift;
+    k.cache_rows = C.capacity * s.Hkv * kCopyPage;
+    k.sink = a.sink;
+    k.local = a.local;
+    size_t bytes = C.attn_bytes;
+    const int rc = launch_kv_attn(s2, k, ws + C.off_attn, &bytes, dev, stream);
+    if (rc != 0) return rc;
+    p.copied = c.copied;
+  }
+
+  const int64_t gq = s.Hq / s.Hkv;
+  const int64_t most_q = C.capacity > 0 && a.bt.T > s.B ? std::max<int64_t>(1, kCopyRows / gq) : a.max_q;
+  const int nt = a.listed ? 1 : tiles_of(s, most_q);
+  const int64_t blocks = (a.bt.T * gq + 8 * nt - 1) / (8 * nt) + s.B;   // row blocks of a KV head, at most
   while (blocks * s.Hkv * (((s.n_cap / kTile + 2) >> p.ush) + 1 + kItemCost) >= (int64_t(1) << 31)) ++p.ush;
   // Items of few tiles are not shared between blocks, which saves the merge.
   const int64_t most = a.listed ? p.sink_end + static_cast<int64_t>(a.K) + (p.n - p.local_start)
-                                : std::min<int64_t>(s.n_cap, static_cast<int64_t>(a.local) + a.sink + a.max_q - 1);
+                                : std::min<int64_t>(s.n_cap, static_cast<int64_t>(p.a.local) + p.a.sink + 8 * nt / gq - 1);
   p.whole = most <= kWholeTokens;
   const int grid = dev.num_sms;
   const Layout L = layout_of(8 * nt, grid);
-  if (ws_bytes < L.total) return static_cast<int>(cudaErrorInvalidValue);
   p.share = reinterpret_cast<Share*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);
   p.part_o = reinterpret_cast<float*>(ws + L.off_o);

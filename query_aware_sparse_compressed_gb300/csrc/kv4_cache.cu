@@ -364,9 +364,51 @@ struct ReadArgs {
   unsigned* err;
 };
 
+// The tile's rows in bf16: token i's row of KV head 0 is row0[i] (-1: rows of zeros
+// where `zeros` is -1, none written otherwise; -2: none written), strides of the
+// outputs in values.
+__device__ __forceinline__ void read_rows(const Kv4Cache& kv, int Hkv, const int64_t* row0, int64_t head_rows, uint16_t* K_out,
+                                          int64_t k_token, int64_t k_head, uint16_t* V_out, int64_t v_token, int64_t v_head,
+                                          int zeros) {
+  const int tid = threadIdx.x, c = tid & (kRowLanes - 1);
+  // passes of 16 tokens of one head and side: keys and values of a head, the tile's halves
+  const int passes = 2 * (kReadTok / kReadRows) * Hkv;
+  for (int i0 = 0; i0 < passes; i0 += kReadBatch) {
+    uint32_t w[kReadBatch], sf[kReadBatch];
+#pragma unroll
+    for (int k = 0; k < kReadBatch; ++k) {
+      const int i = i0 + k, side = i & 1, g = i >> 2;
+      const int64_t row = row0[tid / kRowLanes + (i >> 1 & 1) * kReadRows];
+      w[k] = sf[k] = 0;
+      if (i < passes && row >= 0) {
+        const int64_t r = row + g * head_rows;
+        w[k] = __ldg(reinterpret_cast<const uint32_t*>((side ? kv.V : kv.K) + r * kKv4Codes) + c);
+        sf[k] = __ldg((side ? kv.V_sf : kv.K_sf) + r * kKv4Groups + (c >> 1));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kReadBatch; ++k) {
+      const int i = i0 + k, side = i & 1, g = i >> 2, tk = tid / kRowLanes + (i >> 1 & 1) * kReadRows;
+      if (i >= passes || row0[tk] < zeros) continue;
+      const float f = side ? kv.v_scale : kv.k_scale;
+      const __half2 s = kv4_scales(sf[k] * 0x101u);
+      __half2 h[4];
+      kv4_codes(w[k], h);
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = __half22float2(__hmul2(h[e], s));
+        o[e] = pack_bf16(v.x * f, v.y * f);
+      }
+      uint16_t* dst = side ? V_out + tk * v_token + g * v_head : K_out + tk * k_token + g * k_head;
+      *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, KV4_RB) kv4_read_kernel(const ReadArgs a) {
   __shared__ int64_t row0[kReadTok];
-  const int tid = threadIdx.x, c = tid & (kRowLanes - 1);
+  const int tid = threadIdx.x;
   pdl_wait();
   for (int64_t b = static_cast<int64_t>(blockIdx.x) * kThreads + tid; b < a.bt.B; b += static_cast<int64_t>(gridDim.x) * kThreads) {
     const int len = __ldg(a.bt.lens + b);
@@ -387,38 +429,116 @@ __global__ void __launch_bounds__(kThreads, KV4_RB) kv4_read_kernel(const ReadAr
       row0[tid] = row;
     }
     __syncthreads();
-    // rows in passes of 16 tokens of one head and side: keys and values of a head, the tile's halves
-    const int passes = 2 * (kReadTok / kReadRows) * a.Hkv;
-    for (int i0 = 0; i0 < passes; i0 += kReadBatch) {
-      uint32_t w[kReadBatch], sf[kReadBatch];
-#pragma unroll
-      for (int k = 0; k < kReadBatch; ++k) {
-        const int i = i0 + k, side = i & 1, g = i >> 2;
-        const int64_t row = row0[tid / kRowLanes + (i >> 1 & 1) * kReadRows];
-        if (i < passes && row >= 0) {
-          const int64_t r = row + g * head_rows;
-          w[k] = __ldg(reinterpret_cast<const uint32_t*>((side ? a.kv.V : a.kv.K) + r * kKv4Codes) + c);
-          sf[k] = __ldg((side ? a.kv.V_sf : a.kv.K_sf) + r * kKv4Groups + (c >> 1));
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kReadBatch; ++k) {
-        const int i = i0 + k, side = i & 1, g = i >> 2, tk = tid / kRowLanes + (i >> 1 & 1) * kReadRows;
-        if (i >= passes || row0[tk] < 0) continue;
-        const float f = side ? a.kv.v_scale : a.kv.k_scale;
-        const __half2 s = kv4_scales(sf[k] * 0x101u);
-        __half2 h[4];
-        kv4_codes(w[k], h);
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 v = __half22float2(__hmul2(h[e], s));
-          o[e] = pack_bf16(v.x * f, v.y * f);
-        }
-        uint16_t* dst = side ? a.V_out + (t0 + tk) * a.v_token + g * a.v_head : a.K_out + (t0 + tk) * a.k_token + g * a.k_head;
-        *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+    read_rows(a.kv, a.Hkv, row0, head_rows, a.K_out + t0 * a.k_token, a.k_token, a.k_head, a.V_out + t0 * a.v_token, a.v_token,
+              a.v_head, 0);
+  }
+  pdl_trigger();
+}
+
+// ---- the bf16 copy that long sequences of a window call attend to
+constexpr int kPlanThreads = 1024;
+
+struct CopyArgs {
+  Kv4Cache kv;
+  Kv4Copy c;
+  PageMap pm;
+  Batch bt;
+  int B, Hkv, gsh;
+  int32_t sink, local;
+  int64_t n_cap;
+  unsigned* err;
+};
+
+// Which sequences are copied, their pages and the copy's block table; one block.
+// Sequences take pages in their order as long as all of theirs are left.
+__global__ void __launch_bounds__(kPlanThreads) kv4_copy_plan_kernel(const CopyArgs a) {
+  __shared__ int32_t sums[32];
+  __shared__ int32_t taken;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  if (tid == 0) taken = 0;
+  __syncthreads();
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int pages = 0, len2 = 0, drop = 0;
+    if (b < a.B) {
+      const int64_t q0 = min(max(a.bt.cu_q ? __ldg(a.bt.cu_q + b) : static_cast<int64_t>(b), int64_t(0)), a.bt.T);
+      const int64_t q1 = min(max(a.bt.cu_q ? __ldg(a.bt.cu_q + b + 1) : static_cast<int64_t>(b) + 1, q0), a.bt.T);
+      const int64_t len = min(max(static_cast<int64_t>(__ldg(a.bt.lens + b)), int64_t(0)), a.n_cap);
+      if (((q1 - q0) << a.gsh) > a.c.most_rows && len > 0) {
+        const int64_t lo = max(len - (q1 - q0) - a.local + 1, int64_t(0));   // the first row's window
+        drop = static_cast<int>(max(lo - a.sink, int64_t(0)));
+        len2 = static_cast<int>(len) - drop;
+        pages = (len2 + kCopyPage - 1) / kCopyPage;
+        if (pages > a.c.pages_per_seq) pages = 0;   // more new tokens than the call said
       }
     }
+    // exclusive sums over the block; a sequence that does not fit takes none, and is asked again without it
+    int inc = pages;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += w;
+    }
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    int before = taken;
+    for (int w = 0; w < warp; ++w) before += sums[w];
+    int total = taken;
+    for (int w = 0; w < kPlanThreads / 32; ++w) total += sums[w];
+    const int first = before + inc - pages;
+    const bool fits = pages > 0 && first + pages <= a.c.capacity;
+    if (b < a.B) {
+      a.c.copied[b] = fits;
+      a.c.lens[b] = fits ? len2 : 0;
+      a.c.drop[b] = drop;
+      a.c.first[b] = static_cast<int>(min(static_cast<int64_t>(first), a.c.capacity));
+    }
+    __syncthreads();
+    if (tid == 0) taken = total;
+    __syncthreads();
+  }
+  if (tid == 0) a.c.first[a.B] = static_cast<int>(min(static_cast<int64_t>(taken), a.c.capacity));
+  __syncthreads();
+  for (int b = 0; b < a.B; ++b) {
+    if (a.c.copied[b] == 0) continue;
+    const int pages = (a.c.lens[b] + kCopyPage - 1) / kCopyPage;
+    for (int i = tid; i < pages; i += kPlanThreads) a.c.table[b * a.c.pages_per_seq + i] = a.c.first[b] + i;
+  }
+  pdl_trigger();
+}
+
+// Tiles of kReadTok tokens of the copy's pages.
+__global__ void __launch_bounds__(kThreads, KV4_RB) kv4_copy_kernel(const CopyArgs a) {
+  __shared__ int64_t row0[kReadTok];
+  const int tid = threadIdx.x;
+  pdl_wait();
+  const int64_t head_rows = a.pm.table ? (int64_t(1) << a.pm.page_shift) : a.n_cap;
+  constexpr int kParts = kCopyPage / kReadTok;
+  const int tiles = __ldcg(a.c.first + a.B) * kParts;
+  for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
+    const int page = i / kParts, part = i - page * kParts;
+    int lo = 0, hi = a.B;   // the last sequence whose pages begin at or before this one: those of none stand before it
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldcg(a.c.first + mid) <= page) lo = mid;
+      else hi = mid;
+    }
+    const int len = __ldcg(a.c.lens + lo), at = (page - __ldcg(a.c.first + lo)) * kCopyPage + part * kReadTok;
+    __syncthreads();
+    if (tid < kReadTok) {
+      int64_t row = -2;   // behind the last token: not written
+      if (at + tid < len) {
+        const int t = at + tid < a.sink ? at + tid : at + tid + __ldcg(a.c.drop + lo);
+        row = cache_row(a.pm, lo, 0, a.Hkv, a.n_cap, t);
+        if (row < 0) record_error(a.err, kErrBadPage);   // rows of zeros
+      }
+      row0[tid] = row;
+    }
+    __syncthreads();
+    const int64_t to = (static_cast<int64_t>(page) * a.Hkv * kCopyPage + part * kReadTok) * kD;
+    read_rows(a.kv, a.Hkv, row0, head_rows, a.c.K + to, kD, static_cast<int64_t>(kCopyPage) * kD, a.c.V + to, kD,
+              static_cast<int64_t>(kCopyPage) * kD, -1);
   }
   pdl_trigger();
 }
@@ -478,6 +598,27 @@ cudaError_t launch_kv4_read(const qasc_shape& s, const PageMap& pm, const Batch&
   const int64_t tiles = (bt.T + kReadTok - 1) / kReadTok;
   const int64_t most = static_cast<int64_t>(dev.num_sms) * 8;
   return launch_dependent(kv4_read_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads), 0, stream,
+                          1, a);
+}
+
+cudaError_t launch_kv4_copy(const qasc_shape& s, const PageMap& pm, const Batch& bt, const Kv4Cache& kv, int32_t sink,
+                            int32_t local, const Kv4Copy& c, const DeviceInfo& dev, cudaStream_t stream) {
+  CopyArgs a{};
+  a.kv = kv;
+  a.c = c;
+  a.pm = pm;
+  a.bt = bt;
+  a.B = s.B;
+  a.Hkv = s.Hkv;
+  while ((1 << a.gsh) < s.Hq / s.Hkv) ++a.gsh;
+  a.sink = sink;
+  a.local = local;
+  a.n_cap = s.n_cap;
+  a.err = dev.err_word;
+  const cudaError_t e = launch_dependent(kv4_copy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, 1, a);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = c.capacity * (kCopyPage / kReadTok), most = static_cast<int64_t>(dev.num_sms) * 8;
+  return launch_dependent(kv4_copy_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads), 0, stream,
                           1, a);
 }
 
