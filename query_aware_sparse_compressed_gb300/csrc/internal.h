@@ -331,8 +331,6 @@ struct Kv4Copy {
   int64_t pages_per_seq = 0;       // of the copy's block table
   int32_t* copied = nullptr;       // [B] 1: copied
   int32_t* lens = nullptr;         // [B] tokens in the copy (0: not copied)
-  int32_t* first = nullptr;        // [B + 1] first page of each sequence, and all pages
-  int32_t* drop = nullptr;         // [B] tokens left out behind the sink
   int32_t* table = nullptr;        // [B][pages_per_seq]
   uint16_t* K = nullptr;           // [capacity][Hkv][kCopyPage][d]
   uint16_t* V = nullptr;

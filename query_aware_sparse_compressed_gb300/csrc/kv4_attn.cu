@@ -279,25 +279,24 @@ __device__ __forceinline__ bool attends(const Args& p, int pos, int t) {
   return t <= pos && (t < p.a.sink || t > pos - p.a.local);
 }
 
-// Token of slot s of an item; -1: none that any of its rows attends to.  Of a window
+constexpr int kNoToken = INT_MIN;
+
+// Token of slot s of an item; kNoToken: none that any of its rows attends to.  Of a window
 // call the slots of the sink end with a tile and the window's begin with a multiple of
 // 32 tokens, so that a tile never leaves its page and its rows stand in a line.
 template <bool kList>
 __device__ __forceinline__ int token_of_slot(const Args& p, const Piece& pc, int s) {
-  if (s >= pc.cnt) return -1;
+  if (s >= pc.cnt) return kNoToken;
   if (!kList) {
-    if (s < pc.head) return s < p.a.sink ? s : -1;
+    if (s < pc.head) return s < p.a.sink ? s : kNoToken;
     const int t = pc.lo + s - pc.head;
-    return t <= pc.p1 && (t < p.a.sink || t > pc.p0 - p.a.local) ? t : -1;
+    return t <= pc.p1 && (t < p.a.sink || t > pc.p0 - p.a.local) ? t : kNoToken;
   }
   if (s < pc.head) return s;
   const int i = s - pc.head;
   if (i >= pc.lo) return p.local_start + i - pc.lo;
   const int64_t list = p.a.sel_per_kv ? static_cast<int64_t>(pc.b) * p.Hkv + pc.g : pc.b;
-  const int t = __ldg(p.a.sel + list * p.a.K + i);
-  if (t >= 0 && t < p.n) return t;
-  record_error(p.err, kErrBadPage);
-  return -1;
+  return __ldg(p.a.sel + list * p.a.K + i);   // (checked when it is used, a tile later: see next_rows)
 }
 
 // The item that holds place x.
@@ -521,9 +520,10 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
   int lt = 0, left = 0;                     // next tile of the newest item, tiles left of it
   int at0 = 0, m0 = 0, m1 = 0, tg = 0;      // of that item: token of tile 0's first slot in a line, whole tiles, KV head
   int64_t base = 0;
-  int tok = -1, tok_g = 0, tok_kind = kNone;   // lane's token of the tile after the next (of a line: its first)
+  int tok = kNoToken, tok_g = 0, tok_kind = kNone;   // lane's token of the tile after the next (of a line: its first)
   int64_t tok_base = 0;
-  int row = -1, row_kind = kNone;           // lane's row of the next tile (of a line: its first); -1: none
+  int at = kNoToken, at_g = 0, at_kind = kNone;      // lane's token of the next tile,
+  int at_page = 0;                                   // and its page or first row
   auto next_tokens = [&]() {
     if (__builtin_expect(left == 0, 0)) {
       Piece& pc = S.queue[warp][pushed % kQueue];
@@ -554,22 +554,18 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
     ++lt;
     --left;
   };
+  // What is read here is used a tile later, so that no tile waits for it.
   auto next_rows = [&]() {
-    row_kind = tok_kind;
-    row = -1;
-    if (tok_kind != kNone && tok >= 0) {
-      if (p.a.pm.table == nullptr) {
-        row = static_cast<int>(tok_base) + tok;
-      } else {
-        const int page = __ldg(p.a.pm.table + tok_base + (tok >> p.a.pm.page_shift));
-        if (page >= 0 && page < p.a.pm.num_pages) {
-          row = ((page * p.Hkv + tok_g) << p.a.pm.page_shift) + (tok & ((1 << p.a.pm.page_shift) - 1));
-        } else {
-          record_error(p.err, kErrBadPage);
-          row_kind = kRowwise;
-        }
-      }
+    at_kind = tok_kind;
+    at = tok;
+    at_g = tok_g;
+    if (kList && tok_kind != kNone && tok != kNoToken && (tok < 0 || tok >= p.n)) {   // an entry outside the cache
+      record_error(p.err, kErrBadPage);
+      at = kNoToken;
     }
+    at_page = static_cast<int>(tok_base);
+    if (p.a.pm.table != nullptr && at_kind != kNone && at != kNoToken)
+      at_page = __ldg(p.a.pm.table + tok_base + (at >> p.a.pm.page_shift));
     next_tokens();
   };
   uint32_t put = 0;   // stage that the next copies go to
@@ -579,30 +575,41 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
   const uint32_t k_at = 16 * lane, kf_at = kTileCodes + lane * kKv4Groups;
   const uint32_t v_at = kTileCodes + kTileScales + ((r & 4) | (r & 1) << 1 | (r >> 1 & 1)) * kKv4Codes + 16 * (j ^ (r >> 1 & 2));
   auto issue = [&]() {
-    const uint32_t at = ring_s + put * kStage;
-    if (__builtin_expect(!kList && row_kind == kLine, !kList)) {
+    const uint32_t to = ring_s + put * kStage;
+    int row = -1;   // lane's row (of a line: its first); -1: none
+    if (at_kind != kNone && at != kNoToken) {
+      if (p.a.pm.table == nullptr) {
+        row = at_page + at;
+      } else if (at_page >= 0 && at_page < p.a.pm.num_pages) {
+        row = ((at_page * p.Hkv + at_g) << p.a.pm.page_shift) + (at & ((1 << p.a.pm.page_shift) - 1));
+      } else {   // (of a line: in every lane)
+        record_error(p.err, kErrBadPage);
+        at_kind = kRowwise;
+      }
+    }
+    if (__builtin_expect(!kList && at_kind == kLine, !kList)) {
       const int64_t codes = static_cast<int64_t>(row) * kKv4Codes + 16 * lane;
       const int64_t scales = static_cast<int64_t>(row) * kKv4Groups + kKv4Groups * lane;
       const uint8_t* k = p.a.kv.K + codes;
       const uint8_t* v = p.a.kv.V + codes;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        cp_async16(at + k_at + 8 * i * kKv4Codes, k + 8 * i * kKv4Codes);
-        cp_async16(at + v_at + 8 * i * kKv4Codes, v + 8 * i * kKv4Codes);
+        cp_async16(to + k_at + 8 * i * kKv4Codes, k + 8 * i * kKv4Codes);
+        cp_async16(to + v_at + 8 * i * kKv4Codes, v + 8 * i * kKv4Codes);
       }
-      cp_async8(at + kf_at, p.a.kv.K_sf + scales);
-      cp_async8(at + kf_at + kTileCodes + kTileScales, p.a.kv.V_sf + scales);
-    } else if (row_kind == kRowwise) {
+      cp_async8(to + kf_at, p.a.kv.K_sf + scales);
+      cp_async8(to + kf_at + kTileCodes + kTileScales, p.a.kv.V_sf + scales);
+    } else if (at_kind == kRowwise) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int from = __shfl_sync(0xffffffffu, row, r + 8 * i);   // rows that are none: zeros
         const int64_t src = static_cast<int64_t>(max(from, 0)) * kKv4Codes + 16 * j;
-        cp_async16(at + k_at + 8 * i * kKv4Codes, p.a.kv.K + src, from >= 0 ? 16 : 0);
-        cp_async16(at + v_at + 8 * i * kKv4Codes, p.a.kv.V + src, from >= 0 ? 16 : 0);
+        cp_async16(to + k_at + 8 * i * kKv4Codes, p.a.kv.K + src, from >= 0 ? 16 : 0);
+        cp_async16(to + v_at + 8 * i * kKv4Codes, p.a.kv.V + src, from >= 0 ? 16 : 0);
       }
       const int64_t own = static_cast<int64_t>(max(row, 0)) * kKv4Groups;
-      cp_async8(at + kf_at, p.a.kv.K_sf + own, row >= 0 ? 8 : 0);
-      cp_async8(at + kf_at + kTileCodes + kTileScales, p.a.kv.V_sf + own, row >= 0 ? 8 : 0);
+      cp_async8(to + kf_at, p.a.kv.K_sf + own, row >= 0 ? 8 : 0);
+      cp_async8(to + kf_at + kTileCodes + kTileScales, p.a.kv.V_sf + own, row >= 0 ? 8 : 0);
     }
     cp_async_commit();
     put = put + 1 == kStages ? 0 : put + 1;
@@ -724,7 +731,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 const int pos = pc.p0 + ((8 * nt + 2 * j + c) >> p.gsh);
-                if (kList ? slot >= pc.cnt : token < 0 || !attends(p, pos, token)) s[mt][nt][2 * h + c] = -INFINITY;
+                if (kList ? slot >= pc.cnt : token == kNoToken || !attends(p, pos, token)) s[mt][nt][2 * h + c] = -INFINITY;
               }
           }
       }
@@ -1022,7 +1029,7 @@ CopyLayout copy_layout(const qasc_shape& s, int64_t T, int64_t max_q, int32_t si
   const int64_t most = std::min(kCopyBytes / (2 * page_bytes), ((int64_t(1) << 31) - 1) / (s.Hkv * kCopyPage));
   L.capacity = std::min(seqs * L.pages_per_seq, most);
   L.off_lists = align_up(L.total, 256);
-  L.off_attn = align_up(L.off_lists + (4 * static_cast<size_t>(s.B) + 1 + static_cast<size_t>(s.B) * L.pages_per_seq) * sizeof(int32_t), 256);
+  L.off_attn = align_up(L.off_lists + static_cast<size_t>(s.B) * (2 + L.pages_per_seq) * sizeof(int32_t), 256);
   L.attn_bytes = kv_attn_workspace_bytes(T, s.B, s.Hq, s.Hkv, false, kMaxSmsForSizing);
   L.off_k = align_up(L.off_attn + L.attn_bytes, 256);
   L.off_v = L.off_k + static_cast<size_t>(L.capacity * page_bytes);
@@ -1065,9 +1072,7 @@ int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, cons
     c.pages_per_seq = C.pages_per_seq;
     c.copied = reinterpret_cast<int32_t*>(ws + C.off_lists);
     c.lens = c.copied + s.B;
-    c.drop = c.lens + s.B;
-    c.first = c.drop + s.B;
-    c.table = c.first + s.B + 1;
+    c.table = c.lens + s.B;
     c.K = reinterpret_cast<uint16_t*>(ws + C.off_k);
     c.V = reinterpret_cast<uint16_t*>(ws + C.off_v);
     const cudaError_t e = launch_kv4_copy(s, a.pm, a.bt, a.kv, p.a.sink, p.a.local, c, dev, stream);
@@ -1098,8 +1103,8 @@ int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, cons
   }
 
   const int64_t gq = s.Hq / s.Hkv;
-  const int64_t most_q = C.capacity > 0 && a.bt.T > s.B ? std::max<int64_t>(1, kCopyRows / gq) : a.max_q;
-  const int nt = a.listed ? 1 : tiles_of(s, most_q);
+  // What a call with long sequences leaves is likely to be single tokens.
+  const int nt = a.listed || C.capacity > 0 ? 1 : tiles_of(s, a.max_q);
   const int64_t blocks = (a.bt.T * gq + 8 * nt - 1) / (8 * nt) + s.B;   // row blocks of a KV head, at most
   while (blocks * s.Hkv * (((s.n_cap / kTile + 2) >> p.ush) + 1 + kItemCost) >= (int64_t(1) << 31)) ++p.ush;
   // Items of few tiles are not shared between blocks, which saves the merge.

@@ -436,8 +436,6 @@ __global__ void __launch_bounds__(kThreads, KV4_RB) kv4_read_kernel(const ReadAr
 }
 
 // ---- the bf16 copy that long sequences of a window call attend to
-constexpr int kPlanThreads = 1024;
-
 struct CopyArgs {
   Kv4Cache kv;
   Kv4Copy c;
@@ -449,31 +447,32 @@ struct CopyArgs {
   unsigned* err;
 };
 
-// Which sequences are copied, their pages and the copy's block table; one block.
-// Sequences take pages in their order as long as all of theirs are left.
-__global__ void __launch_bounds__(kPlanThreads) kv4_copy_plan_kernel(const CopyArgs a) {
-  __shared__ int32_t sums[32];
-  __shared__ int32_t taken;
+constexpr int kCopySeq = 2048;
+
+// Every block makes the plan for itself: which sequences are copied and their
+// first pages (sequences take pages in their order as long as all of theirs
+// are left); block 0 writes it down.  Then tiles of kReadTok tokens.
+__global__ void __launch_bounds__(kThreads, KV4_RB) kv4_copy_kernel(const CopyArgs a) {
+  __shared__ int64_t row0[kReadTok];
+  __shared__ int32_t first[kCopySeq + 1];
+  __shared__ int32_t sums[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
-  if (tid == 0) taken = 0;
-  __syncthreads();
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+  auto shape_of = [&](int b, int* drop) {   // tokens of the copy and those left out behind the sink; 0: not copied
+    const int64_t q0 = min(max(a.bt.cu_q ? __ldg(a.bt.cu_q + b) : static_cast<int64_t>(b), int64_t(0)), a.bt.T);
+    const int64_t q1 = min(max(a.bt.cu_q ? __ldg(a.bt.cu_q + b + 1) : static_cast<int64_t>(b) + 1, q0), a.bt.T);
+    const int64_t len = min(max(static_cast<int64_t>(__ldg(a.bt.lens + b)), int64_t(0)), a.n_cap);
+    if (((q1 - q0) << a.gsh) <= a.c.most_rows) return 0;
+    const int64_t lo = max(len - (q1 - q0) - a.local + 1, int64_t(0));   // the first row's window
+    *drop = static_cast<int>(max(lo - a.sink, int64_t(0)));
+    const int tokens = static_cast<int>(len) - *drop;
+    return tokens <= a.c.pages_per_seq * kCopyPage ? tokens : 0;   // (0: more new tokens than the call said)
+  };
+  int taken = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
     const int b = b0 + tid;
-    int pages = 0, len2 = 0, drop = 0;
-    if (b < a.B) {
-      const int64_t q0 = min(max(a.bt.cu_q ? __ldg(a.bt.cu_q + b) : static_cast<int64_t>(b), int64_t(0)), a.bt.T);
-      const int64_t q1 = min(max(a.bt.cu_q ? __ldg(a.bt.cu_q + b + 1) : static_cast<int64_t>(b) + 1, q0), a.bt.T);
-      const int64_t len = min(max(static_cast<int64_t>(__ldg(a.bt.lens + b)), int64_t(0)), a.n_cap);
-      if (((q1 - q0) << a.gsh) > a.c.most_rows && len > 0) {
-        const int64_t lo = max(len - (q1 - q0) - a.local + 1, int64_t(0));   // the first row's window
-        drop = static_cast<int>(max(lo - a.sink, int64_t(0)));
-        len2 = static_cast<int>(len) - drop;
-        pages = (len2 + kCopyPage - 1) / kCopyPage;
-        if (pages > a.c.pages_per_seq) pages = 0;   // more new tokens than the call said
-      }
-    }
-    // exclusive sums over the block; a sequence that does not fit takes none, and is asked again without it
+    int drop = 0;
+    const int tokens = b < a.B ? shape_of(b, &drop) : 0, pages = (tokens + kCopyPage - 1) / kCopyPage;
     int inc = pages;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -482,59 +481,48 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_copy_plan_kernel(const CopyA
     }
     if (lane == 31) sums[warp] = inc;
     __syncthreads();
-    int before = taken;
-    for (int w = 0; w < warp; ++w) before += sums[w];
-    int total = taken;
-    for (int w = 0; w < kPlanThreads / 32; ++w) total += sums[w];
-    const int first = before + inc - pages;
-    const bool fits = pages > 0 && first + pages <= a.c.capacity;
-    if (b < a.B) {
-      a.c.copied[b] = fits;
-      a.c.lens[b] = fits ? len2 : 0;
-      a.c.drop[b] = drop;
-      a.c.first[b] = static_cast<int>(min(static_cast<int64_t>(first), a.c.capacity));
+    int before = taken + inc - pages, total = taken;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
     }
-    __syncthreads();
-    if (tid == 0) taken = total;
+    if (b < a.B) {
+      first[b] = before;
+      if (blockIdx.x == 0) {
+        const bool fits = pages > 0 && before + pages <= a.c.capacity;
+        a.c.copied[b] = fits;
+        a.c.lens[b] = fits ? tokens : 0;
+      }
+    }
+    taken = total;
     __syncthreads();
   }
-  if (tid == 0) a.c.first[a.B] = static_cast<int>(min(static_cast<int64_t>(taken), a.c.capacity));
-  __syncthreads();
-  for (int b = 0; b < a.B; ++b) {
-    if (a.c.copied[b] == 0) continue;
-    const int pages = (a.c.lens[b] + kCopyPage - 1) / kCopyPage;
-    for (int i = tid; i < pages; i += kPlanThreads) a.c.table[b * a.c.pages_per_seq + i] = a.c.first[b] + i;
-  }
-  pdl_trigger();
-}
-
-// Tiles of kReadTok tokens of the copy's pages.
-__global__ void __launch_bounds__(kThreads, KV4_RB) kv4_copy_kernel(const CopyArgs a) {
-  __shared__ int64_t row0[kReadTok];
-  const int tid = threadIdx.x;
-  pdl_wait();
   const int64_t head_rows = a.pm.table ? (int64_t(1) << a.pm.page_shift) : a.n_cap;
   constexpr int kParts = kCopyPage / kReadTok;
-  const int tiles = __ldcg(a.c.first + a.B) * kParts;
+  const int tiles = static_cast<int>(min(static_cast<int64_t>(taken), a.c.capacity)) * kParts;
   for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
     const int page = i / kParts, part = i - page * kParts;
     int lo = 0, hi = a.B;   // the last sequence whose pages begin at or before this one: those of none stand before it
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldcg(a.c.first + mid) <= page) lo = mid;
+      if (first[mid] <= page) lo = mid;
       else hi = mid;
     }
-    const int len = __ldcg(a.c.lens + lo), at = (page - __ldcg(a.c.first + lo)) * kCopyPage + part * kReadTok;
+    int drop = 0;
+    const int tokens = shape_of(lo, &drop), pages = (tokens + kCopyPage - 1) / kCopyPage;
+    if (first[lo] + pages > a.c.capacity) continue;   // the whole block: it has not got all of its pages
+    const int at = (page - first[lo]) * kCopyPage + part * kReadTok;
     __syncthreads();
     if (tid < kReadTok) {
       int64_t row = -2;   // behind the last token: not written
-      if (at + tid < len) {
-        const int t = at + tid < a.sink ? at + tid : at + tid + __ldcg(a.c.drop + lo);
+      if (at + tid < tokens) {
+        const int t = at + tid < a.sink ? at + tid : at + tid + drop;
         row = cache_row(a.pm, lo, 0, a.Hkv, a.n_cap, t);
         if (row < 0) record_error(a.err, kErrBadPage);   // rows of zeros
       }
       row0[tid] = row;
     }
+    if (part == 0 && tid == 0) a.c.table[lo * a.c.pages_per_seq + page - first[lo]] = page;
     __syncthreads();
     const int64_t to = (static_cast<int64_t>(page) * a.Hkv * kCopyPage + part * kReadTok) * kD;
     read_rows(a.kv, a.Hkv, row0, head_rows, a.c.K + to, kD, static_cast<int64_t>(kCopyPage) * kD, a.c.V + to, kD,
@@ -615,8 +603,6 @@ cudaError_t launch_kv4_copy(const qasc_shape& s, const PageMap& pm, const Batch&
   a.local = local;
   a.n_cap = s.n_cap;
   a.err = dev.err_word;
-  const cudaError_t e = launch_dependent(kv4_copy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, 1, a);
-  if (e != cudaSuccess) return e;
   const int64_t tiles = c.capacity * (kCopyPage / kReadTok), most = static_cast<int64_t>(dev.num_sms) * 8;
   return launch_dependent(kv4_copy_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads), 0, stream,
                           1, a);
