@@ -80,6 +80,7 @@ constexpr float kScale = 1.4426950408889634f * 0.08838834764831845f;
 struct Args {
   Kv4AttnArgs a;
   int B, Hq, Hkv, gsh;      // gsh = log2(Hq / Hkv)
+  int seqs;                 // sequences of the line: B, or (listed) the KV heads of all
   int64_t n_cap;
   int n, sink_end, local_start;   // listed: tokens of every sequence, its regions
   const int32_t* copied;    // [B] not 0: a sequence that is left out here (NULL: none)
@@ -142,8 +143,8 @@ __device__ __forceinline__ int clampi(int64_t v, int64_t lo, int64_t hi) {
 template <bool kList>
 __device__ __forceinline__ Seq seq_of(const Args& p, int b) {
   Seq r;
-  if (kList) {
-    r.q0 = b;
+  if (kList) {   // (the line's sequences are KV heads of sequences here, each with a list)
+    r.q0 = b / p.Hkv;
     r.ql = 1;
     r.len = p.n;
     return r;
@@ -167,8 +168,9 @@ __device__ __forceinline__ int list_len(const Args& p, int b, int g) {
 
 // Items of a sequence (row blocks times KV heads) and the places of each: the
 // most tiles that any of them has (whole items: one).
-template <int kRows>
+template <bool kList, int kRows>
 __device__ __forceinline__ int items_of(const Args& p, const Seq& s, int b) {
+  if (kList) return 1;
   const int64_t rows = static_cast<int64_t>(s.ql) << p.gsh;
   if (p.copied && __ldcg(p.copied + b)) return 0;
   return static_cast<int>((rows + kRows - 1) / kRows) * p.Hkv;
@@ -178,9 +180,7 @@ __device__ __forceinline__ int span_of(const Args& p, const Seq& s, int b) {
   if (p.whole) return 1;
   int tiles;
   if (kList) {
-    int most = 0;
-    for (int g = 0; g < (p.a.sel_per_kv ? p.Hkv : 1); ++g) most = max(most, list_len(p, b, g));
-    tiles = (p.sink_end + most + (p.n - p.local_start) + kTile - 1) / kTile;
+    tiles = (p.sink_end + list_len(p, b / p.Hkv, b % p.Hkv) + (p.n - p.local_start) + kTile - 1) / kTile;
   } else {
     // the sink's tiles, the window's, and one more where it begins inside a tile
     const int window = (p.a.local + min(s.ql, kRows >> p.gsh) - 1 + 2 * (kTile - 1)) / kTile;
@@ -192,14 +192,16 @@ __device__ __forceinline__ int span_of(const Args& p, const Seq& s, int b) {
 // A line of U places over G blocks: block c has the places [c U / G, (c + 1) U / G),
 // in 32 bits (64-bit divisions at a block's start cost it 2 us).
 struct Line {
-  unsigned U, G, q, r;
+  unsigned U, G, q, r, inv;   // inv = ceil(2^32 / G): n inv / 2^32 is n / G for n < 2^16
   __device__ __forceinline__ Line(int places, int grid) {
     U = places;
     G = grid;
-    q = U / G;
+    inv = 0xffffffffu / G + 1;
+    q = G == 1 ? U : __umulhi(U, inv);   // n / G or one above for any n < 2^31
+    if (q * G > U) --q;
     r = U - q * G;
   }
-  __device__ __forceinline__ int start(unsigned c) const { return static_cast<int>(c * q + c * r / G); }
+  __device__ __forceinline__ int start(unsigned c) const { return static_cast<int>(c * q + (G == 1 ? 0 : __umulhi(c * r, inv))); }
   // The block that holds place x.
   __device__ __forceinline__ int block(int x) const {
     int c = min(static_cast<int>(__fdividef(static_cast<float>(x) * static_cast<float>(G), static_cast<float>(U))), static_cast<int>(G) - 1);
@@ -223,17 +225,19 @@ struct Smem {
   int place[kSums + 1];          // places before a group of sequences
 };
 
+// (64 bytes are fetched into L2, not the default 128: of scattered rows the rest would be
+// read for nothing, 215 MB where 95 are listed: four 128K contexts at 20 %, 48 against 40 us.)
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {   // the rest zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.ca.shared.global.L2::64B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.ca.shared.global.L2::64B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -302,7 +306,7 @@ __device__ __forceinline__ int token_of_slot(const Args& p, const Piece& pc, int
 // The item that holds place x.
 template <bool kList, int kRows>
 __device__ __forceinline__ Walk walk_at(const Args& p, const int* place, int x) {
-  int lo = 0, hi = (p.B + (1 << p.ssh) - 1) >> p.ssh;   // the last group with place <= x
+  int lo = 0, hi = (p.seqs + (1 << p.ssh) - 1) >> p.ssh;   // the last group with place <= x
   if (hi == 1) hi = 0;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -313,7 +317,7 @@ __device__ __forceinline__ Walk walk_at(const Args& p, const int* place, int x) 
   int at = hi == 0 ? 0 : place[lo];
   for (w.b = lo << p.ssh;; ++w.b) {
     w.s = seq_of<kList>(p, w.b);
-    w.items = items_of<kRows>(p, w.s, w.b);
+    w.items = items_of<kList, kRows>(p, w.s, w.b);
     if (w.items == 0) continue;
     w.span = span_of<kList, kRows>(p, w.s, w.b);
     const int all = w.items * w.span;
@@ -325,15 +329,15 @@ __device__ __forceinline__ Walk walk_at(const Args& p, const int* place, int x) 
   return w;
 }
 
-// The next item (w.b == p.B behind the last).
+// The next item (w.b == p.seqs behind the last).
 template <bool kList, int kRows>
 __device__ __forceinline__ void walk_on(const Args& p, Walk& w) {
   w.x0 += w.span;
   if (++w.rem < w.items) return;
   w.rem = 0;
-  while (++w.b < p.B) {
+  while (++w.b < p.seqs) {
     w.s = seq_of<kList>(p, w.b);
-    w.items = items_of<kRows>(p, w.s, w.b);
+    w.items = items_of<kList, kRows>(p, w.s, w.b);
     if (w.items == 0) continue;
     w.span = span_of<kList, kRows>(p, w.s, w.b);
     return;
@@ -344,11 +348,11 @@ __device__ __forceinline__ void walk_on(const Args& p, Walk& w) {
 template <bool kList, int kRows>
 __device__ __forceinline__ Piece piece_of(const Args& p, const Walk& w) {
   Piece pc;
-  const unsigned blocks = static_cast<unsigned>(w.items) / static_cast<unsigned>(p.Hkv);
-  pc.b = w.b;
-  pc.g = blocks == 1 ? w.rem : static_cast<int>(static_cast<unsigned>(w.rem) / blocks);
+  const unsigned blocks = kList || w.items == p.Hkv ? 1 : static_cast<unsigned>(w.items) / static_cast<unsigned>(p.Hkv);
+  pc.b = kList ? w.s.q0 : w.b;
+  pc.g = kList ? w.b - w.s.q0 * p.Hkv : (blocks == 1 ? w.rem : static_cast<int>(static_cast<unsigned>(w.rem) / blocks));
   pc.x0 = w.x0;
-  const int r0 = (w.rem - pc.g * static_cast<int>(blocks)) * kRows;
+  const int r0 = kList ? 0 : (w.rem - pc.g * static_cast<int>(blocks)) * kRows;
   pc.rows = static_cast<int>(min(static_cast<int64_t>(kRows), (static_cast<int64_t>(w.s.ql) << p.gsh) - r0));
   pc.tok0 = w.s.q0 + (r0 >> p.gsh);
   pc.p0 = w.s.len - w.s.ql + (r0 >> p.gsh);
@@ -393,7 +397,7 @@ __device__ __noinline__ int next_piece(const Args& p, Smem<kNT>& S, int warp, Pi
   const int lane = threadIdx.x & 31;
   Walk walk = S.walk[warp];
   bool found = false;
-  auto more = [&]() { return p.whole ? walk.left > 0 : walk.b < p.B && walk.x0 < walk.end; };
+  auto more = [&]() { return p.whole ? walk.left > 0 : walk.b < p.seqs && walk.x0 < walk.end; };
   __syncwarp();
   while (!found && more()) {
     const Piece pc = piece_of<kList, kRows>(p, walk);
@@ -406,6 +410,13 @@ __device__ __noinline__ int next_piece(const Args& p, Smem<kNT>& S, int warp, Pi
     }
     found = pc.n > 0;
     if (found && lane == 0) to = pc;
+    if (kList && found) {
+      // the list's next entries and the sequence's pages, all of which come one behind the other otherwise
+      const int64_t list = (p.a.sel_per_kv ? static_cast<int64_t>(pc.b) * p.Hkv + pc.g : pc.b) * p.a.K;
+      const int e = max(kTile * pc.t0 - pc.head, 0) + kTile * lane;
+      if (lane < 8 && e < pc.lo) prefetch_l2(p.a.sel + list + e);
+      if (p.a.pm.table && kTile * lane < p.a.pm.pages_per_seq) prefetch_l2(p.a.pm.table + pc.base + kTile * lane);
+    }
     --walk.left;
     if (!p.whole || walk.left > 0) walk_on<kList, kRows>(p, walk);
   }
@@ -425,7 +436,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
   pdl_wait();
 
   // ---- this warp's part of the work.  Whole items of single tokens need no sums.
-  const int groups = (p.B + (1 << p.ssh) - 1) >> p.ssh;
+  const int groups = (p.seqs + (1 << p.ssh) - 1) >> p.ssh;
   const bool plain = p.whole && (kList || p.a.bt.cu_q == nullptr);
   if (tid < 2 * kWarps) S.there[tid] = 0;
   if (!kList && blockIdx.x == gridDim.x - 1)
@@ -437,9 +448,9 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
   if (!plain) {
     for (int i = tid; i < groups; i += kThreads) {
       int sum = 0;
-      for (int b = i << p.ssh; b < min(p.B, (i + 1) << p.ssh); ++b) {
+      for (int b = i << p.ssh; b < min(p.seqs, (i + 1) << p.ssh); ++b) {
         const Seq s = seq_of<kList>(p, b);
-        const int items = items_of<kRows>(p, s, b);
+        const int items = items_of<kList, kRows>(p, s, b);
         if (items > 0) sum += items * span_of<kList, kRows>(p, s, b);
       }
       S.place[i] = sum;
@@ -452,7 +463,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
           const int b = b0 + lane;
           const int v = b < groups ? S.place[b] : 0;
           int vi = v;
-#pragma unroll
+#pragma unroll 1
           for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, vi, o);
             if (lane >= o) vi += x;
@@ -468,7 +479,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
   }
   const Line line(places, max(1, min(static_cast<int>(gridDim.x), p.whole ? places : (places + kLeast - 1) / kLeast)));
   Walk walk;
-  walk.b = p.B;
+  walk.b = p.seqs;
   walk.x0 = walk.end = walk.start = walk.left = 0;
   if (blockIdx.x < line.G && places > 0) {
     const unsigned first = line.start(blockIdx.x), all = line.start(blockIdx.x + 1) - first;
@@ -485,10 +496,10 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
       }
       if (left > 0) {
         if (plain) {
-          walk.b = (first + item) / p.Hkv;
-          walk.rem = first + item - walk.b * p.Hkv;
+          walk.b = kList ? first + item : (first + item) / p.Hkv;
+          walk.rem = kList ? 0 : first + item - walk.b * p.Hkv;
           walk.s = seq_of<kList>(p, walk.b);
-          walk.items = p.Hkv;
+          walk.items = kList ? 1 : p.Hkv;
           walk.span = 1;
         } else {
           walk = walk_at<kList, kRows>(p, S.place, first + item);
@@ -872,60 +883,65 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
   }
 
   // ---- the warps' parts joined: a chain begins with an item's first part, or with
-  // the block's first one where the item began before; parts of earlier items of a
-  // warp (even places) continue it until one ends.  A warp joins a row; lane k has
-  // part k's maximum and sum.
+  // the block's first one where the item began before; the firsts of the warps behind it
+  // (even places) continue it until one ends.  A thread joins four channels of a row.
+  // (With a warp to a row, or a warp finding a row's factors first, this took 6000
+  // cycles behind the last product, 5 % of 64 sequences with a 4K window.)
   __syncthreads();
   const int state = lane < 2 * kWarps ? S.there[lane] : 0;
   const unsigned present = __ballot_sync(0xffffffffu, state != 0), ended = __ballot_sync(0xffffffffu, state == 2);
   constexpr unsigned kFirsts = 0x55555555u;   // even places
-  const unsigned heads = present & (~kFirsts | (present & -present));
   bool left_over = false;   // an item goes on behind the block
-  for (unsigned todo = heads; todo != 0; todo &= todo - 1) {
-    const int i = __ffs(todo) - 1;
+  int x = tid;              // of the chains' rows, 32 fours of channels each, the next that is this thread's
+  for (unsigned heads = present & (~kFirsts | (present & -present)); heads != 0; heads &= heads - 1) {
+    const int i = __ffs(heads) - 1;
     const bool begins = (i & 1) != 0;
     // the even places behind i up to the first that ends (the one at i itself may)
-    const unsigned behind = present & kFirsts & ~((2u << i) - 1);
-    const unsigned stop = ((ended >> i) & 1) ? 0 : behind & ended;   // first of them
-    const unsigned reach = ((ended >> i) & 1) ? 0 : (stop ? behind & ((2u << (__ffs(stop) - 1)) - 1) : behind);
-    const unsigned chain = (1u << i) | reach;
+    unsigned chain = ((ended >> i) & 1) ? 0 : present & kFirsts & ~((2u << i) - 1);
+    const unsigned stop = chain & ended;
     const bool ends = ((ended >> i) & 1) || stop != 0;
+    if (stop) chain &= (stop & -stop) * 2u - 1;
     left_over |= begins && !ends;
+    const int w0 = (i >> 1) + 1, w1 = chain ? (31 - __clz(chain)) >> 1 : 0;   // warps of the others
+    const Part<kRows>& head = begins ? *reinterpret_cast<const Part<kRows>*>(S.ring[i >> 1]) : S.first[i >> 1];
     const Piece& pc = S.part[i];
-    const bool mine = (chain >> lane) & 1;
-    const Part<kRows>* own = (lane & 1) ? reinterpret_cast<const Part<kRows>*>(S.ring[lane >> 1]) : &S.first[lane >> 1];
-    for (int col = warp; col < pc.rows; col += kWarps) {
-      const float2 ml = mine ? own->ml[col] : make_float2(-INFINITY, 0.0f);
-      const float m = warp_max(ml.x);
-      const float f = mine ? (m == -INFINITY ? 1.0f : ex2_approx(ml.x - m)) : 0.0f;
-      float l = mine ? ml.y * f : 0.0f;
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int rows = pc.rows;
+#pragma unroll 1
+    for (; x < 32 * rows; x += kThreads) {
+      const int col = x >> 5, four = x & 31, at = four ^ (col >> 1 & 3);
+      float m = head.ml[col].x;
 #pragma unroll 4
-      for (unsigned rest = chain; rest != 0; rest &= rest - 1) {
-        const int k = __ffs(rest) - 1;
-        const Part<kRows>* from = (k & 1) ? reinterpret_cast<const Part<kRows>*>(S.ring[k >> 1]) : &S.first[k >> 1];
-        const float g = __shfl_sync(0xffffffffu, f, k);
-        const float4 y = from->o[col][lane ^ (col >> 1 & 3)];
-        o = make_float4(o.x + y.x * g, o.y + y.y * g, o.z + y.z * g, o.w + y.w * g);
-      }
+      for (int w = w0; w <= w1; ++w)
+        if ((chain >> 2 * w) & 1) m = fmaxf(m, S.first[w].ml[col].x);
+      float l = 0.0f;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      auto add = [&](const Part<kRows>& part) {
+        const float2 ml = part.ml[col];
+        const float4 y = part.o[col][at];
+        const float f = m == -INFINITY ? 1.0f : ex2_approx(ml.x - m);
+        l += ml.y * f;
+        o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
+      };
+      add(head);
+#pragma unroll 4
+      for (int w = w0; w <= w1; ++w)
+        if ((chain >> 2 * w) & 1) add(S.first[w]);
       if (begins && ends) {
-        const int64_t at = row_of(p, pc.tok0, pc.g, col);
+        const int64_t row = row_of(p, pc.tok0, pc.g, col);
         const float inv = inverse_of(p, l);
-        *reinterpret_cast<uint2*>(p.a.out + at * kD + 4 * lane) =
-            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (p.a.lse && lane == 0) p.a.lse[at] = lse_of(m, l);
+        *reinterpret_cast<uint2*>(p.a.out + row * kD + 4 * four) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        if (p.a.lse && four == 0) p.a.lse[row] = lse_of(m, l);
       } else {
         const int64_t to = (static_cast<int64_t>(blockIdx.x) * 2 + begins) * kRows + col;
-        *(reinterpret_cast<float4*>(p.part_o + to * kD) + lane) = o;
-        if (lane == 0) p.part_ml[to] = make_float2(m, l);
+        *(reinterpret_cast<float4*>(p.part_o + to * kD) + four) = o;
+        if (four == 0) p.part_ml[to] = make_float2(m, l);
       }
     }
-    if (tid == 0 && begins && !ends) {
+    x -= 32 * rows;
+    if (tid == kThreads - 1 && begins && !ends) {
       Share sh;
       sh.first = static_cast<int64_t>(pc.tok0) << p.gsh;
-      sh.rows = pc.rows;
+      sh.rows = rows;
       sh.g = pc.g;
       sh.last = line.block(pc.x0 + kItemCost + ((pc.tiles - 1) >> p.ush));
       sh.pad = 0;
@@ -1061,7 +1077,8 @@ int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, cons
     p.sink_end = static_cast<int>(R.sink_end);
     p.local_start = static_cast<int>(R.local_start);
   }
-  while ((s.B - 1) >> p.ssh >= kSums) ++p.ssh;
+  p.seqs = a.listed ? s.B * s.Hkv : s.B;
+  while ((p.seqs - 1) >> p.ssh >= kSums) ++p.ssh;
   p.err = dev.err_word;
 
   const CopyLayout C = a.listed ? CopyLayout() : copy_layout(s, a.bt.T, a.max_q, a.sink, a.local);

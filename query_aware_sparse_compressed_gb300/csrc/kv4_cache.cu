@@ -347,7 +347,7 @@ constexpr int kReadTok = 32;     // tokens of a read block's tile
 constexpr int kRowLanes = 16;    // threads of a row: 8 values each
 constexpr int kReadRows = kThreads / kRowLanes;   // rows of a pass
 #ifndef KV4_RB
-#define KV4_RB 4
+#define KV4_RB 6
 #define KV4_RF 4
 #endif
 constexpr int kReadBatch = KV4_RF;    // rows whose loads a thread has in flight
