@@ -389,10 +389,9 @@ __device__ __forceinline__ Piece piece_of(const Args& p, const Walk& w) {
 }
 
 // Puts the next item of a warp's range into `to`: 0 where there is none, 1 for the
-// last, else 2.  Items without a token are written on the way.  (A call of its own: what runs once an
-// item would stand in the loop over its tiles otherwise, whose code is long as it is.)
+// last, else 2.  Items without a token are written on the way.
 template <int kNT, bool kList>
-__device__ __noinline__ int next_piece(const Args& p, Smem<kNT>& S, int warp, Piece& to) {
+__device__ __forceinline__ int next_piece(const Args& p, Smem<kNT>& S, int warp, Piece& to) {
   constexpr int kRows = 8 * kNT;
   const int lane = threadIdx.x & 31;
   Walk walk = S.walk[warp];
