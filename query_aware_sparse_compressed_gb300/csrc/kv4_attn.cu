@@ -414,7 +414,8 @@ __device__ __forceinline__ int next_piece(const Args& p, Smem<kNT>& S, int warp,
       const int64_t list = (p.a.sel_per_kv ? static_cast<int64_t>(pc.b) * p.Hkv + pc.g : pc.b) * p.a.K;
       const int e = max(kTile * pc.t0 - pc.head, 0) + kTile * lane;
       if (lane < 8 && e < pc.lo) prefetch_l2(p.a.sel + list + e);
-      if (p.a.pm.table && kTile * lane < p.a.pm.pages_per_seq) prefetch_l2(p.a.pm.table + pc.base + kTile * lane);
+      if (p.a.pm.table && kTile * lane < p.a.pm.pages_per_seq)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.a.pm.table + pc.base + kTile * lane) : "memory");
     }
     --walk.left;
     if (!p.whole || walk.left > 0) walk_on<kList, kRows>(p, walk);
