@@ -193,7 +193,7 @@ const DeviceInfo* device_info() {
     if (configure_score_kernels(d) != cudaSuccess || configure_select_kernels(d) != cudaSuccess ||
         configure_head_select_kernels(d) != cudaSuccess || configure_group_kernels(d) != cudaSuccess ||
         configure_expand_kernels(d) != cudaSuccess || configure_kv_attn_kernels(d) != cudaSuccess ||
-        configure_kv4_kernels(d) != cudaSuccess ||
+        configure_kv4_kernels(d) != cudaSuccess || configure_kv4_cache_kernels(d) != cudaSuccess ||
         configure_attn_kernels(d) != cudaSuccess || configure_snapkv_kernels(d) != cudaSuccess)
       return nullptr;
     ready[dev] = true;

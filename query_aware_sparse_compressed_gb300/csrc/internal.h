@@ -361,6 +361,7 @@ size_t kv4_window_workspace_bytes(const qasc_shape& s, int64_t T, int64_t max_q,
 // The workspace has the size above (kv4_attn_least_bytes() of a listed call).
 int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t configure_kv4_kernels(const DeviceInfo& dev);
+cudaError_t configure_kv4_cache_kernels(const DeviceInfo& dev);
 
 // Neighbour expansion: rows of K ascending candidates in, the ascending union
 // of their +-radius neighbourhoods within C out ([rows][cap], the first

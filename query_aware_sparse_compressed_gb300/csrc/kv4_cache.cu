@@ -29,7 +29,11 @@ constexpr int kThreads = 256;
 constexpr int kMaxTok = 4;       // tokens of an append block's tile
 constexpr int kFreqs = kD / 2;
 constexpr int kUnits = 8;        // threads of a head: 16 values each
-constexpr int kBatch = 2;        // heads whose loads a thread has in flight
+#ifndef KV4_RING
+#define KV4_RING 4
+#endif
+constexpr int kRing = KV4_RING;         // units that a thread's copies are ahead
+constexpr size_t kRingBytes = static_cast<size_t>(kThreads) * kRing * 32;
 constexpr int kPoints = 256;     // of a quarter turn
 
 struct Points {
@@ -111,17 +115,23 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t ang, Pair& c, Pair& s) {
   s = add_low(two_sum(S.h, ps), S.l + (es + (C.h * sl + (C.l * rh - S.h * v))));
 }
 
-// a c + b s (or minus) rounded once to bf16, bits.  Where the high part stands
-// on the middle between two bf16 values, the low part decides.
-__device__ __forceinline__ uint32_t rotated_bf16(float a, Pair c, float b, Pair s) {
-  const float p1 = __fmul_rn(a, c.h), e1 = fmaf(a, c.h, -p1);
-  const float p2 = __fmul_rn(b, s.h), e2 = fmaf(b, s.h, -p2);
+// p1 + p2 + low to 2^-40 of p1 and p2, as what rounds to its bf16 value: where the sum
+// in fp32 stands on the middle between two bf16 values the rest decides.
+__device__ __forceinline__ float sum_for_bf16(float p1, float p2, float low) {
   const Pair t = two_sum(p1, p2);
-  const Pair y = add_low(t, (e1 + e2) + (a * c.l + b * s.l));
-  uint32_t u = __float_as_uint(y.h);
-  if ((u & 0xffffu) == 0x8000u && y.l != 0.0f) u += (y.l > 0.0f) == !(u >> 31) ? 1u : 0xffffffffu;
-  if (!(fabsf(y.h) <= 3.402823466e38f)) u = __float_as_uint(t.h);   // infinities and NaN
-  return static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(u))));
+  const float l = __fadd_rn(t.l, low), h = __fadd_rn(t.h, l), rest = __fadd_rn(l, -__fadd_rn(h, -t.h));
+  int u = __float_as_int(h);
+  const int away = ((u ^ __float_as_int(rest)) >> 31) | 1;   // 1: the rest has the sum's sign
+  if ((u & 0xffff) == 0x8000 && rest != 0.0f) u += away;
+  return t.l == t.l ? __int_as_float(u) : t.h;   // (an infinity leaves no exact rest)
+}
+
+// The pair (a, b) rotated.  c and s are the high parts, of 16 bits, so that their
+// products with a bf16 value are exact in fp32, cl and sl the rest.
+__device__ __forceinline__ void rotate_exactly(float& a, float& b, float c, float s, float cl, float sl) {
+  const float x = sum_for_bf16(__fmul_rn(a, c), -__fmul_rn(b, s), fmaf(a, cl, -__fmul_rn(b, sl)));
+  b = sum_for_bf16(__fmul_rn(b, c), __fmul_rn(a, s), fmaf(b, cl, __fmul_rn(a, sl)));
+  a = x;
 }
 
 struct AppendArgs {
@@ -152,6 +162,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ uint32_t abs_max(const uint4& x) {
   const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
   return max(m & 0xffffu, m >> 16);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Codes of eight values, `f` what turns them into quotients.
@@ -202,10 +221,9 @@ __device__ __forceinline__ void store_quantised(const uint4& x, const uint4& y, 
 #define KV4_AB 3
 #endif
 __global__ void __launch_bounds__(kThreads, KV4_AB) kv4_append_kernel(const AppendArgs a) {
-  __shared__ __align__(16) float turn[4][kMaxTok][kFreqs];   // cos, sin, and their low parts
-  __shared__ int64_t row0[kMaxTok];     // cache row of KV head 0, -1: not written
-  __shared__ int32_t rpos[kMaxTok];     // position that rotates
-  __shared__ int8_t live[kMaxTok];      // the token belongs to a sequence
+  // of this tile and the next one, which is prepared ahead: one barrier a tile
+  __shared__ __align__(16) float turns_of[2][4][kMaxTok][kFreqs];   // cos, sin (16 bits) and their rests
+  __shared__ int64_t rows_of[2][kMaxTok];    // cache row of KV head 0; -1: not written, -2: a token of no sequence
   const int tid = threadIdx.x;
   const int freq = tid & (kFreqs - 1), half = a.rot >> 1;
   pdl_wait();
@@ -226,119 +244,186 @@ __global__ void __launch_bounds__(kThreads, KV4_AB) kv4_append_kernel(const Appe
   const int64_t head_rows = a.pm.table ? (int64_t(1) << a.pm.page_shift) : a.n_cap;   // rows from head to head
   const int nq = a.q ? a.Hq : 0;
   const unsigned unit_mask = 0xffu << (tid & 24);
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tok; t0 < a.bt.T; t0 += static_cast<int64_t>(gridDim.x) * a.tok) {
-    const int n = static_cast<int>(min(static_cast<int64_t>(a.tok), a.bt.T - t0));
-    if (tid < n) {
-      const int64_t t = t0 + tid;
-      TokenAt at = token_of(a.bt, t);
-      live[tid] = at.b >= 0;
-      int64_t row = -1;
+  // A thread has the angle of one frequency of a token.
+  auto prepare = [&](int64_t t0, int buf) {
+    const int tk = tid / kFreqs;   // kThreads / kFreqs = kMaxTok
+    if (tk >= a.tok || t0 + tk >= a.bt.T) return;
+    const int64_t t = t0 + tk;
+    const TokenAt at = token_of(a.bt, t);
+    if (freq == 0) {
+      int64_t row = -2;
       if (at.b >= 0) {
+        row = -1;
         if (at.pos >= 0 && at.pos < a.n_cap) row = cache_row(a.pm, at.b, 0, a.Hkv, a.n_cap, at.pos);
         if (row < 0) record_error(a.err, kErrBadPage);
       }
-      row0[tid] = row;
-      rpos[tid] = a.positions ? __ldg(a.positions + t) : static_cast<int32_t>(at.pos);
+      rows_of[buf][tk] = row;
     }
-    __syncthreads();
-    for (int i = tid; i < n * kFreqs; i += kThreads) {   // i mod 64 = freq: the block is a multiple of 64
-      const int tk = i / kFreqs;
+    if (freq < half) {
+      const int32_t pos = a.positions ? __ldg(a.positions + t) : static_cast<int32_t>(at.pos);
       Pair c, s;
-      turn_cos_sin(F * static_cast<uint64_t>(static_cast<int64_t>(rpos[tk])), c, s);
-      turn[0][tk][freq] = c.h;
-      turn[1][tk][freq] = s.h;
-      turn[2][tk][freq] = c.l;
-      turn[3][tk][freq] = s.l;
+      turn_cos_sin(F * static_cast<uint64_t>(static_cast<int64_t>(pos)), c, s);
+      const float ch = __uint_as_float(__float_as_uint(c.h) & 0xffffff00u), sh = __uint_as_float(__float_as_uint(s.h) & 0xffffff00u);
+      turns_of[buf][0][tk][freq] = ch;
+      turns_of[buf][1][tk][freq] = sh;
+      turns_of[buf][2][tk][freq] = __fadd_rn(__fadd_rn(c.h, -ch), c.l);
+      turns_of[buf][3][tk][freq] = __fadd_rn(__fadd_rn(s.h, -sh), s.l);
     }
-    __syncthreads();
-    const int u = tid & (kUnits - 1), tk = (tid / kUnits) & (a.tok - 1), slice = tid / (kUnits * a.tok);
-    const int step = kThreads / (kUnits * a.tok);
-    if (tk < n && live[tk]) {
-      const int64_t t = t0 + tk, row = row0[tk];
-      const int r16 = a.rot / 16;
-      const bool turns = u < r16;
-      // chunks of the unit in a rotated head and in a copied one
-      const int c0 = turns && !a.interleaved ? u : 2 * u, c1 = turns && !a.interleaved ? u + r16 : 2 * u + 1;
-      float cs[8], sn[8];
+  };
+  // A thread's units: of every tile its slice's heads of queries, then of keys and
+  // values in turn, two 16-byte chunks of each.  They are copied into a ring of its own
+  // ahead of their use, from tile to tile, whatever the unit at hand costs.
+  const int u = tid & (kUnits - 1), tk = (tid / kUnits) & (a.tok - 1), slice = tid / (kUnits * a.tok);
+  const int step = kThreads / (kUnits * a.tok);
+  const int q_units = (nq + step - 1) / step, units = q_units + 2 * ((a.Hkv + step - 1) / step);
+  const int r16 = a.rot / 16;
+  const bool turns = u < r16;
+  // chunks of the unit in a rotated head and in a copied one
+  const int c0 = turns && !a.interleaved ? u : 2 * u, c1 = turns && !a.interleaved ? u + r16 : 2 * u + 1;
+  // the lane, and which of its chunks, that holds chunk c of a rotated head
+  auto holder = [&](int c) {
+    const bool pairs = a.interleaved || c >= 2 * r16;
+    return Halves{(tid & 24) + (pairs ? c >> 1 : (c < r16 ? c : c - r16)), pairs ? (c & 1) != 0 : c >= r16};
+  };
+  const Halves px = holder(c0 ^ 1), py = holder(c1 ^ 1);
+  const int64_t t_step = static_cast<int64_t>(gridDim.x) * a.tok;
+  extern __shared__ __align__(16) uint4 ring_of[];
+  uint4* const ring = ring_of + (tid / 32) * (kRing * 64) + (tid & 31);
+  // the next unit to copy: its token's rows, the unit
+  int64_t load_t = static_cast<int64_t>(blockIdx.x) * a.tok + tk;
+  const int head0 = slice * kD;
+  const uint16_t *load_q = a.q + load_t * a.qs + head0 + 8 * c0, *load_k = a.k + load_t * a.ks + head0 + 8 * c0,
+                 *load_v = a.v + load_t * a.vs + head0 + 16 * u;
+  const int apart = 8 * (c1 - c0);   // values from chunk to chunk
+  const uint32_t ring_s = smem_u32(ring);
+  int unit = 0, load_place = 0, place = 0;
+  auto load = [&]() {
+    const uint32_t to = ring_s + load_place * 1024;
+    if (load_t < a.bt.T) {
+      if (unit < q_units) {
+        if (slice + unit * step < nq) {
+          const uint16_t* src = load_q + unit * step * kD;
+          cp_async16(to, src);
+          cp_async16(to + 512, src + apart);
+        }
+      } else {
+        const int i = unit - q_units, h = (i >> 1) * step;
+        if (slice + h < a.Hkv) {
+          const uint16_t* src = ((i & 1) ? load_v : load_k) + h * kD;
+          cp_async16(to, src);
+          cp_async16(to + 512, src + ((i & 1) ? 8 : apart));
+        }
+      }
+      if (++unit == units) {
+        unit = 0;
+        load_t += t_step;
+        load_q += t_step * a.qs;
+        load_k += t_step * a.ks;
+        load_v += t_step * a.vs;
+      }
+    }
+    cp_async_commit();
+    load_place = load_place + 1 == kRing ? 0 : load_place + 1;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kRing; ++i) load();
+  int buf = 0;
+  prepare(static_cast<int64_t>(blockIdx.x) * a.tok, 0);
+  __syncthreads();
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tok; t0 < a.bt.T; t0 += t_step, buf ^= 1) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(a.tok), a.bt.T - t0));
+    if (t0 + t_step < a.bt.T) prepare(t0 + t_step, buf ^ 1);
+    const float (&turn)[4][kMaxTok][kFreqs] = turns_of[buf];
+    const int64_t* row0 = rows_of[buf];
+    const int64_t t = t0 + tk, row = tk < n ? row0[tk] : -2;
+    // the unit just arrived, and its place for the one after the next kRing - 1
+    auto take = [&](uint4& x, uint4& y) {
+      cp_async_wait<kRing - 1>();
+      const uint4* from = ring + place * 64;   // what this lane has copied itself
+      x = from[0];
+      y = from[32];
+      load();
+      place = place + 1 == kRing ? 0 : place + 1;
+    };
+    auto angles = [&](int i, float (&v)[8]) {
+      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(&turn[i][tk][8 * u]);
+      *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(&turn[i][tk][8 * u + 4]);
+    };
+    if (nq > 0) {
+      float cs[8], sn[8], cl[8], sl[8];
+      angles(0, cs);
+      angles(1, sn);
+      angles(2, cl);
+      angles(3, sl);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        cs[i] = turns ? turn[0][tk][8 * u + i] : 1.0f;
-        sn[i] = turns ? turn[1][tk][8 * u + i] : 0.0f;
+        cs[i] += cl[i];
+        sn[i] += sl[i];
       }
-      for (int h0 = slice; h0 < nq; h0 += kBatch * step) {
-        uint4 x[kBatch], y[kBatch];
+      uint16_t* dst = a.q_out + (t * a.Hq + slice) * kD + 8 * c0;
+#pragma unroll 1
+      for (int h = slice; h < q_units * step + slice; h += step, dst += step * kD) {
+        uint4 x, y;
+        take(x, y);
+        if (h >= nq || row == -2) continue;
+        uint32_t* xa = &x.x;
+        uint32_t* ya = &y.x;
+        if (turns) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int h = h0 + i * step;
-          if (h < nq) {
-            const uint16_t* src = a.q + t * a.qs + h * kD;
-            x[i] = *reinterpret_cast<const uint4*>(src + 8 * c0);
-            y[i] = *reinterpret_cast<const uint4*>(src + 8 * c1);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int h = h0 + i * step;
-          if (h >= nq) continue;
-          uint32_t* xa = &x[i].x;
-          uint32_t* ya = &y[i].x;
-          if (turns) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = bf2_to_f2(xa[e]), g = bf2_to_f2(ya[e]);
-              if (a.interleaved) {
-                xa[e] = pack_bf16(f.x * cs[e] - f.y * sn[e], f.y * cs[e] + f.x * sn[e]);
-                ya[e] = pack_bf16(g.x * cs[4 + e] - g.y * sn[4 + e], g.y * cs[4 + e] + g.x * sn[4 + e]);
-              } else {
-                xa[e] = pack_bf16(f.x * cs[2 * e] - g.x * sn[2 * e], f.y * cs[2 * e + 1] - g.y * sn[2 * e + 1]);
-                ya[e] = pack_bf16(g.x * cs[2 * e] + f.x * sn[2 * e], g.y * cs[2 * e + 1] + f.y * sn[2 * e + 1]);
-              }
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = bf2_to_f2(xa[e]), g = bf2_to_f2(ya[e]);
+            if (a.interleaved) {
+              xa[e] = pack_bf16(f.x * cs[e] - f.y * sn[e], f.y * cs[e] + f.x * sn[e]);
+              ya[e] = pack_bf16(g.x * cs[4 + e] - g.y * sn[4 + e], g.y * cs[4 + e] + g.x * sn[4 + e]);
+            } else {
+              xa[e] = pack_bf16(f.x * cs[2 * e] - g.x * sn[2 * e], f.y * cs[2 * e + 1] - g.y * sn[2 * e + 1]);
+              ya[e] = pack_bf16(g.x * cs[2 * e] + f.x * sn[2 * e], g.y * cs[2 * e + 1] + f.y * sn[2 * e + 1]);
             }
           }
-          uint16_t* dst = a.q_out + (t * a.Hq + h) * kD;
-          *reinterpret_cast<uint4*>(dst + 8 * c0) = x[i];
-          *reinterpret_cast<uint4*>(dst + 8 * c1) = y[i];
         }
+        *reinterpret_cast<uint4*>(dst) = x;
+        *reinterpret_cast<uint4*>(dst + apart) = y;
       }
-      // the lane, and which of its chunks, that holds chunk c of a rotated head
-      auto holder = [&](int c) {
-        const bool pairs = a.interleaved || c >= 2 * r16;
-        return Halves{(tid & 24) + (pairs ? c >> 1 : (c < r16 ? c : c - r16)), pairs ? (c & 1) != 0 : c >= r16};
-      };
-      const Halves px = holder(c0 ^ 1), py = holder(c1 ^ 1);
-      if (row >= 0)
-        for (int h = slice; h < a.Hkv; h += step) {
-          const uint16_t* ksrc = a.k + t * a.ks + h * kD;
-          const uint16_t* vsrc = a.v + t * a.vs + h * kD;
-          uint4 x = *reinterpret_cast<const uint4*>(ksrc + 8 * c0), y = *reinterpret_cast<const uint4*>(ksrc + 8 * c1);
-          const uint4 v0 = *reinterpret_cast<const uint4*>(vsrc + 16 * u), v1 = *reinterpret_cast<const uint4*>(vsrc + 16 * u + 8);
-          const int64_t r = row + h * head_rows;
-          store_quantised(v0, v1, 2 * u, 2 * u + 1, true, px, py, a.v_inv, a.kv.V + r * kKv4Codes, a.kv.V_sf + r * kKv4Groups,
-                          unit_mask, u == 0);
-          if (turns) {
-            uint32_t* xa = &x.x;
-            uint32_t* ya = &y.x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = bf2_to_f2(xa[e]), g = bf2_to_f2(ya[e]);
-              const int e0 = a.interleaved ? e : 2 * e, e1 = a.interleaved ? 4 + e : 2 * e + 1;
-              const Pair c{turn[0][tk][8 * u + e0], turn[2][tk][8 * u + e0]}, s{turn[1][tk][8 * u + e0], turn[3][tk][8 * u + e0]};
-              const Pair d{turn[0][tk][8 * u + e1], turn[2][tk][8 * u + e1]}, w{turn[1][tk][8 * u + e1], turn[3][tk][8 * u + e1]};
-              const Pair sm{-s.h, -s.l}, wm{-w.h, -w.l};
-              if (a.interleaved) {
-                xa[e] = rotated_bf16(f.x, c, f.y, sm) | rotated_bf16(f.y, c, f.x, s) << 16;
-                ya[e] = rotated_bf16(g.x, d, g.y, wm) | rotated_bf16(g.y, d, g.x, w) << 16;
-              } else {
-                xa[e] = rotated_bf16(f.x, c, g.x, sm) | rotated_bf16(f.y, d, g.y, wm) << 16;
-                ya[e] = rotated_bf16(g.x, c, f.x, s) | rotated_bf16(g.y, d, f.y, w) << 16;
-              }
-            }
-          }
-          store_quantised(x, y, c0, c1, a.interleaved != 0, px, py, a.k_inv, a.kv.K + r * kKv4Codes, a.kv.K_sf + r * kKv4Groups,
-                          unit_mask, u == 0);
-        }
     }
-    __syncthreads();   // the next tile rewrites the angles
+#pragma unroll 1
+    for (int k = q_units; k < units; k += 2) {
+      const int h = slice + ((k - q_units) >> 1) * step;
+      const bool mine = h < a.Hkv && row >= 0;
+      const int64_t r = row + h * head_rows;
+      uint4 x, y;
+      take(x, y);
+      if (mine) {
+        if (turns) {
+          float c[8], sx[8], cl[8], sl[8];
+          angles(0, c);
+          angles(1, sx);
+          angles(2, cl);
+          angles(3, sl);
+          uint32_t* xa = &x.x;
+          uint32_t* ya = &y.x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float2 f = bf2_to_f2(xa[e]), g = bf2_to_f2(ya[e]);
+            if (a.interleaved) {
+              rotate_exactly(f.x, f.y, c[e], sx[e], cl[e], sl[e]);
+              rotate_exactly(g.x, g.y, c[4 + e], sx[4 + e], cl[4 + e], sl[4 + e]);
+            } else {
+              rotate_exactly(f.x, g.x, c[2 * e], sx[2 * e], cl[2 * e], sl[2 * e]);
+              rotate_exactly(f.y, g.y, c[2 * e + 1], sx[2 * e + 1], cl[2 * e + 1], sl[2 * e + 1]);
+            }
+            xa[e] = pack_bf16(f.x, f.y);
+            ya[e] = pack_bf16(g.x, g.y);
+          }
+        }
+        store_quantised(x, y, c0, c1, a.interleaved != 0, px, py, a.k_inv, a.kv.K + r * kKv4Codes, a.kv.K_sf + r * kKv4Groups,
+                        unit_mask, u == 0);
+      }
+      take(x, y);
+      if (mine)
+        store_quantised(x, y, 2 * u, 2 * u + 1, true, px, py, a.v_inv, a.kv.V + r * kKv4Codes, a.kv.V_sf + r * kKv4Groups,
+                        unit_mask, u == 0);
+    }
+    __syncthreads();   // the next tile is ready, and this one's place free
   }
   pdl_trigger();
 }
@@ -563,8 +648,13 @@ cudaError_t launch_kv4_append(const qasc_shape& s, const PageMap& pm, const Batc
   a.tok = bt.T >= 4 * dev.num_sms ? kMaxTok : 1;
   const int64_t tiles = (bt.T + a.tok - 1) / a.tok;
   const int64_t most = static_cast<int64_t>(dev.num_sms) * 6;
-  return launch_dependent(kv4_append_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads), 0,
-                          stream, 1, a);
+  return launch_dependent(kv4_append_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads),
+                          kRingBytes, stream, 1, a);
+}
+
+cudaError_t configure_kv4_cache_kernels(const DeviceInfo& dev) {
+  (void)dev;
+  return cudaFuncSetAttribute(kv4_append_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingBytes));
 }
 
 cudaError_t launch_kv4_read(const qasc_shape& s, const PageMap& pm, const Batch& bt, const Kv4Cache& kv, uint16_t* K_out,
