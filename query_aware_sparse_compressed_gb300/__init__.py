@@ -27,7 +27,6 @@ Entry points keep the C names:
 """
 
 import ctypes
-import typing
 
 import torch
 
@@ -646,17 +645,24 @@ def kv_prefix_attn_paged(q, K_pool, V_pool, prefix_table, block_table, kv_lens, 
 
 
 # ---------------------------------------------------------- the 4-bit cache
-class KV4(typing.NamedTuple):
+class KV4:
     """A 4-bit cache: codes K, V [B, Hkv, n_cap, 64] uint8 and scales K_sf, V_sf
     [B, Hkv, n_cap, 8] float8_e4m3fn, or pools [num_pages, Hkv, P, ..] of them;
     value i of a row = factor * scale[i // 16] * code[i], the codes 4-bit floats,
-    k_scale and v_scale the factors of keys and values (powers of two)."""
-    K: torch.Tensor
-    K_sf: torch.Tensor
-    V: torch.Tensor
-    V_sf: torch.Tensor
-    k_scale: float = 1.0
-    v_scale: float = 1.0
+    k_scale and v_scale the factors of keys and values (powers of two).  A handle
+    that a program keeps with its cache: its tensors are checked once, at the first
+    call, and do not change."""
+    __slots__ = ("K", "K_sf", "V", "V_sf", "k_scale", "v_scale", "_checked")
+
+    def __init__(self, K, K_sf, V, V_sf, k_scale=1.0, v_scale=1.0):
+        for name, value in zip(KV4.__slots__, (K, K_sf, V, V_sf, float(k_scale), float(v_scale), None)):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a KV4 does not change; make another of its tensors")
+
+    def __iter__(self):
+        return iter((self.K, self.K_sf, self.V, self.V_sf, self.k_scale, self.v_scale))
 
 
 _E4M3 = torch.float8_e4m3fn
@@ -670,28 +676,38 @@ def alloc_kv4(rows, Hkv, tokens, device=None, k_scale=1.0, v_scale=1.0):
     return KV4(codes[0], scales[0].view(_E4M3), codes[1], scales[1].view(_E4M3), k_scale, v_scale)
 
 
+def _check4(kv):
+    """Checks a KV4's tensors: (device index, shape of K, addresses, descriptor)."""
+    if not isinstance(kv.K, _Tensor) or kv.K.dim() != 4 or kv.K.shape[3] != D // 2:
+        raise ValueError("kv.K must be a [B or num_pages, Hkv, tokens, %d] tensor" % (D // 2))
+    dev, shape = kv.K.get_device(), kv.K.shape
+    scales = shape[:3] + (D // 16,)
+    where = (_at(kv.K, "kv.K", _U8, shape, dev), _at(kv.K_sf, "kv.K_sf", _E4M3, scales, dev),
+             _at(kv.V, "kv.V", _U8, shape, dev), _at(kv.V_sf, "kv.V_sf", _E4M3, scales, dev))
+    checked = dev, tuple(shape), where, _lib.pack_kv4(*where, kv.k_scale, kv.v_scale)
+    object.__setattr__(kv, "_checked", checked)
+    return checked
+
+
 def _cache4(kv, block_table, B, Hkv, dev):
     """A KV4 [B, Hkv, n_cap, ..], or of pools under block_table [B, pages_per_seq]:
     (descriptor of the pool or None, n_cap, Hkv, descriptor of the cache)."""
-    if not isinstance(kv, KV4):
+    if type(kv) is not KV4:
         raise TypeError("kv must be a KV4")
-    if not isinstance(kv.K, _Tensor) or kv.K.dim() != 4:
-        raise ValueError("kv.K must be a [%s, Hkv, tokens, %d] tensor" % ("B" if block_table is None else "num_pages", D // 2))
-    rows, heads, tokens, _ = shape = kv.K.shape
-    if shape[3] != D // 2 or (Hkv is not None and heads != Hkv) or (block_table is None and rows != B):
+    checked = kv._checked
+    if checked is None or checked[2] != (kv.K.data_ptr(), kv.K_sf.data_ptr(), kv.V.data_ptr(), kv.V_sf.data_ptr()):
+        checked = _check4(kv)
+    rows, heads, tokens, _ = shape = checked[1]
+    if checked[0] != dev or (Hkv is not None and heads != Hkv) or (block_table is None and rows != B):
         _dims(kv.K, "kv.K", (B if block_table is None else None, Hkv, None, D // 2))
+        raise ValueError("kv is on cuda:%d, the call's other tensors on %s" % (checked[0], "cuda:%d" % dev if dev >= 0 else "the CPU"))
     if block_table is None:
-        cache, n_cap = None, tokens
-    else:
-        table = block_table.shape
-        if len(table) != 2 or table[0] != B:
-            _dims(block_table, "block_table", (B, None))
-        n_cap = table[1] * tokens
-        cache = _lib.pack_cache(_at(block_table, "block_table", _I32, table, dev), tokens, table[1], rows)
-    scales = (rows, heads, tokens, D // 16)
-    return cache, n_cap, heads, _lib.pack_kv4(
-        _at(kv.K, "kv.K", _U8, shape, dev), _at(kv.K_sf, "kv.K_sf", _E4M3, scales, dev),
-        _at(kv.V, "kv.V", _U8, shape, dev), _at(kv.V_sf, "kv.V_sf", _E4M3, scales, dev), kv.k_scale, kv.v_scale)
+        return None, tokens, heads, checked[3]
+    table = block_table.shape
+    if len(table) != 2 or table[0] != B:
+        _dims(block_table, "block_table", (B, None))
+    cache = _lib.pack_cache(_at(block_table, "block_table", _I32, table, dev), tokens, table[1], rows)
+    return cache, table[1] * tokens, heads, checked[3]
 
 
 def _rope_append4(name, q, k, v, q_out, kv, block_table, kv_lens, inv_freq, cu_q, positions, interleaved, stream):

@@ -306,8 +306,9 @@ def test_append_does_not_depend_on_the_cut():
             qasc.kv4_rope_append(None, k[lo:hi], v[lo:hi], None, kv, ln, f, cu_q=c)
         caches.append(kv)
     qasc.qasc_device_error()
-    for a, b in zip(caches[0][:4], caches[1][:4]):
-        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    for name in ("K", "K_sf", "V", "V_sf"):
+        a, b = (getattr(kv, name).view(torch.uint8) for kv in caches)
+        assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("bad", ["page", "position", "length"])
@@ -531,7 +532,7 @@ def test_window_equals_the_bf16_call_on_the_cache_read_back():
     c, ln = batch_tensors([0, 90, 91], lens)
     K, V = (torch.zeros((2, Hkv, n_cap, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
     for b, n in enumerate(lens):
-        one = qasc.KV4(*(x[b:b + 1] for x in kv[:4]))
+        one = qasc.KV4(*(x[b:b + 1] for x in (kv.K, kv.K_sf, kv.V, kv.V_sf)))
         cb, lb = batch_tensors([0, n], [n])
         qasc.kv4_read(one, lb, K[b, :, :n].transpose(0, 1), V[b, :, :n].transpose(0, 1), cu_q=cb)
     want, want_lse = outputs(91, Hq)

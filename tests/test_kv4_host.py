@@ -224,10 +224,12 @@ def test_binding_checks_the_cache():
             call(kv)                                     # all is well but the device
         with pytest.raises(TypeError):
             call(tuple(kv))
-        for bad in (kv._replace(K=kv.K[..., :32]), kv._replace(K=kv.K[0]), kv._replace(V=kv.V[:, :1]),
-                    kv._replace(K_sf=kv.K_sf.view(u8)), kv._replace(K=kv.K.float()), kv._replace(V_sf=kv.K_sf[:, :, ::2])):
-            with pytest.raises(ValueError):
-                call(bad)
+        for bad in (dict(K=kv.K[..., :32]), dict(K=kv.K[0]), dict(V=kv.V[:, :1]), dict(K_sf=kv.K_sf.view(u8)),
+                    dict(K=kv.K.float()), dict(V_sf=kv.K_sf[:, :, ::2]), dict(K=None), dict(V=3)):
+            with pytest.raises((ValueError, TypeError)):
+                call(qasc.KV4(**{**dict(zip(("K", "K_sf", "V", "V_sf"), kv)), **bad}))
+    with pytest.raises(AttributeError):
+        kv.K = kv.V
     with pytest.raises(ValueError, match="block_table"):
         qasc.kv4_read_paged(kv, torch.zeros((2, 1), dtype=i32), lens, k, k)
 
