@@ -123,7 +123,8 @@ struct Walk {
   int x0;              // the item's first place
   int b, rem, items, span;
   int start, end;      // the warp's places; whole items: its part of each of them and their parts
-  int left;            // whole items: items left
+  int left;            // whole items: items left, this one among them
+  int used;            // this item has been handed out
   Seq s;
 };
 
@@ -303,19 +304,11 @@ __device__ __forceinline__ int token_of_slot(const Args& p, const Piece& pc, int
   return __ldg(p.a.sel + list * p.a.K + i);   // (checked when it is used, a tile later: see next_rows)
 }
 
-// The item that holds place x.
+// The item that holds place x, of sequence b or a later one; `at` places stand before b.
 template <bool kList, int kRows>
-__device__ __forceinline__ Walk walk_at(const Args& p, const int* place, int x) {
-  int lo = 0, hi = (p.seqs + (1 << p.ssh) - 1) >> p.ssh;   // the last group with place <= x
-  if (hi == 1) hi = 0;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (place[mid] <= x) lo = mid;
-    else hi = mid;
-  }
+__device__ __forceinline__ Walk walk_from(const Args& p, int b, int at, int x) {
   Walk w;
-  int at = hi == 0 ? 0 : place[lo];
-  for (w.b = lo << p.ssh;; ++w.b) {
+  for (w.b = b;; ++w.b) {
     w.s = seq_of<kList>(p, w.b);
     w.items = items_of<kList, kRows>(p, w.s, w.b);
     if (w.items == 0) continue;
@@ -396,9 +389,17 @@ __device__ __forceinline__ int next_piece(const Args& p, Smem<kNT>& S, int warp,
   const int lane = threadIdx.x & 31;
   Walk walk = S.walk[warp];
   bool found = false;
-  auto more = [&]() { return p.whole ? walk.left > 0 : walk.b < p.seqs && walk.x0 < walk.end; };
+  // whether an item may stand behind this one
+  auto more = [&]() { return p.whole ? walk.left > 1 : walk.x0 + walk.span < walk.end; };
   __syncwarp();
-  while (!found && more()) {
+  while (!found) {
+    if (walk.used) {
+      if (!more()) break;
+      --walk.left;
+      walk_on<kList, kRows>(p, walk);
+    }
+    if (walk.b >= p.seqs) break;
+    walk.used = 1;
     const Piece pc = piece_of<kList, kRows>(p, walk);
     if (pc.tiles == 0 && (p.whole ? walk.start == 0 : walk.x0 >= walk.start)) {
       for (int i = 0; i < pc.rows; ++i) {
@@ -417,8 +418,6 @@ __device__ __forceinline__ int next_piece(const Args& p, Smem<kNT>& S, int warp,
       if (p.a.pm.table && kTile * lane < p.a.pm.pages_per_seq)
         asm volatile("prefetch.global.L1 [%0];" ::"l"(p.a.pm.table + pc.base + kTile * lane) : "memory");
     }
-    --walk.left;
-    if (!p.whole || walk.left > 0) walk_on<kList, kRows>(p, walk);
   }
   if (lane == 0) S.walk[warp] = walk;
   __syncwarp();
@@ -444,8 +443,32 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
       const int len = __ldg(p.a.bt.lens + b);
       if (len < 0 || len > p.n_cap) record_error(p.err, kErrBadPage);
     }
+  // A lane has kLaneSeq sequences of a short line (every warp for itself, without a
+  // barrier), a thread a group of a long one.
+  constexpr int kLaneSeq = 4;
+  const bool short_line = p.seqs <= 32 * kLaneSeq;
+  const int each_lane = (p.seqs + 31) / 32;
+  int lane_places = 0, lane_before = 0;   // of the lane's sequences, and before them
   int places = p.B * p.Hkv;
-  if (!plain) {
+  if (!plain && short_line) {
+#pragma unroll
+    for (int i = 0; i < kLaneSeq; ++i) {
+      const int b = lane * each_lane + i;
+      if (i < each_lane && b < p.seqs) {
+        const Seq s = seq_of<kList>(p, b);
+        const int items = items_of<kList, kRows>(p, s, b);
+        if (items > 0) lane_places += items * span_of<kList, kRows>(p, s, b);
+      }
+    }
+    int inc = lane_places;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    lane_before = inc - lane_places;
+    places = __shfl_sync(0xffffffffu, inc, 31);
+  } else if (!plain) {
     for (int i = tid; i < groups; i += kThreads) {
       int sum = 0;
       for (int b = i << p.ssh; b < min(p.seqs, (i + 1) << p.ssh); ++b) {
@@ -456,31 +479,43 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
       S.place[i] = sum;
     }
     __syncthreads();
-    if (groups > 1) {
-      if (warp == 0) {
-        int sum = 0;
-        for (int b0 = 0; b0 < groups; b0 += 32) {
-          const int b = b0 + lane;
-          const int v = b < groups ? S.place[b] : 0;
-          int vi = v;
+    if (warp == 0) {
+      int sum = 0;
+      for (int b0 = 0; b0 < groups; b0 += 32) {
+        const int b = b0 + lane;
+        const int v = b < groups ? S.place[b] : 0;
+        int vi = v;
 #pragma unroll 1
-          for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, vi, o);
-            if (lane >= o) vi += x;
-          }
-          if (b < groups) S.place[b] = sum + vi - v;
-          sum += __shfl_sync(0xffffffffu, vi, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, vi, o);
+          if (lane >= o) vi += x;
         }
-        if (lane == 0) S.place[groups] = sum;
+        if (b < groups) S.place[b] = sum + vi - v;
+        sum += __shfl_sync(0xffffffffu, vi, 31);
       }
-      __syncthreads();
+      if (lane == 0) S.place[groups] = sum;
     }
-    places = S.place[groups > 1 ? groups : 0];   // (of one group the sum itself stands there)
+    __syncthreads();
+    places = S.place[groups];
   }
+  auto walk_at = [&](int x) {   // the item that holds place x
+    if (short_line) {
+      const unsigned here = __ballot_sync(0xffffffffu, lane_before <= x && x < lane_before + lane_places);
+      const int from = __ffs(here) - 1;
+      return walk_from<kList, kRows>(p, from * each_lane, __shfl_sync(0xffffffffu, lane_before, from), x);
+    }
+    int lo = 0, hi = groups;   // the last group with place <= x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (S.place[mid] <= x) lo = mid;
+      else hi = mid;
+    }
+    return walk_from<kList, kRows>(p, lo << p.ssh, S.place[lo], x);
+  };
   const Line line(places, max(1, min(static_cast<int>(gridDim.x), p.whole ? places : (places + kLeast - 1) / kLeast)));
   Walk walk;
   walk.b = p.seqs;
-  walk.x0 = walk.end = walk.start = walk.left = 0;
+  walk.x0 = walk.end = walk.start = walk.left = walk.used = 0;
   if (blockIdx.x < line.G && places > 0) {
     const unsigned first = line.start(blockIdx.x), all = line.start(blockIdx.x + 1) - first;
     if (p.whole) {   // items of its own for every warp, or warps for every item
@@ -502,17 +537,19 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
           walk.items = kList ? 1 : p.Hkv;
           walk.span = 1;
         } else {
-          walk = walk_at<kList, kRows>(p, S.place, first + item);
+          walk = walk_at(first + item);
         }
       }
       walk.left = left;
+      walk.used = 0;
       walk.start = part;
       walk.end = parts;
     } else {
       const unsigned each = all / kWarps, more = all - each * kWarps;
       const int start = first + each * warp + more * warp / kWarps;
       const int end = first + each * (warp + 1) + more * (warp + 1) / kWarps;
-      if (start < end) walk = walk_at<kList, kRows>(p, S.place, start);
+      if (start < end) walk = walk_at(start);
+      walk.used = 0;
       walk.start = start;
       walk.end = end;
     }
@@ -975,9 +1012,23 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const Args 
       l = l * a + v.y * b;
       o = make_float4(o.x * a + y.x * b, o.y * a + y.y * b, o.z * a + y.z * b, o.w * a + y.w * b);
     };
-    for (int c = blockIdx.x + warp; c <= sh.last; c += kMergeWarps) {
-      const int64_t part = (static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x))) * kRows + col;
-      join(__ldcg(p.part_ml + part), __ldcg(reinterpret_cast<const float4*>(p.part_o + part * kD) + lane));
+    constexpr int kAhead = 4;   // parts whose loads a warp has in flight
+    for (int c0 = blockIdx.x + warp; c0 <= sh.last; c0 += kAhead * kMergeWarps) {
+      float2 v[kAhead];
+      float4 y[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int c = c0 + i * kMergeWarps;
+        v[i] = make_float2(-INFINITY, 0.0f);
+        y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c <= sh.last) {
+          const int64_t part = (static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x))) * kRows + col;
+          v[i] = __ldcg(p.part_ml + part);
+          y[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + part * kD) + lane);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) join(v[i], y[i]);
     }
     so[warp][lane] = o;
     if (lane == 0) sml[warp] = make_float2(m, l);
