@@ -311,6 +311,57 @@ def test_append_does_not_depend_on_the_cut():
         assert torch.equal(a, b)
 
 
+def test_append_in_place_and_without_queries():
+    T, Hq, Hkv = 300, 16, 4
+    q, k, v = (rand((T, h, 128), 16 + h).cuda() for h in (Hq, Hkv, 2 * Hkv))
+    v = v[:, ::2].contiguous()
+    f = (10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)).float().cuda()
+    c, ln = batch_tensors([0, T], [T + 5])
+    caches, outs = [], []
+    for way in ("apart", "in place", "none"):
+        kv = qasc.alloc_kv4(1, Hkv, T + 5)
+        qq = q.clone()
+        out = {"apart": torch.zeros_like(q), "in place": qq, "none": None}[way]
+        qasc.kv4_rope_append(None if out is None else qq, k, v, out, kv, ln, f, cu_q=c)
+        caches.append(kv)
+        outs.append(out)
+    qasc.qasc_device_error()
+    assert torch.equal(outs[0], outs[1])
+    for kv in caches[1:]:
+        assert torch.equal(kv.K, caches[0].K) and torch.equal(kv.V_sf.view(torch.uint8), caches[0].V_sf.view(torch.uint8))
+
+
+@pytest.mark.parametrize("ql", [[1, 1, 1], [300, 2, 400]])
+def test_append_and_read_replay_in_a_graph(ql):
+    """A captured call follows the lengths and offsets on the device."""
+    T, Hkv, P = sum(ql), 2, 64
+    single = ql == [1] * 3
+    k, v = rand((T, Hkv, 128), 17).cuda(), rand((T, Hkv, 128), 18).cuda()
+    f = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float().cuda()
+    table = torch.arange(30, dtype=torch.int32).reshape(3, 10).cuda()
+    c, ln = batch_tensors(None if single else np.concatenate([[0], np.cumsum(ql)]).tolist(), [m + 5 for m in ql])
+
+    def call(kv, K, V):
+        qasc.kv4_rope_append_paged(None, k, v, None, kv, table, ln, f, cu_q=c)
+        qasc.kv4_read_paged(kv, table, ln, K, V, cu_q=c)
+
+    def fresh():
+        return qasc.alloc_kv4(30, Hkv, P), torch.zeros_like(k), torch.zeros_like(v)
+    one, two = fresh(), fresh()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        call(*one)
+    for shift in (0, 40):
+        ln.copy_(torch.tensor([m + 5 + shift for m in ql], dtype=torch.int32))
+        graph.replay()
+        call(*two)
+        torch.cuda.synchronize()
+        assert torch.equal(one[0].K, two[0].K) and torch.equal(one[0].V, two[0].V)
+        assert torch.equal(one[1], two[1]) and torch.equal(one[2], two[2]) and bool(one[1].any())
+    qasc.qasc_device_error()
+
+
 @pytest.mark.parametrize("bad", ["page", "position", "length"])
 def test_append_and_read_skip_what_lies_outside(bad):
     P, Hkv = 64, 2
@@ -651,6 +702,106 @@ def test_two_windows_on_two_streams():
     assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
 
 
+def test_two_graphs_take_turns_with_one_workspace():
+    """Nothing of a call stays in its workspace: a call shared between blocks, one that is not
+    and one over a copy, captured with the same one and replayed in turn."""
+    Hq, Hkv, P, n = 16, 2, 64, 5000
+    pages = Pages4([n, n - 9], Hkv, P, cdiv(n, P), seed=47, random=True)
+    kv, table = pages.cache(), pages.table.cuda()
+    kinds = [([0, 1, 2], 2, n, 1), ([0, 1, 2], 2, 300, 1), ([0, 60, 90], 90, 700, 60)]
+    ws = qasc.alloc_workspace(max(qasc.kv4_window_attn_workspace_bytes(T, 2, Hq, Hkv, pages.pps * P, local=local, max_q=m)
+                                  for _, T, local, m in kinds))
+    ln = batch_tensors(None, [n, n - 9])[1]
+    graphs, outs, wants = [], [], []
+    for cu, T, local, m in kinds:
+        q, c = rand((T, Hq, 128), 48 + T).cuda(), batch_tensors(cu, [0])[0]
+        out, want = outputs(T, Hq), outputs(T, Hq)
+
+        def call(o, ws=ws, q=q, c=c, local=local, m=m):
+            qasc.kv4_window_attn_paged(q, kv, table, ln, o[0], ws, local=local, cu_q=c, max_q=m, lse=o[1])
+        call(want)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            call(out)
+        graphs.append((graph, call))
+        outs.append(out)
+        wants.append(want)
+    for _ in range(3):
+        for graph, _ in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    qasc.qasc_device_error()
+    for out, want in zip(outs, wants):
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def repeated(n, Hkv, P, seed):
+    """A sequence of n tokens whose pages come around again: a long context in a small pool."""
+    pages = Pages4([8 * P], Hkv, P, 8, seed=seed, random=True)
+    first = pages.table[0].clone()
+    pages.pps = cdiv(n, P)
+    pages.table = first.repeat(cdiv(pages.pps, 8))[:pages.pps].reshape(1, -1).contiguous()
+    reps = cdiv(n, 8 * P)
+    values = [np.concatenate([pages.values(side)[0]] * reps, axis=1)[:, :n] for side in range(2)]
+    return pages, values
+
+
+def test_window_places_of_more_than_a_tile():
+    """So many row blocks of so wide a table that a place of the line is several tiles."""
+    T, Hq, Hkv, P, n = 8200, 8, 1, 64, 9000
+    pages, values = repeated(n, Hkv, P, 49)
+    wide = 1 << 17                                          # n_cap = 2^23
+    table = torch.full((1, wide), POISON, dtype=torch.int32)
+    table[0, :pages.pps] = pages.table[0]
+    q = rand((T, Hq, 128), 50)
+    out, lse = outputs(T, Hq)
+    c, ln = batch_tensors([0, T], [n])
+    ws = window_ws(T, 1, Hq, Hkv, wide * P, 64, max_q=1)
+    qasc.kv4_window_attn_paged(q.cuda(), pages.cache(), table.cuda(), ln, out, ws, local=64, cu_q=c, max_q=1, lse=lse)
+    qasc.qasc_device_error()
+    tokens = [0, 3, 700, 4099, T - 1]
+    ref = osv.window_attention(f64(q), values[:1], values[1:], [0, T], [n], 4, 64, tokens=tokens)
+    check_rows(out, lse, ref, 68, 6.0, rows=tokens)
+
+
+def test_window_longer_than_the_copy():
+    """A chunk of a context that the copy has no room for stands beside one that it has."""
+    Hq, Hkv, P, ql = 64, 64, 64, [130, 131]
+    lens = [140000, 300]
+    long, values = repeated(lens[0], Hkv, P, 51)
+    pps = long.pps
+    table = torch.cat([long.table, long.table[:, :8].repeat(1, cdiv(pps, 8))[:, :pps]])
+    q = rand((261, Hq, 128), 52)
+    c, ln = batch_tensors([0, 130, 261], lens)
+    out, lse = outputs(261, Hq)
+    ws = window_ws(261, 2, Hq, Hkv, pps * P, lens[0], max_q=131)
+    assert ws.numel() < 5 << 30                             # 4 GiB of a copy at most
+    qasc.kv4_window_attn_paged(q.cuda(), long.cache(), table.cuda(), ln, out, ws, local=lens[0], cu_q=c, max_q=131, lse=lse)
+    qasc.qasc_device_error()
+    for t, h in ((0, 0), (77, 63), (129, 31), (130, 5), (260, 63)):
+        b = t >= 130
+        n = lens[b] - ql[b] + t - (130 if b else 0) + 1
+        want = osv.attend(f64(q)[t, h], values[0][h, :n], values[1][h, :n])
+        ref = tuple(np.asarray(x)[None, None] for x in want)
+        check_rows(out[t:t + 1, h:h + 1].contiguous(), lse[t:t + 1, h:h + 1], ref, n, 6.0, p=2.0 ** -8)
+
+
+def test_window_bad_page_of_a_copied_sequence():
+    pages = Pages4([300], 2, 64, 5, seed=53, random=True)
+    pages.table[0, 2] = -1
+    q = rand((70, 8, 128), 54)
+    out, lse = outputs(70, 8)
+    c, ln = batch_tensors([0, 70], [300])
+    qasc.kv4_window_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), ln, out, window_ws(70, 1, 8, 2, 320, 300), local=300,
+                               cu_q=c, lse=lse)
+    with pytest.raises(qasc.QascError, match="BAD_TABLE"):
+        qasc.qasc_device_error()
+    K, V = pages.values(0), pages.values(1)
+    K[0][:, 128:192], V[0][:, 128:192] = 0, 0               # rows of zeros
+    check_rows(out, lse, osv.window_attention(f64(q), K, V, [0, 70], [300], 4, 300), 300, 6.0, p=2.0 ** -8)
+
+
 # --------------------------------------------------------------------- sparse
 def sparse_ref(q, pages, lists, n, sink, local):
     """lists[b][g]: listed tokens."""
@@ -713,8 +864,6 @@ def test_sparse(B, Hq, Hkv, n, K, sink, local, per_head, with_len, paged):
     args = dict(n=n, sink=sink, local=local, lengths=None if lens is None else lens.reshape(shape).cuda(),
                 per_kv_head=per_head, lse=lse)
     sel_arg = sel.reshape(*shape, K).cuda() if K else None
-    if K == 0 and per_head:
-        pytest.skip("no list")
     n_cap = pages.pps * P if paged else n + 7
     ws = qasc.alloc_workspace(qasc.kv4_sparse_attn_workspace_bytes(B, Hq, Hkv, n, n_cap, K, sink, local))
     ws.fill_(255)
@@ -724,6 +873,56 @@ def test_sparse(B, Hq, Hkv, n, K, sink, local, per_head, with_len, paged):
         qasc.kv4_sparse_attn(q.cuda(), pages.contiguous(n_cap), sel_arg, out, ws, **args)
     qasc.qasc_device_error()
     check_rows(out, lse, ref, n, max(6.0, vmax_of(pages)))
+
+
+def test_sparse_of_many_lists():
+    B, Hq, Hkv, n, K, P = 300, 16, 8, 900, 40, 64
+    pages = Pages4([n], Hkv, P, cdiv(n, P), seed=57, random=True)
+    table = pages.table.repeat(B, 1).cuda()                 # all sequences over the same pages
+    g = torch.Generator().manual_seed(58)
+    sel = torch.randint(4, n - 64, (B, Hkv, K), generator=g).int()      # in any order, some twice
+    lens = torch.randint(0, K + 1, (B, Hkv), generator=g).int()
+    q = rand((B, Hq, 128), 59)
+    out, lse = outputs(B, Hq)
+    ws = qasc.alloc_workspace(qasc.kv4_sparse_attn_workspace_bytes(B, Hq, Hkv, n, pages.pps * P, K, 4, 64))
+    qasc.kv4_sparse_attn_paged(q.cuda(), pages.cache(), table, sel.cuda(), out, ws, n=n, local=64, lengths=lens.cuda(),
+                               per_kv_head=True, lse=lse)
+    qasc.qasc_device_error()
+    rows = list(range(0, B, 37)) + [B - 1]
+    K1, V1 = pages.values(0) * B, pages.values(1) * B
+
+    class Held:
+        values = staticmethod(lambda side: [(K1, V1)[side][b] for b in rows])
+    Held.Hkv = Hkv
+    ref = sparse_ref(f64(q)[rows], Held, [[sel[b, gg, :int(lens[b, gg])].tolist() for gg in range(Hkv)] for b in rows], n, 4, 64)
+    check_rows(out[rows], lse[rows], ref, n, 6.0)
+
+
+def test_sparse_replays_in_a_graph():
+    """The captured call follows the lists and their lengths; a list of the whole context is split."""
+    B, Hq, Hkv, n, K, P = 2, 32, 8, 6000, 4000, 64
+    pages = Pages4([n] * B, Hkv, P, cdiv(n, P), seed=55, random=True)
+    kv, table = pages.cache(), pages.table.cuda()
+    q = rand((B, Hq, 128), 56).cuda()
+    sel = torch.arange(4, 4 + K, dtype=torch.int32).repeat(B, 1).cuda()
+    lens = torch.full((B,), K, dtype=torch.int32, device="cuda")
+    ws = qasc.alloc_workspace(qasc.kv4_sparse_attn_workspace_bytes(B, Hq, Hkv, n, pages.pps * P, K))
+
+    def call(o):
+        qasc.kv4_sparse_attn_paged(q, kv, table, sel, o[0], ws, n=n, lengths=lens, lse=o[1])
+    got, want = outputs(B, Hq), outputs(B, Hq)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        call(got)
+    for use in ([K, K], [17, 3000], [0, K]):
+        lens.copy_(torch.tensor(use, dtype=torch.int32))
+        sel.copy_(sel.flip(1) if use[0] == 17 else sel)
+        graph.replay()
+        call(want)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    qasc.qasc_device_error()
 
 
 def test_sparse_entry_outside_is_reported():
