@@ -55,19 +55,17 @@ namespace qasc {
 namespace {
 
 constexpr int kTile = 32;                      // tokens of a warp's tile
-#ifndef KV4_W
-#define KV4_W 12
-#define KV4_S 3
-#define KV4_C 2
-#endif
-constexpr int warps_of(int nt) { return nt == 1 ? KV4_W : 8; }
-constexpr int stages_of(int nt) { return nt == 1 ? KV4_S : 4; }   // tiles of a warp's ring
+// Of a block, by its items' column tiles: as many warps as the registers allow
+// (166 and 243 of a thread).  64 sequences with a 4K window: 12 warps of three stages 66
+// us, 8 of four 69, 16 of two, which spill, 67.
+constexpr int warps_of(int nt) { return nt == 1 ? 12 : 8; }
+constexpr int stages_of(int nt) { return nt == 1 ? 3 : 4; }   // tiles of a warp's ring
 constexpr int kTileCodes = kTile * kKv4Codes;  // bytes
 constexpr int kTileScales = kTile * kKv4Groups;
 constexpr int kStage = 2 * (kTileCodes + kTileScales);
 constexpr int kSums = 512;                     // places are summed for as many groups of sequences at most
 constexpr int kQueue = 8;                      // items that a warp's loads are ahead of its products, at most
-constexpr int kItemCost = KV4_C;                   // places of an item beside its tiles: queries, output
+constexpr int kItemCost = 2;                   // places of an item beside its tiles: queries, output (4: 2 % more)
 constexpr int kTokensMost = 1 << 24;           // above n_cap, and sink and local as the kernel has them
 constexpr int kTilesMost = kTokensMost / kTile;
 constexpr int kLeast = 8;                      // places that a block takes at least
@@ -226,16 +224,17 @@ struct Smem {
   int place[kSums + 1];          // places before a group of sequences
 };
 
-// (64 bytes are fetched into L2, not the default 128: of scattered rows the rest would be
-// read for nothing, 215 MB where 95 are listed: four 128K contexts at 20 %, 48 against 40 us.)
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {   // the rest zeros
-  asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global.L2::64B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// Rows of their own, zeros behind `bytes`.  (64 bytes are fetched into L2, not the default
+// 128: of scattered rows the rest would be read for nothing, 215 MB where 95 are listed:
+// four 128K contexts at 20 %, 48 against 40 us.)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global.L2::64B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -1070,12 +1069,23 @@ static_assert(sizeof(Smem<1>) <= 232448 && sizeof(Smem<2>) <= 232448, "shared me
 int tiles_of(const qasc_shape& s, int64_t max_q) { return max_q * (s.Hq / s.Hkv) <= 8 ? 1 : 2; }
 
 // Sequences of more rows than this take their keys and values from a bf16 copy and
-// go to kv_window_attn's kernel, whose products are tcgen05's.
-#ifndef KV4_CR
-#define KV4_CR 128
-#endif
-constexpr int64_t kCopyRows = KV4_CR;
+// go to kv_window_attn's kernel, whose products are tcgen05's: a row block here costs
+// what it costs whether the next one needs the same keys or not.  One sequence of
+// 32768 tokens, 32 heads, 8 KV heads, here and over a copy: 64 rows 45 and 75 us,
+// 128 rows 78 and 79, 256 rows 143 and 88; 32 sequences of 4096, 64 heads, 128 rows: 283 and 261.
+constexpr int64_t kCopyRows = 128;
 constexpr int64_t kCopyBytes = int64_t(1) << 32;   // of a copy, at most
+
+// Whether the copy pays for a call that may have such sequences (microseconds, from
+// the same runs): it is two kernels more and its bytes; here every block of 16 rows
+// takes 1.05 ns a tile on 152 SMs.  8 sequences of 64 tokens over a window of 1000, 8 heads, 2
+// KV heads: 21 us here, 31 over a copy; of 257 tokens 49 and 32.
+bool copy_pays(const qasc_shape& s, int64_t T, int64_t tokens, int64_t seqs) {
+  const double gq = s.Hq / s.Hkv, keys = static_cast<double>(tokens) * s.Hkv;
+  const double here = 10.0 + (T * gq / 16.0 + 1.0) * keys / kTile * 1.05e-3;
+  const double copy = 27.0 + seqs * keys * 656.0 / 5.5e6 + T * gq * keys * 512.0 / 1.4e9;
+  return copy < here;
+}
 
 struct CopyLayout {
   int64_t capacity = 0, pages_per_seq = 0;   // capacity 0: no copy
@@ -1092,6 +1102,7 @@ CopyLayout copy_layout(const qasc_shape& s, int64_t T, int64_t max_q, int32_t si
   const int64_t cap = L.pages_per_seq * kCopyPage;
   if (cap >= kTokensMost || static_cast<int64_t>(s.B) * s.Hkv * cap >= (int64_t(1) << 31)) return L;
   const int64_t seqs = std::min<int64_t>(s.B, T * gq / (kCopyRows + 1));   // that can be as long
+  if (!copy_pays(s, T, tokens, seqs)) return L;
   const int64_t page_bytes = static_cast<int64_t>(s.Hkv) * kCopyPage * kD * 2;
   const int64_t most = std::min(kCopyBytes / (2 * page_bytes), ((int64_t(1) << 31) - 1) / (s.Hkv * kCopyPage));
   L.capacity = std::min(seqs * L.pages_per_seq, most);

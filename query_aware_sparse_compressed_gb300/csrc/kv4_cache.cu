@@ -29,10 +29,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxTok = 4;       // tokens of an append block's tile
 constexpr int kFreqs = kD / 2;
 constexpr int kUnits = 8;        // threads of a head: 16 values each
-#ifndef KV4_RING
-#define KV4_RING 4
-#endif
-constexpr int kRing = KV4_RING;         // units that a thread's copies are ahead
+constexpr int kRing = 4;         // units that a thread's copies are ahead
 constexpr size_t kRingBytes = static_cast<size_t>(kThreads) * kRing * 32;
 constexpr int kPoints = 256;     // of a quarter turn
 
@@ -217,10 +214,7 @@ __device__ __forceinline__ void store_quantised(const uint4& x, const uint4& y, 
 // A unit of a head is 16 values in two 16-byte chunks: both members of eight
 // pairs, or values that are only copied; unit u of a head uses the frequencies
 // 8u .. 8u + 7 in either pairing.
-#ifndef KV4_AB
-#define KV4_AB 3
-#endif
-__global__ void __launch_bounds__(kThreads, KV4_AB) kv4_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const AppendArgs a) {
   // of this tile and the next one, which is prepared ahead: one barrier a tile
   __shared__ __align__(16) float turns_of[2][4][kMaxTok][kFreqs];   // cos, sin (16 bits) and their rests
   __shared__ int64_t rows_of[2][kMaxTok];    // cache row of KV head 0; -1: not written, -2: a token of no sequence
@@ -431,11 +425,8 @@ __global__ void __launch_bounds__(kThreads, KV4_AB) kv4_append_kernel(const Appe
 constexpr int kReadTok = 32;     // tokens of a read block's tile
 constexpr int kRowLanes = 16;    // threads of a row: 8 values each
 constexpr int kReadRows = kThreads / kRowLanes;   // rows of a pass
-#ifndef KV4_RB
-#define KV4_RB 6
-#define KV4_RF 4
-#endif
-constexpr int kReadBatch = KV4_RF;    // rows whose loads a thread has in flight
+constexpr int kReadBlocks = 6;   // blocks of an SM
+constexpr int kReadBatch = 4;    // rows whose loads a thread has in flight
 
 struct ReadArgs {
   Kv4Cache kv;
@@ -491,7 +482,7 @@ __device__ __forceinline__ void read_rows(const Kv4Cache& kv, int Hkv, const int
   }
 }
 
-__global__ void __launch_bounds__(kThreads, KV4_RB) kv4_read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kThreads, kReadBlocks) kv4_read_kernel(const ReadArgs a) {
   __shared__ int64_t row0[kReadTok];
   const int tid = threadIdx.x;
   pdl_wait();
@@ -537,7 +528,7 @@ constexpr int kCopySeq = 2048;
 // Every block makes the plan for itself: which sequences are copied and their
 // first pages (sequences take pages in their order as long as all of theirs
 // are left); block 0 writes it down.  Then tiles of kReadTok tokens.
-__global__ void __launch_bounds__(kThreads, KV4_RB) kv4_copy_kernel(const CopyArgs a) {
+__global__ void __launch_bounds__(kThreads, kReadBlocks) kv4_copy_kernel(const CopyArgs a) {
   __shared__ int64_t row0[kReadTok];
   __shared__ int32_t first[kCopySeq + 1];
   __shared__ int32_t sums[kThreads / 32];

@@ -183,6 +183,11 @@ def window(q, pages, cu, lens, sink, local, max_q=None):
     return out, lse
 
 
+def goes_over_a_copy(T, B, Hq, Hkv, n_cap, local, sink, max_q):
+    size = qasc.kv4_window_attn_workspace_bytes
+    return size(T, B, Hq, Hkv, n_cap, local=local, sink=sink, max_q=max_q) > size(T, B, Hq, Hkv, n_cap, local=local, sink=sink, max_q=1)
+
+
 def vmax_of(pages):
     return max(np.abs(v).max() if v.size else 0.0 for v in pages.values(1))
 
@@ -708,7 +713,8 @@ def test_two_graphs_take_turns_with_one_workspace():
     Hq, Hkv, P, n = 16, 2, 64, 5000
     pages = Pages4([n, n - 9], Hkv, P, cdiv(n, P), seed=47, random=True)
     kv, table = pages.cache(), pages.table.cuda()
-    kinds = [([0, 1, 2], 2, n, 1), ([0, 1, 2], 2, 300, 1), ([0, 60, 90], 90, 700, 60)]
+    kinds = [([0, 1, 2], 2, n, 1), ([0, 1, 2], 2, 300, 1), ([0, 400, 560], 560, 2000, 400)]
+    assert goes_over_a_copy(560, 2, Hq, Hkv, pages.pps * P, 2000, 4, 400)
     ws = qasc.alloc_workspace(max(qasc.kv4_window_attn_workspace_bytes(T, 2, Hq, Hkv, pages.pps * P, local=local, max_q=m)
                                   for _, T, local, m in kinds))
     ln = batch_tensors(None, [n, n - 9])[1]
@@ -776,7 +782,7 @@ def test_window_longer_than_the_copy():
     c, ln = batch_tensors([0, 130, 261], lens)
     out, lse = outputs(261, Hq)
     ws = window_ws(261, 2, Hq, Hkv, pps * P, lens[0], max_q=131)
-    assert ws.numel() < 5 << 30                             # 4 GiB of a copy at most
+    assert goes_over_a_copy(261, 2, Hq, Hkv, pps * P, lens[0], 4, 131) and ws.numel() < 5 << 30   # 4 GiB of a copy at most
     qasc.kv4_window_attn_paged(q.cuda(), long.cache(), table.cuda(), ln, out, ws, local=lens[0], cu_q=c, max_q=131, lse=lse)
     qasc.qasc_device_error()
     for t, h in ((0, 0), (77, 63), (129, 31), (130, 5), (260, 63)):
@@ -787,19 +793,59 @@ def test_window_longer_than_the_copy():
         check_rows(out[t:t + 1, h:h + 1].contiguous(), lse[t:t + 1, h:h + 1], ref, n, 6.0, p=2.0 ** -8)
 
 
+COPIED = [
+    # Hq, Hkv, P, new tokens, lens, sink, local: calls that go over a copy
+    (64, 8, 64, [200, 1, 300, 2], [1500, 900, 800, 77], 4, 100000),
+    (64, 8, 128, [400, 30, 0, 1], [1300, 700, 50, 1], 4, 300),
+    (32, 8, 64, [700], [5000], 200, 90),
+    (8, 8, 64, [1000, 129], [1000, 4000], 0, 2500),
+    (64, 8, 64, [150, 16, 17, 400], [100, 2000, 2000, 401], 4, 1000),   # more new tokens than cached ones
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,P,ql,lens,sink,local", COPIED)
+def test_window_over_a_copy(Hq, Hkv, P, ql, lens, sink, local):
+    T, B = sum(ql), len(ql)
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    pages = Pages4(lens, Hkv, P, cdiv(max(lens), P) + 1, seed=61, random=True, t=(0.5, 4.0))
+    K, V = pages.values(0), pages.values(1)
+    for b, n in enumerate(lens):                           # what no query attends to
+        first = max(0, n - ql[b])
+        if ql[b] == 0:
+            pages.hide(b, 0, n)
+        elif first - local + 1 > sink:
+            pages.hide(b, sink, first - local + 1)
+    assert goes_over_a_copy(T + 2, B, Hq, Hkv, pages.pps * P, local, sink, max(ql))
+    q = rand((T + 2, Hq, 128), 62, 0.3)                    # two tokens of no sequence
+    out, lse = window(q, pages, cu, lens, sink, local, max_q=max(ql))
+    tokens = sorted({t for a, z in zip(cu, cu[1:]) if z > a for t in (a, (a + z) // 2, z - 1)})
+    ref = osv.window_attention(f64(q[:T]), K, V, cu, lens, sink, local, tokens=tokens)
+    check_rows(out[:T], lse[:T], ref, max(lens), 24.0, rows=tokens, p=p_error(ql, Hq // Hkv))
+    # and every row against the calls without a copy, with both roundings
+    out1, lse1 = window(q, pages, cu, lens, sink, local, max_q=1)
+    assert float((out[:T].float() - out1[:T].float()).abs().max()) <= 24.0 * (2 * 2.0 ** -8 + 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16)
+    finite = torch.isfinite(lse1[:T])
+    assert torch.equal(finite, torch.isfinite(lse[:T]))
+    assert float((lse[:T][finite] - lse1[:T][finite]).abs().max()) <= 1e-3
+    assert bool((out[T:] == CANARY).all()) and bool((lse[T:] == CANARY).all())
+
+
 def test_window_bad_page_of_a_copied_sequence():
-    pages = Pages4([300], 2, 64, 5, seed=53, random=True)
+    Hq, Hkv, n, m = 64, 8, 1500, 300
+    pages = Pages4([n], Hkv, 64, 24, seed=53, random=True)
     pages.table[0, 2] = -1
-    q = rand((70, 8, 128), 54)
-    out, lse = outputs(70, 8)
-    c, ln = batch_tensors([0, 70], [300])
-    qasc.kv4_window_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), ln, out, window_ws(70, 1, 8, 2, 320, 300), local=300,
+    assert goes_over_a_copy(m, 1, Hq, Hkv, 24 * 64, n, 4, m)
+    q = rand((m, Hq, 128), 54)
+    out, lse = outputs(m, Hq)
+    c, ln = batch_tensors([0, m], [n])
+    qasc.kv4_window_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), ln, out, window_ws(m, 1, Hq, Hkv, 24 * 64, n), local=n,
                                cu_q=c, lse=lse)
     with pytest.raises(qasc.QascError, match="BAD_TABLE"):
         qasc.qasc_device_error()
     K, V = pages.values(0), pages.values(1)
     K[0][:, 128:192], V[0][:, 128:192] = 0, 0               # rows of zeros
-    check_rows(out, lse, osv.window_attention(f64(q), K, V, [0, 70], [300], 4, 300), 300, 6.0, p=2.0 ** -8)
+    tokens = [0, 100, m - 1]
+    check_rows(out, lse, osv.window_attention(f64(q), K, V, [0, m], [n], 4, n, tokens=tokens), n, 6.0, rows=tokens, p=2.0 ** -8)
 
 
 # --------------------------------------------------------------------- sparse
