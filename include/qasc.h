@@ -467,7 +467,7 @@ QASC_API qasc_status kv_prefix_attn_paged(const qasc_shape* shape, const qasc_pa
  * Quantising 16 values x, of bf16: a = max |x| / t, scale = e4m3(a / 6) (at most
  * 448), code = e2m1(x / t / scale), both rounded to nearest, ties to even.  Larger
  * magnitudes than 2688 t, infinities among them, become 2688 t; a group with a NaN
- * reads back as NaN; one whose scale rounds to 0 (a <= 2^-10 * 6) as 0.
+ * reads back as NaN; one whose scale rounds to 0 (a <= 6 * 2^-10) as 0.
  * ------------------------------------------------------------------------- */
 typedef struct {
   uint8_t* K;      /* device [B, Hkv, n_cap, d / 2], or a pool's [num_pages, Hkv, P, d / 2] */
@@ -518,11 +518,20 @@ QASC_API qasc_status kv4_read_paged(const qasc_shape* shape, const qasc_paged_ca
  *          tokens (without cu_q: not used).  It chooses how the work is done;
  *          a sequence of more tokens is computed all the same.
  *   workspace, ws_bytes >= kv4_window_attn_workspace_bytes(shape, tokens, max_q,
- *          sink, local)
- *   other arguments, refusals and rows without a token as for kv_window_attn; out
- *   is rounded once from fp32, the probabilities of the second product hold 11
- *   bits or more.  A block-table entry outside the pool stands for rows of zeros
- *   and is recorded as QASC_ERR_BAD_TABLE. */
+ *          sink, local), for these numbers: 4.3 MB, and more where sequences may
+ *          have more than 128 rows (new tokens times Hq / Hkv) and it pays: those
+ *          attend to a bf16 copy in the workspace of the tokens that they see (512 bytes a
+ *          token and KV head, 4 GiB at most; a sequence that finds no room goes without)
+ *          by kv_window_attn's kernel.  The workspace need not be cleared and
+ *          is free again once the call has finished on the stream; calls that can
+ *          overlap need one each.
+ *   other arguments, refusals, lengths outside the cache and rows without a token as for
+ *   kv_window_attn; out is rounded once from fp32; the probabilities of the second product
+ *   are fp16 (bf16 over a copy), sums and statistics fp32.  Rows that no query attends
+ *   to may hold anything, as there; a row with a NaN scale that some attend to reaches
+ *   their outputs, and may reach those of its sequence's other queries in that KV
+ *   head.  A block-table entry outside the pool stands for rows of zeros and is recorded
+ *   as QASC_ERR_BAD_TABLE. */
 QASC_API size_t kv4_window_attn_workspace_bytes(const qasc_shape* shape, int64_t tokens, int64_t max_q, int32_t sink,
                                                 int32_t local);
 QASC_API qasc_status kv4_window_attn(const qasc_shape* shape, const qasc_batch* batch, int64_t max_q, int32_t sink,
@@ -538,10 +547,10 @@ QASC_API qasc_status kv4_window_attn_paged(const qasc_shape* shape, const qasc_p
  *
  *   q        [B, Hq, d] bf16;  out [B, Hq, d] bf16, written (rounded once; not to
  *            overlap q);  lse [B, Hq] fp32, written if non-NULL
- *   sel, sel_len, sel_per_kv_head   as for ts_sparse_attn_ex, in any order; an
- *            entry in use outside [0, n) stands for a row of zeros and is recorded as
- *            QASC_ERR_BAD_TABLE
- *   workspace, ws_bytes >= kv4_sparse_attn_workspace_bytes(shape, params)
+ *   sel, sel_len, sel_per_kv_head   as for ts_sparse_attn_ex, in any order (an entry
+ *            that occurs twice is attended to twice); an entry in use outside [0, n)
+ *            stands for a row of zeros and is recorded as QASC_ERR_BAD_TABLE
+ *   workspace, ws_bytes >= kv4_sparse_attn_workspace_bytes(shape, params), 4.3 MB
  * A row without any token gives out 0 and lse -inf.  B <= 2048 (more:
  * QASC_ERR_UNSUPPORTED). */
 QASC_API size_t kv4_sparse_attn_workspace_bytes(const qasc_shape* shape, const qasc_ts_params* params);

@@ -6,26 +6,31 @@
 //
 // What bounds it.  144 bytes of a token and KV head are read for 512 operations
 // per query head: bytes, as long as the codes become operands fast enough.  At
-// HBM's rate an SM gets some 22 bytes a cycle, 45 values, twice as bf16 what its
-// shared memory could write and tensor cores read again (128 bytes a cycle): so
-// codes go from shared memory to registers, become fp16 there, and are the
-// register operand of the product (mma.sync, 16 x 8 x 16), which a tcgen05
-// product does not have for 8 to 16 query rows.  The products themselves take
-// a fourth of that path's rate.
+// HBM's rate an SM gets some 22 bytes a cycle, 45 values, which as bf16 take 90
+// bytes a cycle to write to shared memory and 90 for tensor cores to read again, of
+// 128 that there are: so codes go from shared memory to registers, become fp16
+// there, and are the register operand of the product (mma.sync, 16 x 8 x 16); a
+// tcgen05 product takes its second operand from shared memory only, and 128 rows
+// where there are 1 to 16.  The products take a fourth of mma.sync's rate.  One
+// sequence of 32768 tokens, 16 rows: 21 us; over a bf16 copy on tcgen05, which is
+// where calls of many rows go (see copy_pays), 75.
 //
 // Work.  The queries of a KV head's group share its keys: an item is up to
 // 8 kNT rows (token, head of the group) of a sequence and KV head.  Its tokens
-// (sink, window or list) are numbered without gaps, in tiles of 32.  The tiles of
+// are numbered in tiles of 32: the sink's, then those of the window, each of which
+// stands in one page, or a list's without gaps.  The tiles of
 // all items are laid end to end, every block takes an equal range of that line and
-// every warp of it an equal part of the range: a warp walks its tiles alone, loads
-// three ahead of their use, and writes the rows of items that are all its own.
+// every warp of it an equal part of the range: a warp walks its tiles alone, has
+// the next two on their way (three with 16 columns), and writes the rows of items
+// that are all its own.
 // Of an item that it shares it keeps (max, sum, O); the block joins its warps' at
 // its end, once, and those that go beyond it are left in the workspace, two places a block
 // (the item that it begins with, the one that it ends with), where
 // kv4_merge_kernel joins them.  (With the tiles of every item dealt to all warps and
 // joined in the block, a third of the instructions were the joins': 64 sequences
-// with a 4K window 91 us.)  Short items are not shared between blocks, and have no
-// merge to wait for.
+// with a 4K window 91 us, 73 so.)  Short items are not shared between blocks: each
+// block has items of its own, and there is no merge to wait for (4 sequences, sink and
+// 256 tokens: 7.0 us, 11 with them on the line).
 // Keys stand as rows of the first product and channels as rows of the second,
 // queries as columns of both:
 //   S^T = K Q^T      (16 tokens x 8 queries, over d)
@@ -40,11 +45,23 @@
 // Numbers.  scale * code is exact in fp16 (kv4.cuh).  A query row is scaled by a
 // power of two to a largest value of 2^14 to 2^15 and is exact in fp16 but for
 // values 2^-28 below that one.  Products, statistics and sums are fp32.  P is
-// rounded to fp16 (2^-12 of each weight, a sixteenth of the bf16 output's own
+// rounded to fp16 (2^-11 of each weight, an eighth of the bf16 output's own
 // rounding); its base is 2^-10 of the row's maximum when it was taken, and moves
 // when the maximum grows by more than 2^5: P stays below 2^15, and weights down
 // to 2^-24 of the largest keep all their bits.  The sum that divides takes P
 // unrounded.
+//
+// Measured among others of its kind.  64 sequences, 4K window, 8 KV heads (280 MB): 58
+// us, 4.8 TB/s (70 % of a copy's rate): 4.3 us until the first tile is there (lengths,
+// places, pages, rows: four loads one behind the other), then 231 cycles a tile and SM, of
+// which HBM's rate allows 201 and the instructions 150, and 3 us of join and merge.  One
+// sequence of 131072 tokens, 64 heads (151 MB): 36.5 us.  Four 128K contexts at 20 %, a
+// list a KV head: 38 us; of scattered rows HBM reads 64 bytes for 8 of scales, 134 MB for
+// 95, at 6.1 TB/s once the first rows are there (7 us).  ncu, the first case: 279.7 MB
+// read, hmma pipe 22 %, ALU pipe 44 %, issue 53 %.  What did not pay: 16 warps of
+// two stages (spills), the first product of a tile beside the second of the one before
+// (65.9 against 65.7), one loop over items and tiles (66.8 against 62.1), the first tiles' pages
+// asked for together (59.7 against 58.5), L2's default fetch of 128 bytes for lists (48 against 40).
 #include <algorithm>
 #include <climits>
 
@@ -300,7 +317,7 @@ __device__ __forceinline__ int token_of_slot(const Args& p, const Piece& pc, int
   const int i = s - pc.head;
   if (i >= pc.lo) return p.local_start + i - pc.lo;
   const int64_t list = p.a.sel_per_kv ? static_cast<int64_t>(pc.b) * p.Hkv + pc.g : pc.b;
-  return __ldg(p.a.sel + list * p.a.K + i);   // (checked when it is used, a tile later: see next_rows)
+  return __ldg(p.a.sel + list * p.a.K + i);   // (checked a tile later, where it is used: next_rows)
 }
 
 // The item that holds place x, of sequence b or a later one; `at` places stand before b.

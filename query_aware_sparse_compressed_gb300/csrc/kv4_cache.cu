@@ -12,13 +12,24 @@
 // pairs (high, low part) from a table of 1024 points of the turn and the
 // series of the remainder r < 2^-8:
 //   cos(t + r) = C - (S sin r + C (1 - cos r)),  sin(t + r) = S + (C sin r - S (1 - cos r))
-// and the products' errors from fused multiply-adds (Dekker's and Knuth's exact
-// sums).  The queries take the high parts alone, with fp32's error.
+// (Knuth's exact sum).  cos and sin are handed on as 16 bits and the rest: products
+// of the 16 bits with a bf16 value are exact in fp32.  The queries take the whole cos and
+// sin, with fp32's error.
 //
-// Read.  A thread takes 8 values of a row: 4 bytes of codes, one scale, 16
-// bytes out; scale * code is exact.
+// Append's bound: bytes, (2 Hq + 2 Hkv) 256 + 144 Hkv a token.  32768 tokens of 64 + 8 + 8
+// heads (1.21 GB): 192 us, 6.3 TB/s, 93 % of a copy's rate; issue slots 66 % (a
+// key's rotation and quantising take 9 times a query's instructions).  What that took: a thread's
+// units (two 16-byte chunks of a head) are copied into a ring of its own ahead of
+// their use, so that the loads go on under a key's arithmetic (245 us with loads a
+// loop ahead in registers), queries, keys and values in loops of their own (565 us in
+// one, with the angles read from shared memory), no division, one barrier a tile, and 80
+// registers (64 spill: 253 us; two blocks of 128 an SM: 199).
 //
-// Bound: bytes.
+// Read.  A thread takes two chunks of 8 values of a row, 4 bytes of codes, a scale and
+// 16 bytes out each, of two rows at a time; scale * code is exact.  Bound: bytes, 656
+// a token and KV head.  131072 tokens, 8 KV heads (688 MB): 108 us, 6.4 TB/s, 94 % of a
+// copy's rate; 16 contexts of up to 5003 tokens, 2 KV heads: 11.6 us.  With a
+// chunk a thread, four rows at a time: 119 and 12.2.
 #include "kv4.cuh"
 #include "internal.h"
 
@@ -423,10 +434,10 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const AppendArg
 }
 
 constexpr int kReadTok = 32;     // tokens of a read block's tile
-constexpr int kRowLanes = 16;    // threads of a row: 8 values each
-constexpr int kReadRows = kThreads / kRowLanes;   // rows of a pass
+constexpr int kRowLanes = 8;     // threads of a row: chunks c and c + 8 of 8 values each
+static_assert(kThreads / kRowLanes == kReadTok, "a pass has a row of every token of the tile");
 constexpr int kReadBlocks = 6;   // blocks of an SM
-constexpr int kReadBatch = 4;    // rows whose loads a thread has in flight
+constexpr int kReadBatch = 2;     // rows whose loads a thread has in flight
 
 struct ReadArgs {
   Kv4Cache kv;
@@ -446,38 +457,47 @@ struct ReadArgs {
 __device__ __forceinline__ void read_rows(const Kv4Cache& kv, int Hkv, const int64_t* row0, int64_t head_rows, uint16_t* K_out,
                                           int64_t k_token, int64_t k_head, uint16_t* V_out, int64_t v_token, int64_t v_head,
                                           int zeros) {
-  const int tid = threadIdx.x, c = tid & (kRowLanes - 1);
-  // passes of 16 tokens of one head and side: keys and values of a head, the tile's halves
-  const int passes = 2 * (kReadTok / kReadRows) * Hkv;
-  for (int i0 = 0; i0 < passes; i0 += kReadBatch) {
-    uint32_t w[kReadBatch], sf[kReadBatch];
+  const int c = threadIdx.x & (kRowLanes - 1), tk = threadIdx.x / kRowLanes;
+  const int64_t row = row0[tk];
+  if (row < zeros) return;
+  const bool there = row >= 0;
+  // keys and values of a head in turn
+  const int64_t from = max(row, int64_t(0));
+  for (int i0 = 0; i0 < 2 * Hkv; i0 += kReadBatch) {
+    uint32_t w[kReadBatch][2], sf[kReadBatch][2];
 #pragma unroll
     for (int k = 0; k < kReadBatch; ++k) {
-      const int i = i0 + k, side = i & 1, g = i >> 2;
-      const int64_t row = row0[tid / kRowLanes + (i >> 1 & 1) * kReadRows];
-      w[k] = sf[k] = 0;
-      if (i < passes && row >= 0) {
-        const int64_t r = row + g * head_rows;
-        w[k] = __ldg(reinterpret_cast<const uint32_t*>((side ? kv.V : kv.K) + r * kKv4Codes) + c);
-        sf[k] = __ldg((side ? kv.V_sf : kv.K_sf) + r * kKv4Groups + (c >> 1));
+      const int side = k & 1, g = (i0 + k) >> 1;
+      w[k][0] = w[k][1] = sf[k][0] = sf[k][1] = 0;
+      if (there && i0 + k < 2 * Hkv) {
+        const int64_t r = from + g * head_rows;
+        const uint32_t* codes = reinterpret_cast<const uint32_t*>((side ? kv.V : kv.K) + r * kKv4Codes) + c;
+        const uint8_t* scales = (side ? kv.V_sf : kv.K_sf) + r * kKv4Groups + (c >> 1);
+        w[k][0] = __ldg(codes);
+        w[k][1] = __ldg(codes + 8);
+        sf[k][0] = __ldg(scales);
+        sf[k][1] = __ldg(scales + 4);
       }
     }
 #pragma unroll
     for (int k = 0; k < kReadBatch; ++k) {
-      const int i = i0 + k, side = i & 1, g = i >> 2, tk = tid / kRowLanes + (i >> 1 & 1) * kReadRows;
-      if (i >= passes || row0[tk] < zeros) continue;
+      const int side = k & 1, g = (i0 + k) >> 1;
+      if (i0 + k >= 2 * Hkv) continue;
       const float f = side ? kv.v_scale : kv.k_scale;
-      const __half2 s = kv4_scales(sf[k] * 0x101u);
-      __half2 h[4];
-      kv4_codes(w[k], h);
-      uint32_t o[4];
+      uint16_t* dst = (side ? V_out + tk * v_token + g * v_head : K_out + tk * k_token + g * k_head) + 8 * c;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 v = __half22float2(__hmul2(h[e], s));
-        o[e] = pack_bf16(v.x * f, v.y * f);
+      for (int half = 0; half < 2; ++half) {
+        const __half2 s = kv4_scales(sf[k][half] * 0x101u);
+        __half2 h[4];
+        kv4_codes(w[k][half], h);
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = __half22float2(__hmul2(h[e], s));
+          o[e] = pack_bf16(v.x * f, v.y * f);
+        }
+        *reinterpret_cast<uint4*>(dst + 64 * half) = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      uint16_t* dst = side ? V_out + tk * v_token + g * v_head : K_out + tk * k_token + g * k_head;
-      *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -491,23 +511,21 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv4_read_kernel(const R
     if (len < 0 || len > a.n_cap) record_error(a.err, kErrBadPage);
   }
   const int64_t head_rows = a.pm.table ? (int64_t(1) << a.pm.page_shift) : a.n_cap;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kReadTok; t0 < a.bt.T; t0 += static_cast<int64_t>(gridDim.x) * kReadTok) {
-    __syncthreads();
-    if (tid < kReadTok) {
-      int64_t row = -1;
-      if (t0 + tid < a.bt.T) {
-        const TokenAt at = token_of(a.bt, t0 + tid);
-        if (at.b >= 0) {
-          if (at.pos >= 0 && at.pos < a.n_cap) row = cache_row(a.pm, at.b, 0, a.Hkv, a.n_cap, at.pos);
-          if (row < 0) record_error(a.err, kErrBadPage);
-        }
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kReadTok;
+  if (tid < kReadTok) {
+    int64_t row = -1;
+    if (t0 + tid < a.bt.T) {
+      const TokenAt at = token_of(a.bt, t0 + tid);
+      if (at.b >= 0) {
+        if (at.pos >= 0 && at.pos < a.n_cap) row = cache_row(a.pm, at.b, 0, a.Hkv, a.n_cap, at.pos);
+        if (row < 0) record_error(a.err, kErrBadPage);
       }
-      row0[tid] = row;
     }
-    __syncthreads();
-    read_rows(a.kv, a.Hkv, row0, head_rows, a.K_out + t0 * a.k_token, a.k_token, a.k_head, a.V_out + t0 * a.v_token, a.v_token,
-              a.v_head, 0);
+    row0[tid] = row;
   }
+  __syncthreads();
+  read_rows(a.kv, a.Hkv, row0, head_rows, a.K_out + t0 * a.k_token, a.k_token, a.k_head, a.V_out + t0 * a.v_token, a.v_token,
+            a.v_head, 0);
   pdl_trigger();
 }
 
@@ -638,7 +656,7 @@ cudaError_t launch_kv4_append(const qasc_shape& s, const PageMap& pm, const Batc
   // go one to a block, over more SMs.
   a.tok = bt.T >= 4 * dev.num_sms ? kMaxTok : 1;
   const int64_t tiles = (bt.T + a.tok - 1) / a.tok;
-  const int64_t most = static_cast<int64_t>(dev.num_sms) * 6;
+  const int64_t most = static_cast<int64_t>(dev.num_sms) * 12;
   return launch_dependent(kv4_append_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads),
                           kRingBytes, stream, 1, a);
 }
@@ -664,10 +682,10 @@ cudaError_t launch_kv4_read(const qasc_shape& s, const PageMap& pm, const Batch&
   a.Hkv = s.Hkv;
   a.n_cap = s.n_cap;
   a.err = dev.err_word;
+  // a block a tile, so that the device shares them out (six tiles' blocks an SM, each
+  // with every 912th tile: 115 us for 131072 tokens, 108 so)
   const int64_t tiles = (bt.T + kReadTok - 1) / kReadTok;
-  const int64_t most = static_cast<int64_t>(dev.num_sms) * 8;
-  return launch_dependent(kv4_read_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads), 0, stream,
-                          1, a);
+  return launch_dependent(kv4_read_kernel, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), 0, stream, 1, a);
 }
 
 cudaError_t launch_kv4_copy(const qasc_shape& s, const PageMap& pm, const Batch& bt, const Kv4Cache& kv, int32_t sink,
@@ -684,7 +702,7 @@ cudaError_t launch_kv4_copy(const qasc_shape& s, const PageMap& pm, const Batch&
   a.local = local;
   a.n_cap = s.n_cap;
   a.err = dev.err_word;
-  const int64_t tiles = c.capacity * (kCopyPage / kReadTok), most = static_cast<int64_t>(dev.num_sms) * 8;
+  const int64_t tiles = c.capacity * (kCopyPage / kReadTok), most = static_cast<int64_t>(dev.num_sms) * kReadBlocks;
   return launch_dependent(kv4_copy_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads), 0, stream,
                           1, a);
 }
