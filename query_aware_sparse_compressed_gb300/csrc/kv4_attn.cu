@@ -220,9 +220,9 @@ struct Line {
   __device__ __forceinline__ int start(unsigned c) const { return static_cast<int>(c * q + (G == 1 ? 0 : __umulhi(c * r, inv))); }
   // The block that holds place x.
   __device__ __forceinline__ int block(int x) const {
-    int c = min(static_cast<int>(__fdividef(static_cast<float>(x) * static_cast<float>(G), static_cast<float>(U))), static_cast<int>(G) - 1);
-    while (start(c) > x) --c;
-    while (start(c + 1) <= x) ++c;
+    int c = clampi(static_cast<int>(__fdividef(static_cast<float>(x) * static_cast<float>(G), static_cast<float>(U))), 0, G - 1);
+    while (c > 0 && start(c) > x) --c;
+    while (c + 1 < static_cast<int>(G) && start(c + 1) <= x) ++c;
     return c;
   }
 };
@@ -321,20 +321,26 @@ __device__ __forceinline__ int token_of_slot(const Args& p, const Piece& pc, int
 }
 
 // The item that holds place x, of sequence b or a later one; `at` places stand before b.
+// (Offsets of new tokens that do not ascend can make a line of more than 2^32 places: sums
+// wrap then, and a place may belong to no item, w.b == p.seqs, but to none outside
+// its sequence.)
 template <bool kList, int kRows>
-__device__ __forceinline__ Walk walk_from(const Args& p, int b, int at, int x) {
+__device__ __forceinline__ Walk walk_from(const Args& p, int b, unsigned at, unsigned x) {
   Walk w;
-  for (w.b = b;; ++w.b) {
+  w.rem = w.x0 = 0;
+  for (w.b = b; w.b < p.seqs; ++w.b) {
     w.s = seq_of<kList>(p, w.b);
     w.items = items_of<kList, kRows>(p, w.s, w.b);
     if (w.items == 0) continue;
     w.span = span_of<kList, kRows>(p, w.s, w.b);
-    const int all = w.items * w.span;
-    if (x < at + all) break;
+    const unsigned all = static_cast<unsigned>(w.items) * static_cast<unsigned>(w.span);
+    if (x - at < all) {
+      w.rem = (x - at) / static_cast<unsigned>(w.span);
+      w.x0 = at + w.rem * w.span;
+      break;
+    }
     at += all;
   }
-  w.rem = static_cast<unsigned>(x - at) / static_cast<unsigned>(w.span);
-  w.x0 = at + w.rem * w.span;
   return w;
 }
 
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
   constexpr int kLaneSeq = 4;
   const bool short_line = p.seqs <= 32 * kLaneSeq;
   const int each_lane = (p.seqs + 31) / 32;
-  int lane_places = 0, lane_before = 0;   // of the lane's sequences, and before them
+  unsigned lane_places = 0, lane_before = 0;   // of the lane's sequences, and before them
   int places = p.B * p.Hkv;
   if (!plain && short_line) {
 #pragma unroll
@@ -473,51 +479,51 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
       if (i < each_lane && b < p.seqs) {
         const Seq s = seq_of<kList>(p, b);
         const int items = items_of<kList, kRows>(p, s, b);
-        if (items > 0) lane_places += items * span_of<kList, kRows>(p, s, b);
+        if (items > 0) lane_places += static_cast<unsigned>(items) * span_of<kList, kRows>(p, s, b);
       }
     }
-    int inc = lane_places;
+    unsigned inc = lane_places;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      const unsigned x = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += x;
     }
     lane_before = inc - lane_places;
-    places = __shfl_sync(0xffffffffu, inc, 31);
+    places = static_cast<int>(__shfl_sync(0xffffffffu, inc, 31));
   } else if (!plain) {
     for (int i = tid; i < groups; i += kThreads) {
-      int sum = 0;
+      unsigned sum = 0;
       for (int b = i << p.ssh; b < min(p.seqs, (i + 1) << p.ssh); ++b) {
         const Seq s = seq_of<kList>(p, b);
         const int items = items_of<kList, kRows>(p, s, b);
-        if (items > 0) sum += items * span_of<kList, kRows>(p, s, b);
+        if (items > 0) sum += static_cast<unsigned>(items) * span_of<kList, kRows>(p, s, b);
       }
-      S.place[i] = sum;
+      S.place[i] = static_cast<int>(sum);
     }
     __syncthreads();
     if (warp == 0) {
-      int sum = 0;
+      unsigned sum = 0;
       for (int b0 = 0; b0 < groups; b0 += 32) {
         const int b = b0 + lane;
-        const int v = b < groups ? S.place[b] : 0;
-        int vi = v;
+        const unsigned v = b < groups ? S.place[b] : 0;
+        unsigned vi = v;
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, vi, o);
+          const unsigned x = __shfl_up_sync(0xffffffffu, vi, o);
           if (lane >= o) vi += x;
         }
-        if (b < groups) S.place[b] = sum + vi - v;
+        if (b < groups) S.place[b] = static_cast<int>(sum + vi - v);
         sum += __shfl_sync(0xffffffffu, vi, 31);
       }
-      if (lane == 0) S.place[groups] = sum;
+      if (lane == 0) S.place[groups] = static_cast<int>(sum);
     }
     __syncthreads();
     places = S.place[groups];
   }
   auto walk_at = [&](int x) {   // the item that holds place x
     if (short_line) {
-      const unsigned here = __ballot_sync(0xffffffffu, lane_before <= x && x < lane_before + lane_places);
-      const int from = __ffs(here) - 1;
+      const unsigned here = __ballot_sync(0xffffffffu, static_cast<unsigned>(x) - lane_before < lane_places);
+      const int from = max(__ffs(here) - 1, 0);
       return walk_from<kList, kRows>(p, from * each_lane, __shfl_sync(0xffffffffu, lane_before, from), x);
     }
     int lo = 0, hi = groups;   // the last group with place <= x

@@ -830,6 +830,37 @@ def test_window_over_a_copy(Hq, Hkv, P, ql, lens, sink, local):
     assert bool((out[T:] == CANARY).all()) and bool((lse[T:] == CANARY).all())
 
 
+def test_window_over_a_copy_of_a_contiguous_cache():
+    Hq, Hkv, ql, lens, n_cap, sink, local = 64, 8, [300, 2, 140], [900, 70, 333], 960, 4, 500
+    T = sum(ql)
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    pages = Pages4(lens, Hkv, 64, n_cap // 64, seed=63, random=True)
+    assert goes_over_a_copy(T, 3, Hq, Hkv, n_cap, local, sink, max(ql))
+    q = rand((T, Hq, 128), 64, 0.3)
+    out, lse = outputs(T, Hq)
+    c, ln = batch_tensors(cu, lens)
+    qasc.kv4_window_attn(q.cuda(), pages.contiguous(n_cap), ln, out, window_ws(T, 3, Hq, Hkv, n_cap, local, sink, max(ql)),
+                         sink=sink, local=local, cu_q=c, max_q=max(ql), lse=lse)
+    qasc.qasc_device_error()
+    tokens = [0, 150, 299, 300, 301, 302, T - 1]
+    ref = osv.window_attention(f64(q), pages.values(0), pages.values(1), cu, lens, sink, local, tokens=tokens)
+    check_rows(out, lse, ref, max(lens), 6.0, rows=tokens, p=p_error(ql, Hq // Hkv))
+
+
+@pytest.mark.parametrize("local,max_q", [(2000, 6), (2000, None), (100, 6)])
+def test_window_offsets_that_do_not_ascend(local, max_q):
+    """Each sequence as its own two offsets say; a token that two of them have is one's or the other's."""
+    cu, lens, Hq, Hkv = [0, 5, 3, 9, 9], [1500, 50, 1700, 80], 8, 2
+    pages = Pages4(lens, Hkv, 64, 27, seed=65, random=True)
+    q = rand((9, Hq, 128), 66)
+    out, lse = window(q, pages, cu, lens, 4, local, max_q=max_q)
+    K, V = pages.values(0), pages.values(1)
+    for b, lo, hi, own in ((0, 0, 5, slice(0, 3)), (2, 3, 9, slice(2, 6))):
+        ref = osv.window_attention(f64(q)[lo:hi], K[b:b + 1], V[b:b + 1], [0, hi - lo], [lens[b]], 4, local)
+        rows = list(range(hi - lo))[own]
+        check_rows(out[lo:hi], lse[lo:hi], ref, lens[b], 6.0, rows=rows)
+
+
 def test_window_bad_page_of_a_copied_sequence():
     Hq, Hkv, n, m = 64, 8, 1500, 300
     pages = Pages4([n], Hkv, 64, 24, seed=53, random=True)
