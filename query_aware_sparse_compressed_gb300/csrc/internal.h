@@ -290,6 +290,8 @@ struct KvAttnArgs {
   int64_t cache_rows = 0;        // rows of K and of V
   int32_t sink = 0, local = 0;
   int64_t n_prefix = 0;
+  bool skip_empty = false;       // (with cu_q) rows of sequences without a cached token are left as they are,
+  int seqs = 0;                  // and about as many sequences have some (0: all)
   int64_t stall = -1;            // self-test (>= 0): the tile at this place of each block's ring never comes,
   unsigned long long wait_ns = 0;   // and waits give up after this time
 };
@@ -334,6 +336,9 @@ struct Kv4Copy {
   int32_t* table = nullptr;        // [B][pages_per_seq]
   uint16_t* K = nullptr;           // [capacity][Hkv][kCopyPage][d]
   uint16_t* V = nullptr;
+  // The copy needs nothing of the kernel launched before it, which lets it start once its own
+  // blocks have waited for what went before.
+  bool beside = false;
 };
 cudaError_t launch_kv4_copy(const qasc_shape& s, const PageMap& pm, const Batch& bt, const Kv4Cache& kv, int32_t sink,
                             int32_t local, const Kv4Copy& c, const DeviceInfo& dev, cudaStream_t stream);

@@ -18,6 +18,14 @@ constexpr int kKv4Group = 16;                    // values of a scale
 constexpr int kKv4Groups = kD / kKv4Group;       // scales of a row, bytes
 constexpr int kKv4Codes = kD / 2;                // bytes of a row's codes
 
+// Tokens of a sequence of `len` that its newest ql attend to, sink and window, and
+// how many in between none of them does.
+__device__ __forceinline__ int kv4_tokens_seen(int64_t len, int64_t ql, int sink, int local, int* between) {
+  const int64_t lo = max(len - ql - local + 1, int64_t(0));   // the first row's window
+  *between = static_cast<int>(max(lo - sink, int64_t(0)));
+  return static_cast<int>(len) - *between;
+}
+
 // Two e4m3 of a word's low 16 bits -> fp16 pair (exact).
 __device__ __forceinline__ __half2 kv4_scales(uint32_t two) {
   uint32_t h;

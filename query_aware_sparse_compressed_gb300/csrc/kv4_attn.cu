@@ -85,12 +85,24 @@ constexpr int kQueue = 8;                      // items that a warp's loads are 
 constexpr int kItemCost = 2;                   // places of an item beside its tiles: queries, output (4: 2 % more)
 constexpr int kTokensMost = 1 << 24;           // above n_cap, and sink and local as the kernel has them
 constexpr int kTilesMost = kTokensMost / kTile;
+// Sequences of more rows than this take their keys and values from a bf16 copy and
+// go to kv_window_attn's kernel, whose products are tcgen05's: a row block here costs
+// what it costs whether the next one needs the same keys or not.  One sequence of
+// 32768 tokens, 32 heads, 8 KV heads, here and over a copy: 64 rows 45 and 75 us,
+// 128 rows 78 and 79, 256 rows 143 and 88; 32 sequences of 4096, 64 heads, 128 rows: 283 and 261.
+constexpr int64_t kCopyRows = 128;
 constexpr int kLeast = 8;                      // places that a block takes at least
-constexpr int kWholeTokens = 1024;             // an item of more tokens may be shared between blocks
+// Items of more tokens than this may be shared between blocks; with more items than warps those
+// of more than the second.  (256 sequences of one token, 8 KV heads, 1000 tokens each: 84 us as whole
+// items, 69 shared; 200: 55 and 57; 400 of 260 tokens: 42 and 45.)
+constexpr int kWholeTokens = 1024, kWholeMany = 288;
 constexpr float kBase = 10.0f;                 // log2 of P at the maximum that the base was taken from
 constexpr float kGrow = 5.0f;                  // growth of the maximum that moves the base
 // log2(e) / sqrt(128): logits in base-2 units.
 constexpr float kScale = 1.4426950408889634f * 0.08838834764831845f;
+
+// Window calls; what they have beside a copy of all sequences of many rows; listed ones.
+enum Kind { kWindow, kRest, kListed };
 
 struct Args {
   Kv4AttnArgs a;
@@ -98,7 +110,8 @@ struct Args {
   int seqs;                 // sequences of the line: B, or (listed) the KV heads of all
   int64_t n_cap;
   int n, sink_end, local_start;   // listed: tokens of every sequence, its regions
-  const int32_t* copied;    // [B] not 0: a sequence that is left out here (NULL: none)
+  const int32_t* copied;    // [B] not 0: a sequence that is left out here (NULL: none of these)
+  int64_t copy_tokens;      // kRest: sequences of more than kCopyRows rows that see 1 to as many tokens are left out
   int whole;                // items are not shared between blocks
   int ssh;                  // sequences of a sum: 2^ssh
   int ush;                  // tiles of a place: 2^ush, so that the line has fewer than 2^31 places
@@ -184,11 +197,16 @@ __device__ __forceinline__ int list_len(const Args& p, int b, int g) {
 
 // Items of a sequence (row blocks times KV heads) and the places of each: the
 // most tiles that any of them has (whole items: one).
-template <bool kList, int kRows>
+template <int kKind, int kRows>
 __device__ __forceinline__ int items_of(const Args& p, const Seq& s, int b) {
-  if (kList) return 1;
+  if (kKind == kListed) return 1;
   const int64_t rows = static_cast<int64_t>(s.ql) << p.gsh;
-  if (p.copied && __ldcg(p.copied + b)) return 0;
+  if (kKind == kWindow && p.copied && __ldcg(p.copied + b)) return 0;
+  if (kKind == kRest && rows > kCopyRows) {
+    int between;
+    const int tokens = kv4_tokens_seen(s.len, s.ql, p.a.sink, p.a.local, &between);
+    if (tokens > 0 && tokens <= p.copy_tokens) return 0;
+  }
   return static_cast<int>((rows + kRows - 1) / kRows) * p.Hkv;
 }
 template <bool kList, int kRows>
@@ -324,13 +342,14 @@ __device__ __forceinline__ int token_of_slot(const Args& p, const Piece& pc, int
 // (Offsets of new tokens that do not ascend can make a line of more than 2^32 places: sums
 // wrap then, and a place may belong to no item, w.b == p.seqs, but to none outside
 // its sequence.)
-template <bool kList, int kRows>
+template <int kKind, int kRows>
 __device__ __forceinline__ Walk walk_from(const Args& p, int b, unsigned at, unsigned x) {
+  constexpr bool kList = kKind == kListed;
   Walk w;
   w.rem = w.x0 = 0;
   for (w.b = b; w.b < p.seqs; ++w.b) {
     w.s = seq_of<kList>(p, w.b);
-    w.items = items_of<kList, kRows>(p, w.s, w.b);
+    w.items = items_of<kKind, kRows>(p, w.s, w.b);
     if (w.items == 0) continue;
     w.span = span_of<kList, kRows>(p, w.s, w.b);
     const unsigned all = static_cast<unsigned>(w.items) * static_cast<unsigned>(w.span);
@@ -345,14 +364,15 @@ __device__ __forceinline__ Walk walk_from(const Args& p, int b, unsigned at, uns
 }
 
 // The next item (w.b == p.seqs behind the last).
-template <bool kList, int kRows>
+template <int kKind, int kRows>
 __device__ __forceinline__ void walk_on(const Args& p, Walk& w) {
+  constexpr bool kList = kKind == kListed;
   w.x0 += w.span;
   if (++w.rem < w.items) return;
   w.rem = 0;
   while (++w.b < p.seqs) {
     w.s = seq_of<kList>(p, w.b);
-    w.items = items_of<kList, kRows>(p, w.s, w.b);
+    w.items = items_of<kKind, kRows>(p, w.s, w.b);
     if (w.items == 0) continue;
     w.span = span_of<kList, kRows>(p, w.s, w.b);
     return;
@@ -405,8 +425,9 @@ __device__ __forceinline__ Piece piece_of(const Args& p, const Walk& w) {
 
 // Puts the next item of a warp's range into `to`: 0 where there is none, 1 for the
 // last, else 2.  Items without a token are written on the way.
-template <int kNT, bool kList>
+template <int kNT, int kKind>
 __device__ __forceinline__ int next_piece(const Args& p, Smem<kNT>& S, int warp, Piece& to) {
+  constexpr bool kList = kKind == kListed;
   constexpr int kRows = 8 * kNT;
   const int lane = threadIdx.x & 31;
   Walk walk = S.walk[warp];
@@ -418,7 +439,7 @@ __device__ __forceinline__ int next_piece(const Args& p, Smem<kNT>& S, int warp,
     if (walk.used) {
       if (!more()) break;
       --walk.left;
-      walk_on<kList, kRows>(p, walk);
+      walk_on<kKind, kRows>(p, walk);
     }
     if (walk.b >= p.seqs) break;
     walk.used = 1;
@@ -446,15 +467,17 @@ __device__ __forceinline__ int next_piece(const Args& p, Smem<kNT>& S, int warp,
   return found ? 1 + more() : 0;
 }
 
-template <int kNT, bool kList>
+template <int kNT, int kKind>
 __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const __grid_constant__ Args p) {
   using Sm = Smem<kNT>;
+  constexpr bool kList = kKind == kListed;
   constexpr int kRows = Sm::kRows, kWarps = Sm::kWarps, kThreads = 32 * kWarps, kStages = Sm::kStages;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Sm& S = *reinterpret_cast<Sm*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, j = lane & 3;
   pdl_wait();
+  if (kKind == kRest && p.whole) pdl_trigger();   // the copy begins beside it
 
   // ---- this warp's part of the work.  Whole items of single tokens need no sums.
   const int groups = (p.seqs + (1 << p.ssh) - 1) >> p.ssh;
@@ -478,7 +501,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
       const int b = lane * each_lane + i;
       if (i < each_lane && b < p.seqs) {
         const Seq s = seq_of<kList>(p, b);
-        const int items = items_of<kList, kRows>(p, s, b);
+        const int items = items_of<kKind, kRows>(p, s, b);
         if (items > 0) lane_places += static_cast<unsigned>(items) * span_of<kList, kRows>(p, s, b);
       }
     }
@@ -495,7 +518,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
       unsigned sum = 0;
       for (int b = i << p.ssh; b < min(p.seqs, (i + 1) << p.ssh); ++b) {
         const Seq s = seq_of<kList>(p, b);
-        const int items = items_of<kList, kRows>(p, s, b);
+        const int items = items_of<kKind, kRows>(p, s, b);
         if (items > 0) sum += static_cast<unsigned>(items) * span_of<kList, kRows>(p, s, b);
       }
       S.place[i] = static_cast<int>(sum);
@@ -524,7 +547,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
     if (short_line) {
       const unsigned here = __ballot_sync(0xffffffffu, static_cast<unsigned>(x) - lane_before < lane_places);
       const int from = max(__ffs(here) - 1, 0);
-      return walk_from<kList, kRows>(p, from * each_lane, __shfl_sync(0xffffffffu, lane_before, from), x);
+      return walk_from<kKind, kRows>(p, from * each_lane, __shfl_sync(0xffffffffu, lane_before, from), x);
     }
     int lo = 0, hi = groups;   // the last group with place <= x
     while (hi - lo > 1) {
@@ -532,7 +555,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
       if (S.place[mid] <= x) lo = mid;
       else hi = mid;
     }
-    return walk_from<kList, kRows>(p, lo << p.ssh, S.place[lo], x);
+    return walk_from<kKind, kRows>(p, lo << p.ssh, S.place[lo], x);
   };
   const Line line(places, max(1, min(static_cast<int>(gridDim.x), p.whole ? places : (places + kLeast - 1) / kLeast)));
   Walk walk;
@@ -597,7 +620,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
   auto next_tokens = [&]() {
     if (__builtin_expect(left == 0, 0)) {
       Piece& pc = S.queue[warp][pushed % kQueue];
-      const int found = more ? next_piece<kNT, kList>(p, S, warp, pc) : 0;
+      const int found = more ? next_piece<kNT, kKind>(p, S, warp, pc) : 0;
       more = found == 2;
       if (found == 0) {
         tok_kind = kNone;
@@ -1080,9 +1103,9 @@ Layout layout_of(int rows, int grid) {
 }
 
 using Kernel = void (*)(Args);
-Kernel kernel_of(int nt, bool list) {
-  if (nt == 1) return list ? kv4_attn_kernel<1, true> : kv4_attn_kernel<1, false>;
-  return kv4_attn_kernel<2, false>;
+Kernel kernel_of(int nt, Kind kind) {
+  if (nt == 1) return kind == kListed ? kv4_attn_kernel<1, kListed> : (kind == kRest ? kv4_attn_kernel<1, kRest> : kv4_attn_kernel<1, kWindow>);
+  return kv4_attn_kernel<2, kWindow>;
 }
 Kernel merge_of(int nt) { return nt == 1 ? kv4_merge_kernel<1> : kv4_merge_kernel<2>; }
 size_t smem_of(int nt) { return nt == 1 ? sizeof(Smem<1>) : sizeof(Smem<2>); }
@@ -1091,27 +1114,27 @@ static_assert(sizeof(Smem<1>) <= 232448 && sizeof(Smem<2>) <= 232448, "shared me
 // Columns of an item: single tokens have at most eight.
 int tiles_of(const qasc_shape& s, int64_t max_q) { return max_q * (s.Hq / s.Hkv) <= 8 ? 1 : 2; }
 
-// Sequences of more rows than this take their keys and values from a bf16 copy and
-// go to kv_window_attn's kernel, whose products are tcgen05's: a row block here costs
-// what it costs whether the next one needs the same keys or not.  One sequence of
-// 32768 tokens, 32 heads, 8 KV heads, here and over a copy: 64 rows 45 and 75 us,
-// 128 rows 78 and 79, 256 rows 143 and 88; 32 sequences of 4096, 64 heads, 128 rows: 283 and 261.
-constexpr int64_t kCopyRows = 128;
 constexpr int64_t kCopyBytes = int64_t(1) << 32;   // of a copy, at most
 
+// Sequences of a call that are copied, of `seqs` that may be: they are taken to have two thirds
+// of max_q new tokens.
+double copies_of(int64_t T, int64_t max_q, int64_t seqs) { return std::min<double>(seqs, std::max(1.0, 1.5 * T / max_q)); }
+
 // Whether the copy pays for a call that may have such sequences (microseconds, from
-// the same runs): it is two kernels more and its bytes; here every block of 16 rows
-// takes 1.05 ns a tile on 152 SMs.  8 sequences of 64 tokens over a window of 1000, 8 heads, 2
-// KV heads: 21 us here, 31 over a copy; of 257 tokens 49 and 32.
-bool copy_pays(const qasc_shape& s, int64_t T, int64_t tokens, int64_t seqs) {
-  const double gq = s.Hq / s.Hkv, keys = static_cast<double>(tokens) * s.Hkv;
-  const double here = 10.0 + (T * gq / 16.0 + 1.0) * keys / kTile * 1.05e-3;
-  const double copy = 27.0 + seqs * keys * 656.0 / 5.5e6 + T * gq * keys * 512.0 / 1.4e9;
+// the same runs): it is two kernels more, its bytes, and the products over it; here every block
+// of 16 rows takes 1.05 ns a tile that its rows see on 152 SMs.
+bool copy_pays(const qasc_shape& s, int64_t T, int64_t max_q, int64_t tokens, int64_t seqs, int64_t window) {
+  const double gq = s.Hq / s.Hkv, rows = T * gq, copies = copies_of(T, max_q, seqs);
+  const double seen = std::min<int64_t>(tokens, window + 15), seen256 = std::min<double>(tokens, window + 255 / gq);
+  const double here = 10.0 + (rows / 16.0 + 1.0) * seen * s.Hkv / kTile * 1.05e-3;
+  const double copy = 23.0 + copies * tokens * s.Hkv * 656.0 / 5.5e6 + rows * seen256 * s.Hkv * 512.0 / 1.4e9;
   return copy < here;
 }
 
 struct CopyLayout {
   int64_t capacity = 0, pages_per_seq = 0;   // capacity 0: no copy
+  int64_t seqs = 0;                          // sequences that can be long enough
+  bool all = false;                          // there is room for every sequence that is long enough
   size_t off_lists = 0, off_attn = 0, attn_bytes = 0, off_k = 0, off_v = 0, total = 0;
 };
 // Of a call whose sequences have at most max_q new tokens.
@@ -1125,10 +1148,12 @@ CopyLayout copy_layout(const qasc_shape& s, int64_t T, int64_t max_q, int32_t si
   const int64_t cap = L.pages_per_seq * kCopyPage;
   if (cap >= kTokensMost || static_cast<int64_t>(s.B) * s.Hkv * cap >= (int64_t(1) << 31)) return L;
   const int64_t seqs = std::min<int64_t>(s.B, T * gq / (kCopyRows + 1));   // that can be as long
-  if (!copy_pays(s, T, tokens, seqs)) return L;
+  if (!copy_pays(s, T, max_q, tokens, seqs, static_cast<int64_t>(sink) + local)) return L;
   const int64_t page_bytes = static_cast<int64_t>(s.Hkv) * kCopyPage * kD * 2;
   const int64_t most = std::min(kCopyBytes / (2 * page_bytes), ((int64_t(1) << 31) - 1) / (s.Hkv * kCopyPage));
   L.capacity = std::min(seqs * L.pages_per_seq, most);
+  L.seqs = seqs;
+  L.all = L.capacity == seqs * L.pages_per_seq;
   L.off_lists = align_up(L.total, 256);
   L.off_attn = align_up(L.off_lists + static_cast<size_t>(s.B) * (2 + L.pages_per_seq) * sizeof(int32_t), 256);
   L.attn_bytes = kv_attn_workspace_bytes(T, s.B, s.Hq, s.Hkv, false, kMaxSmsForSizing);
@@ -1136,6 +1161,44 @@ CopyLayout copy_layout(const qasc_shape& s, int64_t T, int64_t max_q, int32_t si
   L.off_v = L.off_k + static_cast<size_t>(L.capacity * page_bytes);
   L.total = L.off_v + static_cast<size_t>(L.capacity * page_bytes);
   return L;
+}
+
+// The sequences that are copied: their copy, and kv_window_attn's kernel over it.
+int attend_over_copy(const qasc_shape& s, const Kv4AttnArgs& a, const Args& p, const CopyLayout& C, uint8_t* ws,
+                     const DeviceInfo& dev, cudaStream_t stream) {
+  Kv4Copy c;
+  c.most_rows = kCopyRows;
+  c.capacity = C.capacity;
+  c.pages_per_seq = C.pages_per_seq;
+  c.copied = reinterpret_cast<int32_t*>(ws + C.off_lists);
+  c.lens = c.copied + s.B;
+  c.table = c.lens + s.B;
+  c.K = reinterpret_cast<uint16_t*>(ws + C.off_k);
+  c.V = reinterpret_cast<uint16_t*>(ws + C.off_v);
+  c.beside = C.all && p.whole;
+  const cudaError_t e = launch_kv4_copy(s, a.pm, a.bt, a.kv, p.a.sink, p.a.local, c, dev, stream);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  qasc_shape s2 = s;
+  s2.n = s2.n_cap = C.pages_per_seq * kCopyPage;
+  KvAttnArgs k;
+  k.q = a.q;
+  k.K = c.K;
+  k.V = c.V;
+  k.out = a.out;
+  k.lse = a.lse;
+  k.bt = a.bt;
+  k.bt.lens = c.lens;
+  k.skip_empty = true;   // those that are not copied have no tokens there
+  k.seqs = static_cast<int>(copies_of(a.bt.T, a.max_q, C.seqs) + 0.5);
+  k.pm.table = c.table;
+  k.pm.pages_per_seq = C.pages_per_seq;
+  k.pm.num_pages = C.capacity;
+  while ((1 << k.pm.page_shift) < kCopyPage) ++k.pm.page_shift;
+  k.cache_rows = C.capacity * s.Hkv * kCopyPage;
+  k.sink = a.sink;
+  k.local = a.local;
+  size_t bytes = C.attn_bytes;
+  return launch_kv_attn(s2, k, ws + C.off_attn, &bytes, dev, stream);
 }
 
 }  // namespace
@@ -1167,58 +1230,44 @@ int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, cons
   p.err = dev.err_word;
 
   const CopyLayout C = a.listed ? CopyLayout() : copy_layout(s, a.bt.T, a.max_q, a.sink, a.local);
-  if (C.capacity > 0) {
-    Kv4Copy c;
-    c.most_rows = kCopyRows;
-    c.capacity = C.capacity;
-    c.pages_per_seq = C.pages_per_seq;
-    c.copied = reinterpret_cast<int32_t*>(ws + C.off_lists);
-    c.lens = c.copied + s.B;
-    c.table = c.lens + s.B;
-    c.K = reinterpret_cast<uint16_t*>(ws + C.off_k);
-    c.V = reinterpret_cast<uint16_t*>(ws + C.off_v);
-    const cudaError_t e = launch_kv4_copy(s, a.pm, a.bt, a.kv, p.a.sink, p.a.local, c, dev, stream);
-    if (e != cudaSuccess) return static_cast<int>(e);
-    // The copied sequences; rows of the others come out as those of sequences without a
-    // token, and are written again below.
-    qasc_shape s2 = s;
-    s2.n = s2.n_cap = C.pages_per_seq * kCopyPage;
-    KvAttnArgs k;
-    k.q = a.q;
-    k.K = c.K;
-    k.V = c.V;
-    k.out = a.out;
-    k.lse = a.lse;
-    k.bt = a.bt;
-    k.bt.lens = c.lens;
-    k.pm.table = c.table;
-    k.pm.pages_per_seq = C.pages_per_seq;
-    k.pm.num_pages = C.capacity;
-    while ((1 << k.pm.page_shift) < kCopyPage) ++k.pm.page_shift;
-    k.cache_rows = C.capacity * s.Hkv * kCopyPage;
-    k.sink = a.sink;
-    k.local = a.local;
-    size_t bytes = C.attn_bytes;
-    const int rc = launch_kv_attn(s2, k, ws + C.off_attn, &bytes, dev, stream);
-    if (rc != 0) return rc;
-    p.copied = c.copied;
-  }
-
   const int64_t gq = s.Hq / s.Hkv;
   // What a call with long sequences leaves is likely to be single tokens.
   const int nt = a.listed || C.capacity > 0 ? 1 : tiles_of(s, a.max_q);
   const int64_t blocks = (a.bt.T * gq + 8 * nt - 1) / (8 * nt) + s.B;   // row blocks of a KV head, at most
   while (blocks * s.Hkv * (((s.n_cap / kTile + 2) >> p.ush) + 1 + kItemCost) >= (int64_t(1) << 31)) ++p.ush;
-  // Items of few tiles are not shared between blocks, which saves the merge.
+  // Items of few tiles are not shared between blocks, which saves the merge, where no warp has
+  // to take a second one.
   const int64_t most = a.listed ? p.sink_end + static_cast<int64_t>(a.K) + (p.n - p.local_start)
                                 : std::min<int64_t>(s.n_cap, static_cast<int64_t>(p.a.local) + p.a.sink + 8 * nt / gq - 1);
-  p.whole = most <= kWholeTokens;
   const int grid = dev.num_sms;
+  const bool packed = !a.listed && a.bt.cu_q && C.capacity == 0;
+  const int64_t items = (packed ? a.bt.T * gq / (8 * nt) + (s.B + 1) / 2 : s.B) * s.Hkv;   // about
+  p.whole = most <= (items <= static_cast<int64_t>(grid) * warps_of(nt) ? kWholeTokens : kWholeMany);
   const Layout L = layout_of(8 * nt, grid);
   p.share = reinterpret_cast<Share*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);
   p.part_o = reinterpret_cast<float*>(ws + L.off_o);
-  cudaError_t e = launch_dependent(kernel_of(nt, a.listed), dim3(grid), dim3(32 * warps_of(nt)), smem_of(nt), stream, 1, p);
+  const Kind kind = a.listed ? kListed : (C.all ? kRest : kWindow);
+  auto attend = [&]() {
+    return launch_dependent(kernel_of(nt, kind), dim3(grid), dim3(32 * warps_of(nt)), smem_of(nt), stream, 1, p);
+  };
+  // Of a call with a copy the rest goes first, where no plan has to tell which sequences found
+  // room (31 single tokens beside 512 new ones, 8192 cached, 64 / 8 heads: 178 us, 266 when
+  // the copied ones went first and took the others for sequences without a token).  Where items
+  // are short, most SMs have none and the copy is made on them at the same time (16 ragged
+  // sequences: 31 us, 34.4 one behind the other); where they are long it is kept from an even
+  // spread by those that run (300 new and 40 single tokens, 2048 cached: 71 and 64).
+  p.copy_tokens = C.pages_per_seq * kCopyPage;
+  cudaError_t e = cudaSuccess;
+  if (C.capacity == 0 || C.all) e = attend();
+  if (e == cudaSuccess && C.capacity > 0) {
+    const int rc = attend_over_copy(s, a, p, C, ws, dev, stream);
+    if (rc != 0) return rc;
+    if (!C.all) {
+      p.copied = reinterpret_cast<const int32_t*>(ws + C.off_lists);
+      e = attend();
+    }
+  }
   if (e != cudaSuccess || p.whole) return static_cast<int>(e);
   e = launch_dependent(merge_of(nt), dim3(grid, 8 * nt), dim3(32 * kMergeWarps), 0, stream, 1, p);
   return static_cast<int>(e);
@@ -1227,8 +1276,8 @@ int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, cons
 cudaError_t configure_kv4_kernels(const DeviceInfo& dev) {
   (void)dev;
   for (int nt = 1; nt <= 2; ++nt)
-    for (int list = 0; list < 2; ++list) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel_of(nt, list != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
+    for (Kind kind : {kWindow, kRest, kListed}) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel_of(nt, kind), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  static_cast<int>(smem_of(nt)));
       if (e != cudaSuccess) return e;
     }

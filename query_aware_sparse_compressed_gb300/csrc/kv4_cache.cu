@@ -542,6 +542,8 @@ struct CopyArgs {
 };
 
 constexpr int kCopySeq = 2048;
+constexpr size_t kCopyShared = 216 << 10;   // of an SM, for the blocks that it may have
+constexpr size_t kCopyStatic = 10 << 10;    // of a block beside what it asks for, at least
 
 // Every block makes the plan for itself: which sequences are copied and their
 // first pages (sequences take pages in their order as long as all of theirs
@@ -551,15 +553,13 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv4_copy_kernel(const C
   __shared__ int32_t first[kCopySeq + 1];
   __shared__ int32_t sums[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_wait();
+  if (!a.c.beside) pdl_wait();
   auto shape_of = [&](int b, int* drop) {   // tokens of the copy and those left out behind the sink; 0: not copied
     const int64_t q0 = min(max(a.bt.cu_q ? __ldg(a.bt.cu_q + b) : static_cast<int64_t>(b), int64_t(0)), a.bt.T);
     const int64_t q1 = min(max(a.bt.cu_q ? __ldg(a.bt.cu_q + b + 1) : static_cast<int64_t>(b) + 1, q0), a.bt.T);
     const int64_t len = min(max(static_cast<int64_t>(__ldg(a.bt.lens + b)), int64_t(0)), a.n_cap);
     if (((q1 - q0) << a.gsh) <= a.c.most_rows) return 0;
-    const int64_t lo = max(len - (q1 - q0) - a.local + 1, int64_t(0));   // the first row's window
-    *drop = static_cast<int>(max(lo - a.sink, int64_t(0)));
-    const int tokens = static_cast<int>(len) - *drop;
+    const int tokens = kv4_tokens_seen(len, q1 - q0, a.sink, a.local, drop);
     return tokens <= a.c.pages_per_seq * kCopyPage ? tokens : 0;   // (0: more new tokens than the call said)
   };
   int taken = 0;
@@ -623,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv4_copy_kernel(const C
               static_cast<int64_t>(kCopyPage) * kD, -1);
   }
   pdl_trigger();
+  if (a.c.beside) pdl_wait();   // so that what waits for this kernel waits for the one before as well
 }
 
 }  // namespace
@@ -663,6 +664,9 @@ cudaError_t launch_kv4_append(const qasc_shape& s, const PageMap& pm, const Batc
 
 cudaError_t configure_kv4_cache_kernels(const DeviceInfo& dev) {
   (void)dev;
+  const cudaError_t e = cudaFuncSetAttribute(kv4_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kCopyShared - kCopyStatic));
+  if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(kv4_append_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingBytes));
 }
 
@@ -702,9 +706,13 @@ cudaError_t launch_kv4_copy(const qasc_shape& s, const PageMap& pm, const Batch&
   a.local = local;
   a.n_cap = s.n_cap;
   a.err = dev.err_word;
+  // Beside another kernel blocks go where there is room first, and those with work were all on
+  // few SMs (512 tokens of 8 heads, 16 blocks: 34 us with the attention, 25 spread out): so a block
+  // asks for as much shared memory as leaves none for more than its share of them on an SM.
   const int64_t tiles = c.capacity * (kCopyPage / kReadTok), most = static_cast<int64_t>(dev.num_sms) * kReadBlocks;
-  return launch_dependent(kv4_copy_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads), 0, stream,
-                          1, a);
+  const int64_t grid = tiles < most ? tiles : most, share = (grid + dev.num_sms - 1) / dev.num_sms;
+  return launch_dependent(kv4_copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+                          c.beside ? kCopyShared / static_cast<size_t>(share) - kCopyStatic : 0, stream, 1, a);
 }
 
 }  // namespace qasc

@@ -330,6 +330,7 @@ __device__ __forceinline__ int find_last(const int32_t* arr, int n, int x) {
 }
 
 __device__ __forceinline__ int q_tiles(const Args& p, const Seq& s) {
+  if (p.a.skip_empty && s.len == 0) return 0;
   return ((s.ql << p.gsh) + p.item_rows - 1) / p.item_rows;
 }
 
@@ -1508,7 +1509,7 @@ int launch_kv_attn(const qasc_shape& s, const KvAttnArgs& a, uint8_t* ws, size_t
   p.gsh = gq == 8 ? 3 : (gq == 4 ? 2 : (gq == 2 ? 1 : 0));
   p.n_cap = s.n_cap;
   const bool prefix = a.n_prefix > 0;
-  const Schedule plan = attn_schedule(a, s.B, gq, s.Hkv, s.n_cap, dev.num_sms,
+  const Schedule plan = attn_schedule(a, a.seqs > 0 ? a.seqs : s.B, gq, s.Hkv, s.n_cap, dev.num_sms,
                                       may_split(a.bt.T, s.B, s.Hq, s.Hkv, prefix, dev.num_sms));
   p.split = plan.split;
   p.item_rows = plan.item_rows;

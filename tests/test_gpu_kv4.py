@@ -579,6 +579,26 @@ def test_window_of_many_sequences():
     check_rows(out, lse, ref, 150, 6.0, rows=tokens)
 
 
+@pytest.mark.parametrize("ql,local", [(1, 400), (1, 100), (3, 400)])
+def test_window_of_more_short_items_than_warps(ql, local):
+    """Items of a few hundred tokens, which blocks then share."""
+    B, Hq, Hkv, n = 240, 16, 8, 620
+    pages = Pages4([n], Hkv, 64, 10, seed=69, random=True)
+    pages.table = pages.table.repeat(B, 1)                 # all sequences over the same pages
+    lens = [n - (7 * b) % 300 for b in range(B)]
+    K, V = ([pages.values(side)[0][:, :m] for m in lens] for side in range(2))
+    T, cu = ql * B, list(range(0, ql * B + 1, ql))
+    q = rand((T, Hq, 128), 70)
+    out, lse = outputs(T, Hq)
+    c, ln = batch_tensors(cu if ql > 1 else None, lens)
+    qasc.kv4_window_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), ln, out, window_ws(T, B, Hq, Hkv, 640, local, 4, ql),
+                               local=local, cu_q=c, max_q=ql, lse=lse)
+    qasc.qasc_device_error()
+    tokens = list(range(0, T, 17)) + [T - 1]
+    ref = osv.window_attention(f64(q), K, V, cu, lens, 4, local, tokens=tokens)
+    check_rows(out, lse, ref, n, 6.0, rows=tokens)
+
+
 def test_window_equals_the_bf16_call_on_the_cache_read_back():
     """What kv4_read gives, attended to by kv_window_attn: the same up to both calls' roundings."""
     lens, ql, Hq, Hkv, n_cap = [700, 64], [90, 1], 16, 4, 704
@@ -709,12 +729,12 @@ def test_two_windows_on_two_streams():
 
 def test_two_graphs_take_turns_with_one_workspace():
     """Nothing of a call stays in its workspace: a call shared between blocks, one that is not
-    and one over a copy, captured with the same one and replayed in turn."""
+    and two over a copy, captured with the same one and replayed in turn."""
     Hq, Hkv, P, n = 16, 2, 64, 5000
     pages = Pages4([n, n - 9], Hkv, P, cdiv(n, P), seed=47, random=True)
     kv, table = pages.cache(), pages.table.cuda()
-    kinds = [([0, 1, 2], 2, n, 1), ([0, 1, 2], 2, 300, 1), ([0, 400, 560], 560, 2000, 400)]
-    assert goes_over_a_copy(560, 2, Hq, Hkv, pages.pps * P, 2000, 4, 400)
+    kinds = [([0, 1, 2], 2, n, 1), ([0, 1, 2], 2, 300, 1), ([0, 400, 560], 560, 2000, 400), ([0, 550, 560], 560, 1000, 550)]
+    assert all(goes_over_a_copy(560, 2, Hq, Hkv, pages.pps * P, local, 4, m) for _, _, local, m in kinds[2:])
     ws = qasc.alloc_workspace(max(qasc.kv4_window_attn_workspace_bytes(T, 2, Hq, Hkv, pages.pps * P, local=local, max_q=m)
                                   for _, T, local, m in kinds))
     ln = batch_tensors(None, [n, n - 9])[1]
@@ -797,7 +817,7 @@ COPIED = [
     # Hq, Hkv, P, new tokens, lens, sink, local: calls that go over a copy
     (64, 8, 64, [200, 1, 300, 2], [1500, 900, 800, 77], 4, 100000),
     (64, 8, 128, [400, 30, 0, 1], [1300, 700, 50, 1], 4, 300),
-    (32, 8, 64, [700], [5000], 200, 90),
+    (64, 8, 64, [700], [5000], 200, 90),
     (8, 8, 64, [1000, 129], [1000, 4000], 0, 2500),
     (64, 8, 64, [150, 16, 17, 400], [100, 2000, 2000, 401], 4, 1000),   # more new tokens than cached ones
 ]
@@ -952,8 +972,9 @@ def test_sparse(B, Hq, Hkv, n, K, sink, local, per_head, with_len, paged):
     check_rows(out, lse, ref, n, max(6.0, vmax_of(pages)))
 
 
-def test_sparse_of_many_lists():
-    B, Hq, Hkv, n, K, P = 300, 16, 8, 900, 40, 64
+@pytest.mark.parametrize("K", [40, 300])
+def test_sparse_of_many_lists(K):
+    B, Hq, Hkv, n, P = 300, 16, 8, 900, 64
     pages = Pages4([n], Hkv, P, cdiv(n, P), seed=57, random=True)
     table = pages.table.repeat(B, 1).cuda()                 # all sequences over the same pages
     g = torch.Generator().manual_seed(58)
