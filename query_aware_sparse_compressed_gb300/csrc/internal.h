@@ -330,6 +330,7 @@ constexpr int kCopyPage = 256;
 struct Kv4Copy {
   int64_t most_rows = 0;           // sequences with more query rows of a KV head are copied
   int64_t capacity = 0;            // pages of K and of V
+  int64_t likely = 0;              // of them that the call is likely to take
   int64_t pages_per_seq = 0;       // of the copy's block table
   int32_t* copied = nullptr;       // [B] 1: copied
   int32_t* lens = nullptr;         // [B] tokens in the copy (0: not copied)

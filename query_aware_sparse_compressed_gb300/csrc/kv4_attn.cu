@@ -1170,6 +1170,8 @@ int attend_over_copy(const qasc_shape& s, const Kv4AttnArgs& a, const Args& p, c
   c.most_rows = kCopyRows;
   c.capacity = C.capacity;
   c.pages_per_seq = C.pages_per_seq;
+  const int copies = static_cast<int>(copies_of(a.bt.T, a.max_q, C.seqs) + 0.5);
+  c.likely = std::min(copies * C.pages_per_seq, C.capacity);
   c.copied = reinterpret_cast<int32_t*>(ws + C.off_lists);
   c.lens = c.copied + s.B;
   c.table = c.lens + s.B;
@@ -1189,7 +1191,7 @@ int attend_over_copy(const qasc_shape& s, const Kv4AttnArgs& a, const Args& p, c
   k.bt = a.bt;
   k.bt.lens = c.lens;
   k.skip_empty = true;   // those that are not copied have no tokens there
-  k.seqs = static_cast<int>(copies_of(a.bt.T, a.max_q, C.seqs) + 0.5);
+  k.seqs = copies;
   k.pm.table = c.table;
   k.pm.pages_per_seq = C.pages_per_seq;
   k.pm.num_pages = C.capacity;

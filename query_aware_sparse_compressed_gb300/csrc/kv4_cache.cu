@@ -30,6 +30,8 @@
 // a token and KV head.  131072 tokens, 8 KV heads (688 MB): 108 us, 6.4 TB/s, 94 % of a
 // copy's rate; 16 contexts of up to 5003 tokens, 2 KV heads: 11.6 us.  With a
 // chunk a thread, four rows at a time: 119 and 12.2.
+#include <algorithm>
+
 #include "kv4.cuh"
 #include "internal.h"
 
@@ -706,11 +708,15 @@ cudaError_t launch_kv4_copy(const qasc_shape& s, const PageMap& pm, const Batch&
   a.local = local;
   a.n_cap = s.n_cap;
   a.err = dev.err_word;
-  // Beside another kernel blocks go where there is room first, and those with work were all on
-  // few SMs (512 tokens of 8 heads, 16 blocks: 34 us with the attention, 25 spread out): so a block
-  // asks for as much shared memory as leaves none for more than its share of them on an SM.
-  const int64_t tiles = c.capacity * (kCopyPage / kReadTok), most = static_cast<int64_t>(dev.num_sms) * kReadBlocks;
-  const int64_t grid = tiles < most ? tiles : most, share = (grid + dev.num_sms - 1) / dev.num_sms;
+  // Beside another kernel blocks go where there is room first, and those with work, the first
+  // ones, were all on few SMs (512 tokens of 8 heads, 16 blocks: 34 us with the attention, 25
+  // spread out): so a block asks for as much shared memory as leaves none on an SM for more
+  // than its share of them, and of a third more, which ragged batches may have (16 of
+  // 1 to 257 new tokens: 31 us, 34 without that).
+  constexpr int kParts = kCopyPage / kReadTok;
+  const int64_t sms = dev.num_sms, tiles = c.capacity * kParts;
+  const int64_t share = c.beside ? std::min<int64_t>(kReadBlocks, (c.likely * kParts * 4 / 3 + sms - 1) / sms) : kReadBlocks;
+  const int64_t grid = std::min(tiles, sms * share);
   return launch_dependent(kv4_copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
                           c.beside ? kCopyShared / static_cast<size_t>(share) - kCopyStatic : 0, stream, 1, a);
 }
