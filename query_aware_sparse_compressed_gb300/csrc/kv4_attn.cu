@@ -482,7 +482,6 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
   // ---- this warp's part of the work.  Whole items of single tokens need no sums.
   const int groups = (p.seqs + (1 << p.ssh) - 1) >> p.ssh;
   const bool plain = p.whole && (kList || p.a.bt.cu_q == nullptr);
-  if (tid < 2 * kWarps) S.there[tid] = 0;
   if (!kList && blockIdx.x == gridDim.x - 1)
     for (int b = tid; b < p.B; b += kThreads) {
       const int len = __ldg(p.a.bt.lens + b);
@@ -600,6 +599,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
     }
   }
   if (lane == 0) S.walk[warp] = walk;
+  if (lane < 2) S.there[2 * warp + lane] = 0;   // each warp its own: no barrier stands before its stores to them
   __syncwarp();
 
   uint8_t* const ring = S.ring[warp];

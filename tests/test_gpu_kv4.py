@@ -708,6 +708,34 @@ def test_window_is_deterministic_and_replays_in_a_graph(T, B, n):
     qasc.qasc_device_error()
 
 
+@pytest.mark.parametrize("kind", ["single", "packed", "listed"])
+def test_short_items_of_several_warps_keep_every_part(kind):
+    """One item for the warps of a block, a tile or two each, joined at its end: in thousands of
+    launches none of the warps' parts is left out."""
+    Hq, Hkv, P, n = 8, 1, 64, 380
+    pages = Pages4([n], Hkv, P, cdiv(n, P), seed=71, random=True)
+    kv, table = pages.cache(), pages.table.cuda()
+    q = rand((1, Hq, 128), 72).cuda()
+    c, ln = batch_tensors([0, 1] if kind == "packed" else None, [n])
+    sel = torch.arange(4, n - 64, dtype=torch.int32, device="cuda").reshape(1, -1)
+    ref = osv.window_attention(f64(q), pages.values(0), pages.values(1), [0, 1], [n], 4, n)
+    outs = [torch.full((2000, 1, Hq, w), CANARY, dtype=t, device="cuda") for w, t in ((128, torch.bfloat16), (1, torch.float32))]
+    wss = [window_ws(1, 1, Hq, Hkv, pages.pps * P, n) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(2000):
+        out, lse, s = outs[0][i], outs[1][i, :, :, 0], streams[i % 2]
+        if kind == "listed":
+            qasc.kv4_sparse_attn_paged(q, kv, table, sel, out, wss[i % 2], n=n, local=64, lse=lse, stream=s)
+        else:
+            qasc.kv4_window_attn_paged(q, kv, table, ln, out, wss[i % 2], local=n, cu_q=c, lse=lse, stream=s)
+    torch.cuda.synchronize()
+    qasc.qasc_device_error()
+    check_rows(outs[0][0], outs[1][0, :, :, 0], ref, n, 6.0)
+    for o in outs:
+        assert torch.equal(o, o[:1].expand_as(o))
+
+
 def test_two_windows_on_two_streams():
     Hq, Hkv, P, n = 16, 4, 64, 6000
     pages = Pages4([n, n - 3], Hkv, P, cdiv(n, P), seed=45, random=True)
