@@ -83,10 +83,11 @@ struct Pair {
   float h, l;
 };
 
-// h + l of a + b exactly (Knuth), and with a low part added, renormalised.
+// h + l of a + b exactly (Knuth; l = -0 where there is no rest: its three sums are exact, and
+// rounded down a sum of nothing is -0), and with a low part added, renormalised.
 __device__ __forceinline__ Pair two_sum(float a, float b) {
   const float t = __fadd_rn(a, b), bb = __fadd_rn(t, -a);
-  return {t, __fadd_rn(__fadd_rn(a, -__fadd_rn(t, -bb)), __fadd_rn(b, -bb))};
+  return {t, __fadd_rd(__fadd_rd(a, -__fadd_rn(t, -bb)), __fadd_rd(b, -bb))};
 }
 __device__ __forceinline__ Pair add_low(Pair t, float low) {
   const float l = __fadd_rn(t.l, low), h = __fadd_rn(t.h, l);
@@ -126,10 +127,11 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t ang, Pair& c, Pair& s) {
 }
 
 // p1 + p2 + low to 2^-40 of p1 and p2, as what rounds to its bf16 value: where the sum
-// in fp32 stands on the middle between two bf16 values the rest decides.
+// in fp32 stands on the middle between two bf16 values the rest decides.  (The low parts are
+// summed rounded down: no rest is -0, which leaves a zero the sign of p1 + p2.)
 __device__ __forceinline__ float sum_for_bf16(float p1, float p2, float low) {
   const Pair t = two_sum(p1, p2);
-  const float l = __fadd_rn(t.l, low), h = __fadd_rn(t.h, l), rest = __fadd_rn(l, -__fadd_rn(h, -t.h));
+  const float l = __fadd_rd(t.l, low), h = __fadd_rn(t.h, l), rest = __fadd_rn(l, -__fadd_rn(h, -t.h));
   int u = __float_as_int(h);
   const int away = ((u ^ __float_as_int(rest)) >> 31) | 1;   // 1: the rest has the sum's sign
   if ((u & 0xffff) == 0x8000 && rest != 0.0f) u += away;

@@ -298,6 +298,25 @@ def test_append_of_a_long_prompt_is_exact():
     assert np.array_equal(kv.K[0].cpu().numpy().transpose(1, 0, 2), want[0])
 
 
+@pytest.mark.parametrize("inter", [True, False])
+def test_append_of_zeros_keeps_their_signs(inter):
+    """Pairs of zeros of either sign at angles of every quadrant: the code's sign bit is that of the rotation."""
+    T = 64
+    k = torch.zeros((T, 2, 128))
+    k[:, 1] = -0.0
+    k[:, :, 3::7] *= -1
+    f = (torch.arange(64) * 0.37 + 0.1).float()
+    want = okv4.quantise(round_bf16(osv.rotate(f64(k.bfloat16()), np.arange(T), f.numpy(), inter)))
+    kv = qasc.alloc_kv4(1, 2, T)
+    c, ln = batch_tensors([0, T], [T])
+    kd = k.bfloat16().cuda()
+    qasc.kv4_rope_append(None, kd, kd, None, kv, ln, f.cuda(), cu_q=c, interleaved=inter)
+    qasc.qasc_device_error()
+    assert np.array_equal(kv.K[0].cpu().numpy().transpose(1, 0, 2), want[0])
+    assert 8 in want[0] and 128 in want[0]                 # signs of either value of a byte
+    assert np.array_equal(kv.V[0].cpu().numpy().transpose(1, 0, 2), okv4.quantise(f64(kd))[0])
+
+
 def test_append_does_not_depend_on_the_cut():
     """Token by token, in chunks and at once: the same cache, bit for bit."""
     T, Hkv = 900, 4
