@@ -481,9 +481,9 @@ typedef struct {
  * (rotated) and values quantised, their queries rotated.
  *
  * Arguments, strides and refusals as for kv_rope_append.  What is quantised of a
- * key is its rotation rounded to bf16, which is computed to 2^-40 here (the
- * angles to their fp64 product's error), so that the cache does not depend on how
- * a batch was cut; the queries as in kv_rope_append. */
+ * key is its rotation rounded to bf16, computed here to 2^-38 of |x_a cos| + |x_b sin|
+ * (angles to 2^-63 of a turn at any position), and the same for a token however its
+ * batch was cut; the queries as in kv_rope_append. */
 QASC_API qasc_status kv4_rope_append(const qasc_shape* shape, const qasc_batch* batch, const qasc_rope* rope,
                                      const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
                                      const uint16_t* v, int64_t v_stride, uint16_t* q_out, const qasc_kv4* kv,

@@ -7,9 +7,10 @@
 //   a = max |x| of 16 values,  scale = e4m3(a / 6),  code = e2m1(x / scale)
 // both rounded to nearest, ties to even.  Near the border between two codes
 // the smallest error of a rotated key moves its code by a step, so that its
-// rotation is computed to 2^-40 and then rounded: the cache does not depend on
-// how a batch was cut or where its angles were computed.  cos and sin of an angle come as
-// pairs (high, low part) from a table of 1024 points of the turn and the
+// rotation is computed to 2^-38 and then rounded once.  The angle is a fixed-point number of
+// turns, position times the frequency's 96 bits of a turn: good to 2^-63 at every
+// position.  cos and sin of an angle come as
+// pairs (high, low part), good to 2^-39, from a table of 1024 points of the turn and the
 // series of the remainder r < 2^-8:
 //   cos(t + r) = C - (S sin r + C (1 - cos r)),  sin(t + r) = S + (C sin r - S (1 - cos r))
 // (Knuth's exact sum).  cos and sin are handed on as 16 bits and the rest: products
@@ -94,7 +95,55 @@ __device__ __forceinline__ Pair add_low(Pair t, float low) {
   return {h, __fadd_rn(l, -__fadd_rn(h, -t.h))};
 }
 
-// cos and sin of `ang` / 2^64 turns, to 2^-41.
+// A frequency in turns per position: the 96 bits behind the point, hi and lo.
+struct Turns {
+  uint64_t hi;
+  uint32_t lo;
+};
+// f / 2 pi: the float's 24 bits times 128 of 1 / 2 pi, shifted by its exponent; good to 2^-96,
+// and from a frequency of 2^32 on to 2^-128 of itself.  (One fp64 product is good to 2^-53: at
+// position 2^24 that is an angle 2^-29 off, more than a border forgives.)
+__device__ __forceinline__ Turns turns_of_frequency(float f) {
+  constexpr uint64_t inv_hi = 0x28be60db9391054aull, inv_lo = 0x7f09d5f47d4d3770ull;   // of 2^128 / 2 pi
+  const uint32_t u = __float_as_uint(f);
+  const int exponent = static_cast<int>(u >> 23 & 255);
+  if (exponent == 0 || exponent == 255) return {0, 0};   // less than 2^-128 turns; no number
+  const uint64_t m = (u & 0x7fffff) | 0x800000;
+  // m / 2 pi: w[0] whole turns, then 64 bits each
+  const uint64_t low = __umul64hi(m, inv_lo);
+  uint64_t w[3] = {__umul64hi(m, inv_hi), m * inv_hi + low, m * inv_lo};
+  w[0] += w[1] < low;
+  int right = 150 - exponent;
+  if (right < 0) {   // (no frequency of use)
+    right += 64;
+    if (right <= 0) return {0, 0};
+    w[0] = w[1];
+    w[1] = w[2];
+    w[2] = 0;
+  }
+  for (; right >= 64; right -= 64) {
+    w[2] = w[1];
+    w[1] = w[0];
+    w[0] = 0;
+  }
+  if (right > 0) {
+    w[2] = w[2] >> right | w[1] << (64 - right);
+    w[1] = w[1] >> right | w[0] << (64 - right);
+  }
+  Turns t{w[1], static_cast<uint32_t>(w[2] >> 32)};
+  if (u >> 31) {   // the other way round
+    t.hi = ~t.hi + (t.lo == 0);
+    t.lo = ~t.lo + 1;
+  }
+  return t;
+}
+// The angle at `pos`, in turns times 2^64.
+__device__ __forceinline__ uint64_t angle_at(Turns t, int32_t pos) {
+  const int64_t n = pos;
+  return t.hi * static_cast<uint64_t>(n) + static_cast<uint64_t>((n * static_cast<int64_t>(t.lo)) >> 32);
+}
+
+// cos and sin of `ang` / 2^64 turns, to 2^-39.
 __device__ __forceinline__ void turn_cos_sin(uint64_t ang, Pair& c, Pair& s) {
   const uint64_t j = (ang + (1ull << 53)) >> 54;
   const int64_t rem = static_cast<int64_t>(ang - (j << 54));       // [-2^53, 2^53)
@@ -126,7 +175,7 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t ang, Pair& c, Pair& s) {
   s = add_low(two_sum(S.h, ps), S.l + (es + (C.h * sl + (C.l * rh - S.h * v))));
 }
 
-// p1 + p2 + low to 2^-40 of p1 and p2, as what rounds to its bf16 value: where the sum
+// p1 + p2 + low to 2^-38 of p1 and p2, as what rounds to its bf16 value: where the sum
 // in fp32 stands on the middle between two bf16 values the rest decides.  (The low parts are
 // summed rounded down: no rest is -0, which leaves a zero the sign of p1 + p2.)
 __device__ __forceinline__ float sum_for_bf16(float p1, float p2, float low) {
@@ -233,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const AppendArg
   // of this tile and the next one, which is prepared ahead: one barrier a tile
   __shared__ __align__(16) float turns_of[2][4][kMaxTok][kFreqs];   // cos, sin (16 bits) and their rests
   __shared__ int64_t rows_of[2][kMaxTok];    // cache row of KV head 0; -1: not written, -2: a token of no sequence
+  __shared__ Turns turns_at[kThreads];       // each thread's own (as registers they would spill)
   const int tid = threadIdx.x;
   const int freq = tid & (kFreqs - 1), half = a.rot >> 1;
   pdl_wait();
@@ -244,12 +294,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const AppendArg
       const int len = __ldg(a.bt.lens + b);
       if (len < 0 || len > a.n_cap) record_error(a.err, kErrBadPage);
     }
-  uint64_t F = 0;   // of a turn per position, times 2^64
-  if (freq < half) {
-    const double turns = static_cast<double>(__ldg(a.inv_freq + freq)) * 0.15915494309189533577;
-    const double frac = turns - floor(turns);
-    F = frac < 1.0 ? __double2ull_rn(frac * 18446744073709551616.0) : 0;
-  }
+  if (freq < half) turns_at[tid] = turns_of_frequency(__ldg(a.inv_freq + freq));
   const int64_t head_rows = a.pm.table ? (int64_t(1) << a.pm.page_shift) : a.n_cap;   // rows from head to head
   const int nq = a.q ? a.Hq : 0;
   const unsigned unit_mask = 0xffu << (tid & 24);
@@ -271,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const AppendArg
     if (freq < half) {
       const int32_t pos = a.positions ? __ldg(a.positions + t) : static_cast<int32_t>(at.pos);
       Pair c, s;
-      turn_cos_sin(F * static_cast<uint64_t>(static_cast<int64_t>(pos)), c, s);
+      turn_cos_sin(angle_at(turns_at[tid], pos), c, s);
       const float ch = __uint_as_float(__float_as_uint(c.h) & 0xffffff00u), sh = __uint_as_float(__float_as_uint(s.h) & 0xffffff00u);
       turns_of[buf][0][tk][freq] = ch;
       turns_of[buf][1][tk][freq] = sh;

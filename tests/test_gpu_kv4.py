@@ -3,7 +3,7 @@ kv4_sparse_attn*) against the fp64 oracle.
 
 Tolerances, fixed before the first run (A = sum_j p_j |V_j|, from the oracle):
   codes, scales   equal: the oracle quantises the fp64 rotation rounded to bf16, which
-                  the kernel has to 2^-40
+                  the kernel has to 2^-38
   values read     equal
   rotated query   2^-8 |y| (one rounding to bf16: half a step) + 2^-20 (|x_a| + |x_b|)
   logit           e = 2^-17 max_j sum_e |q_e K_e| / sqrt(d) (128 fp32 additions of
@@ -293,6 +293,56 @@ def test_append_of_a_long_prompt_is_exact():
     kv = qasc.alloc_kv4(1, Hkv, T)
     c, ln = batch_tensors([0, T], [T])
     qasc.kv4_rope_append(None, k.cuda(), v.cuda(), None, kv, ln, f.cuda(), cu_q=c, positions=pos.cuda())
+    qasc.qasc_device_error()
+    assert np.array_equal(kv.K_sf.view(torch.uint8)[0].cpu().numpy().transpose(1, 0, 2), want[1])
+    assert np.array_equal(kv.K[0].cpu().numpy().transpose(1, 0, 2), want[0])
+
+
+# Position, frequency, and a pair (a, b) one of whose rotated values stands 2^-33 to 2^-28 beside the middle
+# between a border of two codes of scale 1 and the next bf16 value: the angle has to be better than
+# that at these positions for the code to be right (a product of 53 bits is 2^-29 off there).
+BORDERS = [
+    (16774594, 0.8815479278564453, -1.6953125, 3.640625),
+    (16777213, 0.6797472238540649, 3.453125, 0.5390625),
+    (16775826, 0.6150959730148315, 0.84765625, 1.65625),
+    (15199687, 0.8867228031158447, -1.4453125, 1.359375),
+    (16774875, 0.8313730955123901, -1.484375, 1.9296875),
+    (16776500, 0.6090608835220337, -2.921875, 1.0390625),
+]
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_append_beside_the_codes_borders_at_far_positions(sign):
+    """A value of 6 that does not turn makes the scale 1; the pair turns at its own frequency."""
+    T = len(BORDERS)
+    k = torch.zeros((T, 1, 128))
+    f = torch.zeros(64)
+    k[:, 0, 0] = 6
+    for t, (_, freq, a, b) in enumerate(BORDERS):
+        f[1 + t] = freq
+        k[t, 0, 2 + 2 * t], k[t, 0, 3 + 2 * t] = a, sign * b    # (the angle's sign turned with b's: the same values)
+    k, f = k.bfloat16(), f * sign
+    pos = torch.tensor([p for p, *_ in BORDERS], dtype=torch.int32)
+    want = okv4.quantise(round_bf16(osv.rotate(f64(k), pos.numpy(), f.numpy(), True)))
+    kv = qasc.alloc_kv4(1, 1, T)
+    c, ln = batch_tensors([0, T], [T])
+    qasc.kv4_rope_append(None, k.cuda(), k.cuda(), None, kv, ln, f.cuda(), cu_q=c, positions=pos.cuda(), interleaved=True)
+    qasc.qasc_device_error()
+    assert np.array_equal(kv.K_sf.view(torch.uint8)[0].cpu().numpy().transpose(1, 0, 2), want[1])
+    assert np.array_equal(kv.K[0].cpu().numpy().transpose(1, 0, 2), want[0])
+
+
+def test_append_at_far_positions():
+    """4 million rotated keys below position 2^24, and in front of position 0."""
+    T, Hkv = 2048, 16
+    k = rand((T, Hkv, 128), 73)
+    f = (500000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float()
+    pos = ((1 << 24) - 1 - 3 * torch.arange(T)).int()
+    pos[::16] = -pos[::16]
+    want = okv4.quantise(round_bf16(osv.rotate(f64(k), pos.numpy(), f.numpy(), False)))
+    kv = qasc.alloc_kv4(1, Hkv, T)
+    c, ln = batch_tensors([0, T], [T])
+    qasc.kv4_rope_append(None, k.cuda(), k.cuda(), None, kv, ln, f.cuda(), cu_q=c, positions=pos.cuda())
     qasc.qasc_device_error()
     assert np.array_equal(kv.K_sf.view(torch.uint8)[0].cpu().numpy().transpose(1, 0, 2), want[1])
     assert np.array_equal(kv.K[0].cpu().numpy().transpose(1, 0, 2), want[0])
