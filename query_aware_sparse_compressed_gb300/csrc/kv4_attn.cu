@@ -615,6 +615,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
   int64_t base = 0;
   int tok = kNoToken, tok_g = 0, tok_kind = kNone;   // lane's token of the tile after the next (of a line: its first)
   int64_t tok_base = 0;
+  bool tok_there = false;                            // listed: the lane has a slot (an entry may be any number)
   int at = kNoToken, at_g = 0, at_kind = kNone;      // lane's token of the next tile,
   int at_page = 0;                                   // and its page or first row
   auto next_tokens = [&]() {
@@ -640,7 +641,9 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
       tok = at0 + lt * kTile;
     } else {
       tok_kind = kRowwise;
-      tok = token_of_slot<kList>(p, S.queue[warp][(pushed - 1) % kQueue], lt * kTile + lane);
+      const Piece& pc = S.queue[warp][(pushed - 1) % kQueue];
+      tok = token_of_slot<kList>(p, pc, lt * kTile + lane);
+      tok_there = lt * kTile + lane < pc.cnt;
     }
     tok_g = tg;
     tok_base = base;
@@ -652,7 +655,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
     at_kind = tok_kind;
     at = tok;
     at_g = tok_g;
-    if (kList && tok_kind != kNone && tok != kNoToken && (tok < 0 || tok >= p.n)) {   // an entry outside the cache
+    if (kList && tok_kind != kNone && tok_there && (tok < 0 || tok >= p.n)) {   // an entry outside the cache
       record_error(p.err, kErrBadPage);
       at = kNoToken;
     }

@@ -1136,6 +1136,24 @@ def test_sparse_entry_outside_is_reported():
     check_rows(out, lse, sparse_ref(f64(q), pages, [[[10, 11, 12, 40]] * 2], n, 4, 64), n, 6.0)
 
 
+@pytest.mark.parametrize("entry", [-2 ** 31, -2 ** 31 + 1, 2 ** 31 - 1])
+def test_sparse_entry_far_outside_is_reported(entry):
+    """One entry outside, the ends of its type: a row of zeros, and recorded."""
+    n, P = 400, 64
+    pages = Pages4([n], 2, P, 7, seed=74, random=True)
+    q = rand((1, 8, 128), 75)
+    sel = torch.tensor([[10, entry, 40]], dtype=torch.int32)
+    out, lse = outputs(1, 8)
+    ws = qasc.alloc_workspace(qasc.kv4_sparse_attn_workspace_bytes(1, 8, 2, n, 448, 3, 4, 64))
+    qasc.kv4_sparse_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), sel.cuda(), out, ws, n=n, local=64, lse=lse)
+    with pytest.raises(qasc.QascError, match="BAD_TABLE"):
+        qasc.qasc_device_error()
+    K, V = pages.values(0), pages.values(1)
+    K[0][:, 11], V[0][:, 11] = 0, 0                         # a row of zeros in its place
+    pages.values = lambda side: (K, V)[side]
+    check_rows(out, lse, sparse_ref(f64(q), pages, [[[10, 11, 40]] * 2], n, 4, 64), n, 6.0)
+
+
 def test_decode_steps_over_a_4_bit_cache():
     """The run of a serving loop: a prompt in two chunks, then steps that append, select on the
     index and attend to the selected tokens, against the oracle on what the cache holds."""
