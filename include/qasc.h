@@ -531,7 +531,8 @@ QASC_API qasc_status kv4_read_paged(const qasc_shape* shape, const qasc_paged_ca
  *   to may hold anything, as there; a row with a NaN scale that some attend to reaches
  *   their outputs, and may reach those of its sequence's other queries in that KV
  *   head.  A block-table entry outside the pool stands for rows of zeros and is recorded
- *   as QASC_ERR_BAD_TABLE. */
+ *   as QASC_ERR_BAD_TABLE.  A call over a copy records a cu_q that does not ascend as
+ *   QASC_ERR_BAD_TABLE; its outputs are not defined then. */
 QASC_API size_t kv4_window_attn_workspace_bytes(const qasc_shape* shape, int64_t tokens, int64_t max_q, int32_t sink,
                                                 int32_t local);
 QASC_API qasc_status kv4_window_attn(const qasc_shape* shape, const qasc_batch* batch, int64_t max_q, int32_t sink,

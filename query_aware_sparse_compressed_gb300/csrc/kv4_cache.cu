@@ -632,6 +632,10 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv4_copy_kernel(const C
     if (b < a.B) {
       first[b] = before;
       if (blockIdx.x == 0) {
+        // Offsets that do not ascend make more long sequences than there is room for, and rows that the
+        // attention over the copy holds for two of them.
+        if (a.bt.cu_q && min(max(__ldg(a.bt.cu_q + b), 0), static_cast<int>(a.bt.T)) > max(__ldg(a.bt.cu_q + b + 1), 0))
+          record_error(a.err, kErrBadPage);
         const bool fits = pages > 0 && before + pages <= a.c.capacity;
         a.c.copied[b] = fits;
         a.c.lens[b] = fits ? tokens : 0;

@@ -978,6 +978,38 @@ def test_window_offsets_that_do_not_ascend(local, max_q):
         check_rows(out[lo:hi], lse[lo:hi], ref, lens[b], 6.0, rows=rows)
 
 
+@pytest.mark.parametrize("lens", [[20000, 50, 19900], [300, 50, 400]])
+def test_window_offsets_that_do_not_ascend_over_a_copy(lens):
+    """Two long sequences where T tokens can have one, and the copy room for one of 20000 cached tokens: recorded.
+    The next call over the same workspace is right again."""
+    T, Hq, Hkv, P, n = 20, 64, 8, 64, 20000
+    pages, values = repeated(n, Hkv, P, 76)
+    q = rand((T, Hq, 128), 77, 0.3)
+    kv, table = pages.cache(), pages.table.repeat(3, 1).cuda()
+    ws = window_ws(T, 3, Hq, Hkv, pages.pps * P, n, 4, 17)
+    assert goes_over_a_copy(T, 3, Hq, Hkv, pages.pps * P, n, 4, 17)
+
+    def call(cu):
+        out, lse = outputs(T, Hq)
+        c, ln = batch_tensors(cu, lens)
+        qasc.kv4_window_attn_paged(q.cuda(), kv, table, ln, out, ws, local=n, cu_q=c, max_q=17, lse=lse)
+        return out, lse
+    call([0, 17, 3, 20])
+    with pytest.raises(qasc.QascError, match="BAD_TABLE"):
+        qasc.qasc_device_error()
+    for cu in ([0, 17, 17, 20], [-5, 0, 3, 27]):            # (values outside [0, T] are clamped)
+        out, lse = call(cu)
+        qasc.qasc_device_error()
+        cu = [min(max(x, 0), T) for x in cu]
+        for b, t, h in ((0, 0, 0), (0, 16, 63), (1, 1, 3), (2, 17, 5), (2, 19, 40)):
+            if not cu[b] <= t < cu[b + 1]:
+                continue
+            m = lens[b] - (cu[b + 1] - t) + 1
+            want = osv.attend(f64(q)[t, h], values[0][h // 8, :m], values[1][h // 8, :m])
+            check_rows(out[t:t + 1, h:h + 1].contiguous(), lse[t:t + 1, h:h + 1].contiguous(),
+                       tuple(np.asarray(x)[None, None] for x in want), m, 6.0, p=2.0 ** -8)
+
+
 def test_window_bad_page_of_a_copied_sequence():
     Hq, Hkv, n, m = 64, 8, 1500, 300
     pages = Pages4([n], Hkv, 64, 24, seed=53, random=True)
