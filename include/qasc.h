@@ -517,12 +517,14 @@ QASC_API qasc_status kv4_read_paged(const qasc_shape* shape, const qasc_paged_ca
  *   max_q  the most new tokens of any sequence, or any larger number up to
  *          tokens (without cu_q: not used).  It chooses how the work is done;
  *          a sequence of more tokens is computed all the same.
- *   workspace, ws_bytes >= kv4_window_attn_workspace_bytes(shape, tokens, max_q,
- *          sink, local), for these numbers: 4.3 MB, and more where sequences may
- *          have more than 128 rows (new tokens times Hq / Hkv) and it pays: those
- *          attend to a bf16 copy in the workspace of the tokens that they see (512 bytes a
- *          token and KV head, 4 GiB at most; a sequence that finds no room goes without)
- *          by kv_window_attn's kernel.  The workspace need not be cleared and
+ *   workspace, ws_bytes >= 4.3 MB, the size for max_q = 1.  The size for tokens, max_q,
+ *          sink and local has more where sequences may have more than 128 rows (new
+ *          tokens times Hq / Hkv) and it may pay: those attend to a bf16 copy in the
+ *          workspace of the tokens that they see (512 bytes a token and KV head, 4 GiB at
+ *          most) by kv_window_attn's kernel, up to 8 times as fast.  It does not fall with
+ *          more tokens, sequences or a larger max_q, so that one of the largest call's size
+ *          serves every smaller one; with less than that a call copies what there is room
+ *          for, and the others go without.  The workspace need not be cleared and
  *          is free again once the call has finished on the stream; calls that can
  *          overlap need one each.
  *   other arguments, refusals, lengths outside the cache and rows without a token as for

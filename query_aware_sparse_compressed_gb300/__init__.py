@@ -781,6 +781,8 @@ def kv4_read_paged(kv_pool, block_table, kv_lens, K_out, V_out, *, cu_q=None, st
 
 
 def kv4_window_attn_workspace_bytes(T, B, Hq, Hkv, n_cap, *, local, sink=4, max_q=None):
+    """Bytes with which every call of up to T tokens, max_q of a sequence (None: T), takes
+    its fastest form; calls accept less, down to the size for max_q = 1."""
     return _sized(_L().kv4_window_attn_workspace_bytes(ctypes.byref(make_shape(B, Hq, Hkv, n_cap, n_cap)), T,
                                                        T if max_q is None else max_q, _tokens32(sink), _tokens32(local)))
 

@@ -884,10 +884,9 @@ qasc_status kv4_attn_call(const char* fn, const qasc_shape* shape, qasc::Kv4Attn
   if (a.bt.T == 0) return ok();
   QASC_REQUIRE_PTR(q, 16, fn);
   QASC_REQUIRE_PTR(out, 16, fn);
-  const size_t need = a.listed ? qasc::kv4_attn_least_bytes()
-                               : qasc::kv4_window_workspace_bytes(*shape, a.bt.T, a.max_q, a.sink, a.local);
-  if (!workspace || ws_bytes < need)
-    return fail(QASC_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need, workspace ? ws_bytes : size_t(0));
+  if (!workspace || ws_bytes < qasc::kv4_attn_least_bytes())
+    return fail(QASC_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, qasc::kv4_attn_least_bytes(),
+                workspace ? ws_bytes : size_t(0));
   QASC_REQUIRE_PTR(workspace, 256, fn);
   qasc_status st;
   const qasc::DeviceInfo* dev = need_device(fn, &st);
@@ -895,7 +894,8 @@ qasc_status kv4_attn_call(const char* fn, const qasc_shape* shape, qasc::Kv4Attn
   a.q = q;
   a.out = out;
   a.lse = lse;
-  const int rc = qasc::launch_kv4_attn(*shape, a, static_cast<uint8_t*>(workspace), *dev, static_cast<cudaStream_t>(stream));
+  const int rc = qasc::launch_kv4_attn(*shape, a, static_cast<uint8_t*>(workspace), ws_bytes, *dev,
+                                       static_cast<cudaStream_t>(stream));
   if (rc != 0) return cuda_fail(rc, fn);
   return ok();
 }

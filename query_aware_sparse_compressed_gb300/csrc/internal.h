@@ -362,10 +362,11 @@ struct Kv4AttnArgs {
   int32_t K = 0;                 // entries of a list
   bool sel_per_kv = false;
 };
-size_t kv4_attn_least_bytes();   // for the most SMs
+size_t kv4_attn_least_bytes();   // for the most SMs; what every call has to have
+// With room for the copies of any call of up to T tokens and max_q of a sequence.
 size_t kv4_window_workspace_bytes(const qasc_shape& s, int64_t T, int64_t max_q, int32_t sink, int32_t local);
-// The workspace has the size above (kv4_attn_least_bytes() of a listed call).
-int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream);
+int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, size_t ws_bytes, const DeviceInfo& dev,
+                    cudaStream_t stream);
 cudaError_t configure_kv4_kernels(const DeviceInfo& dev);
 cudaError_t configure_kv4_cache_kernels(const DeviceInfo& dev);
 

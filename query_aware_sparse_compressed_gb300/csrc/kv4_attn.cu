@@ -1134,35 +1134,61 @@ bool copy_pays(const qasc_shape& s, int64_t T, int64_t max_q, int64_t tokens, in
   return copy < here;
 }
 
+// Whether it may pay for any call of up to T tokens, whatever its max_q: what attention takes here
+// (which does not fall with max_q) against the least that a copy takes, both lines in the tokens.
+bool copy_may_pay(const qasc_shape& s, int64_t T, int64_t window) {
+  const double gq = s.Hq / s.Hkv, least = kCopyRows / (s.Hq / s.Hkv) + 1;   // new tokens of a sequence that is copied
+  const double seen = std::min<int64_t>(s.n_cap, window + 15), tokens = std::min<double>(s.n_cap, window + least - 1);
+  for (const double t : {static_cast<double>(T), least}) {
+    const double here = 10.0 + (t * gq / 16.0 + 1.0) * seen * s.Hkv / kTile * 1.05e-3;
+    const double copy = 23.0 + tokens * s.Hkv * 656.0 / 5.5e6 + t * gq * tokens * s.Hkv * 512.0 / 1.4e9;
+    if (copy < here + 1e-6) return true;
+  }
+  return false;
+}
+
 struct CopyLayout {
   int64_t capacity = 0, pages_per_seq = 0;   // capacity 0: no copy
   int64_t seqs = 0;                          // sequences that can be long enough
-  bool all = false;                          // there is room for every sequence that is long enough
+  bool all = false;                          // (of a call) there is room for every sequence that is long enough
   size_t off_lists = 0, off_attn = 0, attn_bytes = 0, off_k = 0, off_v = 0, total = 0;
 };
-// Of a call whose sequences have at most max_q new tokens.
-CopyLayout copy_layout(const qasc_shape& s, int64_t T, int64_t max_q, int32_t sink, int32_t local) {
+// Of calls whose sequences have at most max_q new tokens: everything that a copy takes.  No part of it
+// falls with more tokens, sequences or a larger max_q.
+CopyLayout copy_space(const qasc_shape& s, int64_t T, int64_t max_q, int64_t window) {
   CopyLayout L;
-  const int64_t gq = s.Hq / s.Hkv;
-  L.total = kv4_attn_least_bytes();
-  if (max_q * gq <= kCopyRows) return L;
-  const int64_t tokens = std::min<int64_t>(s.n_cap, static_cast<int64_t>(sink) + local + max_q - 1);
+  const int64_t gq = s.Hq / s.Hkv, tokens = std::min<int64_t>(s.n_cap, window + max_q - 1);
   L.pages_per_seq = (tokens + kCopyPage - 1) / kCopyPage;
-  const int64_t cap = L.pages_per_seq * kCopyPage;
-  if (cap >= kTokensMost || static_cast<int64_t>(s.B) * s.Hkv * cap >= (int64_t(1) << 31)) return L;
-  const int64_t seqs = std::min<int64_t>(s.B, T * gq / (kCopyRows + 1));   // that can be as long
-  if (!copy_pays(s, T, max_q, tokens, seqs, static_cast<int64_t>(sink) + local)) return L;
+  L.seqs = std::min<int64_t>(s.B, T * gq / (kCopyRows + 1));   // that can be as long
   const int64_t page_bytes = static_cast<int64_t>(s.Hkv) * kCopyPage * kD * 2;
   const int64_t most = std::min(kCopyBytes / (2 * page_bytes), ((int64_t(1) << 31) - 1) / (s.Hkv * kCopyPage));
-  L.capacity = std::min(seqs * L.pages_per_seq, most);
-  L.seqs = seqs;
-  L.all = L.capacity == seqs * L.pages_per_seq;
-  L.off_lists = align_up(L.total, 256);
+  L.capacity = std::min(L.seqs * L.pages_per_seq, most);
+  L.off_lists = align_up(kv4_attn_least_bytes(), 256);
   L.off_attn = align_up(L.off_lists + static_cast<size_t>(s.B) * (2 + L.pages_per_seq) * sizeof(int32_t), 256);
   L.attn_bytes = kv_attn_workspace_bytes(T, s.B, s.Hq, s.Hkv, false, kMaxSmsForSizing);
   L.off_k = align_up(L.off_attn + L.attn_bytes, 256);
   L.off_v = L.off_k + static_cast<size_t>(L.capacity * page_bytes);
   L.total = L.off_v + static_cast<size_t>(L.capacity * page_bytes);
+  return L;
+}
+
+// Of one call with a workspace of ws_bytes: the copy takes what room there is, if it is enough for
+// the longest sequence.
+CopyLayout copy_layout(const qasc_shape& s, int64_t T, int64_t max_q, int32_t sink, int32_t local, size_t ws_bytes) {
+  const int64_t window = static_cast<int64_t>(sink) + local;
+  if (max_q * (s.Hq / s.Hkv) <= kCopyRows) return CopyLayout();
+  CopyLayout L = copy_space(s, T, max_q, window);
+  const int64_t cap = L.pages_per_seq * kCopyPage;
+  if (cap >= kTokensMost || static_cast<int64_t>(s.B) * s.Hkv * cap >= (int64_t(1) << 31)) return CopyLayout();
+  if (!copy_pays(s, T, max_q, std::min(s.n_cap, window + max_q - 1), L.seqs, window)) return CopyLayout();
+  const size_t page_bytes = static_cast<size_t>(s.Hkv) * kCopyPage * kD * 2;
+  const size_t room = ws_bytes > L.off_k ? (ws_bytes - L.off_k) / (2 * page_bytes) : 0;
+  if (room < static_cast<size_t>(L.capacity)) {
+    if (room < static_cast<size_t>(L.pages_per_seq)) return CopyLayout();
+    L.capacity = static_cast<int64_t>(room);
+    L.off_v = L.off_k + room * page_bytes;
+  }
+  L.all = L.capacity == L.seqs * L.pages_per_seq;
   return L;
 }
 
@@ -1211,10 +1237,13 @@ int attend_over_copy(const qasc_shape& s, const Kv4AttnArgs& a, const Args& p, c
 size_t kv4_attn_least_bytes() { return layout_of(16, kMaxSmsForSizing).total; }
 
 size_t kv4_window_workspace_bytes(const qasc_shape& s, int64_t T, int64_t max_q, int32_t sink, int32_t local) {
-  return copy_layout(s, T, max_q, sink, local).total;
+  const int64_t window = static_cast<int64_t>(sink) + local;
+  if (max_q * (s.Hq / s.Hkv) <= kCopyRows || !copy_may_pay(s, T, window)) return kv4_attn_least_bytes();
+  return copy_space(s, T, max_q, window).total;
 }
 
-int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, const DeviceInfo& dev, cudaStream_t stream) {
+int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, size_t ws_bytes, const DeviceInfo& dev,
+                    cudaStream_t stream) {
   Args p{};
   p.a = a;
   p.a.sink = std::min(a.sink, kTokensMost);   // more mean the same
@@ -1234,7 +1263,7 @@ int launch_kv4_attn(const qasc_shape& s, const Kv4AttnArgs& a, uint8_t* ws, cons
   while ((p.seqs - 1) >> p.ssh >= kSums) ++p.ssh;
   p.err = dev.err_word;
 
-  const CopyLayout C = a.listed ? CopyLayout() : copy_layout(s, a.bt.T, a.max_q, a.sink, a.local);
+  const CopyLayout C = a.listed ? CopyLayout() : copy_layout(s, a.bt.T, a.max_q, a.sink, a.local, ws_bytes);
   const int64_t gq = s.Hq / s.Hkv;
   // What a call with long sequences leaves is likely to be single tokens.
   const int nt = a.listed || C.capacity > 0 ? 1 : tiles_of(s, a.max_q);

@@ -947,6 +947,54 @@ def test_window_over_a_copy(Hq, Hkv, P, ql, lens, sink, local):
     assert bool((out[T:] == CANARY).all()) and bool((lse[T:] == CANARY).all())
 
 
+@pytest.mark.parametrize("pages", [0, 5, 6, 9, 11])
+def test_window_with_less_workspace_than_the_whole_copy(pages):
+    """Room for no page, for less than, just as much as and more than the longest sequence takes, and for nearly all of
+    them: the same rows, from a copy or from the 4-bit cache."""
+    Hq, Hkv, P, ql, lens, local = 64, 8, 64, [200, 1, 300, 2], [1500, 900, 800, 77], 1200
+    T, cu = sum(ql), np.concatenate([[0], np.cumsum(ql)]).tolist()
+    caches = Pages4(lens, Hkv, P, 24, seed=78, random=True)
+    size = qasc.kv4_window_attn_workspace_bytes
+    full = size(T, 4, Hq, Hkv, 24 * P, local=local, max_q=300)
+    least = size(1, 4, Hq, Hkv, 24 * P, local=local, max_q=1)
+    page = 2 * Hkv * 256 * 256                              # of 256 tokens; sequences of up to 1503 tokens take 6
+    assert full - least > 24 * page and goes_over_a_copy(T, 4, Hq, Hkv, 24 * P, local, 4, 300)
+    ws = qasc.alloc_workspace(full - (24 - pages) * page if pages else least)
+    ws.fill_(255)
+    q = rand((T, Hq, 128), 79, 0.3)
+    c, ln = batch_tensors(cu, lens)
+    out, lse = outputs(T, Hq)
+    qasc.kv4_window_attn_paged(q.cuda(), caches.cache(), caches.table.cuda(), ln, out, ws, local=local, cu_q=c, max_q=300, lse=lse)
+    qasc.qasc_device_error()
+    tokens = [0, 100, 199, 200, 201, 350, 500, 501, 502]
+    ref = osv.window_attention(f64(q), caches.values(0), caches.values(1), cu, lens, 4, local, tokens=tokens)
+    check_rows(out, lse, ref, 1500, 6.0, rows=tokens, p=p_error(ql, Hq // Hkv))
+    whole, whole_lse = window(q, caches, cu, lens, 4, local, max_q=300)
+    assert float((out.float() - whole.float()).abs().max()) <= 6.0 * (2 * 2.0 ** -8 + 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16)
+    assert float((lse - whole_lse).abs().max()) <= 1e-3
+
+
+@pytest.mark.parametrize("T,m", [(103, 53), (96, 53), (53, 53), (16, 1)])
+def test_window_smaller_calls_take_the_largest_ones_workspace(T, m):
+    """A workspace sized once, at 103 tokens of up to 53, where a call does not copy and a smaller one does."""
+    B, Hq, Hkv, P, n = 16, 32, 8, 256, 131072
+    pages = Pages4([2000], Hkv, P, 8, seed=80, random=True)
+    table = torch.full((B, n // P), POISON, dtype=torch.int32)
+    table[:, :8] = pages.table
+    ws = qasc.alloc_workspace(qasc.kv4_window_attn_workspace_bytes(103, B, Hq, Hkv, n, local=4096, max_q=53))
+    ql = [m] + [1] * (T - m) + [0] * (B - 1 - (T - m)) if T - m < B else [m, T - m - (B - 2)] + [1] * (B - 2)
+    cu, lens = np.concatenate([[0], np.cumsum(ql)]).tolist(), [2000 - b for b in range(B)]
+    q = rand((T, Hq, 128), 81, 0.3)
+    c, ln = batch_tensors(cu, lens)
+    out, lse = outputs(T, Hq)
+    qasc.kv4_window_attn_paged(q.cuda(), pages.cache(), table.cuda(), ln, out, ws, local=4096, cu_q=c, max_q=m, lse=lse)
+    qasc.qasc_device_error()
+    K, V = ([pages.values(side)[0][:, :x] for x in lens] for side in range(2))
+    tokens = sorted({0, T // 2, T - 1})
+    check_rows(out, lse, osv.window_attention(f64(q), K, V, cu, lens, 4, 4096, tokens=tokens), 2000, 6.0, rows=tokens,
+               p=p_error(ql, Hq // Hkv))
+
+
 def test_window_over_a_copy_of_a_contiguous_cache():
     Hq, Hkv, ql, lens, n_cap, sink, local = 64, 8, [300, 2, 140], [900, 70, 333], 960, 4, 500
     T = sum(ql)

@@ -200,6 +200,38 @@ def test_sizes_follow_the_calls_rules():
             qasc.kv4_sparse_attn_workspace_bytes(**{**dict(B=3, Hq=8, Hkv=2, n=512, n_cap=512, K=100), **bad})
 
 
+SHAPES = [   # B, Hq, Hkv, n_cap, local
+    (2, 8, 8, 8192, 256), (16, 32, 8, 131072, 4096), (1, 64, 8, 32768, 32768), (64, 64, 8, 131072, 131072),
+    (7, 8, 2, 5000, 1000), (3, 8, 1, 300, 1), (2048, 64, 8, 131071, 131071), (1, 8, 8, (1 << 24) - 1, 1 << 24),
+]
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,n_cap,local", SHAPES)
+def test_window_size_does_not_fall_with_a_larger_call(lib, B, Hq, Hkv, n_cap, local):
+    steps = [1, 2, 16, 17, 18, 33, 53, 64, 65, 96, 100, 103, 128, 129, 130, 200, 257, 1000, 1941, 4181, 6502, 6602, 20000, 32768]
+
+    def size(T, m, b=B):
+        return qasc.kv4_window_attn_workspace_bytes(T, b, Hq, Hkv, n_cap, local=local, max_q=m)
+    least = size(1, 1)
+    below = {}
+    for T in steps:
+        for m in [m for m in steps if m <= T]:
+            got = size(T, m)
+            assert got >= least and got >= max((below[k] for k in below if k[0] <= T and k[1] <= m), default=0)
+            assert got >= size(T, m, max(1, B // 2)) and got <= (5 << 30)
+            below[T, m] = got
+    assert len(set(below.values())) > 1 or local == 1
+
+
+def test_window_sizes_of_calls_that_do_and_do_not_copy():
+    """Where the rule for a copy goes back and forth: T, max_q of a call and of a smaller one."""
+    for (B, Hq, Hkv, n_cap, local), (T, m), (T1, m1) in (
+            ((2, 8, 8, 8192, 256), (6502, 4181), (6502, 1941)), ((2, 8, 8, 8192, 256), (6602, 6602), (6502, 1941)),
+            ((16, 32, 8, 131072, 4096), (103, 53), (96, 53))):
+        big, small = (qasc.kv4_window_attn_workspace_bytes(t, B, Hq, Hkv, n_cap, local=local, max_q=q) for t, q in ((T, m), (T1, m1)))
+        assert big >= small > 50e6
+
+
 def test_no_tokens_is_no_call(lib):
     c = Call()
     c.b.tokens, c.max_q = 0, 0
