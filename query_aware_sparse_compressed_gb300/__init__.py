@@ -825,7 +825,7 @@ def kv4_window_attn_paged(q, kv_pool, block_table, kv_lens, out, workspace, *, l
 
 
 def kv4_sparse_attn_workspace_bytes(B, Hq, Hkv, n, n_cap, K, sink=4, local=256):
-    shape, params = make_shape(B, Hq, Hkv, n, n_cap), ts_params(K, sink, local, 1)
+    shape, params = make_shape(B, Hq, Hkv, n, n_cap), ts_params(K, _tokens32(sink), _tokens32(local), 1)
     return _sized(_L().kv4_sparse_attn_workspace_bytes(ctypes.byref(shape), ctypes.byref(params)))
 
 
@@ -837,7 +837,7 @@ def _sparse4(name, q, kv, block_table, sel, out, workspace, n, sink, local, leng
     K = sel.shape[-1] if sel is not None else 0
     sp = _at(sel, "sel", _I32, lists + (K,), dev) if K else None
     up = None if lengths is None else _at(lengths, "lengths", _I32, lists, dev)
-    params = _lib.pack_params(K, sink, local, 1)
+    params = _lib.pack_params(K, _tokens32(sink), _tokens32(local), 1)
     _run(getattr(_L(), name), dev, stream, _lib.pack_shape(B, Hq, Hkv, D, D_IDX, 0, n, n_cap), None,
          *((params,) if cache is None else (params, cache)), qp, kvp, sp, up, 1 if per_kv_head else 0, *outputs)
 

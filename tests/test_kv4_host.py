@@ -232,6 +232,24 @@ def test_window_sizes_of_calls_that_do_and_do_not_copy():
         assert big >= small > 50e6
 
 
+@pytest.mark.parametrize("far", [2 ** 31 - 1, 2 ** 31, 2 ** 40])
+def test_sparse_sink_and_local_of_any_number(monkeypatch, far):
+    """More tokens than 32 bits hold mean all of them, as in the window calls; negative ones are refused."""
+    assert qasc.kv4_sparse_attn_workspace_bytes(1, 8, 2, 512, 512, 0, sink=far) > 0
+    assert qasc.kv4_sparse_attn_workspace_bytes(1, 8, 2, 512, 512, 0, local=far) > 0
+    kv = qasc.alloc_kv4(1, 2, 64, device="cpu")
+    q, ws = torch.zeros((1, 8, 128), dtype=bf), torch.zeros(1024, dtype=u8)
+    passed = []
+    monkeypatch.setattr(qasc, "_run", lambda fn, dev, stream, shape, cache, params, *rest: passed.append(params))
+    for kw in (dict(sink=far, local=far), dict(sink=-far, local=4), dict(sink=4, local=-far)):
+        qasc.kv4_sparse_attn(q, kv, None, q, ws, n=10, **kw)
+    got = [_lib.qasc_ts_params.from_buffer_copy(p) for p in passed]
+    assert (got[0].sink, got[0].local) == (2 ** 31 - 1, 2 ** 31 - 1) and got[1].sink < 0 and got[2].local < 0
+    for bad in (dict(sink=-far), dict(local=-far)):
+        with pytest.raises(qasc.QascError):
+            qasc.kv4_sparse_attn_workspace_bytes(1, 8, 2, 512, 512, 0, **bad)
+
+
 def test_no_tokens_is_no_call(lib):
     c = Call()
     c.b.tokens, c.max_q = 0, 0
