@@ -39,6 +39,9 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 // its writes are visible (a no-op without a programmatic predecessor); every
 // thread calls it before touching global memory.  pdl_trigger() lets the next
 // kernel launch; each CTA calls it once its work is done.
+// One pair of kernels departs from that: kv4_attn_kernel, where it has the rest of
+// a batch as whole items, triggers behind its wait, and kv4_copy_kernel beside it
+// begins without one (Kv4Copy::beside says on which conditions).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -337,8 +337,13 @@ struct Kv4Copy {
   int32_t* table = nullptr;        // [B][pages_per_seq]
   uint16_t* K = nullptr;           // [capacity][Hkv][kCopyPage][d]
   uint16_t* V = nullptr;
-  // The copy needs nothing of the kernel launched before it, which lets it start once its own
-  // blocks have waited for what went before.
+  // The copy runs beside the kernel launched before it: it reads and writes without waiting for
+  // that one, and waits before it ends.  This is sound as long as the kernel before
+  //   - triggers only behind its own pdl_wait(): the copy begins when all blocks have triggered, and where that wait has
+  //     returned whatever was launched earlier has completed and its writes are visible;
+  //   - writes nothing that the copy reads, and neither reads nor writes the part of the workspace that
+  //     the copy writes (copied, lens, table, K, V);
+  // and as the copy's wait makes what comes behind it wait for both.
   bool beside = false;
 };
 cudaError_t launch_kv4_copy(const qasc_shape& s, const PageMap& pm, const Batch& bt, const Kv4Cache& kv, int32_t sink,

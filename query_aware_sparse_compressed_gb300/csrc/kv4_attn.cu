@@ -477,7 +477,9 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, j = lane & 3;
   pdl_wait();
-  if (kKind == kRest && p.whole) pdl_trigger();   // the copy begins beside it
+  // The copy begins beside it (Kv4Copy::beside).  From here on a call of this kind writes out and lse
+  // and nothing else: whole items leave no parts in the workspace.
+  if (kKind == kRest && p.whole) pdl_trigger();
 
   // ---- this warp's part of the work.  Whole items of single tokens need no sums.
   const int groups = (p.seqs + (1 << p.ssh) - 1) >> p.ssh;

@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv4_copy_kernel(const C
   __shared__ int32_t first[kCopySeq + 1];
   __shared__ int32_t sums[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (!a.c.beside) pdl_wait();
+  if (!a.c.beside) pdl_wait();   // (beside: see Kv4Copy)
   auto shape_of = [&](int b, int* drop) {   // tokens of the copy and those left out behind the sink; 0: not copied
     const int64_t q0 = min(max(a.bt.cu_q ? __ldg(a.bt.cu_q + b) : static_cast<int64_t>(b), int64_t(0)), a.bt.T);
     const int64_t q1 = min(max(a.bt.cu_q ? __ldg(a.bt.cu_q + b + 1) : static_cast<int64_t>(b) + 1, q0), a.bt.T);
