@@ -349,6 +349,29 @@ def test_append_at_far_positions():
 
 
 @pytest.mark.parametrize("inter", [True, False])
+def test_append_rotates_infinities_and_nan(inter):
+    """Infinite, huge and NaN keys under rotation, at position 0 as well (where infinity times sin 0 is NaN)."""
+    T, Hkv = 40, 2
+    k = rand((T, Hkv, 128), 82)
+    g = torch.Generator().manual_seed(83)
+    for value in (float("inf"), -float("inf"), float("nan"), 3.3e38, -3.3e38, 3e-39):
+        at = torch.randint(0, T * Hkv * 128, (12,), generator=g)
+        k.reshape(-1)[at] = value
+    k[0, 0, 0], k[0, 1, 70] = float("inf"), float("nan")
+    f = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float()
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = okv4.quantise(round_bf16(osv.rotate(f64(k), np.arange(T), f.numpy(), inter)))
+    kv = qasc.alloc_kv4(1, Hkv, T)
+    c, ln = batch_tensors([0, T], [T])
+    qasc.kv4_rope_append(None, k.cuda(), k.cuda(), None, kv, ln, f.cuda(), cu_q=c, interleaved=inter)
+    qasc.qasc_device_error()
+    codes, sf = kv.K[0].cpu().numpy().transpose(1, 0, 2), kv.K_sf.view(torch.uint8)[0].cpu().numpy().transpose(1, 0, 2)
+    assert np.array_equal(sf, want[1]) and (sf == 127).any() and (sf == 126).any()
+    broken = np.repeat(sf == 127, 8, axis=-1)              # a NaN group's codes may be any
+    assert np.array_equal(np.where(broken, 0, codes), np.where(broken, 0, want[0]))
+
+
+@pytest.mark.parametrize("inter", [True, False])
 def test_append_of_zeros_keeps_their_signs(inter):
     """Pairs of zeros of either sign at angles of every quadrant: the code's sign bit is that of the rotation."""
     T = 64
@@ -692,6 +715,42 @@ def test_window_equals_the_bf16_call_on_the_cache_read_back():
     assert float((lse - want_lse).abs().max()) <= 1e-4
 
 
+@pytest.mark.parametrize("tk,tv", [(-32, 32), (32, -32)])
+@pytest.mark.parametrize("Hq,Hkv,ql,lens,local", [
+    (8, 2, [1, 1], [700, 33], 300),                        # whole items
+    (8, 1, [3], [6000], 6000),                             # shared between blocks
+    (64, 8, [300, 2], [900, 80], 1000),                    # over a copy
+])
+def test_window_of_factors_at_the_ends_of_their_range(Hq, Hkv, ql, lens, local, tk, tv):
+    T, P, cu = sum(ql), 64, np.concatenate([[0], np.cumsum(ql)]).tolist()
+    pages = Pages4(lens, Hkv, P, cdiv(max(lens), P), seed=84, random=True, t=(2.0 ** tk, 2.0 ** tv))
+    q = rand((T, Hq, 128), 85, 0.3 * 2.0 ** -tk)
+    assert goes_over_a_copy(T, len(ql), Hq, Hkv, pages.pps * P, local, 4, max(ql)) == (max(ql) == 300)
+    out, lse = window(q, pages, cu, lens, 4, local, max_q=max(ql))
+    tokens = sorted({0, T // 2, T - 1})
+    ref = osv.window_attention(f64(q), pages.values(0), pages.values(1), cu, lens, 4, local, tokens=tokens)
+    check_rows(out, lse, ref, max(lens), 6.0 * 2.0 ** tv, rows=tokens, p=p_error(ql, Hq // Hkv))
+
+
+def test_window_rows_that_are_not_copied_keep_fp16_probabilities():
+    """More than 128 rows of a sequence, on the 4-bit cache because the call says so (max_q) or has no room for a copy:
+    the smaller of the two errors."""
+    Hq, Hkv, P, ql, lens, local = 64, 8, 64, [200, 40], [1500, 700], 1000
+    T, cu = sum(ql), [0, 200, 240]
+    pages = Pages4(lens, Hkv, P, 24, seed=86, random=True)
+    q = rand((T, Hq, 128), 87, 0.3)
+    tokens = [0, 77, 199, 200, 239]
+    ref = osv.window_attention(f64(q), pages.values(0), pages.values(1), cu, lens, 4, local, tokens=tokens)
+    assert goes_over_a_copy(T, 2, Hq, Hkv, 24 * P, local, 4, 200)
+    c, ln = batch_tensors(cu, lens)
+    for max_q in (1, 16, 200):
+        ws = window_ws(T, 2, Hq, Hkv, 24 * P, local, 4, 1)
+        out, lse = outputs(T, Hq)
+        qasc.kv4_window_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), ln, out, ws, local=local, cu_q=c, max_q=max_q, lse=lse)
+        qasc.qasc_device_error()
+        check_rows(out, lse, ref, 1500, 6.0, rows=tokens)
+
+
 @pytest.mark.parametrize("n,m", [(1900, 1), (900, 40)])
 @pytest.mark.parametrize("side", [0, 1])
 def test_window_not_a_number_stays_visible(n, m, side):
@@ -822,6 +881,31 @@ def test_two_windows_on_two_streams():
     torch.cuda.synchronize()
     qasc.qasc_device_error()
     assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
+
+
+@pytest.mark.parametrize("ql,lens,local", [([300, 1, 200], [900, 700, 800], 300), ([300, 1, 200], [4000, 3000, 2500], 5000)])
+def test_two_windows_over_copies_on_two_streams(ql, lens, local):
+    """The rest and the copy beside it, or one behind the other, of two calls at once, each with a workspace of its own."""
+    Hq, Hkv, P, T = 64, 8, 64, sum(ql)
+    cu = np.concatenate([[0], np.cumsum(ql)]).tolist()
+    pages = Pages4(lens, Hkv, P, cdiv(max(lens), P), seed=88, random=True)
+    kv, table = pages.cache(), pages.table.cuda()
+    assert goes_over_a_copy(T, 3, Hq, Hkv, pages.pps * P, local, 4, 300)
+    qs = [rand((T, Hq, 128), 89 + i, 0.3).cuda() for i in range(2)]
+    c, ln = batch_tensors(cu, lens)
+    wss = [window_ws(T, 3, Hq, Hkv, pages.pps * P, local, 4, 300) for _ in range(2)]
+    wants, gots = ([outputs(T, Hq) for _ in range(2)] for _ in range(2))
+    for q, want, ws in zip(qs, wants, wss):
+        qasc.kv4_window_attn_paged(q, kv, table, ln, want[0], ws, local=local, cu_q=c, max_q=300, lse=want[1])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for q, got, ws, s in zip(qs, gots, wss, streams):
+            qasc.kv4_window_attn_paged(q, kv, table, ln, got[0], ws, local=local, cu_q=c, max_q=300, lse=got[1], stream=s)
+    torch.cuda.synchronize()
+    qasc.qasc_device_error()
+    for want, got in zip(wants, gots):
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
 
 
 def test_two_graphs_take_turns_with_one_workspace():
@@ -1171,6 +1255,19 @@ def test_sparse_of_many_lists(K):
     Held.Hkv = Hkv
     ref = sparse_ref(f64(q)[rows], Held, [[sel[b, gg, :int(lens[b, gg])].tolist() for gg in range(Hkv)] for b in rows], n, 4, 64)
     check_rows(out[rows], lse[rows], ref, n, 6.0)
+
+
+@pytest.mark.parametrize("tk,tv", [(-32, 32), (32, -32)])
+def test_sparse_of_factors_at_the_ends_of_their_range(tk, tv):
+    n, P = 900, 64
+    pages = Pages4([n], 2, P, 15, seed=91, random=True, t=(2.0 ** tk, 2.0 ** tv))
+    q = rand((1, 8, 128), 92, 0.3 * 2.0 ** -tk)
+    sel = torch.arange(10, 710, 7, dtype=torch.int32).reshape(1, -1)
+    out, lse = outputs(1, 8)
+    ws = qasc.alloc_workspace(qasc.kv4_sparse_attn_workspace_bytes(1, 8, 2, n, 960, 100, 4, 64))
+    qasc.kv4_sparse_attn_paged(q.cuda(), pages.cache(), pages.table.cuda(), sel.cuda(), out, ws, n=n, local=64, lse=lse)
+    qasc.qasc_device_error()
+    check_rows(out, lse, sparse_ref(f64(q), pages, [[sel[0].tolist()] * 2], n, 4, 64), n, 6.0 * 2.0 ** tv)
 
 
 def test_sparse_replays_in_a_graph():
