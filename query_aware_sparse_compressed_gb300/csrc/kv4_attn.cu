@@ -259,25 +259,17 @@ struct Smem {
   int place[kSums + 1];          // places before a group of sequences
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 // Rows of their own, zeros behind `bytes`.  (64 bytes are fetched into L2, not the default
 // 128: of scattered rows the rest would be read for nothing, 215 MB where 95 are listed:
 // four 128K contexts at 20 %, 48 against 40 us.)
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
+__device__ __forceinline__ void cp_async8_zfill(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global.L2::64B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // c (+)= A (16 x 16, rows) B (16 x 8, columns), fp16 operands.
@@ -297,10 +289,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) { return bits(__floats2half2_rn(lo, hi)); }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 
 // Row of the queries and outputs of row `col` of an item.
 __device__ __forceinline__ int64_t row_of(const Args& p, int tok0, int g, int col) {
@@ -702,12 +690,12 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1) kv4_attn_kernel(const _
       for (int i = 0; i < 4; ++i) {
         const int from = __shfl_sync(0xffffffffu, row, r + 8 * i);   // rows that are none: zeros
         const int64_t src = static_cast<int64_t>(max(from, 0)) * kKv4Codes + 16 * j;
-        cp_async16(to + k_at + 8 * i * kKv4Codes, p.a.kv.K + src, from >= 0 ? 16 : 0);
-        cp_async16(to + v_at + 8 * i * kKv4Codes, p.a.kv.V + src, from >= 0 ? 16 : 0);
+        cp_async16_zfill(to + k_at + 8 * i * kKv4Codes, p.a.kv.K + src, from >= 0 ? 16 : 0);
+        cp_async16_zfill(to + v_at + 8 * i * kKv4Codes, p.a.kv.V + src, from >= 0 ? 16 : 0);
       }
       const int64_t own = static_cast<int64_t>(max(row, 0)) * kKv4Groups;
-      cp_async8(to + kf_at, p.a.kv.K_sf + own, row >= 0 ? 8 : 0);
-      cp_async8(to + kf_at + kTileCodes + kTileScales, p.a.kv.V_sf + own, row >= 0 ? 8 : 0);
+      cp_async8_zfill(to + kf_at, p.a.kv.K_sf + own, row >= 0 ? 8 : 0);
+      cp_async8_zfill(to + kf_at + kTileCodes + kTileScales, p.a.kv.V_sf + own, row >= 0 ? 8 : 0);
     }
     cp_async_commit();
     put = put + 1 == kStages ? 0 : put + 1;
