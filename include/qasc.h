@@ -529,7 +529,8 @@ QASC_API qasc_status kv4_read_paged(const qasc_shape* shape, const qasc_paged_ca
  *          overlap need one each.
  *   other arguments, refusals, lengths outside the cache and rows without a token as for
  *   kv_window_attn; out is rounded once from fp32; the probabilities of the second product
- *   are fp16 (bf16 over a copy), sums and statistics fp32.  Rows that no query attends
+ *   are fp16 (bf16 over a copy: which of the two a sequence of more than 128 rows gets depends
+ *   on its batch, max_q and the workspace), sums and statistics fp32.  Rows that no query attends
  *   to may hold anything, as there; a row with a NaN scale that some attend to reaches
  *   their outputs, and may reach those of its sequence's other queries in that KV
  *   head.  A block-table entry outside the pool stands for rows of zeros and is recorded
@@ -555,7 +556,8 @@ QASC_API qasc_status kv4_window_attn_paged(const qasc_shape* shape, const qasc_p
  *            stands for a row of zeros and is recorded as QASC_ERR_BAD_TABLE
  *   workspace, ws_bytes >= kv4_sparse_attn_workspace_bytes(shape, params), 4.3 MB
  * A row without any token gives out 0 and lse -inf.  B <= 2048 (more:
- * QASC_ERR_UNSUPPORTED). */
+ * QASC_ERR_UNSUPPORTED).  The calls that select tokens read an index made from bf16 keys
+ * (ts_index_append*). */
 QASC_API size_t kv4_sparse_attn_workspace_bytes(const qasc_shape* shape, const qasc_ts_params* params);
 QASC_API qasc_status kv4_sparse_attn(const qasc_shape* shape, const qasc_ts_params* params, const uint16_t* q,
                                      const qasc_kv4* kv, const int32_t* sel, const int32_t* sel_len,

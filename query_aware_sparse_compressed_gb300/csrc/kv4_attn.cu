@@ -13,7 +13,8 @@
 // tcgen05 product takes its second operand from shared memory only, and 128 rows
 // where there are 1 to 16.  The products take a fourth of mma.sync's rate.  One
 // sequence of 32768 tokens, 16 rows: 21 us; over a bf16 copy on tcgen05, which is
-// where calls of many rows go (see copy_pays), 75.
+// where calls of many rows go (see copy_pays), 70.  (For 17 to 128 rows the reckoning is
+// another: 180 of 128 bytes a cycle are 1.4 times HBM's time, less than the passes of 16 rows take here.)
 //
 // Work.  The queries of a KV head's group share its keys: an item is up to
 // 8 kNT rows (token, head of the group) of a sequence and KV head.  Its tokens
@@ -88,8 +89,8 @@ constexpr int kTilesMost = kTokensMost / kTile;
 // Sequences of more rows than this take their keys and values from a bf16 copy and
 // go to kv_window_attn's kernel, whose products are tcgen05's: a row block here costs
 // what it costs whether the next one needs the same keys or not.  One sequence of
-// 32768 tokens, 32 heads, 8 KV heads, here and over a copy: 64 rows 45 and 75 us,
-// 128 rows 78 and 79, 256 rows 143 and 88; 32 sequences of 4096, 64 heads, 128 rows: 283 and 261.
+// 32768 tokens, 32 heads, 8 KV heads, here and over a copy: 64 rows 49 and 71 us,
+// 128 rows 86 and 76, 256 rows 161 and 85; 32 sequences of 4096, 64 heads, 136 rows: 348 and 241.
 constexpr int64_t kCopyRows = 128;
 constexpr int kLeast = 8;                      // places that a block takes at least
 // Items of more tokens than this may be shared between blocks; with more items than warps those
@@ -1113,9 +1114,11 @@ constexpr int64_t kCopyBytes = int64_t(1) << 32;   // of a copy, at most
 // of max_q new tokens.
 double copies_of(int64_t T, int64_t max_q, int64_t seqs) { return std::min<double>(seqs, std::max(1.0, 1.5 * T / max_q)); }
 
-// Whether the copy pays for a call that may have such sequences (microseconds, from
-// the same runs): it is two kernels more, its bytes, and the products over it; here every block
-// of 16 rows takes 1.05 ns a tile that its rows see on 152 SMs.
+// Whether the copy pays for a call that may have such sequences (microseconds on 152 SMs, within a
+// quarter of what was measured for 132 to 8192 rows a sequence, 256 to 131072 tokens of window): it is two kernels more
+// (23), its bytes (5.5 TB/s), and the products over it (1.4 PFLOP/s); here every block of 16 rows takes
+// 1.05 ns a tile that its rows see.  2048 new of 32768 tokens, 32 / 8 heads: 4671 us here, 726 over a copy (the
+// lines: 4423 and 840); 16 sequences of 64 new tokens, local 512, 8 / 2 heads: 22.5 and 23 (19 and 27).
 bool copy_pays(const qasc_shape& s, int64_t T, int64_t max_q, int64_t tokens, int64_t seqs, int64_t window) {
   const double gq = s.Hq / s.Hkv, rows = T * gq, copies = copies_of(T, max_q, seqs);
   const double seen = std::min<int64_t>(tokens, window + 15), seen256 = std::min<double>(tokens, window + 255 / gq);

@@ -18,7 +18,7 @@
 // sin, with fp32's error.
 //
 // Append's bound: bytes, (2 Hq + 2 Hkv) 256 + 144 Hkv a token.  32768 tokens of 64 + 8 + 8
-// heads (1.21 GB): 192 us, 6.3 TB/s, 93 % of a copy's rate; issue slots 66 % (a
+// heads (1.21 GB): 193 us, 6.3 TB/s, 92 % of a copy's rate; issue slots 66 % (a
 // key's rotation and quantising take 9 times a query's instructions).  What that took: a thread's
 // units (two 16-byte chunks of a head) are copied into a ring of its own ahead of
 // their use, so that the loads go on under a key's arithmetic (245 us with loads a
